@@ -1,0 +1,466 @@
+"""What is measured of the dense-attention operators: the paged key/value cache
+(quantised as it is written, and read back), causal attention over packed
+prompts, and attention of a tree of drafted tokens over the cache.
+
+``run`` computes an operator in its plain form (elementary torch operations in
+32 bits) or, with ``own`` set, calls the framework's entry point.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+DEV = "cuda"
+E4M3_MAX = 448.0
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+def listed():
+    return [
+        # one decode step of 64 sequences: 64 new rows into an 8-bit cache
+        dict(name="write_step_e4m3", op="write", n=64, kvh=8, hd=128, page=64, fmt="e4m3", pad=0, fused=True, shape=1),
+        # a prompt chunk's rows, padding rows among them, straight from the fused projection
+        dict(name="write_prompt_e4m3", op="write", n=16383, kvh=8, hd=128, page=64, fmt="e4m3", pad=100, fused=True, shape=2),
+        # a short sequence's earlier rows, small pages
+        dict(name="read_short_e4m3", op="read", batch=1, max_len=513, kvh=8, hd=128, page=16, fmt="e4m3", shape=3),
+        # the earlier rows of some long sequences, for the attention of their next chunk
+        dict(name="read_long_e4m3", op="read", batch=4, max_len=16384, kvh=8, hd=128, page=64, fmt="e4m3", shape=4),
+        # the first prompt of an idle server: latency
+        dict(name="prompt_tiny", op="prompt", batch=1, max_len=64, prior=0, nh=4, kvh=2, hd=64, window=0, sink=True, shape=5),
+        # a batch of prompts of different lengths, packed
+        dict(name="prompt_packed", op="prompt", batch=7, max_len=2000, prior=0, nh=32, kvh=8, hd=128, window=0, sink=False, shape=6),
+        # one long prompt
+        dict(name="prompt_long", op="prompt", batch=1, max_len=16384, prior=0, nh=32, kvh=8, hd=128, window=0, sink=False, shape=7),
+        # a layer with a sliding window and sinks, head width 64, a chunk behind earlier rows
+        dict(name="prompt_window_chunk", op="prompt", batch=2, max_len=4096, prior=4096, nh=64, kvh=8, hd=64, window=128, sink=True, shape=8),
+        # single-token decode of one sequence, rows not quantised
+        dict(name="tree_one_token_bf16", op="tree", batch=1, max_q=1, max_len=8192, nh=32, kvh=8, hd=128, page=64, fmt="bf16",
+             window=0, sink=False, mask=False, shape=9),
+        # single-token decode of a batch of sequences of different lengths on the 8-bit cache
+        dict(name="tree_batch_one_token", op="tree", batch=48, max_q=1, max_len=8191, nh=64, kvh=8, hd=128, page=64, fmt="e4m3",
+             window=0, sink=True, mask=False, shape=10),
+        # trees of drafted tokens of a batch
+        dict(name="tree_batch_drafts", op="tree", batch=8, max_q=16, max_len=16384, nh=32, kvh=8, hd=128, page=64, fmt="e4m3",
+             window=0, sink=False, mask=True, shape=11),
+        # the largest trees, over long caches
+        dict(name="tree_wide_long", op="tree", batch=4, max_q=64, max_len=32768, nh=64, kvh=8, hd=128, page=64, fmt="e4m3",
+             window=0, sink=False, mask=True, shape=12),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "read", "prompt", "prompt", "tree", "tree"])
+    kvh = rng.choice([1, 2, 4, 8])
+    hd = rng.choice([64, 128, 128, 80, 96])
+    page, fmt = rng.choice([16, 32, 64, 128]), rng.choice(["e4m3", "e4m3", "bf16"])
+    shape = rng.randrange(1 << 30)
+    if op == "write":
+        return dict(op=op, n=_log(rng, 1, 16383), kvh=kvh, hd=hd, page=page, fmt=fmt, pad=rng.choice([0, 3]), fused=rng.random() < 0.5, shape=shape)
+    if op == "read":
+        batch = _log(rng, 1, 32)
+        return dict(op=op, batch=batch, max_len=_log(rng, 1, 65536 // batch), kvh=kvh, hd=hd, page=page, fmt=fmt, shape=shape)
+    nh = kvh * rng.choice([1, 2, 4, 5, 8] if kvh < 8 else [1, 4, 8])
+    if op == "prompt":
+        max_len = _log(rng, 1, 6000)
+        batch = min(_log(rng, 1, 16), max(1, 6000 // max_len))
+        return dict(op=op, batch=batch, max_len=max_len, prior=rng.choice([0, 0, _log(rng, 1, 4000)]), nh=nh, kvh=kvh, hd=hd,
+                    window=rng.choice([0, 0, 128, 1000]), sink=rng.random() < 0.5, shape=shape)
+    max_q = rng.choice([1, 1, _log(rng, 2, 64)])
+    max_len = _log(rng, 64, 32768)
+    batch = min(_log(rng, 1, 64), max(1, 131072 // max_len))
+    return dict(op=op, batch=batch, max_q=max_q, max_len=max_len, nh=nh, kvh=kvh, hd=hd, page=page, fmt=fmt,
+                window=rng.choice([0, 0, 128]), sink=rng.random() < 0.5, mask=max_q > 1, shape=shape)
+
+
+def _lens(c):
+    """The sequences' lengths: the longest is max_len, the others are spread below it."""
+    r = random.Random(c["shape"])
+    lo = c["max_q"] if c["op"] == "tree" else 1
+    return [c["max_len"]] + [r.randint(max(lo, c["max_len"] // 8), c["max_len"]) for _ in range(c["batch"] - 1)]
+
+
+def _drafts(c):
+    """The drafted tokens of each sequence: max_q for the first, the others at least half of that."""
+    r = random.Random(c["shape"] + 1)
+    return [c["max_q"]] + [r.randint((c["max_q"] + 1) // 2, c["max_q"]) for _ in range(c["batch"] - 1)]
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+def _cu(lens):
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    return torch.tensor(at, dtype=torch.int32, device=DEV)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV)
+
+
+def _keys(g, *shape):
+    """Keys as trained models have them: a few channels larger than the rest."""
+    k = _randn(g, *shape)
+    k[..., :4] *= 3.0
+    return k
+
+
+def _quantise(x):
+    """x [..., hd] to e4m3 with one scale for each row: s = amax / 448, the codes of x / s."""
+    x = x.float()
+    s = x.abs().amax(-1) / E4M3_MAX
+    return (x / s.clamp_min(1e-30).unsqueeze(-1)).to(torch.float8_e4m3fn), s
+
+
+def _cache(g, c, n_pages):
+    """A cache that holds rows already: [page, head, row of the page, hd], K and V, and the scales."""
+    shape = (n_pages, c["kvh"], c["page"], c["hd"])
+    k, v = _keys(g, *shape), _randn(g, *shape)
+    if c["fmt"] == "bf16":
+        return dict(k=k.bfloat16(), v=v.bfloat16(), k_scales=None, v_scales=None)
+    (kc, ks), (vc, vs) = _quantise(k.bfloat16()), _quantise(v.bfloat16())
+    return dict(k=kc, v=vc, k_scales=ks, v_scales=vs)
+
+
+def _pages(g, c, lens):
+    """Each sequence's pages, in no order, among some that belong to nobody."""
+    need = [-(-n // c["page"]) for n in lens]
+    n_pages = sum(need) + 3
+    order = torch.randperm(n_pages, generator=g, device=DEV).to(torch.int32)
+    table = torch.zeros(len(lens), max(need), dtype=torch.int32, device=DEV)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    return n_pages, table
+
+
+def _tree_mask(c, drafts):
+    """For each drafted token the bits of itself and its ancestors; each token's parent is an earlier one of its sequence."""
+    r = random.Random(c["shape"] + 2)
+    rows = []
+    for n in drafts:
+        own_rows = []
+        for t in range(n):
+            up = own_rows[r.randint(max(0, t - 5), t - 1)] if t else 0
+            own_rows.append(up | (1 << t))
+        rows += own_rows
+    return torch.tensor([w - (1 << 64) if w >> 63 else w for w in rows], dtype=torch.int64, device=DEV).unsqueeze(1)
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device=DEV).manual_seed(seed * 1009 + c["shape"] % 1000)
+    if c["op"] == "write":
+        kvh, hd, n = c["kvh"], c["hd"], c["n"]
+        if c["fused"]:  # q | k | v of a fused projection with as many query heads
+            qkv = _keys(g, n, 3 * kvh, hd).bfloat16()
+            k, v = qkv[:, kvh:2 * kvh], qkv[:, 2 * kvh:]
+        else:
+            k, v = _keys(g, n, kvh, hd).bfloat16(), _randn(g, n, kvh, hd).bfloat16()
+        n_pages = -(-n // c["page"]) + 3
+        slots = torch.randperm(n_pages * c["page"], generator=g, device=DEV)[:n]
+        if n > 256:  # a prompt's rows lie one after another, a step's anywhere
+            slots = slots.sort().values
+        if c["pad"]:
+            slots[-min(c["pad"], n // 2 + 1):] = -1
+        return dict(c=c, k=k, v=v, slots=slots, cache=_cache(g, c, n_pages))
+    if c["op"] == "read":
+        lens = _lens(c)
+        n_pages, table = _pages(g, c, lens)
+        return dict(c=c, cache=_cache(g, c, n_pages), table=table, cu=_cu(lens), rows=sum(lens), lens=torch.tensor(lens, device=DEV))
+    scale = c["hd"] ** -0.5
+    sink = _randn(g, c["nh"]) if c["sink"] else None
+    if c["op"] == "prompt":
+        lens = _lens(c)
+        lens_k = [n + c["prior"] for n in lens]
+        q = _randn(g, sum(lens), c["nh"], c["hd"]).bfloat16()
+        k = _keys(g, sum(lens_k), c["kvh"], c["hd"]).bfloat16()
+        v = _randn(g, sum(lens_k), c["kvh"], c["hd"]).bfloat16()
+        return dict(c=c, q=q, k=k, v=v, cu_q=_cu(lens), cu_k=_cu(lens_k), max_q=max(lens), max_k=max(lens_k), scale=scale, sink=sink)
+    lens, drafts = _lens(c), _drafts(c)
+    n_pages, table = _pages(g, c, lens)
+    q = _randn(g, sum(drafts), c["nh"], c["hd"]).bfloat16()
+    return dict(c=c, q=q, cache=_cache(g, c, n_pages), table=table, lens=torch.tensor(lens, dtype=torch.int32, device=DEV),
+                cu_q=_cu(drafts), max_q=max(drafts), max_len=max(lens), scale=scale, sink=sink,
+                mask=_tree_mask(c, drafts) if c["mask"] else None)
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+def run(state):
+    op = state["c"]["op"]
+    if own:
+        return _OWN[op](state)
+    return _PLAIN[op](state)
+
+
+def _own_cache(s):
+    from compressed_sparse_attention_window_gb300 import ds41
+    return ds41.KvCache(**s["cache"])
+
+
+def _own_write(s):
+    from compressed_sparse_attention_window_gb300 import ds41
+    ds41.kv_cache_write(_own_cache(s), s["k"], s["v"], s["slots"])
+    return s["cache"]
+
+
+def _own_read(s):
+    from compressed_sparse_attention_window_gb300 import ds41
+    k, v = ds41.kv_cache_read(_own_cache(s), s["table"], s["cu"], s["rows"])
+    return {"k": k, "v": v}
+
+
+def _own_prompt(s):
+    from compressed_sparse_attention_window_gb300 import ds41
+    lse = torch.empty(s["q"].shape[:2], device=DEV)
+    o = ds41.prompt_attn_fwd(s["q"], s["k"], s["v"], s["cu_q"], s["cu_k"], s["max_q"], s["scale"], sink=s["sink"],
+                             window=s["c"]["window"], lse=lse)
+    return {"o": o, "lse": lse}
+
+
+def _own_tree(s):
+    from compressed_sparse_attention_window_gb300 import ds41
+    lse = torch.empty(s["q"].shape[:2], device=DEV)
+    o = ds41.tree_attn_fwd(s["q"], _own_cache(s), s["table"], s["lens"], s["cu_q"], s["max_q"], s["max_len"], s["scale"],
+                           mask=s["mask"], sink=s["sink"], window=s["c"]["window"], lse=lse)
+    return {"o": o, "lse": lse}
+
+
+def _plain_write(s):
+    cache, page = s["cache"], s["c"]["page"]
+    keep = s["slots"] >= 0
+    slots = s["slots"][keep]
+    at, off = slots // page, slots % page
+    k, v = s["k"][keep], s["v"][keep]
+    if cache["k_scales"] is None:
+        cache["k"][at, :, off] = k
+        cache["v"][at, :, off] = v
+        return cache
+    (kc, ks), (vc, vs) = _quantise(k), _quantise(v)
+    cache["k"].view(torch.uint8)[at, :, off] = kc.view(torch.uint8)
+    cache["v"].view(torch.uint8)[at, :, off] = vc.view(torch.uint8)
+    cache["k_scales"][at, :, off] = ks
+    cache["v_scales"][at, :, off] = vs
+    return cache
+
+
+def _rows_of(x, scales, at, off):
+    """Cache rows [..., kvh, hd] as 32-bit values: page `at`, row `off` of the page."""
+    if scales is None:
+        return x[at, :, off].float()
+    return x.view(torch.uint8)[at, :, off].view(torch.float8_e4m3fn).float() * scales[at, :, off].unsqueeze(-1)
+
+
+def _plain_read(s):
+    cache, page = s["cache"], s["c"]["page"]
+    seq = torch.repeat_interleave(torch.arange(len(s["lens"]), device=DEV), s["lens"], output_size=s["rows"])
+    pos = torch.arange(s["rows"], device=DEV) - s["cu"].long()[seq]
+    at, off = s["table"].long()[seq, pos // page], pos % page
+    return {"k": _rows_of(cache["k"], cache["k_scales"], at, off).bfloat16(),
+            "v": _rows_of(cache["v"], cache["v_scales"], at, off).bfloat16()}
+
+
+def _attend(q, k, v, visible, scale, sink):
+    """q [B, Q, nh, hd], k and v [B, L, kvh, hd] in 32 bits, visible [B, Q, L] -> o [B, Q, nh, hd] and the log of the
+    denominators [B, Q, nh]."""
+    B, Q, nh, hd = q.shape
+    L, kvh = k.shape[1:3]
+    grouped = q.reshape(B, Q, kvh, nh // kvh, hd).permute(0, 2, 3, 1, 4).reshape(B, kvh, -1, hd)
+    s = (grouped @ k.permute(0, 2, 3, 1)).mul_(scale).view(B, nh, Q, L)
+    s.masked_fill_(~visible.unsqueeze(1), -math.inf)
+    top = s.amax(-1) if sink is None else torch.maximum(s.amax(-1), sink.view(1, nh, 1))
+    top = torch.where(top == -math.inf, 0.0, top)
+    p = s.sub_(top.unsqueeze(-1)).exp_()
+    den = p.sum(-1) if sink is None else p.sum(-1) + (sink.view(1, nh, 1) - top).exp()
+    o = (p.view(B, kvh, -1, L) @ v.permute(0, 2, 1, 3)).view(B, nh, Q, hd)
+    o = torch.where(den.unsqueeze(-1) > 0, o / den.unsqueeze(-1), 0.0)
+    return o.transpose(1, 2), (top + den.log()).transpose(1, 2)
+
+
+def _padded(cu, width):
+    """Rows of a packed tensor for [B, width], the last one where a sequence is shorter, and which of them are real."""
+    first, n = cu[:-1].long(), (cu[1:] - cu[:-1]).long()
+    i = torch.arange(width, device=DEV)
+    return (first[:, None] + i).clamp_max(cu[-1].long() - 1), i < n[:, None], n
+
+
+def _plain_prompt(s):
+    rows_q, real_q, n_q = _padded(s["cu_q"], s["max_q"])
+    rows_k, real_k, n_k = _padded(s["cu_k"], s["max_k"])
+    pos = torch.arange(s["max_q"], device=DEV) + (n_k - n_q)[:, None]  # [B, Q]
+    j = torch.arange(s["max_k"], device=DEV)
+    visible = (j <= pos[..., None]) & real_k[:, None]
+    if s["c"]["window"]:
+        visible &= j > pos[..., None] - s["c"]["window"]
+    o, lse = _attend(s["q"][rows_q].float(), s["k"][rows_k].float(), s["v"][rows_k].float(), visible, s["scale"], s["sink"])
+    return {"o": o[real_q].bfloat16(), "lse": lse[real_q]}
+
+
+def _plain_tree(s):
+    cache, page = s["cache"], s["c"]["page"]
+    rows_q, real_q, n_q = _padded(s["cu_q"], s["max_q"])
+    j = torch.arange(s["max_len"], device=DEV)
+    at, off = s["table"].long()[:, j // page], (j % page).expand(len(n_q), -1)
+    k = _rows_of(cache["k"], cache["k_scales"], at, off)
+    v = _rows_of(cache["v"], cache["v_scales"], at, off)
+    lens = s["lens"].long()
+    t = j - (lens - n_q)[:, None]  # [B, L]: which drafted token a row is, below 0 for the earlier rows
+    i = torch.arange(s["max_q"], device=DEV)
+    if s["mask"] is None:
+        drafted = t[:, None] <= i[:, None]
+        depth = i.expand(len(n_q), -1)
+    else:
+        bits = s["mask"][:, 0][rows_q]  # [B, Q]
+        drafted = ((bits[..., None] >> t[:, None].clamp(0, 63)) & 1).bool()
+        depth = ((bits[..., None] >> torch.arange(64, device=DEV)) & 1).sum(-1) - 1
+    real = (j < lens[:, None])[:, None]
+    visible = torch.where(t[:, None] < 0, torch.ones_like(drafted), drafted) & real
+    if s["c"]["window"]:  # counted from the token's place on its own path
+        first = (lens - n_q)[:, None] + depth - s["c"]["window"]
+        visible &= (j > first[..., None]) | (t[:, None] >= 0)
+    o, lse = _attend(s["q"][rows_q].float(), k, v, visible, s["scale"], s["sink"])
+    return {"o": o[real_q].bfloat16(), "lse": lse[real_q]}
+
+
+_OWN = {"write": _own_write, "read": _own_read, "prompt": _own_prompt, "tree": _own_tree}
+_PLAIN = {"write": _plain_write, "read": _plain_read, "prompt": _plain_prompt, "tree": _plain_tree}
+
+
+# ---------------------------------------------------------------------------
+# What a pass cannot do without
+# ---------------------------------------------------------------------------
+def _row_bytes(c):
+    """Bytes of one cache row, K and V of every head."""
+    return 2 * c["kvh"] * (2 * c["hd"] if c["fmt"] == "bf16" else c["hd"] + 4)
+
+
+def work(case):
+    c = case
+    if c["op"] == "write":
+        n = c["n"] - min(c["pad"], c["n"] // 2 + 1)
+        return {"bytes": n * (4 * c["kvh"] * c["hd"] + _row_bytes(c)) + 8 * c["n"], "flops": 0}
+    lens = _lens(c)
+    if c["op"] == "read":
+        return {"bytes": sum(lens) * (4 * c["kvh"] * c["hd"] + _row_bytes(c)), "flops": 0}
+    if c["op"] == "prompt":
+        window = c["window"] or 1 << 40
+        pairs = sum(_visible(n, c["prior"], window) for n in lens)
+        rows_k = sum(lens) + c["prior"] * len(lens) if not c["window"] else sum(n + min(c["prior"], window - 1) for n in lens)
+        return {"bytes": sum(lens) * c["nh"] * (4 * c["hd"] + 4) + 4 * rows_k * c["kvh"] * c["hd"], "flops": 4 * c["hd"] * c["nh"] * pairs}
+    window = c["window"] or 1 << 40
+    drafts = _drafts(c)
+    seen = [min(n, window + d - 1) for n, d in zip(lens, drafts)]
+    return {"bytes": sum(seen) * _row_bytes(c) + sum(drafts) * c["nh"] * (4 * c["hd"] + 4),
+            "flops": 4 * c["hd"] * c["nh"] * sum(d * min(n, window) for n, d in zip(lens, drafts))}
+
+
+def _visible(n, prior, window):
+    """Pairs of a causal prompt of n tokens behind `prior` earlier ones: token i sees min(window, prior + i + 1) rows."""
+    full = min(n, max(0, window - prior - 1))  # tokens that see everything before them
+    return full * prior + full * (full + 1) // 2 + (n - full) * window if window < prior + n else n * prior + n * (n + 1) // 2
+
+
+# ---------------------------------------------------------------------------
+# The definition in 64 bits
+# ---------------------------------------------------------------------------
+def _e4m3_grid(x):
+    """x (64 bits, |x| <= 448) on the e4m3 grid, to the nearest, ties to the even code."""
+    e = torch.floor(torch.log2(x.abs().clamp_min(2.0 ** -20))).clamp_min(-6.0)
+    step = torch.exp2(e - 3)
+    return torch.round(x / step) * step
+
+
+def _exact_rows(cache, name):
+    """The cache's values [page, head, row, hd] in 64 bits."""
+    x = cache[name].double()
+    return x if cache[name + "_scales"] is None else x * cache[name + "_scales"].double()[..., None]
+
+
+def _exact_seq(q, k, v, visible, scale, sink):
+    """One sequence, one query head after another's group: q [Q, nh, hd], k and v [L, kvh, hd], visible [Q, L]."""
+    Q, nh, hd = q.shape
+    per = nh // k.shape[1]
+    o = torch.empty(Q, nh, hd, dtype=torch.float64, device=DEV)
+    lse = torch.empty(Q, nh, dtype=torch.float64, device=DEV)
+    for h in range(nh):
+        x = torch.einsum("qd,ld->ql", q[:, h].double(), k[:, h // per].double()) * scale
+        x = torch.where(visible, x, -math.inf)
+        if sink is not None:
+            x = torch.cat([x, sink[h].double().expand(Q, 1)], 1)
+        lse[:, h] = torch.logsumexp(x, 1)
+        p = torch.exp(x - torch.where(lse[:, h] == -math.inf, 0.0, lse[:, h])[:, None])
+        o[:, h] = p[:, :k.shape[0]] @ v[:, h // per].double()
+    return o, lse
+
+
+def exact(case, seed):
+    c = case
+    if work(c)["flops"] > 3e12:
+        return None
+    s = prepare(case, seed)
+    if c["op"] == "write":
+        cache, page = s["cache"], c["page"]
+        got = {n: cache[n].double() for n in ("k", "v")}
+        if c["fmt"] == "bf16":
+            got |= {"k_scales": None, "v_scales": None}
+        else:
+            got |= {n: cache[n].double() for n in ("k_scales", "v_scales")}
+        real = torch.nonzero(s["slots"] >= 0)[:, 0]
+        at, off = s["slots"][real] // page, s["slots"][real] % page
+        for n in ("k", "v"):
+            x = s[n][real].double()
+            if c["fmt"] != "bf16":
+                scale = x.abs().max(dim=-1).values / E4M3_MAX
+                got[n + "_scales"][at, :, off] = scale
+                x = _e4m3_grid(x / scale.clamp_min(1e-300)[..., None])
+            got[n][at, :, off] = x
+        return got
+    if c["op"] == "read":
+        out = {}
+        for n in ("k", "v"):
+            rows = _exact_rows(s["cache"], n).transpose(1, 2)  # [page, row, head, hd]
+            out[n] = torch.cat([rows[s["table"][b].long()].flatten(0, 1)[:m] for b, m in enumerate(_lens(c))])
+        return out
+    outs = []
+    lens = _lens(c)
+    if c["op"] == "prompt":
+        at_q = at_k = 0
+        for n in lens:
+            m = n + c["prior"]
+            i, j = torch.arange(n, device=DEV)[:, None] + c["prior"], torch.arange(m, device=DEV)
+            visible = (j <= i) & (j > i - (c["window"] or m + 1))
+            outs.append(_exact_seq(s["q"][at_q:at_q + n], s["k"][at_k:at_k + m], s["v"][at_k:at_k + m], visible, s["scale"], s["sink"]))
+            at_q, at_k = at_q + n, at_k + m
+    else:
+        at_q = 0
+        ks, vs = (_exact_rows(s["cache"], n).transpose(1, 2) for n in ("k", "v"))
+        for b, (n, d) in enumerate(zip(lens, _drafts(c))):
+            pages = s["table"][b].long()
+            k, v = ks[pages].flatten(0, 1)[:n], vs[pages].flatten(0, 1)[:n]
+            visible = torch.ones(d, n, dtype=torch.bool, device=DEV)
+            depth = torch.arange(d, device=DEV)
+            if s["mask"] is None:
+                visible[:, n - d:] = torch.ones(d, d, device=DEV).tril().bool()
+            else:
+                bits = [w % (1 << 64) for w in s["mask"][at_q:at_q + d, 0].tolist()]
+                own_rows = torch.tensor([[w >> t & 1 for t in range(d)] for w in bits], device=DEV).bool()
+                visible[:, n - d:] = own_rows
+                depth = own_rows.sum(1) - 1
+            if c["window"]:
+                seen = torch.arange(n, device=DEV) > (n - d + depth - c["window"])[:, None]
+                visible[:, :n - d] &= seen[:, :n - d]
+            outs.append(_exact_seq(s["q"][at_q:at_q + d], k, v, visible, s["scale"], s["sink"]))
+            at_q += d
+    return {"o": torch.cat([o for o, _ in outs]), "lse": torch.cat([x for _, x in outs])}
