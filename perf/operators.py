@@ -115,10 +115,10 @@ def _keys(g, *shape):
 
 
 def _quantise(x):
-    """x [..., hd] to e4m3 with one scale for each row: s = amax / 448, the codes of x / s."""
+    """x [..., hd] to e4m3 with one scale for each row: s = amax / 448 (amax floored at 448 * 2^-126), the codes of x / s."""
     x = x.float()
-    s = x.abs().amax(-1) / E4M3_MAX
-    return (x / s.clamp_min(1e-30).unsqueeze(-1)).to(torch.float8_e4m3fn), s
+    s = x.abs().amax(-1).clamp_min(E4M3_MAX * 2.0 ** -126) / E4M3_MAX
+    return (x / s.unsqueeze(-1)).to(torch.float8_e4m3fn), s
 
 
 def _cache(g, c, n_pages):
@@ -422,9 +422,9 @@ def exact(case, seed):
         for n in ("k", "v"):
             x = s[n][real].double()
             if c["fmt"] != "bf16":
-                scale = x.abs().max(dim=-1).values / E4M3_MAX
+                scale = x.abs().max(dim=-1).values.clamp_min(E4M3_MAX * 2.0 ** -126) / E4M3_MAX
                 got[n + "_scales"][at, :, off] = scale
-                x = _e4m3_grid(x / scale.clamp_min(1e-300)[..., None])
+                x = _e4m3_grid(x / scale[..., None])
             got[n][at, :, off] = x
         return got
     if c["op"] == "read":
