@@ -1,0 +1,48 @@
+// ds41_dense.cuh - what the dense-attention entry points share: the paged
+// key/value cache as kernels see it, the argument checks of its layout, and
+// the e4m3 codec of its rows.  Nothing here is shared with the CPU oracle.
+#pragma once
+
+#include "ds41_common.cuh"
+
+namespace ds41 {
+
+// A paged cache: [n_pages][kvh][page][hd] values (bf16 or e4m3 codes) of K and
+// V, and for e4m3 the f32 scales [n_pages][kvh][page].
+struct PagedKv {
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* ks;  // null for bf16
+    const float* vs;
+    int64_t n_pages;
+    int page, page_shift, kvh, hd;
+};
+
+// Host: checks a cache's layout (DS41_E_ARG with a message) and fills `out`.
+int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
+                int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out);
+
+inline bool aligned_to(const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// First element of row `off` of page `pg`, head `h`, counted in elements.
+// 64-bit: a cache of a few million rows passes 2^31 elements.
+__device__ __forceinline__ int64_t paged_row(const PagedKv& c, int64_t pg, int h, int off) {
+    return (pg * c.kvh + h) * c.page + off;
+}
+
+// Two e4m3 codes (low byte first) -> their exact values as bf16x2.  The code's
+// exponent and mantissa bits moved into a bf16's give the value times 2^-120
+// (exponent bias 7 against 127, subnormals included), so one exact bf16
+// product restores it.  A NaN code (0x7f, 0xff) would come out as +-480, so
+// the caller that has to keep NaN uses e4m3x2_to_bf16x2_nan.
+__device__ __forceinline__ uint32_t e4m3_spread(uint32_t hi_bytes) {
+    // hi_bytes: a code in the upper byte of each half, the lower bytes zero
+    const uint32_t r = (hi_bytes & 0x80008000u) | ((hi_bytes >> 4) & 0x07f007f0u);
+    uint32_t out;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out) : "r"(r), "r"(0x7b807b80u));  // 2^120
+    return out;
+}
+
+}  // namespace ds41

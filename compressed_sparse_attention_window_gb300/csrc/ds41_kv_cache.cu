@@ -1,0 +1,288 @@
+// ds41_kv_cache.cu - the paged key/value cache: rows quantised (or copied) as
+// they are written, and read back as bf16.
+//
+// Mathematics.  An e4m3 row x[0..hd) of one token and head keeps one scale
+//   s = max(amax |x|, 448 * 2^-126) / 448        (f32, correctly rounded)
+// and the codes e4m3(x / s), to nearest, ties to the even code.  448 is the
+// largest e4m3 value, so the largest element gets the largest code; the floor
+// keeps s a normal number, so a zero row has codes +-0.  A row that holds a NaN
+// or an infinity keeps the scale NaN and zero codes: whatever reads it sees NaN.
+// Reading back is bf16(code * s), one rounding.
+//
+// Both kernels move bytes and little else.
+#include "ds41_dense.cuh"
+
+namespace ds41 {
+
+int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
+                int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out) {
+    DS41_REQUIRE(fmt == DS41_KV_BF16 || fmt == DS41_KV_E4M3, DS41_E_ARG,
+                 "%s: fmt=%d is neither DS41_KV_BF16 nor DS41_KV_E4M3", name, fmt);
+    DS41_REQUIRE(page >= 16 && page <= 256 && (page & (page - 1)) == 0, DS41_E_ARG,
+                 "%s: page=%lld must be a power of two of 16 .. 256", name, (long long)page);
+    DS41_REQUIRE(kvh >= 1 && kvh <= 1024 && hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
+                 "%s: kvh=%lld hd=%lld (hd a multiple of 16, at most 128)", name, (long long)kvh,
+                 (long long)hd);
+    DS41_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31), DS41_E_ARG, "%s: n_pages=%lld", name,
+                 (long long)n_pages);
+    DS41_REQUIRE(k && v && aligned16(k) && aligned16(v), DS41_E_ARG,
+                 "%s: the caches must be non-null and 16-byte aligned", name);
+    if (fmt == DS41_KV_E4M3)
+        DS41_REQUIRE(ks && vs && aligned16(ks) && aligned16(vs), DS41_E_ARG,
+                     "%s: an e4m3 cache needs its scales (non-null, 16-byte aligned)", name);
+    out->k = static_cast<const uint8_t*>(k);
+    out->v = static_cast<const uint8_t*>(v);
+    out->ks = fmt == DS41_KV_E4M3 ? ks : nullptr;
+    out->vs = fmt == DS41_KV_E4M3 ? vs : nullptr;
+    out->n_pages = n_pages;
+    out->page = (int)page;
+    out->page_shift = 0;
+    while ((1 << out->page_shift) < page) out->page_shift++;
+    out->kvh = (int)kvh;
+    out->hd = (int)hd;
+    return DS41_OK;
+}
+
+namespace {
+
+constexpr int THREADS = 256;
+
+struct WriteArgs {
+    const uint16_t* x[2];  // k, v
+    int64_t stride[2];     // elements from a token's rows to the next token's
+    uint8_t* cache[2];
+    float* scales[2];
+    const int64_t* slots;
+    int64_t n, n_slots;
+    int kvh, hd, page, page_shift;
+    unsigned int* status;
+};
+
+// L lanes take one (token, head): 8 elements of its K row and of its V row
+// each, so both rows' loads are in flight together.
+template <int L, bool E4M3>
+__global__ void __launch_bounds__(THREADS) kv_write_kernel(const WriteArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / L;
+    const int c = (threadIdx.x % L) * 8;
+    const int64_t t = g / a.kvh;
+    const int h = (int)(g - t * a.kvh);
+    const bool live = t < a.n;
+    const bool mine = live && c < a.hd;
+    const int64_t slot = live ? a.slots[t] : -1;
+    uint4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        x[i] = mine ? *reinterpret_cast<const uint4*>(a.x[i] + t * a.stride[i] + h * a.hd + c)
+                    : make_uint4(0, 0, 0, 0);
+    const bool keep = slot >= 0 && slot < a.n_slots;
+    if (live && !keep && slot != -1 && c == 0 && h == 0) raise_status(a.status, DS41_E_INDEX);
+    const int64_t row = ((slot >> a.page_shift) * a.kvh + h) * a.page + (slot & (a.page - 1));
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        if (!E4M3) {
+            if (keep && mine)
+                *reinterpret_cast<uint4*>(a.cache[i] + (row * a.hd + c) * 2) = x[i];
+            continue;
+        }
+        // the largest magnitude as bf16 bits (ordered like the values; the
+        // bits of infinities and NaN are the largest of all)
+        uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+        for (int off = L / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const bool fin = m < 0x7f80u;
+        const float s = __fdiv_rn(fmaxf(bf2f((uint16_t)m), 448.0f * 0x1p-126f), 448.0f);
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t codes[2] = {0, 0};
+        if (fin) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float lo = __fdiv_rn(__uint_as_float(w[e] << 16), s);
+                const float hi = __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), s);
+                uint16_t r;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+                codes[e / 2] |= (uint32_t)r << (16 * (e & 1));
+            }
+        }
+        if (keep && mine) {
+            *reinterpret_cast<uint2*>(a.cache[i] + row * a.hd + c) = make_uint2(codes[0], codes[1]);
+            if (c == 0) a.scales[i][row] = fin ? s : __uint_as_float(0x7fc00000u);
+        }
+    }
+}
+
+struct ReadArgs {
+    PagedKv kv;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* starts;
+    uint16_t* out[2];
+    int64_t rows;
+    int B, max_pages;
+    unsigned int* status;
+};
+
+// L lanes take one (row, head), 16 elements of K and of V each; the rows of one
+// head are consecutive groups, as they lie in a page.
+template <int L, bool E4M3>
+__global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int h = blockIdx.y;
+    const int64_t r = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / L;
+    const int c = (threadIdx.x % L) * 16;
+    if (r >= a.rows || c >= a.kv.hd) return;
+    if (r >= a.cu[a.B]) return;  // behind the last sequence
+    int lo = 0, hi = a.B;        // the last b with cu[b] <= r
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    const int64_t pos = r - a.cu[lo] + (a.starts ? a.starts[lo] : 0);
+    const int64_t pi = pos >> a.kv.page_shift;
+    int64_t pg = -1;
+    if (pos >= 0 && pi < a.max_pages) pg = a.table[(int64_t)lo * a.max_pages + pi];
+    const bool ok = pg >= 0 && pg < a.kv.n_pages;
+    if (!ok) raise_status(a.status, DS41_E_INDEX);
+    const int64_t row = paged_row(a.kv, ok ? pg : 0, h, (int)(pos & (a.kv.page - 1)));
+    uint4 in[2][2];
+    float s[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint8_t* src = i ? a.kv.v : a.kv.k;
+        in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
+        s[i] = 0.0f;
+        if (!ok) continue;
+        if (E4M3) {
+            in[i][0] = *reinterpret_cast<const uint4*>(src + row * a.kv.hd + c);
+            s[i] = (i ? a.kv.vs : a.kv.ks)[row];
+        } else {
+            in[i][0] = *reinterpret_cast<const uint4*>(src + (row * a.kv.hd + c) * 2);
+            in[i][1] = *reinterpret_cast<const uint4*>(src + (row * a.kv.hd + c) * 2 + 16);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out[i] + (r * a.kv.kvh + h) * a.kv.hd + c);
+        if (!E4M3) {
+            dst[0] = in[i][0];
+            dst[1] = in[i][1];
+            continue;
+        }
+        const uint32_t w[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            uint32_t h2;
+            const uint16_t two = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// smallest power of two of lanes that covers n vectors (n <= 16)
+int lanes_for(int64_t n) { return n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : n <= 8 ? 8 : 16; }
+
+template <bool E4M3>
+void (*pick_write(int L))(const WriteArgs) {
+    return L == 2 ? kv_write_kernel<2, E4M3>
+                  : L == 4 ? kv_write_kernel<4, E4M3>
+                           : L == 8 ? kv_write_kernel<8, E4M3> : kv_write_kernel<16, E4M3>;
+}
+template <bool E4M3>
+void (*pick_read(int L))(const ReadArgs) {
+    return L == 1 ? kv_read_kernel<1, E4M3>
+                  : L == 2 ? kv_read_kernel<2, E4M3>
+                           : L == 4 ? kv_read_kernel<4, E4M3> : kv_read_kernel<8, E4M3>;
+}
+
+}  // namespace
+}  // namespace ds41
+
+using namespace ds41;
+
+extern "C" int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const ds41_bf16* v,
+                                   int64_t v_stride, const int64_t* slots, void* k_cache,
+                                   void* v_cache, float* k_scales, float* v_scales, int fmt,
+                                   int64_t n_pages, int64_t page, int64_t kvh, int64_t hd,
+                                   int64_t n, ds41_stream_t stream) {
+    const char* name = "ds41_kv_cache_write";
+    PagedKv kv;
+    if (int rc = check_paged(name, k_cache, v_cache, k_scales, v_scales, fmt, n_pages, page, kvh,
+                             hd, &kv))
+        return rc;
+    DS41_REQUIRE(n >= 0 && n < (int64_t(1) << 31), DS41_E_RANGE, "%s: n=%lld", name, (long long)n);
+    if (n == 0) return DS41_OK;
+    DS41_REQUIRE(k && v && aligned16(k) && aligned16(v) && slots && aligned_to(slots, 8), DS41_E_ARG,
+                 "%s: k and v must be non-null and 16-byte aligned, slots non-null and aligned",
+                 name);
+    DS41_REQUIRE(k_stride >= kvh * hd && v_stride >= kvh * hd && k_stride % 8 == 0 &&
+                     v_stride % 8 == 0,
+                 DS41_E_ARG, "%s: token strides %lld, %lld (at least kvh*hd, multiples of 8)", name,
+                 (long long)k_stride, (long long)v_stride);
+    WriteArgs a{{k, v},
+                {k_stride, v_stride},
+                {static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache)},
+                {k_scales, v_scales},
+                slots,
+                n,
+                n_pages * page,
+                (int)kvh,
+                (int)hd,
+                (int)page,
+                kv.page_shift,
+                nullptr};
+    if (int rc = status_word(&a.status)) return rc;
+    const int L = lanes_for(hd / 8);
+    const int64_t blocks = (n * kvh * L + THREADS - 1) / THREADS;
+    DS41_REQUIRE(blocks < (int64_t(1) << 31), DS41_E_RANGE, "%s: n=%lld kvh=%lld", name,
+                 (long long)n, (long long)kvh);
+    return launch_pdl(fmt == DS41_KV_E4M3 ? pick_write<true>(L) : pick_write<false>(L),
+                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream, name, a);
+}
+
+extern "C" int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scales,
+                                  const float* v_scales, int fmt, int64_t n_pages, int64_t page,
+                                  int64_t kvh, int64_t hd, const int32_t* page_table,
+                                  int64_t max_pages, const int32_t* cu_k, const int32_t* starts,
+                                  int64_t B, ds41_bf16* k, ds41_bf16* v, int64_t rows,
+                                  ds41_stream_t stream) {
+    const char* name = "ds41_kv_cache_read";
+    ReadArgs a{};
+    if (int rc = check_paged(name, k_cache, v_cache, k_scales, v_scales, fmt, n_pages, page, kvh,
+                             hd, &a.kv))
+        return rc;
+    DS41_REQUIRE(B >= 0 && B < (int64_t(1) << 31) && rows >= 0 && rows < (int64_t(1) << 31) &&
+                     max_pages >= 0 && max_pages < (int64_t(1) << 31),
+                 DS41_E_RANGE, "%s: B=%lld rows=%lld max_pages=%lld", name, (long long)B,
+                 (long long)rows, (long long)max_pages);
+    if (B == 0 || rows == 0) return DS41_OK;
+    DS41_REQUIRE(k && v && aligned16(k) && aligned16(v) && cu_k && page_table &&
+                     aligned_to(cu_k, 4) && aligned_to(page_table, 4) && aligned_to(starts, 4),
+                 DS41_E_ARG,
+                 "%s: k and v must be non-null and 16-byte aligned, cu_k and page_table non-null "
+                 "and aligned", name);
+    a.table = page_table;
+    a.cu = cu_k;
+    a.starts = starts;
+    a.out[0] = k;
+    a.out[1] = v;
+    a.rows = rows;
+    a.B = (int)B;
+    a.max_pages = (int)max_pages;
+    if (int rc = status_word(&a.status)) return rc;
+    const int L = lanes_for(hd / 16);
+    const int64_t blocks = (rows * L + THREADS - 1) / THREADS;
+    return launch_pdl(fmt == DS41_KV_E4M3 ? pick_read<true>(L) : pick_read<false>(L),
+                      dim3((unsigned)blocks, (unsigned)kvh), dim3(THREADS), 0,
+                      (cudaStream_t)stream, name, a);
+}

@@ -71,6 +71,17 @@ SIGNATURES = {
     "ds41_host_step_launch": (ctypes.c_int, [_P, _P]),
     "ds41_host_step_destroy": (ctypes.c_int, [_P]),
     "ds41_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int, _P, _P]),
+    "ds41_kv_cache_write": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, ctypes.c_int]
+                            + [_I64] * 5 + [_P]),
+    "ds41_kv_cache_read": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _P,
+                                          _I64, _P, _P, _I64, _P, _P, _I64, _P]),
+    "ds41_prompt_attn_workspace_bytes": (_SZ, [_I64] * 6),
+    "ds41_prompt_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]
+                             + [_I64] * 7 + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "ds41_tree_attn_workspace_bytes": (_SZ, [_I64] * 7 + [ctypes.c_int]),
+    "ds41_tree_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64, _I64,
+                                          _P, _I64, _P, _P, _P, _I64] + [_I64] * 7
+                           + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
     "ds41_sparse_attn_noalloc_capacity": (_SZ, []),
     "ds41_sparse_attn_sink_fwd_noalloc": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _F,
                                                          _P, _P, _I64, _I64, _I64, _P]),
@@ -712,3 +723,210 @@ def forward(inp: Dict[str, torch.Tensor], wl, freqs_cis: torch.Tensor,
     out["o"] = sparse_attn_sink_fwd(inp["q"], rows_a, rows_b, idx, inp["sink"], wl.scale,
                                     o=out.get("o"), lse=out.get("lse"), ws=out.get("ws_attn"))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Dense attention with grouped heads, and its paged cache
+# ---------------------------------------------------------------------------
+class KvCache(NamedTuple):
+    """A paged key/value cache: K and V [n_pages, kvh, page, hd], bf16 or
+    float8_e4m3fn codes with their scales [n_pages, kvh, page] f32 (None for
+    bf16); value = code * scale.  Slot s is row s % page of page s // page."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
+
+
+def make_kv_cache(n_pages: int, kvh: int, page: int, hd: int, e4m3: bool = True,
+                  device="cuda") -> KvCache:
+    """An empty (zeroed) cache of n_pages pages of ``page`` rows."""
+    dtype = torch.float8_e4m3fn if e4m3 else _BF
+    k, v = (torch.zeros(n_pages, kvh, page, hd, dtype=dtype, device=device) for _ in range(2))
+    if not e4m3:
+        return KvCache(k, v)
+    ks, vs = (torch.zeros(n_pages, kvh, page, dtype=torch.float32, device=device)
+              for _ in range(2))
+    return KvCache(k, v, ks, vs)
+
+
+def _same_device(dev: torch.device, **tensors) -> None:
+    """The call runs on the current device's stream: every tensor is there."""
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}: the call runs on its stream")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _shape(name: str, t: torch.Tensor, want, dtype) -> Optional[int]:
+    """The pointer of a contiguous tensor of this shape and type (None for None)."""
+    if t is None:
+        return None
+    if t.shape != want or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype} {tuple(want)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _heads(name: str, t: torch.Tensor, dense: bool = False):
+    """(pointer, token stride, head stride) of a bf16 tensor [tokens, heads, hd]
+    whose last dimension is dense (with ``dense``: the heads too)."""
+    if t.dim() != 3 or t.dtype != _BF:
+        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, hd], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    n, h, hd = t.shape
+    tok, head, one = t.stride()
+    if h == 1 or n == 0:
+        head = hd
+    if n <= 1:  # a stride that no address depends on
+        tok = h * hd if head == hd else max(hd, 8)
+    if (one != 1 and hd > 1) or (dense and head != hd):
+        raise ValueError(f"{name}: strides {t.stride()}: the last dimension"
+                         + (" and the heads" if dense else "") + " must be dense")
+    return t.data_ptr() or None, tok, head
+
+
+def _cache_args(c: KvCache, dev):
+    """The cache's arguments of the C calls, its layout checked; and kvh, page, hd."""
+    if c.k.dim() != 4:
+        raise ValueError(f"cache: expected [n_pages, kvh, page, hd], got {tuple(c.k.shape)}")
+    n_pages, kvh, page, hd = c.k.shape
+    e4m3 = c.k.dtype == torch.float8_e4m3fn
+    if not e4m3 and c.k.dtype != _BF:
+        raise ValueError(f"cache: expected bfloat16 or float8_e4m3fn, got {c.k.dtype}")
+    if e4m3 != (c.k_scales is not None) or e4m3 != (c.v_scales is not None):
+        raise ValueError("cache: an e4m3 cache has k_scales and v_scales, a bf16 cache none")
+    for name, t in zip(c._fields, c):
+        if t is not None and t.device != dev:
+            raise ValueError(f"cache.{name} is on {t.device}, expected {dev}")
+    want = (n_pages, kvh, page)
+    return (_shape("cache.k", c.k, c.k.shape, c.k.dtype),
+            _shape("cache.v", c.v, c.k.shape, c.k.dtype),
+            _shape("cache.k_scales", c.k_scales, want, torch.float32),
+            _shape("cache.v_scales", c.v_scales, want, torch.float32),
+            1 if e4m3 else 0, n_pages, page), kvh, page, hd
+
+
+def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """ds41_kv_cache_write: the rows k, v [n, kvh, hd] bf16 (heads dense, any
+    token stride) into the cache's slots [n] int64 (-1: not written)."""
+    dev = k.device
+    _same_device(dev, v=v, slots=slots)
+    c, kvh, page, hd = _cache_args(cache, dev)
+    n = k.shape[0]
+    if k.shape != (n, kvh, hd) or v.shape != k.shape:
+        raise ValueError(f"k, v: expected {(n, kvh, hd)}, got {tuple(k.shape)}, {tuple(v.shape)}")
+    kp, k_tok, _ = _heads("k", k, dense=True)
+    vp, v_tok, _ = _heads("v", v, dense=True)
+    _call("ds41_kv_cache_write", kp, k_tok, vp, v_tok, _shape("slots", slots, (n,), torch.int64),
+          *c, kvh, hd, n, _stream())
+
+
+def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, rows: int,
+                  starts: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                  v: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """ds41_kv_cache_read: the sequences' rows, packed: k and v [rows, kvh, hd]
+    bf16 (given or new).  Sequence b gets cu_k[b + 1] - cu_k[b] rows from
+    position starts[b] (0 without starts); rows behind cu_k[-1] are left as
+    they were (uninitialised in a new tensor)."""
+    dev = cu_k.device
+    _same_device(dev, page_table=page_table, starts=starts, k=k, v=v)
+    c, kvh, page, hd = _cache_args(cache, dev)
+    B = cu_k.shape[0] - 1
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
+    mp = page_table.shape[1]
+    k = torch.empty(rows, kvh, hd, dtype=_BF, device=dev) if k is None else k
+    v = torch.empty(rows, kvh, hd, dtype=_BF, device=dev) if v is None else v
+    _call("ds41_kv_cache_read", *c, kvh, hd,
+          _shape("page_table", page_table, (B, mp), torch.int32), mp,
+          _shape("cu_k", cu_k, (B + 1,), torch.int32), _shape("starts", starts, (B,), torch.int32),
+          B, _shape("k", k, (rows, kvh, hd), _BF), _shape("v", v, (rows, kvh, hd), _BF), rows,
+          _stream())
+    return k, v
+
+
+def _ws(need: int, ws: Optional[torch.Tensor], dev):
+    """A workspace of at least ``need`` bytes: the one given, or a new one."""
+    if need == 0:
+        return None
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: expected a contiguous tensor of at least {need} bytes on {dev}")
+    return ws
+
+
+def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                    cu_k: torch.Tensor, max_q: int, scale: float,
+                    sink: Optional[torch.Tensor] = None, window: int = 0,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_prompt_attn_fwd: causal attention of packed prompts, q [Tq, nh, hd]
+    over k, v [Tk, kvh, hd] (any token and head strides that are multiples of
+    8); returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
+    dev = q.device
+    _same_device(dev, k=k, v=v, cu_q=cu_q, cu_k=cu_k, sink=sink, o=o, lse=lse)
+    qp, q_tok, q_head = _heads("q", q)
+    kp, k_tok, k_head = _heads("k", k)
+    vp, v_tok, v_head = _heads("v", v)
+    Tq, nh, hd = q.shape
+    Tk, kvh = k.shape[:2]
+    if k.shape[2] != hd or v.shape != k.shape:
+        raise ValueError(f"k, v: expected [Tk, kvh, {hd}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    B = cu_q.shape[0] - 1
+    o = torch.empty(Tq, nh, hd, dtype=_BF, device=dev) if o is None else o
+    need = load().ds41_prompt_attn_workspace_bytes(B, Tq, max_q, nh, kvh, hd)
+    ws = _ws(need, ws, dev)
+    _call("ds41_prompt_attn_fwd", qp, q_tok, q_head, kp, k_tok, k_head, vp, v_tok, v_head,
+          _shape("cu_q", cu_q, (B + 1,), torch.int32), _shape("cu_k", cu_k, (B + 1,), torch.int32),
+          B, Tq, Tk, max_q, nh, kvh, hd, scale, window, _shape("sink", sink, (nh,), torch.float32),
+          _shape("o", o, (Tq, nh, hd), _BF), _shape("lse", lse, (Tq, nh), torch.float32),
+          None if ws is None else ws.data_ptr(), need, _stream())
+    return o
+
+
+def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, lens: torch.Tensor,
+                  cu_q: torch.Tensor, max_q: int, max_len: int, scale: float,
+                  mask: Optional[torch.Tensor] = None, sink: Optional[torch.Tensor] = None,
+                  window: int = 0, o: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_tree_attn_fwd: drafted tokens q [Tq, nh, hd] (packed by cu_q) over
+    the paged cache, whose last rows of each sequence (lens [B]) are their own;
+    ``mask`` [Tq, words] int64 has a bit for each drafted token that a token
+    sees (None: a chain; one token per sequence: plain decode).  Returns
+    o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
+    dev = q.device
+    _same_device(dev, page_table=page_table, lens=lens, cu_q=cu_q, mask=mask, sink=sink, o=o,
+                 lse=lse)
+    c, kvh, page, hd = _cache_args(cache, dev)
+    qp, q_tok, q_head = _heads("q", q)
+    Tq, nh = q.shape[:2]
+    if q.shape[2] != hd:
+        raise ValueError(f"q: expected [Tq, nh, {hd}], got {tuple(q.shape)}")
+    B = cu_q.shape[0] - 1
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
+    mp = page_table.shape[1]
+    words = 0
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError(f"mask: expected [Tq, words], got {tuple(mask.shape)}")
+        words = mask.shape[1]
+    o = torch.empty(Tq, nh, hd, dtype=_BF, device=dev) if o is None else o
+    need = load().ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, c[4])
+    ws = _ws(need, ws, dev)
+    _call("ds41_tree_attn_fwd", qp, q_tok, q_head, *c,
+          _shape("page_table", page_table, (B, mp), torch.int32), mp,
+          _shape("lens", lens, (B,), torch.int32), _shape("cu_q", cu_q, (B + 1,), torch.int32),
+          _shape("mask", mask, (Tq, words), torch.int64), words, B, Tq, max_q, max_len, nh, kvh,
+          hd, scale, window, _shape("sink", sink, (nh,), torch.float32),
+          _shape("o", o, (Tq, nh, hd), _BF), _shape("lse", lse, (Tq, nh), torch.float32),
+          None if ws is None else ws.data_ptr(), need, _stream())
+    return o

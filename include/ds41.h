@@ -520,6 +520,122 @@ int ds41_attn_out_proj(ds41_bf16* o, const float* freqs_cis, int64_t max_pos,
                        int64_t m, int64_t start_pos, int64_t nh, int64_t hd, int64_t rd,
                        int64_t groups, int64_t o_rank, int64_t dim, ds41_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Dense attention with grouped heads, and its paged cache                    */
+/* ------------------------------------------------------------------------ */
+/* No counterpart on the pages: the layers of a model that attend to every
+ * earlier token with separate keys and values, and the small model that drafts
+ * tokens for it, stand beside the compressed sparse ones.  nh query heads
+ * share kvh key/value heads, nh % kvh == 0, query head h reads head
+ * h / (nh / kvh); hd is a multiple of 16 of at most 128.  Index arrays
+ * (slots, cu_q, cu_k, lens, starts, page_table, mask) need the alignment of
+ * their type only.  A packed batch of B sequences is described by prefix sums
+ * cu [B + 1] int32, cu[0] <= cu[1] <= ...: sequence b owns rows cu[b] ..
+ * cu[b + 1] - 1 of the packed tensor; rows behind cu[B] belong to nobody and
+ * what they hold in an output is left as it was.  Sequences may be empty.
+ * Sizes that only the device knows (prefix sums, lengths, pages, slots) are
+ * checked there: a sequence or row that breaks its limits is skipped (its
+ * output rows left as they were unless said otherwise), nothing outside the
+ * tensors is read or written, and DS41_E_INDEX is raised in the status word. */
+
+/* The paged cache: K and V each [n_pages, kvh, page, hd], page a power of two
+ * of 16 .. 256, as bf16 (DS41_KV_BF16) or as e4m3 codes (DS41_KV_E4M3) with
+ * scales [n_pages, kvh, page] f32, one per row and head; value = code * scale.
+ * Slot s is row s % page of page s / page.  Scales are NULL for bf16. */
+enum { DS41_KV_BF16 = 0, DS41_KV_E4M3 = 1 };
+
+/* Writes the K and V rows of n tokens into their slots.  For e4m3, per token
+ * and head: scale s = max(amax, 448 * 2^-126) / 448 in f32, codes
+ * e4m3(x / s), round to nearest even.  A row that holds a NaN or an infinity
+ * gets the scale NaN and zero codes.
+ *   k, v   [n, kvh, hd] bf16, heads dense, k_stride / v_stride elements from
+ *          one token to the next (>= kvh * hd, multiples of 8): a slice of a
+ *          fused projection can be given as it is
+ *   slots  [n] int64: -1 = the row is not written (padding, or a drafted token
+ *          that was not accepted); slots of one call are distinct (of rows that
+ *          name the same slot, which codes and which scale stay is undefined).
+ *          A slot outside -1 .. n_pages * page - 1 raises DS41_E_INDEX.
+ * Every other slot is left as it was.  n == 0 is a no-op. */
+int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const ds41_bf16* v,
+                        int64_t v_stride, const int64_t* slots, void* k_cache, void* v_cache,
+                        float* k_scales, float* v_scales, int fmt, int64_t n_pages, int64_t page,
+                        int64_t kvh, int64_t hd, int64_t n, ds41_stream_t stream);
+
+/* Reads rows back, packed: output row r of sequence b (cu_k[b] <= r <
+ * cu_k[b + 1]) is position starts[b] + r - cu_k[b] of the sequence, row
+ * position % page of page page_table[b][position / page]; an e4m3 row comes
+ * as bf16(code * scale).  k and v are what ds41_prompt_attn_fwd takes.
+ *   page_table [B, max_pages] int32;  starts nullable [B] int32 (NULL: 0)
+ *   k, v [rows, kvh, hd] bf16 outputs
+ * A position before 0 or whose page is outside the table or the cache reads
+ * as zeros and raises DS41_E_INDEX.  rows == 0 or B == 0 is a no-op. */
+int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scales,
+                       const float* v_scales, int fmt, int64_t n_pages, int64_t page, int64_t kvh,
+                       int64_t hd, const int32_t* page_table, int64_t max_pages,
+                       const int32_t* cu_k, const int32_t* starts, int64_t B, ds41_bf16* k,
+                       ds41_bf16* v, int64_t rows, ds41_stream_t stream);
+
+/* Scratch bytes ds41_prompt_attn_fwd needs (may be 0). */
+size_t ds41_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t nh,
+                                        int64_t kvh, int64_t hd);
+
+/* Causal attention over whole prompts, packed.  Sequence b has lq = cu_q[b+1]
+ * - cu_q[b] queries and lk = cu_k[b+1] - cu_k[b] keys, aligned at their ends:
+ * query i stands at p = i + lk - lq and sees the keys j with j <= p and, when
+ * window > 0, j > p - window (lk > lq: a chunk behind earlier rows; lk < lq:
+ * the first queries see nothing).  Per query and head
+ *   s_j = scale * <q, k_j>,  o = sum_j e^{s_j} v_j / (e^{sink} + sum_j e^{s_j})
+ * with f32 accumulation and the weights rounded to bf16 for the second
+ * product; a query that sees nothing gets o = 0 and lse = sink (or -inf).
+ *   q [Tq, nh, hd], k and v [Tk, kvh, hd] bf16, each with its own strides in
+ *     elements between tokens and between heads (multiples of 8, hd dense)
+ *   cu_q, cu_k [B + 1] int32;  max_q: no sequence has more queries (a longer
+ *     one raises DS41_E_INDEX)
+ *   sink nullable [nh] f32 (NULL: no sink);  scale > 0;  window >= 0 (0: none)
+ *   o [Tq, nh, hd] bf16 output;  lse nullable [Tq, nh] f32 output, the natural
+ *     log of the denominator
+ * A NaN or an infinity in a v row of a sequence can reach every query of that
+ * sequence (zero weight times NaN), never another sequence.  B == 0, Tq == 0
+ * or max_q == 0 is a no-op; Tk may be 0 (k and v may be NULL then). */
+int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const ds41_bf16* k,
+                         int64_t k_tok, int64_t k_head, const ds41_bf16* v, int64_t v_tok,
+                         int64_t v_head, const int32_t* cu_q, const int32_t* cu_k, int64_t B,
+                         int64_t Tq, int64_t Tk, int64_t max_q, int64_t nh, int64_t kvh,
+                         int64_t hd, float scale, int64_t window, const float* sink, ds41_bf16* o,
+                         float* lse, void* ws, size_t ws_bytes, ds41_stream_t stream);
+
+/* Scratch bytes ds41_tree_attn_fwd needs (may be 0). */
+size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len,
+                                      int64_t nh, int64_t kvh, int64_t hd, int fmt);
+
+/* Attention of drafted tokens over a paged cache: sequence b has len =
+ * lens[b] rows in the cache, the last n = cu_q[b+1] - cu_q[b] of which are its
+ * drafted tokens' own (written before, ds41_kv_cache_write).  Drafted token t
+ * sees every earlier row j < len - n, and drafted row len - n + u when bit
+ * u % 64 of mask[cu_q[b] + t][u / 64] is set (its ancestors and itself; bits
+ * past n are ignored).  mask NULL: a chain, u <= t; n = 1 with it is
+ * single-token decode.  With window > 0 the token stands at p = len - n + d,
+ * d = t without a mask, else the number of bits (below n) set in its mask row
+ * less one, and sees the earlier rows j > p - window only; drafted rows go by
+ * the mask alone, so the window must be at least max_q.  Softmax, sink, o and
+ * lse as ds41_prompt_attn_fwd.
+ *   q [Tq, nh, hd] bf16 with strides q_tok, q_head (multiples of 8, hd dense)
+ *   page_table [B, max_pages] int32;  lens [B] int32, each at least n, at most
+ *     max_len and max_pages * page;  cu_q [B + 1] int32, n <= max_q
+ *   mask nullable [Tq, mask_words] int64, max_q <= 64 * mask_words <= 256
+ * A page outside 0 .. n_pages - 1 raises DS41_E_INDEX and its rows are not
+ * seen.  Rows behind len in the last page are never used, whatever they hold.
+ * A NaN or an infinity in a bf16 v row can reach the tokens of its sequence
+ * that do not see it.  B == 0, Tq == 0 or max_q == 0 is a no-op. */
+int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const void* k_cache,
+                       const void* v_cache, const float* k_scales, const float* v_scales, int fmt,
+                       int64_t n_pages, int64_t page, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* lens, const int32_t* cu_q,
+                       const int64_t* mask, int64_t mask_words, int64_t B, int64_t Tq,
+                       int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t hd,
+                       float scale, int64_t window, const float* sink, ds41_bf16* o, float* lse,
+                       void* ws, size_t ws_bytes, ds41_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
