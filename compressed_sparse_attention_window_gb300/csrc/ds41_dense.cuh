@@ -22,6 +22,13 @@ struct PagedKv {
 int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
                 int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out);
 
+// Host: the heads' counts, the head width, scale and window of a call.
+int check_heads(const char* name, int64_t nh, int64_t kvh, int64_t hd, float scale,
+                int64_t window);
+// strides between tokens and between heads, in elements
+inline bool good_strides(int64_t tok, int64_t head, int64_t hd) {
+    return tok % 8 == 0 && head % 8 == 0 && head >= hd && tok >= hd;
+}
 inline bool aligned_to(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }

@@ -307,71 +307,10 @@ __global__ void __launch_bounds__(NT) dense_attn_kernel(const DenseArgs a) {
     }
 }
 
-int check_heads(const char* name, int64_t nh, int64_t kvh, int64_t hd, float scale,
-                int64_t window) {
-    DS41_REQUIRE(kvh >= 1 && nh >= kvh && nh % kvh == 0 && nh <= 4096, DS41_E_ARG,
-                 "%s: nh=%lld must be a multiple of kvh=%lld", name, (long long)nh, (long long)kvh);
-    DS41_REQUIRE(hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
-                 "%s: hd=%lld must be a multiple of 16 of at most 128", name, (long long)hd);
-    DS41_REQUIRE(scale > 0.0f && scale < INFINITY, DS41_E_ARG, "%s: scale=%g must be positive",
-                 name, (double)scale);
-    DS41_REQUIRE(window >= 0, DS41_E_ARG, "%s: window=%lld", name, (long long)window);
-    return DS41_OK;
-}
-
-bool good_strides(int64_t tok, int64_t head, int64_t heads, int64_t hd) {
-    return tok % 8 == 0 && head % 8 == 0 && head >= hd && tok >= hd && (heads >= 1);
-}
-
 }  // namespace
 }  // namespace ds41
 
 using namespace ds41;
-
-extern "C" size_t ds41_prompt_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t,
-                                                   int64_t) {
-    return 0;
-}
-
-extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
-                                    const ds41_bf16* k, int64_t k_tok, int64_t k_head,
-                                    const ds41_bf16* v, int64_t v_tok, int64_t v_head,
-                                    const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
-                                    int64_t Tk, int64_t max_q, int64_t nh, int64_t kvh, int64_t hd,
-                                    float scale, int64_t window, const float* sink, ds41_bf16* o,
-                                    float* lse, void* ws, size_t ws_bytes, ds41_stream_t stream) {
-    const char* name = "ds41_prompt_attn_fwd";
-    if (int rc = check_heads(name, nh, kvh, hd, scale, window)) return rc;
-    const int64_t lim = int64_t(1) << 31;
-    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && Tk >= 0 && Tk < lim && max_q >= 0 &&
-                     max_q < lim,
-                 DS41_E_RANGE, "%s: B=%lld Tq=%lld Tk=%lld max_q=%lld", name, (long long)B,
-                 (long long)Tq, (long long)Tk, (long long)max_q);
-    if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
-    DS41_REQUIRE(q && o && cu_q && cu_k && (Tk == 0 || (k && v)), DS41_E_ARG,
-                 "%s: q, k, v, cu_q, cu_k and o must be non-null", name);
-    DS41_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(o) &&
-                     aligned_to(cu_q, 4) && aligned_to(cu_k, 4) && aligned_to(sink, 4) &&
-                     aligned_to(lse, 4),
-                 DS41_E_ARG, "%s: q, k, v and o must be 16-byte aligned", name);
-    DS41_REQUIRE(good_strides(q_tok, q_head, nh, hd) &&
-                     (Tk == 0 || (good_strides(k_tok, k_head, kvh, hd) &&
-                                  good_strides(v_tok, v_head, kvh, hd))),
-                 DS41_E_ARG, "%s: strides must be multiples of 8 and at least hd", name);
-    DenseArgs a{};
-    a.q = q; a.q_tok = q_tok; a.q_head = q_head;
-    a.k = k; a.k_tok = k_tok; a.k_head = k_head;
-    a.v = v; a.v_tok = v_tok; a.v_head = v_head;
-    a.cu_q = cu_q; a.cu_k = cu_k; a.Tq = Tq; a.Tk = Tk;
-    a.max_q = (int)max_q; a.nh = (int)nh; a.kvh = (int)kvh; a.hd = (int)hd; a.G = (int)(nh / kvh);
-    a.scale_log2 = scale * LOG2E; a.window = window; a.sink = sink; a.o = o; a.lse = lse;
-    if (int rc = status_word(&a.status)) return rc;
-    const int64_t tiles = (max_q * a.G + ROWS - 1) / ROWS;
-    return launch_pdl(hd <= 64 ? dense_attn_kernel<64, false, false>
-                               : dense_attn_kernel<128, false, false>,
-                      dim3((unsigned)tiles, (unsigned)kvh, (unsigned)B), dim3(NT), 0,
-                      (cudaStream_t)stream, name, a);
-}
 
 extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t,
                                                  int64_t, int64_t, int) {
@@ -410,7 +349,7 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
                      aligned_to(page_table, 4) && aligned_to(mask, 8) && aligned_to(sink, 4) &&
                      aligned_to(lse, 4),
                  DS41_E_ARG, "%s: q and o must be 16-byte aligned", name);
-    DS41_REQUIRE(good_strides(q_tok, q_head, nh, hd), DS41_E_ARG,
+    DS41_REQUIRE(good_strides(q_tok, q_head, hd), DS41_E_ARG,
                  "%s: strides must be multiples of 8 and at least hd", name);
     a.q = q; a.q_tok = q_tok; a.q_head = q_head;
     a.table = page_table; a.max_pages = (int)max_pages; a.lens = lens; a.max_len = (int)max_len;

@@ -43,6 +43,19 @@ int check_paged(const char* name, const void* k, const void* v, const float* ks,
     return DS41_OK;
 }
 
+int check_heads(const char* name, int64_t nh, int64_t kvh, int64_t hd, float scale,
+                int64_t window) {
+    DS41_REQUIRE(kvh >= 1 && nh >= kvh && nh % kvh == 0 && nh <= 4096, DS41_E_ARG,
+                 "%s: nh=%lld must be a multiple of kvh=%lld (at most 4096)", name, (long long)nh,
+                 (long long)kvh);
+    DS41_REQUIRE(hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
+                 "%s: hd=%lld must be a multiple of 16 of at most 128", name, (long long)hd);
+    DS41_REQUIRE(scale > 0.0f && scale <= 3.4028234e38f, DS41_E_ARG,
+                 "%s: scale=%g must be positive", name, (double)scale);
+    DS41_REQUIRE(window >= 0, DS41_E_ARG, "%s: window=%lld", name, (long long)window);
+    return DS41_OK;
+}
+
 namespace {
 
 constexpr int THREADS = 256;

@@ -1,0 +1,638 @@
+// ds41_prompt_attn.cu - causal attention over packed prompts with grouped
+// heads, on the 5th-generation tensor cores.
+//
+// Mathematics.  Per query row and key block of 128, in units of log2 with
+// c = scale log2(e):
+//   S = q K^T,  p_j = 2^(c S_j - c m),  l += sum p_j,  O += p V
+// with a reference m that follows the running maximum of the row; whenever m
+// moves from m0 to m1, l and O are scaled by 2^(c (m0 - m1)).  At the end
+// o = O / (l + 2^(sink - c m)).  m need not be the exact maximum, only close
+// enough that nothing overflows: it moves when a block exceeds it by 2^4, so O
+// is rescaled on the first few blocks of a row and hardly ever after.
+//
+// Rows.  The query heads that share a key/value head see the same keys, so a
+// tile of 128 rows is TT tokens times the G heads of a group (row = token * G +
+// head; G = 4: 32 tokens), and a CTA holds two such tiles over one stream of
+// key/value blocks.
+//
+// Design.  One CTA per SM, warp-specialised: warp 0 issues the TMA copies (two
+// query tiles once, then K and V blocks through a ring of stages), warp 1
+// issues the MMAs, warps 4..7 and 8..11 compute the softmax of tile 0 and of
+// tile 1, a thread per row.  S_t (128 columns of f32) and O_t live in tensor
+// memory; the weights go back as bf16 into the columns of S_t and are the A
+// operand of the second product from there, so neither S nor P touches shared
+// memory.  Issue order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1): while the softmax of
+// one tile runs, the tensor core works on the other.  A commit after QK_t(j+1)
+// also covers PV_t(j), so a softmax thread that has seen S_t(j+1) may rescale
+// its row of O_t itself: no fourth role, no further barrier.
+#include "ds41_dense.cuh"
+#include "ds41_tc.cuh"
+
+namespace ds41 {
+namespace pa {
+
+using namespace tc;
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 4.0f;
+constexpr int KB = 128;         // keys per block
+constexpr int ROWS = 128;       // rows per tile
+constexpr int THREADS = 384;
+
+template <int D>
+struct Cfg {
+    static constexpr int NB = D / 64;                   // 64-column blocks of a row
+    static constexpr uint32_t BLK = 128 * 128;          // [128 rows][64 columns] bf16
+    static constexpr uint32_t TILE = NB * BLK;          // a query tile, or a K or V block
+    static constexpr int STAGES = D == 128 ? 5 : 10;
+    static constexpr uint32_t Q_OFF = 0;                // two query tiles
+    static constexpr uint32_t KV_OFF = 2 * TILE;
+    static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
+    static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// tensor memory columns: S_0 S_1 O_0 O_1
+constexpr uint32_t TM_S = 0, TM_O = 256;
+
+struct Params {
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    const float* sink;
+    uint16_t* o;
+    float* lse;
+    int64_t Tq, Tk, window;
+    int B, max_q, nh, hd;
+    int G;        // heads of a tile
+    int TT;       // tokens of a tile
+    int n_groups; // key/value heads times tiles' head groups per key/value head
+    int subs;     // head groups per key/value head
+    float c;      // scale * log2(e)
+    unsigned int* status;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// D += A B with A in tensor memory (bf16, two per column, lane = row)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A CTA's work: one head group of one pair of tiles of one sequence.
+struct Item {
+    int b;          // sequence, -1: none
+    int q0, n;      // its queries
+    int k0, len;    // its keys
+    int t0;         // first token of tile 0
+};
+
+// The key blocks [lo, hi) that some row of tile t sees; count = its tokens.
+struct Range {
+    int lo, hi, count, p_first;
+};
+__device__ __forceinline__ Range tile_range(const Item& it, const Params& p, int t) {
+    Range r;
+    const int first = it.t0 + t * p.TT;
+    r.count = max(0, min(p.TT, it.n - first));
+    r.p_first = first + it.len - it.n;
+    r.lo = r.hi = 0;
+    if (r.count > 0) {
+        const int64_t last = r.p_first + (int64_t)r.count - 1;
+        if (last >= 0) {
+            r.hi = (int)(last / KB) + 1;
+            const int64_t lo = p.window ? max((int64_t)0, r.p_first - p.window + 1) : 0;
+            r.lo = (int)(lo / KB);
+        }
+    }
+    return r;
+}
+
+// Sequence and tile pair of flat index w (a warp; every lane gets the result).
+// A sequence that breaks its limits has no tiles.  Tiles of a sequence come
+// in falling order: the longest first.
+__device__ Item find_item(const Params& p, int w, bool report, int lane) {
+    Item it;
+    it.b = -1;
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        int q0 = 0, n = 0, k0 = 0, len = 0, tiles = 0;
+        if (b < p.B) {
+            q0 = p.cu_q[b];
+            k0 = p.cu_k[b];
+            const int64_t ln = (int64_t)p.cu_q[b + 1] - q0, lk = (int64_t)p.cu_k[b + 1] - k0;
+            const bool ok = q0 >= 0 && ln >= 0 && ln <= p.max_q && q0 + ln <= p.Tq && k0 >= 0 &&
+                            lk >= 0 && k0 + lk <= p.Tk;
+            if (ok) {
+                n = (int)ln;
+                len = (int)lk;
+                tiles = (n + 2 * p.TT - 1) / (2 * p.TT);
+            } else if (report) {
+                raise_status(p.status, DS41_E_INDEX);
+            }
+        }
+        int sum = tiles;  // inclusive prefix sum over the lanes
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += v;
+        }
+        const unsigned mine = __ballot_sync(0xffffffffu, it.b < 0 && w >= base + sum - tiles &&
+                                                             w < base + sum);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            it.b = b0 + src;
+            it.q0 = __shfl_sync(0xffffffffu, q0, src);
+            it.n = __shfl_sync(0xffffffffu, n, src);
+            it.k0 = __shfl_sync(0xffffffffu, k0, src);
+            it.len = __shfl_sync(0xffffffffu, len, src);
+            const int end = base + __shfl_sync(0xffffffffu, sum, src);
+            it.t0 = (end - 1 - w) * 2 * p.TT;
+            if (!report) return it;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const Params p) {
+    pdl_wait();
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+    uint64_t* b_q = bars;                      // queries landed
+    uint64_t* b_full = bars + 1;               // stage landed
+    uint64_t* b_empty = b_full + C::STAGES;    // stage read
+    uint64_t* b_s = b_empty + C::STAGES;       // S_t in tensor memory [2]
+    uint64_t* b_p = b_s + 2;                   // P_t in tensor memory, O_t rescaled [2]
+    uint64_t* b_o = b_p + 2;                   // O_t complete [2]
+    uint64_t* b_tail = b_o + 2;                // the V block that ends behind the last key landed
+    uint64_t* b_fix = b_tail + 1;              // its rows behind the last key are zero
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_fix + 1);
+    volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* sh_item = reinterpret_cast<int*>(tmem_slot + 2);
+    static_assert((1 + 2 * C::STAGES + 8) * 8 + 8 + 6 * 4 <= 512, "barrier area");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int grp = blockIdx.x % p.n_groups;
+    const int w = blockIdx.x / p.n_groups;
+
+    if (warp == 0) {
+        const Item it = find_item(p, w, blockIdx.x == 0, lane);
+        if (lane == 0) {
+            sh_item[0] = it.b;
+            sh_item[1] = it.q0;
+            sh_item[2] = it.n;
+            sh_item[3] = it.k0;
+            sh_item[4] = it.len;
+            sh_item[5] = it.t0;
+        }
+    }
+    if (threadIdx.x == 32) {
+        mbar_init(b_q, 1);
+        for (int s = 0; s < C::STAGES; s++) {
+            mbar_init(&b_full[s], 1);
+            mbar_init(&b_empty[s], 1);
+        }
+        for (int t = 0; t < 2; t++) {
+            mbar_init(&b_s[t], 1);
+            mbar_init(&b_p[t], 4);
+            mbar_init(&b_o[t], 1);
+        }
+        mbar_init(b_tail, 1);
+        mbar_init(b_fix, 1);
+        *abort_f = 0;
+        mbar_init_fence();
+    }
+    __syncthreads();
+    Item it;
+    it.b = sh_item[0];
+    if (it.b < 0) return;
+    it.q0 = sh_item[1];
+    it.n = sh_item[2];
+    it.k0 = sh_item[3];
+    it.len = sh_item[4];
+    it.t0 = sh_item[5];
+    if (warp == 1) {
+        asm volatile(
+            "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                smem_u32(tmem_slot))
+            : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    // rows of the query tiles that no copy fills
+    const int used = p.TT * p.G;
+    if (used < ROWS) {
+        const int per = (ROWS - used) * 8;  // 16-byte pieces of one 64-column block
+        for (int x = threadIdx.x; x < 2 * C::NB * per; x += THREADS)
+            *reinterpret_cast<uint4*>(sm + C::Q_OFF + (x / per) * C::BLK + used * 128 +
+                                      (x % per) * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    }
+    const Range rg[2] = {tile_range(it, p, 0), tile_range(it, p, 1)};
+    int jlo = rg[0].lo, jhi = rg[0].hi;
+    if (rg[1].hi > rg[1].lo) {
+        jlo = rg[0].hi > rg[0].lo ? min(jlo, rg[1].lo) : rg[1].lo;
+        jhi = max(jhi, rg[1].hi);
+    }
+    // keys of the last block when it is not full: the rest of its V rows belong
+    // to another sequence (or to nobody)
+    const int tail = (jhi * KB > it.len) ? it.len - (jhi - 1) * KB : 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+        if (warp == 0 && lane == 0 && jhi > jlo) {
+            const int head0 = grp * p.G;
+            const int kvh = grp / p.subs;
+            uint32_t q_tiles = 0;
+            for (int t = 0; t < 2; t++) q_tiles += rg[t].hi > rg[t].lo;
+            mbar_arrive_expect_tx(b_q, q_tiles * C::NB * (uint32_t)used * 128);
+            for (int t = 0; t < 2; t++)
+                if (rg[t].hi > rg[t].lo)
+                    for (int x = 0; x < C::NB; x++)
+                        tma_load_3d(sbase + C::Q_OFF + t * C::TILE + x * C::BLK, &map_q, 64 * x,
+                                    head0, it.q0 + it.t0 + t * p.TT, b_q);
+            uint32_t n = 0;
+            bool ok = true;
+            for (int j = jlo; j < jhi && ok; j++) {
+                for (int kv = 0; kv < 2; kv++, n++) {
+                    const uint32_t s = n % C::STAGES, use = n / C::STAGES;
+                    if (use > 0 && !wait_bar(&b_empty[s], (use - 1) & 1, abort_f, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&b_full[s], C::TILE);
+                    for (int x = 0; x < C::NB; x++)
+                        tma_load_3d(sbase + C::KV_OFF + s * C::TILE + x * C::BLK,
+                                    kv ? &map_v : &map_k, 64 * x, kvh, it.k0 + j * KB,
+                                    &b_full[s]);
+                }
+            }
+            // everything that was started lands before the CTA ends
+            drain_bar(b_q, 0, p.status);
+            for (uint32_t s = 0; s < C::STAGES && s < n; s++)
+                drain_bar(&b_full[s], ((n - 1 - s) / C::STAGES) & 1, p.status);
+        } else if (warp == 1 && lane == 0 && jhi > jlo) {
+            const uint32_t IDESC_S = idesc_bf16(128, KB, 0, 0);
+            const uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
+            const int ksteps = p.hd / 16;
+            const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
+            const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
+            const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
+            uint32_t done_p[2] = {0, 0};
+            auto stage_of = [&](int j, int kv) { return (uint32_t)(2 * (j - jlo) + kv); };
+            auto wait_stage = [&](uint32_t n) {
+                const bool ok =
+                    wait_bar(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
+                tc_fence_after();
+                return ok;
+            };
+            auto qk = [&](int t, uint32_t n) {
+                const uint64_t a = qd + ((t * C::TILE) >> 4);
+                const uint64_t b = kd + (((n % C::STAGES) * C::TILE) >> 4);
+#pragma unroll
+                for (int k = 0; k < D / 16; k++)
+                    if (k < ksteps)
+                        tc_mma(tmem + TM_S + 128 * t, a + (((k >> 2) * C::BLK + (k & 3) * 32) >> 4),
+                               b + (((k >> 2) * C::BLK + (k & 3) * 32) >> 4), IDESC_S, k > 0);
+                tc_commit(&b_s[t]);
+            };
+            auto pv = [&](int t, uint32_t n, int steps, bool acc) {
+                const uint64_t b = vd + (((n % C::STAGES) * C::TILE) >> 4);
+#pragma unroll
+                for (int k = 0; k < KB / 16; k++)
+                    if (k < steps)
+                        tc_mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * k,
+                                  b + ((k * 2048) >> 4), IDESC_O, acc || k > 0);
+            };
+            bool ok = wait_bar(b_q, 0, abort_f, p.status) && wait_stage(0);
+            if (ok) {
+                for (int t = 0; t < 2; t++)
+                    if (jlo >= rg[t].lo && jlo < rg[t].hi) qk(t, 0);
+                tc_commit(&b_empty[0]);
+            }
+            for (int j = jlo; j < jhi && ok; j++) {
+                const uint32_t nv = stage_of(j, 1), nk = stage_of(j + 1, 0);
+                ok = wait_stage(nv);
+                const bool last = j == jhi - 1 && tail > 0;
+                if (ok && last) {
+                    mbar_arrive(b_tail);
+                    ok = wait_bar(b_fix, 0, abort_f, p.status);
+                    tc_fence_after();
+                }
+                const int steps = last ? (tail + 15) / 16 : KB / 16;
+                bool have_k = false;
+                for (int t = 0; t < 2 && ok; t++) {
+                    if (j >= rg[t].lo && j < rg[t].hi) {
+                        if (!wait_bar(&b_p[t], done_p[t] & 1, abort_f, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        done_p[t]++;
+                        tc_fence_after();
+                        pv(t, nv, steps, j > rg[t].lo);
+                        if (j + 1 == rg[t].hi) tc_commit(&b_o[t]);
+                    }
+                    if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
+                    if (j + 1 >= rg[t].lo && j + 1 < rg[t].hi) {
+                        if (!have_k && !wait_stage(nk)) {
+                            ok = false;
+                            break;
+                        }
+                        have_k = true;
+                        qk(t, nk);
+                    }
+                }
+                if (ok && j + 1 < jhi) {
+                    if (!have_k) ok = wait_stage(nk);
+                    tc_commit(&b_empty[nk % C::STAGES]);
+                }
+            }
+        } else if (warp == 2 && tail > 0 && jhi > jlo) {
+            // zero the V rows behind the last key, up to the next multiple of 16
+            const uint32_t n = 2 * (uint32_t)(jhi - 1 - jlo) + 1, s = n % C::STAGES;
+            if (wait_bar(b_tail, 0, abort_f, p.status)) {
+                const int rows = ((tail + 15) / 16) * 16 - tail;
+                for (int x = lane; x < rows * C::NB * 8; x += 32) {
+                    const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
+                    *reinterpret_cast<uint4*>(sm + C::KV_OFF + s * C::TILE + (piece / 8) * C::BLK +
+                                              r * 128 + (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_fix);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+        const int t = (warp - 4) >> 2;
+        const Range r = rg[t];
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tm_s = tmem + lanes + TM_S + 128 * t, tm_o = tmem + lanes + TM_O + 128 * t;
+        const int row = 32 * (warp & 3) + lane;
+        const int tok = row / p.G, gh = row - tok * p.G;
+        const bool live = tok < r.count;
+        const int64_t pos = (int64_t)r.p_first + tok;              // the last key it sees
+        const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
+        const int64_t p_last = (int64_t)r.p_first + r.count - 1;
+        const float c = p.c;
+        float m = -INFINITY, l = 0.0f;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int j = r.lo; j < r.hi; j++, ph++) {
+            if (!wait_bar(&b_s[t], ph & 1, abort_f, p.status)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
+            tc_wait_ld();
+            const int64_t j0 = (int64_t)j * KB;
+            if (j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window)) {
+                const int hi = (int)max((int64_t)-1, min((int64_t)KB, pos - j0));
+                const int lo = (int)max((int64_t)-1, min((int64_t)KB, before - j0));
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int e = 0; e < 32; e++)
+                        if (32 * i + e > hi || 32 * i + e <= lo) s[i][e] = 0xff800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                for (int e = 1; e < 32; e++) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // (-inf - -inf is NaN: no move)
+            const bool move = (top - m) * c > RESCALE_LOG2 && live;
+            if (__any_sync(0xffffffffu, move)) {
+                const float to = move ? top : m;
+                const float f = move ? ex2((m - to) * c) : 1.0f;
+                m = to;
+                l *= f;
+                if (j > r.lo) {
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t ov[32];
+                        tc_ld32(tm_o + x, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e++)
+                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                        tc_st32(tm_o + x, ov);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.0f : m * c;
+            float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float a0 = ex2(fmaf(__uint_as_float(s[2 * h + i][e]), c, -base));
+                        const float a1 = ex2(fmaf(__uint_as_float(s[2 * h + i][e + 1]), c, -base));
+                        sum[2 * i] += a0;
+                        sum[2 * i + 1] += a1;
+                        pk[16 * i + e / 2] = bf16x2(a0, a1);
+                    }
+                tc_st32(tm_s + 32 * h, pk);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b_p[t]);
+        }
+        // the sink is one more term of the denominator
+        const int head = grp * p.G + gh;
+        const float snk = live && p.sink ? p.sink[head] * LOG2E : -INFINITY;
+        const float mc = m == -INFINITY ? -INFINITY : m * c;
+        const float top = fmaxf(mc, snk);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float f = ex2(mc - base);
+        const float den = l * f + ex2(snk - base);
+        const float inv = den == 0.0f ? 0.0f : f / den;
+        const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
+        if (live && ok && p.lse) p.lse[at] = (base + log2f(den)) * LN2;
+        if (r.count > 0 && ok) {
+            uint16_t* dst = p.o + at * p.hd;
+            if (r.hi > r.lo) {
+                ok = wait_bar(&b_o[t], 0, abort_f, p.status);
+                tc_fence_after();
+            }
+            if (ok) {
+#pragma unroll
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t ov[32] = {};
+                    if (r.hi > r.lo) {
+                        tc_ld32(tm_o + x, ov);
+                        tc_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        if (live && x + e < p.hd) {
+                            uint4 v;
+                            v.x = bf16x2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
+                            v.y = bf16x2(__uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
+                            v.z = bf16x2(__uint_as_float(ov[e + 4]) * inv, __uint_as_float(ov[e + 5]) * inv);
+                            v.w = bf16x2(__uint_as_float(ov[e + 6]) * inv, __uint_as_float(ov[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(dst + x + e) = v;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem)
+                     : "memory");
+}
+
+// [tokens][heads][hd] with strides in elements; a box of 64 columns x box_h
+// heads x box_t tokens, 128-byte swizzle, zeros outside.
+int make_map_heads(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const void* ptr,
+                   int64_t tokens, int64_t heads, int64_t hd, int64_t tok, int64_t head, int box_h,
+                   int box_t) {
+    cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)tok * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_h, (cuuint32_t)box_t};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(DS41_E_CUDA, "cuTensorMapEncodeTiled (heads) failed (%d)", (int)r);
+    return DS41_OK;
+}
+
+}  // namespace pa
+}  // namespace ds41
+
+using namespace ds41;
+
+extern "C" size_t ds41_prompt_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t,
+                                                   int64_t) {
+    return 0;
+}
+
+extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
+                                    const ds41_bf16* k, int64_t k_tok, int64_t k_head,
+                                    const ds41_bf16* v, int64_t v_tok, int64_t v_head,
+                                    const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
+                                    int64_t Tk, int64_t max_q, int64_t nh, int64_t kvh, int64_t hd,
+                                    float scale, int64_t window, const float* sink, ds41_bf16* o,
+                                    float* lse, void* ws, size_t ws_bytes, ds41_stream_t stream) {
+    const char* name = "ds41_prompt_attn_fwd";
+    if (int rc = check_heads(name, nh, kvh, hd, scale, window)) return rc;
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && Tk >= 0 && Tk < lim && max_q >= 0 &&
+                     max_q < lim,
+                 DS41_E_RANGE, "%s: B=%lld Tq=%lld Tk=%lld max_q=%lld", name, (long long)B,
+                 (long long)Tq, (long long)Tk, (long long)max_q);
+    if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
+    DS41_REQUIRE(q && o && cu_q && cu_k && (Tk == 0 || (k && v)), DS41_E_ARG,
+                 "%s: q, k, v, cu_q, cu_k and o must be non-null", name);
+    DS41_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(o) &&
+                     aligned_to(cu_q, 4) && aligned_to(cu_k, 4) && aligned_to(sink, 4) &&
+                     aligned_to(lse, 4),
+                 DS41_E_ARG, "%s: q, k, v and o must be 16-byte aligned", name);
+    DS41_REQUIRE(good_strides(q_tok, q_head, hd) &&
+                     (Tk == 0 ||
+                      (good_strides(k_tok, k_head, hd) && good_strides(v_tok, v_head, hd))),
+                 DS41_E_ARG, "%s: strides must be multiples of 8 and at least hd", name);
+    pa::Params p{};
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.sink = sink;
+    p.o = o;
+    p.lse = lse;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.window = window;
+    p.B = (int)B;
+    p.max_q = (int)max_q;
+    p.nh = (int)nh;
+    p.hd = (int)hd;
+    p.c = scale * pa::LOG2E;
+    // heads per tile: the whole group, or its largest divisor that fits
+    int G = (int)(nh / kvh);
+    p.subs = 1;
+    if (G > pa::ROWS) {
+        int d = pa::ROWS;
+        while (G % d) d--;
+        p.subs = G / d;
+        G = d;
+    }
+    p.G = G;
+    p.TT = pa::ROWS / G;
+    p.n_groups = (int)kvh * p.subs;
+    if (int rc = status_word(&p.status)) return rc;
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = tc::get_encode(&enc)) return rc;
+    CUtensorMap mq, mk, mv;
+    if (int rc = pa::make_map_heads(enc, &mq, q, Tq, nh, hd, q_tok, q_head, G, p.TT)) return rc;
+    if (Tk > 0) {
+        if (int rc = pa::make_map_heads(enc, &mk, k, Tk, kvh, hd, k_tok, k_head, 1, pa::KB))
+            return rc;
+        if (int rc = pa::make_map_heads(enc, &mv, v, Tk, kvh, hd, v_tok, v_head, 1, pa::KB))
+            return rc;
+    } else {
+        mk = mv = mq;  // never read
+    }
+    // every sequence has at most one tile pair that is not full
+    const int64_t pairs = Tq / (2 * p.TT) + B;
+    const int64_t blocks = pairs * p.n_groups;
+    DS41_REQUIRE(blocks < lim, DS41_E_RANGE, "%s: Tq=%lld B=%lld kvh=%lld", name, (long long)Tq,
+                 (long long)B, (long long)kvh);
+    auto kern = hd <= 64 ? pa::prompt_attn_kernel<64> : pa::prompt_attn_kernel<128>;
+    const size_t smem = hd <= 64 ? pa::Cfg<64>::SMEM : pa::Cfg<128>::SMEM;
+    if (int rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)smem),
+                            name))
+        return rc;
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(pa::THREADS), smem, (cudaStream_t)stream,
+                      name, mq, mk, mv, p);
+}
