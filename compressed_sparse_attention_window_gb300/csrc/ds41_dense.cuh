@@ -39,14 +39,13 @@ __device__ __forceinline__ int64_t paged_row(const PagedKv& c, int64_t pg, int h
     return (pg * c.kvh + h) * c.page + off;
 }
 
-// Two e4m3 codes (low byte first) -> their exact values as bf16x2.  The code's
-// exponent and mantissa bits moved into a bf16's give the value times 2^-120
-// (exponent bias 7 against 127, subnormals included), so one exact bf16
-// product restores it.  A NaN code (0x7f, 0xff) would come out as +-480, so
-// the caller that has to keep NaN uses e4m3x2_to_bf16x2_nan.
-__device__ __forceinline__ uint32_t e4m3_spread(uint32_t hi_bytes) {
-    // hi_bytes: a code in the upper byte of each half, the lower bytes zero
-    const uint32_t r = (hi_bytes & 0x80008000u) | ((hi_bytes >> 4) & 0x07f007f0u);
+// Two e4m3 codes, in the upper bytes of the halves of x (the lower bytes are
+// ignored), as bf16x2, exact.  The code's exponent and mantissa bits moved into
+// a bf16's give the value times 2^-120 (exponent bias 7 against 127, subnormals
+// included); one exact bf16 product restores it.  The NaN codes 0x7f and 0xff,
+// which the cache never holds, would come out as +-480.
+__device__ __forceinline__ uint32_t e4m3_spread(uint32_t x) {
+    const uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
     uint32_t out;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out) : "r"(r), "r"(0x7b807b80u));  // 2^120
     return out;

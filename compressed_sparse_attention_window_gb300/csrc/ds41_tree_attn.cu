@@ -1,0 +1,514 @@
+// ds41_tree_attn.cu - attention of drafted tokens (or of one token, plain
+// decode) over a paged cache, few rows per key/value head.
+//
+// Mathematics.  One pass with a running reference m and sum l per row, in units
+// of log2: t_j = scale log2(e) ks_j <q, k_j> (ks_j, vs_j: the row's scales, 1
+// for bf16), p_j = 2^(t_j - m), l += p_j, O += (p_j vs_j) v_j, the weights
+// rounded to bf16 for the tensor cores.  m follows the running maximum lazily:
+// it moves (and l and O are rescaled) when a score exceeds it by 2^4.  The codes
+// of an e4m3 row are exact in bf16, so the scales stay outside the products.
+//
+// Rows.  All queries of a (sequence, key/value head): tokens times the G heads
+// that share it, 16 rows a CTA (the M of an m16n8k16 product).
+//
+// What bounds it.  Every cache row is read once for 16 rows of queries: HBM
+// bandwidth, if enough is in flight and the conversion of codes keeps up.  So
+// the keys of a sequence are split over CTAs (chunks of a length that fills the
+// GPU), every warp streams its own 16-key groups (a group lies in one page, so
+// its K and its V are one contiguous run each) through a private ring of
+// cp.async stages, with no barrier between warps until the end, and the fragments
+// are taken from shared memory with an order of hd (for Q K^T) and of the output
+// columns (for P V) in which each lane's share is contiguous: the same order on
+// both operands leaves the product unchanged.  The codes are widened in
+// registers on the way into the products.
+#include "ds41_internal.cuh"
+#include "ds41_tree.cuh"
+
+namespace ds41 {
+namespace tree {
+
+constexpr int WARPS = 4;
+constexpr int NT = WARPS * 32;
+constexpr int GROUP = 16;  // keys of a group
+
+template <int HD, bool E4M3>
+struct Cfg {
+    static constexpr int RB = HD * (E4M3 ? 1 : 2);          // bytes of a row's slot
+    static constexpr int STAGES = RB == 256 ? 3 : 4;
+    static constexpr int STAGE = 2 * GROUP * RB + 2 * GROUP * 4;  // K, V, their scales
+    static constexpr int SMEM = WARPS * STAGES * STAGE;
+    static constexpr int CH = RB / 16;                       // 16-byte pieces of a row
+    static constexpr int MERGE = WARPS * 16 * (HD + 4) * 4;  // the warps' results
+    static constexpr int BYTES = SMEM > MERGE ? SMEM : MERGE;
+};
+
+// Where piece ch of row r lies: rows that one quarter-warp reads together fall
+// into different banks.
+template <int RB>
+__device__ __forceinline__ int k_piece(int r, int ch) {
+    return RB == 64 ? ch : ch ^ ((r & 1) << 2);
+}
+template <int RB>
+__device__ __forceinline__ int v_piece(int r, int ch) {
+    const int c = (r >> 1) & 3;
+    return RB == 64 ? ch ^ ((c & 1) << 1) : RB == 128 ? ch ^ (c << 1) : ch ^ ((c & 1) | ((c >> 1) << 2));
+}
+
+template <int HD, bool E4M3>
+__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a) {
+    pdl_wait();
+    using C = Cfg<HD, E4M3>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int split = blockIdx.x, h = blockIdx.y % a.kvh, rt = blockIdx.y / a.kvh, b = blockIdx.z;
+    const Seq s = load_seq(a, b);
+    if (!s.ok) {
+        if (threadIdx.x == 0) raise_status(a.status, DS41_E_INDEX);
+        return;
+    }
+    const int rows = s.n * a.G, r0 = rt * 16;
+    if (r0 >= rows) return;
+    const int k_first = first_key(a, s);
+    const int k0 = k_first + split * a.chunk, k1 = min(s.len, k0 + a.chunk);
+    if (k0 >= k1 && split > 0) return;  // (a sequence without keys has its split 0)
+
+    uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
+    const int n_groups = k0 < k1 ? (k1 - k0 + GROUP - 1) / GROUP : 0;
+    const int mine = (n_groups - warp + WARPS - 1) / WARPS;  // groups warp, warp + 4, ...
+    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    unsigned bad = 0;  // stages whose page does not exist
+
+    auto fetch = [&](int i) {
+        if (i < mine) {
+            const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
+            const int64_t pg = table[j >> a.kv.page_shift];
+            const bool ok = pg >= 0 && pg < a.kv.n_pages;
+            if (!ok && lane == 0) raise_status(a.status, DS41_E_INDEX);
+            bad = ok ? bad & ~(1u << st) : bad | (1u << st);
+            const int64_t row = paged_row(a.kv, ok ? pg : 0, h, j & (a.kv.page - 1));
+            const uint32_t dst = smem_u32(ring + st * C::STAGE);
+            const int rb = a.hd * (E4M3 ? 1 : 2);  // bytes of a row in the cache
+            // rows behind the sequence's end are read as zeros, whatever they hold
+            const int live = ok ? min(GROUP, k1 - j) : 0;
+#pragma unroll
+            for (int x = 0; x < GROUP * C::CH / 32; x++) {
+                const int r = (x * 32 + lane) / C::CH, ch = (x * 32 + lane) % C::CH;
+                const bool in = r < live && ch * 16 < rb;
+                const int64_t off = in ? (row + r) * rb + ch * 16 : 0;
+                cp_async16(dst + r * C::RB + k_piece<C::RB>(r, ch) * 16, a.kv.k + off, in);
+                cp_async16(dst + GROUP * C::RB + r * C::RB + v_piece<C::RB>(r, ch) * 16,
+                           a.kv.v + off, in);
+            }
+            if (E4M3 && lane < 8) {
+                const float* src = lane < 4 ? a.kv.ks : a.kv.vs;
+                cp_async16(dst + 2 * GROUP * C::RB + lane * 16, src + row + (lane & 3) * 4, ok);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; i++) fetch(i);
+
+    // the queries: rows g and g + 8 of the tile, hd in the order of the keys'
+    // fragments (fp8: lane c owns bytes 16 c .. and 64 + 16 c .. of a row, bf16:
+    // 16 c + 64 i ..; four elements a step)
+    RowView view[2];
+    uint32_t qf[HD / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int r = min(r0 + g + 8 * i, rows - 1);
+        const int t = r / a.G;
+        view[i] = row_view(a, s, t);
+        const uint16_t* qp = a.q + (s.q0 + t) * a.q_tok + (h * a.G + r % a.G) * a.q_head;
+#pragma unroll
+        for (int st = 0; st < HD / 16; st++) {
+            const int d = E4M3 ? (c + 4 * (st / 4)) * 16 + 4 * (st % 4)
+                               : (c + 4 * (st / 2)) * 8 + 4 * (st % 2);
+            const uint2 v = d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
+            // of four codes in a word the even ones spread together, then the odd
+            qf[st][i] = E4M3 ? __byte_perm(v.x, v.y, 0x5410) : v.x;
+            qf[st][i + 2] = E4M3 ? __byte_perm(v.x, v.y, 0x7632) : v.y;
+        }
+    }
+    // keys below `easy` are seen by both rows (and none lies at or before lo)
+    const int easy = min(view[0].pre, view[1].pre);
+    const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
+
+    float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
+    for (int i = 0; i < mine; i++) {
+        fetch(i + C::STAGES - 1);
+        cp_async_wait<C::STAGES - 1>();
+        __syncwarp();
+        const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
+        const uint8_t* kx = ring + st * C::STAGE;
+        const uint8_t* vx = kx + GROUP * C::RB;
+        const float* sx = reinterpret_cast<const float*>(kx + 2 * GROUP * C::RB);
+        float sc[2][4] = {};
+        // ---- S = Q K^T ----
+#pragma unroll
+        for (int x = 0; x < C::CH / 4; x++) {
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const int r = n * 8 + g;
+                const uint4 kv = *reinterpret_cast<const uint4*>(
+                    kx + r * C::RB + k_piece<C::RB>(r, c + 4 * x) * 16);
+                const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+                if (E4M3) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int q = 4 * x + e;
+                        mma_bf16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3],
+                                 e4m3_spread(w[e] << 8), e4m3_spread(w[e]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int q = 2 * x + e;
+                        mma_bf16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], w[2 * e],
+                                 w[2 * e + 1]);
+                    }
+                }
+            }
+        }
+        // ---- softmax: this lane has rows g, g + 8 and keys 2c, 2c+1, 2c+8, 2c+9 ----
+        float2 ks[2], vs[2];
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+            ks[n] = E4M3 ? *reinterpret_cast<const float2*>(sx + n * 8 + 2 * c) : make_float2(1, 1);
+            vs[n] = E4M3 ? *reinterpret_cast<const float2*>(sx + 16 + n * 8 + 2 * c)
+                         : make_float2(1, 1);
+            ks[n].x *= a.scale_log2;
+            ks[n].y *= a.scale_log2;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
+        if ((bad >> st) & 1) {
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[n][e] = -INFINITY;
+        } else if (j + GROUP > easy || j <= lo) {
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (!seen(view[e >> 1], j + n * 8 + 2 * c + (e & 1), s.len))
+                        sc[n][e] = -INFINITY;
+        }
+        float mx[2];
+#pragma unroll
+        for (int i2 = 0; i2 < 2; i2++)
+            mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
+                           fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + RESCALE_LOG2 || mx[1] > m[1] + RESCALE_LOG2)) {
+#pragma unroll
+            for (int i2 = 0; i2 < 2; i2++) {
+                float t = mx[i2];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                if (t > m[i2] + RESCALE_LOG2) {
+                    const float f = exp2f(m[i2] - t);
+                    m[i2] = t;
+                    l[i2] *= f;
+#pragma unroll
+                    for (int d = 0; d < HD / 8; d++) {
+                        o[d][2 * i2] *= f;
+                        o[d][2 * i2 + 1] *= f;
+                    }
+                }
+            }
+        }
+        uint32_t pf[4];
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int i2 = 0; i2 < 2; i2++) {
+                const float base = m[i2] == -INFINITY ? 0.0f : m[i2];
+                const float p0 = ex2(sc[n][2 * i2] - base), p1 = ex2(sc[n][2 * i2 + 1] - base);
+                l[i2] += p0 + p1;
+                // a row that is not seen weighs nothing, whatever its scale holds
+                const float w0 = sc[n][2 * i2] == -INFINITY ? 0.0f : p0 * vs[n].x;
+                const float w1 = sc[n][2 * i2 + 1] == -INFINITY ? 0.0f : p1 * vs[n].y;
+                pf[2 * n + i2] = bf16x2(w0, w1);
+            }
+        // ---- O += P V: n-tile d holds the columns g HD/8 + d ----
+        if (E4M3) {
+            uint32_t w[4][HD / 32];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                if (HD == 128) {
+                    *reinterpret_cast<uint4*>(w[r]) = *reinterpret_cast<const uint4*>(
+                        vx + row * C::RB + v_piece<C::RB>(row, g) * 16);
+                } else {
+                    *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(
+                        vx + row * C::RB + v_piece<C::RB>(row, g >> 1) * 16 + (g & 1) * 8);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < HD / 8; d += 2) {
+                // bytes d, d + 1 of two rows
+                const uint32_t s0 = (d & 2) ? 0x7632u : 0x5410u;
+                const uint32_t x0 = __byte_perm(w[0][d / 4], w[1][d / 4], s0);
+                const uint32_t x1 = __byte_perm(w[2][d / 4], w[3][d / 4], s0);
+                mma_bf16(o[d], pf[0], pf[1], pf[2], pf[3], e4m3_spread(x0 << 8),
+                         e4m3_spread(x1 << 8));
+                mma_bf16(o[d + 1], pf[0], pf[1], pf[2], pf[3], e4m3_spread(x0),
+                         e4m3_spread(x1));
+            }
+        } else {
+            uint32_t w[4][HD / 16];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+                for (int x = 0; x < HD / 64; x++)
+                    *reinterpret_cast<uint4*>(w[r] + 4 * x) = *reinterpret_cast<const uint4*>(
+                        vx + row * C::RB + v_piece<C::RB>(row, g * (HD / 64) + x) * 16);
+            }
+#pragma unroll
+            for (int d = 0; d < HD / 8; d++) {
+                const uint32_t sel = (d & 1) ? 0x7632u : 0x5410u;
+                mma_bf16(o[d], pf[0], pf[1], pf[2], pf[3],
+                         __byte_perm(w[0][d / 2], w[1][d / 2], sel),
+                         __byte_perm(w[2][d / 2], w[3][d / 2], sel));
+            }
+        }
+        __syncwarp();  // the stage is read before it is filled again
+    }
+    pdl_trigger();
+    cp_async_wait<0>();
+    __syncthreads();
+    // ---- the warps' results: through shared memory, 16 rows ----
+    constexpr int P = HD + 4;
+    float* out = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        float* row = out + (warp * 16 + g + 8 * i) * P;
+        if (c == 0) {
+            row[HD] = m[i];
+            row[HD + 1] = l[i];
+        }
+#pragma unroll
+        for (int d = 0; d < HD / 8; d++) {
+            row[2 * c * (HD / 8) + d] = o[d][2 * i];
+            row[(2 * c + 1) * (HD / 8) + d] = o[d][2 * i + 1];
+        }
+    }
+    __syncthreads();
+    constexpr int PER = NT / 16;  // threads of a row
+    const int row = threadIdx.x / PER, part = threadIdx.x % PER;
+    const int r = r0 + row;
+    if (r >= rows) return;
+    float mm = -INFINITY, f[WARPS], ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + row) * P + HD]);
+    const float base = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) {
+        f[w] = exp2f(out[(w * 16 + row) * P + HD] - base);
+        ll += f[w] * out[(w * 16 + row) * P + HD + 1];
+    }
+    const int t = r / a.G, head = h * a.G + r % a.G;
+    const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
+    float inv = 1.0f;
+    if (a.splits == 1) {
+        const Final fin = finish(a, head, mm, ll);
+        inv = fin.factor;
+        if (a.lse && part == 0) a.lse[at] = fin.lse;
+    }
+    float* po = a.part + ((int64_t)split * a.Tq * a.nh + at) * a.hd;
+    for (int x = part * 4; x < a.hd; x += PER * 4) {
+        float v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) {
+            const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + row) * P + x]);
+            v[0] += f[w] * ow.x;
+            v[1] += f[w] * ow.y;
+            v[2] += f[w] * ow.z;
+            v[3] += f[w] * ow.w;
+        }
+        if (a.splits == 1)
+            *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
+                make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
+        else
+            *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    if (a.splits > 1 && part == 0)
+        a.part_ml[(int64_t)split * a.Tq * a.nh + at] = make_float2(mm, ll);
+}
+
+// One warp per (token, head): the splits' results joined, the sink added.
+__global__ void __launch_bounds__(256) tree_join_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int b = blockIdx.y;
+    const Seq s = load_seq(a, b);
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (!s.ok || i >= (int64_t)s.n * a.nh) return;
+    const int head = (int)(i % a.nh);
+    const int64_t at = (int64_t)s.q0 * a.nh + i, step = a.Tq * a.nh;
+    const int n = max(1, (s.len - first_key(a, s) + a.chunk - 1) / a.chunk);
+    float m = -INFINITY, l = 0.0f;
+    for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[x * step + at].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int x0 = 0; x0 < n; x0 += 32) {
+        float f = 0.0f;
+        if (x0 + lane < n) {
+            const float2 ml = a.part_ml[(x0 + lane) * step + at];
+            f = exp2f(ml.x - base);
+            l += f * ml.y;
+        }
+        for (int x = x0; x < min(n, x0 + 32); x++) {
+            const float fx = __shfl_sync(0xffffffffu, f, x - x0);
+            if (lane * 4 < a.hd) {
+                const float4 p =
+                    *reinterpret_cast<const float4*>(a.part + (x * step + at) * a.hd + lane * 4);
+                v.x += fx * p.x;
+                v.y += fx * p.y;
+                v.z += fx * p.z;
+                v.w += fx * p.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const Final fin = finish(a, head, m, l);
+    if (a.lse && lane == 0) a.lse[at] = fin.lse;
+    if (lane * 4 < a.hd)
+        *reinterpret_cast<uint2*>(a.o + at * a.hd + lane * 4) =
+            make_uint2(bf16x2(v.x * fin.factor, v.y * fin.factor),
+                       bf16x2(v.z * fin.factor, v.w * fin.factor));
+}
+
+// How the keys of a call are split: chunks long enough that the CTAs of all
+// sequences and heads, at the longest length, make about two waves of three
+// CTAs an SM (two: of bf16), and a multiple of 64 keys (a group for every warp).
+struct Plan {
+    int chunk, splits, row_tiles;
+};
+Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t window,
+               int sms) {
+    Plan p;
+    int64_t len = max_len;
+    if (window && window + max_q + GROUP < len) len = window + max_q + GROUP;
+    if (len < 1) len = 1;
+    p.row_tiles = (int)((max_q * (nh / kvh) + 15) / 16);
+    const int64_t units = B * kvh * p.row_tiles, want = 6 * (int64_t)sms;
+    int64_t chunk = (len * units + want - 1) / want;
+    chunk = (chunk + 63) / 64 * 64;
+    if (chunk < 64) chunk = 64;
+    p.chunk = (int)chunk;
+    p.splits = (int)((len + chunk - 1) / chunk);
+    return p;
+}
+
+}  // namespace tree
+}  // namespace ds41
+
+using namespace ds41;
+
+extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q,
+                                                 int64_t max_len, int64_t nh, int64_t kvh,
+                                                 int64_t hd, int64_t window, int fmt) {
+    (void)fmt;
+    if (B < 1 || Tq < 1 || max_q < 1 || max_q > 256 || max_len < 0 || kvh < 1 || nh < kvh ||
+        nh % kvh || hd < 1 || window < 0)
+        return 0;
+    const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, window, device_sm_count());
+    return pl.splits == 1 ? 0 : (size_t)pl.splits * Tq * nh * (hd * 4 + 8);
+}
+
+extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
+                                  const void* k_cache, const void* v_cache, const float* k_scales,
+                                  const float* v_scales, int fmt, int64_t n_pages, int64_t page,
+                                  const int32_t* page_table, int64_t max_pages,
+                                  const int32_t* lens, const int32_t* cu_q, const int64_t* mask,
+                                  int64_t mask_words, int64_t B, int64_t Tq, int64_t max_q,
+                                  int64_t max_len, int64_t nh, int64_t kvh, int64_t hd, float scale,
+                                  int64_t window, const float* sink, ds41_bf16* o, float* lse,
+                                  void* ws, size_t ws_bytes, ds41_stream_t stream) {
+    const char* name = "ds41_tree_attn_fwd";
+    if (int rc = check_heads(name, nh, kvh, hd, scale, window)) return rc;
+    tree::Args a{};
+    if (int rc = check_paged(name, k_cache, v_cache, k_scales, v_scales, fmt, n_pages, page, kvh,
+                             hd, &a.kv))
+        return rc;
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && max_q >= 0 && max_q <= 256 &&
+                     max_len >= 0 && max_len < lim / 2 && max_pages >= 0 && max_pages < lim,
+                 DS41_E_RANGE, "%s: B=%lld Tq=%lld max_q=%lld (at most 256) max_len=%lld", name,
+                 (long long)B, (long long)Tq, (long long)max_q, (long long)max_len);
+    DS41_REQUIRE(!mask || (mask_words >= 1 && mask_words <= 4 && max_q <= 64 * mask_words),
+                 DS41_E_ARG, "%s: mask_words=%lld for max_q=%lld", name, (long long)mask_words,
+                 (long long)max_q);
+    DS41_REQUIRE(window == 0 || window >= max_q, DS41_E_ARG,
+                 "%s: window=%lld is below max_q=%lld", name, (long long)window, (long long)max_q);
+    if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
+    DS41_REQUIRE(q && o && cu_q && lens && page_table, DS41_E_ARG,
+                 "%s: q, page_table, lens, cu_q and o must be non-null", name);
+    DS41_REQUIRE(aligned16(q) && aligned16(o) && aligned_to(cu_q, 4) && aligned_to(lens, 4) &&
+                     aligned_to(page_table, 4) && aligned_to(mask, 8) && aligned_to(sink, 4) &&
+                     aligned_to(lse, 4),
+                 DS41_E_ARG, "%s: q and o must be 16-byte aligned", name);
+    DS41_REQUIRE(good_strides(q_tok, q_head, hd), DS41_E_ARG,
+                 "%s: strides must be multiples of 8 and at least hd", name);
+    const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, window, device_sm_count());
+    const size_t need =
+        ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, window, fmt);
+    DS41_REQUIRE(need == 0 || (ws && aligned16(ws) && ws_bytes >= need), DS41_E_WORKSPACE,
+                 "%s: needs %zu bytes of workspace, got %zu", name, need, ws ? ws_bytes : 0);
+    a.q = q;
+    a.q_tok = q_tok;
+    a.q_head = q_head;
+    a.table = page_table;
+    a.max_pages = (int)max_pages;
+    a.lens = lens;
+    a.max_len = (int)max_len;
+    a.mask = mask;
+    a.mask_words = (int)mask_words;
+    a.cu_q = cu_q;
+    a.Tq = Tq;
+    a.max_q = (int)max_q;
+    a.nh = (int)nh;
+    a.kvh = (int)kvh;
+    a.hd = (int)hd;
+    a.G = (int)(nh / kvh);
+    a.scale_log2 = scale * tree::LOG2E;
+    a.window = window;
+    a.sink = sink;
+    a.o = o;
+    a.lse = lse;
+    a.chunk = pl.chunk;
+    a.splits = pl.splits;
+    a.part = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)pl.splits * Tq * nh * hd);
+    if (int rc = status_word(&a.status)) return rc;
+    using namespace tree;
+    const bool e = fmt == DS41_KV_E4M3;
+    auto kern = e ? (hd <= 64 ? tree_few_kernel<64, true> : tree_few_kernel<128, true>)
+                  : (hd <= 64 ? tree_few_kernel<64, false> : tree_few_kernel<128, false>);
+    const int smem = e ? (hd <= 64 ? Cfg<64, true>::BYTES : Cfg<128, true>::BYTES)
+                       : (hd <= 64 ? Cfg<64, false>::BYTES : Cfg<128, false>::BYTES);
+    DS41_REQUIRE(kvh * pl.row_tiles < 65536, DS41_E_RANGE, "%s: kvh=%lld max_q=%lld nh=%lld", name,
+                 (long long)kvh, (long long)max_q, (long long)nh);
+    if (int rc = cuda_check(
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
+        return rc;
+    if (int rc = launch_pdl(kern,
+                            dim3((unsigned)pl.splits, (unsigned)(kvh * pl.row_tiles), (unsigned)B),
+                            dim3(NT), smem, (cudaStream_t)stream, name, a))
+        return rc;
+    if (pl.splits == 1) return DS41_OK;
+    return launch_pdl(tree_join_kernel,
+                      dim3((unsigned)((max_q * nh + 7) / 8), (unsigned)B), dim3(256), 0,
+                      (cudaStream_t)stream, name, a);
+}

@@ -78,7 +78,7 @@ SIGNATURES = {
     "ds41_prompt_attn_workspace_bytes": (_SZ, [_I64] * 6),
     "ds41_prompt_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]
                              + [_I64] * 7 + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
-    "ds41_tree_attn_workspace_bytes": (_SZ, [_I64] * 7 + [ctypes.c_int]),
+    "ds41_tree_attn_workspace_bytes": (_SZ, [_I64] * 8 + [ctypes.c_int]),
     "ds41_tree_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64, _I64,
                                           _P, _I64, _P, _P, _P, _I64] + [_I64] * 7
                            + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
@@ -920,7 +920,7 @@ def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, len
             raise ValueError(f"mask: expected [Tq, words], got {tuple(mask.shape)}")
         words = mask.shape[1]
     o = torch.empty(Tq, nh, hd, dtype=_BF, device=dev) if o is None else o
-    need = load().ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, c[4])
+    need = load().ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, window, c[4])
     ws = _ws(need, ws, dev)
     _call("ds41_tree_attn_fwd", qp, q_tok, q_head, *c,
           _shape("page_table", page_table, (B, mp), torch.int32), mp,

@@ -606,7 +606,8 @@ int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, cons
 
 /* Scratch bytes ds41_tree_attn_fwd needs (may be 0). */
 size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len,
-                                      int64_t nh, int64_t kvh, int64_t hd, int fmt);
+                                      int64_t nh, int64_t kvh, int64_t hd, int64_t window,
+                                      int fmt);
 
 /* Attention of drafted tokens over a paged cache: sequence b has len =
  * lens[b] rows in the cache, the last n = cu_q[b+1] - cu_q[b] of which are its
