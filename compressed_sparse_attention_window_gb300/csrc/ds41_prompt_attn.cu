@@ -26,16 +26,13 @@
 // also covers PV_t(j), so a softmax thread that has seen S_t(j+1) may rescale
 // its row of O_t itself: no fourth role, no further barrier.
 #include "ds41_dense.cuh"
-#include "ds41_tc.cuh"
+#include "ds41_softmax_tc.cuh"
 
 namespace ds41 {
 namespace pa {
 
 using namespace tc;
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float RESCALE_LOG2 = 4.0f;
 constexpr int KB = 128;         // keys per block
 constexpr int ROWS = 128;       // rows per tile
 constexpr int THREADS = 384;
@@ -72,33 +69,6 @@ struct Params {
     unsigned int* status;
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-// D += A B with A in tensor memory (bf16, two per column, lane = row)
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // A CTA's work: one head group of one pair of tiles of one sequence.
 struct Item {
     int b;          // sequence, -1: none
@@ -106,6 +76,11 @@ struct Item {
     int k0, len;    // its keys
     int t0;         // first token of tile 0
 };
+
+// the lowest n bits (none for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
 
 // The key blocks [lo, hi) that some row of tile t sees; count = its tokens.
 struct Range {
@@ -271,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
         if (warp == 0 && lane == 0 && jhi > jlo) {
             const int head0 = grp * p.G;
             const int kvh = grp / p.subs;
@@ -321,19 +296,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             auto qk = [&](int t, uint32_t n) {
                 const uint64_t a = qd + ((t * C::TILE) >> 4);
                 const uint64_t b = kd + (((n % C::STAGES) * C::TILE) >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    if (k < ksteps)
-                        tc_mma(tmem + TM_S + 128 * t, a + (((k >> 2) * C::BLK + (k & 3) * 32) >> 4),
-                               b + (((k >> 2) * C::BLK + (k & 3) * 32) >> 4), IDESC_S, k > 0);
+                for (int k = 0; k < ksteps; k++) {
+                    const uint32_t off = ((k >> 2) * C::BLK + (k & 3) * 32) >> 4;
+                    tc_mma(tmem + TM_S + 128 * t, a + off, b + off, IDESC_S, k > 0);
+                }
                 tc_commit(&b_s[t]);
             };
             auto pv = [&](int t, uint32_t n, int steps, bool acc) {
                 const uint64_t b = vd + (((n % C::STAGES) * C::TILE) >> 4);
-#pragma unroll
-                for (int k = 0; k < KB / 16; k++)
-                    if (k < steps)
-                        tc_mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * k,
+                for (int k = 0; k < steps; k++)
+                    tc_mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * k,
                                   b + ((k * 2048) >> 4), IDESC_O, acc || k > 0);
             };
             bool ok = wait_bar(b_q, 0, abort_f, p.status) && wait_stage(0);
@@ -395,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
         const int t = (warp - 4) >> 2;
         const Range r = rg[t];
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -416,82 +388,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 break;
             }
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
-            tc_wait_ld();
             const int64_t j0 = (int64_t)j * KB;
-            if (j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window)) {
+            const bool masked = j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
+            uint32_t vis[4] = {};
+            if (masked) {
                 const int hi = (int)max((int64_t)-1, min((int64_t)KB, pos - j0));
                 const int lo = (int)max((int64_t)-1, min((int64_t)KB, before - j0));
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int e = 0; e < 32; e++)
-                        if (32 * i + e > hi || 32 * i + e <= lo) s[i][e] = 0xff800000u;
+                    vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
             }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-                for (int e = 1; e < 32; e++) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // (-inf - -inf is NaN: no move)
-            const bool move = (top - m) * c > RESCALE_LOG2 && live;
-            if (__any_sync(0xffffffffu, move)) {
-                const float to = move ? top : m;
-                const float f = move ? ex2((m - to) * c) : 1.0f;
-                m = to;
-                l *= f;
-                if (j > r.lo) {
-#pragma unroll
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t ov[32];
-                        tc_ld32(tm_o + x, ov);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e++)
-                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-                        tc_st32(tm_o + x, ov);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.0f : m * c;
-            float sum[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float a0 = ex2(fmaf(__uint_as_float(s[2 * h + i][e]), c, -base));
-                        const float a1 = ex2(fmaf(__uint_as_float(s[2 * h + i][e + 1]), c, -base));
-                        sum[2 * i] += a0;
-                        sum[2 * i + 1] += a1;
-                        pk[16 * i + e / 2] = bf16x2(a0, a1);
-                    }
-                tc_st32(tm_s + 32 * h, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tc_wait_st();
+            softmax_block<D, false>(tm_s, tm_o, j > r.lo, masked, vis, c, nullptr, nullptr, live, m,
+                                    l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b_p[t]);
         }
         // the sink is one more term of the denominator
         const int head = grp * p.G + gh;
-        const float snk = live && p.sink ? p.sink[head] * LOG2E : -INFINITY;
-        const float mc = m == -INFINITY ? -INFINITY : m * c;
-        const float top = fmaxf(mc, snk);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float f = ex2(mc - base);
-        const float den = l * f + ex2(snk - base);
-        const float inv = den == 0.0f ? 0.0f : f / den;
+        const RowEnd end = row_end(m, l, c, live && p.sink ? p.sink[head] : -INFINITY);
+        const float inv = end.factor;
         const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
-        if (live && ok && p.lse) p.lse[at] = (base + log2f(den)) * LN2;
+        if (live && ok && p.lse) p.lse[at] = end.lse;
         if (r.count > 0 && ok) {
             uint16_t* dst = p.o + at * p.hd;
             if (r.hi > r.lo) {
@@ -596,7 +514,7 @@ extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q
     p.max_q = (int)max_q;
     p.nh = (int)nh;
     p.hd = (int)hd;
-    p.c = scale * pa::LOG2E;
+    p.c = scale * tc::SM_LOG2E;
     // heads per tile: the whole group, or its largest divisor that fits
     int G = (int)(nh / kvh);
     p.subs = 1;

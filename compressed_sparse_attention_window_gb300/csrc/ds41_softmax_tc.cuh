@@ -1,0 +1,196 @@
+// ds41_softmax_tc.cuh - one block of 128 keys of a softmax whose scores and
+// output live in tensor memory: shared by the tensor-core kernels of the dense
+// attention (packed prompts, trees over a paged cache).
+#pragma once
+
+#include "ds41_tc.cuh"
+
+namespace ds41 {
+namespace tc {
+
+constexpr float SM_LOG2E = 1.4426950408889634f;
+constexpr float SM_LN2 = 0.6931471805599453f;
+// the reference of a row moves when a block's maximum exceeds it by 2^4
+constexpr float SM_RESCALE_LOG2 = 4.0f;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// D += A B with A in tensor memory (bf16, two per column, lane = row)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two f32 operations in one instruction
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+// One thread's row: its 128 scores of the block (columns tm_s .. of its lane)
+// become weights, bf16, two per column from tm_s on.
+//   t_j = c S_j (SCALED: c ks_j S_j), p_j = 2^(t_j - c m), l += p_j, the weight
+//   p_j (SCALED: p_j vs_j; 0 for a key that is not seen, whatever vs_j holds)
+// Keys whose bit of vis is clear are not seen (vis is read when `masked`).
+// Where the maximum exceeds the reference m (in units of S ks) by 2^4, m moves
+// and l and, with `have_o`, the D columns of the output at tm_o are rescaled;
+// the caller has seen the products before this block complete.  All lanes of a
+// warp take part; `live` = the row exists.
+template <int D, bool SCALED>
+__device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool have_o,
+                                              bool masked, const uint32_t (&vis)[4], float c,
+                                              const float* ks, const float* vs, bool live,
+                                              float& m, float& l) {
+    uint32_t s[4][32];
+#pragma unroll
+    for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
+    tc_wait_ld();
+    if (SCALED) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * i + e);
+                float a, b;
+                unf2(mul2(f2(u2f(s[i][e]), u2f(s[i][e + 1])), f2(k4.x, k4.y)), a, b);
+                s[i][e] = __float_as_uint(a);
+                s[i][e + 1] = __float_as_uint(b);
+                unf2(mul2(f2(u2f(s[i][e + 2]), u2f(s[i][e + 3])), f2(k4.z, k4.w)), a, b);
+                s[i][e + 2] = __float_as_uint(a);
+                s[i][e + 3] = __float_as_uint(b);
+            }
+    }
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+                if (!((vis[i] >> e) & 1)) s[i][e] = 0xff800000u;
+    }
+    float mx[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        mx[i] = fmaxf(u2f(s[i][0]), u2f(s[i][1]));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], u2f(s[i][e]), u2f(s[i][e + 1]));
+    }
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    // (-inf - -inf is NaN: no move)
+    const bool move = (top - m) * c > SM_RESCALE_LOG2 && live;
+    if (__any_sync(0xffffffffu, move)) {
+        const float to = move ? top : m;
+        const float f = move ? ex2((m - to) * c) : 1.0f;
+        m = to;
+        l *= f;
+        if (have_o) {
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
+                uint32_t ov[16];
+                tc_ld16(tm_o + x, ov);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e++) ov[e] = __float_as_uint(u2f(ov[e]) * f);
+                tc_st16(tm_o + x, ov);
+            }
+        }
+    }
+    const float base = m == -INFINITY ? 0.0f : m * c;
+    const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            float p[4];
+            unf2(fma2(f2(u2f(s[h][e]), u2f(s[h][e + 1])), c2, b2), p[0], p[1]);
+            unf2(fma2(f2(u2f(s[h][e + 2]), u2f(s[h][e + 3])), c2, b2), p[2], p[3]);
+#pragma unroll
+            for (int x = 0; x < 4; x++) p[x] = ex2(p[x]);
+            sum[0] = add2(sum[0], f2(p[0], p[1]));
+            sum[1] = add2(sum[1], f2(p[2], p[3]));
+            if (SCALED) {
+                const float4 v4 = *reinterpret_cast<const float4*>(vs + 32 * h + e);
+                unf2(mul2(f2(p[0], p[1]), f2(v4.x, v4.y)), p[0], p[1]);
+                unf2(mul2(f2(p[2], p[3]), f2(v4.z, v4.w)), p[2], p[3]);
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+                        if (!((vis[h] >> (e + x)) & 1)) p[x] = 0.0f;
+                }
+            }
+            pk[e / 2] = bf16x2(p[0], p[1]);
+            pk[e / 2 + 1] = bf16x2(p[2], p[3]);
+        }
+        tc_st16(tm_s + 16 * h, pk);
+    }
+    float a, b;
+    unf2(add2(sum[0], sum[1]), a, b);
+    l += a + b;
+    tc_wait_st();
+}
+
+// The end of a row: the sink joins the denominator; O times factor is the
+// output.  m in units of S, snk in natural units; a row that saw nothing (m =
+// -inf) has factor 0.
+struct RowEnd {
+    float factor, lse;
+};
+__device__ __forceinline__ RowEnd row_end(float m, float l, float c, float snk) {
+    const float mc = m == -INFINITY ? -INFINITY : m * c;
+    snk *= SM_LOG2E;
+    const float top = fmaxf(mc, snk);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float f = ex2(mc - base);
+    const float den = l * f + ex2(snk - base);
+    RowEnd r;
+    r.factor = den == 0.0f ? 0.0f : f / den;
+    r.lse = (base + log2f(den)) * SM_LN2;
+    return r;
+}
+
+}  // namespace tc
+}  // namespace ds41
