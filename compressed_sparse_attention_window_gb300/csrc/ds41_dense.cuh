@@ -39,16 +39,30 @@ __device__ __forceinline__ int64_t paged_row(const PagedKv& c, int64_t pg, int h
     return (pg * c.kvh + h) * c.page + off;
 }
 
-// Two e4m3 codes, in the upper bytes of the halves of x (the lower bytes are
-// ignored), as bf16x2, exact.  The code's exponent and mantissa bits moved into
-// a bf16's give the value times 2^-120 (exponent bias 7 against 127, subnormals
-// included); one exact bf16 product restores it.  The NaN codes 0x7f and 0xff,
-// which the cache never holds, would come out as +-480.
-__device__ __forceinline__ uint32_t e4m3_spread(uint32_t x) {
-    const uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-    uint32_t out;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out) : "r"(r), "r"(0x7b807b80u));  // 2^120
-    return out;
+// Four e4m3 codes -> their exact values as f16 (every e4m3 value is a normal f16
+// or zero): lo = codes 0, 1, hi = codes 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
+// The exponent that brings a row of queries with the largest magnitude amax (bf16
+// bits) to [2^14, 2^15), so that bf16 values become f16 exactly down to 2^-28 of
+// it (at least -120: below 2^-106 the row becomes smaller f16 values, still
+// exact); 0 for a row of zeros or one that is not finite.
+__device__ __forceinline__ int query_exponent(uint32_t amax_bits) {
+    const int e = (int)(amax_bits >> 7);
+    return e == 0 || e == 255 ? 0 : max(e - 127 - 14, -120);
+}
+// two bf16 times 2^-e as f16
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float down) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+        : "=r"(r)
+        : "f"(__uint_as_float(x & 0xffff0000u) * down), "f"(__uint_as_float(x << 16) * down));
+    return r;
 }
 
 }  // namespace ds41

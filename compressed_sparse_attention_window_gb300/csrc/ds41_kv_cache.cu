@@ -23,8 +23,8 @@ int check_paged(const char* name, const void* k, const void* v, const float* ks,
     DS41_REQUIRE(kvh >= 1 && kvh <= 1024 && hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
                  "%s: kvh=%lld hd=%lld (hd a multiple of 16, at most 128)", name, (long long)kvh,
                  (long long)hd);
-    DS41_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31), DS41_E_ARG, "%s: n_pages=%lld", name,
-                 (long long)n_pages);
+    DS41_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31) / kvh, DS41_E_ARG,
+                 "%s: n_pages=%lld kvh=%lld", name, (long long)n_pages, (long long)kvh);
     DS41_REQUIRE(k && v && aligned16(k) && aligned16(v), DS41_E_ARG,
                  "%s: the caches must be non-null and 16-byte aligned", name);
     if (fmt == DS41_KV_E4M3)

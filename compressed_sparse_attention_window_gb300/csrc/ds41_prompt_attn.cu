@@ -379,14 +379,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
         const int64_t p_last = (int64_t)r.p_first + r.count - 1;
         const float c = p.c;
-        float m = -INFINITY, l = 0.0f;
+        RowState st(false);
         uint32_t ph = 0;
         bool ok = true;
         for (int j = r.lo; j < r.hi; j++, ph++) {
-            if (!wait_bar(&b_s[t], ph & 1, abort_f, p.status)) {
-                ok = false;
-                break;
-            }
+            ok = __all_sync(0xffffffffu, wait_bar(&b_s[t], ph & 1, abort_f, p.status));
+            if (!ok) break;
             tc_fence_after();
             const int64_t j0 = (int64_t)j * KB;
             const bool masked = j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
@@ -398,22 +396,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 4; i++)
                     vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
             }
-            softmax_block<D, false>(tm_s, tm_o, j > r.lo, masked, vis, c, nullptr, nullptr, live, m,
-                                    l);
+            softmax_block<D, false>(tm_s, tm_o, j > r.lo, masked, vis, c, nullptr, nullptr, 0.0f,
+                                    live, st);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b_p[t]);
         }
         // the sink is one more term of the denominator
         const int head = grp * p.G + gh;
-        const RowEnd end = row_end(m, l, c, live && p.sink ? p.sink[head] : -INFINITY);
+        const RowEnd end = row_end(st.reference(c), st.l,
+                                   live && p.sink ? p.sink[head] : -INFINITY);
         const float inv = end.factor;
         const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
         if (live && ok && p.lse) p.lse[at] = end.lse;
         if (r.count > 0 && ok) {
             uint16_t* dst = p.o + at * p.hd;
             if (r.hi > r.lo) {
-                ok = wait_bar(&b_o[t], 0, abort_f, p.status);
+                ok = __all_sync(0xffffffffu, wait_bar(&b_o[t], 0, abort_f, p.status));
                 tc_fence_after();
             }
             if (ok) {

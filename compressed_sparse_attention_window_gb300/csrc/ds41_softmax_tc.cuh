@@ -70,20 +70,48 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The state of a row: the reference m (in units of its scores), the sum l of
+// 2^(c (S - m) - lr), and for scaled values their common exponent lr, which
+// moves when a scale exceeds vlim = 2^(lr + 8).  2^lr is about the size of the
+// value scales, so that a weight times its value's scale stays in the range of
+// f16 (2^4 of the lazy maximum, 2^9 of the scale); both O and l carry 2^-lr, so
+// nothing has to be undone at the end.
+struct RowState {
+    float m, l, lr, vlim;
+    __device__ __forceinline__ explicit RowState(bool scaled)
+        : m(-INFINITY), l(0.0f), lr(scaled ? VS_MIN : 0.0f), vlim(0.0f) {}
+    // scales below 2^-60 count as 2^-60: l stays far from the end of f32
+    static constexpr float VS_MIN = -60.0f;
+    __device__ __forceinline__ float reference(float c) const {  // in log2 units
+        return m == -INFINITY ? -INFINITY : m * c + lr;
+    }
+};
+// the exponent that a value scale asks for
+__device__ __forceinline__ float scale_exponent(float vmax) {
+    return fmaxf((float)((int)(__float_as_uint(vmax) >> 23) - 127), RowState::VS_MIN);
+}
+
 // One thread's row: its 128 scores of the block (columns tm_s .. of its lane)
-// become weights, bf16, two per column from tm_s on.
-//   t_j = c S_j (SCALED: c ks_j S_j), p_j = 2^(t_j - c m), l += p_j, the weight
-//   p_j (SCALED: p_j vs_j; 0 for a key that is not seen, whatever vs_j holds)
+// become weights, two per column from tm_s on: bf16, or f16 when SCALED.
+//   t_j = c S_j (SCALED: c ks_j S_j), p_j = 2^(t_j - reference), l += p_j, the
+//   weight p_j (SCALED: p_j vs_j; 0 for a key that is not seen, whatever vs_j
+//   holds)
 // Keys whose bit of vis is clear are not seen (vis is read when `masked`).
-// Where the maximum exceeds the reference m (in units of S ks) by 2^4, m moves
-// and l and, with `have_o`, the D columns of the output at tm_o are rescaled;
-// the caller has seen the products before this block complete.  All lanes of a
-// warp take part; `live` = the row exists.
+// Where the maximum exceeds the reference by 2^4 it moves and l and, with
+// `have_o`, the D columns of the output at tm_o are rescaled; the caller has
+// seen the products before this block complete.  All lanes of a warp take part;
+// `live` = the row exists.  vmax: the largest vs of the block.
 template <int D, bool SCALED>
 __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool have_o,
                                               bool masked, const uint32_t (&vis)[4], float c,
-                                              const float* ks, const float* vs, bool live,
-                                              float& m, float& l) {
+                                              const float* ks, const float* vs, float vmax,
+                                              bool live, RowState& st) {
     uint32_t s[4][32];
 #pragma unroll
     for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
@@ -119,12 +147,19 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
     }
     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     // (-inf - -inf is NaN: no move)
-    const bool move = (top - m) * c > SM_RESCALE_LOG2 && live;
-    if (__any_sync(0xffffffffu, move)) {
-        const float to = move ? top : m;
-        const float f = move ? ex2((m - to) * c) : 1.0f;
-        m = to;
-        l *= f;
+    const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
+    const bool vmove = SCALED && vmax > st.vlim;
+    if (__any_sync(0xffffffffu, move || vmove)) {
+        float shift = move ? (st.m - top) * c : 0.0f;
+        if (move) st.m = top;
+        if (vmove) {
+            const float lr = scale_exponent(vmax);
+            shift += st.lr - lr;
+            st.lr = lr;
+            st.vlim = ex2(lr + 8.0f);
+        }
+        const float f = ex2(shift);
+        st.l *= f;
         if (have_o) {
 #pragma unroll 1
             for (int x = 0; x < D; x += 16) {
@@ -137,7 +172,16 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
             }
         }
     }
-    const float base = m == -INFINITY ? 0.0f : m * c;
+    float base = st.m == -INFINITY ? 0.0f : SCALED ? fmaf(st.m, c, st.lr) : st.m * c;
+    if (fabsf(base) > 0x1p22f) {
+        // c m itself is rounded by more than a fraction of one power of two: take
+        // the differences first
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        base = SCALED ? st.lr : 0.0f;
+    }
     const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -162,30 +206,29 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
                         if (!((vis[h] >> (e + x)) & 1)) p[x] = 0.0f;
                 }
             }
-            pk[e / 2] = bf16x2(p[0], p[1]);
-            pk[e / 2 + 1] = bf16x2(p[2], p[3]);
+            pk[e / 2] = SCALED ? f16x2(p[0], p[1]) : bf16x2(p[0], p[1]);
+            pk[e / 2 + 1] = SCALED ? f16x2(p[2], p[3]) : bf16x2(p[2], p[3]);
         }
         tc_st16(tm_s + 16 * h, pk);
     }
     float a, b;
     unf2(add2(sum[0], sum[1]), a, b);
-    l += a + b;
+    st.l += a + b;
     tc_wait_st();
 }
 
 // The end of a row: the sink joins the denominator; O times factor is the
-// output.  m in units of S, snk in natural units; a row that saw nothing (m =
+// output.  m in log2 units, snk in natural ones; a row that saw nothing (m =
 // -inf) has factor 0.
 struct RowEnd {
     float factor, lse;
 };
-__device__ __forceinline__ RowEnd row_end(float m, float l, float c, float snk) {
-    const float mc = m == -INFINITY ? -INFINITY : m * c;
+__device__ __forceinline__ RowEnd row_end(float m, float l, float snk) {
     snk *= SM_LOG2E;
-    const float top = fmaxf(mc, snk);
+    const float top = fmaxf(m, snk);
     const float base = top == -INFINITY ? 0.0f : top;
-    const float f = ex2(mc - base);
-    const float den = l * f + ex2(snk - base);
+    const float f = exp2f(m - base);
+    const float den = l * f + exp2f(snk - base);
     RowEnd r;
     r.factor = den == 0.0f ? 0.0f : f / den;
     r.lse = (base + log2f(den)) * SM_LN2;

@@ -4,13 +4,13 @@
 #pragma once
 
 #include "ds41_dense.cuh"
+#include "ds41_softmax_tc.cuh"
 
 namespace ds41 {
 namespace tree {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float RESCALE_LOG2 = 4.0f;
+using tc::bf16x2;
+using tc::ex2;
 
 struct Args {
     const uint16_t* q;
@@ -28,9 +28,10 @@ struct Args {
     int max_q, nh, kvh, hd, G;
     float scale_log2;
     int64_t window;
-    // the split of the keys: chunk keys a split; partial results when splits > 1:
-    // part [splits][Tq][nh][hd], part_ml [splits][Tq][nh] (reference, sum)
-    int chunk, splits;
+    // the split of the keys: chunk keys a split from the first one on (rounded
+    // down to `align`), `per` partial results each; with parts > 1:
+    // part [parts][Tq][nh][hd], part_ml [parts][Tq][nh] (reference in log2, sum)
+    int chunk, align, per, parts;
     float* part;
     float2* part_ml;
     unsigned int* status;
@@ -51,11 +52,11 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b) {
            s.len <= a.max_len && s.len <= (int64_t)a.max_pages * a.kv.page;
     return s;
 }
-// The first key that some row of the sequence may see, rounded down to a group
-// of 16: no token stands before the last earlier row.
+// The first key that some row of the sequence may see, rounded down: no token
+// stands before the last earlier row.
 __device__ __forceinline__ int first_key(const Args& a, const Seq& s) {
     const int64_t lo = a.window ? (int64_t)s.len - s.n - a.window : 0;
-    return lo > 0 ? (int)(lo & ~(int64_t)15) : 0;
+    return lo > 0 ? (int)(lo & ~(int64_t)(a.align - 1)) : 0;
 }
 
 // What one row sees: of the earlier keys (below pre) those behind lo, of the
@@ -94,33 +95,10 @@ __device__ __forceinline__ bool seen(const RowView& w, int j, int len) {
     return (w.bits[u >> 6] >> (u & 63)) & 1;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// The end of a row: the sink joins the denominator; O times factor is the
-// output.  A row that sees nothing (m = -inf) has factor 0.
-struct Final {
-    float factor, lse;
-};
-__device__ __forceinline__ Final finish(const Args& a, int head, float m, float l) {
-    const float snk = a.sink ? a.sink[head] * LOG2E : -INFINITY;
-    const float top = fmaxf(m, snk);
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float f = exp2f(m - base);
-    const float den = l * f + exp2f(snk - base);
-    Final r;
-    r.factor = den == 0.0f ? 0.0f : f / den;
-    r.lse = (base + log2f(den)) * LN2;
-    return r;
-}
+// The tensor-core kernel, for more than 16 rows per key/value head; pair: two
+// tiles of 128 rows a CTA, else one (of at most 128 rows, two partial results).
+int launch_many(const Args& a, bool pair, int row_tiles, int64_t B, const char* name,
+                cudaStream_t st);
 
 }  // namespace tree
 }  // namespace ds41

@@ -4,9 +4,13 @@
 // Mathematics.  One pass with a running reference m and sum l per row, in units
 // of log2: t_j = scale log2(e) ks_j <q, k_j> (ks_j, vs_j: the row's scales, 1
 // for bf16), p_j = 2^(t_j - m), l += p_j, O += (p_j vs_j) v_j, the weights
-// rounded to bf16 for the tensor cores.  m follows the running maximum lazily:
-// it moves (and l and O are rescaled) when a score exceeds it by 2^4.  The codes
-// of an e4m3 row are exact in bf16, so the scales stay outside the products.
+// rounded to 16 bits for the tensor cores.  m follows the running maximum lazily:
+// it moves (and l and O are rescaled) when a score exceeds it by 2^4.  An e4m3
+// cache runs on f16 products: its codes are exact in f16 (one instruction for
+// two codes; bf16 takes four), the queries become f16 with an exponent per row,
+// and l and O carry 2^-lr with lr about the exponent of the value scales, which
+// keeps p_j vs_j in the range of f16 (RowState in ds41_softmax_tc.cuh).  The
+// scales stay outside the products.
 //
 // Rows.  All queries of a (sequence, key/value head): tokens times the G heads
 // that share it, 16 rows a CTA (the M of an m16n8k16 product).
@@ -60,14 +64,14 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     using C = Cfg<HD, E4M3>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x, h = blockIdx.y % a.kvh, rt = blockIdx.y / a.kvh, b = blockIdx.z;
+    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const Seq s = load_seq(a, b);
     if (!s.ok) {
         if (threadIdx.x == 0) raise_status(a.status, DS41_E_INDEX);
         return;
     }
-    const int rows = s.n * a.G, r0 = rt * 16;
-    if (r0 >= rows) return;
+    const int rows = s.n * a.G;  // at most 16
+    if (rows == 0) return;
     const int k_first = first_key(a, s);
     const int k0 = k_first + split * a.chunk, k1 = min(s.len, k0 + a.chunk);
     if (k0 >= k1 && split > 0) return;  // (a sequence without keys has its split 0)
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     uint32_t qf[HD / 16][4];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int r = min(r0 + g + 8 * i, rows - 1);
+        const int r = min(g + 8 * i, rows - 1);
         const int t = r / a.G;
         view[i] = row_view(a, s, t);
         const uint16_t* qp = a.q + (s.q0 + t) * a.q_tok + (h * a.G + r % a.G) * a.q_head;
@@ -125,9 +129,29 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             const int d = E4M3 ? (c + 4 * (st / 4)) * 16 + 4 * (st % 4)
                                : (c + 4 * (st / 2)) * 8 + 4 * (st % 2);
             const uint2 v = d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
-            // of four codes in a word the even ones spread together, then the odd
-            qf[st][i] = E4M3 ? __byte_perm(v.x, v.y, 0x5410) : v.x;
-            qf[st][i + 2] = E4M3 ? __byte_perm(v.x, v.y, 0x7632) : v.y;
+            qf[st][i] = v.x;
+            qf[st][i + 2] = v.y;
+        }
+    }
+    float cr[2] = {a.scale_log2, a.scale_log2};
+    if (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int st = 0; st < HD / 16; st++)
+                m2 = __vmaxu2(m2, __vmaxu2(qf[st][i] & 0x7fff7fffu, qf[st][i + 2] & 0x7fff7fffu));
+            uint32_t mb = max(m2 & 0xffffu, m2 >> 16);  // four lanes have the row
+            mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+            mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+            const int e = query_exponent(mb);
+            const float down = exp2f((float)-e);
+            cr[i] *= exp2f((float)e);
+#pragma unroll
+            for (int st = 0; st < HD / 16; st++) {
+                qf[st][i] = bf16x2_to_f16x2(qf[st][i], down);
+                qf[st][i + 2] = bf16x2_to_f16x2(qf[st][i + 2], down);
+            }
         }
     }
     // keys below `easy` are seen by both rows (and none lies at or before lo)
@@ -135,6 +159,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
 
     float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
+    float lr = E4M3 ? tc::RowState::VS_MIN : 0.0f, vlim = 0.0f;
     for (int i = 0; i < mine; i++) {
         fetch(i + C::STAGES - 1);
         cp_async_wait<C::STAGES - 1>();
@@ -157,8 +182,9 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int q = 4 * x + e;
-                        mma_bf16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3],
-                                 e4m3_spread(w[e] << 8), e4m3_spread(w[e]));
+                        uint32_t lo16, hi16;
+                        e4m3x4_to_f16(w[e], lo16, hi16);
+                        mma_f16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], lo16, hi16);
                     }
                 } else {
 #pragma unroll
@@ -172,18 +198,15 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         }
         // ---- softmax: this lane has rows g, g + 8 and keys 2c, 2c+1, 2c+8, 2c+9 ----
         float2 ks[2], vs[2];
+        if (E4M3) {
 #pragma unroll
-        for (int n = 0; n < 2; n++) {
-            ks[n] = E4M3 ? *reinterpret_cast<const float2*>(sx + n * 8 + 2 * c) : make_float2(1, 1);
-            vs[n] = E4M3 ? *reinterpret_cast<const float2*>(sx + 16 + n * 8 + 2 * c)
-                         : make_float2(1, 1);
-            ks[n].x *= a.scale_log2;
-            ks[n].y *= a.scale_log2;
+            for (int n = 0; n < 2; n++) {
+                ks[n] = *reinterpret_cast<const float2*>(sx + n * 8 + 2 * c);
+                vs[n] = *reinterpret_cast<const float2*>(sx + 16 + n * 8 + 2 * c);
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
+            }
         }
-#pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
         if ((bad >> st) & 1) {
 #pragma unroll
             for (int n = 0; n < 2; n++)
@@ -202,21 +225,37 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         for (int i2 = 0; i2 < 2; i2++)
             mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
                            fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + RESCALE_LOG2 || mx[1] > m[1] + RESCALE_LOG2)) {
+        // scales that no key needs (behind the sequence's end) may be NaN: fmaxf skips them
+        float vm = E4M3 ? fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y)) : 0.0f;
+        const bool moves = (mx[0] - m[0]) * cr[0] > tc::SM_RESCALE_LOG2 ||
+                           (mx[1] - m[1]) * cr[1] > tc::SM_RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
+            float shift = 0.0f;
+            if (E4M3) {
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                if (vm > vlim) {
+                    const float to = tc::scale_exponent(vm);
+                    shift = lr - to;
+                    lr = to;
+                    vlim = exp2f(to + 8.0f);
+                }
+            }
 #pragma unroll
             for (int i2 = 0; i2 < 2; i2++) {
-                float t = mx[i2];
+                float t = mx[i2], sh = shift;
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                if (t > m[i2] + RESCALE_LOG2) {
-                    const float f = exp2f(m[i2] - t);
+                if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
+                    sh += (m[i2] - t) * cr[i2];
                     m[i2] = t;
-                    l[i2] *= f;
+                }
+                const float f = exp2f(sh);
+                l[i2] *= f;
 #pragma unroll
-                    for (int d = 0; d < HD / 8; d++) {
-                        o[d][2 * i2] *= f;
-                        o[d][2 * i2 + 1] *= f;
-                    }
+                for (int d = 0; d < HD / 8; d++) {
+                    o[d][2 * i2] *= f;
+                    o[d][2 * i2 + 1] *= f;
                 }
             }
         }
@@ -226,12 +265,18 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
 #pragma unroll
             for (int i2 = 0; i2 < 2; i2++) {
                 const float base = m[i2] == -INFINITY ? 0.0f : m[i2];
-                const float p0 = ex2(sc[n][2 * i2] - base), p1 = ex2(sc[n][2 * i2 + 1] - base);
+                const float s0 = sc[n][2 * i2], s1 = sc[n][2 * i2 + 1];
+                const float p0 = ex2(fmaf(s0 - base, cr[i2], -lr));
+                const float p1 = ex2(fmaf(s1 - base, cr[i2], -lr));
                 l[i2] += p0 + p1;
-                // a row that is not seen weighs nothing, whatever its scale holds
-                const float w0 = sc[n][2 * i2] == -INFINITY ? 0.0f : p0 * vs[n].x;
-                const float w1 = sc[n][2 * i2 + 1] == -INFINITY ? 0.0f : p1 * vs[n].y;
-                pf[2 * n + i2] = bf16x2(w0, w1);
+                if (E4M3) {
+                    // a row that is not seen weighs nothing, whatever its scale holds
+                    const float w0 = s0 == -INFINITY ? 0.0f : p0 * vs[n].x;
+                    const float w1 = s1 == -INFINITY ? 0.0f : p1 * vs[n].y;
+                    pf[2 * n + i2] = tc::f16x2(w0, w1);
+                } else {
+                    pf[2 * n + i2] = bf16x2(p0, p1);
+                }
             }
         // ---- O += P V: n-tile d holds the columns g HD/8 + d ----
         if (E4M3) {
@@ -249,14 +294,13 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             }
 #pragma unroll
             for (int d = 0; d < HD / 8; d += 2) {
-                // bytes d, d + 1 of two rows
-                const uint32_t s0 = (d & 2) ? 0x7632u : 0x5410u;
-                const uint32_t x0 = __byte_perm(w[0][d / 4], w[1][d / 4], s0);
-                const uint32_t x1 = __byte_perm(w[2][d / 4], w[3][d / 4], s0);
-                mma_bf16(o[d], pf[0], pf[1], pf[2], pf[3], e4m3_spread(x0 << 8),
-                         e4m3_spread(x1 << 8));
-                mma_bf16(o[d + 1], pf[0], pf[1], pf[2], pf[3], e4m3_spread(x0),
-                         e4m3_spread(x1));
+                // bytes d, d + 1 of two rows, side by side
+                const uint32_t sel = (d & 2) ? 0x7362u : 0x5140u;
+                uint32_t a0, a1, b0, b1;
+                e4m3x4_to_f16(__byte_perm(w[0][d / 4], w[1][d / 4], sel), a0, a1);
+                e4m3x4_to_f16(__byte_perm(w[2][d / 4], w[3][d / 4], sel), b0, b1);
+                mma_f16(o[d], pf[0], pf[1], pf[2], pf[3], a0, b0);
+                mma_f16(o[d + 1], pf[0], pf[1], pf[2], pf[3], a1, b1);
             }
         } else {
             uint32_t w[4][HD / 16];
@@ -290,7 +334,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
         float* row = out + (warp * 16 + g + 8 * i) * P;
         if (c == 0) {
-            row[HD] = m[i];
+            row[HD] = m[i] == -INFINITY ? -INFINITY : fmaf(m[i], cr[i], lr);
             row[HD + 1] = l[i];
         }
 #pragma unroll
@@ -302,7 +346,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     __syncthreads();
     constexpr int PER = NT / 16;  // threads of a row
     const int row = threadIdx.x / PER, part = threadIdx.x % PER;
-    const int r = r0 + row;
+    const int r = row;
     if (r >= rows) return;
     float mm = -INFINITY, f[WARPS], ll = 0.0f;
 #pragma unroll
@@ -316,10 +360,10 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     const int t = r / a.G, head = h * a.G + r % a.G;
     const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
     float inv = 1.0f;
-    if (a.splits == 1) {
-        const Final fin = finish(a, head, mm, ll);
-        inv = fin.factor;
-        if (a.lse && part == 0) a.lse[at] = fin.lse;
+    if (a.parts == 1) {
+        const tc::RowEnd end = tc::row_end(mm, ll, a.sink ? a.sink[head] : -INFINITY);
+        inv = end.factor;
+        if (a.lse && part == 0) a.lse[at] = end.lse;
     }
     float* po = a.part + ((int64_t)split * a.Tq * a.nh + at) * a.hd;
     for (int x = part * 4; x < a.hd; x += PER * 4) {
@@ -332,80 +376,95 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             v[2] += f[w] * ow.z;
             v[3] += f[w] * ow.w;
         }
-        if (a.splits == 1)
+        if (a.parts == 1)
             *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
                 make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
         else
             *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
     }
-    if (a.splits > 1 && part == 0)
+    if (a.parts > 1 && part == 0)
         a.part_ml[(int64_t)split * a.Tq * a.nh + at] = make_float2(mm, ll);
 }
 
-// One warp per (token, head): the splits' results joined, the sink added.
-__global__ void __launch_bounds__(256) tree_join_kernel(const Args a) {
+// One CTA per (token, head) of a sequence: its partial results joined, the sink
+// added.  Warp w takes the parts w, w + 4, ..., four rows in flight.
+__global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.y;
-    const Seq s = load_seq(a, b);
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (!s.ok || i >= (int64_t)s.n * a.nh) return;
-    const int head = (int)(i % a.nh);
-    const int64_t at = (int64_t)s.q0 * a.nh + i, step = a.Tq * a.nh;
-    const int n = max(1, (s.len - first_key(a, s) + a.chunk - 1) / a.chunk);
+    __shared__ float4 acc[WARPS][32];
+    __shared__ float sums[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Seq s = load_seq(a, blockIdx.y);
+    if (!s.ok || (int)blockIdx.x >= s.n * a.nh) return;
+    const int head = (int)blockIdx.x % a.nh;
+    const int64_t at = (int64_t)s.q0 * a.nh + blockIdx.x, step = a.Tq * a.nh;
+    const int n = a.per * max(1, (s.len - first_key(a, s) + a.chunk - 1) / a.chunk);
     float m = -INFINITY, l = 0.0f;
     for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[x * step + at].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     const float base = m == -INFINITY ? 0.0f : m;
     float4 v = make_float4(0, 0, 0, 0);
-    for (int x0 = 0; x0 < n; x0 += 32) {
-        float f = 0.0f;
-        if (x0 + lane < n) {
-            const float2 ml = a.part_ml[(x0 + lane) * step + at];
-            f = exp2f(ml.x - base);
-            l += f * ml.y;
-        }
-        for (int x = x0; x < min(n, x0 + 32); x++) {
-            const float fx = __shfl_sync(0xffffffffu, f, x - x0);
-            if (lane * 4 < a.hd) {
-                const float4 p =
-                    *reinterpret_cast<const float4*>(a.part + (x * step + at) * a.hd + lane * 4);
-                v.x += fx * p.x;
-                v.y += fx * p.y;
-                v.z += fx * p.z;
-                v.w += fx * p.w;
-            }
-        }
+    const bool mine = lane * 4 < a.hd;
+#pragma unroll 4
+    for (int x = warp; x < n; x += WARPS) {
+        const float2 ml = a.part_ml[x * step + at];
+        const float4 p = mine ? *reinterpret_cast<const float4*>(a.part + (x * step + at) * a.hd +
+                                                                 lane * 4)
+                              : make_float4(0, 0, 0, 0);
+        const float f = exp2f(ml.x - base);
+        l += f * ml.y;
+        v.x += f * p.x;
+        v.y += f * p.y;
+        v.z += f * p.z;
+        v.w += f * p.w;
     }
+    acc[warp][lane] = v;
+    if (lane == 0) sums[warp] = l;
+    __syncthreads();
+    if (warp > 0) return;
+    l = sums[0] + sums[1] + sums[2] + sums[3];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    const Final fin = finish(a, head, m, l);
-    if (a.lse && lane == 0) a.lse[at] = fin.lse;
-    if (lane * 4 < a.hd)
+    for (int w = 1; w < WARPS; w++) {
+        v.x += acc[w][lane].x;
+        v.y += acc[w][lane].y;
+        v.z += acc[w][lane].z;
+        v.w += acc[w][lane].w;
+    }
+    const tc::RowEnd end = tc::row_end(m, l, a.sink ? a.sink[head] : -INFINITY);
+    if (a.lse && lane == 0) a.lse[at] = end.lse;
+    if (mine)
         *reinterpret_cast<uint2*>(a.o + at * a.hd + lane * 4) =
-            make_uint2(bf16x2(v.x * fin.factor, v.y * fin.factor),
-                       bf16x2(v.z * fin.factor, v.w * fin.factor));
+            make_uint2(bf16x2(v.x * end.factor, v.y * end.factor),
+                       bf16x2(v.z * end.factor, v.w * end.factor));
 }
 
-// How the keys of a call are split: chunks long enough that the CTAs of all
-// sequences and heads, at the longest length, make about two waves of three
-// CTAs an SM (two: of bf16), and a multiple of 64 keys (a group for every warp).
+// How the keys of a call are split.  Up to 16 rows per key/value head: chunks
+// long enough that the CTAs of all sequences and heads, at the longest length,
+// make about two waves of three CTAs an SM, a multiple of 64 keys (a group for
+// every warp).  More rows: the tensor-core kernel, one CTA an SM, about three
+// waves, at least 512 keys (its start and end cost some blocks' time).
 struct Plan {
-    int chunk, splits, row_tiles;
+    bool many, pair;
+    int chunk, align, splits, per, row_tiles;
 };
 Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t window,
                int sms) {
     Plan p;
+    const int64_t rows = max_q * (nh / kvh);
+    p.many = rows > 16;
+    p.pair = rows > 128;
+    p.align = p.many ? 128 : GROUP;
+    p.per = p.many && !p.pair ? 2 : 1;
     int64_t len = max_len;
-    if (window && window + max_q + GROUP < len) len = window + max_q + GROUP;
+    if (window && window + max_q + p.align < len) len = window + max_q + p.align;
     if (len < 1) len = 1;
-    p.row_tiles = (int)((max_q * (nh / kvh) + 15) / 16);
-    const int64_t units = B * kvh * p.row_tiles, want = 6 * (int64_t)sms;
+    p.row_tiles = p.many ? (int)((rows + 255) / 256) : 1;
+    const int64_t units = B * kvh * p.row_tiles, want = (p.many ? 3 : 6) * (int64_t)sms;
+    const int64_t unit = p.many ? 256 : 64, least = p.many ? 512 : 64;
     int64_t chunk = (len * units + want - 1) / want;
-    chunk = (chunk + 63) / 64 * 64;
-    if (chunk < 64) chunk = 64;
+    chunk = (chunk + unit - 1) / unit * unit;
+    if (chunk < least) chunk = least;
     p.chunk = (int)chunk;
     p.splits = (int)((len + chunk - 1) / chunk);
     return p;
@@ -424,7 +483,8 @@ extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t 
         nh % kvh || hd < 1 || window < 0)
         return 0;
     const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, window, device_sm_count());
-    return pl.splits == 1 ? 0 : (size_t)pl.splits * Tq * nh * (hd * 4 + 8);
+    const int64_t parts = (int64_t)pl.splits * pl.per;
+    return parts == 1 ? 0 : (size_t)parts * Tq * nh * (hd * 4 + 8);
 }
 
 extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
@@ -482,33 +542,39 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
     a.kvh = (int)kvh;
     a.hd = (int)hd;
     a.G = (int)(nh / kvh);
-    a.scale_log2 = scale * tree::LOG2E;
+    a.scale_log2 = scale * tc::SM_LOG2E;
     a.window = window;
     a.sink = sink;
     a.o = o;
     a.lse = lse;
     a.chunk = pl.chunk;
-    a.splits = pl.splits;
+    a.align = pl.align;
+    a.per = pl.per;
+    a.parts = pl.splits * pl.per;
     a.part = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)pl.splits * Tq * nh * hd);
+    a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)a.parts * Tq * nh * hd);
     if (int rc = status_word(&a.status)) return rc;
-    using namespace tree;
-    const bool e = fmt == DS41_KV_E4M3;
-    auto kern = e ? (hd <= 64 ? tree_few_kernel<64, true> : tree_few_kernel<128, true>)
-                  : (hd <= 64 ? tree_few_kernel<64, false> : tree_few_kernel<128, false>);
-    const int smem = e ? (hd <= 64 ? Cfg<64, true>::BYTES : Cfg<128, true>::BYTES)
-                       : (hd <= 64 ? Cfg<64, false>::BYTES : Cfg<128, false>::BYTES);
+    cudaStream_t st = (cudaStream_t)stream;
     DS41_REQUIRE(kvh * pl.row_tiles < 65536, DS41_E_RANGE, "%s: kvh=%lld max_q=%lld nh=%lld", name,
                  (long long)kvh, (long long)max_q, (long long)nh);
-    if (int rc = cuda_check(
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
-        return rc;
-    if (int rc = launch_pdl(kern,
-                            dim3((unsigned)pl.splits, (unsigned)(kvh * pl.row_tiles), (unsigned)B),
-                            dim3(NT), smem, (cudaStream_t)stream, name, a))
-        return rc;
-    if (pl.splits == 1) return DS41_OK;
-    return launch_pdl(tree_join_kernel,
-                      dim3((unsigned)((max_q * nh + 7) / 8), (unsigned)B), dim3(256), 0,
-                      (cudaStream_t)stream, name, a);
+    if (pl.many) {
+        if (int rc = tree::launch_many(a, pl.pair, pl.row_tiles, B, name, st)) return rc;
+    } else {
+        using namespace tree;
+        const bool e = fmt == DS41_KV_E4M3;
+        auto kern = e ? (hd <= 64 ? tree_few_kernel<64, true> : tree_few_kernel<128, true>)
+                      : (hd <= 64 ? tree_few_kernel<64, false> : tree_few_kernel<128, false>);
+        const int smem = e ? (hd <= 64 ? Cfg<64, true>::BYTES : Cfg<128, true>::BYTES)
+                           : (hd <= 64 ? Cfg<64, false>::BYTES : Cfg<128, false>::BYTES);
+        if (int rc = cuda_check(
+                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                name))
+            return rc;
+        if (int rc = launch_pdl(kern, dim3((unsigned)pl.splits, (unsigned)kvh, (unsigned)B),
+                                dim3(NT), smem, st, name, a))
+            return rc;
+    }
+    if (a.parts == 1) return DS41_OK;
+    return launch_pdl(tree::tree_join_kernel, dim3((unsigned)(max_q * nh), (unsigned)B),
+                      dim3(tree::NT), 0, st, name, a);
 }

@@ -13,9 +13,14 @@ roundings:
 * the sum over n keys adds n f32 terms (and the rescaling products): n 2^-23 of
   the sum of magnitudes; the same holds for the denominator;
 * the output is rounded to bf16: 2^-8 relative.
-All of it scales with S except the last: |o - exact| <= 2^-8 |exact| +
-S (2^-8 + 2 (hd + 4) 2^-23 A + 2^-20 + 2 n 2^-23) (1 + 2^-7), the last factor
-for the products of the small terms.
+* on an e4m3 cache the weights p_j vs_j are rounded to f16 instead, 2^-11
+  relative, but not finer than 2^-25 of their reference, which is at most
+  p_max vs_max: that adds 2^-25 p_max vs_max sum_j |code_j|.
+* what lies below 2^-126 may be taken for 0 (a weight, the factor that a sink
+  leaves, an output): 2^-126 (1 + sum_j |v_j|).
+All of it scales with S except the last three: |o - exact| <= 2^-8 |exact| +
+S (2^-8 + 2 (hd + 4) 2^-23 A + 2^-20 + 2 n 2^-23) (1 + 2^-7) (+ the f16 and the
+smallest-number terms), the last factor for the products of the small terms.
 """
 from __future__ import annotations
 
@@ -42,10 +47,10 @@ def values(codes, scales):
     return codes.double() if scales is None else codes.double() * scales.double()[..., None]
 
 
-def attend(q, k, v, visible, scale, sink):
+def attend(q, k, v, visible, scale, sink, vs=None):
     """q [n, nh, hd], k, v [L, kvh, hd], visible [n, L]: (o, lse, tolerance of o,
     tolerance of lse), 64 bits.  v rows that a query does not see do not count,
-    whatever they hold."""
+    whatever they hold.  vs [L, kvh]: the scales of v on an e4m3 cache."""
     n, nh, hd = q.shape
     L, kvh = k.shape[:2]
     per = nh // kvh
@@ -69,6 +74,11 @@ def attend(q, k, v, visible, scale, sink):
         dt = (hd + 4) * 2.0 ** -23 * A + 2.0 ** -21
         rel = 2.0 ** -8 + 2 * dt + 2 * L * 2.0 ** -23
         tol[:, h] = 2.0 ** -8 * o[:, h].abs() + (p @ vh.abs()) * rel[:, None] * (1 + 2.0 ** -7)
+        tol[:, h] += 2.0 ** -126 * (1 + visible.double() @ vh.abs())
+        if vs is not None and L:
+            x = torch.where(visible.any(0), vs[:, h // per].double(), 0.0)
+            code = vh.abs() / x.clamp_min(2.0 ** -126)[:, None]
+            tol[:, h] += 2.0 ** -25 * (p.amax(1) * x.max())[:, None] * (visible.double() @ code)
         ltol[:, h] = (dt + L * 2.0 ** -23) * (1 + 2.0 ** -7) + 2.0 ** -21 * (
             1 + torch.where(torch.isfinite(lse[:, h]), lse[:, h].abs(), 0.0))
     return o, lse, tol, ltol

@@ -316,10 +316,15 @@ TREES = [
 ]
 
 
-def run_tree(g, lens, drafts, nh, kvh, hd, page, e4m3, window, sink, masked, q_heads_out=False):
+def run_tree(g, lens, drafts, nh, kvh, hd, page, e4m3, window, sink, masked, q_heads_out=False,
+             spread=0, q_gain=None):
     need = max(max(-(-n // page) for n in lens), 1)
     n_pages = need * len(lens) + 2
     cache = filled_cache(g, n_pages, kvh, page, hd, e4m3)
+    if spread:  # rows of very different sizes
+        for s in cache[2:]:
+            s.mul_(torch.exp2(torch.randint(-spread, spread + 1, s.shape, generator=g,
+                                            device=DEV).float()))
     table = torch.randperm(n_pages, generator=g, device=DEV)[:need * len(lens)].view(
         len(lens), need).int()
     # behind each sequence's end: whatever an earlier user left there
@@ -332,6 +337,8 @@ def run_tree(g, lens, drafts, nh, kvh, hd, page, e4m3, window, sink, masked, q_h
         table[b, -(-n // page):] = -5  # never read
     Tq = sum(drafts)
     q = randn(g, Tq, nh, hd)
+    if q_gain is not None:
+        q = q * q_gain
     if q_heads_out:
         q = q.transpose(0, 1).contiguous().transpose(0, 1)
     snk = torch.randn(nh, generator=g, device=DEV) if sink else None
@@ -361,8 +368,9 @@ def run_tree(g, lens, drafts, nh, kvh, hd, page, e4m3, window, sink, masked, q_h
     for b, (n, d) in enumerate(zip(lens, drafts)):
         pages = table[b, :-(-n // page)].long()
         k, v = (x[pages].transpose(1, 2).flatten(0, 1)[:n] for x in (kx, vx))
+        vs = cache.v_scales[pages].transpose(1, 2).flatten(0, 1)[:n] if e4m3 else None
         want = ref.attend(q[at:at + d], k, v, ref.tree_visible(d, n, bits[b], window, DEV),
-                          hd ** -0.5, snk)
+                          hd ** -0.5, snk, vs)
         ref.close(o[at:at + d], lse[at:at + d], *want)
         at += d
 
@@ -375,6 +383,30 @@ def test_tree(case):
 def test_tree_strided_queries():
     run_tree(gen(41), *TREES[10], q_heads_out=True)
     run_tree(gen(42), *TREES[5], q_heads_out=True)
+
+
+@pytest.mark.parametrize("spread", [3, 12, 40])
+@pytest.mark.parametrize("case", [3, 10, 12, 15])
+def test_tree_scales_far_apart(case, spread):
+    """Rows whose scales differ by up to 2^(2 spread), so that the common exponent
+    of the value scales moves along the way."""
+    run_tree(gen(300 + case), *TREES[case], spread=spread)
+
+
+@pytest.mark.parametrize("q_gain", [1e-30, 1e-4, 30.0])
+@pytest.mark.parametrize("case", [3, 10, 12])
+def test_tree_small_and_large_queries(case, q_gain):
+    run_tree(gen(320 + case), *TREES[case], q_gain=q_gain)
+
+
+def test_tree_query_with_outliers():
+    """A query channel 1000 times larger than the rest, and a zero query."""
+    for case in (3, 10, 12):
+        c = list(TREES[case])
+        q_gain = torch.ones(sum(c[1]), c[2], c[4], device=DEV, dtype=torch.bfloat16)
+        q_gain[:, :, 5] = 1000.0
+        q_gain[0, 1] = 0.0
+        run_tree(gen(340 + case), *c, q_gain=q_gain)
 
 
 def test_tree_token_that_sees_nothing():
