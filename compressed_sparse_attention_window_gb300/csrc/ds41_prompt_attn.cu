@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (warp == 0 && lane == 0 && jhi > jlo) {
             const int head0 = grp * p.G;
             const int kvh = grp / p.subs;
@@ -278,85 +278,79 @@ __global__ void __launch_bounds__(THREADS, 1)
             drain_bar(b_q, 0, p.status);
             for (uint32_t s = 0; s < C::STAGES && s < n; s++)
                 drain_bar(&b_full[s], ((n - 1 - s) / C::STAGES) & 1, p.status);
-        } else if (warp == 1 && lane == 0 && jhi > jlo) {
-            const uint32_t IDESC_S = idesc_bf16(128, KB, 0, 0);
-            const uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
-            const int ksteps = p.hd / 16;
+        } else if (warp == 1 && jhi > jlo) {
+            constexpr uint32_t IDESC_S = idesc_bf16(128, KB, 0, 0);
+            constexpr uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
             const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
             const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
             const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
             uint32_t done_p[2] = {0, 0};
-            auto stage_of = [&](int j, int kv) { return (uint32_t)(2 * (j - jlo) + kv); };
             auto wait_stage = [&](uint32_t n) {
                 const bool ok =
-                    wait_bar(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
+                    warp_wait(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
                 tc_fence_after();
                 return ok;
             };
-            auto qk = [&](int t, uint32_t n) {
-                const uint64_t a = qd + ((t * C::TILE) >> 4);
-                const uint64_t b = kd + (((n % C::STAGES) * C::TILE) >> 4);
-                for (int k = 0; k < ksteps; k++) {
-                    const uint32_t off = ((k >> 2) * C::BLK + (k & 3) * 32) >> 4;
-                    tc_mma(tmem + TM_S + 128 * t, a + off, b + off, IDESC_S, k > 0);
-                }
-                tc_commit(&b_s[t]);
-            };
-            auto pv = [&](int t, uint32_t n, int steps, bool acc) {
-                const uint64_t b = vd + (((n % C::STAGES) * C::TILE) >> 4);
-                for (int k = 0; k < steps; k++)
-                    tc_mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * k,
-                                  b + ((k * 2048) >> 4), IDESC_O, acc || k > 0);
-            };
-            bool ok = wait_bar(b_q, 0, abort_f, p.status) && wait_stage(0);
-            if (ok) {
+            auto stage_off = [&](uint32_t n) { return ((n % C::STAGES) * C::TILE) >> 4; };
+            bool ok = warp_wait(b_q, 0, abort_f, p.status) && wait_stage(0);
+            if (ok && elect_one()) {
+#pragma unroll
                 for (int t = 0; t < 2; t++)
-                    if (jlo >= rg[t].lo && jlo < rg[t].hi) qk(t, 0);
+                    if (jlo >= rg[t].lo && jlo < rg[t].hi) {
+                        mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t, qd + ((t * C::TILE) >> 4),
+                                               kd + stage_off(0));
+                        tc_commit(&b_s[t]);
+                    }
                 tc_commit(&b_empty[0]);
             }
             for (int j = jlo; j < jhi && ok; j++) {
-                const uint32_t nv = stage_of(j, 1), nk = stage_of(j + 1, 0);
+                const uint32_t nv = 2 * (uint32_t)(j - jlo) + 1, nk = nv + 1;
                 ok = wait_stage(nv);
-                const bool last = j == jhi - 1 && tail > 0;
-                if (ok && last) {
-                    mbar_arrive(b_tail);
-                    ok = wait_bar(b_fix, 0, abort_f, p.status);
+                if (ok && j == jhi - 1 && tail > 0) {
+                    if (lane == 0) mbar_arrive(b_tail);
+                    ok = warp_wait(b_fix, 0, abort_f, p.status);
                     tc_fence_after();
                 }
-                const int steps = last ? (tail + 15) / 16 : KB / 16;
                 bool have_k = false;
-                for (int t = 0; t < 2 && ok; t++) {
-                    if (j >= rg[t].lo && j < rg[t].hi) {
-                        if (!wait_bar(&b_p[t], done_p[t] & 1, abort_f, p.status)) {
-                            ok = false;
-                            break;
-                        }
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const bool now = j >= rg[t].lo && j < rg[t].hi;
+                    const bool next = j + 1 >= rg[t].lo && j + 1 < rg[t].hi;
+                    if (ok && now) {
+                        ok = warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
                         done_p[t]++;
                         tc_fence_after();
-                        pv(t, nv, steps, j > rg[t].lo);
-                        if (j + 1 == rg[t].hi) tc_commit(&b_o[t]);
                     }
-                    if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
-                    if (j + 1 >= rg[t].lo && j + 1 < rg[t].hi) {
-                        if (!have_k && !wait_stage(nk)) {
-                            ok = false;
-                            break;
-                        }
+                    if (ok && next && !have_k) {
+                        ok = wait_stage(nk);
                         have_k = true;
-                        qk(t, nk);
                     }
+                    if (ok && elect_one()) {
+                        if (now) {
+                            mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
+                                                   vd + stage_off(nv), j > rg[t].lo);
+                            if (j + 1 == rg[t].hi) tc_commit(&b_o[t]);
+                        }
+                        if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
+                        if (next) {
+                            mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                                   qd + ((t * C::TILE) >> 4), kd + stage_off(nk));
+                            tc_commit(&b_s[t]);
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (ok && j + 1 < jhi) {
                     if (!have_k) ok = wait_stage(nk);
-                    tc_commit(&b_empty[nk % C::STAGES]);
+                    if (ok && elect_one()) tc_commit(&b_empty[nk % C::STAGES]);
+                    __syncwarp();
                 }
             }
         } else if (warp == 2 && tail > 0 && jhi > jlo) {
-            // zero the V rows behind the last key, up to the next multiple of 16
+            // zero the V rows behind the last key
             const uint32_t n = 2 * (uint32_t)(jhi - 1 - jlo) + 1, s = n % C::STAGES;
-            if (wait_bar(b_tail, 0, abort_f, p.status)) {
-                const int rows = ((tail + 15) / 16) * 16 - tail;
-                for (int x = lane; x < rows * C::NB * 8; x += 32) {
+            if (warp_wait(b_tail, 0, abort_f, p.status)) {
+                for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
                     const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
                     *reinterpret_cast<uint4*>(sm + C::KV_OFF + s * C::TILE + (piece / 8) * C::BLK +
                                               r * 128 + (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -367,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         const int t = (warp - 4) >> 2;
         const Range r = rg[t];
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -383,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0;
         bool ok = true;
         for (int j = r.lo; j < r.hi; j++, ph++) {
-            ok = __all_sync(0xffffffffu, wait_bar(&b_s[t], ph & 1, abort_f, p.status));
+            ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
             if (!ok) break;
             tc_fence_after();
             const int64_t j0 = (int64_t)j * KB;
@@ -412,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (r.count > 0 && ok) {
             uint16_t* dst = p.o + at * p.hd;
             if (r.hi > r.lo) {
-                ok = __all_sync(0xffffffffu, wait_bar(&b_o[t], 0, abort_f, p.status));
+                ok = warp_wait(&b_o[t], 0, abort_f, p.status);
                 tc_fence_after();
             }
             if (ok) {

@@ -29,6 +29,39 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+// One lane of a converged warp, the same one every time.  The warps that issue
+// MMAs run their loops as whole warps and elect a lane around each sequence: a
+// loop that one lane runs alone cannot keep its descriptors in uniform registers,
+// and every MMA then waits for them to be moved there (measured: 144 cycles an
+// MMA instead of 64, twice the time of a long prompt).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+// A whole warp's bounded wait: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_f,
+                                          unsigned int* status) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_f, status));
+}
+// S = Q K^T for 128 rows and 128 keys: both K-major in 64-column blocks of
+// [128 rows][128 bytes], 128-byte swizzled.
+template <int D, uint32_t IDESC>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k) {
+#pragma unroll
+    for (int x = 0; x < D / 16; x++) {
+        constexpr uint32_t BLK = 128 * 128;
+        const uint32_t off = ((x >> 2) * BLK + (x & 3) * 32) >> 4;
+        tc_mma(d, q + off, k + off, IDESC, x > 0);
+    }
+}
+// O (+)= P V, P in tensor memory, V [128 keys][D] in the same blocks
+template <int D, uint32_t IDESC>
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint64_t v, bool acc) {
+#pragma unroll
+    for (int x = 0; x < 8; x++) tc_mma_ts(d, p + 8 * x, v + ((x * 2048) >> 4), IDESC, acc || x > 0);
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

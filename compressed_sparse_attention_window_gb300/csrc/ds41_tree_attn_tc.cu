@@ -76,12 +76,6 @@ __device__ __forceinline__ int pos_v(int j, int n) {
     return min(LA, n) + j + min(j, max(0, n - LA));
 }
 
-// A whole warp's bounded wait: all of its lanes go on, or none.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_f,
-                                          unsigned int* status) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_f, status));
-}
-
 // Which of the keys j .. j + 31 a row sees.
 __device__ __forceinline__ uint32_t low_bits(int64_t n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -214,7 +208,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     const int n_ring = 2 * n_blocks;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 72 : 88));
         if (warp == 0 && !E4M3) {
             // pages -> stages, and which keys are real
             bool ok = true;
@@ -278,36 +272,35 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             }
             for (int st = 0; st < C::STAGES; st++)
                 if (armed[st]) drain_bar(&b_full[st], (armed[st] - 1) & 1, a.status);
-        } else if (warp == 1 && lane == 0) {
-            const uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
-            const uint32_t IDESC_O = E4M3 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
-            const int ksteps = a.hd / 16;
+        } else if (warp == 1) {
+            constexpr uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
+            constexpr uint32_t IDESC_O = E4M3 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
             const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
             const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
             const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
-            uint32_t done_p[2] = {0, 0};
+            int done_p[2] = {0, 0};
             auto wait_entry = [&](int e) {
-                const bool ok = wait_bar(&b_full[e % C::STAGES], (e / C::STAGES) & 1, abort_f,
-                                         a.status);
+                const bool ok =
+                    warp_wait(&b_full[e % C::STAGES], (e / C::STAGES) & 1, abort_f, a.status);
                 tc_fence_after();
                 return ok;
             };
-            auto qk = [&](int t, int e) {
-                const uint64_t x = qd + ((PAIR ? t * C::TILE : 0) >> 4);
-                const uint64_t y = kd + (((e % C::STAGES) * C::TILE) >> 4);
-                for (int k = 0; k < ksteps; k++) {
-                    const uint32_t off = ((k >> 2) * C::BLK + (k & 3) * 32) >> 4;
-                    tc_mma(tmem + TM_S + 128 * t, x + off, y + off, IDESC_S, k > 0);
-                }
+            auto stage_off = [&](int e) { return ((e % C::STAGES) * C::TILE) >> 4; };
+            auto scores = [&](int t, int e) {
+                mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                       qd + ((PAIR ? t * C::TILE : 0) >> 4), kd + stage_off(e));
                 tc_commit(&b_s[t]);
             };
             bool ok = true;
             for (int j = 0; j < min(C::LA, n_blocks) && ok; j++) {
                 ok = wait_entry(j);
-                if (!ok) break;
-                for (int t = 0; t < 2; t++)
-                    if (uses(t, j)) qk(t, j);
-                tc_commit(&b_empty[j % C::STAGES]);
+                if (ok && elect_one()) {
+#pragma unroll
+                    for (int t = 0; t < 2; t++)
+                        if (uses(t, j)) scores(t, j);
+                    tc_commit(&b_empty[j % C::STAGES]);
+                }
+                __syncwarp();
             }
             for (int j = 0; j < n_blocks && ok; j++) {
                 const int ev = pos_v<C::LA>(j, n_blocks);
@@ -315,36 +308,37 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const int ek = pos_k<C::LA>(j + C::LA);
                 ok = wait_entry(ev);
                 if (ok && !E4M3 && tail < KB && j == n_blocks - 1) {
-                    mbar_arrive(b_tail);
-                    ok = wait_bar(b_fix, 0, abort_f, a.status);
+                    if (lane == 0) mbar_arrive(b_tail);
+                    ok = warp_wait(b_fix, 0, abort_f, a.status);
                     tc_fence_after();
                 }
                 bool have_k = false;
-                for (int t = 0; t < 2 && ok; t++) {
-                    if (uses(t, j)) {
-                        if (!wait_bar(&b_p[t], done_p[t] & 1, abort_f, a.status)) {
-                            ok = false;
-                            break;
-                        }
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const bool now = uses(t, j), next = more && uses(t, j + C::LA);
+                    if (ok && now) {
+                        ok = warp_wait(&b_p[t], done_p[t] & 1, abort_f, a.status);
                         done_p[t]++;
                         tc_fence_after();
-                        const uint64_t y = vd + (((ev % C::STAGES) * C::TILE) >> 4);
-                        for (int k = 0; k < KB / 16; k++)
-                            tc_mma_ts(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t + 8 * k,
-                                      y + ((k * 2048) >> 4), IDESC_O, done_p[t] > 1 || k > 0);
-                        if ((int)done_p[t] == nt[t]) tc_commit(&b_o[t]);
                     }
-                    if (t == 1) tc_commit(&b_empty[ev % C::STAGES]);
-                    if (more && uses(t, j + C::LA)) {
-                        if (!have_k && !wait_entry(ek)) {
-                            ok = false;
-                            break;
+                    if (ok && elect_one()) {
+                        if (now) {
+                            mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
+                                                   vd + stage_off(ev), done_p[t] > 1);
+                            if (done_p[t] == nt[t]) tc_commit(&b_o[t]);
                         }
+                        if (t == 1) tc_commit(&b_empty[ev % C::STAGES]);
+                    }
+                    __syncwarp();
+                    if (ok && next) {
+                        if (!have_k) ok = wait_entry(ek);
                         have_k = true;
-                        qk(t, ek);
+                        if (ok && elect_one()) scores(t, ek);
+                        __syncwarp();
                     }
                 }
-                if (ok && more) tc_commit(&b_empty[ek % C::STAGES]);
+                if (ok && more && elect_one()) tc_commit(&b_empty[ek % C::STAGES]);
+                __syncwarp();
             }
         } else if (warp == 2 && !E4M3 && tail < KB) {
             // the V rows behind the last key hold whatever an earlier user left
@@ -362,7 +356,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             }
         }
     } else if (E4M3 && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
         const int tid = threadIdx.x - 384;
         constexpr int PIECES = KB * D / 16 / 128;  // 16-code pieces a thread has of a tile
         // piece x of this thread: row and which of the row's pieces.  Eight lanes
@@ -503,7 +497,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
         }
         cp_async_wait<0>();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 176 : 224));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 176 : 208));
         const int t = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tm_s = tmem + lanes + TM_S + 128 * t, tm_o = tmem + lanes + TM_O + 128 * t;
