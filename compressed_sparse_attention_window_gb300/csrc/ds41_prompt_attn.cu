@@ -390,8 +390,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 4; i++)
                     vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
             }
-            softmax_block<D, false>(tm_s, tm_o, j > r.lo, masked, vis, c, nullptr, nullptr, 0.0f,
-                                    live, st);
+            if (masked)
+                softmax_block<D, false, true>(tm_s, tm_o, j > r.lo, vis, c, nullptr, nullptr, 0.0f,
+                                              live, st);
+            else
+                softmax_block<D, false, false>(tm_s, tm_o, j > r.lo, vis, c, nullptr, nullptr,
+                                               0.0f, live, st);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b_p[t]);

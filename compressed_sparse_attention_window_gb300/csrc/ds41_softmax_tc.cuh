@@ -130,55 +130,100 @@ __device__ __forceinline__ float scale_exponent(float vmax) {
     return fmaxf((float)((int)(__float_as_uint(vmax) >> 23) - 127), RowState::VS_MIN);
 }
 
+// 32 scores of a row, scaled by ks, with those that are not seen at -inf.
+template <bool SCALED, bool MASKED>
+__device__ __forceinline__ void prepare32(uint32_t (&s)[32], const float* ks, uint32_t vis) {
+    if (SCALED) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const float4 k4 = *reinterpret_cast<const float4*>(ks + e);
+            float a, b;
+            unf2(mul2(f2(u2f(s[e]), u2f(s[e + 1])), f2(k4.x, k4.y)), a, b);
+            s[e] = __float_as_uint(a);
+            s[e + 1] = __float_as_uint(b);
+            unf2(mul2(f2(u2f(s[e + 2]), u2f(s[e + 3])), f2(k4.z, k4.w)), a, b);
+            s[e + 2] = __float_as_uint(a);
+            s[e + 3] = __float_as_uint(b);
+        }
+    }
+    if (MASKED) {
+#pragma unroll
+        for (int e = 0; e < 32; e++)
+            if (!((vis >> e) & 1)) s[e] = 0xff800000u;
+    }
+}
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+    float a = fmaxf(u2f(s[0]), u2f(s[1])), b = fmaxf(u2f(s[2]), u2f(s[3]));
+#pragma unroll
+    for (int e = 4; e < 32; e += 4) {
+        a = max3(a, u2f(s[e]), u2f(s[e + 1]));
+        b = max3(b, u2f(s[e + 2]), u2f(s[e + 3]));
+    }
+    return fmaxf(a, b);
+}
+// 32 scores -> 32 weights, two per column from tm_p on; their sum joins `sum`
+template <bool SCALED, bool MASKED>
+__device__ __forceinline__ void weights32(uint32_t (&s)[32], uint32_t tm_p, float c, float base,
+                                          float m_first, const float* vs, uint32_t vis,
+                                          uint64_t (&sum)[2]) {
+    const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
+    if (m_first != 0.0f) {  // (see softmax_block)
+#pragma unroll
+        for (int e = 0; e < 32; e++) s[e] = __float_as_uint(u2f(s[e]) - m_first);
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        float p[4];
+        unf2(fma2(f2(u2f(s[e]), u2f(s[e + 1])), c2, b2), p[0], p[1]);
+        unf2(fma2(f2(u2f(s[e + 2]), u2f(s[e + 3])), c2, b2), p[2], p[3]);
+#pragma unroll
+        for (int x = 0; x < 4; x++) p[x] = ex2(p[x]);
+        sum[0] = add2(sum[0], f2(p[0], p[1]));
+        sum[1] = add2(sum[1], f2(p[2], p[3]));
+        if (SCALED) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
+            unf2(mul2(f2(p[0], p[1]), f2(v4.x, v4.y)), p[0], p[1]);
+            unf2(mul2(f2(p[2], p[3]), f2(v4.z, v4.w)), p[2], p[3]);
+            if (MASKED) {
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+                    if (!((vis >> (e + x)) & 1)) p[x] = 0.0f;
+            }
+        }
+        pk[e / 2] = SCALED ? f16x2(p[0], p[1]) : bf16x2(p[0], p[1]);
+        pk[e / 2 + 1] = SCALED ? f16x2(p[2], p[3]) : bf16x2(p[2], p[3]);
+    }
+    tc_st16(tm_p, pk);
+}
+
 // One thread's row: its 128 scores of the block (columns tm_s .. of its lane)
 // become weights, two per column from tm_s on: bf16, or f16 when SCALED.
 //   t_j = c S_j (SCALED: c ks_j S_j), p_j = 2^(t_j - reference), l += p_j, the
 //   weight p_j (SCALED: p_j vs_j; 0 for a key that is not seen, whatever vs_j
 //   holds)
-// Keys whose bit of vis is clear are not seen (vis is read when `masked`).
+// MASKED: keys whose bit of vis is clear are not seen.  A block that every row
+// sees whole takes the other instance: as a run-time choice the compiler turned
+// the selects into predicated code for every block, twice the instructions.
 // Where the maximum exceeds the reference by 2^4 it moves and l and, with
 // `have_o`, the D columns of the output at tm_o are rescaled; the caller has
 // seen the products before this block complete.  All lanes of a warp take part;
 // `live` = the row exists.  vmax: the largest vs of the block.
-template <int D, bool SCALED>
+template <int D, bool SCALED, bool MASKED>
 __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool have_o,
-                                              bool masked, const uint32_t (&vis)[4], float c,
+                                              const uint32_t (&vis)[4], float c,
                                               const float* ks, const float* vs, float vmax,
                                               bool live, RowState& st) {
     uint32_t s[4][32];
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
     tc_wait_ld();
-    if (SCALED) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * i + e);
-                float a, b;
-                unf2(mul2(f2(u2f(s[i][e]), u2f(s[i][e + 1])), f2(k4.x, k4.y)), a, b);
-                s[i][e] = __float_as_uint(a);
-                s[i][e + 1] = __float_as_uint(b);
-                unf2(mul2(f2(u2f(s[i][e + 2]), u2f(s[i][e + 3])), f2(k4.z, k4.w)), a, b);
-                s[i][e + 2] = __float_as_uint(a);
-                s[i][e + 3] = __float_as_uint(b);
-            }
-    }
-    if (masked) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 32; e++)
-                if (!((vis[i] >> e) & 1)) s[i][e] = 0xff800000u;
-    }
-    float mx[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        mx[i] = fmaxf(u2f(s[i][0]), u2f(s[i][1]));
-#pragma unroll
-        for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], u2f(s[i][e]), u2f(s[i][e + 1]));
+        prepare32<SCALED, MASKED>(s[i], SCALED ? ks + 32 * i : nullptr, vis[i]);
+        top = fmaxf(top, max32(s[i]));
     }
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     // (-inf - -inf is NaN: no move)
     const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
     const bool vmove = SCALED && vmax > st.vlim;
@@ -206,44 +251,18 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
         }
     }
     float base = st.m == -INFINITY ? 0.0f : SCALED ? fmaf(st.m, c, st.lr) : st.m * c;
+    float m_first = 0.0f;
     if (fabsf(base) > 0x1p22f) {
         // c m itself is rounded by more than a fraction of one power of two: take
         // the differences first
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        m_first = st.m;
         base = SCALED ? st.lr : 0.0f;
     }
-    const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int h = 0; h < 4; h++) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-            float p[4];
-            unf2(fma2(f2(u2f(s[h][e]), u2f(s[h][e + 1])), c2, b2), p[0], p[1]);
-            unf2(fma2(f2(u2f(s[h][e + 2]), u2f(s[h][e + 3])), c2, b2), p[2], p[3]);
-#pragma unroll
-            for (int x = 0; x < 4; x++) p[x] = ex2(p[x]);
-            sum[0] = add2(sum[0], f2(p[0], p[1]));
-            sum[1] = add2(sum[1], f2(p[2], p[3]));
-            if (SCALED) {
-                const float4 v4 = *reinterpret_cast<const float4*>(vs + 32 * h + e);
-                unf2(mul2(f2(p[0], p[1]), f2(v4.x, v4.y)), p[0], p[1]);
-                unf2(mul2(f2(p[2], p[3]), f2(v4.z, v4.w)), p[2], p[3]);
-                if (masked) {
-#pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        if (!((vis[h] >> (e + x)) & 1)) p[x] = 0.0f;
-                }
-            }
-            pk[e / 2] = SCALED ? f16x2(p[0], p[1]) : bf16x2(p[0], p[1]);
-            pk[e / 2 + 1] = SCALED ? f16x2(p[2], p[3]) : bf16x2(p[2], p[3]);
-        }
-        tc_st16(tm_s + 16 * h, pk);
-    }
+    for (int i = 0; i < 4; i++)
+        weights32<SCALED, MASKED>(s[i], tm_s + 16 * i, c, base, m_first,
+                                  SCALED ? vs + 32 * i : nullptr, vis[i], sum);
     float a, b;
     unf2(add2(sum[0], sum[1]), a, b);
     st.l += a + b;

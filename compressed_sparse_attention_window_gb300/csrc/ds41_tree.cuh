@@ -28,12 +28,14 @@ struct Args {
     int max_q, nh, kvh, hd, G;
     float scale_log2;
     int64_t window;
-    // the split of the keys: chunk keys a split from the first one on (rounded
-    // down to `align`), `per` partial results each; with parts > 1:
-    // part [parts][Tq][nh][hd], part_ml [parts][Tq][nh] (reference in log2, sum)
-    int chunk, align, per, parts;
-    float* part;
-    float2* part_ml;
+    // the work: see `Share`
+    int block, align, tile_rows;  // keys of a block; first keys are multiples of align; rows of a tile
+    int row_tiles;                // of the most drafted tokens
+    int workers;
+    float* part;                  // [workers][2][tile_rows][hd]
+    float2* part_ml;              // [workers][2][tile_rows]: reference (log2), sum
+    int2* ends;                   // [B][kvh][row_tiles]: first and last worker of a unit
+    int B;
     unsigned int* status;
 };
 
@@ -57,6 +59,117 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b) {
 __device__ __forceinline__ int first_key(const Args& a, const Seq& s) {
     const int64_t lo = a.window ? (int64_t)s.len - s.n - a.window : 0;
     return lo > 0 ? (int)(lo & ~(int64_t)(a.align - 1)) : 0;
+}
+
+__device__ __forceinline__ int blocks_of(const Args& a, const Seq& s) {
+    return (s.len - first_key(a, s) + a.block - 1) / a.block;
+}
+__device__ __forceinline__ int tiles_of(const Args& a, const Seq& s) {
+    return (s.n * a.G + a.tile_rows - 1) / a.tile_rows;
+}
+
+// How the work is shared.  A unit is a tile of rows of one (sequence, key/value
+// head); it has a number of key blocks that only the device knows.  All blocks
+// of all units, in order (sequence, head, tile of rows, block), are dealt to the
+// workers (CTAs) in equal runs, so that sequences of different lengths leave no
+// worker with more than its share.  A run covers whole units and at most a part
+// of one at each of its ends; whole units go straight to the output, parts to
+// the worker's two slots of the workspace (slot 0: a unit that an earlier worker
+// began, slot 1: one that a later worker goes on with), to be joined.
+struct Share {
+    int b;         // sequence of the run's first block
+    int64_t at;    // that block, counted within the sequence
+    int64_t left;  // blocks of the run
+};
+// Every thread of the CTA calls it; `report` (one worker) raises DS41_E_INDEX
+// for sequences that break their limits.  sh: 2 * NT / 32 + 4 int64 of shared memory.
+template <int NT>
+__device__ __forceinline__ Share find_share(const Args& a, int64_t* sh, bool report) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (a.B + NT - 1) / NT;
+    const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; b++) {
+        const Seq s = load_seq(a, b);
+        if (s.ok && s.n > 0) mine += (int64_t)blocks_of(a, s) * tiles_of(a, s) * a.kvh;
+        if (!s.ok && report) raise_status(a.status, DS41_E_INDEX);
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += v;
+    }
+    if (lane == 31) sh[warp] = sum;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < NT / 32; i++) {
+        if (i < warp) before += sh[i];
+        total += sh[i];
+    }
+    // with fewer blocks than workers the last workers have none (and not some in
+    // between: the parts of a unit are with consecutive workers)
+    const int64_t n = min((int64_t)a.workers, total), w = blockIdx.x;
+    const int64_t x0 = w < n ? total * w / n : 0, x1 = w < n ? total * (w + 1) / n : 0;
+    int64_t* out = sh + NT / 32;
+    const int64_t start = before + sum - mine;
+    if (x1 > x0 && x0 >= start && x0 < start + mine) {
+        int64_t rem = x0 - start;
+        int b = b0;
+        for (; b < b1; b++) {
+            const Seq s = load_seq(a, b);
+            const int64_t n =
+                s.ok && s.n > 0 ? (int64_t)blocks_of(a, s) * tiles_of(a, s) * a.kvh : 0;
+            if (rem < n) break;
+            rem -= n;
+        }
+        out[0] = b;
+        out[1] = rem;
+    }
+    __syncthreads();
+    Share r;
+    r.b = x1 > x0 ? (int)out[0] : 0;
+    r.at = x1 > x0 ? out[1] : 0;
+    r.left = x1 - x0;
+    return r;
+}
+
+// The next piece of a worker's run: blocks first .. first + count - 1 of a unit
+// with n_blocks of them.  Uniform over the CTA; false when the run is done.
+struct Piece {
+    Seq s;
+    int b, h, tile, first, count, n_blocks;
+};
+__device__ __forceinline__ bool next_piece(const Args& a, Share& w, Piece& p) {
+    if (w.left <= 0) return false;
+    for (;; w.b++, w.at = 0) {
+        if (w.b >= a.B) return false;
+        p.s = load_seq(a, w.b);
+        if (!p.s.ok || p.s.n == 0) continue;
+        p.n_blocks = blocks_of(a, p.s);
+        const int tiles = tiles_of(a, p.s);
+        const int64_t unit = w.at / p.n_blocks;
+        if (unit >= (int64_t)tiles * a.kvh) continue;
+        p.b = w.b;
+        p.h = (int)(unit / tiles);
+        p.tile = (int)(unit % tiles);
+        p.first = (int)(w.at - unit * p.n_blocks);
+        p.count = (int)min((int64_t)(p.n_blocks - p.first), w.left);
+        w.at += p.count;
+        w.left -= p.count;
+        return true;
+    }
+}
+__device__ __forceinline__ bool is_whole(const Piece& p) { return p.count == p.n_blocks; }
+// the slot of a piece that is not whole
+__device__ __forceinline__ int64_t slot_of(const Piece& p) {
+    return 2 * (int64_t)blockIdx.x + (p.first == 0 ? 1 : 0);
+}
+// one thread: which workers a unit's first and last block are with
+__device__ __forceinline__ void note_ends(const Args& a, const Piece& p) {
+    int2* e = a.ends + ((int64_t)p.b * a.kvh + p.h) * a.row_tiles + p.tile;
+    if (p.first == 0) e->x = blockIdx.x;
+    if (p.first + p.count == p.n_blocks) e->y = blockIdx.x;
 }
 
 // What one row sees: of the earlier keys (below pre) those behind lo, of the
@@ -95,10 +208,9 @@ __device__ __forceinline__ bool seen(const RowView& w, int j, int len) {
     return (w.bits[u >> 6] >> (u & 63)) & 1;
 }
 
-// The tensor-core kernel, for more than 16 rows per key/value head; pair: two
-// tiles of 128 rows a CTA, else one (of at most 128 rows, two partial results).
-int launch_many(const Args& a, bool pair, int row_tiles, int64_t B, const char* name,
-                cudaStream_t st);
+// The tensor-core kernel, for more than 16 rows per key/value head, in tiles of
+// 256 rows, or of 128 where no sequence has more.
+int launch_many(const Args& a, const char* name, cudaStream_t st);
 
 }  // namespace tree
 }  // namespace ds41

@@ -17,8 +17,8 @@
 //
 // What bounds it.  Every cache row is read once for 16 rows of queries: HBM
 // bandwidth, if enough is in flight and the conversion of codes keeps up.  So
-// the keys of a sequence are split over CTAs (chunks of a length that fills the
-// GPU), every warp streams its own 16-key groups (a group lies in one page, so
+// the key blocks of all sequences are dealt to the CTAs in equal runs (Share in
+// ds41_tree.cuh), every warp streams its own 16-key groups (a group lies in one page, so
 // its K and its V are one contiguous run each) through a private ring of
 // cp.async stages, with no barrier between warps until the end, and the fragments
 // are taken from shared memory with an order of hd (for Q K^T) and of the output
@@ -33,7 +33,8 @@ namespace tree {
 
 constexpr int WARPS = 4;
 constexpr int NT = WARPS * 32;
-constexpr int GROUP = 16;  // keys of a group
+constexpr int GROUP = 16;          // keys of a group
+constexpr int BLOCK = WARPS * GROUP;  // keys of a block: a group for every warp
 
 template <int HD, bool E4M3>
 struct Cfg {
@@ -63,23 +64,21 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     pdl_wait();
     using C = Cfg<HD, E4M3>;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sh[2 * WARPS + 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const Seq s = load_seq(a, b);
-    if (!s.ok) {
-        if (threadIdx.x == 0) raise_status(a.status, DS41_E_INDEX);
-        return;
-    }
+    Share share = find_share<NT>(a, sh, blockIdx.x == 0);
+    Piece pc;
+    while (next_piece(a, share, pc)) {
+    const Seq s = pc.s;
+    const int h = pc.h;
     const int rows = s.n * a.G;  // at most 16
-    if (rows == 0) return;
-    const int k_first = first_key(a, s);
-    const int k0 = k_first + split * a.chunk, k1 = min(s.len, k0 + a.chunk);
-    if (k0 >= k1 && split > 0) return;  // (a sequence without keys has its split 0)
+    const int k0 = first_key(a, s) + pc.first * BLOCK, k1 = min(s.len, k0 + pc.count * BLOCK);
+    if (threadIdx.x == 0) note_ends(a, pc);
 
     uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
-    const int n_groups = k0 < k1 ? (k1 - k0 + GROUP - 1) / GROUP : 0;
+    const int n_groups = (k1 - k0 + GROUP - 1) / GROUP;
     const int mine = (n_groups - warp + WARPS - 1) / WARPS;  // groups warp, warp + 4, ...
-    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    const int32_t* table = a.table + (int64_t)pc.b * a.max_pages;
     unsigned bad = 0;  // stages whose page does not exist
 
     auto fetch = [&](int i) {
@@ -322,7 +321,6 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         }
         __syncwarp();  // the stage is read before it is filled again
     }
-    pdl_trigger();
     cp_async_wait<0>();
     __syncthreads();
     // ---- the warps' results: through shared memory, 16 rows ----
@@ -345,49 +343,53 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     }
     __syncthreads();
     constexpr int PER = NT / 16;  // threads of a row
-    const int row = threadIdx.x / PER, part = threadIdx.x % PER;
-    const int r = row;
-    if (r >= rows) return;
-    float mm = -INFINITY, f[WARPS], ll = 0.0f;
+    const int r = threadIdx.x / PER, part = threadIdx.x % PER;
+    if (r < rows) {
+        float mm = -INFINITY, f[WARPS], ll = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + row) * P + HD]);
-    const float base = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-    for (int w = 0; w < WARPS; w++) {
-        f[w] = exp2f(out[(w * 16 + row) * P + HD] - base);
-        ll += f[w] * out[(w * 16 + row) * P + HD + 1];
-    }
-    const int t = r / a.G, head = h * a.G + r % a.G;
-    const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
-    float inv = 1.0f;
-    if (a.parts == 1) {
-        const tc::RowEnd end = tc::row_end(mm, ll, a.sink ? a.sink[head] : -INFINITY);
-        inv = end.factor;
-        if (a.lse && part == 0) a.lse[at] = end.lse;
-    }
-    float* po = a.part + ((int64_t)split * a.Tq * a.nh + at) * a.hd;
-    for (int x = part * 4; x < a.hd; x += PER * 4) {
-        float v[4] = {0, 0, 0, 0};
+        for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + r) * P + HD]);
+        const float base = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
         for (int w = 0; w < WARPS; w++) {
-            const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + row) * P + x]);
-            v[0] += f[w] * ow.x;
-            v[1] += f[w] * ow.y;
-            v[2] += f[w] * ow.z;
-            v[3] += f[w] * ow.w;
+            f[w] = exp2f(out[(w * 16 + r) * P + HD] - base);
+            ll += f[w] * out[(w * 16 + r) * P + HD + 1];
         }
-        if (a.parts == 1)
-            *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
-                make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
-        else
-            *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
+        const int t = r / a.G, head = h * a.G + r % a.G;
+        const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
+        const bool whole = is_whole(pc);
+        float inv = 1.0f;
+        if (whole) {
+            const tc::RowEnd end = tc::row_end(mm, ll, a.sink ? a.sink[head] : -INFINITY);
+            inv = end.factor;
+            if (a.lse && part == 0) a.lse[at] = end.lse;
+        } else if (part == 0) {
+            a.part_ml[slot_of(pc) * 16 + r] = make_float2(mm, ll);
+        }
+        float* po = a.part + (slot_of(pc) * 16 + r) * a.hd;
+        for (int x = part * 4; x < a.hd; x += PER * 4) {
+            float v[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < WARPS; w++) {
+                const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + r) * P + x]);
+                v[0] += f[w] * ow.x;
+                v[1] += f[w] * ow.y;
+                v[2] += f[w] * ow.z;
+                v[3] += f[w] * ow.w;
+            }
+            if (whole)
+                *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
+                    make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
+            else
+                *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
+        }
     }
-    if (a.parts > 1 && part == 0)
-        a.part_ml[(int64_t)split * a.Tq * a.nh + at] = make_float2(mm, ll);
+    __syncthreads();  // the results are read before the rings are filled again
+    }
+    pdl_trigger();
 }
 
-// One CTA per (token, head) of a sequence: its partial results joined, the sink
-// added.  Warp w takes the parts w, w + 4, ..., four rows in flight.
+// One CTA per (token, head): where its unit was shared, the parts joined and the
+// sink added.  Warp w takes the parts w, w + 4, ..., four rows in flight.
 __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
@@ -396,11 +398,18 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Seq s = load_seq(a, blockIdx.y);
     if (!s.ok || (int)blockIdx.x >= s.n * a.nh) return;
-    const int head = (int)blockIdx.x % a.nh;
-    const int64_t at = (int64_t)s.q0 * a.nh + blockIdx.x, step = a.Tq * a.nh;
-    const int n = a.per * max(1, (s.len - first_key(a, s) + a.chunk - 1) / a.chunk);
+    const int t = (int)blockIdx.x / a.nh, head = (int)blockIdx.x % a.nh;
+    const int r = t * a.G + head % a.G;
+    const int2 ends =
+        a.ends[((int64_t)blockIdx.y * a.kvh + head / a.G) * a.row_tiles + r / a.tile_rows];
+    if (ends.x == ends.y) return;  // the one worker has written the output
+    const int n = ends.y - ends.x + 1;
+    auto index = [&](int x) {
+        return (2 * (int64_t)(ends.x + x) + (x == 0 ? 1 : 0)) * a.tile_rows + r % a.tile_rows;
+    };
+    const int64_t at = (int64_t)s.q0 * a.nh + blockIdx.x;
     float m = -INFINITY, l = 0.0f;
-    for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[x * step + at].x);
+    for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[index(x)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     const float base = m == -INFINITY ? 0.0f : m;
@@ -408,10 +417,10 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     const bool mine = lane * 4 < a.hd;
 #pragma unroll 4
     for (int x = warp; x < n; x += WARPS) {
-        const float2 ml = a.part_ml[x * step + at];
-        const float4 p = mine ? *reinterpret_cast<const float4*>(a.part + (x * step + at) * a.hd +
-                                                                 lane * 4)
-                              : make_float4(0, 0, 0, 0);
+        const float2 ml = a.part_ml[index(x)];
+        const float4 p =
+            mine ? *reinterpret_cast<const float4*>(a.part + index(x) * a.hd + lane * 4)
+                 : make_float4(0, 0, 0, 0);
         const float f = exp2f(ml.x - base);
         l += f * ml.y;
         v.x += f * p.x;
@@ -439,34 +448,33 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
                        bf16x2(v.z * end.factor, v.w * end.factor));
 }
 
-// How the keys of a call are split.  Up to 16 rows per key/value head: chunks
-// long enough that the CTAs of all sequences and heads, at the longest length,
-// make about two waves of three CTAs an SM, a multiple of 64 keys (a group for
-// every warp).  More rows: the tensor-core kernel, one CTA an SM, about three
-// waves, at least 512 keys (its start and end cost some blocks' time).
+// The shape of a call's work: which kernel, its tiles and blocks, its workers.
+// Up to 16 rows per key/value head the few-row kernel, three CTAs an SM (two on a
+// bf16 cache, whose stages are twice as large); above, the tensor-core kernel,
+// one CTA an SM.  Never more workers than blocks at the longest lengths.
 struct Plan {
-    bool many, pair;
-    int chunk, align, splits, per, row_tiles;
+    bool many;
+    int block, align, tile_rows, row_tiles, workers;
+    size_t part_bytes, ml_bytes, ends_bytes;
+    size_t bytes() const { return part_bytes + ml_bytes + ends_bytes; }
 };
-Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t window,
-               int sms) {
+Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t hd,
+               int64_t window, int fmt, int sms) {
     Plan p;
     const int64_t rows = max_q * (nh / kvh);
     p.many = rows > 16;
-    p.pair = rows > 128;
+    p.block = p.many ? 128 : BLOCK;
     p.align = p.many ? 128 : GROUP;
-    p.per = p.many && !p.pair ? 2 : 1;
+    p.tile_rows = !p.many ? 16 : rows > 128 ? 256 : 128;
+    p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     int64_t len = max_len;
     if (window && window + max_q + p.align < len) len = window + max_q + p.align;
-    if (len < 1) len = 1;
-    p.row_tiles = p.many ? (int)((rows + 255) / 256) : 1;
-    const int64_t units = B * kvh * p.row_tiles, want = (p.many ? 3 : 6) * (int64_t)sms;
-    const int64_t unit = p.many ? 256 : 64, least = p.many ? 512 : 64;
-    int64_t chunk = (len * units + want - 1) / want;
-    chunk = (chunk + unit - 1) / unit * unit;
-    if (chunk < least) chunk = least;
-    p.chunk = (int)chunk;
-    p.splits = (int)((len + chunk - 1) / chunk);
+    const int64_t most = B * kvh * p.row_tiles * ((len + p.block - 1) / p.block);
+    const int64_t want = (int64_t)sms * (p.many ? 1 : fmt == DS41_KV_E4M3 ? 3 : 2);
+    p.workers = (int)(most < 1 ? 1 : most < want ? most : want);
+    p.part_bytes = (size_t)p.workers * 2 * p.tile_rows * hd * 4;
+    p.ml_bytes = (size_t)p.workers * 2 * p.tile_rows * 8;
+    p.ends_bytes = (size_t)B * kvh * p.row_tiles * 8;
     return p;
 }
 
@@ -478,13 +486,10 @@ using namespace ds41;
 extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q,
                                                  int64_t max_len, int64_t nh, int64_t kvh,
                                                  int64_t hd, int64_t window, int fmt) {
-    (void)fmt;
     if (B < 1 || Tq < 1 || max_q < 1 || max_q > 256 || max_len < 0 || kvh < 1 || nh < kvh ||
         nh % kvh || hd < 1 || window < 0)
         return 0;
-    const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, window, device_sm_count());
-    const int64_t parts = (int64_t)pl.splits * pl.per;
-    return parts == 1 ? 0 : (size_t)parts * Tq * nh * (hd * 4 + 8);
+    return tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, device_sm_count()).bytes();
 }
 
 extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
@@ -521,11 +526,10 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
                  DS41_E_ARG, "%s: q and o must be 16-byte aligned", name);
     DS41_REQUIRE(good_strides(q_tok, q_head, hd), DS41_E_ARG,
                  "%s: strides must be multiples of 8 and at least hd", name);
-    const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, window, device_sm_count());
-    const size_t need =
-        ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, window, fmt);
-    DS41_REQUIRE(need == 0 || (ws && aligned16(ws) && ws_bytes >= need), DS41_E_WORKSPACE,
-                 "%s: needs %zu bytes of workspace, got %zu", name, need, ws ? ws_bytes : 0);
+    const tree::Plan pl =
+        tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, device_sm_count());
+    DS41_REQUIRE(ws && aligned16(ws) && ws_bytes >= pl.bytes(), DS41_E_WORKSPACE,
+                 "%s: needs %zu bytes of workspace, got %zu", name, pl.bytes(), ws ? ws_bytes : 0);
     a.q = q;
     a.q_tok = q_tok;
     a.q_head = q_head;
@@ -547,18 +551,19 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
     a.sink = sink;
     a.o = o;
     a.lse = lse;
-    a.chunk = pl.chunk;
+    a.B = (int)B;
+    a.block = pl.block;
     a.align = pl.align;
-    a.per = pl.per;
-    a.parts = pl.splits * pl.per;
+    a.tile_rows = pl.tile_rows;
+    a.row_tiles = pl.row_tiles;
+    a.workers = pl.workers;
     a.part = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part + (int64_t)a.parts * Tq * nh * hd);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + pl.part_bytes);
+    a.ends = reinterpret_cast<int2*>(static_cast<uint8_t*>(ws) + pl.part_bytes + pl.ml_bytes);
     if (int rc = status_word(&a.status)) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    DS41_REQUIRE(kvh * pl.row_tiles < 65536, DS41_E_RANGE, "%s: kvh=%lld max_q=%lld nh=%lld", name,
-                 (long long)kvh, (long long)max_q, (long long)nh);
     if (pl.many) {
-        if (int rc = tree::launch_many(a, pl.pair, pl.row_tiles, B, name, st)) return rc;
+        if (int rc = tree::launch_many(a, name, st)) return rc;
     } else {
         using namespace tree;
         const bool e = fmt == DS41_KV_E4M3;
@@ -570,11 +575,10 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
                 cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                 name))
             return rc;
-        if (int rc = launch_pdl(kern, dim3((unsigned)pl.splits, (unsigned)kvh, (unsigned)B),
-                                dim3(NT), smem, st, name, a))
+        if (int rc = launch_pdl(kern, dim3((unsigned)pl.workers), dim3(NT), smem, st, name, a))
             return rc;
     }
-    if (a.parts == 1) return DS41_OK;
+    if (pl.workers == 1) return DS41_OK;  // every unit was whole
     return launch_pdl(tree::tree_join_kernel, dim3((unsigned)(max_q * nh), (unsigned)B),
                       dim3(tree::NT), 0, st, name, a);
 }

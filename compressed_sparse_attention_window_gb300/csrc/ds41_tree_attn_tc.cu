@@ -6,30 +6,28 @@
 // row: a drafted token and one of the G query heads that share the key/value
 // head).
 //
-// Design.  A CTA runs two streams t = 0, 1, each with its own scores S_t and
-// output O_t in tensor memory and its own softmax warpgroup (a thread per row),
-// so that the tensor core works on one while the other's softmax runs; the issue
-// order is PV_0 QK_0 PV_1 QK_1 as in the prompt kernel.  What the streams are
-// depends on the rows:
-// * more than 128 rows: two tiles of 128 rows over the same key blocks (each
+// Design.  One CTA per SM works through its run of the key blocks of all
+// sequences (Share in ds41_tree.cuh).  It has two streams t = 0, 1, each with its
+// own scores S_t and output O_t in tensor memory and its own softmax warpgroup (a
+// thread per row), so that the tensor core works on one while the other's
+// softmax runs; the issue order is PV_0 QK_0 PV_1 QK_1 as in the prompt kernel.
+// What the streams are depends on the rows:
+// * PAIR, more than 128 rows: two tiles of 128 rows over the same key blocks (each
 //   block is loaded and widened once for 256 rows);
-// * up to 128 rows: one tile of rows, the even key blocks to stream 0 and the
-//   odd ones to stream 1, joined at the end like two splits.
-// The keys are split over CTAs (chunks), partial results joined by the second
-// kernel of the few-row path.
+// * else: one tile of rows, the even key blocks to stream 0 and the odd ones to
+//   stream 1, joined through shared memory at the end.
 //
 // A bf16 cache arrives by TMA, page by page, in the layout the products want.  An
-// e4m3 cache has to be widened (the products take one operand type): four warps
-// fetch the codes with cp.async, every thread its own pieces, some tiles ahead,
-// so no barrier stands between a piece's arrival and its use, turn them into f16
-// (exact, two codes an instruction; bf16 takes four) and store them swizzled.
-// The threads' pieces are dealt so that eight lanes store into eight different
-// bank groups (rows r and r + 1 side by side, their halves crossed) and the code
-// buffer is private to each thread, so neither side has bank conflicts.  The
-// queries become f16 with an exponent per row, the scales stay outside the
-// products: ks multiplies the scores, vs the weights.
+// e4m3 cache has to be widened (the products take one operand type): its codes
+// arrive as bulk copies, one for each run of rows of a page, and four warps turn
+// them into f16 (exact, two codes an instruction; bf16 takes four) and store them
+// swizzled.  The threads' 16-code pieces are dealt so that neither side has bank
+// conflicts: eight lanes take four pieces of a row and the other four of the next
+// row, which are 128 contiguous bytes of codes modulo 128 and eight different
+// bank groups of the swizzled tile.  The queries become f16 with an exponent per
+// row, the scales stay outside the products: ks multiplies the scores, vs the
+// weights.
 #include "ds41_internal.cuh"
-#include "ds41_softmax_tc.cuh"
 #include "ds41_tree.cuh"
 
 namespace ds41 {
@@ -40,13 +38,13 @@ using namespace tc;
 constexpr int KB = 128;  // keys per block
 constexpr int SCN = 4;   // blocks whose scales and visibility are held
 
-// warps 0 TMA, 1 MMA, 2 tail, 4..7 and 8..11 softmax, 12..15 widening (e4m3)
+// warps 0 copies, 1 MMA, 2 tail, 4..7 and 8..11 softmax, 12..15 widening (e4m3)
 template <int D, bool E4M3, bool PAIR>
 struct TcCfg {
     static constexpr int THREADS = E4M3 ? 512 : 384;
     static constexpr int NB = D / 64;
     static constexpr uint32_t BLK = 128 * 128;
-    static constexpr uint32_t TILE = NB * BLK;               // a K or V block in bf16
+    static constexpr uint32_t TILE = NB * BLK;               // a K or V block, 16 bits a value
     static constexpr int QT = PAIR ? 2 : 1;                  // tiles of rows
     static constexpr int STAGES = E4M3 ? 3 : 4;
     static constexpr int CODES = PAIR ? 3 : 5;               // tiles of codes in flight
@@ -55,14 +53,16 @@ struct TcCfg {
     static constexpr uint32_t KV_OFF = QT * TILE;
     static constexpr uint32_t C_OFF = KV_OFF + STAGES * TILE;
     static constexpr uint32_t SC_OFF = C_OFF + CODES * CTILE;
-    // per held block: 4 words of real keys, and for e4m3 the largest vs of each
-    // 32 keys, ks [128], vs [128]
-    static constexpr uint32_t SC_BYTES = (E4M3 ? 1024 + 16 : 0) + 16;
+    // per held block: 4 words of real keys and for e4m3 ks [128], vs [128]
+    static constexpr uint32_t SC_BYTES = (E4M3 ? 1024 : 0) + 16;
     static constexpr uint32_t QE_OFF = SC_OFF + SCN * SC_BYTES;  // the queries' exponents
     static constexpr uint32_t BAR_OFF = QE_OFF + (E4M3 ? QT * 128 : 0);
-    static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
+    static constexpr uint32_t SMEM = BAR_OFF + 640 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr int LA = PAIR ? 1 : 2;  // K blocks ahead of the V blocks
+    // the other stream's rows at the end of a piece (no tile is in use then)
+    static constexpr int XP = D + 4;
+    static_assert(PAIR || 128 * XP * 4 <= STAGES * TILE, "exchange area");
 };
 
 // The ring holds K and V blocks in the order in which they are used: the first
@@ -74,6 +74,19 @@ __device__ __forceinline__ int pos_k(int j) {
 template <int LA>
 __device__ __forceinline__ int pos_v(int j, int n) {
     return min(LA, n) + j + min(j, max(0, n - LA));
+}
+// entry e of the ring of n blocks: block j, K (0) or V (1)
+template <int LA>
+__device__ __forceinline__ void entry_of(int e, int n, int& j, int& kv) {
+    const int lead = min(LA, n);
+    if (e < lead) {
+        j = e;
+        kv = 0;
+    } else {
+        const int x = e - lead, both = 2 * max(0, n - LA);
+        kv = x < both ? (x & 1) ^ 1 : 1;
+        j = x < both ? (kv ? x / 2 : x / 2 + LA) : x - both / 2;
+    }
 }
 
 // Which of the keys j .. j + 31 a row sees.
@@ -105,6 +118,39 @@ __device__ __forceinline__ uint32_t seen_word(const RowView& w, int n_drafted, i
     return r;
 }
 
+// A role's walk through its CTA's pieces, and what the barriers have seen before
+// the present one: entries of the ring, blocks, blocks and ends of each stream,
+// V blocks with rows behind the last key.
+template <int D, bool E4M3, bool PAIR>
+struct Walk {
+    Share share;
+    Piece pc;
+    int k0, k1, n_blocks, tail;  // the piece's keys; those of its last block
+    int nt[2];                   // blocks of each stream
+    int ring0 = 0, blocks0 = 0, used0[2] = {0, 0}, ends0[2] = {0, 0}, tails0 = 0;
+    __device__ __forceinline__ bool next(const Args& a) {
+        if (!next_piece(a, share, pc)) return false;
+        const int rows = pc.s.n * a.G, r0 = pc.tile * TcCfg<D, E4M3, PAIR>::QT * 128;
+        k0 = first_key(a, pc.s) + pc.first * KB;
+        k1 = min(pc.s.len, k0 + pc.count * KB);
+        n_blocks = pc.count;
+        tail = (k1 - k0) - (n_blocks - 1) * KB;
+        nt[0] = PAIR ? n_blocks : (n_blocks + 1) / 2;
+        nt[1] = PAIR ? (rows - r0 > 128 ? n_blocks : 0) : n_blocks / 2;
+        return true;
+    }
+    __device__ __forceinline__ void done() {
+        ring0 += 2 * n_blocks;
+        blocks0 += n_blocks;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            used0[t] += nt[t];
+            ends0[t] += nt[t] > 0;
+        }
+        tails0 += tail < KB;
+    }
+};
+
 template <int D, bool E4M3, bool PAIR>
 __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     tree_many_kernel(const __grid_constant__ CUtensorMap map_k,
@@ -118,7 +164,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
     uint64_t* b_full = bars;                  // a K or V block is in its stage
     uint64_t* b_empty = b_full + C::STAGES;   // it has been used
-    uint64_t* b_sc = b_empty + C::STAGES;     // a block's scales and real keys are there
+    uint64_t* b_code = b_empty + C::STAGES;   // a tile of codes has arrived
+    uint64_t* b_codee = b_code + C::CODES;    // it has been read
+    uint64_t* b_sc = b_codee + C::CODES;      // a block's scales and real keys are there
     uint64_t* b_sce = b_sc + SCN;             // they have been read
     uint64_t* b_s = b_sce + SCN;              // S_t in tensor memory [2]
     uint64_t* b_p = b_s + 2;                  // P_t in tensor memory, O_t rescaled [2]
@@ -127,30 +175,23 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     uint64_t* b_fix = b_tail + 1;             // its rows behind the last key are zero
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_fix + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * C::STAGES + 2 * SCN + 8) * 8 + 8 <= 512, "barrier area");
+    int64_t* sh = reinterpret_cast<int64_t*>(tmem_slot + 2);
+    static_assert((2 * C::STAGES + 2 * C::CODES + 2 * SCN + 8) * 8 + 8 +
+                          (2 * C::THREADS / 32 + 4) * 8 <= 640,
+                  "barrier area");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x, h = blockIdx.y % a.kvh, rt = blockIdx.y / a.kvh, b = blockIdx.z;
-    const Seq s = load_seq(a, b);
-    if (!s.ok) {
-        if (threadIdx.x == 0) raise_status(a.status, DS41_E_INDEX);
-        return;
-    }
-    const int rows = s.n * a.G, r0 = rt * C::QT * 128;
-    if (r0 >= rows) return;
-    const int k0 = first_key(a, s) + split * a.chunk, k1 = min(s.len, k0 + a.chunk);
-    if (k0 >= k1) return;
-    const int n_blocks = (k1 - k0 + KB - 1) / KB;
-    const int tail = (k1 - k0) - (n_blocks - 1) * KB;  // keys of the last block
-    const int32_t* table = a.table + (int64_t)b * a.max_pages;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; i++) {
             mbar_init(&b_full[i], E4M3 ? 4 : 1);
             mbar_init(&b_empty[i], 1);
         }
+        for (int i = 0; i < C::CODES; i++) {
+            mbar_init(&b_code[i], 1);
+            mbar_init(&b_codee[i], 4);
+        }
         for (int i = 0; i < SCN; i++) {
-            mbar_init(&b_sc[i], E4M3 ? 4 : 1);
-            mbar_init(&b_sce[i], PAIR && rows - r0 > 128 ? 8 : 4);
+            mbar_init(&b_sc[i], 1);
+            mbar_init(&b_sce[i], PAIR ? 8 : 4);
         }
         for (int t = 0; t < 2; t++) {
             mbar_init(&b_s[t], 1);
@@ -169,422 +210,481 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     }
-    // the queries, 128-byte swizzled; rows that do not exist are zero
-    for (int x = threadIdx.x; x < C::QT * 128 * (D / 8); x += C::THREADS) {
-        const int r = x / (D / 8), ch = x % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r0 + r < rows && ch * 8 < a.hd) {
-            const int t = (r0 + r) / a.G;
-            v = *reinterpret_cast<const uint4*>(
-                a.q + (s.q0 + t) * a.q_tok + (h * a.G + (r0 + r) % a.G) * a.q_head + ch * 8);
-        }
-        if (E4M3) {  // D / 8 lanes have a row
-            const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-            uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
-#pragma unroll
-            for (int off = D / 16; off > 0; off >>= 1)
-                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
-            const int e = query_exponent(mb);
-            const float down = exp2f((float)-e);
-            v = make_uint4(bf16x2_to_f16x2(v.x, down), bf16x2_to_f16x2(v.y, down),
-                           bf16x2_to_f16x2(v.z, down), bf16x2_to_f16x2(v.w, down));
-            if (ch == 0) reinterpret_cast<int8_t*>(sm + C::QE_OFF)[r] = (int8_t)e;
-        }
-        *reinterpret_cast<uint4*>(sm + C::Q_OFF + (r >> 7) * C::TILE + (ch >> 3) * C::BLK +
-                                  (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-    }
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     tc_fence_before();
-    __syncthreads();
+    Share share = find_share<C::THREADS>(a, sh, blockIdx.x == 0);  // (synchronises)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     constexpr uint32_t TM_S = 0, TM_O = 256;
-    // stream t uses block j
-    const int nt[2] = {PAIR ? n_blocks : (n_blocks + 1) / 2,
-                       PAIR ? (rows - r0 > 128 ? n_blocks : 0) : n_blocks / 2};
-    auto uses = [&](int t, int j) { return PAIR ? nt[t] > 0 : (j & 1) == t; };
-    auto block_of = [&](int t, int i) { return PAIR ? i : 2 * i + t; };
-    const int n_ring = 2 * n_blocks;
+    // Every role walks the same pieces; all of them meet where a piece begins (its
+    // queries are in shared memory), for one tile of rows again where its streams
+    // end, and where it ends.  The roles' code is kept apart so that each has its
+    // own share of the register file (128 a thread at launch, 168 on bf16).
+    Walk<D, E4M3, PAIR> w;
+    w.share = share;
+    bool ok = true;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 72 : 88));
-        if (warp == 0 && !E4M3) {
-            // pages -> stages, and which keys are real
-            bool ok = true;
-            uint32_t armed[C::STAGES] = {};
-            for (int e = 0; e < n_ring && ok; e++) {
-                // ring entry e: K block or V block
-                int j, kv;
-                const int lead = min(C::LA, n_blocks);
-                if (e < lead) {
-                    j = e;
-                    kv = 0;
-                } else {
-                    const int x = e - lead, both = 2 * max(0, n_blocks - C::LA);
-                    kv = x < both ? (x & 1) ^ 1 : 1;
-                    j = x < both ? (kv ? x / 2 : x / 2 + C::LA) : x - both / 2;
-                }
-                const int st = e % C::STAGES, use = e / C::STAGES;
-                if (use > 0) ok = warp_wait(&b_empty[st], (use - 1) & 1, abort_f, a.status);
-                if (!ok) break;
-                const int key0 = k0 + j * KB;
-                // lane i: the page of the 16 keys from key0 + 16 i on
-                int64_t pg = -1;
-                const int key = key0 + 16 * (lane & 7);
-                if (key < k1) {
-                    pg = table[key >> a.kv.page_shift];
-                    if (pg < 0 || pg >= a.kv.n_pages) {
-                        pg = -1;
-                        if (kv == 0) raise_status(a.status, DS41_E_INDEX);
-                    }
-                }
-                if (kv == 0) {
-                    const int sl = j % SCN;
-                    if (j >= SCN) ok = warp_wait(&b_sce[sl], ((j / SCN) - 1) & 1, abort_f, a.status);
+        while (w.next(a)) {
+            const int32_t* table = a.table + (int64_t)w.pc.b * a.max_pages;
+            const Piece& pc = w.pc;
+            const int k0 = w.k0, k1 = w.k1, n_blocks = w.n_blocks, n_ring = 2 * n_blocks;
+            const int ring0 = w.ring0, blocks0 = w.blocks0, tail = w.tail, tails0 = w.tails0;
+            const int(&nt)[2] = w.nt;
+            const int(&used0)[2] = w.used0;
+            auto uses = [&](int t, int j) { return PAIR ? nt[t] > 0 : (j & 1) == t; };
+            if (threadIdx.x == 0) note_ends(a, pc);
+            __syncthreads();
+            if (warp == 0 && ok) {
+                // pages -> stages (bf16) or code tiles (e4m3), and which keys are real
+                const int per = min(a.kv.page, KB), copies = KB / per;  // rows of a copy
+                int armed = 0;
+                for (int e = 0; e < n_ring && ok; e++, armed = e) {
+                    int j, kv;
+                    entry_of<C::LA>(e, n_ring / 2, j, kv);
+                    const int ge = ring0 + e;
+                    const int st = ge % (E4M3 ? C::CODES : C::STAGES);
+                    const int use = ge / (E4M3 ? C::CODES : C::STAGES);
+                    uint64_t* full = E4M3 ? &b_code[st] : &b_full[st];
+                    if (use > 0)
+                        ok = warp_wait(E4M3 ? &b_codee[st] : &b_empty[st], (use - 1) & 1, abort_f,
+                                       a.status);
+                    const int gb = blocks0 + j, sl = gb % SCN;
+                    if (ok && kv == 0 && gb >= SCN)
+                        ok = warp_wait(&b_sce[sl], ((gb / SCN) - 1) & 1, abort_f, a.status);
                     if (!ok) break;
-                    const uint32_t good = __ballot_sync(0xffffffffu, pg >= 0) & 0xffu;
-                    if (lane < 4) {
-                        uint32_t w = ((good >> (2 * lane)) & 1 ? 0xffffu : 0u) |
-                                     ((good >> (2 * lane + 1)) & 1 ? 0xffff0000u : 0u);
-                        w &= low_bits((int64_t)k1 - key0 - 32 * lane);
-                        reinterpret_cast<uint32_t*>(sm + C::SC_OFF + sl * C::SC_BYTES)[lane] = w;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_sc[sl]);
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&b_full[st], C::TILE);
-                armed[st]++;
-                __syncwarp();
-                // a copy takes min(page, 128) rows of one page; a page that does
-                // not exist reads as zeros (a coordinate past the tensor)
-                const int per = min(a.kv.page, KB), copies = KB / per;
-                const int src = lane < copies ? lane * per / 16 : 0;
-                const int64_t cp = __shfl_sync(0xffffffffu, pg, src);
-                if (lane < copies) {
-                    const int64_t z = cp >= 0 ? cp * a.kvh + h : a.kv.n_pages * a.kvh;
-                    const int off = (key0 + lane * per) & (a.kv.page - 1);
-                    for (int x = 0; x < C::NB; x++)
-                        tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
-                                        lane * per * 128,
-                                    kv ? &map_v : &map_k, 64 * x, off, (int)z, &b_full[st]);
-                }
-            }
-            for (int st = 0; st < C::STAGES; st++)
-                if (armed[st]) drain_bar(&b_full[st], (armed[st] - 1) & 1, a.status);
-        } else if (warp == 1) {
-            constexpr uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
-            constexpr uint32_t IDESC_O = E4M3 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
-            const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
-            const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
-            const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
-            int done_p[2] = {0, 0};
-            auto wait_entry = [&](int e) {
-                const bool ok =
-                    warp_wait(&b_full[e % C::STAGES], (e / C::STAGES) & 1, abort_f, a.status);
-                tc_fence_after();
-                return ok;
-            };
-            auto stage_off = [&](int e) { return ((e % C::STAGES) * C::TILE) >> 4; };
-            auto scores = [&](int t, int e) {
-                mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
-                                       qd + ((PAIR ? t * C::TILE : 0) >> 4), kd + stage_off(e));
-                tc_commit(&b_s[t]);
-            };
-            bool ok = true;
-            for (int j = 0; j < min(C::LA, n_blocks) && ok; j++) {
-                ok = wait_entry(j);
-                if (ok && elect_one()) {
-#pragma unroll
-                    for (int t = 0; t < 2; t++)
-                        if (uses(t, j)) scores(t, j);
-                    tc_commit(&b_empty[j % C::STAGES]);
-                }
-                __syncwarp();
-            }
-            for (int j = 0; j < n_blocks && ok; j++) {
-                const int ev = pos_v<C::LA>(j, n_blocks);
-                const bool more = j + C::LA < n_blocks;
-                const int ek = pos_k<C::LA>(j + C::LA);
-                ok = wait_entry(ev);
-                if (ok && !E4M3 && tail < KB && j == n_blocks - 1) {
-                    if (lane == 0) mbar_arrive(b_tail);
-                    ok = warp_wait(b_fix, 0, abort_f, a.status);
-                    tc_fence_after();
-                }
-                bool have_k = false;
-#pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    const bool now = uses(t, j), next = more && uses(t, j + C::LA);
-                    if (ok && now) {
-                        ok = warp_wait(&b_p[t], done_p[t] & 1, abort_f, a.status);
-                        done_p[t]++;
-                        tc_fence_after();
-                    }
-                    if (ok && elect_one()) {
-                        if (now) {
-                            mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
-                                                   vd + stage_off(ev), done_p[t] > 1);
-                            if (done_p[t] == nt[t]) tc_commit(&b_o[t]);
+                    const int key0 = k0 + j * KB;
+                    // lane i < copies: its page and the rows it copies
+                    const int key = key0 + lane * per;
+                    int64_t pg = -1;
+                    int n = 0;
+                    if (lane < copies && key < k1) {
+                        n = min(per, k1 - key);
+                        pg = table[key >> a.kv.page_shift];
+                        if (pg < 0 || pg >= a.kv.n_pages) {
+                            pg = -1;
+                            if (kv == 0) raise_status(a.status, DS41_E_INDEX);
                         }
-                        if (t == 1) tc_commit(&b_empty[ev % C::STAGES]);
                     }
-                    __syncwarp();
-                    if (ok && next) {
-                        if (!have_k) ok = wait_entry(ek);
-                        have_k = true;
-                        if (ok && elect_one()) scores(t, ek);
+                    uint8_t* sc = sm + C::SC_OFF + sl * C::SC_BYTES;
+                    if (kv == 0) {
+                        // word i: which of the keys 32 i .. are real
+                        const uint32_t good = __ballot_sync(0xffffffffu, pg >= 0);
+                        if (lane < 4) {
+                            uint32_t w = 0;
+                            for (int x = 0; x < 32; x += 16)
+                                if ((good >> ((32 * lane + x) / per)) & 1) w |= 0xffffu << x;
+                            w &= low_bits((int64_t)k1 - key0 - 32 * lane);
+                            reinterpret_cast<uint32_t*>(sc)[lane] = w;
+                        }
                         __syncwarp();
                     }
+                    const int off = key & (a.kv.page - 1);
+                    if (E4M3) {
+                        const uint32_t bytes = pg >= 0 ? (uint32_t)(n * a.hd) : 0u;
+                        const uint32_t sbytes = pg >= 0 ? (uint32_t)((n + 3) / 4 * 16) : 0u;
+                        const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+                        const uint32_t alls = 2 * __reduce_add_sync(0xffffffffu, sbytes);
+                        uint8_t* dst = sm + C::C_OFF + st * C::CTILE;
+                        // rows that no copy fills are zero, so that no product meets a NaN
+                        for (int i = 0; i < copies; i++) {
+                            const int have = __shfl_sync(0xffffffffu, pg >= 0 ? n : 0, i);
+                            for (int x = lane; x < (per - have) * a.hd / 16; x += 32)
+                                *reinterpret_cast<uint4*>(dst + (i * per + have) * a.hd + x * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, all);
+                            if (kv == 0) mbar_arrive_expect_tx(&b_sc[sl], alls);
+                        }
+                        __syncwarp();
+                        if (pg >= 0) {
+                            const int64_t row = paged_row(a.kv, pg, pc.h, off);
+                            bulk_g2s(dst + lane * per * a.hd, (kv ? a.kv.v : a.kv.k) + row * a.hd,
+                                     bytes, full);
+                            if (kv == 0) {
+                                bulk_g2s(sc + 16 + lane * per * 4, a.kv.ks + row, sbytes, &b_sc[sl]);
+                                bulk_g2s(sc + 528 + lane * per * 4, a.kv.vs + row, sbytes, &b_sc[sl]);
+                            }
+                        }
+                    } else {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, C::TILE);
+                            if (kv == 0) mbar_arrive(&b_sc[sl]);
+                        }
+                        __syncwarp();
+                        if (lane < copies) {
+                            // a page that does not exist reads as zeros (a coordinate
+                            // past the tensor)
+                            const int64_t z = pg >= 0 ? pg * a.kvh + pc.h : a.kv.n_pages * a.kvh;
+                            for (int x = 0; x < C::NB; x++)
+                                tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
+                                                lane * per * 128,
+                                            kv ? &map_v : &map_k, 64 * x, off, (int)z, full);
+                        }
+                    }
                 }
-                if (ok && more && elect_one()) tc_commit(&b_empty[ek % C::STAGES]);
-                __syncwarp();
-            }
-        } else if (warp == 2 && !E4M3 && tail < KB) {
-            // the V rows behind the last key hold whatever an earlier user left
-            const int ev = pos_v<C::LA>(n_blocks - 1, n_blocks);
-            if (warp_wait(b_tail, 0, abort_f, a.status)) {
-                uint8_t* v = sm + C::KV_OFF + (ev % C::STAGES) * C::TILE;
-                for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
-                    const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
-                    *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
-                                              (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                // everything that was started lands before the piece ends
+                const int depth = E4M3 ? C::CODES : C::STAGES;
+                for (int e = max(0, armed - depth); e < armed; e++) {
+                    const int ge = ring0 + e;
+                    drain_bar(E4M3 ? &b_code[ge % depth] : &b_full[ge % depth], (ge / depth) & 1,
+                              a.status);
                 }
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_fix);
+            } else if (warp == 1 && ok) {
+                constexpr uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
+                constexpr uint32_t IDESC_O = E4M3 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
+                const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
+                const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
+                const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
+                int done_p[2] = {0, 0};
+                auto wait_entry = [&](int e) {
+                    const int ge = ring0 + e;
+                    const bool r =
+                        warp_wait(&b_full[ge % C::STAGES], (ge / C::STAGES) & 1, abort_f, a.status);
+                    tc_fence_after();
+                    return r;
+                };
+                auto stage_of = [&](int e) { return (ring0 + e) % C::STAGES; };
+                auto stage_off = [&](int e) { return (stage_of(e) * C::TILE) >> 4; };
+                auto scores = [&](int t, int e) {
+                    mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                           qd + ((PAIR ? t * C::TILE : 0) >> 4), kd + stage_off(e));
+                    tc_commit(&b_s[t]);
+                };
+                for (int j = 0; j < min(C::LA, n_blocks) && ok; j++) {
+                    ok = wait_entry(j);
+                    if (ok && elect_one()) {
+    #pragma unroll
+                        for (int t = 0; t < 2; t++)
+                            if (uses(t, j)) scores(t, j);
+                        tc_commit(&b_empty[stage_of(j)]);
+                    }
+                    __syncwarp();
+                }
+                for (int j = 0; j < n_blocks && ok; j++) {
+                    const int ev = pos_v<C::LA>(j, n_blocks);
+                    const bool more = j + C::LA < n_blocks;
+                    const int ek = pos_k<C::LA>(j + C::LA);
+                    ok = wait_entry(ev);
+                    if (ok && !E4M3 && tail < KB && j == n_blocks - 1) {
+                        if (lane == 0) mbar_arrive(b_tail);
+                        ok = warp_wait(b_fix, tails0 & 1, abort_f, a.status);
+                        tc_fence_after();
+                    }
+                    bool have_k = false;
+    #pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const bool now = uses(t, j), next = more && uses(t, j + C::LA);
+                        if (ok && now) {
+                            ok = warp_wait(&b_p[t], (used0[t] + done_p[t]) & 1, abort_f, a.status);
+                            done_p[t]++;
+                            tc_fence_after();
+                        }
+                        if (ok && elect_one()) {
+                            if (now) {
+                                mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
+                                                       vd + stage_off(ev), done_p[t] > 1);
+                                if (done_p[t] == nt[t]) tc_commit(&b_o[t]);
+                            }
+                            if (t == 1) tc_commit(&b_empty[stage_of(ev)]);
+                        }
+                        __syncwarp();
+                        if (ok && next) {
+                            if (!have_k) ok = wait_entry(ek);
+                            have_k = true;
+                            if (ok && elect_one()) scores(t, ek);
+                            __syncwarp();
+                        }
+                    }
+                    if (ok && more && elect_one()) tc_commit(&b_empty[stage_of(ek)]);
+                    __syncwarp();
+                }
+            } else if (warp == 2 && !E4M3 && tail < KB && ok) {
+                // the V rows behind the last key hold whatever an earlier user left
+                const int ge = ring0 + pos_v<C::LA>(n_blocks - 1, n_blocks);
+                ok = warp_wait(b_tail, tails0 & 1, abort_f, a.status);
+                if (ok) {
+                    uint8_t* v = sm + C::KV_OFF + (ge % C::STAGES) * C::TILE;
+                    for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
+                        const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
+                        *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
+                                                  (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_fix);
+                }
             }
+            if (!PAIR) __syncthreads();
+            w.done();
+            __syncthreads();
+            if (*abort_f) ok = false;
         }
     } else if (E4M3 && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
         const int tid = threadIdx.x - 384;
         constexpr int PIECES = KB * D / 16 / 128;  // 16-code pieces a thread has of a tile
-        // piece x of this thread: row and which of the row's pieces.  Eight lanes
-        // take four pieces of a row and the other four of the next.
-        auto piece = [&](int x, int& r, int& ch) {
-            if (D == 128) {
-                const int p = x * 16 + (tid >> 3);  // 0 .. 127: pair of rows, and which half
-                const int odd = (tid >> 2) & 1;
-                r = (p >> 1) * 2 + odd;
-                ch = (tid & 3) + 4 * (odd ^ (p & 1));
-            } else {
-                r = x * 32 + (tid >> 2);
-                ch = tid & 3;
-            }
-        };
-        // entry e of the ring -> block j, K or V
-        auto entry = [&](int e, int& j, int& kv) {
-            const int lead = min(C::LA, n_blocks);
-            if (e < lead) {
-                j = e;
-                kv = 0;
-            } else {
-                const int x = e - lead, both = 2 * max(0, n_blocks - C::LA);
-                kv = x < both ? (x & 1) ^ 1 : 1;
-                j = x < both ? (kv ? x / 2 : x / 2 + C::LA) : x - both / 2;
-            }
-        };
-        // lane i < 8: the page of the 16 keys from key 16 i of entry e's block on
-        auto pages = [&](int e) {
-            int j, kv, pg = -1;
-            entry(e, j, kv);
-            const int key = k0 + j * KB + 16 * (lane & 7);
-            if (e < n_ring && key < k1) pg = table[key >> a.kv.page_shift];
-            return pg;
-        };
-        // what of an address does not change: the place in a group of 16 (32) keys
-        int r_in, ch_in;
-        piece(0, r_in, ch_in);
-        const int in_group = r_in * a.hd + ch_in * 16;
-        const bool in_row = ch_in * 16 < a.hd;
-        const int64_t page_bytes = (int64_t)a.kv.page * a.hd, pages_bytes = page_bytes * a.kvh;
-        constexpr int RPP = 128 / PIECES;  // rows from a piece to the next
-        auto fetch = [&](int e, int pgs) {
-            if (e < n_ring) {
-                int j, kv;
-                entry(e, j, kv);
-                const uint32_t dst = sbase + C::C_OFF + (e % C::CODES) * C::CTILE + tid * 16;
-                const uint8_t* src = (kv ? a.kv.v : a.kv.k) + h * page_bytes;
-                const int key0 = k0 + j * KB;
+        constexpr int RPP = 128 / PIECES;          // rows from a piece to the next
+        int r_in, ch;
+        if (D == 128) {
+            const int p = tid >> 3, odd = (tid >> 2) & 1;  // pair of rows and half
+            r_in = (p >> 1) * 2 + odd;
+            ch = (tid & 3) + 4 * (odd ^ (p & 1));
+        } else {
+            r_in = tid >> 2;
+            ch = tid & 3;
+        }
+        const bool in_row = ch * 16 < a.hd;
+        const uint32_t src_off = (uint32_t)(r_in * a.hd + ch * 16);
+        const int c0 = (ch & 3) * 2;
+        // (RPP is a multiple of 8, so r & 7 is that of r_in)
+        const uint32_t dst0 =
+            (ch >> 2) * C::BLK + r_in * 128 + (uint32_t)((c0 ^ (r_in & 7)) << 4);
+        const uint32_t dst1 =
+            (ch >> 2) * C::BLK + r_in * 128 + (uint32_t)(((c0 + 1) ^ (r_in & 7)) << 4);
+        while (w.next(a)) {
+            const int n_ring = 2 * w.n_blocks, ring0 = w.ring0;
+            __syncthreads();
+            for (int e = 0; e < n_ring && ok; e++) {
+                const int ge = ring0 + e, cs = ge % C::CODES, st = ge % C::STAGES;
+                ok = warp_wait(&b_code[cs], (ge / C::CODES) & 1, abort_f, a.status);
+                if (!ok) break;
+                uint4 w[PIECES];
+                const uint8_t* from = sm + C::C_OFF + cs * C::CTILE + src_off;
+#pragma unroll
+                for (int x = 0; x < PIECES; x++)
+                    w[x] = in_row ? *reinterpret_cast<const uint4*>(from + x * RPP * a.hd)
+                                  : make_uint4(0, 0, 0, 0);
+                __syncwarp();
+                if (ge >= C::STAGES) {
+                    ok = warp_wait(&b_empty[st], ((ge / C::STAGES) - 1) & 1, abort_f, a.status);
+                    if (!ok) break;
+                }
+                uint8_t* to = sm + C::KV_OFF + st * C::TILE;
 #pragma unroll
                 for (int x = 0; x < PIECES; x++) {
-                    // (a piece's rows lie in one group of 16 keys, so in one page)
-                    const int grp = (x * RPP + r_in) / 16;
-                    const int pg = __shfl_sync(0xffffffffu, pgs, grp);
-                    const int key = key0 + x * RPP + r_in;
-                    const bool in = key < k1 && in_row && pg >= 0 && pg < a.kv.n_pages;
-                    const int off = ((key0 + 16 * grp) & (a.kv.page - 1)) * a.hd +
-                                    in_group + (x * RPP - 16 * grp) * a.hd;
-                    cp_async16(dst + x * 2048, src + (in ? pg * pages_bytes + off : 0), in);
+                    uint32_t out[8];
+                    e4m3x4_to_f16(w[x].x, out[0], out[1]);
+                    e4m3x4_to_f16(w[x].y, out[2], out[3]);
+                    e4m3x4_to_f16(w[x].z, out[4], out[5]);
+                    e4m3x4_to_f16(w[x].w, out[6], out[7]);
+                    *reinterpret_cast<uint4*>(to + dst0 + x * RPP * 128) =
+                        make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4*>(to + dst1 + x * RPP * 128) =
+                        make_uint4(out[4], out[5], out[6], out[7]);
+                }
+                // (the codes have been read: the copies that follow wait for this)
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&b_full[st]);
+                    mbar_arrive(&b_codee[cs]);
                 }
             }
-            cp_async_commit();
-        };
-        // the scales of block j's key tid, loaded a block ahead
-        float ks = 0.0f, vs = 0.0f;
-        bool real = false;
-        auto scales = [&](int j) {
-            const int key = k0 + j * KB + tid;
-            ks = vs = 0.0f;
-            real = false;
-            if (j < n_blocks && key < k1) {
-                const int64_t pg = table[key >> a.kv.page_shift];
-                real = pg >= 0 && pg < a.kv.n_pages;
-                if (real) {
-                    const int64_t at = paged_row(a.kv, pg, h, key & (a.kv.page - 1));
-                    ks = a.kv.ks[at];
-                    vs = a.kv.vs[at];
-                } else {
-                    raise_status(a.status, DS41_E_INDEX);
+            if (!PAIR) __syncthreads();
+            w.done();
+            __syncthreads();
+            if (*abort_f) ok = false;
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 192 : 208));
+        while (w.next(a)) {
+            const Seq& s = w.pc.s;
+            const Piece& pc = w.pc;
+            const int k0 = w.k0, n_blocks = w.n_blocks, blocks0 = w.blocks0;
+            const int(&nt)[2] = w.nt;
+            const int(&used0)[2] = w.used0;
+            const int rows = s.n * a.G, r0 = pc.tile * C::QT * 128;
+            // the queries, 128-byte swizzled; rows that do not exist are zero
+            for (int x = threadIdx.x - 128; x < C::QT * 128 * (D / 8); x += 256) {
+                const int r = x / (D / 8), ch = x % (D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r0 + r < rows && ch * 8 < a.hd) {
+                    const int t = (r0 + r) / a.G;
+                    v = *reinterpret_cast<const uint4*>(a.q + (s.q0 + t) * a.q_tok +
+                                                        (pc.h * a.G + (r0 + r) % a.G) * a.q_head +
+                                                        ch * 8);
                 }
-            }
-        };
-        for (int e = 0; e < C::CODES - 1; e++) fetch(e, pages(e));
-        int ahead = pages(C::CODES - 1);
-        scales(0);
-        bool ok = true;
-        for (int e = 0; e < n_ring && ok; e++) {
-            int j, kv;
-            entry(e, j, kv);
-            fetch(e + C::CODES - 1, ahead);
-            ahead = pages(e + C::CODES);
-            const int st = e % C::STAGES, use = e / C::STAGES;
-            if (use > 0) ok = warp_wait(&b_empty[st], (use - 1) & 1, abort_f, a.status);
-            if (!ok) break;
-            cp_async_wait<C::CODES - 1>();
-            const uint8_t* from = sm + C::C_OFF + (e % C::CODES) * C::CTILE + tid * 16;
-            uint8_t* to = sm + C::KV_OFF + st * C::TILE;
-#pragma unroll
-            for (int x = 0; x < PIECES; x++) {
-                int r, ch;
-                piece(x, r, ch);
-                const uint4 w = *reinterpret_cast<const uint4*>(from + x * 2048);
-                uint32_t out[8];
-                e4m3x4_to_f16(w.x, out[0], out[1]);
-                e4m3x4_to_f16(w.y, out[2], out[3]);
-                e4m3x4_to_f16(w.z, out[4], out[5]);
-                e4m3x4_to_f16(w.w, out[6], out[7]);
-                uint8_t* row = to + (ch >> 2) * C::BLK + r * 128;
-                const int c0 = (ch & 3) * 2;
-                *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) =
-                    make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) =
-                    make_uint4(out[4], out[5], out[6], out[7]);
+                if (E4M3) {  // D / 8 lanes have a row
+                    const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                    uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
+    #pragma unroll
+                    for (int off = D / 16; off > 0; off >>= 1)
+                        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+                    const int e = query_exponent(mb);
+                    const float down = exp2f((float)-e);
+                    v = make_uint4(bf16x2_to_f16x2(v.x, down), bf16x2_to_f16x2(v.y, down),
+                                   bf16x2_to_f16x2(v.z, down), bf16x2_to_f16x2(v.w, down));
+                    if (ch == 0) reinterpret_cast<int8_t*>(sm + C::QE_OFF)[r] = (int8_t)e;
+                }
+                *reinterpret_cast<uint4*>(sm + C::Q_OFF + (r >> 7) * C::TILE + (ch >> 3) * C::BLK +
+                                          (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
             }
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_full[st]);
-            if (kv == 0) {
-                const int sl = j % SCN;
-                if (j >= SCN) ok = warp_wait(&b_sce[sl], ((j / SCN) - 1) & 1, abort_f, a.status);
-                if (!ok) break;
-                float* sc = reinterpret_cast<float*>(sm + C::SC_OFF + sl * C::SC_BYTES);
-                sc[8 + tid] = ks;
-                sc[136 + tid] = vs;
-                const uint32_t w = __ballot_sync(0xffffffffu, real);
-                float vm = vs == vs ? fabsf(vs) : 0.0f;  // (a NaN scale asks for nothing)
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
-                if (lane == 0) {
-                    reinterpret_cast<uint32_t*>(sc)[warp & 3] = w;
-                    sc[4 + (warp & 3)] = vm;
+            __syncthreads();
+
+            // what a stream leaves: reference (log2), sum; its rows are in tensor memory
+            float end_m = -INFINITY, end_l = 0.0f;
+            if (ok) {
+                const int t = (warp - 4) >> 2;
+                const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+                const uint32_t tm_s = tmem + lanes + TM_S + 128 * t;
+                const uint32_t tm_o = tmem + lanes + TM_O + 128 * t;
+                const int row = r0 + (PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane;
+                const bool live = row < rows;
+                const RowView view = row_view(a, s, min(row, rows - 1) / a.G);
+                float c = a.scale_log2;
+                if (E4M3)
+                    c *= exp2f((float)reinterpret_cast<const int8_t*>(
+                        sm + C::QE_OFF)[(PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane]);
+                RowState st(E4M3);
+                for (int j = PAIR ? 0 : t, i = 0; j < n_blocks; j += PAIR ? 1 : 2, i++) {
+                    const int gb = blocks0 + j, sl = gb % SCN;
+                    ok = warp_wait(&b_sc[sl], (gb / SCN) & 1, abort_f, a.status);
+                    if (ok && nt[t] > 0)
+                        ok = warp_wait(&b_s[t], (used0[t] + i) & 1, abort_f, a.status);
+                    if (!ok) break;
+                    if (nt[t] > 0) {
+                        tc_fence_after();
+                        const float* sc =
+                            reinterpret_cast<const float*>(sm + C::SC_OFF + sl * C::SC_BYTES);
+                        const uint4 real = *reinterpret_cast<const uint4*>(sc);
+                        const int j0 = k0 + j * KB;
+                        // one choice for the warp: its lanes load from tensor memory together
+                        const bool any = __any_sync(
+                            0xffffffffu, (real.x & real.y & real.z & real.w) != 0xffffffffu ||
+                                             j0 + KB > view.pre || j0 <= view.lo);
+                        uint32_t vis[4] = {};
+                        if (any) {
+                            vis[0] = real.x & seen_word(view, s.n, j0);
+                            vis[1] = real.y & seen_word(view, s.n, j0 + 32);
+                            vis[2] = real.z & seen_word(view, s.n, j0 + 64);
+                            vis[3] = real.w & seen_word(view, s.n, j0 + 96);
+                        }
+                        float vmax = 0.0f;
+                        if (E4M3) {
+                            // the largest scale of a real key (fmaxf passes over NaN)
+                            const uint32_t w = lane < 16 ? (lane < 8 ? real.x : real.y)
+                                                         : (lane < 24 ? real.z : real.w);
+                            const float4 v4 = *reinterpret_cast<const float4*>(sc + 132 + 4 * lane);
+                            const int b4 = 4 * (lane & 7);
+                            if ((w >> b4) & 1) vmax = fmaxf(vmax, v4.x);
+                            if ((w >> (b4 + 1)) & 1) vmax = fmaxf(vmax, v4.y);
+                            if ((w >> (b4 + 2)) & 1) vmax = fmaxf(vmax, v4.z);
+                            if ((w >> (b4 + 3)) & 1) vmax = fmaxf(vmax, v4.w);
+    #pragma unroll
+                            for (int off = 16; off > 0; off >>= 1)
+                                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+                        }
+                        if (any)
+                            softmax_block<D, E4M3, true>(tm_s, tm_o, i > 0, vis, c, sc + 4, sc + 132,
+                                                         vmax, live, st);
+                        else
+                            softmax_block<D, E4M3, false>(tm_s, tm_o, i > 0, vis, c, sc + 4, sc + 132,
+                                                          vmax, live, st);
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (nt[t] > 0) mbar_arrive(&b_p[t]);
+                        mbar_arrive(&b_sce[sl]);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b_sc[sl]);
-                scales(j + 1);
+                if (nt[t] > 0 && ok) ok = warp_wait(&b_o[t], w.ends0[t] & 1, abort_f, a.status);
+                tc_fence_after();
+                end_m = st.reference(c);
+                end_l = st.l;
+                if (!PAIR && t == 1 && nt[1] > 0 && ok) {
+                    // to the other stream, through the ring (nothing of it is in use)
+                    float* x = reinterpret_cast<float*>(sm + C::KV_OFF) +
+                               (32 * (warp & 3) + lane) * C::XP;
+                    x[D] = end_m;
+                    x[D + 1] = end_l;
+    #pragma unroll 1
+                    for (int d = 0; d < D; d += 16) {
+                        uint32_t ov[16];
+                        tc_ld16(tm_o + d, ov);
+                        tc_wait_ld();
+    #pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4*>(x + d + e) =
+                                make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                    }
+                }
             }
-        }
-        cp_async_wait<0>();
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 176 : 208));
-        const int t = (warp - 4) >> 2;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tm_s = tmem + lanes + TM_S + 128 * t, tm_o = tmem + lanes + TM_O + 128 * t;
-        const int row = r0 + (PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane;
-        const bool live = row < rows;
-        const int tok = min(row, rows - 1) / a.G, head = h * a.G + min(row, rows - 1) % a.G;
-        const RowView view = row_view(a, s, tok);
-        float c = a.scale_log2;
-        if (E4M3)
-            c *= exp2f((float)reinterpret_cast<const int8_t*>(
-                sm + C::QE_OFF)[(PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane]);
-        RowState st(E4M3);
-        bool ok = true;
-        for (int i = 0; i < nt[t]; i++) {
-            const int j = block_of(t, i), sl = j % SCN;
-            ok = warp_wait(&b_sc[sl], (j / SCN) & 1, abort_f, a.status) &&
-                 warp_wait(&b_s[t], i & 1, abort_f, a.status);
-            if (!ok) break;
-            tc_fence_after();
-            const float* sc = reinterpret_cast<const float*>(sm + C::SC_OFF + sl * C::SC_BYTES);
-            const uint4 real = *reinterpret_cast<const uint4*>(sc);
-            const int j0 = k0 + j * KB;
-            const bool masked = (real.x & real.y & real.z & real.w) != 0xffffffffu ||
-                                j0 + KB > view.pre || j0 <= view.lo;
-            uint32_t vis[4] = {};
-            // one choice for the warp: its lanes load from tensor memory together
-            const bool any = __any_sync(0xffffffffu, masked);
-            if (any) {
-                vis[0] = real.x & seen_word(view, s.n, j0);
-                vis[1] = real.y & seen_word(view, s.n, j0 + 32);
-                vis[2] = real.z & seen_word(view, s.n, j0 + 64);
-                vis[3] = real.w & seen_word(view, s.n, j0 + 96);
-            }
-            float vmax = 0.0f;
-            if (E4M3) {
-                const float4 v4 = *reinterpret_cast<const float4*>(sc + 4);
-                vmax = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
-            }
-            softmax_block<D, E4M3>(tm_s, tm_o, i > 0, any, vis, c, sc + 8, sc + 136, vmax, live,
-                                   st);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&b_p[t]);
-                mbar_arrive(&b_sce[sl]);
-            }
-        }
-        if (nt[t] > 0 && ok) ok = warp_wait(&b_o[t], 0, abort_f, a.status);
-        tc_fence_after();
-        const int64_t at = (int64_t)(s.q0 + tok) * a.nh + head;
-        const bool direct = PAIR && a.parts == 1;
-        if (ok && (!PAIR || nt[t] > 0)) {
-            // O is read by whole warps; a stream without blocks (ALT, one block)
-            // still leaves its empty partial result
-            const RowEnd end = direct ? row_end(st.reference(c), st.l,
-                                                a.sink ? a.sink[head] : -INFINITY)
-                                      : RowEnd{1.0f, 0.0f};
-            const int64_t part = PAIR ? split : 2 * split + t;
-            float* po = direct ? nullptr : a.part + (part * a.Tq * a.nh + at) * a.hd;
-#pragma unroll 1
-            for (int x = 0; x < D; x += 16) {
-                uint32_t ov[16] = {};
+            if (!PAIR) __syncthreads();
+            if (warp < (PAIR ? 12 : 8) && ok) {
+                const int t = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
+                const uint32_t tm_o = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_O + 128 * t;
+                const int row = r0 + 128 * t + row_in;
+                const bool live = row < rows;
+                const int tok = min(row, rows - 1) / a.G, head = pc.h * a.G + min(row, rows - 1) % a.G;
+                const int64_t at = (int64_t)(s.q0 + tok) * a.nh + head;
+                const bool whole = is_whole(pc);
+                const float* x = reinterpret_cast<const float*>(sm + C::KV_OFF) + row_in * C::XP;
+                const bool both = !PAIR && nt[1] > 0;
+                float f = 1.0f, fx = 0.0f, m = end_m, l = end_l;
+                if (both) {
+                    m = fmaxf(end_m, x[D]);
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    f = exp2f(end_m - base);
+                    fx = exp2f(x[D] - base);
+                    l = f * end_l + fx * x[D + 1];
+                }
+                if (whole) {
+                    const RowEnd end = row_end(m, l, a.sink ? a.sink[head] : -INFINITY);
+                    if (live && a.lse) a.lse[at] = end.lse;
+                    f *= end.factor;
+                    fx *= end.factor;
+                }
+                const int64_t slot = slot_of(pc) * a.tile_rows + 128 * t + row_in;
+                if (live && !whole) a.part_ml[slot] = make_float2(m, l);
                 if (nt[t] > 0) {
-                    tc_ld16(tm_o + x, ov);
-                    tc_wait_ld();
+    #pragma unroll 1
+                    for (int d = 0; d < D; d += 16) {
+                        uint32_t ov[16];
+                        float v[16];
+                        tc_ld16(tm_o + d, ov);
+                        tc_wait_ld();
+                        if (!live || d >= a.hd) continue;
+    #pragma unroll
+                        for (int e = 0; e < 16; e++) v[e] = u2f(ov[e]) * f;
+                        if (both) {
+    #pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 y = *reinterpret_cast<const float4*>(x + d + e);
+                                v[e] += y.x * fx;
+                                v[e + 1] += y.y * fx;
+                                v[e + 2] += y.z * fx;
+                                v[e + 3] += y.w * fx;
+                            }
+                        }
+                        if (whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.o + at * a.hd + d);
+    #pragma unroll
+                            for (int e = 0; e < 16; e += 8)
+                                dst[e / 8] =
+                                    make_uint4(bf16x2(v[e], v[e + 1]), bf16x2(v[e + 2], v[e + 3]),
+                                               bf16x2(v[e + 4], v[e + 5]), bf16x2(v[e + 6], v[e + 7]));
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(a.part + slot * a.hd + d);
+    #pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                dst[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
+                    }
                 }
-                if (!live || x >= a.hd) continue;
-                if (direct) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.o + at * a.hd + x);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        dst[e / 8] = make_uint4(
-                            bf16x2(u2f(ov[e]) * end.factor, u2f(ov[e + 1]) * end.factor),
-                            bf16x2(u2f(ov[e + 2]) * end.factor, u2f(ov[e + 3]) * end.factor),
-                            bf16x2(u2f(ov[e + 4]) * end.factor, u2f(ov[e + 5]) * end.factor),
-                            bf16x2(u2f(ov[e + 6]) * end.factor, u2f(ov[e + 7]) * end.factor));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<uint4*>(po + x + e) =
-                            make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-                }
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             }
-            if (live && direct && a.lse) a.lse[at] = end.lse;
-            if (live && !direct)
-                a.part_ml[part * a.Tq * a.nh + at] =
-                    make_float2(st.reference(c), st.l);
+            w.done();
+            // tensor memory, the queries and the ring are free for the next piece
+            tc_fence_before();
+            __syncthreads();
+            tc_fence_after();
+            if (*abort_f) ok = false;
         }
     }
 
@@ -615,7 +715,7 @@ int make_map_pages(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const 
 }
 
 template <int D, bool E4M3, bool PAIR>
-int launch_many_as(const Args& a, int row_tiles, int64_t B, const char* name, cudaStream_t st) {
+int launch_many_as(const Args& a, const char* name, cudaStream_t st) {
     using C = TcCfg<D, E4M3, PAIR>;
     CUtensorMap mk = {}, mv = {};
     if (!E4M3) {
@@ -629,25 +729,23 @@ int launch_many_as(const Args& a, int row_tiles, int64_t B, const char* name, cu
                                                  (int)C::SMEM),
                             name))
         return rc;
-    const int splits = a.parts / a.per;
-    return launch_pdl(kern, dim3((unsigned)splits, (unsigned)(a.kvh * row_tiles), (unsigned)B),
-                      dim3(C::THREADS), C::SMEM, st, name, mk, mv, a);
+    return launch_pdl(kern, dim3((unsigned)a.workers), dim3(C::THREADS), C::SMEM, st, name, mk, mv,
+                      a);
 }
 
 }  // namespace
 
-int launch_many(const Args& a, bool pair, int row_tiles, int64_t B, const char* name,
-                cudaStream_t st) {
-    const bool e = a.kv.ks != nullptr;
+int launch_many(const Args& a, const char* name, cudaStream_t st) {
+    const bool e = a.kv.ks != nullptr, pair = a.tile_rows == 256;
     if (a.hd <= 64)
-        return e ? (pair ? launch_many_as<64, true, true>(a, row_tiles, B, name, st)
-                         : launch_many_as<64, true, false>(a, row_tiles, B, name, st))
-                 : (pair ? launch_many_as<64, false, true>(a, row_tiles, B, name, st)
-                         : launch_many_as<64, false, false>(a, row_tiles, B, name, st));
-    return e ? (pair ? launch_many_as<128, true, true>(a, row_tiles, B, name, st)
-                     : launch_many_as<128, true, false>(a, row_tiles, B, name, st))
-             : (pair ? launch_many_as<128, false, true>(a, row_tiles, B, name, st)
-                     : launch_many_as<128, false, false>(a, row_tiles, B, name, st));
+        return e ? (pair ? launch_many_as<64, true, true>(a, name, st)
+                         : launch_many_as<64, true, false>(a, name, st))
+                 : (pair ? launch_many_as<64, false, true>(a, name, st)
+                         : launch_many_as<64, false, false>(a, name, st));
+    return e ? (pair ? launch_many_as<128, true, true>(a, name, st)
+                     : launch_many_as<128, true, false>(a, name, st))
+             : (pair ? launch_many_as<128, false, true>(a, name, st)
+                     : launch_many_as<128, false, false>(a, name, st));
 }
 
 }  // namespace tree
