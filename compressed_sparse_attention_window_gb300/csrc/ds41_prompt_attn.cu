@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int row = 32 * (warp & 3) + lane;
         const int tok = row / p.G, gh = row - tok * p.G;
         const bool live = tok < r.count;
+        const bool idle = !__any_sync(0xffffffffu, live);
         const int64_t pos = (int64_t)r.p_first + tok;              // the last key it sees
         const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
         const int64_t p_last = (int64_t)r.p_first + r.count - 1;
@@ -390,12 +391,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < 4; i++)
                     vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
             }
-            if (masked)
-                softmax_block<D, false, true>(tm_s, tm_o, j > r.lo, vis, c, nullptr, nullptr, 0.0f,
-                                              live, st);
-            else
-                softmax_block<D, false, false>(tm_s, tm_o, j > r.lo, vis, c, nullptr, nullptr,
-                                               0.0f, live, st);
+            if (idle) {
+                // none of the warp's rows exists: whatever its scores hold weighs no one
+            } else if (masked) {
+                softmax_block<D, true>(tm_s, tm_o, j > r.lo, vis, c, live, st);
+            } else {
+                softmax_block<D, false>(tm_s, tm_o, j > r.lo, vis, c, live, st);
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b_p[t]);

@@ -130,6 +130,18 @@ __device__ __forceinline__ float scale_exponent(float vmax) {
     return fmaxf((float)((int)(__float_as_uint(vmax) >> 23) - 127), RowState::VS_MIN);
 }
 
+// tcgen05.wait::ld with the registers it waits for, so that nothing that uses them
+// moves ahead of it; unlike tc_wait_ld it lets loads from shared memory pass
+__device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]));
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
 // 32 scores of a row, scaled by ks, with those that are not seen at -inf.
 template <bool SCALED, bool MASKED>
 __device__ __forceinline__ void prepare32(uint32_t (&s)[32], const float* ks, uint32_t vis) {
@@ -161,17 +173,12 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     }
     return fmaxf(a, b);
 }
-// 32 scores -> 32 weights, two per column from tm_p on; their sum joins `sum`
+// 32 scores -> 32 weights in pk, two to a register; their sum joins `sum`
 template <bool SCALED, bool MASKED>
-__device__ __forceinline__ void weights32(uint32_t (&s)[32], uint32_t tm_p, float c, float base,
-                                          float m_first, const float* vs, uint32_t vis,
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint32_t (&pk)[16], float c,
+                                          float base, const float* vs, uint32_t vis,
                                           uint64_t (&sum)[2]) {
     const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
-    if (m_first != 0.0f) {  // (see softmax_block)
-#pragma unroll
-        for (int e = 0; e < 32; e++) s[e] = __float_as_uint(u2f(s[e]) - m_first);
-    }
-    uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
         float p[4];
@@ -194,26 +201,60 @@ __device__ __forceinline__ void weights32(uint32_t (&s)[32], uint32_t tm_p, floa
         pk[e / 2] = SCALED ? f16x2(p[0], p[1]) : bf16x2(p[0], p[1]);
         pk[e / 2 + 1] = SCALED ? f16x2(p[2], p[3]) : bf16x2(p[2], p[3]);
     }
-    tc_st16(tm_p, pk);
+}
+// The lazy reference has moved: what was computed with the old one times f - the
+// D columns of O at tm_o (with have_o) and the weights that this block has
+// written already, n of 32 keys each, at tm_p.
+template <int D, bool SCALED>
+__device__ __forceinline__ void rescale(uint32_t tm_p, int n, uint32_t tm_o, bool have_o, float f) {
+    tc_wait_st();
+    if (have_o) {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 16) {
+            uint32_t ov[16];
+            tc_ld16(tm_o + x, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e++) ov[e] = __float_as_uint(u2f(ov[e]) * f);
+            tc_st16(tm_o + x, ov);
+        }
+    }
+#pragma unroll 1
+    for (int x = 0; x < 16 * n; x += 16) {
+        uint32_t pv[16];
+        tc_ld16(tm_p + x, pv);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            if (SCALED) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pv[e]));
+                pv[e] = f16x2(v.x * f, v.y * f);
+            } else {
+                pv[e] = bf16x2(u2f(pv[e] << 16) * f, u2f(pv[e] & 0xffff0000u) * f);
+            }
+        }
+        tc_st16(tm_p + x, pv);
+    }
 }
 
 // One thread's row: its 128 scores of the block (columns tm_s .. of its lane)
-// become weights, two per column from tm_s on: bf16, or f16 when SCALED.
-//   t_j = c S_j (SCALED: c ks_j S_j), p_j = 2^(t_j - reference), l += p_j, the
-//   weight p_j (SCALED: p_j vs_j; 0 for a key that is not seen, whatever vs_j
+// become weights, two per column from tm_s on: bf16, or f16 in the scaled form.
+//   t_j = c S_j (scaled: c ks_j S_j), p_j = 2^(t_j - reference), l += p_j, the
+//   weight p_j (scaled: p_j vs_j; 0 for a key that is not seen, whatever vs_j
 //   holds)
 // MASKED: keys whose bit of vis is clear are not seen.  A block that every row
 // sees whole takes the other instance: as a run-time choice the compiler turned
 // the selects into predicated code for every block, twice the instructions.
-// Where the maximum exceeds the reference by 2^4 it moves and l and, with
-// `have_o`, the D columns of the output at tm_o are rescaled; the caller has
+// Where a maximum exceeds the reference by 2^4 (in nearly all blocks none does)
+// the reference moves and what it has been used for is rescaled - the caller has
 // seen the products before this block complete.  All lanes of a warp take part;
-// `live` = the row exists.  vmax: the largest vs of the block.
-template <int D, bool SCALED, bool MASKED>
+// `live` = the row exists.
+//
+// The plain form holds the 128 scores in registers.
+template <int D, bool MASKED>
 __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool have_o,
-                                              const uint32_t (&vis)[4], float c,
-                                              const float* ks, const float* vs, float vmax,
-                                              bool live, RowState& st) {
+                                              const uint32_t (&vis)[4], float c, bool live,
+                                              RowState& st) {
     uint32_t s[4][32];
     float top = -INFINITY;
 #pragma unroll
@@ -221,51 +262,100 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
     tc_wait_ld();
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        prepare32<SCALED, MASKED>(s[i], SCALED ? ks + 32 * i : nullptr, vis[i]);
+        prepare32<false, MASKED>(s[i], nullptr, vis[i]);
         top = fmaxf(top, max32(s[i]));
     }
     // (-inf - -inf is NaN: no move)
     const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
-    const bool vmove = SCALED && vmax > st.vlim;
-    if (__any_sync(0xffffffffu, move || vmove)) {
-        float shift = move ? (st.m - top) * c : 0.0f;
+    if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? ex2((st.m - top) * c) : 1.0f;
         if (move) st.m = top;
-        if (vmove) {
-            const float lr = scale_exponent(vmax);
-            shift += st.lr - lr;
-            st.lr = lr;
-            st.vlim = ex2(lr + 8.0f);
-        }
-        const float f = ex2(shift);
         st.l *= f;
-        if (have_o) {
-#pragma unroll 1
-            for (int x = 0; x < D; x += 16) {
-                uint32_t ov[16];
-                tc_ld16(tm_o + x, ov);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; e++) ov[e] = __float_as_uint(u2f(ov[e]) * f);
-                tc_st16(tm_o + x, ov);
-            }
-        }
+        if (have_o) rescale<D, false>(tm_s, 0, tm_o, true, f);
     }
-    float base = st.m == -INFINITY ? 0.0f : SCALED ? fmaf(st.m, c, st.lr) : st.m * c;
-    float m_first = 0.0f;
+    float base = st.m == -INFINITY ? 0.0f : st.m * c;
     if (fabsf(base) > 0x1p22f) {
         // c m itself is rounded by more than a fraction of one power of two: take
         // the differences first
-        m_first = st.m;
-        base = SCALED ? st.lr : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        base = 0.0f;
     }
     uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        weights32<SCALED, MASKED>(s[i], tm_s + 16 * i, c, base, m_first,
-                                  SCALED ? vs + 32 * i : nullptr, vis[i], sum);
-    float a, b;
-    unf2(add2(sum[0], sum[1]), a, b);
-    st.l += a + b;
+    for (int i = 0; i < 4; i++) {
+        uint32_t pk[16];
+        weights32<false, MASKED>(s[i], pk, c, base, nullptr, vis[i], sum);
+        tc_st16(tm_s + 16 * i, pk);
+    }
+    float x, y;
+    unf2(add2(sum[0], sum[1]), x, y);
+    st.l += x + y;
+    tc_wait_st();
+}
+
+// The scaled form (e4m3 caches), whose warps share registers and issue slots with
+// the widening ones: one pass, 32 keys at a time, the next 32 on their way; a
+// reference that moves within the block takes the weights written before along.
+// vmax: the largest vs of the block.
+template <int D, bool MASKED>
+__device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_o, bool have_o,
+                                                     const uint32_t (&vis)[4], float c,
+                                                     const float* ks, const float* vs, float vmax,
+                                                     bool live, RowState& st) {
+    uint64_t sum[2] = {0, 0};
+    // the reference, times c, and lr: what a score's exponent is reduced by
+    float base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
+    bool vmove = vmax > st.vlim;
+    auto chunk = [&](uint32_t(&s)[32], int i, uint32_t seen) {
+        prepare32<true, MASKED>(s, ks + 32 * i, seen);
+        const float top = max32(s);
+        const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
+        if (__any_sync(0xffffffffu, move || vmove)) {
+            float shift = move ? (st.m - top) * c : 0.0f;
+            if (move) st.m = top;
+            if (vmove) {
+                const float lr = scale_exponent(vmax);
+                shift += st.lr - lr;
+                st.lr = lr;
+                st.vlim = ex2(lr + 8.0f);
+                vmove = false;
+            }
+            const float f = ex2(shift);
+            st.l *= f;
+            sum[0] = mul2(sum[0], f2(f, f));
+            sum[1] = mul2(sum[1], f2(f, f));
+            if (have_o || i > 0) rescale<D, true>(tm_s, i, tm_o, have_o, f);
+            base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
+        }
+        float reduced = base;
+        if (fabsf(base) > 0x1p22f) {  // (as above)
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[e] = __float_as_uint(u2f(s[e]) - st.m);
+            reduced = st.lr;
+        }
+        // (the weights of 32 keys take 16 columns, so they never reach scores that
+        // are still to be read)
+        uint32_t pk[16];
+        weights32<true, MASKED>(s, pk, c, reduced, vs + 32 * i, seen, sum);
+        tc_st16(tm_s + 16 * i, pk);
+    };
+    uint32_t a[32], b[32];
+    tc_ld32(tm_s, a);
+#pragma unroll 1
+    for (int i = 0; i < 4; i += 2) {
+        wait_ld32(a);
+        tc_ld32(tm_s + 32 * (i + 1), b);
+        chunk(a, i, i ? vis[2] : vis[0]);
+        wait_ld32(b);
+        if (i == 0) tc_ld32(tm_s + 64, a);
+        chunk(b, i + 1, i ? vis[3] : vis[1]);
+    }
+    float x, y;
+    unf2(add2(sum[0], sum[1]), x, y);
+    st.l += x + y;
     tc_wait_st();
 }
 

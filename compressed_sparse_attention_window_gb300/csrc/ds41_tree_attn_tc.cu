@@ -36,9 +36,10 @@ namespace tree {
 using namespace tc;
 
 constexpr int KB = 128;  // keys per block
-constexpr int SCN = 4;   // blocks whose scales and visibility are held
+constexpr int SCN = 8;   // blocks whose scales and visibility are held
 
-// warps 0 copies, 1 MMA, 2 tail, 4..7 and 8..11 softmax, 12..15 widening (e4m3)
+// warps 0 K copies, 1 MMA, 2 V copies, 3 the next step, 4..7 and 8..11 softmax,
+// 12..15 widening (e4m3)
 template <int D, bool E4M3, bool PAIR>
 struct TcCfg {
     static constexpr int THREADS = E4M3 ? 512 : 384;
@@ -57,7 +58,7 @@ struct TcCfg {
     static constexpr uint32_t SC_BYTES = (E4M3 ? 1024 : 0) + 16;
     static constexpr uint32_t QE_OFF = SC_OFF + SCN * SC_BYTES;  // the queries' exponents
     static constexpr uint32_t BAR_OFF = QE_OFF + (E4M3 ? QT * 128 : 0);
-    static constexpr uint32_t SMEM = BAR_OFF + 640 + 1024;
+    static constexpr uint32_t SMEM = BAR_OFF + 1024 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr int LA = PAIR ? 1 : 2;  // K blocks ahead of the V blocks
     // the other stream's rows at the end of a piece (no tile is in use then)
@@ -75,20 +76,6 @@ template <int LA>
 __device__ __forceinline__ int pos_v(int j, int n) {
     return min(LA, n) + j + min(j, max(0, n - LA));
 }
-// entry e of the ring of n blocks: block j, K (0) or V (1)
-template <int LA>
-__device__ __forceinline__ void entry_of(int e, int n, int& j, int& kv) {
-    const int lead = min(LA, n);
-    if (e < lead) {
-        j = e;
-        kv = 0;
-    } else {
-        const int x = e - lead, both = 2 * max(0, n - LA);
-        kv = x < both ? (x & 1) ^ 1 : 1;
-        j = x < both ? (kv ? x / 2 : x / 2 + LA) : x - both / 2;
-    }
-}
-
 // Which of the keys j .. j + 31 a row sees.
 __device__ __forceinline__ uint32_t low_bits(int64_t n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -118,38 +105,44 @@ __device__ __forceinline__ uint32_t seen_word(const RowView& w, int n_drafted, i
     return r;
 }
 
-// A role's walk through its CTA's pieces, and what the barriers have seen before
-// the present one: entries of the ring, blocks, blocks and ends of each stream,
-// V blocks with rows behind the last key.
-template <int D, bool E4M3, bool PAIR>
-struct Walk {
-    Share share;
+// A step of the CTA's walk through its pieces, in shared memory (two: one thread
+// plans the next while the roles work on the present): the piece, and what the
+// barriers have seen before it: entries of the ring, blocks, blocks and ends of
+// each stream, V blocks with rows behind the last key.  The roles read what they
+// need when they need it: held in registers through the key loop it would push
+// the softmax warps' scores into local memory, which shared memory of this size
+// leaves hardly any cache for.
+struct Step {
     Piece pc;
-    int k0, k1, n_blocks, tail;  // the piece's keys; those of its last block
+    int more;                    // 0: the walk is over
+    int rows, r0, k0, k1, n_blocks, tail;  // tail: keys of the last block
     int nt[2];                   // blocks of each stream
-    int ring0 = 0, blocks0 = 0, used0[2] = {0, 0}, ends0[2] = {0, 0}, tails0 = 0;
-    __device__ __forceinline__ bool next(const Args& a) {
-        if (!next_piece(a, share, pc)) return false;
-        const int rows = pc.s.n * a.G, r0 = pc.tile * TcCfg<D, E4M3, PAIR>::QT * 128;
-        k0 = first_key(a, pc.s) + pc.first * KB;
-        k1 = min(pc.s.len, k0 + pc.count * KB);
-        n_blocks = pc.count;
-        tail = (k1 - k0) - (n_blocks - 1) * KB;
-        nt[0] = PAIR ? n_blocks : (n_blocks + 1) / 2;
-        nt[1] = PAIR ? (rows - r0 > 128 ? n_blocks : 0) : n_blocks / 2;
-        return true;
-    }
-    __device__ __forceinline__ void done() {
-        ring0 += 2 * n_blocks;
-        blocks0 += n_blocks;
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-            used0[t] += nt[t];
-            ends0[t] += nt[t] > 0;
-        }
-        tails0 += tail < KB;
-    }
+    int ring0, blocks0, used0[2], ends0[2], tails0;
 };
+template <int QT>
+__device__ __forceinline__ void plan_step(const Args& a, Share& share, const Step& was, Step& w) {
+    constexpr bool PAIR = QT == 2;
+    Piece pc;
+    w.more = next_piece(a, share, pc) ? 1 : 0;
+    if (!w.more) return;
+    w.pc = pc;
+    w.rows = pc.s.n * a.G;
+    w.r0 = pc.tile * QT * 128;
+    w.k0 = first_key(a, pc.s) + pc.first * KB;
+    w.k1 = min(pc.s.len, w.k0 + pc.count * KB);
+    w.n_blocks = pc.count;
+    w.tail = (w.k1 - w.k0) - (pc.count - 1) * KB;
+    w.nt[0] = PAIR ? pc.count : (pc.count + 1) / 2;
+    w.nt[1] = PAIR ? (w.rows - w.r0 > 128 ? pc.count : 0) : pc.count / 2;
+    w.ring0 = was.ring0 + 2 * was.n_blocks;
+    w.blocks0 = was.blocks0 + was.n_blocks;
+    for (int t = 0; t < 2; t++) {
+        w.used0[t] = was.used0[t] + was.nt[t];
+        w.ends0[t] = was.ends0[t] + (was.nt[t] > 0);
+    }
+    w.tails0 = was.tails0 + (was.n_blocks > 0 && was.tail < KB);
+    note_ends(a, pc);
+}
 
 template <int D, bool E4M3, bool PAIR>
 __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
@@ -176,8 +169,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_fix + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int64_t* sh = reinterpret_cast<int64_t*>(tmem_slot + 2);
+    Step* steps = reinterpret_cast<Step*>(sh + C::THREADS / 32 + 4);
     static_assert((2 * C::STAGES + 2 * C::CODES + 2 * SCN + 8) * 8 + 8 +
-                          (2 * C::THREADS / 32 + 4) * 8 <= 640,
+                          (C::THREADS / 32 + 4) * 8 + 2 * sizeof(Step) <= 1024,
                   "barrier area");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -219,118 +213,147 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     // queries are in shared memory), for one tile of rows again where its streams
     // end, and where it ends.  The roles' code is kept apart so that each has its
     // own share of the register file (128 a thread at launch, 168 on bf16).
-    Walk<D, E4M3, PAIR> w;
-    w.share = share;
+    if (threadIdx.x == 96) {
+        steps[1].n_blocks = steps[1].ring0 = steps[1].blocks0 = steps[1].tails0 = 0;
+        steps[1].nt[0] = steps[1].nt[1] = 0;
+        for (int t = 0; t < 2; t++) steps[1].used0[t] = steps[1].ends0[t] = 0;
+        plan_step<C::QT>(a, share, steps[1], steps[0]);
+    }
+    __syncthreads();
     bool ok = true;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 72 : 88));
-        while (w.next(a)) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(88));
+        for (int turn = 0; steps[turn & 1].more; turn++) {
+            const Step& w = steps[turn & 1];
             const int32_t* table = a.table + (int64_t)w.pc.b * a.max_pages;
-            const Piece& pc = w.pc;
+            const int h = w.pc.h;
             const int k0 = w.k0, k1 = w.k1, n_blocks = w.n_blocks, n_ring = 2 * n_blocks;
             const int ring0 = w.ring0, blocks0 = w.blocks0, tail = w.tail, tails0 = w.tails0;
-            const int(&nt)[2] = w.nt;
-            const int(&used0)[2] = w.used0;
+            const int nt[2] = {w.nt[0], w.nt[1]}, used0[2] = {w.used0[0], w.used0[1]};
             auto uses = [&](int t, int j) { return PAIR ? nt[t] > 0 : (j & 1) == t; };
-            if (threadIdx.x == 0) note_ends(a, pc);
             __syncthreads();
-            if (warp == 0 && ok) {
-                // pages -> stages (bf16) or code tiles (e4m3), and which keys are real
-                const int per = min(a.kv.page, KB), copies = KB / per;  // rows of a copy
-                int armed = 0;
-                for (int e = 0; e < n_ring && ok; e++, armed = e) {
-                    int j, kv;
-                    entry_of<C::LA>(e, n_ring / 2, j, kv);
-                    const int ge = ring0 + e;
-                    const int st = ge % (E4M3 ? C::CODES : C::STAGES);
-                    const int use = ge / (E4M3 ? C::CODES : C::STAGES);
-                    uint64_t* full = E4M3 ? &b_code[st] : &b_full[st];
-                    if (use > 0)
-                        ok = warp_wait(E4M3 ? &b_codee[st] : &b_empty[st], (use - 1) & 1, abort_f,
-                                       a.status);
+            if (threadIdx.x == 96) plan_step<C::QT>(a, share, w, steps[(turn + 1) & 1]);
+            if ((warp == 0 || warp == 2) && ok) {
+                // pages -> stages (bf16) or code tiles (e4m3): warp 0 the K blocks,
+                // and which keys are real, warp 2 the V blocks (one warp takes 1500
+                // cycles for a block's K and as many for its V)
+                const int kv = warp >> 1;
+                constexpr int DEPTH = E4M3 ? C::CODES : C::STAGES;
+                uint64_t* const arrived = E4M3 ? b_code : b_full;
+                uint64_t* const freed = E4M3 ? b_codee : b_empty;
+                const int shift = min(a.kv.page_shift, 7), per = 1 << shift;  // rows of a copy
+                const int copies = KB >> shift;
+                const bool copier = lane < copies;
+                const uint8_t* const src = kv ? a.kv.v : a.kv.k;
+                const int64_t head_rows = (int64_t)h * a.kv.page;
+                const int64_t page_rows = (int64_t)a.kvh * a.kv.page;
+                // lane i < copies: the page of the rows it copies, looked up a block ahead
+                auto page_of = [&](int j) {
+                    const int key = k0 + j * KB + lane * per;
+                    return copier && key < k1 ? table[key >> a.kv.page_shift] : -1;
+                };
+                int next = page_of(0), sent = 0;
+                for (; sent < n_blocks; sent++) {
+                    const int j = sent, e = kv ? pos_v<C::LA>(j, n_blocks) : pos_k<C::LA>(j);
+                    const int ge = ring0 + e, st = ge % DEPTH, use = ge / DEPTH;
+                    const int page = next;
+                    next = page_of(j + 1);
                     const int gb = blocks0 + j, sl = gb % SCN;
+                    if (use > 0) ok = warp_wait(&freed[st], (use - 1) & 1, abort_f, a.status);
                     if (ok && kv == 0 && gb >= SCN)
                         ok = warp_wait(&b_sce[sl], ((gb / SCN) - 1) & 1, abort_f, a.status);
                     if (!ok) break;
-                    const int key0 = k0 + j * KB;
-                    // lane i < copies: its page and the rows it copies
-                    const int key = key0 + lane * per;
-                    int64_t pg = -1;
-                    int n = 0;
-                    if (lane < copies && key < k1) {
-                        n = min(per, k1 - key);
-                        pg = table[key >> a.kv.page_shift];
-                        if (pg < 0 || pg >= a.kv.n_pages) {
-                            pg = -1;
-                            if (kv == 0) raise_status(a.status, DS41_E_INDEX);
-                        }
-                    }
-                    uint8_t* sc = sm + C::SC_OFF + sl * C::SC_BYTES;
-                    if (kv == 0) {
-                        // word i: which of the keys 32 i .. are real
-                        const uint32_t good = __ballot_sync(0xffffffffu, pg >= 0);
-                        if (lane < 4) {
-                            uint32_t w = 0;
+                    const int key0 = k0 + j * KB, key = key0 + lane * per;
+                    const int n = copier ? max(0, min(per, k1 - key)) : 0;
+                    const bool real = page >= 0 && page < a.kv.n_pages;
+                    const bool lost = n > 0 && !real;
+                    const bool plain = __all_sync(0xffffffffu, !copier || (n == per && real));
+                    if (lost && kv == 0) raise_status(a.status, DS41_E_INDEX);
+                    uint8_t* const sc = sm + C::SC_OFF + sl * C::SC_BYTES;
+                    uint8_t* const dst = sm + C::C_OFF + st * C::CTILE;
+                    uint32_t bytes = (uint32_t)(KB * a.hd), sbytes = 2 * KB * 4;
+                    const uint32_t mine = real ? (uint32_t)(n * a.hd) : 0u;
+                    const uint32_t smine = real ? (uint32_t)((n + 3) / 4 * 16) : 0u;
+                    if (!plain) {
+                        const uint32_t good = __ballot_sync(0xffffffffu, n > 0 && real);
+                        if (kv == 0 && lane < 4) {
+                            // word i: which of the keys 32 i .. are real
+                            uint32_t word = 0;
                             for (int x = 0; x < 32; x += 16)
-                                if ((good >> ((32 * lane + x) / per)) & 1) w |= 0xffffu << x;
-                            w &= low_bits((int64_t)k1 - key0 - 32 * lane);
-                            reinterpret_cast<uint32_t*>(sc)[lane] = w;
+                                if ((good >> ((32 * lane + x) >> shift)) & 1) word |= 0xffffu << x;
+                            reinterpret_cast<uint32_t*>(sc)[lane] =
+                                word & low_bits((int64_t)k1 - key0 - 32 * lane);
                         }
-                        __syncwarp();
-                    }
-                    const int off = key & (a.kv.page - 1);
-                    if (E4M3) {
-                        const uint32_t bytes = pg >= 0 ? (uint32_t)(n * a.hd) : 0u;
-                        const uint32_t sbytes = pg >= 0 ? (uint32_t)((n + 3) / 4 * 16) : 0u;
-                        const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
-                        const uint32_t alls = 2 * __reduce_add_sync(0xffffffffu, sbytes);
-                        uint8_t* dst = sm + C::C_OFF + st * C::CTILE;
-                        // rows that no copy fills are zero, so that no product meets a NaN
-                        for (int i = 0; i < copies; i++) {
-                            const int have = __shfl_sync(0xffffffffu, pg >= 0 ? n : 0, i);
-                            for (int x = lane; x < (per - have) * a.hd / 16; x += 32)
-                                *reinterpret_cast<uint4*>(dst + (i * per + have) * a.hd + x * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(full, all);
-                            if (kv == 0) mbar_arrive_expect_tx(&b_sc[sl], alls);
-                        }
-                        __syncwarp();
-                        if (pg >= 0) {
-                            const int64_t row = paged_row(a.kv, pg, pc.h, off);
-                            bulk_g2s(dst + lane * per * a.hd, (kv ? a.kv.v : a.kv.k) + row * a.hd,
-                                     bytes, full);
-                            if (kv == 0) {
-                                bulk_g2s(sc + 16 + lane * per * 4, a.kv.ks + row, sbytes, &b_sc[sl]);
-                                bulk_g2s(sc + 528 + lane * per * 4, a.kv.vs + row, sbytes, &b_sc[sl]);
+                        if (E4M3) {
+                            bytes = __reduce_add_sync(0xffffffffu, mine);
+                            sbytes = 2 * __reduce_add_sync(0xffffffffu, smine);
+                            // rows that no copy fills are zero: no product meets a NaN
+                            for (int i = 0; i < copies; i++) {
+                                const int have = __shfl_sync(0xffffffffu, real ? n : 0, i);
+                                for (int x = lane; x < (per - have) * a.hd / 16; x += 32)
+                                    *reinterpret_cast<uint4*>(dst + (i * per + have) * a.hd +
+                                                              x * 16) = make_uint4(0, 0, 0, 0);
                             }
                         }
-                    } else {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(full, C::TILE);
-                            if (kv == 0) mbar_arrive(&b_sc[sl]);
-                        }
-                        __syncwarp();
-                        if (lane < copies) {
-                            // a page that does not exist reads as zeros (a coordinate
-                            // past the tensor)
-                            const int64_t z = pg >= 0 ? pg * a.kvh + pc.h : a.kv.n_pages * a.kvh;
-                            for (int x = 0; x < C::NB; x++)
-                                tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
-                                                lane * per * 128,
-                                            kv ? &map_v : &map_k, 64 * x, off, (int)z, full);
+                    } else if (kv == 0 && lane < 4) {
+                        reinterpret_cast<uint32_t*>(sc)[lane] = 0xffffffffu;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&arrived[st], E4M3 ? bytes : C::TILE);
+                        if (kv == 0) {
+                            if (E4M3) mbar_arrive_expect_tx(&b_sc[sl], sbytes);
+                            else mbar_arrive(&b_sc[sl]);
                         }
                     }
+                    __syncwarp();
+                    const int off = key & (a.kv.page - 1);
+                    if (E4M3) {
+                        if (mine) {
+                            const int64_t row = page * page_rows + head_rows + off;
+                            bulk_g2s(dst + lane * per * a.hd, src + row * a.hd, mine, &arrived[st]);
+                            if (kv == 0) {
+                                bulk_g2s(sc + 16 + lane * per * 4, a.kv.ks + row, smine, &b_sc[sl]);
+                                bulk_g2s(sc + 528 + lane * per * 4, a.kv.vs + row, smine,
+                                         &b_sc[sl]);
+                            }
+                        }
+                    } else if (copier) {
+                        // a page that does not exist reads as zeros (a coordinate
+                        // past the tensor)
+                        const int z = (int)(n > 0 && real ? (int64_t)page * a.kvh + h
+                                                          : a.kv.n_pages * a.kvh);
+#pragma unroll
+                        for (int x = 0; x < C::NB; x++)
+                            tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
+                                            lane * per * 128,
+                                        kv ? &map_v : &map_k, 64 * x, off, z, &arrived[st]);
+                    }
                 }
-                // everything that was started lands before the piece ends
-                const int depth = E4M3 ? C::CODES : C::STAGES;
-                for (int e = max(0, armed - depth); e < armed; e++) {
+                if (warp == 2 && !E4M3 && tail < KB && ok) {
+                    // the V rows behind the last key hold whatever an earlier user left
+                    const int ge = ring0 + pos_v<C::LA>(n_blocks - 1, n_blocks);
+                    ok = warp_wait(b_tail, tails0 & 1, abort_f, a.status);
+                    if (ok) {
+                        uint8_t* v = sm + C::KV_OFF + (ge % C::STAGES) * C::TILE;
+                        for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
+                            const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
+                            *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
+                                                      (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_fix);
+                    }
+                }
+                // everything that was started lands before the piece ends (a stage that
+                // the other warp has filled since says so by itself)
+                for (int j = max(0, sent - DEPTH); j < sent; j++) {
+                    const int e = kv ? pos_v<C::LA>(j, n_blocks) : pos_k<C::LA>(j);
                     const int ge = ring0 + e;
-                    drain_bar(E4M3 ? &b_code[ge % depth] : &b_full[ge % depth], (ge / depth) & 1,
-                              a.status);
+                    if (!ok || e >= n_ring - DEPTH)
+                        drain_bar(&arrived[ge % DEPTH], (ge / DEPTH) & 1, a.status);
                 }
             } else if (warp == 1 && ok) {
                 constexpr uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
@@ -401,29 +424,13 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                     if (ok && more && elect_one()) tc_commit(&b_empty[stage_of(ek)]);
                     __syncwarp();
                 }
-            } else if (warp == 2 && !E4M3 && tail < KB && ok) {
-                // the V rows behind the last key hold whatever an earlier user left
-                const int ge = ring0 + pos_v<C::LA>(n_blocks - 1, n_blocks);
-                ok = warp_wait(b_tail, tails0 & 1, abort_f, a.status);
-                if (ok) {
-                    uint8_t* v = sm + C::KV_OFF + (ge % C::STAGES) * C::TILE;
-                    for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
-                        const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
-                        *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
-                                                  (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_fix);
-                }
             }
             if (!PAIR) __syncthreads();
-            w.done();
             __syncthreads();
             if (*abort_f) ok = false;
         }
     } else if (E4M3 && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         const int tid = threadIdx.x - 384;
         constexpr int PIECES = KB * D / 16 / 128;  // 16-code pieces a thread has of a tile
         constexpr int RPP = 128 / PIECES;          // rows from a piece to the next
@@ -444,7 +451,8 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             (ch >> 2) * C::BLK + r_in * 128 + (uint32_t)((c0 ^ (r_in & 7)) << 4);
         const uint32_t dst1 =
             (ch >> 2) * C::BLK + r_in * 128 + (uint32_t)(((c0 + 1) ^ (r_in & 7)) << 4);
-        while (w.next(a)) {
+        for (int turn = 0; steps[turn & 1].more; turn++) {
+            const Step& w = steps[turn & 1];
             const int n_ring = 2 * w.n_blocks, ring0 = w.ring0;
             __syncthreads();
             for (int e = 0; e < n_ring && ok; e++) {
@@ -484,19 +492,16 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 }
             }
             if (!PAIR) __syncthreads();
-            w.done();
             __syncthreads();
             if (*abort_f) ok = false;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 192 : 208));
-        while (w.next(a)) {
-            const Seq& s = w.pc.s;
-            const Piece& pc = w.pc;
-            const int k0 = w.k0, n_blocks = w.n_blocks, blocks0 = w.blocks0;
-            const int(&nt)[2] = w.nt;
-            const int(&used0)[2] = w.used0;
-            const int rows = s.n * a.G, r0 = pc.tile * C::QT * 128;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 176 : 208));
+        for (int turn = 0; steps[turn & 1].more; turn++) {
+            const Step& w = steps[turn & 1];
+            {
+            const Seq s = w.pc.s;
+            const int h = w.pc.h, rows = w.rows, r0 = w.r0;
             // the queries, 128-byte swizzled; rows that do not exist are zero
             for (int x = threadIdx.x - 128; x < C::QT * 128 * (D / 8); x += 256) {
                 const int r = x / (D / 8), ch = x % (D / 8);
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 if (r0 + r < rows && ch * 8 < a.hd) {
                     const int t = (r0 + r) / a.G;
                     v = *reinterpret_cast<const uint4*>(a.q + (s.q0 + t) * a.q_tok +
-                                                        (pc.h * a.G + (r0 + r) % a.G) * a.q_head +
+                                                        (h * a.G + (r0 + r) % a.G) * a.q_head +
                                                         ch * 8);
                 }
                 if (E4M3) {  // D / 8 lanes have a row
@@ -523,6 +528,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 *reinterpret_cast<uint4*>(sm + C::Q_OFF + (r >> 7) * C::TILE + (ch >> 3) * C::BLK +
                                           (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
             }
+            }
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             __syncthreads();
 
@@ -533,9 +539,12 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
                 const uint32_t tm_s = tmem + lanes + TM_S + 128 * t;
                 const uint32_t tm_o = tmem + lanes + TM_O + 128 * t;
-                const int row = r0 + (PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane;
-                const bool live = row < rows;
-                const RowView view = row_view(a, s, min(row, rows - 1) / a.G);
+                const int row = w.r0 + (PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane;
+                const bool live = row < w.rows;
+                const bool idle = !__any_sync(0xffffffffu, live);  // none of the warp's rows is
+                const RowView view = row_view(a, w.pc.s, min(row, w.rows - 1) / a.G);
+                const int nt = w.nt[t], n_blocks = w.n_blocks;
+                const int k0 = w.k0, blocks0 = w.blocks0, used0 = w.used0[t];
                 float c = a.scale_log2;
                 if (E4M3)
                     c *= exp2f((float)reinterpret_cast<const int8_t*>(
@@ -544,10 +553,10 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 for (int j = PAIR ? 0 : t, i = 0; j < n_blocks; j += PAIR ? 1 : 2, i++) {
                     const int gb = blocks0 + j, sl = gb % SCN;
                     ok = warp_wait(&b_sc[sl], (gb / SCN) & 1, abort_f, a.status);
-                    if (ok && nt[t] > 0)
-                        ok = warp_wait(&b_s[t], (used0[t] + i) & 1, abort_f, a.status);
+                    if (ok && nt > 0)
+                        ok = warp_wait(&b_s[t], (used0 + i) & 1, abort_f, a.status);
                     if (!ok) break;
-                    if (nt[t] > 0) {
+                    if (nt > 0 && !idle) {
                         tc_fence_after();
                         const float* sc =
                             reinterpret_cast<const float*>(sm + C::SC_OFF + sl * C::SC_BYTES);
@@ -559,10 +568,10 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                                              j0 + KB > view.pre || j0 <= view.lo);
                         uint32_t vis[4] = {};
                         if (any) {
-                            vis[0] = real.x & seen_word(view, s.n, j0);
-                            vis[1] = real.y & seen_word(view, s.n, j0 + 32);
-                            vis[2] = real.z & seen_word(view, s.n, j0 + 64);
-                            vis[3] = real.w & seen_word(view, s.n, j0 + 96);
+                            vis[0] = real.x & seen_word(view, w.pc.s.n, j0);
+                            vis[1] = real.y & seen_word(view, w.pc.s.n, j0 + 32);
+                            vis[2] = real.z & seen_word(view, w.pc.s.n, j0 + 64);
+                            vis[3] = real.w & seen_word(view, w.pc.s.n, j0 + 96);
                         }
                         float vmax = 0.0f;
                         if (E4M3) {
@@ -579,25 +588,29 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                             for (int off = 16; off > 0; off >>= 1)
                                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
                         }
-                        if (any)
-                            softmax_block<D, E4M3, true>(tm_s, tm_o, i > 0, vis, c, sc + 4, sc + 132,
-                                                         vmax, live, st);
+                        if (E4M3 && any)
+                            softmax_block_scaled<D, true>(tm_s, tm_o, i > 0, vis, c, sc + 4,
+                                                          sc + 132, vmax, live, st);
+                        else if (E4M3)
+                            softmax_block_scaled<D, false>(tm_s, tm_o, i > 0, vis, c, sc + 4,
+                                                           sc + 132, vmax, live, st);
+                        else if (any)
+                            softmax_block<D, true>(tm_s, tm_o, i > 0, vis, c, live, st);
                         else
-                            softmax_block<D, E4M3, false>(tm_s, tm_o, i > 0, vis, c, sc + 4, sc + 132,
-                                                          vmax, live, st);
+                            softmax_block<D, false>(tm_s, tm_o, i > 0, vis, c, live, st);
                         tc_fence_before();
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        if (nt[t] > 0) mbar_arrive(&b_p[t]);
+                        if (nt > 0) mbar_arrive(&b_p[t]);
                         mbar_arrive(&b_sce[sl]);
                     }
                 }
-                if (nt[t] > 0 && ok) ok = warp_wait(&b_o[t], w.ends0[t] & 1, abort_f, a.status);
+                if (nt > 0 && ok) ok = warp_wait(&b_o[t], w.ends0[t] & 1, abort_f, a.status);
                 tc_fence_after();
                 end_m = st.reference(c);
                 end_l = st.l;
-                if (!PAIR && t == 1 && nt[1] > 0 && ok) {
+                if (!PAIR && t == 1 && nt > 0 && ok) {
                     // to the other stream, through the ring (nothing of it is in use)
                     float* x = reinterpret_cast<float*>(sm + C::KV_OFF) +
                                (32 * (warp & 3) + lane) * C::XP;
@@ -619,13 +632,13 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             if (warp < (PAIR ? 12 : 8) && ok) {
                 const int t = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
                 const uint32_t tm_o = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_O + 128 * t;
-                const int row = r0 + 128 * t + row_in;
-                const bool live = row < rows;
-                const int tok = min(row, rows - 1) / a.G, head = pc.h * a.G + min(row, rows - 1) % a.G;
-                const int64_t at = (int64_t)(s.q0 + tok) * a.nh + head;
-                const bool whole = is_whole(pc);
+                const int row = w.r0 + 128 * t + row_in;
+                const bool live = row < w.rows;
+                const int tok = min(row, w.rows - 1) / a.G, head = w.pc.h * a.G + min(row, w.rows - 1) % a.G;
+                const int64_t at = (int64_t)(w.pc.s.q0 + tok) * a.nh + head;
+                const bool whole = is_whole(w.pc);
                 const float* x = reinterpret_cast<const float*>(sm + C::KV_OFF) + row_in * C::XP;
-                const bool both = !PAIR && nt[1] > 0;
+                const bool both = !PAIR && w.nt[1] > 0;
                 float f = 1.0f, fx = 0.0f, m = end_m, l = end_l;
                 if (both) {
                     m = fmaxf(end_m, x[D]);
@@ -640,9 +653,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                     f *= end.factor;
                     fx *= end.factor;
                 }
-                const int64_t slot = slot_of(pc) * a.tile_rows + 128 * t + row_in;
+                const int64_t slot = slot_of(w.pc) * a.tile_rows + 128 * t + row_in;
                 if (live && !whole) a.part_ml[slot] = make_float2(m, l);
-                if (nt[t] > 0) {
+                if (w.nt[t] > 0) {
     #pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
                         uint32_t ov[16];
@@ -679,7 +692,6 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             }
-            w.done();
             // tensor memory, the queries and the ring are free for the next piece
             tc_fence_before();
             __syncthreads();
