@@ -296,62 +296,52 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
     tc_wait_st();
 }
 
-// The scaled form (e4m3 caches), whose warps share registers and issue slots with
-// the widening ones: one pass, 32 keys at a time, the next 32 on their way; a
-// reference that moves within the block takes the weights written before along.
-// vmax: the largest vs of the block.
+// The scaled form (e4m3 caches).  vmax: the largest vs of the block.
 template <int D, bool MASKED>
 __device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_o, bool have_o,
                                                      const uint32_t (&vis)[4], float c,
                                                      const float* ks, const float* vs, float vmax,
                                                      bool live, RowState& st) {
-    uint64_t sum[2] = {0, 0};
-    // the reference, times c, and lr: what a score's exponent is reduced by
-    float base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
-    bool vmove = vmax > st.vlim;
-    auto chunk = [&](uint32_t(&s)[32], int i, uint32_t seen) {
-        prepare32<true, MASKED>(s, ks + 32 * i, seen);
-        const float top = max32(s);
-        const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
-        if (__any_sync(0xffffffffu, move || vmove)) {
-            float shift = move ? (st.m - top) * c : 0.0f;
-            if (move) st.m = top;
-            if (vmove) {
-                const float lr = scale_exponent(vmax);
-                shift += st.lr - lr;
-                st.lr = lr;
-                st.vlim = ex2(lr + 8.0f);
-                vmove = false;
-            }
-            const float f = ex2(shift);
-            st.l *= f;
-            sum[0] = mul2(sum[0], f2(f, f));
-            sum[1] = mul2(sum[1], f2(f, f));
-            if (have_o || i > 0) rescale<D, true>(tm_s, i, tm_o, have_o, f);
-            base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
-        }
-        float reduced = base;
-        if (fabsf(base) > 0x1p22f) {  // (as above)
+    uint32_t s[4][32];
+    float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 32; e++) s[e] = __float_as_uint(u2f(s[e]) - st.m);
-            reduced = st.lr;
+    for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        prepare32<true, MASKED>(s[i], ks + 32 * i, vis[i]);
+        top = fmaxf(top, max32(s[i]));
+        asm volatile("" ::: "memory");
+    }
+    const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
+    const bool vmove = vmax > st.vlim;
+    if (__any_sync(0xffffffffu, move || vmove)) {
+        float shift = move ? (st.m - top) * c : 0.0f;
+        if (move) st.m = top;
+        if (vmove) {
+            const float lr = scale_exponent(vmax);
+            shift += st.lr - lr;
+            st.lr = lr;
+            st.vlim = ex2(lr + 8.0f);
         }
-        // (the weights of 32 keys take 16 columns, so they never reach scores that
-        // are still to be read)
+        const float f = ex2(shift);
+        st.l *= f;
+        if (have_o) rescale<D, true>(tm_s, 0, tm_o, true, f);
+    }
+    float base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
+    if (fabsf(base) > 0x1p22f) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        base = st.lr;
+    }
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
         uint32_t pk[16];
-        weights32<true, MASKED>(s, pk, c, reduced, vs + 32 * i, seen, sum);
+        weights32<true, MASKED>(s[i], pk, c, base, vs + 32 * i, vis[i], sum);
         tc_st16(tm_s + 16 * i, pk);
-    };
-    uint32_t a[32], b[32];
-    tc_ld32(tm_s, a);
-#pragma unroll 1
-    for (int i = 0; i < 4; i += 2) {
-        wait_ld32(a);
-        tc_ld32(tm_s + 32 * (i + 1), b);
-        chunk(a, i, i ? vis[2] : vis[0]);
-        wait_ld32(b);
-        if (i == 0) tc_ld32(tm_s + 64, a);
-        chunk(b, i + 1, i ? vis[3] : vis[1]);
     }
     float x, y;
     unf2(add2(sum[0], sum[1]), x, y);

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     bool ok = true;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(88));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 72 : 88));
         for (int turn = 0; steps[turn & 1].more; turn++) {
             const Step& w = steps[turn & 1];
             const int32_t* table = a.table + (int64_t)w.pc.b * a.max_pages;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             if (*abort_f) ok = false;
         }
     } else if (E4M3 && warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         const int tid = threadIdx.x - 384;
         constexpr int PIECES = KB * D / 16 / 128;  // 16-code pieces a thread has of a tile
         constexpr int RPP = 128 / PIECES;          // rows from a piece to the next
@@ -459,29 +459,33 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const int ge = ring0 + e, cs = ge % C::CODES, st = ge % C::STAGES;
                 ok = warp_wait(&b_code[cs], (ge / C::CODES) & 1, abort_f, a.status);
                 if (!ok) break;
-                uint4 w[PIECES];
-                const uint8_t* from = sm + C::C_OFF + cs * C::CTILE + src_off;
-#pragma unroll
-                for (int x = 0; x < PIECES; x++)
-                    w[x] = in_row ? *reinterpret_cast<const uint4*>(from + x * RPP * a.hd)
-                                  : make_uint4(0, 0, 0, 0);
-                __syncwarp();
                 if (ge >= C::STAGES) {
                     ok = warp_wait(&b_empty[st], ((ge / C::STAGES) - 1) & 1, abort_f, a.status);
                     if (!ok) break;
                 }
+                const uint8_t* from = sm + C::C_OFF + cs * C::CTILE + src_off;
                 uint8_t* to = sm + C::KV_OFF + st * C::TILE;
+                // four pieces at a time: the widening warps live on few registers
+#pragma unroll 1
+                for (int x0 = 0; x0 < PIECES; x0 += 4) {
+                    uint4 w[4];
 #pragma unroll
-                for (int x = 0; x < PIECES; x++) {
-                    uint32_t out[8];
-                    e4m3x4_to_f16(w[x].x, out[0], out[1]);
-                    e4m3x4_to_f16(w[x].y, out[2], out[3]);
-                    e4m3x4_to_f16(w[x].z, out[4], out[5]);
-                    e4m3x4_to_f16(w[x].w, out[6], out[7]);
-                    *reinterpret_cast<uint4*>(to + dst0 + x * RPP * 128) =
-                        make_uint4(out[0], out[1], out[2], out[3]);
-                    *reinterpret_cast<uint4*>(to + dst1 + x * RPP * 128) =
-                        make_uint4(out[4], out[5], out[6], out[7]);
+                    for (int x = 0; x < 4; x++)
+                        w[x] = in_row
+                                   ? *reinterpret_cast<const uint4*>(from + (x0 + x) * RPP * a.hd)
+                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        uint32_t out[8];
+                        e4m3x4_to_f16(w[x].x, out[0], out[1]);
+                        e4m3x4_to_f16(w[x].y, out[2], out[3]);
+                        e4m3x4_to_f16(w[x].z, out[4], out[5]);
+                        e4m3x4_to_f16(w[x].w, out[6], out[7]);
+                        *reinterpret_cast<uint4*>(to + dst0 + (x0 + x) * RPP * 128) =
+                            make_uint4(out[0], out[1], out[2], out[3]);
+                        *reinterpret_cast<uint4*>(to + dst1 + (x0 + x) * RPP * 128) =
+                            make_uint4(out[4], out[5], out[6], out[7]);
+                    }
                 }
                 // (the codes have been read: the copies that follow wait for this)
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             if (*abort_f) ok = false;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 176 : 208));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 200 : 208));
         for (int turn = 0; steps[turn & 1].more; turn++) {
             const Step& w = steps[turn & 1];
             {
