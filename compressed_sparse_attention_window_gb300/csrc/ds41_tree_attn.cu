@@ -388,26 +388,32 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     pdl_trigger();
 }
 
-// One CTA per (token, head): where its unit was shared, the parts joined and the
-// sink added.  Warp w takes the parts w, w + 4, ..., four rows in flight.
+// (token, head) by (token, head): where its unit was shared, the parts joined and
+// the sink added.  PER warps take a row, every PER-th part each, eight parts' rows
+// in flight: one where there are rows enough to fill the GPU (16384 rows of 4
+// parts: 36 us with four warps each, 16 with one), four for a handful of rows of
+// many parts (32 rows of 57: 27 us a call with one, 20 with four).
+template <int PER>
 __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    __shared__ float4 acc[WARPS][32];
+    __shared__ float4 acc[PER > 1 ? WARPS : 1][32];
     __shared__ float sums[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int id = PER > 1 ? (int)blockIdx.x : (int)blockIdx.x * WARPS + warp;
     const Seq s = load_seq(a, blockIdx.y);
-    if (!s.ok || (int)blockIdx.x >= s.n * a.nh) return;
-    const int t = (int)blockIdx.x / a.nh, head = (int)blockIdx.x % a.nh;
+    if (!s.ok || id >= s.n * a.nh) return;
+    const int t = id / a.nh, head = id % a.nh;
     const int r = t * a.G + head % a.G;
     const int2 ends =
         a.ends[((int64_t)blockIdx.y * a.kvh + head / a.G) * a.row_tiles + r / a.tile_rows];
     if (ends.x == ends.y) return;  // the one worker has written the output
     const int n = ends.y - ends.x + 1;
-    auto index = [&](int x) {
-        return (2 * (int64_t)(ends.x + x) + (x == 0 ? 1 : 0)) * a.tile_rows + r % a.tile_rows;
-    };
-    const int64_t at = (int64_t)s.q0 * a.nh + blockIdx.x;
+    // part 0 is its worker's slot 1, the others are slot 0
+    const int64_t row0 = (2 * (int64_t)ends.x + 1) * a.tile_rows + r % a.tile_rows;
+    const int64_t step = 2 * (int64_t)a.tile_rows, row1 = row0 - a.tile_rows;
+    auto index = [&](int x) { return x == 0 ? row0 : row1 + x * step; };
+    const int64_t at = (int64_t)s.q0 * a.nh + id;
     float m = -INFINITY, l = 0.0f;
     for (int x = lane; x < n; x += 32) m = fmaxf(m, a.part_ml[index(x)].x);
 #pragma unroll
@@ -415,8 +421,8 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
     const float base = m == -INFINITY ? 0.0f : m;
     float4 v = make_float4(0, 0, 0, 0);
     const bool mine = lane * 4 < a.hd;
-#pragma unroll 4
-    for (int x = warp; x < n; x += WARPS) {
+#pragma unroll 8
+    for (int x = PER > 1 ? warp : 0; x < n; x += PER) {
         const float2 ml = a.part_ml[index(x)];
         const float4 p =
             mine ? *reinterpret_cast<const float4*>(a.part + index(x) * a.hd + lane * 4)
@@ -428,17 +434,20 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
         v.z += f * p.z;
         v.w += f * p.w;
     }
-    acc[warp][lane] = v;
-    if (lane == 0) sums[warp] = l;
-    __syncthreads();
-    if (warp > 0) return;
-    l = sums[0] + sums[1] + sums[2] + sums[3];
+    if (PER > 1) {
+        acc[warp][lane] = v;
+        if (lane == 0) sums[warp] = l;
+        __syncthreads();
+        if (warp > 0) return;
+        l = sums[0];
 #pragma unroll
-    for (int w = 1; w < WARPS; w++) {
-        v.x += acc[w][lane].x;
-        v.y += acc[w][lane].y;
-        v.z += acc[w][lane].z;
-        v.w += acc[w][lane].w;
+        for (int w = 1; w < PER; w++) {
+            l += sums[w];
+            v.x += acc[w][lane].x;
+            v.y += acc[w][lane].y;
+            v.z += acc[w][lane].z;
+            v.w += acc[w][lane].w;
+        }
     }
     const tc::RowEnd end = tc::row_end(m, l, a.sink ? a.sink[head] : -INFINITY);
     if (a.lse && lane == 0) a.lse[at] = end.lse;
@@ -579,6 +588,10 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
             return rc;
     }
     if (pl.workers == 1) return DS41_OK;  // every unit was whole
-    return launch_pdl(tree::tree_join_kernel, dim3((unsigned)(max_q * nh), (unsigned)B),
+    const int64_t rows = max_q * nh;
+    const bool few_rows = rows * B <= 8 * (int64_t)device_sm_count();
+    return launch_pdl(few_rows ? tree::tree_join_kernel<tree::WARPS> : tree::tree_join_kernel<1>,
+                      dim3((unsigned)(few_rows ? rows : (rows + tree::WARPS - 1) / tree::WARPS),
+                           (unsigned)B),
                       dim3(tree::NT), 0, st, name, a);
 }

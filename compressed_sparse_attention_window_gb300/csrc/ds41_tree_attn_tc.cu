@@ -504,34 +504,49 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
         for (int turn = 0; steps[turn & 1].more; turn++) {
             const Step& w = steps[turn & 1];
             {
-            const Seq s = w.pc.s;
-            const int h = w.pc.h, rows = w.rows, r0 = w.r0;
-            // the queries, 128-byte swizzled; rows that do not exist are zero
-            for (int x = threadIdx.x - 128; x < C::QT * 128 * (D / 8); x += 256) {
-                const int r = x / (D / 8), ch = x % (D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r0 + r < rows && ch * 8 < a.hd) {
-                    const int t = (r0 + r) / a.G;
-                    v = *reinterpret_cast<const uint4*>(a.q + (s.q0 + t) * a.q_tok +
-                                                        (h * a.G + (r0 + r) % a.G) * a.q_head +
-                                                        ch * 8);
+                // the queries, 128-byte swizzled; rows that do not exist are zero.  A
+                // thread has one 16-byte piece of every (256 * 8 / D)-th row, four in
+                // flight
+                constexpr int CPR = D / 8, STEP = 256 / CPR;
+                const int tid = threadIdx.x - 128, ch = tid % CPR;
+                const uint16_t* q0 =
+                    a.q + w.pc.s.q0 * a.q_tok + (int64_t)w.pc.h * a.G * a.q_head + ch * 8;
+                const int rows = w.rows - w.r0;
+#pragma unroll 1
+                for (int k = tid / CPR; k < C::QT * 128; k += 4 * STEP) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const int r = k + u * STEP;
+                        const uint32_t rr = (uint32_t)(w.r0 + r), t = rr / (uint32_t)a.G;
+                        v[u] = make_uint4(0, 0, 0, 0);
+                        if (r < rows && ch * 8 < a.hd)
+                            v[u] = *reinterpret_cast<const uint4*>(q0 + t * a.q_tok +
+                                                                   (rr - t * a.G) * a.q_head);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        const int r = k + u * STEP;
+                        if (E4M3) {  // D / 8 lanes have a row
+                            const uint32_t m2 =
+                                __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu),
+                                         __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu));
+                            uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+                            for (int off = D / 16; off > 0; off >>= 1)
+                                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+                            const int e = query_exponent(mb);
+                            const float down = exp2f((float)-e);
+                            v[u] = make_uint4(
+                                bf16x2_to_f16x2(v[u].x, down), bf16x2_to_f16x2(v[u].y, down),
+                                bf16x2_to_f16x2(v[u].z, down), bf16x2_to_f16x2(v[u].w, down));
+                            if (ch == 0) reinterpret_cast<int8_t*>(sm + C::QE_OFF)[r] = (int8_t)e;
+                        }
+                        *reinterpret_cast<uint4*>(sm + C::Q_OFF + (r >> 7) * C::TILE +
+                                                  (ch >> 3) * C::BLK + (r & 127) * 128 +
+                                                  (((ch & 7) ^ (r & 7)) << 4)) = v[u];
+                    }
                 }
-                if (E4M3) {  // D / 8 lanes have a row
-                    const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                    uint32_t mb = max(m2 & 0xffffu, m2 >> 16);
-    #pragma unroll
-                    for (int off = D / 16; off > 0; off >>= 1)
-                        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
-                    const int e = query_exponent(mb);
-                    const float down = exp2f((float)-e);
-                    v = make_uint4(bf16x2_to_f16x2(v.x, down), bf16x2_to_f16x2(v.y, down),
-                                   bf16x2_to_f16x2(v.z, down), bf16x2_to_f16x2(v.w, down));
-                    if (ch == 0) reinterpret_cast<int8_t*>(sm + C::QE_OFF)[r] = (int8_t)e;
-                }
-                *reinterpret_cast<uint4*>(sm + C::Q_OFF + (r >> 7) * C::TILE + (ch >> 3) * C::BLK +
-                                          (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-            }
             }
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             __syncthreads();
