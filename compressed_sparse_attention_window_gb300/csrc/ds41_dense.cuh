@@ -3,7 +3,10 @@
 // the e4m3 codec of its rows.  Nothing here is shared with the CPU oracle.
 #pragma once
 
+#include <atomic>
+
 #include "ds41_common.cuh"
+#include "ds41_internal.cuh"
 
 namespace ds41 {
 
@@ -31,6 +34,29 @@ inline bool good_strides(int64_t tok, int64_t head, int64_t hd) {
 }
 inline bool aligned_to(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Host: a kernel's dynamic shared memory limit, raised once per device.
+template <auto KERNEL>
+int allow_smem(int bytes, const char* what) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (int rc = cuda_check(cudaGetDevice(&dev), what)) return rc;
+    if (dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1)) return DS41_OK;
+    if (int rc = cuda_check(
+            cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), what))
+        return rc;
+    if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return DS41_OK;
+}
+// Host: the current device's SM count, looked up once per device.
+inline int sm_count_once() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return device_sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) known[dev].store(n = device_sm_count(), std::memory_order_relaxed);
+    return n;
 }
 
 // First element of row `off` of page `pg`, head `h`, counted in elements.

@@ -470,18 +470,13 @@ int make_map_heads(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* m, const 
 
 using namespace ds41;
 
-extern "C" size_t ds41_prompt_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t,
-                                                   int64_t) {
-    return 0;
-}
-
 extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
                                     const ds41_bf16* k, int64_t k_tok, int64_t k_head,
                                     const ds41_bf16* v, int64_t v_tok, int64_t v_head,
                                     const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq,
                                     int64_t Tk, int64_t max_q, int64_t nh, int64_t kvh, int64_t hd,
                                     float scale, int64_t window, const float* sink, ds41_bf16* o,
-                                    float* lse, void* ws, size_t ws_bytes, ds41_stream_t stream) {
+                                    float* lse, ds41_stream_t stream) {
     const char* name = "ds41_prompt_attn_fwd";
     if (int rc = check_heads(name, nh, kvh, hd, scale, window)) return rc;
     const int64_t lim = int64_t(1) << 31;
@@ -546,9 +541,8 @@ extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q
                  (long long)B, (long long)kvh);
     auto kern = hd <= 64 ? pa::prompt_attn_kernel<64> : pa::prompt_attn_kernel<128>;
     const size_t smem = hd <= 64 ? pa::Cfg<64>::SMEM : pa::Cfg<128>::SMEM;
-    if (int rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem),
-                            name))
+    if (int rc = hd <= 64 ? allow_smem<pa::prompt_attn_kernel<64>>((int)smem, name)
+                          : allow_smem<pa::prompt_attn_kernel<128>>((int)smem, name))
         return rc;
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(pa::THREADS), smem, (cudaStream_t)stream,
                       name, mq, mk, mv, p);

@@ -487,6 +487,14 @@ Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kv
     return p;
 }
 
+template <int HD, bool E4M3>
+int launch_few(const Args& a, const char* name, cudaStream_t st) {
+    constexpr int smem = Cfg<HD, E4M3>::BYTES;
+    if (int rc = allow_smem<tree_few_kernel<HD, E4M3>>(smem, name)) return rc;
+    return launch_pdl(tree_few_kernel<HD, E4M3>, dim3((unsigned)a.workers), dim3(NT), smem, st,
+                      name, a);
+}
+
 }  // namespace tree
 }  // namespace ds41
 
@@ -498,7 +506,7 @@ extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t 
     if (B < 1 || Tq < 1 || max_q < 1 || max_q > 256 || max_len < 0 || kvh < 1 || nh < kvh ||
         nh % kvh || hd < 1 || window < 0)
         return 0;
-    return tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, device_sm_count()).bytes();
+    return tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, sm_count_once()).bytes();
 }
 
 extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
@@ -535,8 +543,8 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
                  DS41_E_ARG, "%s: q and o must be 16-byte aligned", name);
     DS41_REQUIRE(good_strides(q_tok, q_head, hd), DS41_E_ARG,
                  "%s: strides must be multiples of 8 and at least hd", name);
-    const tree::Plan pl =
-        tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, device_sm_count());
+    const int sms = sm_count_once();
+    const tree::Plan pl = tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, sms);
     DS41_REQUIRE(ws && aligned16(ws) && ws_bytes >= pl.bytes(), DS41_E_WORKSPACE,
                  "%s: needs %zu bytes of workspace, got %zu", name, pl.bytes(), ws ? ws_bytes : 0);
     a.q = q;
@@ -574,22 +582,16 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
     if (pl.many) {
         if (int rc = tree::launch_many(a, name, st)) return rc;
     } else {
-        using namespace tree;
         const bool e = fmt == DS41_KV_E4M3;
-        auto kern = e ? (hd <= 64 ? tree_few_kernel<64, true> : tree_few_kernel<128, true>)
-                      : (hd <= 64 ? tree_few_kernel<64, false> : tree_few_kernel<128, false>);
-        const int smem = e ? (hd <= 64 ? Cfg<64, true>::BYTES : Cfg<128, true>::BYTES)
-                           : (hd <= 64 ? Cfg<64, false>::BYTES : Cfg<128, false>::BYTES);
-        if (int rc = cuda_check(
-                cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                name))
-            return rc;
-        if (int rc = launch_pdl(kern, dim3((unsigned)pl.workers), dim3(NT), smem, st, name, a))
+        if (int rc = e ? (hd <= 64 ? tree::launch_few<64, true>(a, name, st)
+                                   : tree::launch_few<128, true>(a, name, st))
+                       : (hd <= 64 ? tree::launch_few<64, false>(a, name, st)
+                                   : tree::launch_few<128, false>(a, name, st)))
             return rc;
     }
     if (pl.workers == 1) return DS41_OK;  // every unit was whole
     const int64_t rows = max_q * nh;
-    const bool few_rows = rows * B <= 8 * (int64_t)device_sm_count();
+    const bool few_rows = rows * B <= 8 * (int64_t)sms;
     return launch_pdl(few_rows ? tree::tree_join_kernel<tree::WARPS> : tree::tree_join_kernel<1>,
                       dim3((unsigned)(few_rows ? rows : (rows + tree::WARPS - 1) / tree::WARPS),
                            (unsigned)B),

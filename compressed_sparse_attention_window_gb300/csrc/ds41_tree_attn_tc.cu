@@ -756,10 +756,7 @@ int launch_many_as(const Args& a, const char* name, cudaStream_t st) {
         if (int rc = make_map_pages(enc, &mv, a.kv.v, a.kv)) return rc;
     }
     auto kern = tree_many_kernel<D, E4M3, PAIR>;
-    if (int rc = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)C::SMEM),
-                            name))
-        return rc;
+    if (int rc = allow_smem<tree_many_kernel<D, E4M3, PAIR>>((int)C::SMEM, name)) return rc;
     return launch_pdl(kern, dim3((unsigned)a.workers), dim3(C::THREADS), C::SMEM, st, name, mk, mv,
                       a);
 }

@@ -75,9 +75,8 @@ SIGNATURES = {
                             + [_I64] * 5 + [_P]),
     "ds41_kv_cache_read": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _P,
                                           _I64, _P, _P, _I64, _P, _P, _I64, _P]),
-    "ds41_prompt_attn_workspace_bytes": (_SZ, [_I64] * 6),
     "ds41_prompt_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P]
-                             + [_I64] * 7 + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
+                             + [_I64] * 7 + [_F, _I64, _P, _P, _P, _P]),
     "ds41_tree_attn_workspace_bytes": (_SZ, [_I64] * 8 + [ctypes.c_int]),
     "ds41_tree_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64, _I64,
                                           _P, _I64, _P, _P, _P, _I64] + [_I64] * 7
@@ -123,7 +122,8 @@ def _call(name: str, *args) -> None:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    # the handle alone: building a Stream object around it takes 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "") -> Optional[int]:
@@ -750,41 +750,48 @@ def make_kv_cache(n_pages: int, kvh: int, page: int, hd: int, e4m3: bool = True,
     return KvCache(k, v, ks, vs)
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    """The call runs on the current device's stream: every tensor is there."""
+# The checks below run before every call, some of which take 3 us on the device, so
+# they are written for few Python operations.
+_F32, _I32T, _I64T, _E4M3 = torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
+
+
+def _here(dev: torch.device) -> None:
+    """The call runs on the current device's stream: the tensors are there."""
     if dev.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got one on {dev}")
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}: the call runs on its stream")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _shape(name: str, t: torch.Tensor, want, dtype) -> Optional[int]:
-    """The pointer of a contiguous tensor of this shape and type (None for None)."""
+def _arg(name: str, t: Optional[torch.Tensor], dev, shape, dtype) -> Optional[int]:
+    """The pointer of a contiguous tensor of this shape and type on this device
+    (None for None)."""
     if t is None:
         return None
-    if t.shape != want or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype} {tuple(want)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
         raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
 
 
-def _heads(name: str, t: torch.Tensor, dense: bool = False):
+def _heads(name: str, t: torch.Tensor, dev, hd: int, dense: bool = False):
     """(pointer, token stride, head stride) of a bf16 tensor [tokens, heads, hd]
     whose last dimension is dense (with ``dense``: the heads too)."""
-    if t.dim() != 3 or t.dtype != _BF:
-        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, hd], got {t.dtype} "
+    if t.dim() != 3 or t.dtype != _BF or t.shape[2] != hd:
+        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, {hd}], got {t.dtype} "
                          f"{tuple(t.shape)}")
-    n, h, hd = t.shape
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     tok, head, one = t.stride()
-    if h == 1 or n == 0:
-        head = hd
-    if n <= 1:  # a stride that no address depends on
-        tok = h * hd if head == hd else max(hd, 8)
+    n, h, _ = t.shape
+    if n <= 1 or h == 1:  # a stride that no address depends on
+        head = hd if h == 1 or n == 0 else head
+        tok = (h * hd if head == hd else hd) if n <= 1 else tok
     if (one != 1 and hd > 1) or (dense and head != hd):
         raise ValueError(f"{name}: strides {t.stride()}: the last dimension"
                          + (" and the heads" if dense else "") + " must be dense")
@@ -793,38 +800,37 @@ def _heads(name: str, t: torch.Tensor, dense: bool = False):
 
 def _cache_args(c: KvCache, dev):
     """The cache's arguments of the C calls, its layout checked; and kvh, page, hd."""
-    if c.k.dim() != 4:
-        raise ValueError(f"cache: expected [n_pages, kvh, page, hd], got {tuple(c.k.shape)}")
-    n_pages, kvh, page, hd = c.k.shape
-    e4m3 = c.k.dtype == torch.float8_e4m3fn
-    if not e4m3 and c.k.dtype != _BF:
-        raise ValueError(f"cache: expected bfloat16 or float8_e4m3fn, got {c.k.dtype}")
-    if e4m3 != (c.k_scales is not None) or e4m3 != (c.v_scales is not None):
+    k, v, ks, vs = c
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4:
+        raise ValueError(f"cache: expected [n_pages, kvh, page, hd], got {tuple(shape)}")
+    e4m3 = dtype == _E4M3
+    if not e4m3 and dtype != _BF:
+        raise ValueError(f"cache: expected bfloat16 or float8_e4m3fn, got {dtype}")
+    if e4m3 != (ks is not None) or e4m3 != (vs is not None):
         raise ValueError("cache: an e4m3 cache has k_scales and v_scales, a bf16 cache none")
-    for name, t in zip(c._fields, c):
-        if t is not None and t.device != dev:
-            raise ValueError(f"cache.{name} is on {t.device}, expected {dev}")
-    want = (n_pages, kvh, page)
-    return (_shape("cache.k", c.k, c.k.shape, c.k.dtype),
-            _shape("cache.v", c.v, c.k.shape, c.k.dtype),
-            _shape("cache.k_scales", c.k_scales, want, torch.float32),
-            _shape("cache.v_scales", c.v_scales, want, torch.float32),
-            1 if e4m3 else 0, n_pages, page), kvh, page, hd
+    n_pages, kvh, page, hd = shape
+    kp, vp = _arg("cache.k", k, dev, shape, dtype), _arg("cache.v", v, dev, shape, dtype)
+    if not e4m3:
+        return (kp, vp, None, None, 0, n_pages, page), kvh, page, hd
+    rows = (n_pages, kvh, page)
+    return (kp, vp, _arg("cache.k_scales", ks, dev, rows, _F32),
+            _arg("cache.v_scales", vs, dev, rows, _F32), 1, n_pages, page), kvh, page, hd
 
 
 def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """ds41_kv_cache_write: the rows k, v [n, kvh, hd] bf16 (heads dense, any
     token stride) into the cache's slots [n] int64 (-1: not written)."""
     dev = k.device
-    _same_device(dev, v=v, slots=slots)
+    _here(dev)
     c, kvh, page, hd = _cache_args(cache, dev)
     n = k.shape[0]
     if k.shape != (n, kvh, hd) or v.shape != k.shape:
         raise ValueError(f"k, v: expected {(n, kvh, hd)}, got {tuple(k.shape)}, {tuple(v.shape)}")
-    kp, k_tok, _ = _heads("k", k, dense=True)
-    vp, v_tok, _ = _heads("v", v, dense=True)
-    _call("ds41_kv_cache_write", kp, k_tok, vp, v_tok, _shape("slots", slots, (n,), torch.int64),
-          *c, kvh, hd, n, _stream())
+    kp, k_tok, _ = _heads("k", k, dev, hd, dense=True)
+    vp, v_tok, _ = _heads("v", v, dev, hd, dense=True)
+    _call("ds41_kv_cache_write", kp, k_tok, vp, v_tok, _arg("slots", slots, dev, (n,), _I64T), *c,
+          kvh, hd, n, _stream())
 
 
 def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, rows: int,
@@ -835,19 +841,18 @@ def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, 
     position starts[b] (0 without starts); rows behind cu_k[-1] are left as
     they were (uninitialised in a new tensor)."""
     dev = cu_k.device
-    _same_device(dev, page_table=page_table, starts=starts, k=k, v=v)
+    _here(dev)
     c, kvh, page, hd = _cache_args(cache, dev)
     B = cu_k.shape[0] - 1
     if page_table.dim() != 2:
         raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
     mp = page_table.shape[1]
-    k = torch.empty(rows, kvh, hd, dtype=_BF, device=dev) if k is None else k
-    v = torch.empty(rows, kvh, hd, dtype=_BF, device=dev) if v is None else v
-    _call("ds41_kv_cache_read", *c, kvh, hd,
-          _shape("page_table", page_table, (B, mp), torch.int32), mp,
-          _shape("cu_k", cu_k, (B + 1,), torch.int32), _shape("starts", starts, (B,), torch.int32),
-          B, _shape("k", k, (rows, kvh, hd), _BF), _shape("v", v, (rows, kvh, hd), _BF), rows,
-          _stream())
+    shape = (rows, kvh, hd)
+    k = torch.empty(shape, dtype=_BF, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=_BF, device=dev) if v is None else v
+    _call("ds41_kv_cache_read", *c, kvh, hd, _arg("page_table", page_table, dev, (B, mp), _I32T),
+          mp, _arg("cu_k", cu_k, dev, (B + 1,), _I32T), _arg("starts", starts, dev, (B,), _I32T),
+          B, _arg("k", k, dev, shape, _BF), _arg("v", v, dev, shape, _BF), rows, _stream())
     return k, v
 
 
@@ -865,29 +870,26 @@ def _ws(need: int, ws: Optional[torch.Tensor], dev):
 def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
                     cu_k: torch.Tensor, max_q: int, scale: float,
                     sink: Optional[torch.Tensor] = None, window: int = 0,
-                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    o: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ds41_prompt_attn_fwd: causal attention of packed prompts, q [Tq, nh, hd]
     over k, v [Tk, kvh, hd] (any token and head strides that are multiples of
     8); returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
     dev = q.device
-    _same_device(dev, k=k, v=v, cu_q=cu_q, cu_k=cu_k, sink=sink, o=o, lse=lse)
-    qp, q_tok, q_head = _heads("q", q)
-    kp, k_tok, k_head = _heads("k", k)
-    vp, v_tok, v_head = _heads("v", v)
+    _here(dev)
     Tq, nh, hd = q.shape
-    Tk, kvh = k.shape[:2]
-    if k.shape[2] != hd or v.shape != k.shape:
-        raise ValueError(f"k, v: expected [Tk, kvh, {hd}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    Tk, kvh, _ = k.shape
+    qp, q_tok, q_head = _heads("q", q, dev, hd)
+    kp, k_tok, k_head = _heads("k", k, dev, hd)
+    vp, v_tok, v_head = _heads("v", v, dev, hd)
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected {tuple(k.shape)}, got {tuple(v.shape)}")
     B = cu_q.shape[0] - 1
-    o = torch.empty(Tq, nh, hd, dtype=_BF, device=dev) if o is None else o
-    need = load().ds41_prompt_attn_workspace_bytes(B, Tq, max_q, nh, kvh, hd)
-    ws = _ws(need, ws, dev)
+    o = torch.empty(q.shape, dtype=_BF, device=dev) if o is None else o
     _call("ds41_prompt_attn_fwd", qp, q_tok, q_head, kp, k_tok, k_head, vp, v_tok, v_head,
-          _shape("cu_q", cu_q, (B + 1,), torch.int32), _shape("cu_k", cu_k, (B + 1,), torch.int32),
-          B, Tq, Tk, max_q, nh, kvh, hd, scale, window, _shape("sink", sink, (nh,), torch.float32),
-          _shape("o", o, (Tq, nh, hd), _BF), _shape("lse", lse, (Tq, nh), torch.float32),
-          None if ws is None else ws.data_ptr(), need, _stream())
+          _arg("cu_q", cu_q, dev, (B + 1,), _I32T), _arg("cu_k", cu_k, dev, (B + 1,), _I32T), B,
+          Tq, Tk, max_q, nh, kvh, hd, scale, window, _arg("sink", sink, dev, (nh,), _F32),
+          _arg("o", o, dev, (Tq, nh, hd), _BF), _arg("lse", lse, dev, (Tq, nh), _F32), _stream())
     return o
 
 
@@ -903,13 +905,10 @@ def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, len
     sees (None: a chain; one token per sequence: plain decode).  Returns
     o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
     dev = q.device
-    _same_device(dev, page_table=page_table, lens=lens, cu_q=cu_q, mask=mask, sink=sink, o=o,
-                 lse=lse)
+    _here(dev)
     c, kvh, page, hd = _cache_args(cache, dev)
-    qp, q_tok, q_head = _heads("q", q)
-    Tq, nh = q.shape[:2]
-    if q.shape[2] != hd:
-        raise ValueError(f"q: expected [Tq, nh, {hd}], got {tuple(q.shape)}")
+    qp, q_tok, q_head = _heads("q", q, dev, hd)
+    Tq, nh, _ = q.shape
     B = cu_q.shape[0] - 1
     if page_table.dim() != 2:
         raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
@@ -919,14 +918,14 @@ def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, len
         if mask.dim() != 2:
             raise ValueError(f"mask: expected [Tq, words], got {tuple(mask.shape)}")
         words = mask.shape[1]
-    o = torch.empty(Tq, nh, hd, dtype=_BF, device=dev) if o is None else o
+    o = torch.empty(q.shape, dtype=_BF, device=dev) if o is None else o
     need = load().ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, window, c[4])
     ws = _ws(need, ws, dev)
     _call("ds41_tree_attn_fwd", qp, q_tok, q_head, *c,
-          _shape("page_table", page_table, (B, mp), torch.int32), mp,
-          _shape("lens", lens, (B,), torch.int32), _shape("cu_q", cu_q, (B + 1,), torch.int32),
-          _shape("mask", mask, (Tq, words), torch.int64), words, B, Tq, max_q, max_len, nh, kvh,
-          hd, scale, window, _shape("sink", sink, (nh,), torch.float32),
-          _shape("o", o, (Tq, nh, hd), _BF), _shape("lse", lse, (Tq, nh), torch.float32),
+          _arg("page_table", page_table, dev, (B, mp), _I32T), mp,
+          _arg("lens", lens, dev, (B,), _I32T), _arg("cu_q", cu_q, dev, (B + 1,), _I32T),
+          _arg("mask", mask, dev, (Tq, words), _I64T), words, B, Tq, max_q, max_len, nh, kvh, hd,
+          scale, window, _arg("sink", sink, dev, (nh,), _F32),
+          _arg("o", o, dev, (Tq, nh, hd), _BF), _arg("lse", lse, dev, (Tq, nh), _F32),
           None if ws is None else ws.data_ptr(), need, _stream())
     return o

@@ -575,10 +575,6 @@ int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_
                        const int32_t* cu_k, const int32_t* starts, int64_t B, ds41_bf16* k,
                        ds41_bf16* v, int64_t rows, ds41_stream_t stream);
 
-/* Scratch bytes ds41_prompt_attn_fwd needs (may be 0). */
-size_t ds41_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t nh,
-                                        int64_t kvh, int64_t hd);
-
 /* Causal attention over whole prompts, packed.  Sequence b has lq = cu_q[b+1]
  * - cu_q[b] queries and lk = cu_k[b+1] - cu_k[b] keys, aligned at their ends:
  * query i stands at p = i + lk - lq and sees the keys j with j <= p and, when
@@ -602,7 +598,7 @@ int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, cons
                          int64_t v_head, const int32_t* cu_q, const int32_t* cu_k, int64_t B,
                          int64_t Tq, int64_t Tk, int64_t max_q, int64_t nh, int64_t kvh,
                          int64_t hd, float scale, int64_t window, const float* sink, ds41_bf16* o,
-                         float* lse, void* ws, size_t ws_bytes, ds41_stream_t stream);
+                         float* lse, ds41_stream_t stream);
 
 /* Scratch bytes ds41_tree_attn_fwd needs (may be 0). */
 size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len,

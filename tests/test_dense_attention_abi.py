@@ -36,7 +36,7 @@ def prompt(lib, q=FAKE, q_tok=512, q_head=128, k=FAKE, k_tok=256, k_head=128, v_
            B=1, Tq=4, Tk=4, max_q=4, nh=4, kvh=2, hd=128, scale=0.1, window=0, o=FAKE, lse=None):
     return lib.ds41_prompt_attn_fwd(q, q_tok, q_head, k, k_tok, k_head, FAKE, v_tok, 128, cu, FAKE,
                                     B, Tq, Tk, max_q, nh, kvh, hd, F(scale), window, None, o, lse,
-                                    FAKE, 1 << 40, None)
+                                    None)
 
 
 def tree(lib, q=FAKE, q_tok=512, kc=FAKE, ks=FAKE, fmt=1, n_pages=4, page=16, table=FAKE,
