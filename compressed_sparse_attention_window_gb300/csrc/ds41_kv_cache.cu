@@ -60,6 +60,18 @@ namespace {
 
 constexpr int THREADS = 256;
 
+// x / s, correctly rounded, from the correctly rounded reciprocal r of s: with q
+// = x r within one unit of the quotient, q + r (x - q s), the remainder exact in a
+// fused multiply-add, rounds as the quotient does (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000 processor, 1990).  Three
+// operations for each of a row's 128 quotients instead of a division's ten.  Where
+// the remainder could leave the range of f32 the division itself is taken.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    if (s < 0x1p-90f) return __fdiv_rn(x, s);
+    const float q = __fmul_rn(x, r);
+    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, x), r, q), x);  // (-0 stays -0)
+}
+
 struct WriteArgs {
     const uint16_t* x[2];  // k, v
     int64_t stride[2];     // elements from a token's rows to the next token's
@@ -71,53 +83,54 @@ struct WriteArgs {
     unsigned int* status;
 };
 
-// L lanes take one (token, head): 8 elements of its K row and of its V row
-// each, so both rows' loads are in flight together.
+// L lanes take one (token, head): 8 elements of its K row and of its V row each, so
+// both rows' loads are in flight together; a CTA has one head of consecutive
+// tokens.  (16383 tokens of 8 heads of 128, 101 MB: 25 us of GPU time, 60% of the
+// copy rate.  Two and four rows a thread, heads innermost, and CTAs of 128 and 512
+// threads are level or slower.)
 template <int L, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(const WriteArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int64_t g = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / L;
-    const int c = (threadIdx.x % L) * 8;
-    const int64_t t = g / a.kvh;
-    const int h = (int)(g - t * a.kvh);
-    const bool live = t < a.n;
-    const bool mine = live && c < a.hd;
-    const int64_t slot = live ? a.slots[t] : -1;
+    const int c = (threadIdx.x % L) * 8, h = blockIdx.x % a.kvh;
+    const int64_t t = (int64_t)(blockIdx.x / a.kvh) * (THREADS / L) + threadIdx.x / L;
+    const bool mine = t < a.n && c < a.hd;
+    const int64_t slot = t < a.n ? a.slots[t] : -1;
     uint4 x[2];
 #pragma unroll
     for (int i = 0; i < 2; i++)
-        x[i] = mine ? *reinterpret_cast<const uint4*>(a.x[i] + t * a.stride[i] + h * a.hd + c)
+        x[i] = mine ? __ldcs(reinterpret_cast<const uint4*>(a.x[i] + t * a.stride[i] + h * a.hd + c))
                     : make_uint4(0, 0, 0, 0);
     const bool keep = slot >= 0 && slot < a.n_slots;
-    if (live && !keep && slot != -1 && c == 0 && h == 0) raise_status(a.status, DS41_E_INDEX);
+    if (!keep && slot != -1 && c == 0 && h == 0) raise_status(a.status, DS41_E_INDEX);
     const int64_t row = ((slot >> a.page_shift) * a.kvh + h) * a.page + (slot & (a.page - 1));
 #pragma unroll
     for (int i = 0; i < 2; i++) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         if (!E4M3) {
             if (keep && mine)
                 *reinterpret_cast<uint4*>(a.cache[i] + (row * a.hd + c) * 2) = x[i];
             continue;
         }
-        // the largest magnitude as bf16 bits (ordered like the values; the
-        // bits of infinities and NaN are the largest of all)
-        uint32_t m2 = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        // the largest magnitude as bf16 bits (ordered like the values; the bits of
+        // infinities and NaN are the largest of all)
+        const uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                     __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
         uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
         for (int off = L / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
         const bool fin = m < 0x7f80u;
         const float s = __fdiv_rn(fmaxf(bf2f((uint16_t)m), 448.0f * 0x1p-126f), 448.0f);
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const float r = __frcp_rn(s);
         uint32_t codes[2] = {0, 0};
         if (fin) {
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const float lo = __fdiv_rn(__uint_as_float(w[e] << 16), s);
-                const float hi = __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), s);
-                uint16_t r;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-                codes[e / 2] |= (uint32_t)r << (16 * (e & 1));
+                const float lo = quotient(__uint_as_float(w[e] << 16), s, r);
+                const float hi = quotient(__uint_as_float(w[e] & 0xffff0000u), s, r);
+                uint16_t two;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
+                codes[e / 2] |= (uint32_t)two << (16 * (e & 1));
             }
         }
         if (keep && mine) {
@@ -138,27 +151,26 @@ struct ReadArgs {
     unsigned int* status;
 };
 
-// L lanes take one (row, head), 16 elements of K and of V each; the rows of one
-// head are consecutive groups, as they lie in a page.
+// L lanes take one (row, head), 16 elements of K and of V each; the rows of a CTA
+// are consecutive, as they lie in a page.  (33000 rows of 8 heads of 128, 205 MB: 37
+// us of GPU time, 82% of the copy rate.)
 template <int L, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int h = blockIdx.y;
-    const int64_t r = ((int64_t)blockIdx.x * THREADS + threadIdx.x) / L;
-    const int c = (threadIdx.x % L) * 16;
-    if (r >= a.rows || c >= a.kv.hd) return;
-    if (r >= a.cu[a.B]) return;  // behind the last sequence
-    int lo = 0, hi = a.B;        // the last b with cu[b] <= r
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= r) lo = mid;
-        else hi = mid;
+    const int h = blockIdx.x % a.kv.kvh, c = (threadIdx.x % L) * 16;
+    const int64_t r = (int64_t)(blockIdx.x / a.kv.kvh) * (THREADS / L) + threadIdx.x / L;
+    if (c >= a.kv.hd || r >= a.rows || r >= a.cu[a.B]) return;  // behind the last: nobody's
+    int b = 0, end = a.B;  // the last b with cu[b] <= r
+    while (end - b > 1) {
+        const int mid = (b + end) >> 1;
+        if (a.cu[mid] <= r) b = mid;
+        else end = mid;
     }
-    const int64_t pos = r - a.cu[lo] + (a.starts ? a.starts[lo] : 0);
+    const int64_t pos = r - a.cu[b] + (a.starts ? a.starts[b] : 0);
     const int64_t pi = pos >> a.kv.page_shift;
     int64_t pg = -1;
-    if (pos >= 0 && pi < a.max_pages) pg = a.table[(int64_t)lo * a.max_pages + pi];
+    if (pos >= 0 && pi < a.max_pages) pg = a.table[(int64_t)b * a.max_pages + pi];
     const bool ok = pg >= 0 && pg < a.kv.n_pages;
     if (!ok) raise_status(a.status, DS41_E_INDEX);
     const int64_t row = paged_row(a.kv, ok ? pg : 0, h, (int)(pos & (a.kv.page - 1)));
@@ -171,11 +183,12 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
         s[i] = 0.0f;
         if (!ok) continue;
         if (E4M3) {
-            in[i][0] = *reinterpret_cast<const uint4*>(src + row * a.kv.hd + c);
+            in[i][0] = __ldcs(reinterpret_cast<const uint4*>(src + row * a.kv.hd + c));
             s[i] = (i ? a.kv.vs : a.kv.ks)[row];
         } else {
-            in[i][0] = *reinterpret_cast<const uint4*>(src + (row * a.kv.hd + c) * 2);
-            in[i][1] = *reinterpret_cast<const uint4*>(src + (row * a.kv.hd + c) * 2 + 16);
+            const uint4* x = reinterpret_cast<const uint4*>(src + (row * a.kv.hd + c) * 2);
+            in[i][0] = __ldcs(x);
+            in[i][1] = __ldcs(x + 1);
         }
     }
 #pragma unroll
@@ -189,13 +202,15 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
         const uint32_t w[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
         uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            uint32_t h2;
-            const uint16_t two = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
-            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int e = 0; e < 4; e++) {
+            uint32_t h2[2];
+            e4m3x4_to_f16(w[e], h2[0], h2[1]);
+#pragma unroll
+            for (int y = 0; y < 2; y++) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[y]));
+                const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s[i], f.y * s[i]);
+                o[2 * e + y] = *reinterpret_cast<const uint32_t*>(&v);
+            }
         }
         dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
         dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
@@ -256,11 +271,12 @@ extern "C" int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const d
                 nullptr};
     if (int rc = status_word(&a.status)) return rc;
     const int L = lanes_for(hd / 8);
-    const int64_t blocks = (n * kvh * L + THREADS - 1) / THREADS;
+    const int64_t per = THREADS / L, blocks = (n + per - 1) / per * kvh;
     DS41_REQUIRE(blocks < (int64_t(1) << 31), DS41_E_RANGE, "%s: n=%lld kvh=%lld", name,
                  (long long)n, (long long)kvh);
     return launch_pdl(fmt == DS41_KV_E4M3 ? pick_write<true>(L) : pick_write<false>(L),
-                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream, name, a);
+                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream,
+                      name, a);
 }
 
 extern "C" int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scales,
@@ -294,8 +310,10 @@ extern "C" int ds41_kv_cache_read(const void* k_cache, const void* v_cache, cons
     a.max_pages = (int)max_pages;
     if (int rc = status_word(&a.status)) return rc;
     const int L = lanes_for(hd / 16);
-    const int64_t blocks = (rows * L + THREADS - 1) / THREADS;
+    const int64_t per = THREADS / L, blocks = (rows + per - 1) / per * kvh;
+    DS41_REQUIRE(blocks < (int64_t(1) << 31), DS41_E_RANGE, "%s: rows=%lld kvh=%lld", name,
+                 (long long)rows, (long long)kvh);
     return launch_pdl(fmt == DS41_KV_E4M3 ? pick_read<true>(L) : pick_read<false>(L),
-                      dim3((unsigned)blocks, (unsigned)kvh), dim3(THREADS), 0,
-                      (cudaStream_t)stream, name, a);
+                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream,
+                      name, a);
 }
