@@ -81,30 +81,57 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     const int32_t* table = a.table + (int64_t)pc.b * a.max_pages;
     unsigned bad = 0;  // stages whose page does not exist
 
+    // what of the addresses does not change: a lane copies piece ch of the rows
+    // r_in, r_in + RPI, ...
+    constexpr int RPI = 32 / C::CH;
+    const int r_in = lane / C::CH, ch = lane % C::CH;
+    const int rb = a.hd * (E4M3 ? 1 : 2);  // bytes of a row in the cache
+    const bool in_row = ch * 16 < rb;
+    const int lane_off = r_in * rb + ch * 16, head_rows = h * a.kv.page;
+    const uint32_t ring_u = smem_u32(ring);
+    // (looked up a group ahead)
+    auto page_of = [&](int i) {
+        return i < mine ? table[(k0 + (i * WARPS + warp) * GROUP) >> a.kv.page_shift] : -1;
+    };
+    int page = page_of(0);
     auto fetch = [&](int i) {
         if (i < mine) {
             const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
-            const int64_t pg = table[j >> a.kv.page_shift];
+            const int pg = page;
+            page = page_of(i + 1);
             const bool ok = pg >= 0 && pg < a.kv.n_pages;
             if (!ok && lane == 0) raise_status(a.status, DS41_E_INDEX);
             bad = ok ? bad & ~(1u << st) : bad | (1u << st);
-            const int64_t row = paged_row(a.kv, ok ? pg : 0, h, j & (a.kv.page - 1));
-            const uint32_t dst = smem_u32(ring + st * C::STAGE);
-            const int rb = a.hd * (E4M3 ? 1 : 2);  // bytes of a row in the cache
+            const int64_t row =
+                ok ? (int64_t)pg * a.kvh * a.kv.page + (head_rows + (j & (a.kv.page - 1))) : 0;
+            const uint32_t dst = ring_u + st * C::STAGE + lane / C::CH * C::RB;
+            const uint8_t* kp = a.kv.k + row * rb + lane_off;
+            const uint8_t* vp = a.kv.v + row * rb + lane_off;
             // rows behind the sequence's end are read as zeros, whatever they hold
             const int live = ok ? min(GROUP, k1 - j) : 0;
+            if (live == GROUP && rb == C::RB) {
 #pragma unroll
-            for (int x = 0; x < GROUP * C::CH / 32; x++) {
-                const int r = (x * 32 + lane) / C::CH, ch = (x * 32 + lane) % C::CH;
-                const bool in = r < live && ch * 16 < rb;
-                const int64_t off = in ? (row + r) * rb + ch * 16 : 0;
-                cp_async16(dst + r * C::RB + k_piece<C::RB>(r, ch) * 16, a.kv.k + off, in);
-                cp_async16(dst + GROUP * C::RB + r * C::RB + v_piece<C::RB>(r, ch) * 16,
-                           a.kv.v + off, in);
+                for (int x = 0; x < GROUP / RPI; x++) {
+                    const int r = x * RPI + r_in;
+                    const uint32_t to = dst + x * RPI * C::RB;
+                    cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + x * RPI * C::RB, true);
+                    cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16,
+                               vp + x * RPI * C::RB, true);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < GROUP / RPI; x++) {
+                    const int r = x * RPI + r_in;
+                    const uint32_t to = dst + x * RPI * C::RB;
+                    const bool in = r < live && in_row;
+                    const int off = in ? x * RPI * rb : -lane_off;
+                    cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + off, in);
+                    cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16, vp + off, in);
+                }
             }
             if (E4M3 && lane < 8) {
-                const float* src = lane < 4 ? a.kv.ks : a.kv.vs;
-                cp_async16(dst + 2 * GROUP * C::RB + lane * 16, src + row + (lane & 3) * 4, ok);
+                const float* src = (lane < 4 ? a.kv.ks : a.kv.vs) + row + (lane & 3) * 4;
+                cp_async16(ring_u + st * C::STAGE + 2 * GROUP * C::RB + lane * 16, src, ok);
             }
         }
         cp_async_commit();
@@ -159,6 +186,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
 
     float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
     float lr = E4M3 ? tc::RowState::VS_MIN : 0.0f, vlim = 0.0f;
+    float base[2] = {0.0f, 0.0f};  // c m + lr: what an exponent is reduced by
     for (int i = 0; i < mine; i++) {
         fetch(i + C::STAGES - 1);
         cp_async_wait<C::STAGES - 1>();
@@ -206,17 +234,14 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                 for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
             }
         }
-        if ((bad >> st) & 1) {
-#pragma unroll
-            for (int n = 0; n < 2; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) sc[n][e] = -INFINITY;
-        } else if (j + GROUP > easy || j <= lo) {
+        const bool masked = ((bad >> st) & 1) || j + GROUP > easy || j <= lo;
+        if (masked) {
 #pragma unroll
             for (int n = 0; n < 2; n++)
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (!seen(view[e >> 1], j + n * 8 + 2 * c + (e & 1), s.len))
+                    if (((bad >> st) & 1) ||
+                        !seen(view[e >> 1], j + n * 8 + 2 * c + (e & 1), s.len))
                         sc[n][e] = -INFINITY;
         }
         float mx[2];
@@ -256,27 +281,35 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                     o[d][2 * i2] *= f;
                     o[d][2 * i2 + 1] *= f;
                 }
+                base[i2] = m[i2] == -INFINITY ? 0.0f : fmaf(m[i2], cr[i2], lr);
             }
         }
         uint32_t pf[4];
 #pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-            for (int i2 = 0; i2 < 2; i2++) {
-                const float base = m[i2] == -INFINITY ? 0.0f : m[i2];
-                const float s0 = sc[n][2 * i2], s1 = sc[n][2 * i2 + 1];
-                const float p0 = ex2(fmaf(s0 - base, cr[i2], -lr));
-                const float p1 = ex2(fmaf(s1 - base, cr[i2], -lr));
-                l[i2] += p0 + p1;
-                if (E4M3) {
-                    // a row that is not seen weighs nothing, whatever its scale holds
-                    const float w0 = s0 == -INFINITY ? 0.0f : p0 * vs[n].x;
-                    const float w1 = s1 == -INFINITY ? 0.0f : p1 * vs[n].y;
-                    pf[2 * n + i2] = tc::f16x2(w0, w1);
-                } else {
-                    pf[2 * n + i2] = bf16x2(p0, p1);
-                }
+        for (int i2 = 0; i2 < 2; i2++) {
+            float less = base[i2], at = 0.0f;
+            if (fabsf(less) > 0x1p22f) {  // c m is rounded too far: the difference first
+                less = lr;
+                at = m[i2];
             }
+#pragma unroll
+            for (int n = 0; n < 2; n++) {
+                const float p0 = ex2(fmaf(sc[n][2 * i2] - at, cr[i2], -less));
+                const float p1 = ex2(fmaf(sc[n][2 * i2 + 1] - at, cr[i2], -less));
+                l[i2] += p0 + p1;
+                if (!E4M3) {
+                    pf[2 * n + i2] = bf16x2(p0, p1);
+                    continue;
+                }
+                float w0 = p0 * vs[n].x, w1 = p1 * vs[n].y;
+                if (masked) {
+                    // a row that is not seen weighs nothing, whatever its scale holds
+                    if (sc[n][2 * i2] == -INFINITY) w0 = 0.0f;
+                    if (sc[n][2 * i2 + 1] == -INFINITY) w1 = 0.0f;
+                }
+                pf[2 * n + i2] = tc::f16x2(w0, w1);
+            }
+        }
         // ---- O += P V: n-tile d holds the columns g HD/8 + d ----
         if (E4M3) {
             uint32_t w[4][HD / 32];
