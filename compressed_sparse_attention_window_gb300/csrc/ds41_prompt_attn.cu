@@ -15,10 +15,14 @@
 // head; G = 4: 32 tokens), and a CTA holds two such tiles over one stream of
 // key/value blocks.
 //
-// Design.  One CTA per SM, warp-specialised: warp 0 issues the TMA copies (two
-// query tiles once, then K and V blocks through a ring of stages), warp 1
-// issues the MMAs, warps 4..7 and 8..11 compute the softmax of tile 0 and of
-// tile 1, a thread per row.  S_t (128 columns of f32) and O_t live in tensor
+// Design.  One persistent CTA per SM walks its items (a pair of tiles of one head
+// group), warp-specialised: warp 0 issues the TMA copies (an item's two query
+// tiles, then its K and V blocks through a ring of stages), warp 1 issues the
+// MMAs, warp 3 looks the items up some ahead, warps 4..7 and 8..11 compute the
+// softmax of tile 0 and of tile 1, a thread per row, and write the outputs.  No
+// role waits for another at an item's end: the next item's queries and keys
+// arrive and its first scores are computed while the last one's outputs are
+// written.  S_t (128 columns of f32) and O_t live in tensor
 // memory; the weights go back as bf16 into the columns of S_t and are the A
 // operand of the second product from there, so neither S nor P touches shared
 // memory.  Issue order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1): while the softmax of
@@ -42,11 +46,12 @@ struct Cfg {
     static constexpr int NB = D / 64;                   // 64-column blocks of a row
     static constexpr uint32_t BLK = 128 * 128;          // [128 rows][64 columns] bf16
     static constexpr uint32_t TILE = NB * BLK;          // a query tile, or a K or V block
-    static constexpr int STAGES = D == 128 ? 5 : 10;
-    static constexpr uint32_t Q_OFF = 0;                // two query tiles
-    static constexpr uint32_t KV_OFF = 2 * TILE;
+    static constexpr int STAGES = D == 128 ? 5 : 9;
+    static constexpr int QB = D == 128 ? 1 : 2;         // items whose queries are held
+    static constexpr uint32_t Q_OFF = 0;                // two query tiles each
+    static constexpr uint32_t KV_OFF = QB * 2 * TILE;
     static constexpr uint32_t BAR_OFF = KV_OFF + STAGES * TILE;
-    static constexpr uint32_t SMEM = BAR_OFF + 512 + 1024;
+    static constexpr uint32_t SMEM = BAR_OFF + 640 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -69,13 +74,14 @@ struct Params {
     unsigned int* status;
 };
 
-// A CTA's work: one head group of one pair of tiles of one sequence.
+// An item: one head group of one pair of tiles of one sequence.
 struct Item {
-    int b;          // sequence, -1: none
-    int q0, n;      // its queries
-    int k0, len;    // its keys
+    int grp;        // head group, -1: no more items
+    int q0, n;      // its sequence's queries
+    int k0, len;    // and keys
     int t0;         // first token of tile 0
 };
+constexpr int ITEMS = 4;  // items looked up ahead
 
 // the lowest n bits (none for n <= 0, all for n >= 32)
 __device__ __forceinline__ uint32_t low_bits(int n) {
@@ -103,53 +109,104 @@ __device__ __forceinline__ Range tile_range(const Item& it, const Params& p, int
     return r;
 }
 
-// Sequence and tile pair of flat index w (a warp; every lane gets the result).
-// A sequence that breaks its limits has no tiles.  Tiles of a sequence come
-// in falling order: the longest first.
-__device__ Item find_item(const Params& p, int w, bool report, int lane) {
-    Item it;
-    it.b = -1;
-    int base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        int q0 = 0, n = 0, k0 = 0, len = 0, tiles = 0;
-        if (b < p.B) {
-            q0 = p.cu_q[b];
-            k0 = p.cu_k[b];
-            const int64_t ln = (int64_t)p.cu_q[b + 1] - q0, lk = (int64_t)p.cu_k[b + 1] - k0;
-            const bool ok = q0 >= 0 && ln >= 0 && ln <= p.max_q && q0 + ln <= p.Tq && k0 >= 0 &&
-                            lk >= 0 && k0 + lk <= p.Tk;
-            if (ok) {
-                n = (int)ln;
-                len = (int)lk;
-                tiles = (n + 2 * p.TT - 1) / (2 * p.TT);
-            } else if (report) {
-                raise_status(p.status, DS41_E_INDEX);
-            }
-        }
-        int sum = tiles;  // inclusive prefix sum over the lanes
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += v;
-        }
-        const unsigned mine = __ballot_sync(0xffffffffu, it.b < 0 && w >= base + sum - tiles &&
-                                                             w < base + sum);
-        if (mine) {
-            const int src = __ffs(mine) - 1;
-            it.b = b0 + src;
-            it.q0 = __shfl_sync(0xffffffffu, q0, src);
-            it.n = __shfl_sync(0xffffffffu, n, src);
-            it.k0 = __shfl_sync(0xffffffffu, k0, src);
-            it.len = __shfl_sync(0xffffffffu, len, src);
-            const int end = base + __shfl_sync(0xffffffffu, sum, src);
-            it.t0 = (end - 1 - w) * 2 * p.TT;
-            if (!report) return it;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    return it;
+// A CTA that is through with an item takes over one whose CTA has not started yet:
+// the grid has a CTA for every item, and the launch queue is the list of what is
+// left, longest first, so the SMs end together (items dealt out beforehand left
+// one of them 7% more blocks than the average of a 16384-token prompt).
+__device__ __forceinline__ void take_over(uint32_t response, uint64_t* bar) {
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];\n" ::"r"(response),
+        "r"(smem_u32(bar))
+        : "memory");
 }
+// the answer: the CTA's index, or -1: all have started
+__device__ __forceinline__ int taken_over(uint32_t response) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n.reg .pred p;\n.reg .b128 r;\nld.shared.b128 r, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+        "selp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+        : "=r"(got), "=r"(x)
+        : "r"(response)
+        : "memory");
+    return got ? (int)x : -1;
+}
+
+// Walks the sequences, 32 at a time (a whole warp): flat index w -> sequence and
+// pair of tiles (indices mostly rise from call to call; one that does not starts
+// over).  A sequence that breaks its limits has no tiles.  The tiles of a sequence
+// come in falling order: the longest first.
+struct Finder {
+    int b0 = -32, base = 0, end = 0;  // sequences b0 .. b0 + 31 have pairs base .. end - 1
+    int q0, n, k0, len, tiles, sum;   // this lane's sequence; sum: inclusive prefix of tiles
+    __device__ __forceinline__ bool find(const Params& p, int w, bool report, int lane, Item& it) {
+        if (w < base) {
+            b0 = -32;
+            base = end = 0;
+        }
+        while (w >= end) {
+            b0 += 32;
+            if (b0 >= p.B) {
+                b0 -= 32;
+                return false;
+            }
+            const int b = b0 + lane;
+            q0 = n = k0 = len = tiles = 0;
+            if (b < p.B) {
+                q0 = p.cu_q[b];
+                k0 = p.cu_k[b];
+                const int64_t ln = (int64_t)p.cu_q[b + 1] - q0, lk = (int64_t)p.cu_k[b + 1] - k0;
+                if (q0 >= 0 && ln >= 0 && ln <= p.max_q && q0 + ln <= p.Tq && k0 >= 0 && lk >= 0 &&
+                    k0 + lk <= p.Tk) {
+                    n = (int)ln;
+                    len = (int)lk;
+                    tiles = (n + 2 * p.TT - 1) / (2 * p.TT);
+                } else if (report) {
+                    raise_status(p.status, DS41_E_INDEX);
+                }
+            }
+            sum = tiles;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += v;
+            }
+            base = end;
+            end = base + __shfl_sync(0xffffffffu, sum, 31);
+        }
+        const unsigned mine =
+            __ballot_sync(0xffffffffu, w >= base + sum - tiles && w < base + sum);
+        const int src = __ffs(mine) - 1;
+        it.q0 = __shfl_sync(0xffffffffu, q0, src);
+        it.n = __shfl_sync(0xffffffffu, n, src);
+        it.k0 = __shfl_sync(0xffffffffu, k0, src);
+        it.len = __shfl_sync(0xffffffffu, len, src);
+        it.t0 = (base + __shfl_sync(0xffffffffu, sum, src) - 1 - w) * 2 * p.TT;
+        return true;
+    }
+};
+
+// What every role derives from an item: the tiles' key blocks, their union
+// [jlo, jhi), and the keys of the last block when it is not full (the rest of its
+// V rows belong to another sequence, or to nobody).
+struct Span {
+    Range rg[2];
+    int jlo, jhi, tail;
+    __device__ __forceinline__ Span(const Item& it, const Params& p)
+        : rg{tile_range(it, p, 0), tile_range(it, p, 1)} {
+        jlo = rg[0].lo;
+        jhi = rg[0].hi;
+        if (rg[1].hi > rg[1].lo) {
+            jlo = rg[0].hi > rg[0].lo ? min(jlo, rg[1].lo) : rg[1].lo;
+            jhi = max(jhi, rg[1].hi);
+        }
+        tail = jhi * KB > it.len ? it.len - (jhi - 1) * KB : 0;
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -163,58 +220,51 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = smem_u32(sm);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
-    uint64_t* b_q = bars;                      // queries landed
-    uint64_t* b_full = bars + 1;               // stage landed
+    uint64_t* b_q = bars;                      // an item's queries landed [QB]
+    uint64_t* b_qe = b_q + C::QB;              // and have been used [QB]
+    uint64_t* b_full = b_qe + C::QB;           // stage landed
     uint64_t* b_empty = b_full + C::STAGES;    // stage read
     uint64_t* b_s = b_empty + C::STAGES;       // S_t in tensor memory [2]
     uint64_t* b_p = b_s + 2;                   // P_t in tensor memory, O_t rescaled [2]
     uint64_t* b_o = b_p + 2;                   // O_t complete [2]
-    uint64_t* b_tail = b_o + 2;                // the V block that ends behind the last key landed
+    uint64_t* b_oe = b_o + 2;                  // O_t read [2]
+    uint64_t* b_tail = b_oe + 2;               // the V block that ends behind the last key landed
     uint64_t* b_fix = b_tail + 1;              // its rows behind the last key are zero
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_fix + 1);
+    uint64_t* b_item = b_fix + 1;              // an item is known [ITEMS]
+    uint64_t* b_iteme = b_item + ITEMS;        // and every role is through with it
+    uint64_t* b_clc = b_iteme + ITEMS;         // the answer to a request for another item
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_clc + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* sh_item = reinterpret_cast<int*>(tmem_slot + 2);
-    static_assert((1 + 2 * C::STAGES + 8) * 8 + 8 + 6 * 4 <= 512, "barrier area");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int grp = blockIdx.x % p.n_groups;
-    const int w = blockIdx.x / p.n_groups;
+    Item* items = reinterpret_cast<Item*>(tmem_slot + 2);
+    static_assert((2 * C::QB + 2 * C::STAGES + 11 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <= 624,
+                  "barrier area");
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-    if (warp == 0) {
-        const Item it = find_item(p, w, blockIdx.x == 0, lane);
-        if (lane == 0) {
-            sh_item[0] = it.b;
-            sh_item[1] = it.q0;
-            sh_item[2] = it.n;
-            sh_item[3] = it.k0;
-            sh_item[4] = it.len;
-            sh_item[5] = it.t0;
-        }
-    }
     if (threadIdx.x == 32) {
-        mbar_init(b_q, 1);
-        for (int s = 0; s < C::STAGES; s++) {
-            mbar_init(&b_full[s], 1);
-            mbar_init(&b_empty[s], 1);
+        for (int i = 0; i < C::QB; i++) {
+            mbar_init(&b_q[i], 1);
+            mbar_init(&b_qe[i], 1);
+        }
+        for (int i = 0; i < C::STAGES; i++) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
         }
         for (int t = 0; t < 2; t++) {
             mbar_init(&b_s[t], 1);
             mbar_init(&b_p[t], 4);
             mbar_init(&b_o[t], 1);
+            mbar_init(&b_oe[t], 4);
         }
         mbar_init(b_tail, 1);
         mbar_init(b_fix, 1);
+        for (int i = 0; i < ITEMS; i++) {
+            mbar_init(&b_item[i], 1);
+            mbar_init(&b_iteme[i], 11);
+        }
+        mbar_init(b_clc, 1);
         *abort_f = 0;
         mbar_init_fence();
     }
-    __syncthreads();
-    Item it;
-    it.b = sh_item[0];
-    if (it.b < 0) return;
-    it.q0 = sh_item[1];
-    it.n = sh_item[2];
-    it.k0 = sh_item[3];
-    it.len = sh_item[4];
-    it.t0 = sh_item[5];
     if (warp == 1) {
         asm volatile(
             "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
@@ -226,216 +276,326 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int used = p.TT * p.G;
     if (used < ROWS) {
         const int per = (ROWS - used) * 8;  // 16-byte pieces of one 64-column block
-        for (int x = threadIdx.x; x < 2 * C::NB * per; x += THREADS)
+        for (int x = threadIdx.x; x < C::QB * 2 * C::NB * per; x += THREADS)
             *reinterpret_cast<uint4*>(sm + C::Q_OFF + (x / per) * C::BLK + used * 128 +
                                       (x % per) * 16) = make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     }
-    const Range rg[2] = {tile_range(it, p, 0), tile_range(it, p, 1)};
-    int jlo = rg[0].lo, jhi = rg[0].hi;
-    if (rg[1].hi > rg[1].lo) {
-        jlo = rg[0].hi > rg[0].lo ? min(jlo, rg[1].lo) : rg[1].lo;
-        jhi = max(jhi, rg[1].hi);
-    }
-    // keys of the last block when it is not full: the rest of its V rows belong
-    // to another sequence (or to nobody)
-    const int tail = (jhi * KB > it.len) ? it.len - (jhi - 1) * KB : 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    // the next item of this warp's walk; false at the end (or when a wait gave up)
+    auto next_item = [&](int k, Item& it) {
+        if (!warp_wait(&b_item[k % ITEMS], (k / ITEMS) & 1, abort_f, p.status)) return false;
+        const Item& x = items[k % ITEMS];
+        it.grp = uniform(x.grp);
+        it.q0 = uniform(x.q0);
+        it.n = uniform(x.n);
+        it.k0 = uniform(x.k0);
+        it.len = uniform(x.len);
+        it.t0 = uniform(x.t0);
+        return it.grp >= 0;
+    };
+    auto done_item = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_iteme[k % ITEMS]);
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (warp == 0 && lane == 0 && jhi > jlo) {
-            const int head0 = grp * p.G;
-            const int kvh = grp / p.subs;
-            uint32_t q_tiles = 0;
-            for (int t = 0; t < 2; t++) q_tiles += rg[t].hi > rg[t].lo;
-            mbar_arrive_expect_tx(b_q, q_tiles * C::NB * (uint32_t)used * 128);
-            for (int t = 0; t < 2; t++)
-                if (rg[t].hi > rg[t].lo)
-                    for (int x = 0; x < C::NB; x++)
-                        tma_load_3d(sbase + C::Q_OFF + t * C::TILE + x * C::BLK, &map_q, 64 * x,
-                                    head0, it.q0 + it.t0 + t * p.TT, b_q);
-            uint32_t n = 0;
+        if (warp == 0) {
+            uint32_t n = 0, nq = 0;
             bool ok = true;
-            for (int j = jlo; j < jhi && ok; j++) {
-                for (int kv = 0; kv < 2; kv++, n++) {
-                    const uint32_t s = n % C::STAGES, use = n / C::STAGES;
-                    if (use > 0 && !wait_bar(&b_empty[s], (use - 1) & 1, abort_f, p.status)) {
-                        ok = false;
-                        break;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                const Span sp(it, p);
+                if (sp.jhi > sp.jlo && lane == 0) {
+                    const int head0 = it.grp * p.G, kvh = it.grp / p.subs, qb = nq % C::QB;
+                    if (nq >= C::QB)
+                        ok = wait_bar(&b_qe[qb], ((nq / C::QB) - 1) & 1, abort_f, p.status);
+                    if (ok) {
+                        uint32_t q_tiles = 0;
+                        for (int t = 0; t < 2; t++) q_tiles += sp.rg[t].hi > sp.rg[t].lo;
+                        mbar_arrive_expect_tx(&b_q[qb], q_tiles * C::NB * (uint32_t)used * 128);
+                        for (int t = 0; t < 2; t++)
+                            if (sp.rg[t].hi > sp.rg[t].lo)
+                                for (int x = 0; x < C::NB; x++)
+                                    tma_load_3d(sbase + C::Q_OFF + (2 * qb + t) * C::TILE +
+                                                    x * C::BLK,
+                                                &map_q, 64 * x, head0, it.q0 + it.t0 + t * p.TT,
+                                                &b_q[qb]);
+                        nq++;
                     }
-                    mbar_arrive_expect_tx(&b_full[s], C::TILE);
-                    for (int x = 0; x < C::NB; x++)
-                        tma_load_3d(sbase + C::KV_OFF + s * C::TILE + x * C::BLK,
-                                    kv ? &map_v : &map_k, 64 * x, kvh, it.k0 + j * KB,
-                                    &b_full[s]);
+                    for (int j = sp.jlo; j < sp.jhi && ok; j++) {
+                        for (int kv = 0; kv < 2 && ok; kv++) {
+                            const uint32_t st = n % C::STAGES, use = n / C::STAGES;
+                            if (use > 0)
+                                ok = wait_bar(&b_empty[st], (use - 1) & 1, abort_f, p.status);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&b_full[st], C::TILE);
+                            for (int x = 0; x < C::NB; x++)
+                                tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK,
+                                            kv ? &map_v : &map_k, 64 * x, kvh, it.k0 + j * KB,
+                                            &b_full[st]);
+                            n++;
+                        }
+                    }
                 }
+                ok = __all_sync(0xffffffffu, ok);
+                done_item(k);
             }
             // everything that was started lands before the CTA ends
-            drain_bar(b_q, 0, p.status);
-            for (uint32_t s = 0; s < C::STAGES && s < n; s++)
-                drain_bar(&b_full[s], ((n - 1 - s) / C::STAGES) & 1, p.status);
-        } else if (warp == 1 && jhi > jlo) {
+            if (lane == 0) {
+                for (uint32_t x = nq > C::QB ? nq - C::QB : 0; x < nq; x++)
+                    drain_bar(&b_q[x % C::QB], (x / C::QB) & 1, p.status);
+                for (uint32_t x = n > C::STAGES ? n - C::STAGES : 0; x < n; x++)
+                    drain_bar(&b_full[x % C::STAGES], (x / C::STAGES) & 1, p.status);
+            }
+        } else if (warp == 1) {
             constexpr uint32_t IDESC_S = idesc_bf16(128, KB, 0, 0);
             constexpr uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
-            const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
-            const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
-            const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
-            uint32_t done_p[2] = {0, 0};
+            const uint32_t kd = desc_lo(sbase + C::KV_OFF, 16);
+            const uint32_t vd = desc_lo(sbase + C::KV_OFF, C::BLK);
+            uint32_t ring0 = 0, nq = 0, tails = 0, done_p[2] = {0, 0}, outs[2] = {0, 0};
             auto wait_stage = [&](uint32_t n) {
-                const bool ok =
+                const bool r =
                     warp_wait(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
                 tc_fence_after();
-                return ok;
+                return r;
             };
             auto stage_off = [&](uint32_t n) { return ((n % C::STAGES) * C::TILE) >> 4; };
-            bool ok = warp_wait(b_q, 0, abort_f, p.status) && wait_stage(0);
-            if (ok && elect_one()) {
-#pragma unroll
-                for (int t = 0; t < 2; t++)
-                    if (jlo >= rg[t].lo && jlo < rg[t].hi) {
-                        mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t, qd + ((t * C::TILE) >> 4),
-                                               kd + stage_off(0));
-                        tc_commit(&b_s[t]);
-                    }
-                tc_commit(&b_empty[0]);
-            }
-            for (int j = jlo; j < jhi && ok; j++) {
-                const uint32_t nv = 2 * (uint32_t)(j - jlo) + 1, nk = nv + 1;
-                ok = wait_stage(nv);
-                if (ok && j == jhi - 1 && tail > 0) {
-                    if (lane == 0) mbar_arrive(b_tail);
-                    ok = warp_wait(b_fix, 0, abort_f, p.status);
-                    tc_fence_after();
-                }
-                bool have_k = false;
-#pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    const bool now = j >= rg[t].lo && j < rg[t].hi;
-                    const bool next = j + 1 >= rg[t].lo && j + 1 < rg[t].hi;
-                    if (ok && now) {
-                        ok = warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
-                        done_p[t]++;
-                        tc_fence_after();
-                    }
-                    if (ok && next && !have_k) {
-                        ok = wait_stage(nk);
-                        have_k = true;
-                    }
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                const Span sp(it, p);
+                const int jlo = sp.jlo, jhi = sp.jhi;
+                if (jhi > jlo) {
+                    const int qb = nq % C::QB;
+                    const uint32_t qd = desc_lo(sbase + C::Q_OFF + 2 * qb * C::TILE, 16);
+                    ok = warp_wait(&b_q[qb], (nq / C::QB) & 1, abort_f, p.status) &&
+                         wait_stage(ring0);
+                    nq++;
                     if (ok && elect_one()) {
-                        if (now) {
-                            mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
-                                                   vd + stage_off(nv), j > rg[t].lo);
-                            if (j + 1 == rg[t].hi) tc_commit(&b_o[t]);
-                        }
-                        if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
-                        if (next) {
-                            mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
-                                                   qd + ((t * C::TILE) >> 4), kd + stage_off(nk));
-                            tc_commit(&b_s[t]);
-                        }
+#pragma unroll
+                        for (int t = 0; t < 2; t++)
+                            if (jlo >= sp.rg[t].lo && jlo < sp.rg[t].hi) {
+                                mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                                       qd + ((t * C::TILE) >> 4),
+                                                       kd + stage_off(ring0));
+                                tc_commit(&b_s[t]);
+                            }
+                        tc_commit(&b_empty[ring0 % C::STAGES]);
+                        if (jhi == jlo + 1) tc_commit(&b_qe[qb]);
                     }
                     __syncwarp();
+                    for (int j = jlo; j < jhi && ok; j++) {
+                        const uint32_t nv = ring0 + 2 * (uint32_t)(j - jlo) + 1, nk = nv + 1;
+                        // (both before the waits for the weights: nothing stands between
+                        // their arrival and the products)
+                        ok = wait_stage(nv) && (j + 1 >= jhi || wait_stage(nk));
+                        if (ok && j == jhi - 1 && sp.tail > 0) {
+                            if (lane == 0) mbar_arrive(b_tail);
+                            ok = warp_wait(b_fix, tails & 1, abort_f, p.status);
+                            tails++;
+                            tc_fence_after();
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; t++) {
+                            const bool now = j >= sp.rg[t].lo && j < sp.rg[t].hi;
+                            const bool next = j + 1 >= sp.rg[t].lo && j + 1 < sp.rg[t].hi;
+                            if (ok && now) {
+                                // the last item's outputs have been read
+                                if (j == sp.rg[t].lo && outs[t] > 0)
+                                    ok = warp_wait(&b_oe[t], (outs[t] - 1) & 1, abort_f, p.status);
+                                ok = ok && warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
+                                done_p[t]++;
+                                tc_fence_after();
+                            }
+                            if (ok && elect_one()) {
+                                if (now) {
+                                    mma_output<D, IDESC_O>(tmem + TM_O + 128 * t,
+                                                           tmem + TM_S + 128 * t,
+                                                           vd + stage_off(nv), j > sp.rg[t].lo);
+                                    if (j + 1 == sp.rg[t].hi) tc_commit(&b_o[t]);
+                                }
+                                if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
+                                if (next) {
+                                    mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                                           qd + ((t * C::TILE) >> 4),
+                                                           kd + stage_off(nk));
+                                    tc_commit(&b_s[t]);
+                                }
+                            }
+                            __syncwarp();
+                            if (now && j + 1 == sp.rg[t].hi) outs[t]++;
+                        }
+                        if (ok && j + 1 < jhi && elect_one()) {
+                            tc_commit(&b_empty[nk % C::STAGES]);
+                            if (j + 2 == jhi) tc_commit(&b_qe[qb]);  // the last scores
+                        }
+                        __syncwarp();
+                    }
+                    ring0 += 2 * (uint32_t)(jhi - jlo);
                 }
-                if (ok && j + 1 < jhi) {
-                    if (!have_k) ok = wait_stage(nk);
-                    if (ok && elect_one()) tc_commit(&b_empty[nk % C::STAGES]);
-                    __syncwarp();
-                }
+                done_item(k);
             }
-        } else if (warp == 2 && tail > 0 && jhi > jlo) {
+        } else if (warp == 2) {
             // zero the V rows behind the last key
-            const uint32_t n = 2 * (uint32_t)(jhi - 1 - jlo) + 1, s = n % C::STAGES;
-            if (warp_wait(b_tail, 0, abort_f, p.status)) {
-                for (int x = lane; x < (KB - tail) * C::NB * 8; x += 32) {
-                    const int r = tail + x / (C::NB * 8), piece = x % (C::NB * 8);
-                    *reinterpret_cast<uint4*>(sm + C::KV_OFF + s * C::TILE + (piece / 8) * C::BLK +
-                                              r * 128 + (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+            uint32_t ring0 = 0, tails = 0;
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                const Span sp(it, p);
+                if (sp.jhi > sp.jlo) {
+                    ring0 += 2 * (uint32_t)(sp.jhi - sp.jlo);
+                    if (sp.tail > 0) {
+                        ok = warp_wait(b_tail, tails & 1, abort_f, p.status);
+                        tails++;
+                        if (!ok) break;
+                        uint8_t* v = sm + C::KV_OFF + ((ring0 - 1) % C::STAGES) * C::TILE;
+                        for (int x = lane; x < (KB - sp.tail) * C::NB * 8; x += 32) {
+                            const int r = sp.tail + x / (C::NB * 8), piece = x % (C::NB * 8);
+                            *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
+                                                      (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_fix);
+                    }
                 }
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                done_item(k);
+            }
+        } else {
+            // the items: this CTA's own, then those that it takes over
+            const uint32_t response = sbase + C::BAR_OFF + 640 - 16;
+            Finder f;
+            int id = blockIdx.x;
+            bool ok = true;
+            for (int k = 0, asked = 0; ok && id >= 0;) {
+                if (lane == 0) take_over(response, b_clc);
+                Item it;
+                const int w = id / p.n_groups;
+                if (f.find(p, w, false, lane, it)) {
+                    it.grp = id - w * p.n_groups;
+                    if (k >= ITEMS)
+                        ok = warp_wait(&b_iteme[k % ITEMS], ((k / ITEMS) - 1) & 1, abort_f,
+                                       p.status);
+                    if (ok && lane == 0) {
+                        items[k % ITEMS] = it;
+                        mbar_arrive(&b_item[k % ITEMS]);
+                    }
+                    k++;
+                }
+                if (id == 0) {  // whoever has the first item reports the bad sequences
+                    Finder all;
+                    while (all.find(p, 0x7fffffff, true, lane, it)) {
+                    }
+                }
+                // (an answer that is on its way is waited for in any case)
+                const bool here = __all_sync(
+                    0xffffffffu, drain_bar(b_clc, asked & 1, p.status));
+                asked++;
+                id = here ? taken_over(response) : -1;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_fix);
+                if (id < 0 || !ok) {
+                    if (ok && k >= ITEMS)
+                        ok = warp_wait(&b_iteme[k % ITEMS], ((k / ITEMS) - 1) & 1, abort_f,
+                                       p.status);
+                    if (lane == 0) {
+                        items[k % ITEMS].grp = -1;
+                        mbar_arrive(&b_item[k % ITEMS]);
+                    }
+                    break;
+                }
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         const int t = (warp - 4) >> 2;
-        const Range r = rg[t];
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tm_s = tmem + lanes + TM_S + 128 * t, tm_o = tmem + lanes + TM_O + 128 * t;
         const int row = 32 * (warp & 3) + lane;
         const int tok = row / p.G, gh = row - tok * p.G;
-        const bool live = tok < r.count;
-        const bool idle = !__any_sync(0xffffffffu, live);
-        const int64_t pos = (int64_t)r.p_first + tok;              // the last key it sees
-        const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
-        const int64_t p_last = (int64_t)r.p_first + r.count - 1;
         const float c = p.c;
-        RowState st(false);
-        uint32_t ph = 0;
+        uint32_t ph = 0, outs = 0;
         bool ok = true;
-        for (int j = r.lo; j < r.hi; j++, ph++) {
-            ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            const int64_t j0 = (int64_t)j * KB;
-            const bool masked = j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
-            uint32_t vis[4] = {};
-            if (masked) {
-                const int hi = (int)max((int64_t)-1, min((int64_t)KB, pos - j0));
-                const int lo = (int)max((int64_t)-1, min((int64_t)KB, before - j0));
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
-            }
-            if (idle) {
-                // none of the warp's rows exists: whatever its scores hold weighs no one
-            } else if (masked) {
-                softmax_block<D, true>(tm_s, tm_o, j > r.lo, vis, c, live, st);
-            } else {
-                softmax_block<D, false>(tm_s, tm_o, j > r.lo, vis, c, live, st);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b_p[t]);
-        }
-        // the sink is one more term of the denominator
-        const int head = grp * p.G + gh;
-        const RowEnd end = row_end(st.reference(c), st.l,
-                                   live && p.sink ? p.sink[head] : -INFINITY);
-        const float inv = end.factor;
-        const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
-        if (live && ok && p.lse) p.lse[at] = end.lse;
-        if (r.count > 0 && ok) {
-            uint16_t* dst = p.o + at * p.hd;
-            if (r.hi > r.lo) {
-                ok = warp_wait(&b_o[t], 0, abort_f, p.status);
+        Item it;
+        for (int k = 0; ok && next_item(k, it); k++) {
+            const Range r = tile_range(it, p, t);
+            const bool live = tok < r.count;
+            const bool idle = !__any_sync(0xffffffffu, live);
+            const int64_t pos = (int64_t)r.p_first + tok;              // the last key it sees
+            const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
+            const int64_t p_last = (int64_t)r.p_first + r.count - 1;
+            RowState st(false);
+            for (int j = r.lo; j < r.hi; j++, ph++) {
+                ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
+                if (!ok) break;
                 tc_fence_after();
+                const int64_t j0 = (int64_t)j * KB;
+                const bool masked = j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
+                if (idle) {
+                    // none of the warp's rows exists: whatever its scores hold weighs no one
+                } else if (masked) {
+                    const int hi = (int)max((int64_t)-1, min((int64_t)KB, pos - j0));
+                    const int lo = (int)max((int64_t)-1, min((int64_t)KB, before - j0));
+                    uint32_t vis[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        vis[i] = low_bits(hi + 1 - 32 * i) & ~low_bits(lo + 1 - 32 * i);
+                    softmax_block<D, true>(tm_s, tm_o, j > r.lo, vis, c, live, st);
+                } else {
+                    const uint32_t all[4] = {};
+                    softmax_block<D, false>(tm_s, tm_o, j > r.lo, all, c, live, st);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_p[t]);
             }
-            if (ok) {
+            if (!ok) break;
+            // the sink is one more term of the denominator
+            const int head = it.grp * p.G + gh;
+            const RowEnd end = row_end(st.reference(c), st.l,
+                                       live && p.sink ? p.sink[head] : -INFINITY);
+            const float inv = end.factor;
+            const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
+            if (live && p.lse) p.lse[at] = end.lse;
+            if (r.count > 0) {
+                uint16_t* dst = p.o + at * p.hd;
+                const bool any = r.hi > r.lo;
+                if (any) {
+                    ok = warp_wait(&b_o[t], outs & 1, abort_f, p.status);
+                    if (!ok) break;
+                    outs++;
+                    tc_fence_after();
+                }
 #pragma unroll
                 for (int x = 0; x < D; x += 32) {
                     uint32_t ov[32] = {};
-                    if (r.hi > r.lo) {
+                    if (any) {
                         tc_ld32(tm_o + x, ov);
                         tc_wait_ld();
+                        if (x + 32 == D) {  // O_t is in registers
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&b_oe[t]);
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         if (live && x + e < p.hd) {
                             uint4 v;
-                            v.x = bf16x2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
-                            v.y = bf16x2(__uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
-                            v.z = bf16x2(__uint_as_float(ov[e + 4]) * inv, __uint_as_float(ov[e + 5]) * inv);
-                            v.w = bf16x2(__uint_as_float(ov[e + 6]) * inv, __uint_as_float(ov[e + 7]) * inv);
+                            v.x = bf16x2(u2f(ov[e]) * inv, u2f(ov[e + 1]) * inv);
+                            v.y = bf16x2(u2f(ov[e + 2]) * inv, u2f(ov[e + 3]) * inv);
+                            v.z = bf16x2(u2f(ov[e + 4]) * inv, u2f(ov[e + 5]) * inv);
+                            v.w = bf16x2(u2f(ov[e + 6]) * inv, u2f(ov[e + 7]) * inv);
                             *reinterpret_cast<uint4*>(dst + x + e) = v;
                         }
                     }
                 }
             }
+            done_item(k);
         }
     }
 

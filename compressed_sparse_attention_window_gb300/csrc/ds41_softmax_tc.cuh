@@ -29,6 +29,12 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+// x, which all lanes of the warp hold alike, in a form that says so: what is derived
+// from it (loop bounds, stage numbers, descriptors) may live in uniform registers,
+// where the MMAs want their operands.  (Read back from shared memory it would not:
+// 16384-token prompt 1595 us, with this 1380.)
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // One lane of a converged warp, the same one every time.  The warps that issue
 // MMAs run their loops as whole warps and elect a lane around each sequence: a
 // loop that one lane runs alone cannot keep its descriptors in uniform registers,
@@ -44,22 +50,37 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
                                           unsigned int* status) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_f, status));
 }
-// S = Q K^T for 128 rows and 128 keys: both K-major in 64-column blocks of
-// [128 rows][128 bytes], 128-byte swizzled.
+// The two words of a descriptor of 64-column blocks of [rows][128 bytes], 128-byte
+// swizzled: the upper one is the same for all of them (stride 1024 bytes); the
+// lower one holds the address and the leading stride (1 for K-major, the distance
+// of two blocks for N-major).
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+    return (saddr >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    return ((uint64_t)DESC_HI << 32) | lo;
+}
+// S = Q K^T for 128 rows and 128 keys, both K-major.  (The empty statement keeps the
+// compiler from computing all of the steps' descriptors ahead of the key loop: they
+// would not fit the issuing warp's registers.)
 template <int D, uint32_t IDESC>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t q, uint64_t k) {
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t q, uint32_t k) {
+    asm volatile("" : "+r"(q), "+r"(k));
 #pragma unroll
     for (int x = 0; x < D / 16; x++) {
         constexpr uint32_t BLK = 128 * 128;
         const uint32_t off = ((x >> 2) * BLK + (x & 3) * 32) >> 4;
-        tc_mma(d, q + off, k + off, IDESC, x > 0);
+        tc_mma(d, desc_of(q + off), desc_of(k + off), IDESC, x > 0);
     }
 }
-// O (+)= P V, P in tensor memory, V [128 keys][D] in the same blocks
+// O (+)= P V, P in tensor memory, V [128 keys][D] N-major
 template <int D, uint32_t IDESC>
-__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint64_t v, bool acc) {
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t p, uint32_t v, bool acc) {
+    asm volatile("" : "+r"(p), "+r"(v));
 #pragma unroll
-    for (int x = 0; x < 8; x++) tc_mma_ts(d, p + 8 * x, v + ((x * 2048) >> 4), IDESC, acc || x > 0);
+    for (int x = 0; x < 8; x++)
+        tc_mma_ts(d, p + 8 * x, desc_of(v + ((x * 2048) >> 4)), IDESC, acc || x > 0);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     static_assert((2 * C::STAGES + 2 * C::CODES + 2 * SCN + 8) * 8 + 8 +
                           (C::THREADS / 32 + 4) * 8 + 2 * sizeof(Step) <= 1024,
                   "barrier area");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; i++) {
             mbar_init(&b_full[i], E4M3 ? 4 : 1);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     tc_fence_before();
     Share share = find_share<C::THREADS>(a, sh, blockIdx.x == 0);  // (synchronises)
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
     constexpr uint32_t TM_S = 0, TM_O = 256;
     // Every role walks the same pieces; all of them meet where a piece begins (its
     // queries are in shared memory), for one tile of rows again where its streams
@@ -226,11 +226,14 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(E4M3 ? 72 : 88));
         for (int turn = 0; steps[turn & 1].more; turn++) {
             const Step& w = steps[turn & 1];
-            const int32_t* table = a.table + (int64_t)w.pc.b * a.max_pages;
-            const int h = w.pc.h;
-            const int k0 = w.k0, k1 = w.k1, n_blocks = w.n_blocks, n_ring = 2 * n_blocks;
-            const int ring0 = w.ring0, blocks0 = w.blocks0, tail = w.tail, tails0 = w.tails0;
-            const int nt[2] = {w.nt[0], w.nt[1]}, used0[2] = {w.used0[0], w.used0[1]};
+            const int32_t* table = a.table + (int64_t)uniform(w.pc.b) * a.max_pages;
+            const int h = uniform(w.pc.h);
+            const int k0 = uniform(w.k0), k1 = uniform(w.k1);
+            const int n_blocks = uniform(w.n_blocks), n_ring = 2 * n_blocks;
+            const int ring0 = uniform(w.ring0), blocks0 = uniform(w.blocks0);
+            const int tail = uniform(w.tail), tails0 = uniform(w.tails0);
+            const int nt[2] = {uniform(w.nt[0]), uniform(w.nt[1])};
+            const int used0[2] = {uniform(w.used0[0]), uniform(w.used0[1])};
             auto uses = [&](int t, int j) { return PAIR ? nt[t] > 0 : (j & 1) == t; };
             __syncthreads();
             if (threadIdx.x == 96) plan_step<C::QT>(a, share, w, steps[(turn + 1) & 1]);
@@ -358,9 +361,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             } else if (warp == 1 && ok) {
                 constexpr uint32_t IDESC_S = E4M3 ? idesc_f16(128, KB, 0, 0) : idesc_bf16(128, KB, 0, 0);
                 constexpr uint32_t IDESC_O = E4M3 ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
-                const uint64_t qd = sdesc(sbase + C::Q_OFF, 16, 1024);
-                const uint64_t kd = sdesc(sbase + C::KV_OFF, 16, 1024);
-                const uint64_t vd = sdesc(sbase + C::KV_OFF, C::BLK, 1024);
+                const uint32_t qd = desc_lo(sbase + C::Q_OFF, 16);
+                const uint32_t kd = desc_lo(sbase + C::KV_OFF, 16);
+                const uint32_t vd = desc_lo(sbase + C::KV_OFF, C::BLK);
                 int done_p[2] = {0, 0};
                 auto wait_entry = [&](int e) {
                     const int ge = ring0 + e;
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             (ch >> 2) * C::BLK + r_in * 128 + (uint32_t)(((c0 + 1) ^ (r_in & 7)) << 4);
         for (int turn = 0; steps[turn & 1].more; turn++) {
             const Step& w = steps[turn & 1];
-            const int n_ring = 2 * w.n_blocks, ring0 = w.ring0;
+            const int n_ring = 2 * uniform(w.n_blocks), ring0 = uniform(w.ring0);
             __syncthreads();
             for (int e = 0; e < n_ring && ok; e++) {
                 const int ge = ring0 + e, cs = ge % C::CODES, st = ge % C::STAGES;
@@ -562,8 +565,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const bool live = row < w.rows;
                 const bool idle = !__any_sync(0xffffffffu, live);  // none of the warp's rows is
                 const RowView view = row_view(a, w.pc.s, min(row, w.rows - 1) / a.G);
-                const int nt = w.nt[t], n_blocks = w.n_blocks;
-                const int k0 = w.k0, blocks0 = w.blocks0, used0 = w.used0[t];
+                const int nt = uniform(w.nt[t]), n_blocks = uniform(w.n_blocks);
+                const int k0 = uniform(w.k0), blocks0 = uniform(w.blocks0);
+                const int used0 = uniform(w.used0[t]);
                 float c = a.scale_log2;
                 if (E4M3)
                     c *= exp2f((float)reinterpret_cast<const int8_t*>(
