@@ -630,6 +630,10 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                     }
                 }
                 if (nt > 0 && ok) ok = warp_wait(&b_o[t], w.ends0[t] & 1, abort_f, a.status);
+                // (the exchange below lies in the ring: the other stream's last products
+                // have to have read it too)
+                if (!PAIR && t == 1 && nt > 0 && ok)
+                    ok = warp_wait(&b_o[0], w.ends0[0] & 1, abort_f, a.status);
                 tc_fence_after();
                 end_m = st.reference(c);
                 end_l = st.l;

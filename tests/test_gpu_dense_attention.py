@@ -385,6 +385,15 @@ def test_tree_strided_queries():
     run_tree(gen(42), *TREES[5], q_heads_out=True)
 
 
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_tree_of_middling_rows_over_long_caches(e4m3):
+    """17 to 128 rows per key/value head: one tile of rows, odd and even numbers of
+    blocks a piece, streams that end one after the other."""
+    run_tree(gen(61), [4000, 2417, 900, 129], [16, 9, 16, 5], 32, 8, 128, 64, e4m3, 0, False, True)
+    run_tree(gen(62), [6001], [30], 16, 4, 64, 128, e4m3, 0, True, True)
+    run_tree(gen(63), [3333] * 9, [5] * 9, 16, 2, 128, 32, e4m3, 1000, False, False)
+
+
 @pytest.mark.parametrize("spread", [3, 12, 40])
 @pytest.mark.parametrize("case", [3, 10, 12, 15])
 def test_tree_scales_far_apart(case, spread):
