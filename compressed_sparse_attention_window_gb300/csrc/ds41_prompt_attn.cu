@@ -233,10 +233,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* b_item = b_fix + 1;              // an item is known [ITEMS]
     uint64_t* b_iteme = b_item + ITEMS;        // and every role is through with it
     uint64_t* b_clc = b_iteme + ITEMS;         // the answer to a request for another item
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_clc + 1);
+    uint64_t* b_end = b_clc + 1;               // every product is complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_end + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
     Item* items = reinterpret_cast<Item*>(tmem_slot + 2);
-    static_assert((2 * C::QB + 2 * C::STAGES + 11 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <= 624,
+    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <= 624,
                   "barrier area");
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&b_iteme[i], 11);
         }
         mbar_init(b_clc, 1);
+        mbar_init(b_end, 1);
         *abort_f = 0;
         mbar_init_fence();
     }
@@ -440,6 +442,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 done_item(k);
             }
+            // tensor memory is given back with nothing in flight, whatever gave up
+            if (elect_one()) tc_commit(b_end);
+            __syncwarp();
+            drain_bar(b_end, 0, p.status);
         } else if (warp == 2) {
             // zero the V rows behind the last key
             uint32_t ring0 = 0, tails = 0;

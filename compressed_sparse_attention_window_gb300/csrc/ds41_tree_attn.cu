@@ -69,354 +69,354 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     Share share = find_share<NT>(a, sh, blockIdx.x == 0);
     Piece pc;
     while (next_piece(a, share, pc)) {
-    const Seq s = pc.s;
-    const int h = pc.h;
-    const int rows = s.n * a.G;  // at most 16
-    const int k0 = first_key(a, s) + pc.first * BLOCK, k1 = min(s.len, k0 + pc.count * BLOCK);
-    if (threadIdx.x == 0) note_ends(a, pc);
+        const Seq s = pc.s;
+        const int h = pc.h;
+        const int rows = s.n * a.G;  // at most 16
+        const int k0 = first_key(a, s) + pc.first * BLOCK, k1 = min(s.len, k0 + pc.count * BLOCK);
+        if (threadIdx.x == 0) note_ends(a, pc);
 
-    uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
-    const int n_groups = (k1 - k0 + GROUP - 1) / GROUP;
-    const int mine = (n_groups - warp + WARPS - 1) / WARPS;  // groups warp, warp + 4, ...
-    const int32_t* table = a.table + (int64_t)pc.b * a.max_pages;
-    unsigned bad = 0;  // stages whose page does not exist
+        uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
+        const int n_groups = (k1 - k0 + GROUP - 1) / GROUP;
+        const int mine = (n_groups - warp + WARPS - 1) / WARPS;  // groups warp, warp + 4, ...
+        const int32_t* table = a.table + (int64_t)pc.b * a.max_pages;
+        unsigned bad = 0;  // stages whose page does not exist
 
-    // what of the addresses does not change: a lane copies piece ch of the rows
-    // r_in, r_in + RPI, ...
-    constexpr int RPI = 32 / C::CH;
-    const int r_in = lane / C::CH, ch = lane % C::CH;
-    const int rb = a.hd * (E4M3 ? 1 : 2);  // bytes of a row in the cache
-    const bool in_row = ch * 16 < rb;
-    const int lane_off = r_in * rb + ch * 16, head_rows = h * a.kv.page;
-    const uint32_t ring_u = smem_u32(ring);
-    // (looked up a group ahead)
-    auto page_of = [&](int i) {
-        return i < mine ? table[(k0 + (i * WARPS + warp) * GROUP) >> a.kv.page_shift] : -1;
-    };
-    int page = page_of(0);
-    auto fetch = [&](int i) {
-        if (i < mine) {
-            const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
-            const int pg = page;
-            page = page_of(i + 1);
-            const bool ok = pg >= 0 && pg < a.kv.n_pages;
-            if (!ok && lane == 0) raise_status(a.status, DS41_E_INDEX);
-            bad = ok ? bad & ~(1u << st) : bad | (1u << st);
-            const int64_t row =
-                ok ? (int64_t)pg * a.kvh * a.kv.page + (head_rows + (j & (a.kv.page - 1))) : 0;
-            const uint32_t dst = ring_u + st * C::STAGE + lane / C::CH * C::RB;
-            const uint8_t* kp = a.kv.k + row * rb + lane_off;
-            const uint8_t* vp = a.kv.v + row * rb + lane_off;
-            // rows behind the sequence's end are read as zeros, whatever they hold
-            const int live = ok ? min(GROUP, k1 - j) : 0;
-            if (live == GROUP && rb == C::RB) {
+        // what of the addresses does not change: a lane copies piece ch of the rows
+        // r_in, r_in + RPI, ...
+        constexpr int RPI = 32 / C::CH;
+        const int r_in = lane / C::CH, ch = lane % C::CH;
+        const int rb = a.hd * (E4M3 ? 1 : 2);  // bytes of a row in the cache
+        const bool in_row = ch * 16 < rb;
+        const int lane_off = r_in * rb + ch * 16, head_rows = h * a.kv.page;
+        const uint32_t ring_u = smem_u32(ring);
+        // (looked up a group ahead)
+        auto page_of = [&](int i) {
+            return i < mine ? table[(k0 + (i * WARPS + warp) * GROUP) >> a.kv.page_shift] : -1;
+        };
+        int page = page_of(0);
+        auto fetch = [&](int i) {
+            if (i < mine) {
+                const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
+                const int pg = page;
+                page = page_of(i + 1);
+                const bool ok = pg >= 0 && pg < a.kv.n_pages;
+                if (!ok && lane == 0) raise_status(a.status, DS41_E_INDEX);
+                bad = ok ? bad & ~(1u << st) : bad | (1u << st);
+                const int64_t row =
+                    ok ? (int64_t)pg * a.kvh * a.kv.page + (head_rows + (j & (a.kv.page - 1))) : 0;
+                const uint32_t dst = ring_u + st * C::STAGE + lane / C::CH * C::RB;
+                const uint8_t* kp = a.kv.k + row * rb + lane_off;
+                const uint8_t* vp = a.kv.v + row * rb + lane_off;
+                // rows behind the sequence's end are read as zeros, whatever they hold
+                const int live = ok ? min(GROUP, k1 - j) : 0;
+                if (live == GROUP && rb == C::RB) {
 #pragma unroll
-                for (int x = 0; x < GROUP / RPI; x++) {
-                    const int r = x * RPI + r_in;
-                    const uint32_t to = dst + x * RPI * C::RB;
-                    cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + x * RPI * C::RB, true);
-                    cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16,
-                               vp + x * RPI * C::RB, true);
+                    for (int x = 0; x < GROUP / RPI; x++) {
+                        const int r = x * RPI + r_in;
+                        const uint32_t to = dst + x * RPI * C::RB;
+                        cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + x * RPI * C::RB, true);
+                        cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16,
+                                   vp + x * RPI * C::RB, true);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < GROUP / RPI; x++) {
+                        const int r = x * RPI + r_in;
+                        const uint32_t to = dst + x * RPI * C::RB;
+                        const bool in = r < live && in_row;
+                        const int off = in ? x * RPI * rb : -lane_off;
+                        cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + off, in);
+                        cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16, vp + off, in);
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int x = 0; x < GROUP / RPI; x++) {
-                    const int r = x * RPI + r_in;
-                    const uint32_t to = dst + x * RPI * C::RB;
-                    const bool in = r < live && in_row;
-                    const int off = in ? x * RPI * rb : -lane_off;
-                    cp_async16(to + k_piece<C::RB>(r, ch) * 16, kp + off, in);
-                    cp_async16(to + GROUP * C::RB + v_piece<C::RB>(r, ch) * 16, vp + off, in);
+                if (E4M3 && lane < 8) {
+                    const float* src = (lane < 4 ? a.kv.ks : a.kv.vs) + row + (lane & 3) * 4;
+                    cp_async16(ring_u + st * C::STAGE + 2 * GROUP * C::RB + lane * 16, src, ok);
                 }
             }
-            if (E4M3 && lane < 8) {
-                const float* src = (lane < 4 ? a.kv.ks : a.kv.vs) + row + (lane & 3) * 4;
-                cp_async16(ring_u + st * C::STAGE + 2 * GROUP * C::RB + lane * 16, src, ok);
-            }
-        }
-        cp_async_commit();
-    };
+            cp_async_commit();
+        };
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; i++) fetch(i);
+        for (int i = 0; i < C::STAGES - 1; i++) fetch(i);
 
-    // the queries: rows g and g + 8 of the tile, hd in the order of the keys'
-    // fragments (fp8: lane c owns bytes 16 c .. and 64 + 16 c .. of a row, bf16:
-    // 16 c + 64 i ..; four elements a step)
-    RowView view[2];
-    uint32_t qf[HD / 16][4];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int r = min(g + 8 * i, rows - 1);
-        const int t = r / a.G;
-        view[i] = row_view(a, s, t);
-        const uint16_t* qp = a.q + (s.q0 + t) * a.q_tok + (h * a.G + r % a.G) * a.q_head;
-#pragma unroll
-        for (int st = 0; st < HD / 16; st++) {
-            const int d = E4M3 ? (c + 4 * (st / 4)) * 16 + 4 * (st % 4)
-                               : (c + 4 * (st / 2)) * 8 + 4 * (st % 2);
-            const uint2 v = d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
-            qf[st][i] = v.x;
-            qf[st][i + 2] = v.y;
-        }
-    }
-    float cr[2] = {a.scale_log2, a.scale_log2};
-    if (E4M3) {
+        // the queries: rows g and g + 8 of the tile, hd in the order of the keys'
+        // fragments (fp8: lane c owns bytes 16 c .. and 64 + 16 c .. of a row, bf16:
+        // 16 c + 64 i ..; four elements a step)
+        RowView view[2];
+        uint32_t qf[HD / 16][4];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            uint32_t m2 = 0;
-#pragma unroll
-            for (int st = 0; st < HD / 16; st++)
-                m2 = __vmaxu2(m2, __vmaxu2(qf[st][i] & 0x7fff7fffu, qf[st][i + 2] & 0x7fff7fffu));
-            uint32_t mb = max(m2 & 0xffffu, m2 >> 16);  // four lanes have the row
-            mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-            mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-            const int e = query_exponent(mb);
-            const float down = exp2f((float)-e);
-            cr[i] *= exp2f((float)e);
+            const int r = min(g + 8 * i, rows - 1);
+            const int t = r / a.G;
+            view[i] = row_view(a, s, t);
+            const uint16_t* qp = a.q + (s.q0 + t) * a.q_tok + (h * a.G + r % a.G) * a.q_head;
 #pragma unroll
             for (int st = 0; st < HD / 16; st++) {
-                qf[st][i] = bf16x2_to_f16x2(qf[st][i], down);
-                qf[st][i + 2] = bf16x2_to_f16x2(qf[st][i + 2], down);
+                const int d = E4M3 ? (c + 4 * (st / 4)) * 16 + 4 * (st % 4)
+                                   : (c + 4 * (st / 2)) * 8 + 4 * (st % 2);
+                const uint2 v = d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
+                qf[st][i] = v.x;
+                qf[st][i + 2] = v.y;
             }
         }
-    }
-    // keys below `easy` are seen by both rows (and none lies at or before lo)
-    const int easy = min(view[0].pre, view[1].pre);
-    const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
-
-    float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
-    float lr = E4M3 ? tc::RowState::VS_MIN : 0.0f, vlim = 0.0f;
-    float base[2] = {0.0f, 0.0f};  // c m + lr: what an exponent is reduced by
-    for (int i = 0; i < mine; i++) {
-        fetch(i + C::STAGES - 1);
-        cp_async_wait<C::STAGES - 1>();
-        __syncwarp();
-        const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
-        const uint8_t* kx = ring + st * C::STAGE;
-        const uint8_t* vx = kx + GROUP * C::RB;
-        const float* sx = reinterpret_cast<const float*>(kx + 2 * GROUP * C::RB);
-        float sc[2][4] = {};
-        // ---- S = Q K^T ----
-#pragma unroll
-        for (int x = 0; x < C::CH / 4; x++) {
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const int r = n * 8 + g;
-                const uint4 kv = *reinterpret_cast<const uint4*>(
-                    kx + r * C::RB + k_piece<C::RB>(r, c + 4 * x) * 16);
-                const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
-                if (E4M3) {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int q = 4 * x + e;
-                        uint32_t lo16, hi16;
-                        e4m3x4_to_f16(w[e], lo16, hi16);
-                        mma_f16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], lo16, hi16);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int q = 2 * x + e;
-                        mma_bf16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], w[2 * e],
-                                 w[2 * e + 1]);
-                    }
-                }
-            }
-        }
-        // ---- softmax: this lane has rows g, g + 8 and keys 2c, 2c+1, 2c+8, 2c+9 ----
-        float2 ks[2], vs[2];
+        float cr[2] = {a.scale_log2, a.scale_log2};
         if (E4M3) {
 #pragma unroll
-            for (int n = 0; n < 2; n++) {
-                ks[n] = *reinterpret_cast<const float2*>(sx + n * 8 + 2 * c);
-                vs[n] = *reinterpret_cast<const float2*>(sx + 16 + n * 8 + 2 * c);
+            for (int i = 0; i < 2; i++) {
+                uint32_t m2 = 0;
 #pragma unroll
-                for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
-            }
-        }
-        const bool masked = ((bad >> st) & 1) || j + GROUP > easy || j <= lo;
-        if (masked) {
+                for (int st = 0; st < HD / 16; st++)
+                    m2 = __vmaxu2(m2, __vmaxu2(qf[st][i] & 0x7fff7fffu, qf[st][i + 2] & 0x7fff7fffu));
+                uint32_t mb = max(m2 & 0xffffu, m2 >> 16);  // four lanes have the row
+                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+                const int e = query_exponent(mb);
+                const float down = exp2f((float)-e);
+                cr[i] *= exp2f((float)e);
 #pragma unroll
-            for (int n = 0; n < 2; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (((bad >> st) & 1) ||
-                        !seen(view[e >> 1], j + n * 8 + 2 * c + (e & 1), s.len))
-                        sc[n][e] = -INFINITY;
-        }
-        float mx[2];
-#pragma unroll
-        for (int i2 = 0; i2 < 2; i2++)
-            mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
-                           fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
-        // scales that no key needs (behind the sequence's end) may be NaN: fmaxf skips them
-        float vm = E4M3 ? fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y)) : 0.0f;
-        const bool moves = (mx[0] - m[0]) * cr[0] > tc::SM_RESCALE_LOG2 ||
-                           (mx[1] - m[1]) * cr[1] > tc::SM_RESCALE_LOG2;
-        if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
-            float shift = 0.0f;
-            if (E4M3) {
-                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                if (vm > vlim) {
-                    const float to = tc::scale_exponent(vm);
-                    shift = lr - to;
-                    lr = to;
-                    vlim = exp2f(to + 8.0f);
+                for (int st = 0; st < HD / 16; st++) {
+                    qf[st][i] = bf16x2_to_f16x2(qf[st][i], down);
+                    qf[st][i + 2] = bf16x2_to_f16x2(qf[st][i + 2], down);
                 }
             }
+        }
+        // keys below `easy` are seen by both rows (and none lies at or before lo)
+        const int easy = min(view[0].pre, view[1].pre);
+        const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
+
+        float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
+        float lr = E4M3 ? tc::RowState::VS_MIN : 0.0f, vlim = 0.0f;
+        float base[2] = {0.0f, 0.0f};  // c m + lr: what an exponent is reduced by
+        for (int i = 0; i < mine; i++) {
+            fetch(i + C::STAGES - 1);
+            cp_async_wait<C::STAGES - 1>();
+            __syncwarp();
+            const int st = i % C::STAGES, j = k0 + (i * WARPS + warp) * GROUP;
+            const uint8_t* kx = ring + st * C::STAGE;
+            const uint8_t* vx = kx + GROUP * C::RB;
+            const float* sx = reinterpret_cast<const float*>(kx + 2 * GROUP * C::RB);
+            float sc[2][4] = {};
+            // ---- S = Q K^T ----
+#pragma unroll
+            for (int x = 0; x < C::CH / 4; x++) {
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    const int r = n * 8 + g;
+                    const uint4 kv = *reinterpret_cast<const uint4*>(
+                        kx + r * C::RB + k_piece<C::RB>(r, c + 4 * x) * 16);
+                    const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
+                    if (E4M3) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const int q = 4 * x + e;
+                            uint32_t lo16, hi16;
+                            e4m3x4_to_f16(w[e], lo16, hi16);
+                            mma_f16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], lo16, hi16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int q = 2 * x + e;
+                            mma_bf16(sc[n], qf[q][0], qf[q][1], qf[q][2], qf[q][3], w[2 * e],
+                                     w[2 * e + 1]);
+                        }
+                    }
+                }
+            }
+            // ---- softmax: this lane has rows g, g + 8 and keys 2c, 2c+1, 2c+8, 2c+9 ----
+            float2 ks[2], vs[2];
+            if (E4M3) {
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    ks[n] = *reinterpret_cast<const float2*>(sx + n * 8 + 2 * c);
+                    vs[n] = *reinterpret_cast<const float2*>(sx + 16 + n * 8 + 2 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sc[n][e] *= (e & 1) ? ks[n].y : ks[n].x;
+                }
+            }
+            const bool masked = ((bad >> st) & 1) || j + GROUP > easy || j <= lo;
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < 2; n++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (((bad >> st) & 1) ||
+                            !seen(view[e >> 1], j + n * 8 + 2 * c + (e & 1), s.len))
+                            sc[n][e] = -INFINITY;
+            }
+            float mx[2];
+#pragma unroll
+            for (int i2 = 0; i2 < 2; i2++)
+                mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
+                               fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
+            // scales that no key needs (behind the sequence's end) may be NaN: fmaxf skips them
+            float vm = E4M3 ? fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y)) : 0.0f;
+            const bool moves = (mx[0] - m[0]) * cr[0] > tc::SM_RESCALE_LOG2 ||
+                               (mx[1] - m[1]) * cr[1] > tc::SM_RESCALE_LOG2;
+            if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
+                float shift = 0.0f;
+                if (E4M3) {
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                    if (vm > vlim) {
+                        const float to = tc::scale_exponent(vm);
+                        shift = lr - to;
+                        lr = to;
+                        vlim = exp2f(to + 8.0f);
+                    }
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < 2; i2++) {
+                    float t = mx[i2], sh = shift;
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                    if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
+                        sh += (m[i2] - t) * cr[i2];
+                        m[i2] = t;
+                    }
+                    const float f = exp2f(sh);
+                    l[i2] *= f;
+#pragma unroll
+                    for (int d = 0; d < HD / 8; d++) {
+                        o[d][2 * i2] *= f;
+                        o[d][2 * i2 + 1] *= f;
+                    }
+                    base[i2] = m[i2] == -INFINITY ? 0.0f : fmaf(m[i2], cr[i2], lr);
+                }
+            }
+            uint32_t pf[4];
 #pragma unroll
             for (int i2 = 0; i2 < 2; i2++) {
-                float t = mx[i2], sh = shift;
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
-                    sh += (m[i2] - t) * cr[i2];
-                    m[i2] = t;
+                float less = base[i2], at = 0.0f;
+                if (fabsf(less) > 0x1p22f) {  // c m is rounded too far: the difference first
+                    less = lr;
+                    at = m[i2];
                 }
-                const float f = exp2f(sh);
-                l[i2] *= f;
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    const float p0 = ex2(fmaf(sc[n][2 * i2] - at, cr[i2], -less));
+                    const float p1 = ex2(fmaf(sc[n][2 * i2 + 1] - at, cr[i2], -less));
+                    l[i2] += p0 + p1;
+                    if (!E4M3) {
+                        pf[2 * n + i2] = bf16x2(p0, p1);
+                        continue;
+                    }
+                    float w0 = p0 * vs[n].x, w1 = p1 * vs[n].y;
+                    if (masked) {
+                        // a row that is not seen weighs nothing, whatever its scale holds
+                        if (sc[n][2 * i2] == -INFINITY) w0 = 0.0f;
+                        if (sc[n][2 * i2 + 1] == -INFINITY) w1 = 0.0f;
+                    }
+                    pf[2 * n + i2] = tc::f16x2(w0, w1);
+                }
+            }
+            // ---- O += P V: n-tile d holds the columns g HD/8 + d ----
+            if (E4M3) {
+                uint32_t w[4][HD / 32];
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                    if (HD == 128) {
+                        *reinterpret_cast<uint4*>(w[r]) = *reinterpret_cast<const uint4*>(
+                            vx + row * C::RB + v_piece<C::RB>(row, g) * 16);
+                    } else {
+                        *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(
+                            vx + row * C::RB + v_piece<C::RB>(row, g >> 1) * 16 + (g & 1) * 8);
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < HD / 8; d += 2) {
+                    // bytes d, d + 1 of two rows, side by side
+                    const uint32_t sel = (d & 2) ? 0x7362u : 0x5140u;
+                    uint32_t a0, a1, b0, b1;
+                    e4m3x4_to_f16(__byte_perm(w[0][d / 4], w[1][d / 4], sel), a0, a1);
+                    e4m3x4_to_f16(__byte_perm(w[2][d / 4], w[3][d / 4], sel), b0, b1);
+                    mma_f16(o[d], pf[0], pf[1], pf[2], pf[3], a0, b0);
+                    mma_f16(o[d + 1], pf[0], pf[1], pf[2], pf[3], a1, b1);
+                }
+            } else {
+                uint32_t w[4][HD / 16];
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+                    for (int x = 0; x < HD / 64; x++)
+                        *reinterpret_cast<uint4*>(w[r] + 4 * x) = *reinterpret_cast<const uint4*>(
+                            vx + row * C::RB + v_piece<C::RB>(row, g * (HD / 64) + x) * 16);
+                }
 #pragma unroll
                 for (int d = 0; d < HD / 8; d++) {
-                    o[d][2 * i2] *= f;
-                    o[d][2 * i2 + 1] *= f;
+                    const uint32_t sel = (d & 1) ? 0x7632u : 0x5410u;
+                    mma_bf16(o[d], pf[0], pf[1], pf[2], pf[3],
+                             __byte_perm(w[0][d / 2], w[1][d / 2], sel),
+                             __byte_perm(w[2][d / 2], w[3][d / 2], sel));
                 }
-                base[i2] = m[i2] == -INFINITY ? 0.0f : fmaf(m[i2], cr[i2], lr);
             }
+            __syncwarp();  // the stage is read before it is filled again
         }
-        uint32_t pf[4];
+        cp_async_wait<0>();
+        __syncthreads();
+        // ---- the warps' results: through shared memory, 16 rows ----
+        constexpr int P = HD + 4;
+        float* out = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int i2 = 0; i2 < 2; i2++) {
-            float less = base[i2], at = 0.0f;
-            if (fabsf(less) > 0x1p22f) {  // c m is rounded too far: the difference first
-                less = lr;
-                at = m[i2];
-            }
-#pragma unroll
-            for (int n = 0; n < 2; n++) {
-                const float p0 = ex2(fmaf(sc[n][2 * i2] - at, cr[i2], -less));
-                const float p1 = ex2(fmaf(sc[n][2 * i2 + 1] - at, cr[i2], -less));
-                l[i2] += p0 + p1;
-                if (!E4M3) {
-                    pf[2 * n + i2] = bf16x2(p0, p1);
-                    continue;
-                }
-                float w0 = p0 * vs[n].x, w1 = p1 * vs[n].y;
-                if (masked) {
-                    // a row that is not seen weighs nothing, whatever its scale holds
-                    if (sc[n][2 * i2] == -INFINITY) w0 = 0.0f;
-                    if (sc[n][2 * i2 + 1] == -INFINITY) w1 = 0.0f;
-                }
-                pf[2 * n + i2] = tc::f16x2(w0, w1);
-            }
-        }
-        // ---- O += P V: n-tile d holds the columns g HD/8 + d ----
-        if (E4M3) {
-            uint32_t w[4][HD / 32];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                if (HD == 128) {
-                    *reinterpret_cast<uint4*>(w[r]) = *reinterpret_cast<const uint4*>(
-                        vx + row * C::RB + v_piece<C::RB>(row, g) * 16);
-                } else {
-                    *reinterpret_cast<uint2*>(w[r]) = *reinterpret_cast<const uint2*>(
-                        vx + row * C::RB + v_piece<C::RB>(row, g >> 1) * 16 + (g & 1) * 8);
-                }
-            }
-#pragma unroll
-            for (int d = 0; d < HD / 8; d += 2) {
-                // bytes d, d + 1 of two rows, side by side
-                const uint32_t sel = (d & 2) ? 0x7362u : 0x5140u;
-                uint32_t a0, a1, b0, b1;
-                e4m3x4_to_f16(__byte_perm(w[0][d / 4], w[1][d / 4], sel), a0, a1);
-                e4m3x4_to_f16(__byte_perm(w[2][d / 4], w[3][d / 4], sel), b0, b1);
-                mma_f16(o[d], pf[0], pf[1], pf[2], pf[3], a0, b0);
-                mma_f16(o[d + 1], pf[0], pf[1], pf[2], pf[3], a1, b1);
-            }
-        } else {
-            uint32_t w[4][HD / 16];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-#pragma unroll
-                for (int x = 0; x < HD / 64; x++)
-                    *reinterpret_cast<uint4*>(w[r] + 4 * x) = *reinterpret_cast<const uint4*>(
-                        vx + row * C::RB + v_piece<C::RB>(row, g * (HD / 64) + x) * 16);
+        for (int i = 0; i < 2; i++) {
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            float* row = out + (warp * 16 + g + 8 * i) * P;
+            if (c == 0) {
+                row[HD] = m[i] == -INFINITY ? -INFINITY : fmaf(m[i], cr[i], lr);
+                row[HD + 1] = l[i];
             }
 #pragma unroll
             for (int d = 0; d < HD / 8; d++) {
-                const uint32_t sel = (d & 1) ? 0x7632u : 0x5410u;
-                mma_bf16(o[d], pf[0], pf[1], pf[2], pf[3],
-                         __byte_perm(w[0][d / 2], w[1][d / 2], sel),
-                         __byte_perm(w[2][d / 2], w[3][d / 2], sel));
+                row[2 * c * (HD / 8) + d] = o[d][2 * i];
+                row[(2 * c + 1) * (HD / 8) + d] = o[d][2 * i + 1];
             }
         }
-        __syncwarp();  // the stage is read before it is filled again
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-    // ---- the warps' results: through shared memory, 16 rows ----
-    constexpr int P = HD + 4;
-    float* out = reinterpret_cast<float*>(smem);
+        __syncthreads();
+        constexpr int PER = NT / 16;  // threads of a row
+        const int r = threadIdx.x / PER, part = threadIdx.x % PER;
+        if (r < rows) {
+            float mm = -INFINITY, f[WARPS], ll = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        float* row = out + (warp * 16 + g + 8 * i) * P;
-        if (c == 0) {
-            row[HD] = m[i] == -INFINITY ? -INFINITY : fmaf(m[i], cr[i], lr);
-            row[HD + 1] = l[i];
-        }
-#pragma unroll
-        for (int d = 0; d < HD / 8; d++) {
-            row[2 * c * (HD / 8) + d] = o[d][2 * i];
-            row[(2 * c + 1) * (HD / 8) + d] = o[d][2 * i + 1];
-        }
-    }
-    __syncthreads();
-    constexpr int PER = NT / 16;  // threads of a row
-    const int r = threadIdx.x / PER, part = threadIdx.x % PER;
-    if (r < rows) {
-        float mm = -INFINITY, f[WARPS], ll = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + r) * P + HD]);
-        const float base = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-        for (int w = 0; w < WARPS; w++) {
-            f[w] = exp2f(out[(w * 16 + r) * P + HD] - base);
-            ll += f[w] * out[(w * 16 + r) * P + HD + 1];
-        }
-        const int t = r / a.G, head = h * a.G + r % a.G;
-        const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
-        const bool whole = is_whole(pc);
-        float inv = 1.0f;
-        if (whole) {
-            const tc::RowEnd end = tc::row_end(mm, ll, a.sink ? a.sink[head] : -INFINITY);
-            inv = end.factor;
-            if (a.lse && part == 0) a.lse[at] = end.lse;
-        } else if (part == 0) {
-            a.part_ml[slot_of(pc) * 16 + r] = make_float2(mm, ll);
-        }
-        float* po = a.part + (slot_of(pc) * 16 + r) * a.hd;
-        for (int x = part * 4; x < a.hd; x += PER * 4) {
-            float v[4] = {0, 0, 0, 0};
+            for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + r) * P + HD]);
+            const float base = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
             for (int w = 0; w < WARPS; w++) {
-                const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + r) * P + x]);
-                v[0] += f[w] * ow.x;
-                v[1] += f[w] * ow.y;
-                v[2] += f[w] * ow.z;
-                v[3] += f[w] * ow.w;
+                f[w] = exp2f(out[(w * 16 + r) * P + HD] - base);
+                ll += f[w] * out[(w * 16 + r) * P + HD + 1];
             }
-            if (whole)
-                *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
-                    make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
-            else
-                *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
+            const int t = r / a.G, head = h * a.G + r % a.G;
+            const int64_t at = (int64_t)(s.q0 + t) * a.nh + head;
+            const bool whole = is_whole(pc);
+            float inv = 1.0f;
+            if (whole) {
+                const tc::RowEnd end = tc::row_end(mm, ll, a.sink ? a.sink[head] : -INFINITY);
+                inv = end.factor;
+                if (a.lse && part == 0) a.lse[at] = end.lse;
+            } else if (part == 0) {
+                a.part_ml[slot_of(pc) * 16 + r] = make_float2(mm, ll);
+            }
+            float* po = a.part + (slot_of(pc) * 16 + r) * a.hd;
+            for (int x = part * 4; x < a.hd; x += PER * 4) {
+                float v[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int w = 0; w < WARPS; w++) {
+                    const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + r) * P + x]);
+                    v[0] += f[w] * ow.x;
+                    v[1] += f[w] * ow.y;
+                    v[2] += f[w] * ow.z;
+                    v[3] += f[w] * ow.w;
+                }
+                if (whole)
+                    *reinterpret_cast<uint2*>(a.o + at * a.hd + x) =
+                        make_uint2(bf16x2(v[0] * inv, v[1] * inv), bf16x2(v[2] * inv, v[3] * inv));
+                else
+                    *reinterpret_cast<float4*>(po + x) = make_float4(v[0], v[1], v[2], v[3]);
+            }
         }
-    }
-    __syncthreads();  // the results are read before the rings are filled again
+        __syncthreads();  // the results are read before the rings are filled again
     }
     pdl_trigger();
 }

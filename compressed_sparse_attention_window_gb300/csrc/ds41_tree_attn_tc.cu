@@ -166,11 +166,12 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     uint64_t* b_o = b_p + 2;                  // O_t complete [2]
     uint64_t* b_tail = b_o + 2;               // the V block with the last key landed
     uint64_t* b_fix = b_tail + 1;             // its rows behind the last key are zero
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_fix + 1);
+    uint64_t* b_end = b_fix + 1;              // every product is complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_end + 2);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int64_t* sh = reinterpret_cast<int64_t*>(tmem_slot + 2);
     Step* steps = reinterpret_cast<Step*>(sh + C::THREADS / 32 + 4);
-    static_assert((2 * C::STAGES + 2 * C::CODES + 2 * SCN + 8) * 8 + 8 +
+    static_assert((2 * C::STAGES + 2 * C::CODES + 2 * SCN + 10) * 8 + 8 +
                           (C::THREADS / 32 + 4) * 8 + 2 * sizeof(Step) <= 1024,
                   "barrier area");
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
         }
         mbar_init(b_tail, 1);
         mbar_init(b_fix, 1);
+        mbar_init(b_end, 1);
         *abort_f = 0;
         mbar_init_fence();
     }
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 for (int j = 0; j < min(C::LA, n_blocks) && ok; j++) {
                     ok = wait_entry(j);
                     if (ok && elect_one()) {
-    #pragma unroll
+#pragma unroll
                         for (int t = 0; t < 2; t++)
                             if (uses(t, j)) scores(t, j);
                         tc_commit(&b_empty[stage_of(j)]);
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                         tc_fence_after();
                     }
                     bool have_k = false;
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < 2; t++) {
                         const bool now = uses(t, j), next = more && uses(t, j + C::LA);
                         if (ok && now) {
@@ -431,6 +433,12 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             if (!PAIR) __syncthreads();
             __syncthreads();
             if (*abort_f) ok = false;
+        }
+        if (warp == 1) {
+            // tensor memory is given back with nothing in flight, whatever gave up
+            if (elect_one()) tc_commit(b_end);
+            __syncwarp();
+            drain_bar(b_end, 0, a.status);
         }
     } else if (E4M3 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
@@ -607,7 +615,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                             if ((w >> (b4 + 1)) & 1) vmax = fmaxf(vmax, v4.y);
                             if ((w >> (b4 + 2)) & 1) vmax = fmaxf(vmax, v4.z);
                             if ((w >> (b4 + 3)) & 1) vmax = fmaxf(vmax, v4.w);
-    #pragma unroll
+#pragma unroll
                             for (int off = 16; off > 0; off >>= 1)
                                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
                         }
@@ -643,12 +651,12 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                                (32 * (warp & 3) + lane) * C::XP;
                     x[D] = end_m;
                     x[D + 1] = end_l;
-    #pragma unroll 1
+#pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
                         uint32_t ov[16];
                         tc_ld16(tm_o + d, ov);
                         tc_wait_ld();
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < 16; e += 4)
                             *reinterpret_cast<uint4*>(x + d + e) =
                                 make_uint4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
@@ -683,17 +691,17 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const int64_t slot = slot_of(w.pc) * a.tile_rows + 128 * t + row_in;
                 if (live && !whole) a.part_ml[slot] = make_float2(m, l);
                 if (w.nt[t] > 0) {
-    #pragma unroll 1
+#pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
                         uint32_t ov[16];
                         float v[16];
                         tc_ld16(tm_o + d, ov);
                         tc_wait_ld();
                         if (!live || d >= a.hd) continue;
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < 16; e++) v[e] = u2f(ov[e]) * f;
                         if (both) {
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 16; e += 4) {
                                 const float4 y = *reinterpret_cast<const float4*>(x + d + e);
                                 v[e] += y.x * fx;
@@ -704,14 +712,14 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                         }
                         if (whole) {
                             uint4* dst = reinterpret_cast<uint4*>(a.o + at * a.hd + d);
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 16; e += 8)
                                 dst[e / 8] =
                                     make_uint4(bf16x2(v[e], v[e + 1]), bf16x2(v[e + 2], v[e + 3]),
                                                bf16x2(v[e + 4], v[e + 5]), bf16x2(v[e + 6], v[e + 7]));
                         } else {
                             float4* dst = reinterpret_cast<float4*>(a.part + slot * a.hd + d);
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 16; e += 4)
                                 dst[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                         }

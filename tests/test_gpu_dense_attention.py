@@ -615,3 +615,116 @@ def test_serving_run():
                            cu([1]), 1, 119, scale, lse=lse)
     K4, V4 = (torch.cat([a, quant(b)[[0, 2, 4]], quant(c)]) for a, b, c in ((K, k3, k4), (V, v3, v4)))
     ref.close(o, lse, *ref.attend(q4, K4, V4, ref.tree_visible(1, 119, None, 0, DEV), scale, None))
+
+
+# ---------------------------------------------------------------------------
+# Batches, groups, calls at once
+# ---------------------------------------------------------------------------
+def test_prompt_many_sequences():
+    """More sequences than one lookup takes, empty ones among them."""
+    rng = torch.Generator().manual_seed(70)
+    lens = torch.randint(0, 41, (75,), generator=rng).tolist()
+    lens[30:36] = [0] * 6
+    run_prompt(gen(70), lens, lens, 4, 2, 128, 0, True)
+    run_prompt(gen(71), lens, [n + 130 for n in lens], 8, 1, 64, 100, False)
+
+
+@pytest.mark.parametrize("nh,kvh", [(300, 2), (131, 1), (256, 1), (128, 1)])
+def test_prompt_groups_beyond_a_tile(nh, kvh):
+    run_prompt(gen(72), [70, 5], [90, 5], nh, kvh, 64, 0, True)
+
+
+def test_tree_many_sequences():
+    rng = torch.Generator().manual_seed(73)
+    drafts = torch.randint(0, 6, (90,), generator=rng).tolist()
+    lens = [n + int(torch.randint(0, 400, (1,), generator=rng)) for n in drafts]
+    lens[3], drafts[3] = 0, 0
+    for nh, e4m3 in ((6, True), (6, False), (16, True), (16, False)):
+        run_tree(gen(73), lens, drafts, nh, 2, 128, 32, e4m3, 0, False, True)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("nh,kvh,drafts", [(150, 1, [1]), (17, 1, [1, 1]), (300, 1, [3]),
+                                           (128, 1, [1]), (129, 1, [2, 1])])
+def test_tree_wide_groups(nh, kvh, drafts, e4m3):
+    run_tree(gen(74), [700, 64][:len(drafts)], drafts, nh, kvh, 64, 64, e4m3, 0, True, False)
+
+
+def tree_inputs(g, lens, drafts, nh, kvh, hd, page, e4m3):
+    need = max(-(-n // page) for n in lens)
+    cache = filled_cache(g, need * len(lens), kvh, page, hd, e4m3)
+    table = torch.randperm(need * len(lens), generator=g, device=DEV).view(len(lens), need).int()
+    q = randn(g, sum(drafts), nh, hd)
+    return (q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), cu(drafts),
+            max(drafts), max(lens), hd ** -0.5)
+
+
+def test_same_bits_every_time_and_on_two_streams():
+    """No result depends on the order in which CTAs finish, nor on a call that runs
+    beside it on another stream with a workspace of its own."""
+    g = gen(75)
+    cases = [tree_inputs(g, [5000, 900], [1, 1], 32, 8, 128, 64, True),
+             tree_inputs(g, [5000, 900], [16, 9], 32, 8, 128, 64, True),
+             tree_inputs(g, [3000, 900], [64, 40], 64, 8, 128, 64, False)]
+    q, k, v = (randn(g, 1500, h, 128) for h in (8, 2, 2))
+    c = cu([1000, 500])
+
+    def run():
+        return [ds41.tree_attn_fwd(*a) for a in cases] + [
+            ds41.prompt_attn_fwd(q, k, v, c, c, 1000, 0.09)]
+
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(6):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(run())
+        torch.cuda.synchronize()
+        for outs in got:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_workspace_given():
+    g = gen(76)
+    a = tree_inputs(g, [700], [1], 8, 2, 64, 32, True)
+    need = int(ds41.load().ds41_tree_attn_workspace_bytes(1, 1, 1, 700, 8, 2, 64, 0, 1))
+    want = ds41.tree_attn_fwd(*a)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # whatever it holds
+    assert torch.equal(ds41.tree_attn_fwd(*a, ws=ws), want)
+    with pytest.raises(ValueError):
+        ds41.tree_attn_fwd(*a, ws=ws[:need - 1])
+    assert ds41.load().ds41_tree_attn_workspace_bytes(1, 1, 1, 700, 8, 3, 64, 0, 1) == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    g = gen(77)
+    q, cache, table, lens, c, mq, ml, scale = tree_inputs(g, [70], [2], 8, 2, 64, 32, True)
+    for bad in (dict(q=q[:, :, :48]), dict(q=q.float()), dict(table=table.long()),
+                dict(lens=lens.long()), dict(cache=cache._replace(v_scales=None)),
+                dict(cache=cache._replace(k_scales=cache.k_scales[:1])),
+                dict(cache=cache._replace(v=cache.v[:1])), dict(c=c.cpu())):
+        x = dict(q=q, cache=cache, table=table, lens=lens, c=c) | bad
+        with pytest.raises(ValueError):
+            ds41.tree_attn_fwd(x["q"], x["cache"], x["table"], x["lens"], x["c"], mq, ml, scale)
+    with pytest.raises(ValueError):
+        ds41.tree_attn_fwd(q, cache, table, lens, c, mq, ml, scale, o=torch.empty_like(q)[:1])
+    with pytest.raises(ValueError):
+        ds41.tree_attn_fwd(q, cache, table, lens, c, mq, ml, scale,
+                           mask=torch.zeros(2, dtype=torch.int64, device=DEV))
+    with pytest.raises(ds41.DS41Error) as e:
+        ds41.tree_attn_fwd(q, cache, table, lens, c, mq, ml, scale, window=1)
+    assert e.value.code == 1
+    k = randn(g, 5, 2, 64)
+    with pytest.raises(ValueError):
+        ds41.kv_cache_write(cache, k, k[:4], torch.zeros(5, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError):
+        ds41.kv_cache_write(cache, k, k, torch.zeros(5, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        ds41.prompt_attn_fwd(q, k, k[:, :1], c, c, 2, 0.1)
+    # a broadcast of one head is no layout of heads
+    with pytest.raises(ds41.DS41Error) as e:
+        ds41.prompt_attn_fwd(q, k[:, :1].expand(5, 2, 64), k, c, c, 2, 0.1)
+    assert e.value.code == 1
