@@ -442,10 +442,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 done_item(k);
             }
-            // tensor memory is given back with nothing in flight, whatever gave up
-            if (elect_one()) tc_commit(b_end);
-            __syncwarp();
-            drain_bar(b_end, 0, p.status);
         } else if (warp == 2) {
             // zero the V rows behind the last key
             uint32_t ring0 = 0, tails = 0;
@@ -609,9 +605,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (warp == 1) {
+        // The softmax warps have seen every output complete, unless a wait gave up: then what
+        // this warp issued may still be running.
+        if (*abort_f) {
+            if (elect_one()) tc_commit(b_end);
+            __syncwarp();
+            drain_bar(b_end, 0, p.status);
+        }
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem)
                      : "memory");
+    }
 }
 
 // [tokens][heads][hd] with strides in elements; a box of 64 columns x box_h

@@ -434,12 +434,6 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
             __syncthreads();
             if (*abort_f) ok = false;
         }
-        if (warp == 1) {
-            // tensor memory is given back with nothing in flight, whatever gave up
-            if (elect_one()) tc_commit(b_end);
-            __syncwarp();
-            drain_bar(b_end, 0, a.status);
-        }
     } else if (E4M3 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         const int tid = threadIdx.x - 384;
@@ -739,9 +733,17 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (warp == 1) {
+        // The softmax warps have seen every output complete, unless a wait gave up: then what
+        // this warp issued may still be running.
+        if (*abort_f) {
+            if (elect_one()) tc_commit(b_end);
+            __syncwarp();
+            drain_bar(b_end, 0, a.status);
+        }
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem)
                      : "memory");
+    }
 }
 
 namespace {
