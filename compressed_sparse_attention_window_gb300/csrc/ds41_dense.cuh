@@ -65,6 +65,16 @@ __device__ __forceinline__ int64_t paged_row(const PagedKv& c, int64_t pg, int h
     return (pg * c.kvh + h) * c.page + off;
 }
 
+// c += a b of 16 x 8 x 16 as mma_bf16, with f16 operands
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // Four e4m3 codes -> their exact values as f16 (every e4m3 value is a normal f16
 // or zero): lo = codes 0, 1, hi = codes 2, 3.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {

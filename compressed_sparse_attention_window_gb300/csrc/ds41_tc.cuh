@@ -144,11 +144,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// The same with f16 A and B.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
-    return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
-}
-
 // A bounded wait that also gives up once another role has given up.  After
 // `polls` polls (about a second for the default) it sets the abort flag,
 // raises DS41_E_TIMEOUT in the status word and returns false.
