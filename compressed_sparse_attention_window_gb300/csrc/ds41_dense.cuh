@@ -1,6 +1,6 @@
 // ds41_dense.cuh - what the dense-attention entry points share: the paged
 // key/value cache as kernels see it, the argument checks of its layout, and
-// the e4m3 codec of its rows.  Nothing here is shared with the CPU oracle.
+// the conversions that more than one kernel uses.  Nothing here is shared with the CPU oracle.
 #pragma once
 
 #include <atomic>
@@ -57,6 +57,31 @@ inline int sm_count_once() {
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) known[dev].store(n = device_sm_count(), std::memory_order_relaxed);
     return n;
+}
+
+// two f32 operations in one instruction
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // First element of row `off` of page `pg`, head `h`, counted in elements.

@@ -60,16 +60,30 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// x / s, correctly rounded, from the correctly rounded reciprocal r of s: with q
-// = x r within one unit of the quotient, q + r (x - q s), the remainder exact in a
-// fused multiply-add, rounds as the quotient does (P. Markstein, Computation of
-// elementary functions on the IBM RISC System/6000 processor, 1990).  Three
-// operations for each of a row's 128 quotients instead of a division's ten.  Where
-// the remainder could leave the range of f32 the division itself is taken.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-    if (s < 0x1p-90f) return __fdiv_rn(x, s);
-    const float q = __fmul_rn(x, r);
-    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, x), r, q), x);  // (-0 stays -0)
+// CTAs are numbered by head first, then by block of rows, in two dimensions of the
+// grid as one holds 65535.
+__device__ __forceinline__ int64_t row_block() {
+    return (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+}
+dim3 row_grid(int64_t kvh, int64_t rows, int64_t per) {
+    const int64_t blocks = (rows + per - 1) / per, nz = (blocks + 65534) / 65535;
+    return dim3((unsigned)kvh, (unsigned)((blocks + nz - 1) / nz), (unsigned)nz);
+}
+
+// Two quotients x / s, correctly rounded, from the correctly rounded reciprocal r of s:
+// with q = x r within one unit of the quotient, q + r (x - q s), the remainder exact in
+// a fused multiply-add, rounds as the quotient does (P. Markstein, Computation of
+// elementary functions on the IBM RISC System/6000 processor, 1990).  A quotient of
+// -0 comes out as +0.
+__device__ __forceinline__ uint64_t quotients(uint64_t x, uint64_t minus_s, uint64_t r) {
+    const uint64_t q = mul2(x, r);
+    return fma2(fma2(q, minus_s, x), r, q);
+}
+// x / 448, correctly rounded, by the same rule (x is at least 448 * 2^-126).
+__device__ __forceinline__ float by_448(float x) {
+    constexpr float R = 1.0f / 448.0f;
+    const float q = __fmul_rn(x, R);
+    return __fmaf_rn(__fmaf_rn(q, -448.0f, x), R, q);
 }
 
 struct WriteArgs {
@@ -85,58 +99,90 @@ struct WriteArgs {
 
 // L lanes take one (token, head): 8 elements of its K row and of its V row each, so
 // both rows' loads are in flight together; a CTA has one head of consecutive
-// tokens.  (16383 tokens of 8 heads of 128, 101 MB: 25 us of GPU time, 60% of the
-// copy rate.  Two and four rows a thread, heads innermost, and CTAs of 128 and 512
-// threads are level or slower.)
+// tokens.  What bounds it is the instructions as much as the bytes, so the maxima of
+// K and V share their exchanges, each half of the lanes works out one of the two
+// scales, and the quotients go two at a time.  (16383 tokens of 8
+// heads of 128, 101 MB: 22.6 us of GPU time, two thirds of the copy rate, the issue
+// slots 62% busy; 30.6 us with a maximum, a scale and a division for each.  Two and
+// four rows a thread, heads innermost, and CTAs of 128 and 512 threads are level or
+// slower.)
 template <int L, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_write_kernel(const WriteArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int c = (threadIdx.x % L) * 8, h = blockIdx.x % a.kvh;
-    const int64_t t = (int64_t)(blockIdx.x / a.kvh) * (THREADS / L) + threadIdx.x / L;
+    const int c = (threadIdx.x % L) * 8, h = blockIdx.x;
+    const int64_t t = row_block() * (THREADS / L) + threadIdx.x / L;
     const bool mine = t < a.n && c < a.hd;
     const int64_t slot = t < a.n ? a.slots[t] : -1;
     uint4 x[2];
 #pragma unroll
     for (int i = 0; i < 2; i++)
-        x[i] = mine ? __ldcs(reinterpret_cast<const uint4*>(a.x[i] + t * a.stride[i] + h * a.hd + c))
-                    : make_uint4(0, 0, 0, 0);
+        x[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        if (mine)
+            x[i] = __ldcs(reinterpret_cast<const uint4*>(a.x[i] + t * a.stride[i] + h * a.hd + c));
     const bool keep = slot >= 0 && slot < a.n_slots;
     if (!keep && slot != -1 && c == 0 && h == 0) raise_status(a.status, DS41_E_INDEX);
-    const int64_t row = ((slot >> a.page_shift) * a.kvh + h) * a.page + (slot & (a.page - 1));
+    // (the number of a page and head fits 32 bits: check_paged)
+    const int64_t row = ((int64_t)((int)(slot >> a.page_shift) * a.kvh + h) << a.page_shift) +
+                        ((int)slot & (a.page - 1));
+    if (!E4M3) {
+        if (keep && mine)
+            for (int i = 0; i < 2; i++)
+                *reinterpret_cast<uint4*>(a.cache[i] + (row * a.hd + c) * 2) = x[i];
+        return;
+    }
+    // the rows' largest magnitudes as bf16 bits (ordered like the values; the bits of
+    // infinities and NaN are the largest of all): K's in the lower half, V's above
+    uint32_t m2[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+        m2[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                         __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+    uint32_t m = __vmaxu2(__byte_perm(m2[0], m2[1], 0x5410), __byte_perm(m2[0], m2[1], 0x7632));
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1)
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    // the lower lanes have K's scale, the upper ones V's.  A scale below 2^-90 and its
+    // row are taken 2^100 times: the remainders stay normal numbers.
+    const int l = threadIdx.x % L, own = l / (L / 2);
+    const uint32_t m_own = own ? m >> 16 : m & 0xffffu;
+    const float s_own = by_448(fmaxf(bf2f((uint16_t)m_own), 448.0f * 0x1p-126f));
+    const float up = s_own < 0x1p-90f ? 0x1p100f : 1.0f;
+    const float r_own = __frcp_rn(s_own * up);
+    if (keep && mine && l == own * (L / 2))
+        (own ? a.scales[1] : a.scales[0])[row] =
+            m_own < 0x7f80u ? s_own : __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
+        const float s = __shfl_sync(0xffffffffu, s_own * up, i * (L / 2), L);
+        const float r = __shfl_sync(0xffffffffu, r_own, i * (L / 2), L);
+        const float f = __shfl_sync(0xffffffffu, up, i * (L / 2), L);
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        if (!E4M3) {
-            if (keep && mine)
-                *reinterpret_cast<uint4*>(a.cache[i] + (row * a.hd + c) * 2) = x[i];
-            continue;
-        }
-        // the largest magnitude as bf16 bits (ordered like the values; the bits of
-        // infinities and NaN are the largest of all)
-        const uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                     __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        uint64_t y[4];
 #pragma unroll
-        for (int off = L / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const bool fin = m < 0x7f80u;
-        const float s = __fdiv_rn(fmaxf(bf2f((uint16_t)m), 448.0f * 0x1p-126f), 448.0f);
-        const float r = __frcp_rn(s);
-        uint32_t codes[2] = {0, 0};
-        if (fin) {
+        for (int e = 0; e < 4; e++)
+            y[e] = f2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+        if (f != 1.0f) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float lo = quotient(__uint_as_float(w[e] << 16), s, r);
-                const float hi = quotient(__uint_as_float(w[e] & 0xffff0000u), s, r);
-                uint16_t two;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(hi), "f"(lo));
-                codes[e / 2] |= (uint32_t)two << (16 * (e & 1));
-            }
+            for (int e = 0; e < 4; e++) y[e] = mul2(y[e], f2(f, f));
         }
-        if (keep && mine) {
-            *reinterpret_cast<uint2*>(a.cache[i] + row * a.hd + c) = make_uint2(codes[0], codes[1]);
-            if (c == 0) a.scales[i][row] = fin ? s : __uint_as_float(0x7fc00000u);
+        uint16_t two[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float lo, hi;
+            unf2(quotients(y[e], f2(-s, -s), f2(r, r)), lo, hi);
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two[e]) : "f"(hi), "f"(lo));
         }
+        uint2 codes;  // (with the signs of the elements: a zero keeps its own)
+        codes.x = (two[0] | (uint32_t)two[1] << 16) |
+                  (__byte_perm(w[0], w[1], 0x7531) & 0x80808080u);
+        codes.y = (two[2] | (uint32_t)two[3] << 16) |
+                  (__byte_perm(w[2], w[3], 0x7531) & 0x80808080u);
+        if ((i ? m >> 16 : m & 0xffffu) >= 0x7f80u) codes = make_uint2(0, 0);
+        if (keep && mine)
+            *reinterpret_cast<uint2*>(a.cache[i] + row * a.hd + c) = codes;
     }
 }
 
@@ -158,8 +204,8 @@ template <int L, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
     pdl_wait();
     pdl_trigger();
-    const int h = blockIdx.x % a.kv.kvh, c = (threadIdx.x % L) * 16;
-    const int64_t r = (int64_t)(blockIdx.x / a.kv.kvh) * (THREADS / L) + threadIdx.x / L;
+    const int h = blockIdx.x, c = (threadIdx.x % L) * 16;
+    const int64_t r = row_block() * (THREADS / L) + threadIdx.x / L;
     if (c >= a.kv.hd || r >= a.rows || r >= a.cu[a.B]) return;  // behind the last: nobody's
     int b = 0, end = a.B;  // the last b with cu[b] <= r
     while (end - b > 1) {
@@ -173,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
     if (pos >= 0 && pi < a.max_pages) pg = a.table[(int64_t)b * a.max_pages + pi];
     const bool ok = pg >= 0 && pg < a.kv.n_pages;
     if (!ok) raise_status(a.status, DS41_E_INDEX);
-    const int64_t row = paged_row(a.kv, ok ? pg : 0, h, (int)(pos & (a.kv.page - 1)));
+    const int64_t row = paged_row(a.kv, ok ? pg : 0, h, (int)pos & (a.kv.page - 1));
     uint4 in[2][2];
     float s[2];
 #pragma unroll
@@ -271,12 +317,9 @@ extern "C" int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const d
                 nullptr};
     if (int rc = status_word(&a.status)) return rc;
     const int L = lanes_for(hd / 8);
-    const int64_t per = THREADS / L, blocks = (n + per - 1) / per * kvh;
-    DS41_REQUIRE(blocks < (int64_t(1) << 31), DS41_E_RANGE, "%s: n=%lld kvh=%lld", name,
-                 (long long)n, (long long)kvh);
     return launch_pdl(fmt == DS41_KV_E4M3 ? pick_write<true>(L) : pick_write<false>(L),
-                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream,
-                      name, a);
+                      row_grid(kvh, n, THREADS / L), dim3(THREADS), 0, (cudaStream_t)stream, name,
+                      a);
 }
 
 extern "C" int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scales,
@@ -310,10 +353,7 @@ extern "C" int ds41_kv_cache_read(const void* k_cache, const void* v_cache, cons
     a.max_pages = (int)max_pages;
     if (int rc = status_word(&a.status)) return rc;
     const int L = lanes_for(hd / 16);
-    const int64_t per = THREADS / L, blocks = (rows + per - 1) / per * kvh;
-    DS41_REQUIRE(blocks < (int64_t(1) << 31), DS41_E_RANGE, "%s: rows=%lld kvh=%lld", name,
-                 (long long)rows, (long long)kvh);
     return launch_pdl(fmt == DS41_KV_E4M3 ? pick_read<true>(L) : pick_read<false>(L),
-                      dim3((unsigned)blocks), dim3(THREADS), 0, (cudaStream_t)stream,
+                      row_grid(kvh, rows, THREADS / L), dim3(THREADS), 0, (cudaStream_t)stream,
                       name, a);
 }

@@ -100,6 +100,32 @@ def test_write(n, kvh, hd, page, fused, e4m3):
             assert torch.equal(bits(got), bits(w))
 
 
+@pytest.mark.parametrize("hd", [16, 128])
+def test_write_every_magnitude(hd):
+    """Rows whose largest element is each of the bf16 numbers, zero and infinity
+    among them: the scales and the codes bit for bit."""
+    g = gen(5)
+    tops = torch.arange(0x7f81, device=DEV)
+    n = tops.numel()
+
+    def rows(top):
+        b = (torch.rand(n, 1, hd, generator=g, device=DEV, dtype=torch.float64)
+             * (top[:, None, None] + 1)).long()
+        near = torch.rand(n, 1, hd, generator=g, device=DEV) < 0.5  # most within 2^-10
+        b = torch.where(near, (top[:, None, None] - b % (10 * 128)).clamp_min(0), b)
+        at = torch.randint(hd, (n,), generator=g, device=DEV)
+        b[torch.arange(n, device=DEV), 0, at] = top
+        sign = torch.randint(2, b.shape, generator=g, device=DEV) << 15
+        return (b | sign).to(torch.int16).view(torch.bfloat16)
+    k, v = rows(tops), rows(tops.flip(0))
+    cache = ds41.make_kv_cache((n + 63) // 64, 1, 64, hd)
+    ds41.kv_cache_write(cache, k, v, torch.arange(n, device=DEV))
+    for x, codes, scales in ((k, cache.k, cache.k_scales), (v, cache.v, cache.v_scales)):
+        want, ws = ref.quantise(x)
+        assert torch.equal(bits(scales.view(-1)[:n]), bits(ws.view(-1)))
+        assert torch.equal(u8(codes).view(-1, hd)[:n], u8(want)[:, 0])
+
+
 @pytest.mark.parametrize("e4m3", [True, False])
 @pytest.mark.parametrize("lens,kvh,hd,page,starts", [
     ([1], 1, 16, 16, None), ([5, 0, 33, 1], 3, 80, 16, [3, 0, 7, 15]),
