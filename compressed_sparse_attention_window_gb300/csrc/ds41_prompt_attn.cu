@@ -560,11 +560,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int head = it.grp * p.G + gh;
             const RowEnd end = row_end(st.reference(c), st.l,
                                        live && p.sink ? p.sink[head] : -INFINITY);
-            const float inv = end.factor;
             const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
             if (live && p.lse) p.lse[at] = end.lse;
             if (r.count > 0) {
-                uint16_t* dst = p.o + at * p.hd;
                 const bool any = r.hi > r.lo;
                 if (any) {
                     ok = warp_wait(&b_o[t], outs & 1, abort_f, p.status);
@@ -572,30 +570,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     outs++;
                     tc_fence_after();
                 }
-#pragma unroll
-                for (int x = 0; x < D; x += 32) {
-                    uint32_t ov[32] = {};
-                    if (any) {
-                        tc_ld32(tm_o + x, ov);
-                        tc_wait_ld();
-                        if (x + 32 == D) {  // O_t is in registers
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&b_oe[t]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (live && x + e < p.hd) {
-                            uint4 v;
-                            v.x = bf16x2(u2f(ov[e]) * inv, u2f(ov[e + 1]) * inv);
-                            v.y = bf16x2(u2f(ov[e + 2]) * inv, u2f(ov[e + 3]) * inv);
-                            v.z = bf16x2(u2f(ov[e + 4]) * inv, u2f(ov[e + 5]) * inv);
-                            v.w = bf16x2(u2f(ov[e + 6]) * inv, u2f(ov[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + x + e) = v;
-                        }
-                    }
-                }
+                // (offsets from the tile's first row: at most 128 tokens of 4096 heads)
+                uint16_t* dst = p.o + (int64_t)(it.q0 + it.t0 + t * p.TT) * p.nh * p.hd;
+                store_rows<D>(tm_o, any, end.factor, dst,
+                              live ? (tok * p.nh + head) * p.hd : -1, p.hd, [&] {
+                                  tc_fence_before();
+                                  __syncwarp();
+                                  if (any && lane == 0) mbar_arrive(&b_oe[t]);
+                              });
             }
             done_item(k);
         }
