@@ -7,8 +7,8 @@
 // with a reference m that follows the running maximum of the row; whenever m
 // moves from m0 to m1, l and O are scaled by 2^(c (m0 - m1)).  At the end
 // o = O / (l + 2^(sink - c m)).  m need not be the exact maximum, only close
-// enough that nothing overflows: it moves when a block exceeds it by 2^4, so O
-// is rescaled on the first few blocks of a row and hardly ever after.
+// enough that nothing overflows: it moves when a block exceeds it by 2^8, so O
+// is rescaled on the first blocks of a row, if at all.
 //
 // Rows.  The query heads that share a key/value head see the same keys, so a
 // tile of 128 rows is TT tokens times the G heads of a group (row = token * G +

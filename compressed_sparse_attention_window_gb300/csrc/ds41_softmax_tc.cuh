@@ -11,8 +11,10 @@ namespace tc {
 
 constexpr float SM_LOG2E = 1.4426950408889634f;
 constexpr float SM_LN2 = 0.6931471805599453f;
-// the reference of a row moves when a block's maximum exceeds it by 2^4
-constexpr float SM_RESCALE_LOG2 = 4.0f;
+// The reference of a row moves when a block's maximum exceeds it by this power of
+// two: as much as the weights' type allows.
+constexpr float SM_RESCALE_LOG2 = 8.0f;         // bf16 weights
+constexpr float SM_RESCALE_LOG2_SCALED = 4.0f;  // f16 weights
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {
@@ -248,8 +250,8 @@ __device__ __forceinline__ void rescale(uint32_t tm_p, int n, uint32_t tm_o, boo
 // MASKED: keys whose bit of vis is clear are not seen.  A block that every row
 // sees whole takes the other instance: as a run-time choice the compiler turned
 // the selects into predicated code for every block, twice the instructions.
-// Where a maximum exceeds the reference by 2^4 (in nearly all blocks none does)
-// the reference moves and what it has been used for is rescaled - the caller has
+// Where a maximum exceeds the reference by 2^8, scaled 2^4 (in nearly all blocks none
+// does), the reference moves and what it has been used for is rescaled - the caller has
 // seen the products before this block complete.  All lanes of a warp take part;
 // `live` = the row exists.
 //
@@ -316,7 +318,7 @@ __device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_
         top = fmaxf(top, max32(s[i]));
         asm volatile("" ::: "memory");
     }
-    const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
+    const bool move = (top - st.m) * c > SM_RESCALE_LOG2_SCALED && live;
     const bool vmove = vmax > st.vlim;
     if (__any_sync(0xffffffffu, move || vmove)) {
         float shift = move ? (st.m - top) * c : 0.0f;

@@ -5,7 +5,7 @@
 // of log2: t_j = scale log2(e) ks_j <q, k_j> (ks_j, vs_j: the row's scales, 1
 // for bf16), p_j = 2^(t_j - m), l += p_j, O += (p_j vs_j) v_j, the weights
 // rounded to 16 bits for the tensor cores.  m follows the running maximum lazily:
-// it moves (and l and O are rescaled) when a score exceeds it by 2^4.  An e4m3
+// it moves (and l and O are rescaled) when a score exceeds it by 2^8 (e4m3: 2^4).  An e4m3
 // cache runs on f16 products: its codes are exact in f16 (one instruction for
 // two codes; bf16 takes four), the queries become f16 with an exponent per row,
 // and l and O carry 2^-lr with lr about the exponent of the value scales, which
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     using C = Cfg<HD, E4M3>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sh[2 * WARPS + 4];
+    constexpr float MOVE = E4M3 ? tc::SM_RESCALE_LOG2_SCALED : tc::SM_RESCALE_LOG2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     Share share = find_share<NT>(a, sh, blockIdx.x == 0);
     Piece pc;
@@ -251,8 +252,8 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                                fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
             // scales that no key needs (behind the sequence's end) may be NaN: fmaxf skips them
             float vm = E4M3 ? fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y)) : 0.0f;
-            const bool moves = (mx[0] - m[0]) * cr[0] > tc::SM_RESCALE_LOG2 ||
-                               (mx[1] - m[1]) * cr[1] > tc::SM_RESCALE_LOG2;
+            const bool moves = (mx[0] - m[0]) * cr[0] > MOVE ||
+                               (mx[1] - m[1]) * cr[1] > MOVE;
             if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
                 float shift = 0.0f;
                 if (E4M3) {
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                     float t = mx[i2], sh = shift;
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                    if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
+                    if ((t - m[i2]) * cr[i2] > MOVE) {
                         sh += (m[i2] - t) * cr[i2];
                         m[i2] = t;
                     }
