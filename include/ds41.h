@@ -600,7 +600,9 @@ int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, cons
                          int64_t hd, float scale, int64_t window, const float* sink, ds41_bf16* o,
                          float* lse, ds41_stream_t stream);
 
-/* Scratch bytes ds41_tree_attn_fwd needs (may be 0). */
+/* Scratch bytes ds41_tree_attn_fwd needs (0: sizes that it does not take).  The
+ * scratch holds nothing between calls; calls that may run at the same time, captured
+ * graphs among them, need one each. */
 size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_len,
                                       int64_t nh, int64_t kvh, int64_t hd, int64_t window,
                                       int fmt);
