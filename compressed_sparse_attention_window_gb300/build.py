@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
 shared library next to this file.  No fast-math: the fp4 quantisers and the
-indexer scores must round exactly as IEEE single precision does.
+indexer scores must round exactly as IEEE single precision does.  The host
+compiler builds ``csrc/ds41_binding.cpp``, the extension module with the
+Python side of the dense attention's calls, against the installed torch.
 
 Usage: ``python -m compressed_sparse_attention_window_gb300.build [--force]``.
 """
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libds41.so")
+BINDING_SRC = os.path.join(CSRC, "ds41_binding.cpp")
+BINDING = os.path.join(HERE, "_ds41_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -63,15 +68,42 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_binding(force: bool, verbose: bool) -> None:
+    """The extension module (its libraries are those that torch has loaded)."""
+    if not (force or _stale(BINDING, [BINDING_SRC, __file__] + _headers())):
+        return
+    import torch
+    cxx = shutil.which("g++") or "g++"
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [INCLUDE, os.path.join(root, "include"), sysconfig.get_paths()["include"],
+            os.path.join(cuda, "include")]
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(x for d in dirs for x in ("-I", d)), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source and link libds41.so; returns its path."""
+    """Compile every CUDA source, link libds41.so and build the extension module;
+    returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(_build_binding, force, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cuda_lib = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "lib64")

@@ -2,12 +2,16 @@
 
 Every function here only checks and marshals torch tensors (device, dtype,
 contiguity) into the C ABI and passes the current CUDA stream; all arithmetic
-runs in the library's CUDA kernels.  There is no fallback: if the library is
-missing or a call fails, an exception is raised.
+runs in the library's CUDA kernels.  (The calls of the dense attention, some of
+which take the device less time than Python takes for the checks, have theirs in
+an extension module, ``csrc/ds41_binding.cpp``.)  There is no fallback: if the
+library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from typing import Dict, NamedTuple, Optional, Tuple
@@ -16,6 +20,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libds41.so")
+BINDING_PATH = os.path.join(_HERE, "_ds41_binding.so")
 
 _lib = None
 
@@ -750,87 +755,38 @@ def make_kv_cache(n_pages: int, kvh: int, page: int, hd: int, e4m3: bool = True,
     return KvCache(k, v, ks, vs)
 
 
-# The checks below run before every call, some of which take 3 us on the device, so
-# they are written for few Python operations.
-_F32, _I32T, _I64T, _E4M3 = torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn
+_binding = None
 
 
-def _here(dev: torch.device) -> None:
-    """The call runs on the current device's stream: the tensors are there."""
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {dev}")
-    if dev.index != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}: the call runs on its stream")
+def _failed(name: str, code: int) -> None:
+    raise DS41Error(name, code, load().ds41_last_error().decode(errors="replace"))
 
 
-def _arg(name: str, t: Optional[torch.Tensor], dev, shape, dtype) -> Optional[int]:
-    """The pointer of a contiguous tensor of this shape and type on this device
-    (None for None)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _heads(name: str, t: torch.Tensor, dev, hd: int, dense: bool = False):
-    """(pointer, token stride, head stride) of a bf16 tensor [tokens, heads, hd]
-    whose last dimension is dense (with ``dense``: the heads too)."""
-    if t.dim() != 3 or t.dtype != _BF or t.shape[2] != hd:
-        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, {hd}], got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    tok, head, one = t.stride()
-    n, h, _ = t.shape
-    if n <= 1 or h == 1:  # a stride that no address depends on
-        head = hd if h == 1 or n == 0 else head
-        tok = (h * hd if head == hd else hd) if n <= 1 else tok
-    if (one != 1 and hd > 1) or (dense and head != hd):
-        raise ValueError(f"{name}: strides {t.stride()}: the last dimension"
-                         + (" and the heads" if dense else "") + " must be dense")
-    return t.data_ptr() or None, tok, head
-
-
-def _cache_args(c: KvCache, dev):
-    """The cache's arguments of the C calls, its layout checked; and kvh, page, hd."""
-    k, v, ks, vs = c
-    shape, dtype = k.shape, k.dtype
-    if len(shape) != 4:
-        raise ValueError(f"cache: expected [n_pages, kvh, page, hd], got {tuple(shape)}")
-    e4m3 = dtype == _E4M3
-    if not e4m3 and dtype != _BF:
-        raise ValueError(f"cache: expected bfloat16 or float8_e4m3fn, got {dtype}")
-    if e4m3 != (ks is not None) or e4m3 != (vs is not None):
-        raise ValueError("cache: an e4m3 cache has k_scales and v_scales, a bf16 cache none")
-    n_pages, kvh, page, hd = shape
-    kp, vp = _arg("cache.k", k, dev, shape, dtype), _arg("cache.v", v, dev, shape, dtype)
-    if not e4m3:
-        return (kp, vp, None, None, 0, n_pages, page), kvh, page, hd
-    rows = (n_pages, kvh, page)
-    return (kp, vp, _arg("cache.k_scales", ks, dev, rows, _F32),
-            _arg("cache.v_scales", vs, dev, rows, _F32), 1, n_pages, page), kvh, page, hd
+def _dense():
+    """The extension module that checks the tensors of the calls below (ValueError,
+    TypeError) and makes them: ctypes and Python take 20 us a call for it, more than
+    the small ones take on the device."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m compressed_sparse_attention_window_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_ds41_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_loader("_ds41_binding", loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        lib = load()
+        mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "ds41_kv_cache_write", "ds41_kv_cache_read", "ds41_prompt_attn_fwd",
+            "ds41_tree_attn_fwd", "ds41_tree_attn_workspace_bytes")), _failed)
+        _binding = mod
+    return _binding
 
 
 def kv_cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """ds41_kv_cache_write: the rows k, v [n, kvh, hd] bf16 (heads dense, any
     token stride) into the cache's slots [n] int64 (-1: not written)."""
-    dev = k.device
-    _here(dev)
-    c, kvh, page, hd = _cache_args(cache, dev)
-    n = k.shape[0]
-    if k.shape != (n, kvh, hd) or v.shape != k.shape:
-        raise ValueError(f"k, v: expected {(n, kvh, hd)}, got {tuple(k.shape)}, {tuple(v.shape)}")
-    kp, k_tok, _ = _heads("k", k, dev, hd, dense=True)
-    vp, v_tok, _ = _heads("v", v, dev, hd, dense=True)
-    _call("ds41_kv_cache_write", kp, k_tok, vp, v_tok, _arg("slots", slots, dev, (n,), _I64T), *c,
-          kvh, hd, n, _stream())
+    (_binding or _dense()).kv_cache_write(cache, k, v, slots)
 
 
 def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, rows: int,
@@ -840,31 +796,7 @@ def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, 
     bf16 (given or new).  Sequence b gets cu_k[b + 1] - cu_k[b] rows from
     position starts[b] (0 without starts); rows behind cu_k[-1] are left as
     they were (uninitialised in a new tensor)."""
-    dev = cu_k.device
-    _here(dev)
-    c, kvh, page, hd = _cache_args(cache, dev)
-    B = cu_k.shape[0] - 1
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
-    mp = page_table.shape[1]
-    shape = (rows, kvh, hd)
-    k = torch.empty(shape, dtype=_BF, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=_BF, device=dev) if v is None else v
-    _call("ds41_kv_cache_read", *c, kvh, hd, _arg("page_table", page_table, dev, (B, mp), _I32T),
-          mp, _arg("cu_k", cu_k, dev, (B + 1,), _I32T), _arg("starts", starts, dev, (B,), _I32T),
-          B, _arg("k", k, dev, shape, _BF), _arg("v", v, dev, shape, _BF), rows, _stream())
-    return k, v
-
-
-def _ws(need: int, ws: Optional[torch.Tensor], dev):
-    """A workspace of at least ``need`` bytes: the one given, or a new one."""
-    if need == 0:
-        return None
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws: expected a contiguous tensor of at least {need} bytes on {dev}")
-    return ws
+    return (_binding or _dense()).kv_cache_read(cache, page_table, cu_k, rows, starts, k, v)
 
 
 def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
@@ -875,22 +807,8 @@ def prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     """ds41_prompt_attn_fwd: causal attention of packed prompts, q [Tq, nh, hd]
     over k, v [Tk, kvh, hd] (any token and head strides that are multiples of
     8); returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
-    dev = q.device
-    _here(dev)
-    Tq, nh, hd = q.shape
-    Tk, kvh, _ = k.shape
-    qp, q_tok, q_head = _heads("q", q, dev, hd)
-    kp, k_tok, k_head = _heads("k", k, dev, hd)
-    vp, v_tok, v_head = _heads("v", v, dev, hd)
-    if v.shape != k.shape:
-        raise ValueError(f"v: expected {tuple(k.shape)}, got {tuple(v.shape)}")
-    B = cu_q.shape[0] - 1
-    o = torch.empty(q.shape, dtype=_BF, device=dev) if o is None else o
-    _call("ds41_prompt_attn_fwd", qp, q_tok, q_head, kp, k_tok, k_head, vp, v_tok, v_head,
-          _arg("cu_q", cu_q, dev, (B + 1,), _I32T), _arg("cu_k", cu_k, dev, (B + 1,), _I32T), B,
-          Tq, Tk, max_q, nh, kvh, hd, scale, window, _arg("sink", sink, dev, (nh,), _F32),
-          _arg("o", o, dev, (Tq, nh, hd), _BF), _arg("lse", lse, dev, (Tq, nh), _F32), _stream())
-    return o
+    return (_binding or _dense()).prompt_attn_fwd(q, k, v, cu_q, cu_k, max_q, scale, sink, window,
+                                                  o, lse)
 
 
 def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, lens: torch.Tensor,
@@ -904,28 +822,5 @@ def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, len
     ``mask`` [Tq, words] int64 has a bit for each drafted token that a token
     sees (None: a chain; one token per sequence: plain decode).  Returns
     o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
-    dev = q.device
-    _here(dev)
-    c, kvh, page, hd = _cache_args(cache, dev)
-    qp, q_tok, q_head = _heads("q", q, dev, hd)
-    Tq, nh, _ = q.shape
-    B = cu_q.shape[0] - 1
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table: expected [B, max_pages], got {tuple(page_table.shape)}")
-    mp = page_table.shape[1]
-    words = 0
-    if mask is not None:
-        if mask.dim() != 2:
-            raise ValueError(f"mask: expected [Tq, words], got {tuple(mask.shape)}")
-        words = mask.shape[1]
-    o = torch.empty(q.shape, dtype=_BF, device=dev) if o is None else o
-    need = load().ds41_tree_attn_workspace_bytes(B, Tq, max_q, max_len, nh, kvh, hd, window, c[4])
-    ws = _ws(need, ws, dev)
-    _call("ds41_tree_attn_fwd", qp, q_tok, q_head, *c,
-          _arg("page_table", page_table, dev, (B, mp), _I32T), mp,
-          _arg("lens", lens, dev, (B,), _I32T), _arg("cu_q", cu_q, dev, (B + 1,), _I32T),
-          _arg("mask", mask, dev, (Tq, words), _I64T), words, B, Tq, max_q, max_len, nh, kvh, hd,
-          scale, window, _arg("sink", sink, dev, (nh,), _F32),
-          _arg("o", o, dev, (Tq, nh, hd), _BF), _arg("lse", lse, dev, (Tq, nh), _F32),
-          None if ws is None else ws.data_ptr(), need, _stream())
-    return o
+    return (_binding or _dense()).tree_attn_fwd(q, cache, page_table, lens, cu_q, max_q, max_len,
+                                                scale, mask, sink, window, o, lse, ws)
