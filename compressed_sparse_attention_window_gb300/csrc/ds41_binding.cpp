@@ -107,8 +107,8 @@ struct Cache {
     int64_t n_pages, kvh, page, hd;
 };
 Cache cache_of(PyObject* o, at::Device dev) {
-    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4, "cache: expected a KvCache, got ",
-                     Py_TYPE(o)->tp_name);
+    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4,
+                     "cache: expected a KvCache, got ", Py_TYPE(o)->tp_name);
     const Tensor& k = tensor("cache.k", PyTuple_GET_ITEM(o, 0));
     const Tensor& v = tensor("cache.v", PyTuple_GET_ITEM(o, 1));
     PyObject *ks = PyTuple_GET_ITEM(o, 2), *vs = PyTuple_GET_ITEM(o, 3);
@@ -226,7 +226,8 @@ PyObject* prompt_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "q, k: expected [tokens, heads, hd], got ",
                       q.sizes(), ", ", k.sizes());
     const int64_t Tq = q.size(0), nh = q.size(1), hd = q.size(2), Tk = k.size(0), kvh = k.size(1);
-    const Heads qh = heads("q", q, dev, hd), kh = heads("k", k, dev, hd), vh = heads("v", v, dev, hd);
+    const Heads qh = heads("q", q, dev, hd), kh = heads("k", k, dev, hd);
+    const Heads vh = heads("v", v, dev, hd);
     TORCH_CHECK_VALUE(v.sizes() == k.sizes(), "v: expected ", k.sizes(), ", got ", v.sizes());
     const int64_t B = length("cu_q", cu_q), max_q = integer(a[5]), window = integer(a[8]);
     auto cq = (const int32_t*)data("cu_q", cu_q, dev, {B + 1}, at::kInt);

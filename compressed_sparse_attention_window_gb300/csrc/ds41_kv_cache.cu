@@ -296,7 +296,8 @@ extern "C" int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const d
         return rc;
     DS41_REQUIRE(n >= 0 && n < (int64_t(1) << 31), DS41_E_RANGE, "%s: n=%lld", name, (long long)n);
     if (n == 0) return DS41_OK;
-    DS41_REQUIRE(k && v && aligned16(k) && aligned16(v) && slots && aligned_to(slots, 8), DS41_E_ARG,
+    DS41_REQUIRE(k && v && aligned16(k) && aligned16(v) && slots && aligned_to(slots, 8),
+                 DS41_E_ARG,
                  "%s: k and v must be non-null and 16-byte aligned, slots non-null and aligned",
                  name);
     DS41_REQUIRE(k_stride >= kvh * hd && v_stride >= kvh * hd && k_stride % 8 == 0 &&

@@ -29,6 +29,15 @@
 // one tile runs, the tensor core works on the other.  A commit after QK_t(j+1)
 // also covers PV_t(j), so a softmax thread that has seen S_t(j+1) may rescale
 // its row of O_t itself: no fourth role, no further barrier.
+//
+// What bounds it.  Long prompts: the products.  A pair of blocks takes 2700 cycles
+// where the tensor core's rate alone would allow 2048, as 128 x 128 products with
+// both operands in shared memory read it at its full rate (16384 tokens of 32 heads
+// of 128 over 8: 1.32 ms, 1660 TFLOP/s).  Short ones: the ends of the items, where
+// the tensor core waits for first scores and last outputs (seven prompts of 415 ..
+// 2000 tokens: 150 us, 9 items a CTA); with a window, whose items are two blocks
+// long, one chain of scores, softmax, product and output (chunks of 4096 and 1440
+// tokens, window 128, 64 heads of 64 over 8: 60 us).
 #include "ds41_dense.cuh"
 #include "ds41_softmax_tc.cuh"
 
@@ -237,7 +246,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_end + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
     Item* items = reinterpret_cast<Item*>(tmem_slot + 2);
-    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <= 624,
+    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <=
+                      624,
                   "barrier area");
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
@@ -536,7 +546,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const int64_t j0 = (int64_t)j * KB;
-                const bool masked = j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
+                const bool masked =
+                    j0 + KB - 1 > r.p_first || (p.window && j0 <= p_last - p.window);
                 if (idle) {
                     // none of the warp's rows exists: whatever its scores hold weighs no one
                 } else if (masked) {

@@ -29,7 +29,8 @@ struct Args {
     float scale_log2;
     int64_t window;
     // the work: see `Share`
-    int block, align, tile_rows;  // keys of a block; first keys are multiples of align; rows of a tile
+    int block, align;  // keys of a block; first keys are multiples of align
+    int tile_rows;     // rows of a tile
     int row_tiles;                // of the most drafted tokens
     int workers;
     float* part;                  // [workers][2][tile_rows][hd]

@@ -24,7 +24,8 @@
 // are taken from shared memory with an order of hd (for Q K^T) and of the output
 // columns (for P V) in which each lane's share is contiguous: the same order on
 // both operands leaves the product unchanged.  The codes are widened in
-// registers on the way into the products.
+// registers on the way into the products.  (48 sequences of one token over up to 8191
+// keys, 64 heads of 128 over 8, e4m3: 94 us with the join, 5.0 TB/s.)
 #include "ds41_internal.cuh"
 #include "ds41_tree.cuh"
 
@@ -56,7 +57,9 @@ __device__ __forceinline__ int k_piece(int r, int ch) {
 template <int RB>
 __device__ __forceinline__ int v_piece(int r, int ch) {
     const int c = (r >> 1) & 3;
-    return RB == 64 ? ch ^ ((c & 1) << 1) : RB == 128 ? ch ^ (c << 1) : ch ^ ((c & 1) | ((c >> 1) << 2));
+    return RB == 64    ? ch ^ ((c & 1) << 1)
+           : RB == 128 ? ch ^ (c << 1)
+                       : ch ^ ((c & 1) | ((c >> 1) << 2));
 }
 
 template <int HD, bool E4M3>
@@ -155,7 +158,8 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             for (int st = 0; st < HD / 16; st++) {
                 const int d = E4M3 ? (c + 4 * (st / 4)) * 16 + 4 * (st % 4)
                                    : (c + 4 * (st / 2)) * 8 + 4 * (st % 2);
-                const uint2 v = d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
+                const uint2 v =
+                    d < a.hd ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
                 qf[st][i] = v.x;
                 qf[st][i + 2] = v.y;
             }
@@ -167,7 +171,8 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                 uint32_t m2 = 0;
 #pragma unroll
                 for (int st = 0; st < HD / 16; st++)
-                    m2 = __vmaxu2(m2, __vmaxu2(qf[st][i] & 0x7fff7fffu, qf[st][i + 2] & 0x7fff7fffu));
+                    m2 = __vmaxu2(m2, __vmaxu2(qf[st][i] & 0x7fff7fffu,
+                                               qf[st][i + 2] & 0x7fff7fffu));
                 uint32_t mb = max(m2 & 0xffffu, m2 >> 16);  // four lanes have the row
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
@@ -494,7 +499,10 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
 // The shape of a call's work: which kernel, its tiles and blocks, its workers.
 // Up to 16 rows per key/value head the few-row kernel, three CTAs an SM (two on a
 // bf16 cache, whose stages are twice as large); above, the tensor-core kernel,
-// one CTA an SM.  Never more workers than blocks at the longest lengths.
+// one CTA an SM (for 8 rows it takes 213 us where the few-row kernel takes 94, 48
+// sequences of 8191 e4m3 keys).  Above 128 rows two tiles share a block's loads
+// (4 sequences of 512 rows over 32768 keys: 218 us, 231 a tile at a time).  Never more
+// workers than blocks at the longest lengths.
 struct Plan {
     bool many;
     int block, align, tile_rows, row_tiles, workers;

@@ -112,3 +112,17 @@ def test_binding_refuses_host_tensors():
         ds41.kv_cache_read(c, i.view(1, 2), i, 4)
     with pytest.raises(ValueError):
         ds41.tree_attn_fwd(x, c, i.view(1, 2), i[:1], i, 1, 4, 0.1)
+
+
+def test_binding_refuses_what_is_no_tensor_or_cache():
+    x = torch.zeros(1, 1, 16, dtype=torch.bfloat16)
+    cache = ds41.make_kv_cache(1, 1, 16, 16, device="cpu")
+    idx = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: ds41.kv_cache_write(cache, None, x, idx),
+                 lambda: ds41.kv_cache_write(cache, x, 3, idx),
+                 lambda: ds41.kv_cache_read(cache, [[0]], idx, 1),
+                 lambda: ds41.kv_cache_read(cache, idx[None], None, 1),
+                 lambda: ds41.prompt_attn_fwd(x, x, "v", idx, idx, 1, 1.0),
+                 lambda: ds41.tree_attn_fwd(None, cache, idx[None], idx, idx, 1, 1, 1.0)):
+        with pytest.raises(TypeError):
+            call()

@@ -1,6 +1,8 @@
 """Dense attention with grouped heads and its paged cache on the GPU, against
 the definitions in 64 bits (dense_ref.py, where the tolerances are derived)."""
 import math
+import sys
+import threading
 
 import pytest
 import torch
@@ -711,6 +713,50 @@ def test_same_bits_every_time_and_on_two_streams():
         torch.cuda.synchronize()
         for outs in got:
             assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_calls_from_two_threads_and_no_leak():
+    """Two threads, each on a stream of its own, while neither holds the other's
+    outputs; what a call allocates is given back, the outputs given are returned."""
+    g = gen(78)
+    a = tree_inputs(g, [700, 33], [3, 1], 8, 2, 64, 32, True)
+    q, k, v = (randn(g, 150, h, 64) for h in (8, 2, 2))
+    c = cu([100, 50])
+    cache = filled_cache(g, 5, 2, 32, 64, True)
+    slots = torch.arange(150, device=DEV)
+    rows = torch.arange(5, device=DEV, dtype=torch.int32)[None]
+
+    def run():
+        ds41.kv_cache_write(cache, k, v, slots)  # (both threads the same rows)
+        return (ds41.tree_attn_fwd(*a), ds41.prompt_attn_fwd(q, k, v, c, c, 100, 0.1),
+                *ds41.kv_cache_read(cache, rows, cu([150]), 150))
+    want = run()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(100):
+                if not all(torch.equal(x, y) for x, y in zip(run(), want)):
+                    wrong.append(1)
+        s.synchronize()
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong and torch.cuda.memory_allocated() == before
+    o, lse = torch.empty_like(want[1]), torch.empty(150, 8, device=DEV)
+    refs = sys.getrefcount(o)
+    for _ in range(10):
+        assert ds41.prompt_attn_fwd(q, k, v, c, c, 100, 0.1, o=o, lse=lse) is o
+    assert sys.getrefcount(o) == refs and torch.equal(o, want[1])
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    got = ds41.kv_cache_read(cache, rows, cu([150]), 150, k=k2, v=v2)
+    assert got[0] is k2 and got[1] is v2 and torch.equal(k2, want[2])
 
 
 def test_workspace_given():
