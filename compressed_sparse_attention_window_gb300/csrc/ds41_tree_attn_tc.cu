@@ -30,7 +30,10 @@
 //
 // What bounds it.  No single unit: a block of 128 e4m3 keys takes 96 KB through
 // shared memory to be read and widened, 96 KB for the products' operands, and the
-// scaled softmax 2700 cycles of its warps (1430 without scales).  8 trees of up to
+// scaled softmax 2700 cycles of its warps (1430 without scales); with one tile of rows
+// the widening warps are as busy, 1150 cycles for a block's K and for its V.  The
+// copies' waits look at every second use of a stage and are right because stages are
+// freed in the ring's order.  8 trees of up to
 // 16 tokens over 16384 keys, 32 heads of 128 over 8: 91 us; 4 of 64 over 32768, 64
 // heads: 218 us.
 #include "ds41_internal.cuh"
