@@ -255,8 +255,17 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             for (int i2 = 0; i2 < 2; i2++)
                 mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
                                fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
-            // scales that no key needs (behind the sequence's end) may be NaN: fmaxf skips them
-            float vm = E4M3 ? fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y)) : 0.0f;
+            // (a key that neither row sees has no part in it: behind the sequence's end its
+            // scale is whatever an earlier user left there)
+            float vm = 0.0f;
+            if (E4M3) {
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    const bool x = !masked || fmaxf(sc[n][0], sc[n][2]) > -INFINITY;
+                    const bool y = !masked || fmaxf(sc[n][1], sc[n][3]) > -INFINITY;
+                    vm = fmaxf(vm, fmaxf(x ? vs[n].x : 0.0f, y ? vs[n].y : 0.0f));
+                }
+            }
             const bool moves = (mx[0] - m[0]) * cr[0] > MOVE ||
                                (mx[1] - m[1]) * cr[1] > MOVE;
             if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
