@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t pos = (int64_t)r.p_first + tok;              // the last key it sees
             const int64_t before = p.window ? pos - p.window : -1;     // the last key before those
             const int64_t p_last = (int64_t)r.p_first + r.count - 1;
-            RowState st(false);
+            RowState st;
             for (int j = r.lo; j < r.hi; j++, ph++) {
                 ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
                 if (!ok) break;

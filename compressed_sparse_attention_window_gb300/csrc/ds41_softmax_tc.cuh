@@ -11,10 +11,17 @@ namespace tc {
 
 constexpr float SM_LOG2E = 1.4426950408889634f;
 constexpr float SM_LN2 = 0.6931471805599453f;
-// The reference of a row moves when a block's maximum exceeds it by this power of
-// two: as much as the weights' type allows.
-constexpr float SM_RESCALE_LOG2 = 8.0f;         // bf16 weights
-constexpr float SM_RESCALE_LOG2_SCALED = 4.0f;  // f16 weights
+// Plain form (bf16 weights): the reference of a row moves when a block's maximum
+// exceeds it by this power of two.
+constexpr float SM_RESCALE_LOG2 = 8.0f;
+// Scaled form (f16 weights p_j vs_j): a row's unit is chosen so that the largest weight
+// is 2^8 of it, and moves when one would pass 2^14 (f16 ends at 2^16); f16's smallest
+// step is then 2^-32 of the largest weight at most.  No unit is below 2^-96 of the
+// largest p_j, which keeps the sum of the p_j in that unit inside f32.
+constexpr float SM_WEIGHT_LOG2 = 8.0f;
+constexpr float SM_WEIGHT_MOVE_LOG2 = 14.0f;
+constexpr float SM_UNIT_MIN_LOG2 = -96.0f;
+constexpr float SM_UNIT_MOVE_LOG2 = 100.0f;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {
@@ -114,25 +121,42 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The state of a row: the reference m (in units of its scores), the sum l of
-// 2^(c (S - m) - lr), and for scaled values their common exponent lr, which
-// moves when a scale exceeds vlim = 2^(lr + 8).  2^lr is about the size of the
-// value scales, so that a weight times its value's scale stays in the range of
-// f16 (2^4 of the lazy maximum, 2^9 of the scale); both O and l carry 2^-lr, so
-// nothing has to be undone at the end.
+// 2^(c (S - m) - lr).  For scaled values 2^(c m + lr) is the row's unit: the largest
+// p_j vs_j of the keys that the row sees, whatever the scales of the others, is 2^8 of
+// it or more (see above).  Both O and l are in that unit, so nothing has to be undone
+// at the end.
 struct RowState {
-    float m, l, lr, vlim;
-    __device__ __forceinline__ explicit RowState(bool scaled)
-        : m(-INFINITY), l(0.0f), lr(scaled ? VS_MIN : 0.0f), vlim(0.0f) {}
-    // scales below 2^-60 count as 2^-60: l stays far from the end of f32
-    static constexpr float VS_MIN = -60.0f;
+    float m = -INFINITY, l = 0.0f, lr = 0.0f;
     __device__ __forceinline__ float reference(float c) const {  // in log2 units
-        return m == -INFINITY ? -INFINITY : m * c + lr;
+        return m == -INFINITY ? -INFINITY : fmaf(m, c, lr);
     }
 };
-// the exponent that a value scale asks for
-__device__ __forceinline__ float scale_exponent(float vmax) {
-    return fmaxf((float)((int)(__float_as_uint(vmax) >> 23) - 127), RowState::VS_MIN);
+// What a block's scores may rise above m, in log2 units less lr, before the unit has to be
+// looked at: vmax, the block's largest value scale, bounds its weights.
+__device__ __forceinline__ float unit_limit(float vmax) {
+    const float log2_vmax = (float)((int)(__float_as_uint(vmax) >> 23) - 126);
+    return fminf(SM_WEIGHT_MOVE_LOG2 - log2_vmax, SM_UNIT_MOVE_LOG2);
+}
+// Moves a row's unit if a block asks for it: top is the largest score that the row sees
+// there, e the largest log2 of a weight against top's own p.  Returns the factor for
+// what is in the old unit.
+__device__ __forceinline__ float move_unit(float top, float e, float c, float& m, float& lr) {
+    const float rise = (top - m) * c;  // (-inf - -inf is NaN: no move)
+    if (!(rise + e > lr + SM_WEIGHT_MOVE_LOG2 || rise > lr + SM_UNIT_MOVE_LOG2)) return 1.0f;
+    const float to_m = fmaxf(m, top);
+    const float to =
+        fmaxf((top - to_m) * c + fminf(e, 128.0f) - SM_WEIGHT_LOG2, SM_UNIT_MIN_LOG2);
+    const float f = ex2((m - to_m) * c + lr - to);
+    m = to_m;
+    lr = to;
+    return f;
 }
 
 // tcgen05.wait::ld with the registers it waits for, so that nothing that uses them
@@ -250,10 +274,10 @@ __device__ __forceinline__ void rescale(uint32_t tm_p, int n, uint32_t tm_o, boo
 // MASKED: keys whose bit of vis is clear are not seen.  A block that every row
 // sees whole takes the other instance: as a run-time choice the compiler turned
 // the selects into predicated code for every block, twice the instructions.
-// Where a maximum exceeds the reference by 2^8, scaled 2^4 (in nearly all blocks none
-// does), the reference moves and what it has been used for is rescaled - the caller has
-// seen the products before this block complete.  All lanes of a warp take part;
-// `live` = the row exists.
+// Where a maximum exceeds the reference by 2^8 (scaled: where a weight passes the row's
+// unit by 2^14), which is so in few blocks, the reference moves and what it has been used
+// for is rescaled - the caller has seen the products before this block complete.  All
+// lanes of a warp take part; `live` = the row exists.
 //
 // The plain form holds the 128 scores in registers.
 template <int D, bool MASKED>
@@ -301,7 +325,8 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
     tc_wait_st();
 }
 
-// The scaled form (e4m3 caches).  vmax: the largest vs of the block.
+// The scaled form (e4m3 caches).  vmax: the largest |vs| of the block's real keys, seen or
+// not: a bound alone.
 template <int D, bool MASKED>
 __device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_o, bool have_o,
                                                      const uint32_t (&vis)[4], float c,
@@ -318,18 +343,27 @@ __device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_
         top = fmaxf(top, max32(s[i]));
         asm volatile("" ::: "memory");
     }
-    const bool move = (top - st.m) * c > SM_RESCALE_LOG2_SCALED && live;
-    const bool vmove = vmax > st.vlim;
-    if (__any_sync(0xffffffffu, move || vmove)) {
-        float shift = move ? (st.m - top) * c : 0.0f;
-        if (move) st.m = top;
-        if (vmove) {
-            const float lr = scale_exponent(vmax);
-            shift += st.lr - lr;
-            st.lr = lr;
-            st.vlim = ex2(lr + 8.0f);
+    const bool look = (top - st.m) * c > st.lr + unit_limit(vmax) && live;
+    if (__any_sync(0xffffffffu, look)) {
+        // the largest weight of the keys that the row sees (the scores once more: their
+        // scaled form is in registers that a loop cannot index)
+        float e = -INFINITY;
+#pragma unroll 1
+        for (int x = 0; x < 128; x += 16) {
+            uint32_t r[16];
+            tc_ld16(tm_s + x, r);
+            tc_wait_ld();
+            const uint32_t w = x < 64 ? (x < 32 ? vis[0] : vis[1]) : (x < 96 ? vis[2] : vis[3]);
+#pragma unroll
+            for (int y = 0; y < 16; y++) {
+                // (the product rounded as top was: a fused one would be off by as much as
+                // the unit of large scores)
+                const float t = fmaf(__fmul_rn(u2f(r[y]), ks[x + y]) - top, c,
+                                     lg2(fabsf(vs[x + y])));
+                if (!MASKED || ((w >> ((x & 16) + y)) & 1)) e = fmaxf(e, t);
+            }
         }
-        const float f = ex2(shift);
+        const float f = live ? move_unit(top, e, c, st.m, st.lr) : 1.0f;
         st.l *= f;
         if (have_o) rescale<D, true>(tm_s, 0, tm_o, true, f);
     }

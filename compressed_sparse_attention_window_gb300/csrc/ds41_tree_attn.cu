@@ -5,12 +5,13 @@
 // of log2: t_j = scale log2(e) ks_j <q, k_j> (ks_j, vs_j: the row's scales, 1
 // for bf16), p_j = 2^(t_j - m), l += p_j, O += (p_j vs_j) v_j, the weights
 // rounded to 16 bits for the tensor cores.  m follows the running maximum lazily:
-// it moves (and l and O are rescaled) when a score exceeds it by 2^8 (e4m3: 2^4).  An e4m3
+// it moves (and l and O are rescaled) when a score exceeds it by 2^8.  An e4m3
 // cache runs on f16 products: its codes are exact in f16 (one instruction for
 // two codes; bf16 takes four), the queries become f16 with an exponent per row,
-// and l and O carry 2^-lr with lr about the exponent of the value scales, which
-// keeps p_j vs_j in the range of f16 (RowState in ds41_softmax_tc.cuh).  The
-// scales stay outside the products.
+// and l and O carry 2^-lr, which keeps the largest p_j vs_j that a row sees at 2^8 ..
+// 2^14 of f16's range, and follows it alone: a row of values that weighs nothing may
+// have any scale (RowState in ds41_softmax_tc.cuh).  The scales stay outside the
+// products.
 //
 // Rows.  All queries of a (sequence, key/value head): tokens times the G heads
 // that share it, 16 rows a CTA (the M of an m16n8k16 product).
@@ -68,7 +69,6 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
     using C = Cfg<HD, E4M3>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sh[2 * WARPS + 4];
-    constexpr float MOVE = E4M3 ? tc::SM_RESCALE_LOG2_SCALED : tc::SM_RESCALE_LOG2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     Share share = find_share<NT>(a, sh, blockIdx.x == 0);
     Piece pc;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
 
         float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
-        float lr = E4M3 ? tc::RowState::VS_MIN : 0.0f, vlim = 0.0f;
+        float lr[2] = {0.0f, 0.0f};
         float base[2] = {0.0f, 0.0f};  // c m + lr: what an exponent is reduced by
         for (int i = 0; i < mine; i++) {
             fetch(i + C::STAGES - 1);
@@ -255,48 +255,51 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             for (int i2 = 0; i2 < 2; i2++)
                 mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
                                fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
-            // (a key that neither row sees has no part in it: behind the sequence's end its
-            // scale is whatever an earlier user left there)
-            float vm = 0.0f;
+            float lim[2] = {tc::SM_RESCALE_LOG2, tc::SM_RESCALE_LOG2};
             if (E4M3) {
+                // (a key that neither row sees has no part in it: behind the sequence's end
+                // its scale is whatever an earlier user left there)
+                float vm = 0.0f;
 #pragma unroll
                 for (int n = 0; n < 2; n++) {
                     const bool x = !masked || fmaxf(sc[n][0], sc[n][2]) > -INFINITY;
                     const bool y = !masked || fmaxf(sc[n][1], sc[n][3]) > -INFINITY;
-                    vm = fmaxf(vm, fmaxf(x ? vs[n].x : 0.0f, y ? vs[n].y : 0.0f));
+                    vm = fmaxf(vm, fmaxf(x ? fabsf(vs[n].x) : 0.0f, y ? fabsf(vs[n].y) : 0.0f));
                 }
+                const float up = tc::unit_limit(vm);
+                lim[0] = lr[0] + up;
+                lim[1] = lr[1] + up;
             }
-            const bool moves = (mx[0] - m[0]) * cr[0] > MOVE ||
-                               (mx[1] - m[1]) * cr[1] > MOVE;
-            if (__any_sync(0xffffffffu, moves || (E4M3 && vm > vlim))) {
-                float shift = 0.0f;
-                if (E4M3) {
-                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-                    if (vm > vlim) {
-                        const float to = tc::scale_exponent(vm);
-                        shift = lr - to;
-                        lr = to;
-                        vlim = exp2f(to + 8.0f);
-                    }
-                }
+            const bool look = (mx[0] - m[0]) * cr[0] > lim[0] || (mx[1] - m[1]) * cr[1] > lim[1];
+            if (__any_sync(0xffffffffu, look)) {
 #pragma unroll
                 for (int i2 = 0; i2 < 2; i2++) {
-                    float t = mx[i2], sh = shift;
+                    float t = mx[i2], f = 1.0f;
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                    if ((t - m[i2]) * cr[i2] > MOVE) {
-                        sh += (m[i2] - t) * cr[i2];
+                    if (E4M3) {
+                        // the largest weight of the keys that the row sees
+                        float e = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < 2; n++) {
+                            e = fmaxf(e, fmaf(sc[n][2 * i2] - t, cr[i2], tc::lg2(fabsf(vs[n].x))));
+                            e = fmaxf(e,
+                                      fmaf(sc[n][2 * i2 + 1] - t, cr[i2], tc::lg2(fabsf(vs[n].y))));
+                        }
+                        e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
+                        e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
+                        f = tc::move_unit(t, e, cr[i2], m[i2], lr[i2]);
+                    } else if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
+                        f = exp2f((m[i2] - t) * cr[i2]);
                         m[i2] = t;
                     }
-                    const float f = exp2f(sh);
                     l[i2] *= f;
 #pragma unroll
                     for (int d = 0; d < HD / 8; d++) {
                         o[d][2 * i2] *= f;
                         o[d][2 * i2 + 1] *= f;
                     }
-                    base[i2] = m[i2] == -INFINITY ? 0.0f : fmaf(m[i2], cr[i2], lr);
+                    base[i2] = m[i2] == -INFINITY ? 0.0f : fmaf(m[i2], cr[i2], lr[i2]);
                 }
             }
             uint32_t pf[4];
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             for (int i2 = 0; i2 < 2; i2++) {
                 float less = base[i2], at = 0.0f;
                 if (fabsf(less) > 0x1p22f) {  // c m is rounded too far: the difference first
-                    less = lr;
+                    less = lr[i2];
                     at = m[i2];
                 }
 #pragma unroll
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
             float* row = out + (warp * 16 + g + 8 * i) * P;
             if (c == 0) {
-                row[HD] = m[i] == -INFINITY ? -INFINITY : fmaf(m[i], cr[i], lr);
+                row[HD] = m[i] == -INFINITY ? -INFINITY : fmaf(m[i], cr[i], lr[i]);
                 row[HD + 1] = l[i];
             }
 #pragma unroll

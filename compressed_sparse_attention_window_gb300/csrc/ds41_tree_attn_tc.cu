@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 if (E4M3)
                     c *= exp2f((float)reinterpret_cast<const int8_t*>(
                         sm + C::QE_OFF)[(PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane]);
-                RowState st(E4M3);
+                RowState st;
                 for (int j = PAIR ? 0 : t, i = 0; j < n_blocks; j += PAIR ? 1 : 2, i++) {
                     const int gb = blocks0 + j, sl = gb % SCN;
                     ok = warp_wait(&b_sc[sl], (gb / SCN) & 1, abort_f, a.status);
@@ -611,15 +611,16 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                         }
                         float vmax = 0.0f;
                         if (E4M3) {
-                            // the largest scale of a real key (fmaxf passes over NaN)
+                            // the largest scale of a real key (fmaxf passes over NaN; the sign of one
+                            // that is not this library's has no part in it)
                             const uint32_t w = lane < 16 ? (lane < 8 ? real.x : real.y)
                                                          : (lane < 24 ? real.z : real.w);
                             const float4 v4 = *reinterpret_cast<const float4*>(sc + 132 + 4 * lane);
                             const int b4 = 4 * (lane & 7);
-                            if ((w >> b4) & 1) vmax = fmaxf(vmax, v4.x);
-                            if ((w >> (b4 + 1)) & 1) vmax = fmaxf(vmax, v4.y);
-                            if ((w >> (b4 + 2)) & 1) vmax = fmaxf(vmax, v4.z);
-                            if ((w >> (b4 + 3)) & 1) vmax = fmaxf(vmax, v4.w);
+                            if ((w >> b4) & 1) vmax = fmaxf(vmax, fabsf(v4.x));
+                            if ((w >> (b4 + 1)) & 1) vmax = fmaxf(vmax, fabsf(v4.y));
+                            if ((w >> (b4 + 2)) & 1) vmax = fmaxf(vmax, fabsf(v4.z));
+                            if ((w >> (b4 + 3)) & 1) vmax = fmaxf(vmax, fabsf(v4.w));
 #pragma unroll
                             for (int off = 16; off > 0; off >>= 1)
                                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));

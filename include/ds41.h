@@ -624,6 +624,12 @@ size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int6
  *   mask nullable [Tq, mask_words] int64, max_q <= 64 * mask_words <= 256
  * A page outside 0 .. n_pages - 1 raises DS41_E_INDEX and its rows are not
  * seen.  Rows behind len in the last page are never used, whatever they hold.
+ * On a bf16 cache the weights are rounded to bf16; on an e4m3 cache p_j times its
+ * row's v scale is rounded to f16 in a unit that follows the largest of the rows
+ * that the query sees: each is off by 2^-11 of itself at most, or by 2^-33 of the
+ * largest p_j vs_j (2^-121 of the largest p_j, if that is more).  Values up to 2^96
+ * and, on an e4m3 cache, keys up to 2^96 are taken; larger ones may give infinities,
+ * NaN or sums of fewer bits.
  * A NaN or an infinity in a bf16 v row can reach the tokens of its sequence
  * that do not see it.  B == 0, Tq == 0 or max_q == 0 is a no-op. */
 int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const void* k_cache,

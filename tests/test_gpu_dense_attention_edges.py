@@ -85,3 +85,107 @@ def test_rows_behind_the_end_are_not_used(n, shape, left):
             else:
                 rows.fill_(min(left, torch.finfo(t.dtype).max) if left < math.inf else left)
         ref.close(*attend(q, cache, table, n), *want)
+
+
+# ---------------------------------------------------------------------------
+# Value rows of very different sizes (e4m3)
+# ---------------------------------------------------------------------------
+# Here a row's weights are charged with their own sizes.  The weights p_j vs_j of an
+# e4m3 cache are rounded to f16 in a unit that brings the largest of the keys that the
+# row sees to 2^8 at least, so what f16's smallest step of 2^-24 adds is half of it,
+# 2^-25, times 2^-8 of that largest weight, for every code: 2^-33 max_j(p_j vs_j)
+# sum_j |code_j|; and no unit is below 2^-96 of the largest p_j: 2^-121 p_max sum_j
+# |code_j|.  (Keys are dealt to warps and CTAs, each with a unit of its own from its
+# keys, which is not larger.)
+def close_by_weight(q, cache, table, n, visible, got, sink=None):
+    k, v, vs = rows_of(cache, table, n)
+    hd = q.shape[2]
+    o, lse, tol, ltol = ref.attend(q, k, v, visible, hd ** -0.5, sink)
+    per = q.shape[1] // k.shape[1]
+    for h in range(q.shape[1]):
+        s = torch.where(visible, q[:, h].double() @ k[:, h // per].T * hd ** -0.5, -math.inf)
+        p = torch.exp(s - torch.where(lse[:, h] == -math.inf, 0.0, lse[:, h])[:, None])
+        x = torch.where(visible.any(0), vs[:, h // per].double(), 0.0)
+        codes = torch.where(visible.any(0)[:, None],
+                            v[:, h // per].abs() / vs[:, h // per].double()[:, None], 0.0)
+        unit = 2.0 ** -33 * (p * x).amax(1) + 2.0 ** -121 * p.amax(1)
+        tol[:, h] += unit[:, None] * (visible.double() @ codes)
+    ref.close(*got, o, lse, tol, ltol)
+
+
+def aligned(g, d, nh, n, kvh, hd):
+    """Queries and keys, with a channel that all queries have alike (a key's entry
+    there moves its scores of all rows)."""
+    q, k, v = randn(g, d, nh, hd), randn(g, n, kvh, hd), randn(g, n, kvh, hd)
+    q[..., 0] = 4.0
+    k[..., 0] = 0.0
+    return q, k, v
+
+
+@pytest.mark.parametrize("gain", [2.0 ** 8, 2.0 ** 16, 2.0 ** 20, 2.0 ** 40])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_large_value_row_of_little_weight(hd, shape, gain):
+    """Key 300 has a weight of e^-(hd^-0.5 1200) and values `gain` times the rest's."""
+    d, nh, kvh = shape
+    n = 800
+    q, k, v = aligned(gen(d + hd), d, nh, n, kvh, hd)
+    k[300, :, 0] = -300.0
+    v[300] *= gain
+    cache, table = packed_cache(k, v, 32, True)
+    got = attend(q, cache, table, n)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_large_value_row_that_is_not_seen(shape, gain):
+    """A sibling branch, and rows just before the window, with values `gain` times
+    the rest's."""
+    d, nh, kvh = shape
+    n, hd = 613, 128
+    q, k, v = aligned(gen(d), d, nh, n, kvh, hd)
+    pre = n - d
+    v[pre + 1] *= gain              # seen by drafted token 1 only
+    cache, table = packed_cache(k, v, 16, True)
+    bits = [1 << t | (1 if t > 1 else 0) for t in range(d)]
+    got = attend(q, cache, table, n, bits)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, bits, 0, DEV), got)
+    window = 200
+    v[pre + 1] /= gain
+    v[:pre - window + 1] *= gain    # before what the first token sees
+    cache, table = packed_cache(k, v, 64, True)
+    got = attend(q, cache, table, n, None, window)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, window, DEV), got)
+
+
+@pytest.mark.parametrize("spread", [6, 20, 50])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+@pytest.mark.parametrize("n", [64, 3000])
+def test_value_scales_far_apart(n, shape, spread):
+    """Any key may hold the row's largest p_j vs_j."""
+    d, nh, kvh = shape
+    hd = 128
+    g = gen(n + spread)
+    q, k, v = randn(g, d, nh, hd), randn(g, n, kvh, hd), randn(g, n, kvh, hd)
+    k = k * 3.0
+    cache, table = packed_cache(k, v, 64, True)
+    e = torch.randint(-spread, spread + 1, cache.v_scales.shape, generator=g, device=DEV)
+    cache.v_scales.mul_(torch.exp2(e.float()))
+    sink = torch.randn(nh, generator=g, device=DEV)
+    for snk in (None, sink):
+        got = attend(q, cache, table, n, sink=snk)
+        close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got, snk)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -60, 2.0 ** 60, 2.0 ** 96])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_values_all_small_or_all_large(shape, size):
+    d, nh, kvh = shape
+    n, hd = 900, 64
+    g = gen(d)
+    q, k, v = randn(g, d, nh, hd), randn(g, n, kvh, hd), randn(g, n, kvh, hd) * size
+    v[5] = 0.0
+    cache, table = packed_cache(k, v, 128, True)
+    got = attend(q, cache, table, n)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got)
