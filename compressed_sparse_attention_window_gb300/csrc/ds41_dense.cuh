@@ -28,6 +28,9 @@ int check_paged(const char* name, const void* k, const void* v, const float* ks,
 // Host: the heads' counts, the head width, scale and window of a call.
 int check_heads(const char* name, int64_t nh, int64_t kvh, int64_t hd, float scale,
                 int64_t window);
+// A window of 2^31 or more holds every sequence: none (sums and differences of a window
+// and positions then stay far from the end of 64 bits).
+inline int64_t finite_window(int64_t window) { return window >> 31 ? 0 : window; }
 // strides between tokens and between heads, in elements
 inline bool good_strides(int64_t tok, int64_t head, int64_t hd) {
     return tok % 8 == 0 && head % 8 == 0 && head >= hd && tok >= hd;

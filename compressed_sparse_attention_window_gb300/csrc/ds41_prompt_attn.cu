@@ -666,7 +666,7 @@ extern "C" int ds41_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q
     p.lse = lse;
     p.Tq = Tq;
     p.Tk = Tk;
-    p.window = window;
+    p.window = finite_window(window);
     p.B = (int)B;
     p.max_q = (int)max_q;
     p.nh = (int)nh;

@@ -560,7 +560,9 @@ extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t 
     if (B < 1 || Tq < 1 || max_q < 1 || max_q > 256 || max_len < 0 || kvh < 1 || nh < kvh ||
         nh % kvh || hd < 1 || window < 0)
         return 0;
-    return tree::make_plan(B, max_q, max_len, nh, kvh, hd, window, fmt, sm_count_once()).bytes();
+    return tree::make_plan(B, max_q, max_len, nh, kvh, hd, finite_window(window), fmt,
+                           sm_count_once())
+        .bytes();
 }
 
 extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
@@ -588,6 +590,7 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
                  (long long)max_q);
     DS41_REQUIRE(window == 0 || window >= max_q, DS41_E_ARG,
                  "%s: window=%lld is below max_q=%lld", name, (long long)window, (long long)max_q);
+    window = finite_window(window);
     if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
     DS41_REQUIRE(q && o && cu_q && lens && page_table, DS41_E_ARG,
                  "%s: q, page_table, lens, cu_q and o must be non-null", name);

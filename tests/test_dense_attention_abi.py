@@ -126,3 +126,12 @@ def test_binding_refuses_what_is_no_tensor_or_cache():
                  lambda: ds41.tree_attn_fwd(None, cache, idx[None], idx, idx, 1, 1, 1.0)):
         with pytest.raises(TypeError):
             call()
+
+
+@pytest.mark.parametrize("window", [1 << 31, (1 << 63) - 257, (1 << 63) - 1])
+def test_workspace_of_a_window_larger_than_any_sequence(lib, window):
+    """As without a window: the sum of the window and the tokens must not wrap."""
+    for nh, max_q in ((8, 1), (8, 40), (64, 40)):
+        sizes = [lib.ds41_tree_attn_workspace_bytes(8, 8 * max_q, max_q, 32768, nh, 2, 128, w, 1)
+                 for w in (0, window)]
+        assert sizes[0] == sizes[1] > 0

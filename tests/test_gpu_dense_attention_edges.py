@@ -189,3 +189,25 @@ def test_values_all_small_or_all_large(shape, size):
     cache, table = packed_cache(k, v, 128, True)
     got = attend(q, cache, table, n)
     close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got)
+
+
+# ---------------------------------------------------------------------------
+# The largest windows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 1 << 31, (1 << 63) - 1])
+def test_window_larger_than_any_sequence(window):
+    """The results of no window, bit for bit; more queries than keys among them."""
+    g = gen(90)
+    for hd in (64, 128):
+        for lens_q, lens_k in (([40, 9, 70], [12, 9, 3]), ([33, 200], [533, 200])):
+            q, k, v = (randn(g, n, h, hd) for n, h in
+                       ((sum(lens_q), 8), (sum(lens_k), 2), (sum(lens_k), 2)))
+            both = [ds41.prompt_attn_fwd(q, k, v, cu(lens_q), cu(lens_k), max(lens_q), 0.1, window=w)
+                    for w in (0, window)]
+            assert torch.equal(*both)
+    for d, nh, kvh in (FEW, MIDDLING, MANY):
+        q, k, v = randn(g, d, nh, 64), randn(g, 500, kvh, 64), randn(g, 500, kvh, 64)
+        cache, table = packed_cache(k, v, 32, True)
+        for n in (500, d):
+            both = [attend(q, cache, table, n, None, w) for w in (0, window)]
+            assert all(torch.equal(a, b) for a, b in zip(*both))
