@@ -29,7 +29,7 @@ struct Args {
     float scale_log2;
     int64_t window;
     // the work: see `Share`
-    int block, align;  // keys of a block; first keys are multiples of align
+    int block, align;  // keys of a block; first keys are multiples of align, at most a page
     int tile_rows;     // rows of a tile
     int row_tiles;                // of the most drafted tokens
     int workers;
@@ -55,15 +55,31 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b) {
            s.len <= a.max_len && s.len <= (int64_t)a.max_pages * a.kv.page;
     return s;
 }
-// The first key that some row of the sequence may see, rounded down: no token
-// stands before the last earlier row.
+// The first key that is looked at: the first that some row of the sequence does see,
+// rounded down within its page, as pages wholly before it have left the window and may
+// be gone from the table, or be another sequence's.  A token with an empty mask row
+// stands one place before the others; it is looked for only where that key is in
+// another page (or group of rows).  (Loops that are not unrolled: nothing reaches them
+// without a mask and a window, and every warp fetches past them.)
 __device__ __forceinline__ int first_key(const Args& a, const Seq& s) {
-    const int64_t lo = a.window ? (int64_t)s.len - s.n - a.window : 0;
-    return lo > 0 ? (int)(lo & ~(int64_t)(a.align - 1)) : 0;
+    const int64_t at = a.window ? (int64_t)s.len - s.n - a.window + 1 : 0;
+    if (at <= 0) return 0;
+    if (a.mask && (at & (a.align - 1)) == 0) {
+        const int64_t* bits = a.mask + (int64_t)s.q0 * a.mask_words;
+#pragma unroll 1
+        for (int t = 0; t < s.n; t++, bits += a.mask_words) {
+            uint64_t any = 0;
+#pragma unroll 1
+            for (int i = 0; i * 64 < s.n; i++)
+                any |= (uint64_t)bits[i] << (s.n - 64 * i < 64 ? 64 * (i + 1) - s.n : 0);
+            if (any == 0) return (int)at - a.align;
+        }
+    }
+    return (int)(at & ~(int64_t)(a.align - 1));
 }
 
-__device__ __forceinline__ int blocks_of(const Args& a, const Seq& s) {
-    return (s.len - first_key(a, s) + a.block - 1) / a.block;
+__device__ __forceinline__ int blocks_of(const Args& a, const Seq& s, int first) {
+    return (s.len - first + a.block - 1) / a.block;
 }
 __device__ __forceinline__ int tiles_of(const Args& a, const Seq& s) {
     return (s.n * a.G + a.tile_rows - 1) / a.tile_rows;
@@ -92,7 +108,8 @@ __device__ __forceinline__ Share find_share(const Args& a, int64_t* sh, bool rep
     int64_t mine = 0;
     for (int b = b0; b < b1; b++) {
         const Seq s = load_seq(a, b);
-        if (s.ok && s.n > 0) mine += (int64_t)blocks_of(a, s) * tiles_of(a, s) * a.kvh;
+        if (s.ok && s.n > 0)
+            mine += (int64_t)blocks_of(a, s, first_key(a, s)) * tiles_of(a, s) * a.kvh;
         if (!s.ok && report) raise_status(a.status, DS41_E_INDEX);
     }
     int64_t sum = mine;
@@ -119,8 +136,9 @@ __device__ __forceinline__ Share find_share(const Args& a, int64_t* sh, bool rep
         int b = b0;
         for (; b < b1; b++) {
             const Seq s = load_seq(a, b);
-            const int64_t n =
-                s.ok && s.n > 0 ? (int64_t)blocks_of(a, s) * tiles_of(a, s) * a.kvh : 0;
+            int64_t n = 0;
+            if (s.ok && s.n > 0)
+                n = (int64_t)blocks_of(a, s, first_key(a, s)) * tiles_of(a, s) * a.kvh;
             if (rem < n) break;
             rem -= n;
         }
@@ -140,6 +158,7 @@ __device__ __forceinline__ Share find_share(const Args& a, int64_t* sh, bool rep
 struct Piece {
     Seq s;
     int b, h, tile, first, count, n_blocks;
+    int key;  // its first
 };
 __device__ __forceinline__ bool next_piece(const Args& a, Share& w, Piece& p) {
     if (w.left <= 0) return false;
@@ -147,7 +166,8 @@ __device__ __forceinline__ bool next_piece(const Args& a, Share& w, Piece& p) {
         if (w.b >= a.B) return false;
         p.s = load_seq(a, w.b);
         if (!p.s.ok || p.s.n == 0) continue;
-        p.n_blocks = blocks_of(a, p.s);
+        const int key = first_key(a, p.s);
+        p.n_blocks = blocks_of(a, p.s, key);
         const int tiles = tiles_of(a, p.s);
         const int64_t unit = w.at / p.n_blocks;
         if (unit >= (int64_t)tiles * a.kvh) continue;
@@ -155,6 +175,7 @@ __device__ __forceinline__ bool next_piece(const Args& a, Share& w, Piece& p) {
         p.h = (int)(unit / tiles);
         p.tile = (int)(unit % tiles);
         p.first = (int)(w.at - unit * p.n_blocks);
+        p.key = key + p.first * a.block;
         p.count = (int)min((int64_t)(p.n_blocks - p.first), w.left);
         w.at += p.count;
         w.left -= p.count;

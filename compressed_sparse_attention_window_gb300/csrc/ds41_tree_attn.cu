@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         const Seq s = pc.s;
         const int h = pc.h;
         const int rows = s.n * a.G;  // at most 16
-        const int k0 = first_key(a, s) + pc.first * BLOCK, k1 = min(s.len, k0 + pc.count * BLOCK);
+        const int k0 = pc.key, k1 = min(s.len, k0 + pc.count * BLOCK);
         if (threadIdx.x == 0) note_ends(a, pc);
 
         uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
@@ -627,7 +627,7 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
     a.lse = lse;
     a.B = (int)B;
     a.block = pl.block;
-    a.align = pl.align;
+    a.align = pl.align < page ? pl.align : (int)page;
     a.tile_rows = pl.tile_rows;
     a.row_tiles = pl.row_tiles;
     a.workers = pl.workers;

@@ -137,7 +137,7 @@ __device__ __forceinline__ void plan_step(const Args& a, Share& share, const Ste
     w.pc = pc;
     w.rows = pc.s.n * a.G;
     w.r0 = pc.tile * QT * 128;
-    w.k0 = first_key(a, pc.s) + pc.first * KB;
+    w.k0 = pc.key;
     w.k1 = min(pc.s.len, w.k0 + pc.count * KB);
     w.n_blocks = pc.count;
     w.tail = (w.k1 - w.k0) - (pc.count - 1) * KB;

@@ -623,7 +623,9 @@ size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int6
  *     max_len and max_pages * page;  cu_q [B + 1] int32, n <= max_q
  *   mask nullable [Tq, mask_words] int64, max_q <= 64 * mask_words <= 256
  * A page outside 0 .. n_pages - 1 raises DS41_E_INDEX and its rows are not
- * seen.  Rows behind len in the last page are never used, whatever they hold.
+ * seen; pages with no row that a token sees (before the window) are not looked
+ * at, whatever the table has there.  Rows behind len in the last page are never
+ * used, whatever they hold.
  * On a bf16 cache the weights are rounded to bf16; on an e4m3 cache p_j times its
  * row's v scale is rounded to f16 in a unit that follows the largest of the rows
  * that the query sees: each is off by 2^-11 of itself at most, or by 2^-33 of the

@@ -211,3 +211,71 @@ def test_window_larger_than_any_sequence(window):
         for n in (500, d):
             both = [attend(q, cache, table, n, None, w) for w in (0, window)]
             assert all(torch.equal(a, b) for a, b in zip(*both))
+
+
+# ---------------------------------------------------------------------------
+# Pages that have left the window
+# ---------------------------------------------------------------------------
+def evict(cache, table, first):
+    """The pages whose rows are all before row `first` go to someone else: out of the
+    table (half of them), or kept in it with another sequence's rows, NaN among them."""
+    page = cache.k.shape[2]
+    for i in range(first // page):
+        p = int(table[0, i])
+        for t in cache:
+            if t is not None and t.dtype != torch.float8_e4m3fn:
+                t[p] = math.nan
+            elif t is not None:
+                t[p].view(torch.uint8).fill_(0x7f)  # NaN
+        if i % 2 == 0 or i == first // page - 1 and i % 4 == 1:
+            table[0, i] = -1
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_pages_before_the_window_may_be_gone(shape, page, e4m3):
+    """No error and no trace of them, for windows that end anywhere in a page and a
+    128-key block."""
+    d, nh, kvh = shape
+    n, hd = 1100, 64
+    g = gen(page + d)
+    q, k, v = randn(g, d, nh, hd), randn(g, n, kvh, hd), randn(g, n, kvh, hd)
+    pre = n - d
+    up = [0]
+    for t in range(1, d):
+        up.append(int(torch.randint(0, t, (1,), generator=torch.Generator().manual_seed(t))))
+    tree = []
+    for t in range(d):
+        tree.append((tree[up[t]] if t else 0) | 1 << t)
+    lost = list(tree)
+    lost[d // 2] = 0                # a token that sees no drafted row: it stands at pre - 1
+    kept, _ = packed_cache(k, v, page, e4m3)
+    _, vs = None, None
+    for first in (512, 513, 527, 528, 640, 700):  # the first row that token 0 sees
+        for bits in (None, tree, lost):
+            window = pre - first + 1
+            cache, table = packed_cache(k, v, page, e4m3)
+            kx, vx, vs = rows_of(cache, table, n)
+            visible = ref.tree_visible(d, n, bits, window, DEV)
+            want = ref.attend(q, kx, vx, visible, hd ** -0.5, None, vs)
+            evict(cache, table, first - (1 if bits is lost else 0))
+            ref.close(*attend(q, cache, table, n, bits, window), *want)
+            assert ds41.device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_pages_inside_the_window_are_missed(shape):
+    """A page with a row that some token sees has to be there."""
+    d, nh, kvh = shape
+    g = gen(91)
+    q, k, v = randn(g, d, nh, 64), randn(g, 600, kvh, 64), randn(g, 600, kvh, 64)
+    cache, table = packed_cache(k, v, 16, True)
+    pre = 600 - d
+    table[0, 20] = -1               # rows 320 .. 335
+    empty = [0] * d
+    for window, bits, code in ((pre - 335 + 1, None, 4), (pre - 336 + 1, None, 0),
+                               (pre - 335, empty, 4), (pre - 335, None, 0),
+                               (pre - 336, empty, 0)):
+        attend(q, cache, table, 600, bits, window)
+        assert ds41.device_status() == code, (window, bits, code)
