@@ -206,14 +206,21 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
     pdl_trigger();
     const int h = blockIdx.x, c = (threadIdx.x % L) * 16;
     const int64_t r = row_block() * (THREADS / L) + threadIdx.x / L;
-    if (c >= a.kv.hd || r >= a.rows || r >= a.cu[a.B]) return;  // behind the last: nobody's
+    if (h == 0 && row_block() == 0)  // one CTA reports the sequences that break their limits
+        for (int i = threadIdx.x; i < a.B; i += THREADS)
+            if (a.cu[i] < 0 || a.cu[i + 1] < a.cu[i] || a.cu[i + 1] > a.rows)
+                raise_status(a.status, DS41_E_INDEX);
+    if (c >= a.kv.hd || r >= a.rows) return;
     int b = 0, end = a.B;  // the last b with cu[b] <= r
     while (end - b > 1) {
         const int mid = (b + end) >> 1;
         if (a.cu[mid] <= r) b = mid;
         else end = mid;
     }
-    const int64_t pos = r - a.cu[b] + (a.starts ? a.starts[b] : 0);
+    const int64_t first = a.cu[b], last = a.cu[b + 1];
+    // before the first sequence, behind the last: nobody's
+    if (r < first || r >= last || first < 0 || last > a.rows) return;
+    const int64_t pos = r - first + (a.starts ? a.starts[b] : 0);
     const int64_t pi = pos >> a.kv.page_shift;
     int64_t pg = -1;
     if (pos >= 0 && pi < a.max_pages) pg = a.table[(int64_t)b * a.max_pages + pi];

@@ -794,8 +794,8 @@ def kv_cache_read(cache: KvCache, page_table: torch.Tensor, cu_k: torch.Tensor, 
                   v: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """ds41_kv_cache_read: the sequences' rows, packed: k and v [rows, kvh, hd]
     bf16 (given or new).  Sequence b gets cu_k[b + 1] - cu_k[b] rows from
-    position starts[b] (0 without starts); rows behind cu_k[-1] are left as
-    they were (uninitialised in a new tensor)."""
+    position starts[b] (0 without starts); rows before cu_k[0] and behind
+    cu_k[-1] are left as they were (uninitialised in a new tensor)."""
     return (_binding or _dense()).kv_cache_read(cache, page_table, cu_k, rows, starts, k, v)
 
 

@@ -530,9 +530,9 @@ int ds41_attn_out_proj(ds41_bf16* o, const float* freqs_cis, int64_t max_pos,
  * h / (nh / kvh); hd is a multiple of 16 of at most 128.  Index arrays
  * (slots, cu_q, cu_k, lens, starts, page_table, mask) need the alignment of
  * their type only.  A packed batch of B sequences is described by prefix sums
- * cu [B + 1] int32, cu[0] <= cu[1] <= ...: sequence b owns rows cu[b] ..
- * cu[b + 1] - 1 of the packed tensor; rows behind cu[B] belong to nobody and
- * what they hold in an output is left as it was.  Sequences may be empty.
+ * cu [B + 1] int32, 0 <= cu[0] <= cu[1] <= ...: sequence b owns rows cu[b] ..
+ * cu[b + 1] - 1 of the packed tensor; rows before cu[0] and behind cu[B] belong to
+ * nobody and what they hold in an output is left as it was.  Sequences may be empty.
  * Sizes that only the device knows (prefix sums, lengths, pages, slots) are
  * checked there: a sequence or row that breaks its limits is skipped (its
  * output rows left as they were unless said otherwise), nothing outside the
@@ -568,7 +568,9 @@ int ds41_kv_cache_write(const ds41_bf16* k, int64_t k_stride, const ds41_bf16* v
  *   page_table [B, max_pages] int32;  starts nullable [B] int32 (NULL: 0)
  *   k, v [rows, kvh, hd] bf16 outputs
  * A position before 0 or whose page is outside the table or the cache reads
- * as zeros and raises DS41_E_INDEX.  rows == 0 or B == 0 is a no-op. */
+ * as zeros and raises DS41_E_INDEX.  A sequence whose prefix sums fall, start
+ * below 0 or pass `rows` is skipped and raises it too.  rows == 0 or B == 0 is a
+ * no-op. */
 int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scales,
                        const float* v_scales, int fmt, int64_t n_pages, int64_t page, int64_t kvh,
                        int64_t hd, const int32_t* page_table, int64_t max_pages,

@@ -279,3 +279,42 @@ def test_pages_inside_the_window_are_missed(shape):
                                (pre - 336, empty, 0)):
         attend(q, cache, table, 600, bits, window)
         assert ds41.device_status() == code, (window, bits, code)
+
+
+# ---------------------------------------------------------------------------
+# Prefix sums of a read
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_read_leaves_rows_before_the_first_sequence(e4m3):
+    g = gen(92)
+    cache = filled_cache(g, 6, 2, 16, 64, e4m3)
+    table = i32([[0, 1, 2], [3, 4, 5]])
+    for starts in (None, i32([17, 3])):
+        k, v = (torch.full((60, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        ds41.kv_cache_read(cache, table, i32([5, 30, 50]), 60, starts=starts, k=k, v=v)
+        assert ds41.device_status() == 0
+        want = ds41.kv_cache_read(cache, table, i32([0, 25, 45]), 45, starts=starts)
+        for x, w in zip((k, v), want):
+            assert bool((x[:5] == 7.0).all() and (x[50:] == 7.0).all())
+            assert torch.equal(x[5:50], w)
+
+
+def test_read_skips_sequences_outside_its_rows():
+    """Prefix sums that fall, start below 0 or pass the outputs' rows: those sequences
+    are skipped with an error."""
+    g = gen(93)
+    cache = filled_cache(g, 8, 2, 16, 64, True)
+    table = i32([[0, 1], [2, 3], [4, 5]])
+    whole = ds41.kv_cache_read(cache, table, i32([0, 20, 30, 40]), 40)
+    for prefix, rows, good in (([0, 20, 30, 41], 40, (0, 30)),    # past the rows
+                               ([0, 20, 50, 60], 40, (0, 20)),
+                               ([0, 20, 20, 10], 40, (0, 20)),    # falls
+                               ([-3, 20, 30, 40], 40, (20, 40)),  # before the rows
+                               ([0, 20, 1 << 30, -(1 << 31)], 40, (0, 20))):
+        k, v = (torch.full((rows, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        ds41.kv_cache_read(cache, table, i32(prefix), rows, k=k, v=v)
+        assert ds41.device_status() == 4, prefix
+        a, b = good
+        for x, w in zip((k, v), whole):
+            assert torch.equal(x[a:b], w[a:b]), prefix
+            assert bool((x[:a] == 7.0).all() and (x[b:] == 7.0).all()), prefix
