@@ -21,6 +21,8 @@ struct PagedKv {
     int page, page_shift, kvh, hd;
 };
 
+// Host: a cache's format, heads and head width.
+int check_cache_form(const char* name, int fmt, int64_t kvh, int64_t hd);
 // Host: checks a cache's layout (DS41_E_ARG with a message) and fills `out`.
 int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
                 int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out);

@@ -14,15 +14,20 @@
 
 namespace ds41 {
 
-int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
-                int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out) {
+int check_cache_form(const char* name, int fmt, int64_t kvh, int64_t hd) {
     DS41_REQUIRE(fmt == DS41_KV_BF16 || fmt == DS41_KV_E4M3, DS41_E_ARG,
                  "%s: fmt=%d is neither DS41_KV_BF16 nor DS41_KV_E4M3", name, fmt);
-    DS41_REQUIRE(page >= 16 && page <= 256 && (page & (page - 1)) == 0, DS41_E_ARG,
-                 "%s: page=%lld must be a power of two of 16 .. 256", name, (long long)page);
     DS41_REQUIRE(kvh >= 1 && kvh <= 1024 && hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
                  "%s: kvh=%lld hd=%lld (hd a multiple of 16, at most 128)", name, (long long)kvh,
                  (long long)hd);
+    return DS41_OK;
+}
+
+int check_paged(const char* name, const void* k, const void* v, const float* ks, const float* vs,
+                int fmt, int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, PagedKv* out) {
+    if (int rc = check_cache_form(name, fmt, kvh, hd)) return rc;
+    DS41_REQUIRE(page >= 16 && page <= 256 && (page & (page - 1)) == 0, DS41_E_ARG,
+                 "%s: page=%lld must be a power of two of 16 .. 256", name, (long long)page);
     DS41_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31) / kvh, DS41_E_ARG,
                  "%s: n_pages=%lld kvh=%lld", name, (long long)n_pages, (long long)kvh);
     DS41_REQUIRE(k && v && aligned16(k) && aligned16(v), DS41_E_ARG,

@@ -541,6 +541,18 @@ Plan make_plan(int64_t B, int64_t max_q, int64_t max_len, int64_t nh, int64_t kv
     return p;
 }
 
+int check_sizes(const char* name, int64_t B, int64_t Tq, int64_t max_q, int64_t max_len,
+                int64_t window) {
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && max_q >= 0 && max_q <= 256 &&
+                     max_len >= 0 && max_len < lim / 2,
+                 DS41_E_RANGE, "%s: B=%lld Tq=%lld max_q=%lld (at most 256) max_len=%lld", name,
+                 (long long)B, (long long)Tq, (long long)max_q, (long long)max_len);
+    DS41_REQUIRE(window == 0 || window >= max_q, DS41_E_ARG,
+                 "%s: window=%lld is below max_q=%lld", name, (long long)window, (long long)max_q);
+    return DS41_OK;
+}
+
 template <int HD, bool E4M3>
 int launch_few(const Args& a, const char* name, cudaStream_t st) {
     constexpr int smem = Cfg<HD, E4M3>::BYTES;
@@ -557,8 +569,9 @@ using namespace ds41;
 extern "C" size_t ds41_tree_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q,
                                                  int64_t max_len, int64_t nh, int64_t kvh,
                                                  int64_t hd, int64_t window, int fmt) {
-    if (B < 1 || Tq < 1 || max_q < 1 || max_q > 256 || max_len < 0 || kvh < 1 || nh < kvh ||
-        nh % kvh || hd < 1 || window < 0)
+    const char* name = "ds41_tree_attn_workspace_bytes";
+    if (check_heads(name, nh, kvh, hd, 1.0f, window) || check_cache_form(name, fmt, kvh, hd) ||
+        tree::check_sizes(name, B, Tq, max_q, max_len, window) || B == 0 || Tq == 0 || max_q == 0)
         return 0;
     return tree::make_plan(B, max_q, max_len, nh, kvh, hd, finite_window(window), fmt,
                            sm_count_once())
@@ -580,16 +593,12 @@ extern "C" int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_h
     if (int rc = check_paged(name, k_cache, v_cache, k_scales, v_scales, fmt, n_pages, page, kvh,
                              hd, &a.kv))
         return rc;
-    const int64_t lim = int64_t(1) << 31;
-    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && max_q >= 0 && max_q <= 256 &&
-                     max_len >= 0 && max_len < lim / 2 && max_pages >= 0 && max_pages < lim,
-                 DS41_E_RANGE, "%s: B=%lld Tq=%lld max_q=%lld (at most 256) max_len=%lld", name,
-                 (long long)B, (long long)Tq, (long long)max_q, (long long)max_len);
+    if (int rc = tree::check_sizes(name, B, Tq, max_q, max_len, window)) return rc;
+    DS41_REQUIRE(max_pages >= 0 && max_pages < int64_t(1) << 31, DS41_E_RANGE, "%s: max_pages=%lld",
+                 name, (long long)max_pages);
     DS41_REQUIRE(!mask || (mask_words >= 1 && mask_words <= 4 && max_q <= 64 * mask_words),
                  DS41_E_ARG, "%s: mask_words=%lld for max_q=%lld", name, (long long)mask_words,
                  (long long)max_q);
-    DS41_REQUIRE(window == 0 || window >= max_q, DS41_E_ARG,
-                 "%s: window=%lld is below max_q=%lld", name, (long long)window, (long long)max_q);
     window = finite_window(window);
     if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
     DS41_REQUIRE(q && o && cu_q && lens && page_table, DS41_E_ARG,

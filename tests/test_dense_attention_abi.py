@@ -135,3 +135,16 @@ def test_workspace_of_a_window_larger_than_any_sequence(lib, window):
         sizes = [lib.ds41_tree_attn_workspace_bytes(8, 8 * max_q, max_q, 32768, nh, 2, 128, w, 1)
                  for w in (0, window)]
         assert sizes[0] == sizes[1] > 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(hd=144), dict(hd=24), dict(nh=8192), dict(kvh=2048, nh=2048), dict(B=65536),
+    dict(max_q=257), dict(window=3), dict(fmt=2), dict(fmt=-1), dict(max_len=1 << 30),
+    dict(Tq=1 << 31), dict(B=0), dict(max_len=-1), dict(window=-1)])
+def test_workspace_of_sizes_that_are_refused_is_zero(lib, kw):
+    """What the call refuses, or has nothing to do for, needs no scratch."""
+    size = dict(B=1, Tq=4, max_q=4, max_len=32, nh=4, kvh=2, hd=128, window=0, fmt=1)
+    names = list(size)
+    assert lib.ds41_tree_attn_workspace_bytes(*size.values()) > 0
+    size |= kw
+    assert lib.ds41_tree_attn_workspace_bytes(*(size[n] for n in names)) == 0
