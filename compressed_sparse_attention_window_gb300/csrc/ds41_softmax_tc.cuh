@@ -22,6 +22,9 @@ constexpr float SM_WEIGHT_LOG2 = 8.0f;
 constexpr float SM_WEIGHT_MOVE_LOG2 = 14.0f;
 constexpr float SM_UNIT_MIN_LOG2 = -96.0f;
 constexpr float SM_UNIT_MOVE_LOG2 = 100.0f;
+// The scale of a row's scores with its queries' exponent in it is not below this: at 0 a
+// masked score of -inf would be NaN.  (Scores that small are 0 beside each other.)
+constexpr float SM_C_MIN = 0x1p-126f;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             int z, uint64_t* bar) {

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
                 const int e = query_exponent(mb);
                 const float down = exp2f((float)-e);
-                cr[i] *= exp2f((float)e);
+                cr[i] = fmaxf(cr[i] * exp2f((float)e), tc::SM_C_MIN);
 #pragma unroll
                 for (int st = 0; st < HD / 16; st++) {
                     qf[st][i] = bf16x2_to_f16x2(qf[st][i], down);

@@ -583,8 +583,9 @@ __global__ void __launch_bounds__(TcCfg<D, E4M3, PAIR>::THREADS, 1)
                 const int used0 = uniform(w.used0[t]);
                 float c = a.scale_log2;
                 if (E4M3)
-                    c *= exp2f((float)reinterpret_cast<const int8_t*>(
-                        sm + C::QE_OFF)[(PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane]);
+                    c = fmaxf(c * exp2f((float)reinterpret_cast<const int8_t*>(
+                                      sm + C::QE_OFF)[(PAIR ? 128 * t : 0) + 32 * (warp & 3) + lane]),
+                              SM_C_MIN);
                 RowState st;
                 for (int j = PAIR ? 0 : t, i = 0; j < n_blocks; j += PAIR ? 1 : 2, i++) {
                     const int gb = blocks0 + j, sl = gb % SCN;

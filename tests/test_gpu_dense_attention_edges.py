@@ -318,3 +318,27 @@ def test_read_skips_sequences_outside_its_rows():
         for x, w in zip((k, v), whole):
             assert torch.equal(x[a:b], w[a:b]), prefix
             assert bool((x[:a] == 7.0).all() and (x[b:] == 7.0).all()), prefix
+
+
+# ---------------------------------------------------------------------------
+# The smallest scales
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 1e-35])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_scales_and_queries_next_to_nothing(shape, scale):
+    """Scores that are 0 but for their last bits: the average of what a token sees."""
+    d, nh, kvh = shape
+    n, hd = 150, 64
+    g = gen(94)
+    q = randn(g, d, nh, hd) * 2.0 ** -115
+    k, v = randn(g, n, kvh, hd), randn(g, n, kvh, hd)
+    for e4m3 in (True, False):
+        cache, table = packed_cache(k, v, 32, e4m3)
+        kx, vx, vs = rows_of(cache, table, n)
+        lse = torch.empty(d, nh, device=DEV)
+        o = ds41.tree_attn_fwd(q, cache, table, i32([n]), cu([d]), d, n, scale, lse=lse)
+        ref.close(o, lse, *ref.attend(q, kx, vx, ref.tree_visible(d, n, None, 0, DEV), scale, None,
+                                      vs))
+    lse = torch.empty(d, nh, device=DEV)
+    o = ds41.prompt_attn_fwd(q, k, v, cu([d]), cu([n]), d, scale, lse=lse)
+    ref.close(o, lse, *ref.attend(q, k, v, ref.prompt_visible(d, n, 0, DEV), scale, None))
