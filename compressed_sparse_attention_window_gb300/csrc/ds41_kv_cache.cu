@@ -55,8 +55,9 @@ int check_heads(const char* name, int64_t nh, int64_t kvh, int64_t hd, float sca
                  (long long)kvh);
     DS41_REQUIRE(hd >= 16 && hd <= 128 && hd % 16 == 0, DS41_E_ARG,
                  "%s: hd=%lld must be a multiple of 16 of at most 128", name, (long long)hd);
-    DS41_REQUIRE(scale > 0.0f && scale <= 3.4028234e38f, DS41_E_ARG,
-                 "%s: scale=%g must be positive", name, (double)scale);
+    // (the kernels take scale log2(e))
+    DS41_REQUIRE(scale > 0.0f && scale <= 0x1p127f, DS41_E_ARG,
+                 "%s: scale=%g must be positive and at most 2^127", name, (double)scale);
     DS41_REQUIRE(window >= 0, DS41_E_ARG, "%s: window=%lld", name, (long long)window);
     return DS41_OK;
 }

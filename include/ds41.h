@@ -589,7 +589,8 @@ int ds41_kv_cache_read(const void* k_cache, const void* v_cache, const float* k_
  *     elements between tokens and between heads (multiples of 8, hd dense)
  *   cu_q, cu_k [B + 1] int32;  max_q: no sequence has more queries (a longer
  *     one raises DS41_E_INDEX)
- *   sink nullable [nh] f32 (NULL: no sink);  scale > 0;  window >= 0 (0: none)
+ *   sink nullable [nh] f32 (NULL: no sink);  0 < scale <= 2^127;  window >= 0
+ *     (0: none)
  *   o [Tq, nh, hd] bf16 output;  lse nullable [Tq, nh] f32 output, the natural
  *     log of the denominator
  * A NaN or an infinity in a v row of a sequence can reach every query of that

@@ -148,3 +148,10 @@ def test_workspace_of_sizes_that_are_refused_is_zero(lib, kw):
     assert lib.ds41_tree_attn_workspace_bytes(*size.values()) > 0
     size |= kw
     assert lib.ds41_tree_attn_workspace_bytes(*(size[n] for n in names)) == 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_scale_that_overflows_in_units_of_log2_is_refused(lib, scale):
+    """scale * log2(e) is what the kernels take."""
+    assert prompt(lib, scale=scale) == ARG and tree(lib, scale=scale) == ARG
+    assert b"scale" in lib.ds41_last_error()
