@@ -69,9 +69,8 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _build_binding(force: bool, verbose: bool) -> None:
-    """The extension module (its libraries are those that torch has loaded)."""
-    if not (force or _stale(BINDING, [BINDING_SRC, __file__] + _headers())):
-        return
+    """The extension module (its libraries are those that torch has loaded).  It is
+    stale, too, when the torch, the Python or the command it was built with change."""
     import torch
     cxx = shutil.which("g++") or "g++"
     root = os.path.dirname(torch.__file__)
@@ -81,15 +80,22 @@ def _build_binding(force: bool, verbose: bool) -> None:
     tmp = BINDING + f".{os.getpid()}.tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           *(x for d in dirs for x in ("-I", d)), BINDING_SRC, "-o", tmp,
+           *(x for d in dirs for x in ("-I", d)), BINDING_SRC,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
            "-ltorch_python"]
+    made_with = "\n".join([torch.__version__, sysconfig.get_config_var("SOABI") or "", *cmd])
+    stamp = os.path.join(BUILD, "binding.txt")
+    if not (force or _stale(BINDING, [BINDING_SRC, __file__] + _headers())):
+        if os.path.exists(stamp) and open(stamp).read() == made_with:
+            return
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(made_with)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
