@@ -162,18 +162,6 @@ __device__ __forceinline__ float move_unit(float top, float e, float c, float& m
     return f;
 }
 
-// tcgen05.wait::ld with the registers it waits for, so that nothing that uses them
-// moves ahead of it; unlike tc_wait_ld it lets loads from shared memory pass
-__device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]));
-    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-
 // 32 scores of a row, scaled by ks, with those that are not seen at -inf.
 template <bool SCALED, bool MASKED>
 __device__ __forceinline__ void prepare32(uint32_t (&s)[32], const float* ks, uint32_t vis) {
@@ -234,38 +222,18 @@ __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint32_t (&pk
         pk[e / 2 + 1] = SCALED ? f16x2(p[2], p[3]) : bf16x2(p[2], p[3]);
     }
 }
-// The lazy reference has moved: what was computed with the old one times f - the
-// D columns of O at tm_o (with have_o) and the weights that this block has
-// written already, n of 32 keys each, at tm_p.
-template <int D, bool SCALED>
-__device__ __forceinline__ void rescale(uint32_t tm_p, int n, uint32_t tm_o, bool have_o, float f) {
+// The reference has moved: the D columns of O at tm_o, computed with the old one, times f.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t tm_o, float f) {
     tc_wait_st();
-    if (have_o) {
 #pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-            uint32_t ov[16];
-            tc_ld16(tm_o + x, ov);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e++) ov[e] = __float_as_uint(u2f(ov[e]) * f);
-            tc_st16(tm_o + x, ov);
-        }
-    }
-#pragma unroll 1
-    for (int x = 0; x < 16 * n; x += 16) {
-        uint32_t pv[16];
-        tc_ld16(tm_p + x, pv);
+    for (int x = 0; x < D; x += 16) {
+        uint32_t ov[16];
+        tc_ld16(tm_o + x, ov);
         tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-            if (SCALED) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&pv[e]));
-                pv[e] = f16x2(v.x * f, v.y * f);
-            } else {
-                pv[e] = bf16x2(u2f(pv[e] << 16) * f, u2f(pv[e] & 0xffff0000u) * f);
-            }
-        }
-        tc_st16(tm_p + x, pv);
+        for (int e = 0; e < 16; e++) ov[e] = __float_as_uint(u2f(ov[e]) * f);
+        tc_st16(tm_o + x, ov);
     }
 }
 
@@ -281,8 +249,7 @@ __device__ __forceinline__ void rescale(uint32_t tm_p, int n, uint32_t tm_o, boo
 // unit by 2^14), which is so in few blocks, the reference moves and what it has been used
 // for is rescaled - the caller has seen the products before this block complete.  All
 // lanes of a warp take part; `live` = the row exists.
-//
-// The plain form holds the 128 scores in registers.
+// Both forms hold the 128 scores in registers.
 template <int D, bool MASKED>
 __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool have_o,
                                               const uint32_t (&vis)[4], float c, bool live,
@@ -303,7 +270,7 @@ __device__ __forceinline__ void softmax_block(uint32_t tm_s, uint32_t tm_o, bool
         const float f = move ? ex2((st.m - top) * c) : 1.0f;
         if (move) st.m = top;
         st.l *= f;
-        if (have_o) rescale<D, false>(tm_s, 0, tm_o, true, f);
+        if (have_o) rescale<D>(tm_o, f);
     }
     float base = st.m == -INFINITY ? 0.0f : st.m * c;
     if (fabsf(base) > 0x1p22f) {
@@ -368,7 +335,7 @@ __device__ __forceinline__ void softmax_block_scaled(uint32_t tm_s, uint32_t tm_
         }
         const float f = live ? move_unit(top, e, c, st.m, st.lr) : 1.0f;
         st.l *= f;
-        if (have_o) rescale<D, true>(tm_s, 0, tm_o, true, f);
+        if (have_o) rescale<D>(tm_o, f);
     }
     float base = st.m == -INFINITY ? 0.0f : fmaf(st.m, c, st.lr);
     if (fabsf(base) > 0x1p22f) {
