@@ -9,7 +9,7 @@
 // cache runs on f16 products: its codes are exact in f16 (one instruction for
 // two codes; bf16 takes four), the queries become f16 with an exponent per row,
 // and l and O carry 2^-lr, which keeps the largest p_j vs_j that a row sees at 2^8 ..
-// 2^14 of f16's range, and follows it alone: a row of values that weighs nothing may
+// 2^15 of f16's range, and follows it alone: a row of values that weighs nothing may
 // have any scale (RowState in ds41_softmax_tc.cuh).  The scales stay outside the
 // products.
 //
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
         const int64_t lo = view[0].lo > view[1].lo ? view[0].lo : view[1].lo;
 
         float o[HD / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
-        float lr[2] = {0.0f, 0.0f};
+        float lr[2] = {0.0f, 0.0f}, vlim = 0.0f;
+        float lim[2] = {tc::SM_RESCALE_LOG2, tc::SM_RESCALE_LOG2};
         float base[2] = {0.0f, 0.0f};  // c m + lr: what an exponent is reduced by
         for (int i = 0; i < mine; i++) {
             fetch(i + C::STAGES - 1);
@@ -255,23 +256,20 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
             for (int i2 = 0; i2 < 2; i2++)
                 mx[i2] = fmaxf(fmaxf(sc[0][2 * i2], sc[0][2 * i2 + 1]),
                                fmaxf(sc[1][2 * i2], sc[1][2 * i2 + 1]));
-            float lim[2] = {tc::SM_RESCALE_LOG2, tc::SM_RESCALE_LOG2};
-            if (E4M3) {
-                // (a key that neither row sees has no part in it: behind the sequence's end
-                // its scale is whatever an earlier user left there)
-                float vm = 0.0f;
-#pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    const bool x = !masked || fmaxf(sc[n][0], sc[n][2]) > -INFINITY;
-                    const bool y = !masked || fmaxf(sc[n][1], sc[n][3]) > -INFINITY;
-                    vm = fmaxf(vm, fmaxf(x ? fabsf(vs[n].x) : 0.0f, y ? fabsf(vs[n].y) : 0.0f));
-                }
-                const float up = tc::unit_limit(vm);
-                lim[0] = lr[0] + up;
-                lim[1] = lr[1] + up;
-            }
+            // (scales that no key needs may be NaN, which fmaxf skips, or anything: the look
+            // at the group that follows is exact)
+            float vm = 0.0f;
+            if (E4M3)
+                vm = fmaxf(fmaxf(fabsf(vs[0].x), fabsf(vs[0].y)),
+                           fmaxf(fabsf(vs[1].x), fabsf(vs[1].y)));
             const bool look = (mx[0] - m[0]) * cr[0] > lim[0] || (mx[1] - m[1]) * cr[1] > lim[1];
-            if (__any_sync(0xffffffffu, look)) {
+            if (__any_sync(0xffffffffu, look || (E4M3 && vm > vlim))) {
+                float up = 0.0f;
+                if (E4M3) {
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+                    vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+                    up = tc::unit_limit(vm, vlim);
+                }
 #pragma unroll
                 for (int i2 = 0; i2 < 2; i2++) {
                     float t = mx[i2], f = 1.0f;
@@ -289,6 +287,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tree_few_kernel(const Args a
                         e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 1));
                         e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
                         f = tc::move_unit(t, e, cr[i2], m[i2], lr[i2]);
+                        lim[i2] = lr[i2] + up;
                     } else if ((t - m[i2]) * cr[i2] > tc::SM_RESCALE_LOG2) {
                         f = exp2f((m[i2] - t) * cr[i2]);
                         m[i2] = t;
