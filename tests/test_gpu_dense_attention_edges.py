@@ -342,3 +342,26 @@ def test_scales_and_queries_next_to_nothing(shape, scale):
     lse = torch.empty(d, nh, device=DEV)
     o = ds41.prompt_attn_fwd(q, k, v, cu([d]), cu([n]), d, scale, lse=lse)
     ref.close(o, lse, *ref.attend(q, k, v, ref.prompt_visible(d, n, 0, DEV), scale, None))
+
+
+# ---------------------------------------------------------------------------
+# A key that takes nearly all the weight and has next to no values
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -60, 2.0 ** -8])
+@pytest.mark.parametrize("nats", [8, 30, 60, 200])
+@pytest.mark.parametrize("shape", [FEW, MIDDLING, MANY])
+def test_heavy_key_of_small_values(shape, nats, size):
+    """As the first token of a text often is: what the others add is kept, down to
+    2^-96 of the heavy key's weight."""
+    d, nh, kvh = shape
+    n, hd = 500, 128
+    q, k, v = aligned(gen(d), d, nh, n, kvh, hd)
+    at = 0 if nats == 30 else 260
+    k[at, :, 0] = nats * hd ** 0.5 / 4.0
+    v[at] *= size
+    cache, table = packed_cache(k, v, 64, True)
+    got = attend(q, cache, table, n)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got)
+    sink = torch.full((nh,), float(nats), device=DEV)
+    got = attend(q, cache, table, n, sink=sink)
+    close_by_weight(q, cache, table, n, ref.tree_visible(d, n, None, 0, DEV), got, sink)
