@@ -7,7 +7,7 @@
 // largest e4m3 value, so the largest element gets the largest code; the floor
 // keeps s a normal number, so a zero row has codes +-0.  A row that holds a NaN
 // or an infinity keeps the scale NaN and zero codes: whatever reads it sees NaN.
-// Reading back is bf16(code * s), one rounding.
+// Reading back is bf16(code * s), the product rounded to f32 first.
 //
 // Both kernels move bytes and little else.
 #include "ds41_dense.cuh"
@@ -204,8 +204,8 @@ struct ReadArgs {
 };
 
 // L lanes take one (row, head), 16 elements of K and of V each; the rows of a CTA
-// are consecutive, as they lie in a page.  (33000 rows of 8 heads of 128, 205 MB: 37
-// us of GPU time, 82% of the copy rate.)
+// are consecutive, as they lie in a page.  (33000 rows of 8 heads of 128, 205 MB: 38
+// us of GPU time, 79% of the copy rate.)
 template <int L, bool E4M3>
 __global__ void __launch_bounds__(THREADS) kv_read_kernel(const ReadArgs a) {
     pdl_wait();

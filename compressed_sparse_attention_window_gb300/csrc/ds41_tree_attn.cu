@@ -26,7 +26,7 @@
 // columns (for P V) in which each lane's share is contiguous: the same order on
 // both operands leaves the product unchanged.  The codes are widened in
 // registers on the way into the products.  (48 sequences of one token over up to 8191
-// keys, 64 heads of 128 over 8, e4m3: 94 us with the join, 5.0 TB/s.)
+// keys, 64 heads of 128 over 8, e4m3: 95 us with the join, 5.0 TB/s.)
 #include "ds41_internal.cuh"
 #include "ds41_tree.cuh"
 
@@ -510,9 +510,9 @@ __global__ void __launch_bounds__(NT) tree_join_kernel(const Args a) {
 // The shape of a call's work: which kernel, its tiles and blocks, its workers.
 // Up to 16 rows per key/value head the few-row kernel, three CTAs an SM (two on a
 // bf16 cache, whose stages are twice as large); above, the tensor-core kernel,
-// one CTA an SM (for 8 rows it takes 213 us where the few-row kernel takes 94, 48
+// one CTA an SM (for 8 rows it takes 213 us where the few-row kernel takes 95, 48
 // sequences of 8191 e4m3 keys).  Above 128 rows two tiles share a block's loads
-// (4 sequences of 512 rows over 32768 keys: 218 us, 231 a tile at a time).  Never more
+// (4 sequences of 512 rows over 32768 keys: 217 us, 231 a tile at a time).  Never more
 // workers than blocks at the longest lengths.
 struct Plan {
     bool many;

@@ -35,7 +35,7 @@
 // copies' waits look at every second use of a stage and are right because stages are
 // freed in the ring's order.  8 trees of up to
 // 16 tokens over 16384 keys, 32 heads of 128 over 8: 91 us; 4 of 64 over 32768, 64
-// heads: 218 us.
+// heads: 221 us.
 #include "ds41_internal.cuh"
 #include "ds41_tree.cuh"
 

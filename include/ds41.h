@@ -523,9 +523,9 @@ int ds41_attn_out_proj(ds41_bf16* o, const float* freqs_cis, int64_t max_pos,
 /* ------------------------------------------------------------------------ */
 /* Dense attention with grouped heads, and its paged cache                    */
 /* ------------------------------------------------------------------------ */
-/* No counterpart on the pages: the layers of a model that attend to every
- * earlier token with separate keys and values, and the small model that drafts
- * tokens for it, stand beside the compressed sparse ones.  nh query heads
+/* No counterpart on the pages, whose model has no such layers: for a model that
+ * attends to every earlier token with separate keys and values and is served
+ * beside the sparse one (one that drafts tokens for it, say).  nh query heads
  * share kvh key/value heads, nh % kvh == 0, query head h reads head
  * h / (nh / kvh); hd is a multiple of 16 of at most 128.  Index arrays
  * (slots, cu_q, cu_k, lens, starts, page_table, mask) need the alignment of
