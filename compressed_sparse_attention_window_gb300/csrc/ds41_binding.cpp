@@ -1,5 +1,6 @@
-// ds41_binding.cpp - the Python side of the dense attention's calls as an extension
-// module: their checks of tensors, new outputs and the call itself.
+// ds41_binding.cpp - the Python side of the calls of the dense attention, its pages and
+// blocks, and of beam search as an extension module: their checks of tensors, new outputs
+// and the call itself.
 //
 // What bounds the smallest of these calls is the host: a call through ctypes spends
 // 20 us on attributes of tensors and conversions of 30 arguments in front of a kernel
@@ -15,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
+#include <type_traits>
 
 #include "ds41.h"
 
@@ -27,6 +29,21 @@ decltype(&ds41_kv_cache_read) g_read;
 decltype(&ds41_prompt_attn_fwd) g_prompt;
 decltype(&ds41_tree_attn_fwd) g_tree;
 decltype(&ds41_tree_attn_workspace_bytes) g_tree_ws;
+decltype(&ds41_kv_pages_take) g_take;
+decltype(&ds41_kv_pages_free) g_free;
+decltype(&ds41_kv_pages_fork) g_fork;
+decltype(&ds41_kv_pages_fork_workspace_bytes) g_fork_ws;
+decltype(&ds41_kv_pages_copy) g_copy;
+decltype(&ds41_kv_pages_compact) g_compact;
+decltype(&ds41_kv_pages_compact_workspace_bytes) g_compact_ws;
+decltype(&ds41_beam_select) g_beam;
+decltype(&ds41_beam_select_workspace_bytes) g_beam_ws;
+decltype(&ds41_kv_block_keys) g_keys;
+decltype(&ds41_block_select) g_select;
+decltype(&ds41_block_attn_fwd) g_blocks;
+decltype(&ds41_block_attn_workspace_bytes) g_blocks_ws;
+decltype(&ds41_block_prompt_attn_fwd) g_block_prompt;
+decltype(&ds41_block_prompt_attn_workspace_bytes) g_block_prompt_ws;
 PyObject* g_failed;  // failed(name, code) raises
 
 // An exception that a Python call has set.
@@ -137,12 +154,48 @@ const int32_t* pages(const Tensor& t, at::Device dev, int64_t B) {
     return (const int32_t*)data("page_table", t, dev, {B, t.size(1)}, at::kInt);
 }
 // The output given, or a new one.
-Tensor output(const char* name, PyObject* o, at::Device dev, at::IntArrayRef shape) {
-    if (o == Py_None)
-        return at::empty(shape, at::TensorOptions().dtype(at::kBFloat16).device(dev));
+Tensor output(const char* name, PyObject* o, at::Device dev, at::IntArrayRef shape,
+              at::ScalarType type = at::kBFloat16) {
+    if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
     const Tensor& t = tensor(name, o);
-    data(name, t, dev, shape, at::kBFloat16);
+    data(name, t, dev, shape, type);
     return t;
+}
+// The scratch of a call: what is given, or new.
+struct Scratch {
+    std::optional<Tensor> t;
+    void* p = nullptr;
+    Scratch(PyObject* o, at::Device dev, size_t need) : t(maybe("ws", o)) {
+        if (t) {
+            TORCH_CHECK_VALUE(t->device() == dev && t->is_contiguous() && t->nbytes() >= need,
+                              "ws: expected a contiguous tensor of at least ", need, " bytes on ",
+                              dev);
+        } else if (need > 0) {
+            t = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+        }
+        if (t && need > 0) p = t->data_ptr();
+    }
+};
+// A cache's block keys, or none.
+struct Keys {
+    int8_t* codes = nullptr;
+    float* scales = nullptr;
+};
+Keys keys_of(PyObject* o, at::Device dev, int64_t n_pages, int64_t kvh, int64_t hd) {
+    if (o == Py_None) return {};
+    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 2,
+                     "keys: expected BlockKeys, got ", Py_TYPE(o)->tp_name);
+    return {(int8_t*)data("keys.codes", tensor("keys.codes", PyTuple_GET_ITEM(o, 0)), dev,
+                          {n_pages, kvh, hd}, at::kChar),
+            (float*)data("keys.scales", tensor("keys.scales", PyTuple_GET_ITEM(o, 1)), dev,
+                         {n_pages, kvh}, at::kFloat)};
+}
+const int32_t* ints(const char* name, PyObject* o, at::Device dev, int64_t n) {
+    return (const int32_t*)data(name, tensor(name, o), dev, {n}, at::kInt);
+}
+int64_t count_of(const char* name, const Tensor& t) {
+    TORCH_CHECK_VALUE(t.dim() == 1, name, ": expected one dimension, got ", t.sizes());
+    return t.size(0);
 }
 ds41_stream_t stream_of(at::Device dev) {
     return (ds41_stream_t)c10::cuda::getCurrentCUDAStream(dev.index()).stream();
@@ -275,43 +328,350 @@ PyObject* tree_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const Tensor o = output("o", a[11], dev, q.sizes());
     auto op = (ds41_bf16*)o.data_ptr();
     const size_t need = g_tree_ws(B, Tq, max_q, max_len, nh, c.kvh, c.hd, window, c.fmt);
-    std::optional<Tensor> ws = maybe("ws", a[13]);
-    if (ws) {
-        TORCH_CHECK_VALUE(ws->device() == dev && ws->is_contiguous() && ws->nbytes() >= need,
-                          "ws: expected a contiguous tensor of at least ", need, " bytes on ", dev);
-    } else if (need > 0) {
-        ws = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
-    }
-    void* wp = ws && need > 0 ? ws->data_ptr() : nullptr;
+    const Scratch ws(a[13], dev, need);
     const ds41_stream_t st = stream_of(dev);
     run("ds41_tree_attn_fwd", [&] {
         return g_tree(qh.p, qh.tok, qh.head, c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, pt,
                       table.size(1), lp, cq, mask, words, B, Tq, max_q, max_len, nh, c.kvh, c.hd,
-                      scale, window, sink, op, lse, wp, need, st);
+                      scale, window, sink, op, lse, ws.p, need, st);
     });
     return given_or(a[11], o);
     END_HANDLE_TH_ERRORS
 }
 
-// bind(write, read, prompt, tree, tree_workspace_bytes, failed): the addresses of the
-// entry points, and what raises for a code that is not DS41_OK
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+// kv_pages_take(refs, page_table, lens, new_lens, page, ws)
+PyObject* kv_pages_take(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
     count(n_args, 6);
-    g_write = (decltype(g_write))integer(a[0]);
-    g_read = (decltype(g_read))integer(a[1]);
-    g_prompt = (decltype(g_prompt))integer(a[2]);
-    g_tree = (decltype(g_tree))integer(a[3]);
-    g_tree_ws = (decltype(g_tree_ws))integer(a[4]);
-    Py_XSETREF(g_failed, Py_NewRef(a[5]));
+    const Tensor &refs = tensor("refs", a[0]), &table = tensor("page_table", a[1]);
+    const at::Device dev = here(refs);
+    const int64_t n_pages = count_of("refs", refs), page = integer(a[4]);
+    const int64_t B = count_of("lens", tensor("lens", a[2]));
+    auto rp = (int32_t*)ints("refs", a[0], dev, n_pages);
+    auto pt = (int32_t*)pages(table, dev, B);
+    auto lp = ints("lens", a[2], dev, B), np = ints("new_lens", a[3], dev, B);
+    const Scratch ws(a[5], dev, (size_t)n_pages * 4);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_pages_take", [&] {
+        return g_take(rp, n_pages, page, pt, table.size(1), lp, np, B, ws.p, (size_t)n_pages * 4,
+                      st);
+    });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_pages_free(refs, page_table, lens, page)
+PyObject* kv_pages_free(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 4);
+    const Tensor &refs = tensor("refs", a[0]), &table = tensor("page_table", a[1]);
+    const at::Device dev = here(refs);
+    const int64_t n_pages = count_of("refs", refs), page = integer(a[3]);
+    const int64_t B = count_of("lens", tensor("lens", a[2]));
+    auto rp = (int32_t*)ints("refs", a[0], dev, n_pages);
+    const int32_t* pt = pages(table, dev, B);
+    auto lp = ints("lens", a[2], dev, B);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_pages_free",
+        [&] { return g_free(rp, n_pages, page, pt, table.size(1), lp, B, st); });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_pages_fork(cache, refs, page_table, lens, parents, table_out, lens_out, replace,
+// keys, ws) -> (table_out, lens_out)
+PyObject* kv_pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 10);
+    const Tensor &refs = tensor("refs", a[1]), &table = tensor("page_table", a[2]);
+    const at::Device dev = here(refs);
+    const Cache c = cache_of(a[0], dev);
+    const int64_t B = count_of("lens", tensor("lens", a[3]));
+    const int64_t n = count_of("parents", tensor("parents", a[4]));
+    auto rp = (int32_t*)ints("refs", a[1], dev, c.n_pages);
+    const int32_t* pt = pages(table, dev, B);
+    auto lp = ints("lens", a[3], dev, B), pp = ints("parents", a[4], dev, n);
+    const int64_t max_pages = table.size(1);
+    const Tensor out = output("table_out", a[5], dev, {n, max_pages}, at::kInt);
+    const Tensor out_lens = output("lens_out", a[6], dev, {n}, at::kInt);
+    const int replace = PyObject_IsTrue(a[7]);
+    python_ok(replace >= 0);
+    const Keys keys = keys_of(a[8], dev, c.n_pages, c.kvh, c.hd);
+    const size_t need = g_fork_ws(c.n_pages, B, n);
+    const Scratch ws(a[9], dev, need);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_pages_fork", [&] {
+        return g_fork(c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, c.kvh, c.hd, keys.codes,
+                      keys.scales, rp, pt, max_pages, lp, B, pp, n, replace,
+                      (int32_t*)out.data_ptr(), (int32_t*)out_lens.data_ptr(), ws.p, need, st);
+    });
+    PyObject* both = PyTuple_New(2);
+    python_ok(both != nullptr);
+    PyTuple_SET_ITEM(both, 0, given_or(a[5], out));
+    PyTuple_SET_ITEM(both, 1, given_or(a[6], out_lens));
+    return both;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_pages_copy(cache, src, dst, rows, keys)
+PyObject* kv_pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 5);
+    const Tensor& src = tensor("src", a[1]);
+    const at::Device dev = here(src);
+    const Cache c = cache_of(a[0], dev);
+    const int64_t n = count_of("src", src);
+    auto sp = ints("src", a[1], dev, n), dp = ints("dst", a[2], dev, n);
+    auto rp = (const int32_t*)data_or_null("rows", a[3], dev, {n}, at::kInt);
+    const Keys keys = keys_of(a[4], dev, c.n_pages, c.kvh, c.hd);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_pages_copy", [&] {
+        return g_copy(c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, c.kvh, c.hd, keys.codes,
+                      keys.scales, sp, dp, rp, n, st);
+    });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_pages_compact(cache, refs, page_table, lens, keys, live, ws) -> live
+PyObject* kv_pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 7);
+    const Tensor &refs = tensor("refs", a[1]), &table = tensor("page_table", a[2]);
+    const at::Device dev = here(refs);
+    const Cache c = cache_of(a[0], dev);
+    const int64_t B = count_of("lens", tensor("lens", a[3]));
+    auto rp = (int32_t*)ints("refs", a[1], dev, c.n_pages);
+    auto pt = (int32_t*)pages(table, dev, B);
+    auto lp = ints("lens", a[3], dev, B);
+    const Keys keys = keys_of(a[4], dev, c.n_pages, c.kvh, c.hd);
+    const Tensor live = output("live", a[5], dev, {1}, at::kInt);
+    const size_t need = g_compact_ws(c.n_pages);
+    const Scratch ws(a[6], dev, need);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_pages_compact", [&] {
+        return g_compact(c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, c.kvh, c.hd, keys.codes,
+                         keys.scales, rp, pt, table.size(1), lp, B, (int32_t*)live.data_ptr(),
+                         ws.p, need, st);
+    });
+    return given_or(a[5], live);
+    END_HANDLE_TH_ERRORS
+}
+
+// beam_select(logits, scores, k, ended, end_token, out_scores, parents, tokens, ws)
+// -> (out_scores, parents, tokens)
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 9);
+    const Tensor& x = tensor("logits", a[0]);
+    const at::Device dev = here(x);
+    const bool bf16 = x.scalar_type() == at::kBFloat16;
+    TORCH_CHECK_VALUE(x.dim() == 3 && (bf16 || x.scalar_type() == at::kFloat),
+                      "logits: expected float32 or bfloat16 [B, W, V], got ", x.scalar_type(), " ",
+                      x.sizes());
+    const int64_t B = x.size(0), W = x.size(1), V = x.size(2), k = integer(a[2]);
+    TORCH_CHECK_VALUE(x.stride(2) == 1 || V <= 1, "logits: strides ", x.strides(),
+                      ": the vocabulary must be dense");
+    auto sp = (const float*)data("scores", tensor("scores", a[1]), dev, {B, W}, at::kFloat);
+    const uint8_t* ended = nullptr;
+    if (a[3] != Py_None) {
+        const Tensor& e = tensor("ended", a[3]);
+        ended = (const uint8_t*)data(
+            "ended", e, dev, {B, W}, e.scalar_type() == at::kByte ? at::kByte : at::kBool);
+    }
+    const int64_t end_token = integer(a[4]);
+    TORCH_CHECK_VALUE(k >= 1 && k <= 128, "k=", k, " (1 .. 128)");
+    const int64_t shape[2] = {B, k};
+    const Tensor out = output("out_scores", a[5], dev, shape, at::kFloat);
+    const Tensor parents = output("parents", a[6], dev, shape, at::kInt);
+    const Tensor tokens = output("tokens", a[7], dev, shape, at::kInt);
+    const size_t need = g_beam_ws(B, W, V, k);
+    const Scratch ws(a[8], dev, need);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_beam_select", [&] {
+        return g_beam(x.data_ptr(), bf16 ? DS41_LOGITS_BF16 : DS41_LOGITS_F32, x.stride(0),
+                      x.stride(1), sp, ended, end_token, B, W, V, k, (float*)out.data_ptr(),
+                      (int32_t*)parents.data_ptr(), (int32_t*)tokens.data_ptr(), ws.p, need, st);
+    });
+    PyObject* all = PyTuple_New(3);
+    python_ok(all != nullptr);
+    PyTuple_SET_ITEM(all, 0, given_or(a[5], out));
+    PyTuple_SET_ITEM(all, 1, given_or(a[6], parents));
+    PyTuple_SET_ITEM(all, 2, given_or(a[7], tokens));
+    return all;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_block_keys(cache, keys, page_table, lens, max_new, starts)
+PyObject* kv_block_keys(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 6);
+    const Tensor &table = tensor("page_table", a[2]), &lens = tensor("lens", a[3]);
+    const at::Device dev = here(lens);
+    const Cache c = cache_of(a[0], dev);
+    TORCH_CHECK_TYPE(a[1] != Py_None, "keys: expected BlockKeys");
+    const Keys keys = keys_of(a[1], dev, c.n_pages, c.kvh, c.hd);
+    const int64_t B = count_of("lens", lens), max_new = integer(a[4]);
+    const int32_t* pt = pages(table, dev, B);
+    auto lp = ints("lens", a[3], dev, B);
+    auto starts = (const int32_t*)data_or_null("starts", a[5], dev, {B}, at::kInt);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_kv_block_keys", [&] {
+        return g_keys(c.k, c.ks, c.fmt, c.n_pages, c.page, c.kvh, c.hd, pt, table.size(1), lp,
+                      starts, B, max_new, keys.codes, keys.scales, st);
+    });
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// block_select(q, keys, page, page_table, lens, cu_q, max_q, max_len, topk, first, local,
+// idx) -> idx
+PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 12);
+    const Tensor &q = tensor("q", a[0]), &table = tensor("page_table", a[3]),
+                 &cu_q = tensor("cu_q", a[5]);
+    const at::Device dev = here(q);
+    TORCH_CHECK_TYPE(PyTuple_Check(a[1]) && PyTuple_GET_SIZE(a[1]) == 2,
+                     "keys: expected BlockKeys, got ", Py_TYPE(a[1])->tp_name);
+    const Tensor& codes = tensor("keys.codes", PyTuple_GET_ITEM(a[1], 0));
+    TORCH_CHECK_VALUE(codes.dim() == 3, "keys.codes: expected [n_pages, kvh, hd], got ",
+                      codes.sizes());
+    const int64_t n_pages = codes.size(0), kvh = codes.size(1), hd = codes.size(2);
+    const Keys keys = keys_of(a[1], dev, n_pages, kvh, hd);
+    const Heads qh = heads("q", q, dev, hd);
+    const int64_t Tq = q.size(0), nh = q.size(1), B = length("cu_q", cu_q), page = integer(a[2]);
+    const int64_t max_q = integer(a[6]), max_len = integer(a[7]), topk = integer(a[8]);
+    const int64_t first = integer(a[9]), local = integer(a[10]);
+    const int32_t* pt = pages(table, dev, B);
+    auto lp = ints("lens", a[4], dev, B), cq = ints("cu_q", a[5], dev, B + 1);
+    TORCH_CHECK_VALUE(topk >= 1 && topk <= 1024, "topk=", topk, " (1 .. 1024)");
+    const Tensor idx = output("idx", a[11], dev, {Tq, kvh, topk}, at::kInt);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_block_select", [&] {
+        return g_select(qh.p, qh.tok, qh.head, keys.codes, keys.scales, n_pages, page, kvh, hd, pt,
+                        table.size(1), lp, cq, B, Tq, max_q, max_len, nh, topk, first, local,
+                        (int32_t*)idx.data_ptr(), st);
+    });
+    return given_or(a[11], idx);
+    END_HANDLE_TH_ERRORS
+}
+
+// [Tq, kvh, topk]
+const int32_t* lists(PyObject* o, at::Device dev, int64_t Tq, int64_t kvh, int64_t& topk) {
+    const Tensor& t = tensor("idx", o);
+    TORCH_CHECK_VALUE(t.dim() == 3, "idx: expected [Tq, kvh, topk], got ", t.sizes());
+    topk = t.size(2);
+    return (const int32_t*)data("idx", t, dev, {Tq, kvh, topk}, at::kInt);
+}
+
+// block_attn_fwd(q, cache, page_table, lens, cu_q, max_q, idx, scale, sink, o, lse, ws)
+// -> o
+PyObject* block_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 12);
+    const Tensor &q = tensor("q", a[0]), &table = tensor("page_table", a[2]),
+                 &cu_q = tensor("cu_q", a[4]);
+    const at::Device dev = here(q);
+    const Cache c = cache_of(a[1], dev);
+    const Heads qh = heads("q", q, dev, c.hd);
+    const int64_t Tq = q.size(0), nh = q.size(1), B = length("cu_q", cu_q), max_q = integer(a[5]);
+    const int32_t* pt = pages(table, dev, B);
+    auto lp = ints("lens", a[3], dev, B), cq = ints("cu_q", a[4], dev, B + 1);
+    int64_t topk;
+    const int32_t* idx = lists(a[6], dev, Tq, c.kvh, topk);
+    const float scale = real(a[7]);
+    auto sink = (const float*)data_or_null("sink", a[8], dev, {nh}, at::kFloat);
+    auto lse = (float*)data_or_null("lse", a[10], dev, {Tq, nh}, at::kFloat);
+    const Tensor o = output("o", a[9], dev, q.sizes());
+    const size_t need = g_blocks_ws(Tq, topk, c.page, nh, c.kvh, c.hd, c.fmt);
+    const Scratch ws(a[11], dev, need);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_block_attn_fwd", [&] {
+        return g_blocks(qh.p, qh.tok, qh.head, c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, pt,
+                        table.size(1), lp, cq, idx, topk, B, Tq, max_q, nh, c.kvh, c.hd, scale,
+                        sink, (ds41_bf16*)o.data_ptr(), lse, ws.p, need, st);
+    });
+    return given_or(a[9], o);
+    END_HANDLE_TH_ERRORS
+}
+
+// block_prompt_attn_fwd(q, k, v, cu_q, cu_k, max_q, max_k, idx, block, scale, sink, o, lse,
+// ws) -> o
+PyObject* block_prompt_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 14);
+    const Tensor &q = tensor("q", a[0]), &k = tensor("k", a[1]), &v = tensor("v", a[2]);
+    const Tensor& cu_q = tensor("cu_q", a[3]);
+    const at::Device dev = here(q);
+    TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "q, k: expected [tokens, heads, hd], got ",
+                      q.sizes(), ", ", k.sizes());
+    const int64_t Tq = q.size(0), nh = q.size(1), hd = q.size(2), Tk = k.size(0), kvh = k.size(1);
+    const Heads qh = heads("q", q, dev, hd), kh = heads("k", k, dev, hd);
+    const Heads vh = heads("v", v, dev, hd);
+    TORCH_CHECK_VALUE(v.sizes() == k.sizes(), "v: expected ", k.sizes(), ", got ", v.sizes());
+    const int64_t B = length("cu_q", cu_q), max_q = integer(a[5]), max_k = integer(a[6]);
+    auto cq = ints("cu_q", a[3], dev, B + 1), ck = ints("cu_k", a[4], dev, B + 1);
+    int64_t topk;
+    const int32_t* idx = lists(a[7], dev, Tq, kvh, topk);
+    const int64_t block = integer(a[8]);
+    const float scale = real(a[9]);
+    auto sink = (const float*)data_or_null("sink", a[10], dev, {nh}, at::kFloat);
+    auto lse = (float*)data_or_null("lse", a[12], dev, {Tq, nh}, at::kFloat);
+    const Tensor o = output("o", a[11], dev, q.sizes());
+    const size_t need = g_block_prompt_ws(B, Tq, max_q, max_k, topk, block, nh, kvh);
+    const Scratch ws(a[13], dev, need);
+    const ds41_stream_t st = stream_of(dev);
+    run("ds41_block_prompt_attn_fwd", [&] {
+        return g_block_prompt(qh.p, qh.tok, qh.head, kh.p, kh.tok, kh.head, vh.p, vh.tok, vh.head,
+                              cq, ck, idx, topk, block, B, Tq, Tk, max_q, max_k, nh, kvh, hd,
+                              scale, sink, (ds41_bf16*)o.data_ptr(), lse, ws.p, need, st);
+    });
+    return given_or(a[11], o);
+    END_HANDLE_TH_ERRORS
+}
+
+// bind(failed, the entry points' addresses in this order ...): failed raises for a code that is
+// not DS41_OK
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    HANDLE_TH_ERRORS
+    count(n_args, 21);
+    int i = 0;
+    auto next = [&](auto& f) { f = (std::remove_reference_t<decltype(f)>)integer(a[++i]); };
+    next(g_write);
+    next(g_read);
+    next(g_prompt);
+    next(g_tree);
+    next(g_tree_ws);
+    next(g_take);
+    next(g_free);
+    next(g_fork);
+    next(g_fork_ws);
+    next(g_copy);
+    next(g_compact);
+    next(g_compact_ws);
+    next(g_beam);
+    next(g_beam_ws);
+    next(g_keys);
+    next(g_select);
+    next(g_blocks);
+    next(g_blocks_ws);
+    next(g_block_prompt);
+    next(g_block_prompt_ws);
+    Py_XSETREF(g_failed, Py_NewRef(a[0]));
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
 #define DS41_FAST(f) {#f, (PyCFunction)(void (*)())f, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {DS41_FAST(kv_cache_write), DS41_FAST(kv_cache_read),
-                           DS41_FAST(prompt_attn_fwd), DS41_FAST(tree_attn_fwd), DS41_FAST(bind),
-                           {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {DS41_FAST(kv_cache_write),   DS41_FAST(kv_cache_read),
+                           DS41_FAST(prompt_attn_fwd),  DS41_FAST(tree_attn_fwd),
+                           DS41_FAST(kv_pages_take),    DS41_FAST(kv_pages_free),
+                           DS41_FAST(kv_pages_fork),    DS41_FAST(kv_pages_copy),
+                           DS41_FAST(kv_pages_compact), DS41_FAST(beam_select),
+                           DS41_FAST(kv_block_keys),    DS41_FAST(block_select),
+                           DS41_FAST(block_attn_fwd),   DS41_FAST(block_prompt_attn_fwd),
+                           DS41_FAST(bind),             {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ds41_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,456 @@
+// ds41_blocks.cu - one key for each block (page) of the paged cache, and the blocks that
+// a cheap score against those keys picks for each query.
+//
+// Mathematics.  A block's key is the mean of its rows, summed in f32 in their order, as int8
+// codes with one scale: s = max(amax, 127 2^-126) f32(1/127), c = rint(m / s).  A
+// query row is rounded alike.  The product of the codes is a whole number below 127^2 128 <
+// 2^21, which f16 operands (exact up to 2048) and f32 sums give exactly in any order; the
+// score is two f32 products away, so the picks are the same wherever they are worked out.
+// The scale of a block is not negative, so it may follow the maximum over the heads.
+//
+// What bounds it.  The keys' sums: HBM, one read of the new rows' pages.  Selection for a
+// step of few tokens: a chain of latencies (the page table, the keys, the scores'
+// exchange, the ranking).  For prompts: the products (m16n8k16, blocks by columns of query
+// heads) and the ranking about alike.
+#include "ds41_dense.cuh"
+
+namespace ds41 {
+namespace blocks {
+
+constexpr float STEP = 1.0f / 127.0f;
+constexpr float FLOOR = 127.0f * 0x1p-126f;
+
+// Four elements of a row a lane (of hd of them, 0 behind): codes in a word, the row's scale.
+__device__ __forceinline__ float int8_row(const float (&x)[4], bool mine, float (&code)[4]) {
+    float m = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        m = fmaxf(m, fabsf(x[e]));
+        bad |= !(fabsf(x[e]) < INFINITY);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bad = __any_sync(0xffffffffu, bad && mine);
+    const float s = __fmul_rn(fmaxf(m, FLOOR), STEP);
+#pragma unroll
+    for (int e = 0; e < 4; e++) code[e] = bad ? 0.0f : rintf(__fdiv_rn(x[e], s));
+    return bad ? __uint_as_float(0x7fc00000u) : s;
+}
+
+struct KeyArgs {
+    PagedKv kv;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* starts;
+    int64_t max_pages, max_new;
+    int8_t* codes;
+    float* scales;
+    unsigned int* status;
+};
+
+constexpr int KEY_WARPS = 4;
+
+// A warp for a page and head, four elements a lane, sixteen rows in flight.
+template <bool E4M3>
+__global__ void __launch_bounds__(KEY_WARPS * 32) keys_kernel(const KeyArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int h = blockIdx.x * KEY_WARPS + (threadIdx.x >> 5);
+    const int64_t b = blockIdx.z;
+    const int len = a.lens[b], start = a.starts ? a.starts[b] : 0;
+    if (len < 0 || start < 0 || start > len || len - start > a.max_new ||
+        len > a.max_pages * a.kv.page) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+            raise_status(a.status, DS41_E_INDEX);
+        return;
+    }
+    if (h >= a.kv.kvh) return;
+    for (int64_t i = (start >> a.kv.page_shift) + (int64_t)blockIdx.y;
+         (i << a.kv.page_shift) < len && start < len; i += gridDim.y) {
+        const int64_t pg = a.table[b * a.max_pages + i];
+        if (pg < 0 || pg >= a.kv.n_pages) {
+            if (lane == 0) raise_status(a.status, DS41_E_INDEX);
+            continue;
+        }
+        const int n = (int)min((int64_t)a.kv.page, len - (i << a.kv.page_shift));
+        const bool mine = lane * 4 < a.kv.hd;
+        const int64_t row = paged_row(a.kv, pg, h, 0);
+        const uint8_t* p = a.kv.k + (row * a.kv.hd + (mine ? lane * 4 : 0)) * (E4M3 ? 1 : 2);
+        const int step = a.kv.hd * (E4M3 ? 1 : 2);
+        float sum[4] = {0, 0, 0, 0};
+        constexpr int U = 16;
+        for (int r0 = 0; r0 < n; r0 += U) {
+            uint2 w[U];
+            float s[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                w[u] = make_uint2(0, 0);
+                s[u] = 0.0f;
+                if (r0 + u >= n) continue;
+                if (E4M3) {
+                    w[u].x = __ldcs(reinterpret_cast<const uint32_t*>(p + (r0 + u) * step));
+                    s[u] = a.kv.ks[row + r0 + u];
+                } else {
+                    w[u] = __ldcs(reinterpret_cast<const uint2*>(p + (r0 + u) * step));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                float x[4];
+                if (E4M3) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16(w[u].x, lo, hi);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                    x[0] = __fmul_rn(f.x, s[u]);
+                    x[1] = __fmul_rn(f.y, s[u]);
+                    x[2] = __fmul_rn(g.x, s[u]);
+                    x[3] = __fmul_rn(g.y, s[u]);
+                } else {
+                    x[0] = __uint_as_float(w[u].x << 16);
+                    x[1] = __uint_as_float(w[u].x & 0xffff0000u);
+                    x[2] = __uint_as_float(w[u].y << 16);
+                    x[3] = __uint_as_float(w[u].y & 0xffff0000u);
+                }
+                if (r0 + u < n)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) sum[e] = __fadd_rn(sum[e], x[e]);
+            }
+        }
+        float code[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) sum[e] = mine ? __fdiv_rn(sum[e], (float)n) : 0.0f;
+        const float s = int8_row(sum, mine, code);
+        if (mine) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int e = 0; e < 4; e++) c |= ((uint32_t)(int)code[e] & 0xffu) << (8 * e);
+            *reinterpret_cast<uint32_t*>(a.codes + (pg * a.kv.kvh + h) * a.kv.hd + lane * 4) = c;
+        }
+        if (lane == 0) a.scales[pg * a.kv.kvh + h] = s;
+    }
+}
+
+struct SelectArgs {
+    const uint16_t* q;
+    int64_t q_tok, q_head;
+    const int8_t* codes;
+    const float* scales;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu_q;
+    int32_t* idx;
+    int64_t Tq, n_pages, max_pages;
+    int page, page_shift, kvh, hd, G, max_q, max_len, topk, first, local;
+    int TT;       // tokens of a CTA
+    int NB;       // room for blocks
+    int heads;    // query heads at a time, even
+    unsigned int* status;
+};
+
+constexpr int SEL_WARPS = 8;
+
+// four int8 codes -> their values as f16, exactly: a code plus 128 in the low bits of 1024
+__device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    x ^= 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half((uint16_t)0x6480));  // 1152
+    uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), off);
+    lo = *reinterpret_cast<uint32_t*>(&r);
+    r = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    hi = *reinterpret_cast<uint32_t*>(&r);
+}
+// larger for larger scores; a score that is not a number counts as -inf
+__device__ __forceinline__ uint32_t rank_of(float s) {
+    if (!(s == s)) s = -INFINITY;
+    const uint32_t u = __float_as_uint(s + 0.0f);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// Scores of TT tokens of a sequence for one key/value head, then the tokens' picks.
+// Products: 16 blocks (rows, codes straight from global memory into the fragments) by 8
+// columns; column 2 t + e of tile (quad, i) is token 4 quad + t, head 2 i + e, so that a lane
+// has all heads of its token and their maximum takes no exchange.  hd in the order of tree
+// attention's e4m3 fragments: lane c owns the codes 16 c .. and 64 + 16 c .. of a row.
+template <int HD>
+__global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int KS = HD / 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const int b = blockIdx.y, h = blockIdx.z;
+    const int q0 = a.cu_q[b];
+    const int64_t n64 = (int64_t)a.cu_q[b + 1] - q0;
+    const int len = a.lens[b];
+    if (q0 < 0 || n64 < 0 || n64 > a.max_q || q0 + n64 > a.Tq || len < n64 || len > a.max_len ||
+        len > a.max_pages * a.page) {
+        if (blockIdx.x == 0 && h == 0 && tid == 0) raise_status(a.status, DS41_E_INDEX);
+        return;
+    }
+    const int n = (int)n64, t0 = blockIdx.x * a.TT;
+    if (t0 >= n) return;
+    const int toks = min(a.TT, n - t0), quads = (toks + 3) / 4;
+    const int p0 = len - n + t0;                           // the first token's place
+    const int vis = ((p0 + toks - 1) >> a.page_shift) + 1;  // blocks that some token sees
+    // shared memory: the queries' fragments, their scales, the scores
+    const int pairs = a.heads / 2;
+    uint2* frag = reinterpret_cast<uint2*>(smem);  // [quad][pair][k step][32]
+    float* qs = reinterpret_cast<float*>(frag + (a.TT + 3) / 4 * pairs * KS * 32);  // [token][heads]
+    uint32_t* sc = reinterpret_cast<uint32_t*>(qs + (a.TT + 3) / 4 * 4 * a.heads);  // [token][NB]
+    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+
+    for (int h0 = 0; h0 < a.G; h0 += a.heads) {
+        const int hs = min(a.heads, a.G - h0), hp = (hs + 1) / 2;
+        for (int x = warp; x < quads * 4 * hp * 2; x += SEL_WARPS) {
+            const int t = x / (2 * hp), y = x % (2 * hp);
+            const bool real = t < toks && y < hs;
+            float v[4] = {0, 0, 0, 0}, code[4];
+            const bool mine = lane * 4 < a.hd;
+            if (real && mine) {
+                const uint2 w = *reinterpret_cast<const uint2*>(
+                    a.q + (q0 + t0 + t) * a.q_tok + ((int64_t)h * a.G + h0 + y) * a.q_head + lane * 4);
+                v[0] = __uint_as_float(w.x << 16);
+                v[1] = __uint_as_float(w.x & 0xffff0000u);
+                v[2] = __uint_as_float(w.y << 16);
+                v[3] = __uint_as_float(w.y & 0xffff0000u);
+            }
+            const float s = int8_row(v, mine, code);
+            if (lane * 4 < HD) {
+                const __half2 lo = __floats2half2_rn(code[0], code[1]);
+                const __half2 hi = __floats2half2_rn(code[2], code[3]);
+                const int piece = lane >> 2;
+                const int st = (piece >> 2) * 4 + (lane & 3), col = 2 * (t & 3) + (y & 1);
+                frag[(((t >> 2) * pairs + (y >> 1)) * KS + st) * 32 + col * 4 + (piece & 3)] =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                               *reinterpret_cast<const uint32_t*>(&hi));
+            }
+            if (lane == 0) qs[t * a.heads + y] = real ? s : __uint_as_float(0x7fc00000u);
+        }
+        __syncthreads();
+        for (int j0 = warp * 16; j0 < vis; j0 += SEL_WARPS * 16) {
+            uint32_t af[KS][4];
+            float ks[2];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const int j = j0 + g + 8 * r;
+                int64_t pg = j < vis ? table[j] : 0;
+                const bool ok = pg >= 0 && pg < a.n_pages;
+                if (!ok && c == 0) raise_status(a.status, DS41_E_INDEX);
+                const int64_t at = (ok ? pg : 0) * a.kvh + h;
+                ks[r] = ok ? a.scales[at] : __uint_as_float(0x7fc00000u);
+#pragma unroll
+                for (int x = 0; x < KS / 4; x++) {
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if ((c + 4 * x) * 16 < a.hd && ok)
+                        w = *reinterpret_cast<const uint4*>(a.codes + at * a.hd + (c + 4 * x) * 16);
+                    int8x4_to_f16(w.x, af[4 * x][r], af[4 * x][r + 2]);
+                    int8x4_to_f16(w.y, af[4 * x + 1][r], af[4 * x + 1][r + 2]);
+                    int8x4_to_f16(w.z, af[4 * x + 2][r], af[4 * x + 2][r + 2]);
+                    int8x4_to_f16(w.w, af[4 * x + 3][r], af[4 * x + 3][r + 2]);
+                }
+            }
+            for (int qd = 0; qd < quads; qd++) {
+                const int t = qd * 4 + c;
+                float best[2] = {__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u)};
+                for (int i = 0; i < hp; i++) {
+                    const uint2* f = frag + (qd * pairs + i) * KS * 32 + lane;
+                    float d[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int st = 0; st < KS; st++) {
+                        const uint2 w = f[st * 32];
+                        mma_f16(d, af[st][0], af[st][1], af[st][2], af[st][3], w.x, w.y);
+                    }
+                    const float2 s = *reinterpret_cast<const float2*>(qs + t * a.heads + 2 * i);
+                    best[0] = fmaxf(best[0], fmaxf(__fmul_rn(d[0], s.x), __fmul_rn(d[1], s.y)));
+                    best[1] = fmaxf(best[1], fmaxf(__fmul_rn(d[2], s.x), __fmul_rn(d[3], s.y)));
+                }
+                if (t < toks)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const int j = j0 + g + 8 * r, cur = (p0 + t) >> a.page_shift;
+                        if (j >= vis) continue;
+                        uint32_t* to = sc + t * a.NB + j;
+                        float s = best[r];
+                        if (h0 > 0) s = fmaxf(s, __uint_as_float(*to));
+                        if (h0 + a.heads < a.G) {
+                            *to = __float_as_uint(s);
+                            continue;
+                        }
+                        // 0: out of sight; the largest: taken in any case
+                        *to = j > cur                                 ? 0u
+                              : j < a.first || j > cur - a.local ? 0xffffffffu
+                                                                 : rank_of(__fmul_rn(s, ks[r]));
+                    }
+            }
+        }
+        __syncthreads();
+    }
+    // ---- the picks: a warp for a token ----
+    for (int t = warp; t < toks; t += SEL_WARPS) {
+        const uint32_t* s = sc + t * a.NB;
+        const int m = ((p0 + t) >> a.page_shift) + 1;  // blocks that it sees
+        int32_t* out = a.idx + ((int64_t)(q0 + t0 + t) * a.kvh + h) * a.topk;
+        uint32_t least = 1;  // what is picked is at least this
+        int ties = m;        // of those equal to it, the first ones
+        if (m > a.topk) {
+            // the topk-th largest, bit by bit
+            least = 0;
+            int count = m;
+            for (int bit = 31; bit >= 0 && count != a.topk; bit--) {
+                const uint32_t to = least | (1u << bit);
+                int k = 0;
+                for (int j = lane; j < m; j += 32) k += s[j] >= to;
+                k = __reduce_add_sync(0xffffffffu, k);
+                if (k >= a.topk) {
+                    least = to;
+                    count = k;
+                }
+            }
+            int above = 0;
+            for (int j = lane; j < m; j += 32) above += s[j] > least;
+            ties = a.topk - __reduce_add_sync(0xffffffffu, above);
+        }
+        int at = 0;
+        const uint32_t below = (1u << lane) - 1u;
+        for (int j0 = 0; j0 < m; j0 += 32) {
+            const uint32_t v = j0 + lane < m ? s[j0 + lane] : 0;
+            const uint32_t eq = __ballot_sync(0xffffffffu, v == least && v != 0);
+            const bool take = v > least || (v == least && v != 0 && __popc(eq & below) < ties);
+            const uint32_t all = __ballot_sync(0xffffffffu, take);
+            if (take) out[at + __popc(all & below)] = j0 + lane;
+            at += __popc(all);
+            ties -= min(ties, __popc(eq));
+        }
+        for (int j = at + lane; j < a.topk; j += 32) out[j] = -1;
+    }
+}
+
+}  // namespace blocks
+}  // namespace ds41
+
+using namespace ds41;
+
+extern "C" int ds41_kv_block_keys(const void* k_cache, const float* k_scales, int fmt,
+                                  int64_t n_pages, int64_t page, int64_t kvh, int64_t hd,
+                                  const int32_t* page_table, int64_t max_pages,
+                                  const int32_t* lens, const int32_t* starts, int64_t B,
+                                  int64_t max_new, int8_t* codes, float* key_scales,
+                                  ds41_stream_t stream) {
+    const char* name = "ds41_kv_block_keys";
+    blocks::KeyArgs a{};
+    // (V is not read)
+    if (int rc = check_paged(name, k_cache, k_cache, k_scales, k_scales, fmt, n_pages, page, kvh,
+                             hd, &a.kv))
+        return rc;
+    DS41_REQUIRE(B >= 0 && B < 65536 && max_new >= 0 && max_new < int64_t(1) << 31 &&
+                     max_pages >= 0 && max_pages < int64_t(1) << 31,
+                 DS41_E_RANGE, "%s: B=%lld max_new=%lld max_pages=%lld", name, (long long)B,
+                 (long long)max_new, (long long)max_pages);
+    if (B == 0 || max_new == 0) return DS41_OK;
+    DS41_REQUIRE(codes && aligned16(codes) && key_scales && aligned_to(key_scales, 4) &&
+                     page_table && aligned_to(page_table, 4) && lens && aligned_to(lens, 4) &&
+                     aligned_to(starts, 4),
+                 DS41_E_ARG,
+                 "%s: codes (16-byte aligned), key_scales, page_table and lens must be non-null", name);
+    a.table = page_table;
+    a.lens = lens;
+    a.starts = starts;
+    a.max_pages = max_pages;
+    a.max_new = max_new;
+    a.codes = codes;
+    a.scales = key_scales;
+    if (int rc = status_word(&a.status)) return rc;
+    // pages of a sequence's new rows: one more when they begin inside a page
+    int64_t pages = (max_new + page - 1) / page + (starts ? 1 : 0);
+    if (pages > max_pages) pages = max_pages;
+    if (pages > 65535) pages = 65535;  // (a CTA goes on behind the grid)
+    if (pages < 1) pages = 1;
+    return launch_pdl(fmt == DS41_KV_E4M3 ? blocks::keys_kernel<true> : blocks::keys_kernel<false>,
+                      dim3((unsigned)((kvh + blocks::KEY_WARPS - 1) / blocks::KEY_WARPS),
+                           (unsigned)pages, (unsigned)B),
+                      dim3(blocks::KEY_WARPS * 32), 0, (cudaStream_t)stream, name, a);
+}
+
+extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
+                                 const int8_t* codes, const float* key_scales, int64_t n_pages,
+                                 int64_t page, int64_t kvh, int64_t hd, const int32_t* page_table,
+                                 int64_t max_pages, const int32_t* lens, const int32_t* cu_q,
+                                 int64_t B, int64_t Tq, int64_t max_q, int64_t max_len, int64_t nh,
+                                 int64_t topk, int64_t first, int64_t local, int32_t* idx,
+                                 ds41_stream_t stream) {
+    const char* name = "ds41_block_select";
+    if (int rc = check_heads(name, nh, kvh, hd, 1.0f, 0)) return rc;
+    if (int rc = check_cache_form(name, DS41_KV_BF16, kvh, hd)) return rc;
+    DS41_REQUIRE(page >= 16 && page <= 256 && (page & (page - 1)) == 0, DS41_E_ARG,
+                 "%s: page=%lld must be a power of two of 16 .. 256", name, (long long)page);
+    DS41_REQUIRE(n_pages >= 1 && n_pages < (int64_t(1) << 31) / kvh, DS41_E_ARG,
+                 "%s: n_pages=%lld kvh=%lld", name, (long long)n_pages, (long long)kvh);
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && max_q >= 0 && max_q < lim &&
+                     max_len >= 0 && max_len <= 32768 * page && max_pages >= 0 && max_pages < lim,
+                 DS41_E_RANGE,
+                 "%s: B=%lld Tq=%lld max_q=%lld max_len=%lld (at most 32768 pages) max_pages=%lld",
+                 name, (long long)B, (long long)Tq, (long long)max_q, (long long)max_len,
+                 (long long)max_pages);
+    DS41_REQUIRE(topk >= 1 && topk <= 1024 && first >= 0 && first <= topk && local >= 1 &&
+                     local <= topk - first,
+                 DS41_E_ARG, "%s: topk=%lld (1 .. 1024) first=%lld local=%lld (at least 1)", name,
+                 (long long)topk, (long long)first, (long long)local);
+    if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
+    DS41_REQUIRE(q && aligned16(q) && codes && aligned16(codes) && key_scales &&
+                     aligned_to(key_scales, 4) && page_table && aligned_to(page_table, 4) && lens &&
+                     aligned_to(lens, 4) && cu_q && aligned_to(cu_q, 4) && idx && aligned_to(idx, 4),
+                 DS41_E_ARG,
+                 "%s: q and codes must be non-null and 16-byte aligned, key_scales, page_table, "
+                 "lens, cu_q and idx non-null and aligned", name);
+    DS41_REQUIRE(good_strides(q_tok, q_head, hd), DS41_E_ARG,
+                 "%s: strides must be multiples of 8 and at least hd", name);
+    blocks::SelectArgs a{};
+    a.q = q;
+    a.q_tok = q_tok;
+    a.q_head = q_head;
+    a.codes = codes;
+    a.scales = key_scales;
+    a.table = page_table;
+    a.lens = lens;
+    a.cu_q = cu_q;
+    a.idx = idx;
+    a.Tq = Tq;
+    a.n_pages = n_pages;
+    a.max_pages = max_pages;
+    a.page = (int)page;
+    while ((1 << a.page_shift) < page) a.page_shift++;
+    a.kvh = (int)kvh;
+    a.hd = (int)hd;
+    a.G = (int)(nh / kvh);
+    a.max_q = (int)(max_q < Tq ? max_q : Tq);
+    a.max_len = (int)max_len;
+    a.topk = (int)topk;
+    a.first = (int)first;
+    a.local = (int)local;
+    if (int rc = status_word(&a.status)) return rc;
+    // Tokens of a CTA: 32, or what their scores leave room for (two CTAs an SM), or all;
+    // query heads at a time: a group, or 32 of it.
+    a.NB = (int)((max_len + page - 1) / page);
+    if (a.NB < 1) a.NB = 1;
+    a.heads = a.G >= 32 ? 32 : (a.G + 1) / 2 * 2;
+    const int HD = hd <= 64 ? 64 : 128;
+    auto bytes = [&](int tt) {
+        const int quads = (tt + 3) / 4;
+        return (size_t)quads * (a.heads / 2) * (HD / 16) * 256 + (size_t)quads * 16 * a.heads +
+               (size_t)tt * a.NB * 4;
+    };
+    a.TT = a.max_q < 32 ? a.max_q : 32;
+    while (a.TT > 1 && bytes(a.TT) > 100 * 1024) a.TT = a.TT > 4 ? (a.TT - 1) / 4 * 4 : a.TT - 1;
+    const size_t smem = bytes(a.TT);
+    auto kern = HD == 64 ? blocks::select_kernel<64> : blocks::select_kernel<128>;
+    if (int rc = HD == 64 ? allow_smem<blocks::select_kernel<64>>(224 * 1024, name)
+                          : allow_smem<blocks::select_kernel<128>>(224 * 1024, name))
+        return rc;
+    return launch_pdl(kern,
+                      dim3((unsigned)((a.max_q + a.TT - 1) / a.TT), (unsigned)B, (unsigned)kvh),
+                      dim3(blocks::SEL_WARPS * 32), smem, (cudaStream_t)stream, name, a);
+}

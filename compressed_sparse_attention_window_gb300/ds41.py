@@ -30,7 +30,7 @@ _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 ERRORS = {1: "DS41_E_ARG", 2: "DS41_E_RANGE", 3: "DS41_E_CUDA", 4: "DS41_E_INDEX",
-          5: "DS41_E_WORKSPACE", 6: "DS41_E_TIMEOUT"}
+          5: "DS41_E_WORKSPACE", 6: "DS41_E_TIMEOUT", 7: "DS41_E_PAGES"}
 
 #: Exported symbols of include/ds41.h and their (restype, argtypes).
 SIGNATURES = {
@@ -86,6 +86,32 @@ SIGNATURES = {
     "ds41_tree_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64, _I64,
                                           _P, _I64, _P, _P, _P, _I64] + [_I64] * 7
                            + [_F, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "ds41_kv_pages_take": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "ds41_kv_pages_free": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    "ds41_kv_pages_fork_workspace_bytes": (_SZ, [_I64] * 3),
+    "ds41_kv_pages_fork": (ctypes.c_int, [_P] * 4 + [ctypes.c_int] + [_I64] * 4
+                           + [_P, _P, _P, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _P, _P,
+                              _SZ, _P]),
+    "ds41_kv_pages_copy": (ctypes.c_int, [_P] * 4 + [ctypes.c_int] + [_I64] * 4
+                           + [_P, _P, _P, _P, _P, _I64, _P]),
+    "ds41_kv_pages_compact_workspace_bytes": (_SZ, [_I64]),
+    "ds41_kv_pages_compact": (ctypes.c_int, [_P] * 4 + [ctypes.c_int] + [_I64] * 4
+                              + [_P, _P, _P, _P, _I64, _P, _I64, _P, _P, _SZ, _P]),
+    "ds41_beam_select_workspace_bytes": (_SZ, [_I64] * 4),
+    "ds41_beam_select": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P] + [_I64] * 5
+                         + [_P, _P, _P, _P, _SZ, _P]),
+    "ds41_kv_block_keys": (ctypes.c_int, [_P, _P, ctypes.c_int] + [_I64] * 4
+                           + [_P, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "ds41_block_select": (ctypes.c_int, [_P, _I64, _I64, _P, _P] + [_I64] * 4
+                          + [_P, _I64, _P, _P] + [_I64] * 8 + [_P, _P]),
+    "ds41_block_attn_workspace_bytes": (_SZ, [_I64] * 6 + [ctypes.c_int]),
+    "ds41_block_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64,
+                                           _I64, _P, _I64, _P, _P, _P] + [_I64] * 7
+                            + [_F, _P, _P, _P, _P, _SZ, _P]),
+    "ds41_block_prompt_attn_workspace_bytes": (_SZ, [_I64] * 8),
+    "ds41_block_prompt_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
+                                                  _P, _P, _P] + [_I64] * 10
+                                   + [_F, _P, _P, _P, _P, _SZ, _P]),
     "ds41_sparse_attn_noalloc_capacity": (_SZ, []),
     "ds41_sparse_attn_sink_fwd_noalloc": (ctypes.c_int, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _F,
                                                          _P, _P, _I64, _I64, _I64, _P]),
@@ -776,9 +802,15 @@ def _dense():
         mod = importlib.util.module_from_spec(spec)
         loader.exec_module(mod)
         lib = load()
-        mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        mod.bind(_failed, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "ds41_kv_cache_write", "ds41_kv_cache_read", "ds41_prompt_attn_fwd",
-            "ds41_tree_attn_fwd", "ds41_tree_attn_workspace_bytes")), _failed)
+            "ds41_tree_attn_fwd", "ds41_tree_attn_workspace_bytes", "ds41_kv_pages_take",
+            "ds41_kv_pages_free", "ds41_kv_pages_fork", "ds41_kv_pages_fork_workspace_bytes",
+            "ds41_kv_pages_copy", "ds41_kv_pages_compact",
+            "ds41_kv_pages_compact_workspace_bytes", "ds41_beam_select",
+            "ds41_beam_select_workspace_bytes", "ds41_kv_block_keys", "ds41_block_select",
+            "ds41_block_attn_fwd", "ds41_block_attn_workspace_bytes",
+            "ds41_block_prompt_attn_fwd", "ds41_block_prompt_attn_workspace_bytes")))
         _binding = mod
     return _binding
 
@@ -824,3 +856,127 @@ def tree_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, len
     o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
     return (_binding or _dense()).tree_attn_fwd(q, cache, page_table, lens, cu_q, max_q, max_len,
                                                 scale, mask, sink, window, o, lse, ws)
+
+
+# ---------------------------------------------------------------------------
+# Pages: taken, forked, freed, copied, compacted
+# ---------------------------------------------------------------------------
+class BlockKeys(NamedTuple):
+    """One key a page and head, for block_select: int8 codes [n_pages, kvh, hd] and
+    their scales [n_pages, kvh] f32."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def make_block_keys(n_pages: int, kvh: int, hd: int, device="cuda") -> BlockKeys:
+    """Empty (zeroed) block keys for a cache of n_pages pages."""
+    return BlockKeys(torch.zeros(n_pages, kvh, hd, dtype=torch.int8, device=device),
+                     torch.zeros(n_pages, kvh, dtype=torch.float32, device=device))
+
+
+def kv_pages_take(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                  new_lens: torch.Tensor, page: int, ws: Optional[torch.Tensor] = None) -> None:
+    """ds41_kv_pages_take: free pages (lowest first; refs [n_pages] int32 counts who has
+    a page) into the table's rows for the rows lens .. new_lens - 1 of each sequence."""
+    (_binding or _dense()).kv_pages_take(refs, page_table, lens, new_lens, page, ws)
+
+
+def kv_pages_free(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                  page: int) -> None:
+    """ds41_kv_pages_free: the sequences end, refs of each of their pages less one."""
+    (_binding or _dense()).kv_pages_free(refs, page_table, lens, page)
+
+
+def kv_pages_fork(cache: KvCache, refs: torch.Tensor, page_table: torch.Tensor,
+                  lens: torch.Tensor, parents: torch.Tensor,
+                  table_out: Optional[torch.Tensor] = None,
+                  lens_out: Optional[torch.Tensor] = None, replace: bool = False,
+                  keys: Optional[BlockKeys] = None,
+                  ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """ds41_kv_pages_fork: children [n] that go on from the sequences parents[i] (-1:
+    from none); full pages are shared, the rows of a last page that is not full are
+    copied to a free one.  With ``replace`` the children are instead of the
+    parents (a beam search's step).  Returns the children's table [n, max_pages] and
+    lengths [n] (given or new)."""
+    return (_binding or _dense()).kv_pages_fork(cache, refs, page_table, lens, parents, table_out,
+                                                lens_out, replace, keys, ws)
+
+
+def kv_pages_copy(cache: KvCache, src: torch.Tensor, dst: torch.Tensor,
+                  rows: Optional[torch.Tensor] = None, keys: Optional[BlockKeys] = None) -> None:
+    """ds41_kv_pages_copy: the first rows[i] rows (None: all) of page src[i] to page
+    dst[i] (int32; -1: nothing)."""
+    (_binding or _dense()).kv_pages_copy(cache, src, dst, rows, keys)
+
+
+def kv_pages_compact(cache: KvCache, refs: torch.Tensor, page_table: torch.Tensor,
+                     lens: torch.Tensor, keys: Optional[BlockKeys] = None,
+                     live: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_kv_pages_compact: the pages in use move to the front of the cache, refs and
+    the table's entries with them; returns their number, [1] int32."""
+    return (_binding or _dense()).kv_pages_compact(cache, refs, page_table, lens, keys, live, ws)
+
+
+# ---------------------------------------------------------------------------
+# Beam search
+# ---------------------------------------------------------------------------
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: int,
+                ended: Optional[torch.Tensor] = None, end_token: int = 0,
+                out_scores: Optional[torch.Tensor] = None,
+                parents: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """ds41_beam_select: the best k of the W * V continuations of each search, logits
+    [B, W, V] (f32 or bf16), scores [B, W] f32 so far; a beam that has ``ended`` [B, W]
+    (bool) offers end_token alone, at its score.  Returns scores [B, k] f32, parents [B, k]
+    int32 (numbers b * W + w, for kv_pages_fork) and tokens [B, k] int32."""
+    return (_binding or _dense()).beam_select(logits, scores, k, ended, end_token, out_scores,
+                                              parents, tokens, ws)
+
+
+# ---------------------------------------------------------------------------
+# Attention over selected blocks of the dense cache
+# ---------------------------------------------------------------------------
+def kv_block_keys(cache: KvCache, keys: BlockKeys, page_table: torch.Tensor, lens: torch.Tensor,
+                  max_new: int, starts: Optional[torch.Tensor] = None) -> None:
+    """ds41_kv_block_keys: the block keys of the pages with the rows starts .. lens - 1 (at
+    most max_new of them; None: from 0), after kv_cache_write."""
+    (_binding or _dense()).kv_block_keys(cache, keys, page_table, lens, max_new, starts)
+
+
+def block_select(q: torch.Tensor, keys: BlockKeys, page: int, page_table: torch.Tensor,
+                 lens: torch.Tensor, cu_q: torch.Tensor, max_q: int, max_len: int, topk: int,
+                 first: int = 1, local: int = 2,
+                 idx: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_block_select: for each new token q [Tq, nh, hd] (packed by cu_q, the last of the
+    lens rows) and key/value head topk blocks (pages) of its sequence: the ``first`` ones,
+    the last ``local`` ones and those of the highest scores.  Returns idx [Tq, kvh, topk]
+    int32, ascending, -1 behind."""
+    return (_binding or _dense()).block_select(q, keys, page, page_table, lens, cu_q, max_q,
+                                               max_len, topk, first, local, idx)
+
+
+def block_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, lens: torch.Tensor,
+                   cu_q: torch.Tensor, max_q: int, idx: torch.Tensor, scale: float,
+                   sink: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None,
+                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_block_attn_fwd: new tokens q [Tq, nh, hd] (packed by cu_q, the last of each
+    sequence's lens rows) over the blocks idx [Tq, kvh, topk] of the paged cache (as
+    block_select gives them).  Returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if
+    given)."""
+    return (_binding or _dense()).block_attn_fwd(q, cache, page_table, lens, cu_q, max_q, idx,
+                                                 scale, sink, o, lse, ws)
+
+
+def block_prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                          cu_k: torch.Tensor, max_q: int, max_k: int, idx: torch.Tensor,
+                          block: int, scale: float, sink: Optional[torch.Tensor] = None,
+                          o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ds41_block_prompt_attn_fwd: packed prompts (q, k, v as prompt_attn_fwd) over the
+    blocks idx [Tq, kvh, topk] of ``block`` rows of their sequences.  Returns o [Tq, nh, hd]
+    (and fills lse [Tq, nh] f32 if given)."""
+    return (_binding or _dense()).block_prompt_attn_fwd(q, k, v, cu_q, cu_k, max_q, max_k, idx,
+                                                        block, scale, sink, o, lse, ws)

@@ -47,7 +47,8 @@ enum {
     DS41_E_CUDA = 3,      /* a CUDA call or launch failed */
     DS41_E_INDEX = 4,     /* a device-side index check tripped (device status) */
     DS41_E_WORKSPACE = 5, /* ws is NULL or smaller than *_workspace_bytes */
-    DS41_E_TIMEOUT = 6    /* a bounded device-side wait gave up (device status) */
+    DS41_E_TIMEOUT = 6,   /* a bounded device-side wait gave up (device status) */
+    DS41_E_PAGES = 7      /* a page was needed and none was free (device status) */
 };
 
 /* Message of the calling thread's last error ("" if none).  The pointer stays
@@ -645,6 +646,199 @@ int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const 
                        int64_t max_q, int64_t max_len, int64_t nh, int64_t kvh, int64_t hd,
                        float scale, int64_t window, const float* sink, ds41_bf16* o, float* lse,
                        void* ws, size_t ws_bytes, ds41_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Pages: taken, forked, freed, copied, compacted                             */
+/* ------------------------------------------------------------------------ */
+/* No counterpart on the pages.  Who has which page of the paged cache, kept on the
+ * device, so that a captured step can hand pages out:
+ *   refs [n_pages] int32: how many sequences have the page; 0: it is free
+ *   page_table [B, max_pages] int32, lens [B] int32: sequence b has len rows in the
+ *   pages of its first ceil(len / page) entries
+ * Full pages may be shared; a page that is not full belongs to one sequence, which
+ * writes on in it.  Free pages are handed out lowest first, to the sequences in their
+ * order, so equal calls give equal tables.  A length below 0 or past max_pages * page
+ * makes its sequence one without pages and raises DS41_E_INDEX, as an entry
+ * outside 0 .. n_pages - 1 does, which is skipped.  Block keys (ds41_kv_block_keys)
+ * go where their pages go: codes and key_scales, both NULL where there are none.
+ * Calls on one pool are ordered on one stream. */
+
+/* Pages for rows lens .. new_lens - 1 (new_lens <= lens: none): entries
+ * ceil(len / page) .. ceil(new_len / page) - 1 of the sequence's table row become free
+ * pages, whose refs become 1.  Where no page is left the entry becomes -1 and
+ * DS41_E_PAGES is raised.  Scratch: 4 * n_pages bytes. */
+int ds41_kv_pages_take(int32_t* refs, int64_t n_pages, int64_t page, int32_t* page_table,
+                       int64_t max_pages, const int32_t* lens, const int32_t* new_lens, int64_t B,
+                       void* ws, size_t ws_bytes, ds41_stream_t stream);
+
+/* The sequences end: refs of each of their pages less one.  A page that is free
+ * already stays so and raises DS41_E_INDEX. */
+int ds41_kv_pages_free(int32_t* refs, int64_t n_pages, int64_t page, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* lens, int64_t B, ds41_stream_t stream);
+
+/* Scratch bytes ds41_kv_pages_fork needs. */
+size_t ds41_kv_pages_fork_workspace_bytes(int64_t n_pages, int64_t B, int64_t n);
+
+/* n children go on from where their parents are: child i has the rows of sequence
+ * parents[i] (-1: none).  It shares the full pages, whose refs rise; the rows of a last
+ * page that is not full are copied to a free page.
+ *   parents [n] int32;  table_out [n, max_pages] int32 (not page_table) and lens_out [n]
+ *   int32 outputs, entries behind a child's pages -1
+ *   replace != 0: the children are instead of the parents (a beam search's step, with
+ *   the parents ds41_beam_select gives): the parents' references are dropped, the first child of a
+ *   parent takes its last page over, and pages that nobody has any more are free for
+ *   the copies of this call already; what they hold is then overwritten.
+ * A parent outside -1 .. B - 1 raises DS41_E_INDEX; its child has no rows.  Where no
+ * page is left the entry becomes -1 and DS41_E_PAGES is raised. */
+int ds41_kv_pages_fork(void* k_cache, void* v_cache, float* k_scales, float* v_scales, int fmt,
+                       int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, int8_t* codes,
+                       float* key_scales, int32_t* refs, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* lens, int64_t B, const int32_t* parents,
+                       int64_t n, int replace, int32_t* table_out, int32_t* lens_out, void* ws,
+                       size_t ws_bytes, ds41_stream_t stream);
+
+/* Rows 0 .. rows[i] - 1 (rows NULL: all) of page src[i] to page dst[i], K and V with their
+ * scales, and the page's block keys.  -1 in src or dst: nothing; a page outside
+ * -1 .. n_pages - 1 or rows outside 0 .. page raise DS41_E_INDEX.  The dst of one call
+ * are distinct, and none of them is among the src. */
+int ds41_kv_pages_copy(void* k_cache, void* v_cache, float* k_scales, float* v_scales, int fmt,
+                       int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, int8_t* codes,
+                       float* key_scales, const int32_t* src, const int32_t* dst,
+                       const int32_t* rows, int64_t n, ds41_stream_t stream);
+
+/* Scratch bytes ds41_kv_pages_compact needs. */
+size_t ds41_kv_pages_compact_workspace_bytes(int64_t n_pages);
+
+/* The pages that somebody has move to the front: live of them in all, the i-th free
+ * page below that number gets the i-th one in use from there on, with its refs; the
+ * table's entries follow (every sequence with pages has to be in it: one call, one
+ * pool).  Pages live .. n_pages - 1 are free then.
+ *   live [1] int32 output */
+int ds41_kv_pages_compact(void* k_cache, void* v_cache, float* k_scales, float* v_scales, int fmt,
+                          int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, int8_t* codes,
+                          float* key_scales, int32_t* refs, int32_t* page_table, int64_t max_pages,
+                          const int32_t* lens, int64_t B, int32_t* live, void* ws,
+                          size_t ws_bytes, ds41_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Beam search                                                                */
+/* ------------------------------------------------------------------------ */
+enum { DS41_LOGITS_F32 = 0, DS41_LOGITS_BF16 = 1 };
+
+/* Scratch bytes ds41_beam_select needs (0: sizes that it does not take). */
+size_t ds41_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t k);
+
+/* The best k continuations of each of B searches with W beams over a vocabulary of V.
+ * No counterpart on the pages.  Beam w with score s_w (a sum of log probabilities)
+ * offers token t at
+ *   s_w + x_wt - log sum_u e^{x_wu}
+ * and a search keeps the k best offers of its W * V, best first, ties to the lower w * V + t.
+ * The offers are compared in 64 bits, within a beam by x_wt alone.
+ *   logits [B, W, V] f32 or bf16 (fmt), elements between searches and between beams
+ *     b_stride, w_stride (>= V), the vocabulary dense; any alignment of its type
+ *   scores [B, W] f32: -inf = no beam
+ *   ended  nullable [B, W] uint8: a beam that has ended (not 0) offers end_token alone,
+ *     at s_w
+ *   out_scores [B, k] f32, parents [B, k] int32 (b * W + w, what ds41_kv_pages_fork
+ *     takes), tokens [B, k] int32 outputs; where fewer than k offers are above
+ *     -inf the rest is -inf, -1, -1
+ * A beam whose logits hold a NaN or +inf, or nothing but -inf, or whose score is NaN
+ * or +inf, offers nothing.  1 <= k <= 128, W <= 1024, 0 <= end_token < V with
+ * ended. */
+int ds41_beam_select(const void* logits, int fmt, int64_t b_stride, int64_t w_stride,
+                     const float* scores, const uint8_t* ended, int64_t end_token, int64_t B,
+                     int64_t W, int64_t V, int64_t k, float* out_scores, int32_t* parents,
+                     int32_t* tokens, void* ws, size_t ws_bytes, ds41_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention over selected blocks of the dense cache                          */
+/* ------------------------------------------------------------------------ */
+/* No counterpart on the pages, whose indexer picks single compressed rows: here a
+ * query of the dense attention reads only some blocks of a long cache (a block: a
+ * page), picked for each token and key/value head by a cheap score against one key a
+ * block.  ds41_kv_block_keys keeps those keys beside the cache, ds41_block_select picks,
+ * ds41_block_attn_fwd (few tokens, on the pages) and ds41_block_prompt_attn_fwd (packed
+ * prompts) attend.  Conventions as above for the dense attention. */
+
+/* The block keys of the pages in which rows starts .. len - 1 of the sequences lie
+ * (starts NULL: 0): per page and head, over its n rows below len,
+ *   m = (k_0 + k_1 + ... + k_{n-1}) / n   (f32, in the order of rows; e4m3 rows code * scale in f32)
+ *   s = max(amax, 127 * 2^-126) * f32(1 / 127),  codes rint(m / s)
+ * Where m is not finite the scale is NaN and the codes are 0.  Call it after
+ * ds41_kv_cache_write; the pages are summed anew, so rows that were written over
+ * (rejected drafts) leave nothing behind.
+ *   codes [n_pages, kvh, hd] int8 and key_scales [n_pages, kvh] f32, updated
+ *   max_new: no sequence has len - starts above it (one that has, or starts outside
+ *   0 .. len, is skipped and raises DS41_E_INDEX; so does a page outside the cache)
+ * Sequences that share a full page write the same values. */
+int ds41_kv_block_keys(const void* k_cache, const float* k_scales, int fmt, int64_t n_pages,
+                       int64_t page, int64_t kvh, int64_t hd, const int32_t* page_table,
+                       int64_t max_pages, const int32_t* lens, const int32_t* starts, int64_t B,
+                       int64_t max_new, int8_t* codes, float* key_scales, ds41_stream_t stream);
+
+/* The blocks of each token and key/value head.  Token i of sequence b (n = cu_q[b + 1] -
+ * cu_q[b] tokens, len = lens[b] rows, its own among them) stands at p = len - n + i and
+ * chooses among the blocks j <= p / page.  Its query rows are rounded as the block keys are
+ * (codes c_h, scale s_h); block j with codes k_j, scale t_j scores
+ *   max over the heads h of the group of  f32(f32(<c_h, k_j> s_h) t_j)
+ * (the product of the codes is exact; a head or block that is not finite does not
+ * count: -inf if none does).  The blocks j < first and j > p / page - local are taken
+ * whatever their score, then the highest scores, ties to the lower block, topk in all.
+ *   q [Tq, nh, hd] bf16 with strides q_tok, q_head
+ *   idx [Tq, kvh, topk] int32 output: ascending, -1 behind the last
+ *   1 <= topk <= 1024, first >= 0, local >= 1, first + local <= topk, max_len / page
+ *   at most 32768 (DS41_E_RANGE)
+ * A sequence that breaks its limits (len above max_len or max_pages * page, n above
+ * max_q or len) is skipped, its rows of idx left as they were; a page outside the
+ * cache counts as one that is not finite.  Both raise DS41_E_INDEX. */
+int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const int8_t* codes,
+                      const float* key_scales, int64_t n_pages, int64_t page, int64_t kvh,
+                      int64_t hd, const int32_t* page_table, int64_t max_pages,
+                      const int32_t* lens, const int32_t* cu_q, int64_t B, int64_t Tq,
+                      int64_t max_q, int64_t max_len, int64_t nh, int64_t topk, int64_t first,
+                      int64_t local, int32_t* idx, ds41_stream_t stream);
+
+/* Scratch bytes ds41_block_attn_fwd needs (0: sizes that it does not take). */
+size_t ds41_block_attn_workspace_bytes(int64_t Tq, int64_t topk, int64_t page, int64_t nh,
+                                       int64_t kvh, int64_t hd, int fmt);
+
+/* Attention of new tokens over their blocks of a paged cache: token i of sequence b
+ * at p (as above) sees the rows j <= p of the blocks in idx[t][h].  A list ends at
+ * its first -1; an entry that is not above the one before it, or above p / page, ends it
+ * too and raises DS41_E_INDEX.  Softmax, sink, o, lse, roundings and limits as
+ * ds41_tree_attn_fwd; a token that sees nothing has o = 0 and lse = sink (or -inf).  A
+ * page outside the cache raises DS41_E_INDEX and its rows are not seen.
+ *   idx [Tq, kvh, topk] int32, 1 <= topk <= 1024
+ * Scratch as ds41_tree_attn_fwd's.  B == 0, Tq == 0 or max_q == 0 is a no-op. */
+int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const void* k_cache,
+                        const void* v_cache, const float* k_scales, const float* v_scales,
+                        int fmt, int64_t n_pages, int64_t page, const int32_t* page_table,
+                        int64_t max_pages, const int32_t* lens, const int32_t* cu_q,
+                        const int32_t* idx, int64_t topk, int64_t B, int64_t Tq, int64_t max_q,
+                        int64_t nh, int64_t kvh, int64_t hd, float scale, const float* sink,
+                        ds41_bf16* o, float* lse, void* ws, size_t ws_bytes,
+                        ds41_stream_t stream);
+
+/* Scratch bytes ds41_block_prompt_attn_fwd needs (0: sizes that it does not take). */
+size_t ds41_block_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_k,
+                                              int64_t topk, int64_t block, int64_t nh,
+                                              int64_t kvh);
+
+/* The same over packed prompts, keys and values as ds41_prompt_attn_fwd takes them: query
+ * i of sequence b stands at p = i + lk - lq and sees the keys j <= p of the blocks in
+ * idx (block x: keys x * block .. of the sequence, block a power of two of 16 .. 256).
+ * Lists as ds41_block_attn_fwd's.  max_q, max_k: no sequence has more queries, keys (one
+ * that has, or lk < lq, is skipped and raises DS41_E_INDEX); max_k / block at most
+ * 32768.  A NaN or an infinity in a v row of a listed block can reach the queries that
+ * stand within 2 * 128 / (nh / kvh) tokens of one that lists it. */
+int ds41_block_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
+                               const ds41_bf16* k, int64_t k_tok, int64_t k_head,
+                               const ds41_bf16* v, int64_t v_tok, int64_t v_head,
+                               const int32_t* cu_q, const int32_t* cu_k, const int32_t* idx,
+                               int64_t topk, int64_t block, int64_t B, int64_t Tq, int64_t Tk,
+                               int64_t max_q, int64_t max_k, int64_t nh, int64_t kvh, int64_t hd,
+                               float scale, const float* sink, ds41_bf16* o, float* lse, void* ws,
+                               size_t ws_bytes, ds41_stream_t stream);
 
 #ifdef __cplusplus
 }
