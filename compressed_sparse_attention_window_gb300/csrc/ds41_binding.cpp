@@ -41,7 +41,6 @@ decltype(&ds41_beam_select_workspace_bytes) g_beam_ws;
 decltype(&ds41_kv_block_keys) g_keys;
 decltype(&ds41_block_select) g_select;
 decltype(&ds41_block_attn_fwd) g_blocks;
-decltype(&ds41_block_attn_workspace_bytes) g_blocks_ws;
 decltype(&ds41_block_prompt_attn_fwd) g_block_prompt;
 decltype(&ds41_block_prompt_attn_workspace_bytes) g_block_prompt_ws;
 PyObject* g_failed;  // failed(name, code) raises
@@ -565,11 +564,10 @@ const int32_t* lists(PyObject* o, at::Device dev, int64_t Tq, int64_t kvh, int64
     return (const int32_t*)data("idx", t, dev, {Tq, kvh, topk}, at::kInt);
 }
 
-// block_attn_fwd(q, cache, page_table, lens, cu_q, max_q, idx, scale, sink, o, lse, ws)
-// -> o
+// block_attn_fwd(q, cache, page_table, lens, cu_q, max_q, idx, scale, sink, o, lse) -> o
 PyObject* block_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    count(n_args, 12);
+    count(n_args, 11);
     const Tensor &q = tensor("q", a[0]), &table = tensor("page_table", a[2]),
                  &cu_q = tensor("cu_q", a[4]);
     const at::Device dev = here(q);
@@ -584,13 +582,11 @@ PyObject* block_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     auto sink = (const float*)data_or_null("sink", a[8], dev, {nh}, at::kFloat);
     auto lse = (float*)data_or_null("lse", a[10], dev, {Tq, nh}, at::kFloat);
     const Tensor o = output("o", a[9], dev, q.sizes());
-    const size_t need = g_blocks_ws(Tq, topk, c.page, nh, c.kvh, c.hd, c.fmt);
-    const Scratch ws(a[11], dev, need);
     const ds41_stream_t st = stream_of(dev);
     run("ds41_block_attn_fwd", [&] {
         return g_blocks(qh.p, qh.tok, qh.head, c.k, c.v, c.ks, c.vs, c.fmt, c.n_pages, c.page, pt,
                         table.size(1), lp, cq, idx, topk, B, Tq, max_q, nh, c.kvh, c.hd, scale,
-                        sink, (ds41_bf16*)o.data_ptr(), lse, ws.p, need, st);
+                        sink, (ds41_bf16*)o.data_ptr(), lse, st);
     });
     return given_or(a[9], o);
     END_HANDLE_TH_ERRORS
@@ -635,7 +631,7 @@ PyObject* block_prompt_attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args
 // not DS41_OK
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     HANDLE_TH_ERRORS
-    count(n_args, 21);
+    count(n_args, 20);
     int i = 0;
     auto next = [&](auto& f) { f = (std::remove_reference_t<decltype(f)>)integer(a[++i]); };
     next(g_write);
@@ -655,7 +651,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     next(g_keys);
     next(g_select);
     next(g_blocks);
-    next(g_blocks_ws);
     next(g_block_prompt);
     next(g_block_prompt_ws);
     Py_XSETREF(g_failed, Py_NewRef(a[0]));

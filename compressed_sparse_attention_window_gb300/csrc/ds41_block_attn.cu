@@ -1,13 +1,22 @@
-// ds41_block_attn.cu - attention over the blocks that were picked for each token and
-// key/value head: over the pages of a cache, and over packed prompts.
+// ds41_block_attn.cu - attention of few tokens over the blocks that were picked for each of
+// them and each key/value head, on the pages of a cache; and the same over packed prompts.
 //
-// Mathematics.  One pass with a running reference m and sum l per row:
-//   s_j = scale <q, k_j>,  p_j = e^(s_j - m),  l += p_j,  o += p_j v_j
-// over the rows j <= p of the listed blocks, the sink joining l at the end.
-#include "ds41_softmax_tc.cuh"
+// Mathematics.  As tree attention of few rows (ds41_tree_attn.cu, ds41_few.cuh): one pass
+// over the rows j <= p of the listed pages, with a lazily moved reference per row.  The
+// rows of a tile are the query heads of one token that share a key/value head (lists
+// differ from token to token), at most 16.
+//
+// What bounds it.  Each listed row is read once a token: HBM when there are tokens
+// enough.  A token's list is cut into as many runs as fill the GPU, at most eight, the
+// CTAs of a cluster, which join their results through each other's shared memory: no
+// second launch and no scratch.  The chain before the first row arrives (which sequence, its
+// length, the list, the table) is walked by all threads at once.
+#include "ds41_few.cuh"
 
 namespace ds41 {
 namespace ba {
+
+using few::GROUP;
 
 struct Args {
     const uint16_t* q;
@@ -26,6 +35,8 @@ struct Args {
     int64_t Tq, Tk, max_pages;
     int B, max_q, max_k, nh, kvh, hd, G, topk, block, block_shift;
     float scale;
+    int tiles;  // of 16 query heads of a group
+    int runs;   // of a list
     unsigned int* status;
 };
 
@@ -49,6 +60,249 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int b) {
 }
 
 constexpr int WARPS = 4;
+constexpr int NT = WARPS * 32;
+constexpr int MAX_LIST = 1024;
+constexpr int MAX_RUNS = 8;  // CTAs of a cluster
+
+template <int HD, bool E4M3>
+constexpr int tokens_bytes() {
+    using C = few::Cfg<HD, E4M3>;
+    return WARPS * (C::RING > 16 * C::P * 4 ? C::RING : 16 * C::P * 4);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
+                     : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];\n"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+template <int HD, bool E4M3>
+__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) {
+    pdl_wait();
+    using C = few::Cfg<HD, E4M3>;
+    constexpr int P = C::P;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int list[MAX_LIST];  // pages, -1: outside the cache
+    __shared__ int found[2][WARPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int run = blockIdx.x % a.runs, item = blockIdx.x / a.runs;
+    const int unit = item / a.tiles, h = unit % a.kvh, t = unit / a.kvh;
+    const int y0 = (item - unit * a.tiles) * 16, rows = min(16, a.G - y0);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < a.B; b += NT)
+            if (!load_seq<true>(a, b).ok) raise_status(a.status, DS41_E_INDEX);
+    // the last sequence that begins at or before the token
+    int b = -1;
+    for (int x = tid; x < a.B; x += NT)
+        if (a.cu_q[x] <= t) b = x;
+    const int32_t* src = a.idx + ((int64_t)t * a.kvh + h) * a.topk;
+    int mine[MAX_LIST / NT], before[MAX_LIST / NT];
+#pragma unroll
+    for (int k = 0; k < MAX_LIST / NT; k++) {
+        const int i = k * NT + tid;
+        mine[k] = i < a.topk ? src[i] : -1;
+        before[k] = i > 0 && i < a.topk ? src[i - 1] : -1;
+        if ((k + 1) * NT >= a.topk) break;
+    }
+    b = __reduce_max_sync(0xffffffffu, b);
+    if (lane == 0) found[0][warp] = b;
+    __syncthreads();
+    b = max(max(found[0][0], found[0][1]), max(found[0][2], found[0][3]));
+    if (b < 0) return;  // (the same for the whole cluster)
+    const Seq s = load_seq<true>(a, b);
+    if (!s.ok || t < s.q0 || t >= s.q0 + s.n) return;
+    const int p = s.len - s.n + (t - s.q0), cur = p >> a.block_shift;
+    // the list ends at the first entry that does not rise or lies past the token
+    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    int end = a.topk;
+#pragma unroll
+    for (int k = 0; k < MAX_LIST / NT; k++) {
+        const int i = k * NT + tid;
+        if (i < a.topk) {
+            if (mine[k] <= before[k] || mine[k] > cur) {
+                end = min(end, i);
+            } else {
+                const int pg = table[mine[k]];
+                list[i] = pg >= 0 && pg < a.kv.n_pages ? pg : -1;
+            }
+        }
+        if ((k + 1) * NT >= a.topk) break;
+    }
+    const int least = __reduce_min_sync(0xffffffffu, end);
+    if (lane == 0) found[1][warp] = least;
+    __syncthreads();
+    const int count = min(min(found[1][0], found[1][1]), min(found[1][2], found[1][3]));
+#pragma unroll
+    for (int k = 0; k < MAX_LIST / NT; k++) {
+        const int i = k * NT + tid;
+        if (i < a.topk && ((i == count && mine[k] != -1) || (i < count && list[i] < 0)))
+            raise_status(a.status, DS41_E_INDEX);
+        if ((k + 1) * NT >= a.topk) break;
+    }
+    // rows of the list: its last block may be the token's own
+    int keys = 0;
+    if (count > 0)
+        keys = (count - 1) * a.block + min(a.block, p - (src[count - 1] << a.block_shift) + 1);
+    const int groups = (keys + GROUP - 1) / GROUP;
+    const int first = (int)((int64_t)groups * run / a.runs);
+    const int own = (int)((int64_t)groups * (run + 1) / a.runs) - first;
+    const int n_mine = (own - warp + WARPS - 1) / WARPS;  // groups first + warp, + 4, ...
+
+    uint8_t* ring = smem + warp * C::RING;
+    const uint32_t ring_u = smem_u32(ring);
+    const few::Copier<HD, E4M3> copier(a.hd, lane);
+    const int per = a.block_shift - 4;  // log2 of a page's groups
+    unsigned bad = 0;                   // stages whose page does not exist
+    auto fetch = [&](int i) {
+        if (i < n_mine) {
+            const int st = i % C::STAGES, x = first + i * WARPS + warp;
+            const int pg = list[x >> per];
+            const bool ok = pg >= 0;
+            bad = ok ? bad & ~(1u << st) : bad | (1u << st);
+            const int64_t row = ok ? ((int64_t)pg * a.kvh + h) * a.block +
+                                         ((x & ((1 << per) - 1)) * GROUP)
+                                   : 0;
+            copier.copy(ring_u + st * C::STAGE, a.kv, row, ok ? min(GROUP, keys - x * GROUP) : 0,
+                        ok, lane);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; i++) fetch(i);
+
+    few::Rows<HD, E4M3> mem;
+    const uint16_t* q = a.q + t * a.q_tok + ((int64_t)h * a.G + y0) * a.q_head;
+#pragma unroll
+    for (int i = 0; i < 2; i++) mem.query(i, q + min(g + 8 * i, rows - 1) * a.q_head, a.hd, c);
+    mem.start(a.scale * tc::SM_LOG2E);
+    for (int i = 0; i < n_mine; i++) {
+        fetch(i + C::STAGES - 1);
+        cp_async_wait<C::STAGES - 1>();
+        __syncwarp();
+        const int st = i % C::STAGES, live = keys - (first + i * WARPS + warp) * GROUP;
+        const bool none = (bad >> st) & 1;
+        mem.group(
+            ring + st * C::STAGE, none || live < GROUP,
+            [&](int, int x) { return !none && x < live; }, g, c);
+        __syncwarp();  // the stage is read before it is filled again
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // ---- the warps' results joined into warp 0's place ----
+    float* out = reinterpret_cast<float*>(smem);
+    mem.put(out + warp * 16 * P, g, c);
+    __syncthreads();
+    constexpr int PER = NT / 16;  // threads of a row
+    const int r = tid / PER, part = tid % PER;
+    float mm = -INFINITY, f[WARPS], ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + r) * P + HD]);
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll
+    for (int w = 0; w < WARPS; w++) {
+        f[w] = exp2f(out[(w * 16 + r) * P + HD] - ref);
+        ll += f[w] * out[(w * 16 + r) * P + HD + 1];
+    }
+    __syncwarp();  // (a row's threads are in one warp)
+    for (int x = part * 4; x < a.hd; x += PER * 4) {
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) {
+            const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + r) * P + x]);
+            v.x += f[w] * ow.x;
+            v.y += f[w] * ow.y;
+            v.z += f[w] * ow.z;
+            v.w += f[w] * ow.w;
+        }
+        *reinterpret_cast<float4*>(&out[r * P + x]) = v;
+    }
+    if (part == 0) {
+        out[r * P + HD] = mm;
+        out[r * P + HD + 1] = ll;
+    }
+    // ---- the runs' results: each CTA writes its share of the pieces of four columns ----
+    if (a.runs > 1) cluster_sync();
+    else __syncthreads();
+    const int cols = a.hd / 4;
+    for (int x = run * NT + tid; x < rows * cols; x += a.runs * NT) {
+        const int y = x / cols, d = (x - y * cols) * 4;
+        float m = -INFINITY, l = 0.0f;
+        float4 v = make_float4(0, 0, 0, 0);
+        if (a.runs == 1) {
+            m = out[y * P + HD];
+            l = out[y * P + HD + 1];
+            v = *reinterpret_cast<const float4*>(&out[y * P + d]);
+        } else {
+            float2 ml[MAX_RUNS];
+            float4 o[MAX_RUNS];
+#pragma unroll
+            for (int k = 0; k < MAX_RUNS; k++)
+                if (k < a.runs) {
+                    ml[k] = ld_cluster2(cluster_addr(&out[y * P + HD], k));
+                    o[k] = ld_cluster4(cluster_addr(&out[y * P + d], k));
+                }
+#pragma unroll
+            for (int k = 0; k < MAX_RUNS; k++)
+                if (k < a.runs) m = fmaxf(m, ml[k].x);
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int k = 0; k < MAX_RUNS; k++)
+                if (k < a.runs) {
+                    const float e = exp2f(ml[k].x - base);
+                    l += e * ml[k].y;
+                    v.x += e * o[k].x;
+                    v.y += e * o[k].y;
+                    v.z += e * o[k].z;
+                    v.w += e * o[k].w;
+                }
+        }
+        const int head = h * a.G + y0 + y;
+        const tc::RowEnd fin = tc::row_end(m, l, a.sink ? a.sink[head] : -INFINITY);
+        const int64_t at = (int64_t)t * a.nh + head;
+        if (a.lse && d == 0) a.lse[at] = fin.lse;
+        *reinterpret_cast<uint2*>(a.o + at * a.hd + d) =
+            make_uint2(tc::bf16x2(v.x * fin.factor, v.y * fin.factor),
+                       tc::bf16x2(v.z * fin.factor, v.w * fin.factor));
+    }
+    pdl_trigger();
+    if (a.runs > 1) cluster_sync();  // nobody leaves while its results are read
+}
+
+template <int HD, bool E4M3>
+int launch_tokens(const Args& a, unsigned ctas, const char* name, cudaStream_t st) {
+    constexpr int smem = tokens_bytes<HD, E4M3>();
+    if (int rc = allow_smem<tokens_kernel<HD, E4M3>>(smem, name)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.runs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.runs > 1 ? 2 : 1;
+    if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, tokens_kernel<HD, E4M3>, a), name)) return rc;
+    return launch_check(name);
+}
 
 // A CTA for a token and a key/value head, a warp for every fourth of its query heads;
 // four elements of a row a lane.
@@ -160,11 +414,7 @@ int check_lists(const char* name, const int32_t* idx, int64_t topk, int64_t bloc
 }  // namespace ds41
 
 using namespace ds41;
-
-extern "C" size_t ds41_block_attn_workspace_bytes(int64_t Tq, int64_t topk, int64_t page,
-                                                  int64_t nh, int64_t kvh, int64_t hd, int fmt) {
-    return 0;
-}
+using few::GROUP;
 
 extern "C" int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
                                    const void* k_cache, const void* v_cache,
@@ -173,8 +423,8 @@ extern "C" int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_
                                    int64_t max_pages, const int32_t* lens, const int32_t* cu_q,
                                    const int32_t* idx, int64_t topk, int64_t B, int64_t Tq,
                                    int64_t max_q, int64_t nh, int64_t kvh, int64_t hd, float scale,
-                                   const float* sink, ds41_bf16* o, float* lse, void* ws,
-                                   size_t ws_bytes, ds41_stream_t stream) {
+                                   const float* sink, ds41_bf16* o, float* lse,
+                                   ds41_stream_t stream) {
     const char* name = "ds41_block_attn_fwd";
     if (int rc = check_heads(name, nh, kvh, hd, scale, 0)) return rc;
     ba::Args a{};
@@ -218,11 +468,24 @@ extern "C" int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_
     a.block = (int)page;
     a.block_shift = a.kv.page_shift;
     a.scale = scale;
+    a.tiles = (a.G + 15) / 16;
+    // runs of a list: as many as the GPU holds CTAs for (three an SM on an e4m3 cache, two on
+    // bf16), of two groups a warp at least
+    const int64_t items = Tq * kvh * a.tiles;
+    const int64_t fit = (int64_t)sm_count_once() * (fmt == DS41_KV_E4M3 ? 3 : 2) / items;
+    const int64_t most = topk * page / (2 * ba::WARPS * GROUP);
+    int64_t runs = fit < most ? fit : most;
+    a.runs = (int)(runs < 1 ? 1 : runs < ba::MAX_RUNS ? runs : ba::MAX_RUNS);
+    DS41_REQUIRE(items * a.runs < lim, DS41_E_RANGE, "%s: Tq=%lld kvh=%lld", name, (long long)Tq,
+                 (long long)kvh);
     if (int rc = status_word(&a.status)) return rc;
-    return launch_pdl(fmt == DS41_KV_E4M3 ? ba::block_attn_kernel<true, true>
-                                          : ba::block_attn_kernel<true, false>,
-                      dim3((unsigned)Tq, (unsigned)kvh), dim3(ba::WARPS * 32), 0,
-                      (cudaStream_t)stream, name, a);
+    const unsigned ctas = (unsigned)(items * a.runs);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (fmt == DS41_KV_E4M3)
+        return hd <= 64 ? ba::launch_tokens<64, true>(a, ctas, name, st)
+                        : ba::launch_tokens<128, true>(a, ctas, name, st);
+    return hd <= 64 ? ba::launch_tokens<64, false>(a, ctas, name, st)
+                    : ba::launch_tokens<128, false>(a, ctas, name, st);
 }
 
 extern "C" size_t ds41_block_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q,

@@ -104,10 +104,9 @@ SIGNATURES = {
                            + [_P, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
     "ds41_block_select": (ctypes.c_int, [_P, _I64, _I64, _P, _P] + [_I64] * 4
                           + [_P, _I64, _P, _P] + [_I64] * 8 + [_P, _P]),
-    "ds41_block_attn_workspace_bytes": (_SZ, [_I64] * 6 + [ctypes.c_int]),
     "ds41_block_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P, _P, ctypes.c_int, _I64,
                                            _I64, _P, _I64, _P, _P, _P] + [_I64] * 7
-                            + [_F, _P, _P, _P, _P, _SZ, _P]),
+                            + [_F, _P, _P, _P, _P]),
     "ds41_block_prompt_attn_workspace_bytes": (_SZ, [_I64] * 8),
     "ds41_block_prompt_attn_fwd": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
                                                   _P, _P, _P] + [_I64] * 10
@@ -809,7 +808,7 @@ def _dense():
             "ds41_kv_pages_copy", "ds41_kv_pages_compact",
             "ds41_kv_pages_compact_workspace_bytes", "ds41_beam_select",
             "ds41_beam_select_workspace_bytes", "ds41_kv_block_keys", "ds41_block_select",
-            "ds41_block_attn_fwd", "ds41_block_attn_workspace_bytes",
+            "ds41_block_attn_fwd",
             "ds41_block_prompt_attn_fwd", "ds41_block_prompt_attn_workspace_bytes")))
         _binding = mod
     return _binding
@@ -960,14 +959,13 @@ def block_select(q: torch.Tensor, keys: BlockKeys, page: int, page_table: torch.
 def block_attn_fwd(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, lens: torch.Tensor,
                    cu_q: torch.Tensor, max_q: int, idx: torch.Tensor, scale: float,
                    sink: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
-                   lse: Optional[torch.Tensor] = None,
-                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   lse: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ds41_block_attn_fwd: new tokens q [Tq, nh, hd] (packed by cu_q, the last of each
     sequence's lens rows) over the blocks idx [Tq, kvh, topk] of the paged cache (as
     block_select gives them).  Returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if
     given)."""
     return (_binding or _dense()).block_attn_fwd(q, cache, page_table, lens, cu_q, max_q, idx,
-                                                 scale, sink, o, lse, ws)
+                                                 scale, sink, o, lse)
 
 
 def block_prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,

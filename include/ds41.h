@@ -798,10 +798,6 @@ int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const i
                       int64_t max_q, int64_t max_len, int64_t nh, int64_t topk, int64_t first,
                       int64_t local, int32_t* idx, ds41_stream_t stream);
 
-/* Scratch bytes ds41_block_attn_fwd needs (0: sizes that it does not take). */
-size_t ds41_block_attn_workspace_bytes(int64_t Tq, int64_t topk, int64_t page, int64_t nh,
-                                       int64_t kvh, int64_t hd, int fmt);
-
 /* Attention of new tokens over their blocks of a paged cache: token i of sequence b
  * at p (as above) sees the rows j <= p of the blocks in idx[t][h].  A list ends at
  * its first -1; an entry that is not above the one before it, or above p / page, ends it
@@ -809,15 +805,14 @@ size_t ds41_block_attn_workspace_bytes(int64_t Tq, int64_t topk, int64_t page, i
  * ds41_tree_attn_fwd; a token that sees nothing has o = 0 and lse = sink (or -inf).  A
  * page outside the cache raises DS41_E_INDEX and its rows are not seen.
  *   idx [Tq, kvh, topk] int32, 1 <= topk <= 1024
- * Scratch as ds41_tree_attn_fwd's.  B == 0, Tq == 0 or max_q == 0 is a no-op. */
+ * Needs no scratch.  B == 0, Tq == 0 or max_q == 0 is a no-op. */
 int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const void* k_cache,
                         const void* v_cache, const float* k_scales, const float* v_scales,
                         int fmt, int64_t n_pages, int64_t page, const int32_t* page_table,
                         int64_t max_pages, const int32_t* lens, const int32_t* cu_q,
                         const int32_t* idx, int64_t topk, int64_t B, int64_t Tq, int64_t max_q,
                         int64_t nh, int64_t kvh, int64_t hd, float scale, const float* sink,
-                        ds41_bf16* o, float* lse, void* ws, size_t ws_bytes,
-                        ds41_stream_t stream);
+                        ds41_bf16* o, float* lse, ds41_stream_t stream);
 
 /* Scratch bytes ds41_block_prompt_attn_fwd needs (0: sizes that it does not take). */
 size_t ds41_block_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q, int64_t max_k,
