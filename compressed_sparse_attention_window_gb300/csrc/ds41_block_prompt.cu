@@ -1,0 +1,798 @@
+// ds41_block_prompt.cu - attention of packed prompts over the blocks that were picked for
+// each token and key/value head, on the 5th-generation tensor cores.
+//
+// Mathematics.  As ds41_prompt_attn.cu: S = q K^T, p_j = 2^(c S_j - c m), l += sum p_j, O += p V
+// with a lazily moved reference m per row, over the keys of the blocks that the row's token
+// lists, up to its own place.
+//
+// Rows and keys.  A tile of 128 rows is TT tokens times the G heads of a group, an item two
+// such tiles (2 TT neighbouring tokens), as there.  The keys of an item are the union of
+// its tokens' blocks, packed: 128 keys of an MMA block are as many picked blocks (units
+// of at most 128 keys) side by side, each copied by TMA to its own rows.  A row masks the units
+// that its token does not list.  A tile that no token of lists any of a block's units
+// skips it.
+//
+// Why the union.  A product of 128 rows and 64 keys costs 128 + 128 cycles a unit for the whole
+// tile; token by token (16 rows at most, on mma.sync) the unit's K and V would have to be
+// read from shared memory once for each token that lists it, 256 cycles each time: the
+// union is never twice as slow, and neighbouring tokens mostly list the same blocks.
+//
+// Two kernels.  plan_kernel makes the items' lists: a table of masks in shared memory (a word
+// for 32 tokens and each block), filled from the tokens' lists, is walked in order; what is
+// not empty becomes a slot of a record (128 keys: the units' first rows, and which tokens
+// list them).  block_prompt_kernel is the kernel of ds41_prompt_attn.cu with the records in place of
+// a range of keys.
+#include "ds41_prompt.cuh"
+
+namespace ds41 {
+namespace bp {
+
+using namespace pa;
+
+// An item: one head group of one pair of tiles of one sequence.
+struct Item {
+    int grp;             // head group, -1: nothing
+    int q0, n, k0, len;  // its sequence's queries and keys
+    int t0;              // first token of tile 0
+    int count;           // records
+    int last[2];         // the last record that tile t takes part in, -1: none
+    int tail, tail_end;  // rows of the last record's V behind the last key
+    int id;
+};
+static_assert(sizeof(Item) == 48, "three 16-byte pieces");
+
+constexpr uint32_t ROW = 0x3fffffffu;  // a unit's word: its first row, and which tiles list it
+constexpr int PLAN = 256;              // threads of plan_kernel
+constexpr int TABLE = 8192;            // words of its table
+
+struct Params {
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    const int32_t* idx;
+    const float* sink;
+    uint16_t* o;
+    float* lse;
+    int64_t Tq, Tk;
+    int B, max_q, max_k, nh, kvh, hd, topk;
+    int G, TT, n_groups, subs;
+    int shift, unit_shift;  // log2 of a block's keys, of a unit's
+    int words;              // of a unit's mask: 2 TT tokens
+    int rec_words, max_rec;
+    float c;
+    Item* items;
+    uint32_t* recs;         // [item][max_rec][rec_words]: the units' words, their masks
+    unsigned int* status;
+};
+
+// exclusive prefix of v over the CTA, and the sum.  sh: PLAN / 32 ints
+__device__ __forceinline__ int prefix(int v, int* sh, int& sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    int before = 0;
+    sum = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN / 32; w++) {
+        if (w < warp) before += sh[w];
+        sum += sh[w];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+__global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ uint32_t table[TABLE];
+    __shared__ int end[256], sh[PLAN / 32];
+    __shared__ Item it;
+    const int tid = threadIdx.x, id = blockIdx.x;
+    const int w = id / p.n_groups, grp = id - w * p.n_groups, h = grp / p.subs;
+    if (tid == 0) {
+        it = Item{};
+        it.grp = -1;
+        it.last[0] = it.last[1] = -1;
+        it.id = id;
+    }
+    __syncthreads();
+    // the sequence (its pairs of tiles in falling order, as its longest lists are at the end)
+    for (int b0 = 0, base = 0; b0 < p.B; b0 += PLAN) {
+        const int b = b0 + tid;
+        int q0 = 0, n = 0, k0 = 0, len = 0;
+        if (b < p.B) {
+            q0 = p.cu_q[b];
+            k0 = p.cu_k[b];
+            const int64_t ln = (int64_t)p.cu_q[b + 1] - q0, lk = (int64_t)p.cu_k[b + 1] - k0;
+            if (q0 >= 0 && ln >= 0 && ln <= p.max_q && q0 + ln <= p.Tq && k0 >= 0 && lk >= ln &&
+                lk <= p.max_k && k0 + lk <= p.Tk) {
+                n = (int)ln;
+                len = (int)lk;
+            } else if (id == 0) {
+                raise_status(p.status, DS41_E_INDEX);
+            }
+        }
+        const int tiles = (n + 2 * p.TT - 1) / (2 * p.TT);
+        int sum;
+        const int at = base + prefix(tiles, sh, sum);
+        if (w >= at && w < at + tiles) {
+            it.grp = grp;
+            it.q0 = q0;
+            it.n = n;
+            it.k0 = k0;
+            it.len = len;
+            it.t0 = (at + tiles - 1 - w) * 2 * p.TT;
+        }
+        base += sum;
+        if (w < base && id != 0) break;
+    }
+    if (tid < 256) end[tid] = p.topk;
+    __syncthreads();
+    if (it.grp < 0) {
+        if (tid == 0) p.items[id].grp = -1;
+        return;
+    }
+    const int toks = min(2 * p.TT, it.n - it.t0), p0 = it.len - it.n + it.t0;
+    const int32_t* lists = p.idx + ((int64_t)(it.q0 + it.t0) * p.kvh + h) * p.topk;
+    auto entry = [&](int tok, int i) { return lists[(int64_t)tok * p.kvh * p.topk + i]; };
+    // a list ends at the first entry that does not rise or lies past its token
+    for (int e = tid; e < toks * p.topk; e += PLAN) {
+        const int tok = e / p.topk, i = e - tok * p.topk;
+        const int x = entry(tok, i), before = i > 0 ? entry(tok, i - 1) : -1;
+        if (x <= before || x > (p0 + tok) >> p.shift) atomicMin(&end[tok], i);
+    }
+    __syncthreads();
+    const int blocks = ((p0 + toks - 1) >> p.shift) + 1, W = p.words;
+    const int range = TABLE / W;
+    const int per = 1 << (p.shift - p.unit_shift), nu = KB >> p.unit_shift;
+    uint32_t* recs = p.recs + (int64_t)id * p.max_rec * p.rec_words;
+    int found = 0;
+    for (int r0 = 0; r0 < blocks; r0 += range) {
+        const int size = min(range, blocks - r0);
+        for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
+        __syncthreads();
+        for (int e = tid; e < toks * p.topk; e += PLAN) {
+            const int tok = e / p.topk, i = e - tok * p.topk;
+            if (i > end[tok]) continue;
+            const int x = entry(tok, i);
+            if (i == end[tok]) {
+                if (x != -1 && r0 == 0) raise_status(p.status, DS41_E_INDEX);
+            } else if (x >= r0 && x < r0 + size) {
+                atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
+            }
+        }
+        __syncthreads();
+        for (int x0 = 0; x0 < size; x0 += PLAN) {
+            const int x = x0 + tid;
+            uint32_t tiles = 0;
+            if (x < size)
+                for (int y = 0; y < W; y++) {
+                    const uint32_t m = table[x * W + y], low = low_bits(p.TT - 32 * y);
+                    tiles |= (m & low ? 1u : 0u) | (m & ~low ? 2u : 0u);
+                }
+            int sum;
+            const int at = found + prefix(tiles != 0, sh, sum);
+            found += sum;
+            if (!tiles) continue;
+            for (int k = 0; k < per; k++) {
+                const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
+                if (row >= it.len) break;  // (behind the last key: only the last block's)
+                const int u = at * per + k, rec = u / nu, slot = u - rec * nu;
+                uint32_t* to = recs + (int64_t)rec * p.rec_words;
+                to[slot] = (uint32_t)row | tiles << 30;
+                for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
+                if (tiles & 1) atomicMax(&it.last[0], rec);
+                if (tiles & 2) atomicMax(&it.last[1], rec);
+                atomicMax(&it.count, u + 1);
+                if (row + (1 << p.unit_shift) > it.len) {
+                    it.tail = (slot << p.unit_shift) + it.len - row;
+                    it.tail_end = (slot + 1) << p.unit_shift;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // slots behind the last unit
+    const int units = it.count, recs_n = (units + nu - 1) / nu;
+    for (int u = units + tid; u < recs_n * nu; u += PLAN) {
+        uint32_t* to = recs + (int64_t)(u / nu) * p.rec_words;
+        to[u % nu] = ROW;
+        for (int y = 0; y < W; y++) to[nu + (u % nu) * W + y] = 0;
+    }
+    __syncthreads();
+    if (tid == 0) it.count = recs_n;
+    __syncthreads();
+    if (tid < 3)
+        reinterpret_cast<int4*>(p.items + id)[tid] = reinterpret_cast<const int4*>(&it)[tid];
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    block_prompt_kernel(const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const Params p) {
+    pdl_wait();
+    using C = Cfg<D>;
+    constexpr int ITEMS = 4;  // items looked up ahead
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BAR_OFF);
+    uint64_t* b_q = bars;                      // an item's queries landed [QB]
+    uint64_t* b_qe = b_q + C::QB;              // and have been used [QB]
+    uint64_t* b_full = b_qe + C::QB;           // stage landed
+    uint64_t* b_empty = b_full + C::STAGES;    // stage read
+    uint64_t* b_s = b_empty + C::STAGES;       // S_t in tensor memory [2]
+    uint64_t* b_p = b_s + 2;                   // P_t in tensor memory, O_t rescaled [2]
+    uint64_t* b_o = b_p + 2;                   // O_t complete [2]
+    uint64_t* b_oe = b_o + 2;                  // O_t read [2]
+    uint64_t* b_tail = b_oe + 2;               // the V block that ends behind the last key landed
+    uint64_t* b_fix = b_tail + 1;              // its rows behind the last key are zero
+    uint64_t* b_item = b_fix + 1;              // an item is known [ITEMS]
+    uint64_t* b_iteme = b_item + ITEMS;        // and every role is through with it
+    uint64_t* b_clc = b_iteme + ITEMS;         // the answer to a request for another item
+    uint64_t* b_end = b_clc + 1;               // every product is complete
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_end + 1);
+    volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    Item* items = reinterpret_cast<Item*>(tmem_slot + 2);
+    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <=
+                      624,
+                  "barrier area");
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < C::QB; i++) {
+            mbar_init(&b_q[i], 1);
+            mbar_init(&b_qe[i], 1);
+        }
+        for (int i = 0; i < C::STAGES; i++) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
+        }
+        for (int t = 0; t < 2; t++) {
+            mbar_init(&b_s[t], 1);
+            mbar_init(&b_p[t], 4);
+            mbar_init(&b_o[t], 1);
+            mbar_init(&b_oe[t], 4);
+        }
+        mbar_init(b_tail, 1);
+        mbar_init(b_fix, 1);
+        for (int i = 0; i < ITEMS; i++) {
+            mbar_init(&b_item[i], 1);
+            mbar_init(&b_iteme[i], 11);
+        }
+        mbar_init(b_clc, 1);
+        mbar_init(b_end, 1);
+        *abort_f = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) {
+        asm volatile(
+            "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                smem_u32(tmem_slot))
+            : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    // rows of the query tiles that no copy fills
+    const int used = p.TT * p.G;
+    if (used < ROWS) {
+        const int per = (ROWS - used) * 8;  // 16-byte pieces of one 64-column block
+        for (int x = threadIdx.x; x < C::QB * 2 * C::NB * per; x += THREADS)
+            *reinterpret_cast<uint4*>(sm + C::Q_OFF + (x / per) * C::BLK + used * 128 +
+                                      (x % per) * 16) = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    const int nu = KB >> p.unit_shift;
+    // the next item of this warp's walk; false at the end (or when a wait gave up)
+    auto next_item = [&](int k, Item& it) {
+        if (!warp_wait(&b_item[k % ITEMS], (k / ITEMS) & 1, abort_f, p.status)) return false;
+        const Item& x = items[k % ITEMS];
+        it.grp = uniform(x.grp);
+        it.q0 = uniform(x.q0);
+        it.n = uniform(x.n);
+        it.k0 = uniform(x.k0);
+        it.len = uniform(x.len);
+        it.t0 = uniform(x.t0);
+        it.count = uniform(x.count);
+        it.last[0] = uniform(x.last[0]);
+        it.last[1] = uniform(x.last[1]);
+        it.tail = uniform(x.tail);
+        it.tail_end = uniform(x.tail_end);
+        it.id = uniform(x.id);
+        return it.grp >= 0;
+    };
+    auto done_item = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_iteme[k % ITEMS]);
+    };
+    auto records = [&](const Item& it) { return p.recs + (int64_t)it.id * p.max_rec * p.rec_words; };
+    // record j's units, one a lane (none behind the last)
+    auto units = [&](const uint32_t* recs, const Item& it, int j) {
+        return j < it.count && lane < nu ? recs[(int64_t)j * p.rec_words + lane] : ROW;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (warp == 0) {
+            uint32_t n = 0, nq = 0;
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                if (it.count > 0) {
+                    const int head0 = it.grp * p.G, kvh = it.grp / p.subs, qb = nq % C::QB;
+                    const uint32_t* recs = records(it);
+                    uint32_t unit = units(recs, it, 0);
+                    if (nq >= C::QB)
+                        ok = warp_wait(&b_qe[qb], ((nq / C::QB) - 1) & 1, abort_f, p.status);
+                    if (ok) {
+                        if (lane == 0) {
+                            uint32_t q_tiles = 0;
+#pragma unroll
+                            for (int t = 0; t < 2; t++) q_tiles += it.last[t] >= 0;
+                            mbar_arrive_expect_tx(&b_q[qb], q_tiles * C::NB * (uint32_t)used * 128);
+#pragma unroll
+                            for (int t = 0; t < 2; t++)
+                                if (it.last[t] >= 0)
+                                    for (int x = 0; x < C::NB; x++)
+                                        tma_load_3d(sbase + C::Q_OFF + (2 * qb + t) * C::TILE +
+                                                        x * C::BLK,
+                                                    &map_q, 64 * x, head0,
+                                                    it.q0 + it.t0 + t * p.TT, &b_q[qb]);
+                        }
+                        nq++;
+                    }
+                    // lane l copies unit l % nu, columns 64 (l / nu) ..
+                    const int slot = lane % nu, x = lane / nu;
+                    for (int j = 0; j < it.count && ok; j++) {
+                        const uint32_t word = __shfl_sync(0xffffffffu, unit, slot) & ROW;
+                        unit = units(recs, it, j + 1);
+                        // (behind the last unit: rows that do not exist, read as zeros)
+                        const int row = word == ROW ? (int)p.Tk : it.k0 + (int)word;
+                        for (int kv = 0; kv < 2 && ok; kv++) {
+                            const uint32_t st = n % C::STAGES, use = n / C::STAGES;
+                            if (use > 0)
+                                ok = warp_wait(&b_empty[st], (use - 1) & 1, abort_f, p.status);
+                            if (!ok) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&b_full[st], C::TILE);
+                            __syncwarp();
+                            if (x < C::NB)
+                                tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
+                                                ((slot << p.unit_shift) * 128),
+                                            kv ? &map_v : &map_k, 64 * x, kvh, row, &b_full[st]);
+                            n++;
+                        }
+                    }
+                }
+                done_item(k);
+            }
+            // everything that was started lands before the CTA ends
+            __syncwarp();
+            if (lane == 0) {
+                for (uint32_t x = nq > C::QB ? nq - C::QB : 0; x < nq; x++)
+                    drain_bar(&b_q[x % C::QB], (x / C::QB) & 1, p.status);
+                for (uint32_t x = n > C::STAGES ? n - C::STAGES : 0; x < n; x++)
+                    drain_bar(&b_full[x % C::STAGES], (x / C::STAGES) & 1, p.status);
+            }
+        } else if (warp == 1) {
+            constexpr uint32_t IDESC_S = idesc_bf16(128, KB, 0, 0);
+            constexpr uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
+            const uint32_t kd = desc_lo(sbase + C::KV_OFF, 16);
+            const uint32_t vd = desc_lo(sbase + C::KV_OFF, C::BLK);
+            uint32_t ring0 = 0, nq = 0, tails = 0, done_p[2] = {0, 0}, outs[2] = {0, 0};
+            auto wait_stage = [&](uint32_t n) {
+                const bool r =
+                    warp_wait(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
+                tc_fence_after();
+                return r;
+            };
+            auto stage_off = [&](uint32_t n) { return ((n % C::STAGES) * C::TILE) >> 4; };
+            // which tiles take part in a record
+            auto tiles_of = [&](uint32_t unit) {
+                return (uint32_t)uniform((int)__reduce_or_sync(0xffffffffu, unit) >> 30) & 3u;
+            };
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                if (it.count > 0) {
+                    const uint32_t* recs = records(it);
+                    const int qb = nq % C::QB;
+                    const uint32_t qd = desc_lo(sbase + C::Q_OFF + 2 * qb * C::TILE, 16);
+                    uint32_t now = tiles_of(units(recs, it, 0)), ahead = units(recs, it, 1);
+                    bool begun[2] = {false, false};
+                    ok = warp_wait(&b_q[qb], (nq / C::QB) & 1, abort_f, p.status) &&
+                         wait_stage(ring0);
+                    nq++;
+                    if (ok && elect_one()) {
+#pragma unroll
+                        for (int t = 0; t < 2; t++)
+                            if ((now >> t) & 1) {
+                                mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                                       qd + ((t * C::TILE) >> 4),
+                                                       kd + stage_off(ring0));
+                                tc_commit(&b_s[t]);
+                            }
+                        tc_commit(&b_empty[ring0 % C::STAGES]);
+                        if (it.count == 1) tc_commit(&b_qe[qb]);
+                    }
+                    __syncwarp();
+                    for (int j = 0; j < it.count && ok; j++) {
+                        const uint32_t next = tiles_of(ahead);
+                        ahead = units(recs, it, j + 2);
+                        const uint32_t nv = ring0 + 2 * (uint32_t)j + 1, nk = nv + 1;
+                        const bool more = j + 1 < it.count;
+                        // (both before the waits for the weights: nothing stands between
+                        // their arrival and the products)
+                        ok = wait_stage(nv) && (!more || wait_stage(nk));
+                        if (ok && !more && it.tail > 0) {
+                            if (lane == 0) mbar_arrive(b_tail);
+                            ok = warp_wait(b_fix, tails & 1, abort_f, p.status);
+                            tails++;
+                            tc_fence_after();
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; t++) {
+                            const bool mine = (now >> t) & 1, then = more && ((next >> t) & 1);
+                            if (ok && mine) {
+                                // the last item's outputs have been read
+                                if (!begun[t] && outs[t] > 0)
+                                    ok = warp_wait(&b_oe[t], (outs[t] - 1) & 1, abort_f, p.status);
+                                ok = ok && warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
+                                done_p[t]++;
+                                tc_fence_after();
+                            }
+                            if (ok && elect_one()) {
+                                if (mine) {
+                                    mma_output<D, IDESC_O>(tmem + TM_O + 128 * t,
+                                                           tmem + TM_S + 128 * t,
+                                                           vd + stage_off(nv), begun[t]);
+                                    if (j == it.last[t]) tc_commit(&b_o[t]);
+                                }
+                                if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
+                                if (then) {
+                                    mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
+                                                           qd + ((t * C::TILE) >> 4),
+                                                           kd + stage_off(nk));
+                                    tc_commit(&b_s[t]);
+                                }
+                            }
+                            __syncwarp();
+                            begun[t] |= mine;
+                            if (mine && j == it.last[t]) outs[t]++;
+                        }
+                        if (ok && more && elect_one()) {
+                            tc_commit(&b_empty[nk % C::STAGES]);
+                            if (j + 2 == it.count) tc_commit(&b_qe[qb]);  // the last scores
+                        }
+                        __syncwarp();
+                        now = next;
+                    }
+                    ring0 += 2 * (uint32_t)it.count;
+                }
+                done_item(k);
+            }
+        } else if (warp == 2) {
+            // zero the V rows behind the last key
+            uint32_t ring0 = 0, tails = 0;
+            bool ok = true;
+            Item it;
+            for (int k = 0; ok && next_item(k, it); k++) {
+                ring0 += 2 * (uint32_t)it.count;
+                if (it.count > 0 && it.tail > 0) {
+                    ok = warp_wait(b_tail, tails & 1, abort_f, p.status);
+                    tails++;
+                    if (!ok) break;
+                    uint8_t* v = sm + C::KV_OFF + ((ring0 - 1) % C::STAGES) * C::TILE;
+                    for (int x = lane; x < (it.tail_end - it.tail) * C::NB * 8; x += 32) {
+                        const int r = it.tail + x / (C::NB * 8), piece = x % (C::NB * 8);
+                        *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
+                                                  (piece % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_fix);
+                }
+                done_item(k);
+            }
+        } else {
+            // the items: this CTA's own, then those that it takes over
+            const uint32_t response = sbase + C::BAR_OFF + 640 - 16;
+            int id = blockIdx.x;
+            bool ok = true;
+            for (int k = 0, asked = 0; ok && id >= 0;) {
+                if (lane == 0) take_over(response, b_clc);
+                int4 piece = make_int4(-1, 0, 0, 0);
+                if (lane < 3) piece = reinterpret_cast<const int4*>(p.items + id)[lane];
+                if (uniform(piece.x) >= 0) {  // (grp, of lane 0's piece)
+                    if (k >= ITEMS)
+                        ok = warp_wait(&b_iteme[k % ITEMS], ((k / ITEMS) - 1) & 1, abort_f,
+                                       p.status);
+                    if (ok && lane < 3) {
+                        int* to = reinterpret_cast<int*>(&items[k % ITEMS]) + 4 * lane;
+                        to[0] = piece.x;
+                        to[1] = piece.y;
+                        to[2] = piece.z;
+                        to[3] = piece.w;
+                    }
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(&b_item[k % ITEMS]);
+                    k++;
+                }
+                // (an answer that is on its way is waited for in any case)
+                const bool here = __all_sync(
+                    0xffffffffu, drain_bar(b_clc, asked & 1, p.status));
+                asked++;
+                id = here ? taken_over(response) : -1;
+                __syncwarp();
+                if (id < 0 || !ok) {
+                    if (ok && k >= ITEMS)
+                        ok = warp_wait(&b_iteme[k % ITEMS], ((k / ITEMS) - 1) & 1, abort_f,
+                                       p.status);
+                    if (lane == 0) {
+                        items[k % ITEMS].grp = -1;
+                        mbar_arrive(&b_item[k % ITEMS]);
+                    }
+                    break;
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        const int t = (warp - 4) >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tm_s = tmem + lanes + TM_S + 128 * t, tm_o = tmem + lanes + TM_O + 128 * t;
+        const int row = 32 * (warp & 3) + lane;
+        const int tok = row / p.G, gh = row - tok * p.G;
+        const float c = p.c;
+        uint32_t ph = 0, outs = 0;
+        bool ok = true;
+        Item it;
+        for (int k = 0; ok && next_item(k, it); k++) {
+            const int count = max(0, min(p.TT, it.n - it.t0 - t * p.TT));  // tokens of the tile
+            const bool live = tok < count;
+            const bool idle = !__any_sync(0xffffffffu, live);
+            const int last = t ? it.last[1] : it.last[0];
+            const int pos = it.len - it.n + it.t0 + t * p.TT + tok;  // the last key it sees
+            const int bit = live ? t * p.TT + tok : 0;
+            const uint32_t* recs = records(it);
+            // The row's view of record j: the keys of the units that its token lists, up to its
+            // place; false if none of the tile's tokens lists any.
+            auto look = [&](int j, uint32_t (&vis)[4]) {
+                const uint32_t* rec = recs + (int64_t)j * p.rec_words;
+                const uint32_t* mask = rec + nu + (bit >> 5);
+                uint32_t tiles = 0;
+                auto keys = [&](int unit, int off) {  // of a unit from key off on
+                    const uint32_t word = rec[unit];
+                    tiles |= word >> 30;
+                    const bool mine = live && ((mask[unit * p.words] >> (bit & 31)) & 1);
+                    return low_bits(mine ? pos - (int)(word & ROW) - off + 1 : 0);
+                };
+                if (p.unit_shift >= 5) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int unit = (32 * i) >> p.unit_shift;
+                        vis[i] = keys(unit, 32 * i - (unit << p.unit_shift));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        vis[i] = (keys(2 * i, 0) & 0xffffu) | keys(2 * i + 1, 0) << 16;
+                }
+                return ((tiles >> t) & 1) != 0;
+            };
+            RowState st;
+            bool first = true;
+            for (int j = 0; j <= last; j++) {
+                uint32_t vis[4];
+                if (!look(j, vis)) continue;
+                ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
+                if (!ok) break;
+                ph++;
+                tc_fence_after();
+                const bool whole = (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu;
+                if (idle) {
+                    // none of the warp's rows exists: whatever its scores hold weighs no one
+                } else if (__all_sync(0xffffffffu, whole)) {
+                    softmax_block<D, false>(tm_s, tm_o, !first, vis, c, live, st);
+                } else {
+                    softmax_block<D, true>(tm_s, tm_o, !first, vis, c, live, st);
+                }
+                first = false;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_p[t]);
+            }
+            if (!ok) break;
+            // the sink is one more term of the denominator
+            const int head = it.grp * p.G + gh;
+            const RowEnd end = row_end(st.reference(c), st.l,
+                                       live && p.sink ? p.sink[head] : -INFINITY);
+            const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
+            if (live && p.lse) p.lse[at] = end.lse;
+            if (count > 0) {
+                const bool any = last >= 0;
+                if (any) {
+                    ok = warp_wait(&b_o[t], outs & 1, abort_f, p.status);
+                    if (!ok) break;
+                    outs++;
+                    tc_fence_after();
+                }
+                // (offsets from the tile's first row: at most 128 tokens of 4096 heads)
+                uint16_t* dst = p.o + (int64_t)(it.q0 + it.t0 + t * p.TT) * p.nh * p.hd;
+                store_rows<D>(tm_o, any, end.factor, dst,
+                              live ? (tok * p.nh + head) * p.hd : -1, p.hd, [&] {
+                                  tc_fence_before();
+                                  __syncwarp();
+                                  if (any && lane == 0) mbar_arrive(&b_oe[t]);
+                              });
+            }
+            done_item(k);
+        }
+    }
+
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        // The softmax warps have seen every output complete, unless a wait gave up: then what
+        // this warp issued may still be running.
+        if (*abort_f) {
+            if (elect_one()) tc_commit(b_end);
+            __syncwarp();
+            drain_bar(b_end, 0, p.status);
+        }
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem)
+                     : "memory");
+    }
+}
+
+// The shape of a call's work and its scratch.
+struct Plan {
+    int G, TT, subs, words, unit_shift, rec_words, max_rec;
+    int64_t items;
+    size_t items_bytes, recs_bytes;
+    size_t bytes() const { return items_bytes + recs_bytes; }
+};
+Plan make_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_k, int64_t topk, int64_t block,
+               int64_t nh, int64_t kvh) {
+    Plan pl;
+    pl.G = heads_of_tile(nh / kvh, &pl.subs);
+    pl.TT = ROWS / pl.G;
+    pl.words = (2 * pl.TT + 31) / 32;
+    const int64_t unit = block < KB ? block : KB;
+    pl.unit_shift = 0;
+    while ((1 << pl.unit_shift) < unit) pl.unit_shift++;
+    const int64_t nu = KB / unit;
+    pl.rec_words = (int)(nu * (1 + pl.words));
+    // blocks of an item: as many as there are, or as its tokens can list
+    const int64_t toks = 2 * pl.TT < max_q ? 2 * pl.TT : max_q;
+    int64_t blocks = (max_k + block - 1) / block;
+    if (toks * topk < blocks) blocks = toks * topk;
+    pl.max_rec = (int)((blocks * (block / unit) + nu - 1) / nu);
+    if (pl.max_rec < 1) pl.max_rec = 1;
+    // every sequence has at most one pair of tiles that is not full
+    pl.items = (Tq / (2 * pl.TT) + B) * kvh * pl.subs;
+    pl.items_bytes = (size_t)pl.items * sizeof(Item);
+    pl.recs_bytes = (size_t)pl.items * pl.max_rec * pl.rec_words * 4;
+    return pl;
+}
+
+int check_sizes(const char* name, int64_t B, int64_t Tq, int64_t max_q, int64_t max_k, int64_t topk,
+                int64_t block) {
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(block >= 16 && block <= 256 && (block & (block - 1)) == 0, DS41_E_ARG,
+                 "%s: blocks of %lld rows (a power of two of 16 .. 256)", name, (long long)block);
+    DS41_REQUIRE(topk >= 1 && topk <= 1024, DS41_E_ARG, "%s: topk=%lld (1 .. 1024)", name,
+                 (long long)topk);
+    DS41_REQUIRE(B >= 0 && B < 65536 && Tq >= 0 && Tq < lim && max_q >= 0 && max_q < lim &&
+                     max_k >= 0 && max_k <= 32768 * block,
+                 DS41_E_RANGE, "%s: B=%lld Tq=%lld max_q=%lld max_k=%lld (at most 32768 blocks)",
+                 name, (long long)B, (long long)Tq, (long long)max_q, (long long)max_k);
+    return DS41_OK;
+}
+
+}  // namespace bp
+}  // namespace ds41
+
+using namespace ds41;
+
+extern "C" size_t ds41_block_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max_q,
+                                                         int64_t max_k, int64_t topk,
+                                                         int64_t block, int64_t nh, int64_t kvh) {
+    const char* name = "ds41_block_prompt_attn_workspace_bytes";
+    if (check_heads(name, nh, kvh, 16, 1.0f, 0) ||
+        bp::check_sizes(name, B, Tq, max_q, max_k, topk, block) || B == 0 || Tq == 0 || max_q == 0)
+        return 0;
+    return bp::make_plan(B, Tq, max_q, max_k, topk, block, nh, kvh).bytes();
+}
+
+extern "C" int ds41_block_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
+                                          const ds41_bf16* k, int64_t k_tok, int64_t k_head,
+                                          const ds41_bf16* v, int64_t v_tok, int64_t v_head,
+                                          const int32_t* cu_q, const int32_t* cu_k,
+                                          const int32_t* idx, int64_t topk, int64_t block,
+                                          int64_t B, int64_t Tq, int64_t Tk, int64_t max_q,
+                                          int64_t max_k, int64_t nh, int64_t kvh, int64_t hd,
+                                          float scale, const float* sink, ds41_bf16* o, float* lse,
+                                          void* ws, size_t ws_bytes, ds41_stream_t stream) {
+    const char* name = "ds41_block_prompt_attn_fwd";
+    if (int rc = check_heads(name, nh, kvh, hd, scale, 0)) return rc;
+    if (int rc = bp::check_sizes(name, B, Tq, max_q, max_k, topk, block)) return rc;
+    const int64_t lim = int64_t(1) << 31;
+    DS41_REQUIRE(Tk >= 0 && Tk < lim, DS41_E_RANGE, "%s: Tk=%lld", name, (long long)Tk);
+    if (B == 0 || Tq == 0 || max_q == 0) return DS41_OK;
+    DS41_REQUIRE(q && o && cu_q && cu_k && idx && (Tk == 0 || (k && v)), DS41_E_ARG,
+                 "%s: q, k, v, cu_q, cu_k, idx and o must be non-null", name);
+    DS41_REQUIRE(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(o) &&
+                     aligned_to(cu_q, 4) && aligned_to(cu_k, 4) && aligned_to(idx, 4) &&
+                     aligned_to(sink, 4) && aligned_to(lse, 4),
+                 DS41_E_ARG, "%s: q, k, v and o must be 16-byte aligned", name);
+    DS41_REQUIRE(good_strides(q_tok, q_head, hd) &&
+                     (Tk == 0 ||
+                      (good_strides(k_tok, k_head, hd) && good_strides(v_tok, v_head, hd))),
+                 DS41_E_ARG, "%s: strides must be multiples of 8 and at least hd", name);
+    const bp::Plan pl = bp::make_plan(B, Tq, max_q, max_k, topk, block, nh, kvh);
+    DS41_REQUIRE(pl.items < lim, DS41_E_RANGE, "%s: Tq=%lld B=%lld kvh=%lld", name, (long long)Tq,
+                 (long long)B, (long long)kvh);
+    DS41_REQUIRE(ws && aligned16(ws) && ws_bytes >= pl.bytes(), DS41_E_WORKSPACE,
+                 "%s: needs %zu bytes of workspace, got %zu", name, pl.bytes(), ws ? ws_bytes : 0);
+    bp::Params p{};
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.idx = idx;
+    p.sink = sink;
+    p.o = o;
+    p.lse = lse;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.B = (int)B;
+    p.max_q = (int)max_q;
+    p.max_k = (int)max_k;
+    p.nh = (int)nh;
+    p.kvh = (int)kvh;
+    p.hd = (int)hd;
+    p.topk = (int)topk;
+    p.G = pl.G;
+    p.TT = pl.TT;
+    p.subs = pl.subs;
+    p.n_groups = (int)kvh * pl.subs;
+    while ((1 << p.shift) < block) p.shift++;
+    p.unit_shift = pl.unit_shift;
+    p.words = pl.words;
+    p.rec_words = pl.rec_words;
+    p.max_rec = pl.max_rec;
+    p.c = scale * tc::SM_LOG2E;
+    p.items = static_cast<bp::Item*>(ws);
+    p.recs = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + pl.items_bytes);
+    if (int rc = status_word(&p.status)) return rc;
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int rc = tc::get_encode(&enc)) return rc;
+    CUtensorMap mq, mk, mv;
+    const int unit = 1 << pl.unit_shift;
+    if (int rc = pa::make_map_heads(enc, &mq, q, Tq, nh, hd, q_tok, q_head, pl.G, pl.TT)) return rc;
+    if (Tk > 0) {
+        if (int rc = pa::make_map_heads(enc, &mk, k, Tk, kvh, hd, k_tok, k_head, 1, unit)) return rc;
+        if (int rc = pa::make_map_heads(enc, &mv, v, Tk, kvh, hd, v_tok, v_head, 1, unit)) return rc;
+    } else {
+        mk = mv = mq;  // never read
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    const dim3 grid((unsigned)pl.items);
+    if (int rc = launch_pdl(bp::plan_kernel, grid, dim3(bp::PLAN), 0, st, name, p)) return rc;
+    auto kern = hd <= 64 ? bp::block_prompt_kernel<64> : bp::block_prompt_kernel<128>;
+    const size_t smem = hd <= 64 ? pa::Cfg<64>::SMEM : pa::Cfg<128>::SMEM;
+    if (int rc = hd <= 64 ? allow_smem<bp::block_prompt_kernel<64>>((int)smem, name)
+                          : allow_smem<bp::block_prompt_kernel<128>>((int)smem, name))
+        return rc;
+    return launch_pdl(kern, grid, dim3(pa::THREADS), smem, st, name, mq, mk, mv, p);
+}
