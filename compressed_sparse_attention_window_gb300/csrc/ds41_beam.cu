@@ -6,24 +6,31 @@
 // the end) and the row's best k logits; the beams' lists are then merged by offers
 // worked out in 64 bits.
 //
-// The best k.  A list of keys (x as an ordered integer, then the lower token) gets what
-// passes the k-th best so far, which few do after the first part of a row: for that part
-// the k-th largest of the threads' maxima is a bound that at least k logits reach.
+// The best k.  A bound that k logits of a run reach follows from the lanes' maxima: k lanes
+// at least have one that is not below the lowest, over the 8 warps, of a warp's (k / 8)-th
+// largest.  What is not below the bound (fewer and fewer) goes to the warp's list as a
+// key, x as an ordered integer and then the lower token.  The lists are joined without
+// sorting: what is among the best k has fewer than k above it.
 //
-// What bounds it.  The logits are read once: HBM.  A row is cut into runs so that every
-// SM has some, and a thread has the next part of its run in flight while it works on
-// one.
+// What bounds it.  The logits are read once: HBM, if the exponentials (16 a cycle and SM)
+// and the instructions around them keep up.  A row is cut into runs so that every SM has
+// some; a warp goes through its part of a run alone, with the next step's logits in flight.
+#include <cfloat>
+#include <type_traits>
+
 #include "ds41_softmax_tc.cuh"
 
 namespace ds41 {
 namespace beam {
 
-constexpr int NT = 256;
-constexpr int PER = 16;          // logits of a thread in a part of a run
-constexpr int PART = NT * PER;
-constexpr int CAP = 1024;        // keys of a list
-constexpr int TRIM = 384;        // a list this long is cut to its best
+constexpr int WARPS = 8;
+constexpr int NT = WARPS * 32;
+constexpr int PER = 16;          // logits of a lane in a step
+constexpr int STEP = 32 * PER;   // tokens of a warp's step
+constexpr int PART = WARPS * STEP;
+constexpr int CAP = STEP;        // keys of a warp's list
 constexpr int MAX_K = 128;
+constexpr int OFFERS = 1024;     // that are ranked at once
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct Args {
@@ -51,146 +58,189 @@ __device__ __forceinline__ float x_of(uint64_t key) {
     return __uint_as_float((o >> 31) ? o ^ 0x80000000u : ~o);
 }
 __device__ __forceinline__ int token_of(uint64_t key) { return (int)~(uint32_t)key; }
+// larger for larger numbers; a NaN is a number like the least
+__device__ __forceinline__ uint32_t rank_of(float x) {
+    const uint32_t u = __float_as_uint(x == x ? x : -INFINITY);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float score_of(uint32_t rank) {
+    return __uint_as_float((rank >> 31) ? rank ^ 0x80000000u : ~rank);
+}
 // whether a beam reads its logits
 __device__ __forceinline__ bool reads(const Args& a, int64_t row) {
     const float s = a.scores[row];
     return s > -INFINITY && s < INFINITY && !(a.ended && a.ended[row]);
 }
 
-struct List {
-    uint64_t key[CAP];
-    uint64_t sorted[MAX_K];
-    uint64_t best[NT / 32];
-    float most[NT];
-    float bound;
-    int n;
+// The order of offers: the value (as an ordered integer), then the lower beam, then within
+// a beam the logit and the lower token.
+struct Offer {
+    uint64_t v, key;
+    int w;
 };
-// The list's best k, in order, and the bound that a further logit has to pass.  All threads.
-__device__ __forceinline__ void trim(List& l, int k) {
-    const int n = min(l.n, CAP);
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const uint64_t mine = l.key[i];
-        int rank = 0;
-        for (int j = 0; j < n; j++) rank += l.key[j] > mine;
-        if (rank < k) l.sorted[rank] = mine;
-    }
-    __syncthreads();
-    const int kept = min(n, k);
-    for (int i = threadIdx.x; i < kept; i += NT) l.key[i] = l.sorted[i];
-    if (threadIdx.x == 0) {
-        l.n = kept;
-        if (kept == k) l.bound = x_of(l.sorted[k - 1]);
-    }
-    __syncthreads();
+__device__ __forceinline__ bool better(const Offer& x, const Offer& y) {
+    if (x.v != y.v) return x.v > y.v;
+    if (x.w != y.w) return x.w < y.w;
+    return x.key > y.key;
+}
+// larger for larger numbers, 0 for -inf and what is none; -0 is 0
+__device__ __forceinline__ uint64_t order_of(double v) {
+    if (!(v > -INFINITY)) return 0;
+    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ double number_of(uint64_t o) {
+    return __longlong_as_double((long long)((o >> 63) ? o ^ 0x8000000000000000ull : ~o));
 }
 
-// Thread t has the tokens t, t + NT, ... of a part, whatever the row's alignment, so equal
-// rows have equal sums to the last bit, and their offers tie.
+// A warp has the tokens of every eighth step of 512 of a run, token `lane` of each 32 of them,
+// whatever the row's alignment: equal rows have equal sums to the last bit, and their
+// offers tie.
 template <bool BF16>
 __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    __shared__ List l;
-    __shared__ float2 parts[NT / 32];
+    __shared__ uint64_t lists[WARPS][CAP];
+    __shared__ uint64_t all[WARPS * MAX_K];
+    __shared__ int n_of[WARPS], n_all;
+    __shared__ float bound_of[WARPS];
+    __shared__ volatile uint32_t nth[WARPS];  // the warps' r-th largest lane maxima, as ranks
+    __shared__ float2 parts[WARPS];
     const int64_t row = blockIdx.y;
     if (!reads(a, row)) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
     const int64_t b = row / a.W, first = b * a.b_stride + (row - b * a.W) * a.w_stride;
     const int j0 = blockIdx.x * a.run, j1 = min(a.V, j0 + a.run);
-    auto load = [&](int t) -> uint32_t {
-        if (t >= j1) return BF16 ? 0xff80u : 0xff800000u;  // -inf
-        return BF16 ? (uint32_t)__ldcs(static_cast<const uint16_t*>(a.x) + first + t)
-                    : __ldcs(static_cast<const uint32_t*>(a.x) + first + t);
-    };
-    if (tid == 0) {
-        l.n = 0;
-        l.bound = -INFINITY;
-    }
+    using T = typename std::conditional<BF16, uint16_t, uint32_t>::type;
+    const T* from = static_cast<const T*>(a.x) + first;
+    uint64_t* list = lists[warp];
     uint32_t next[PER];
+    auto load = [&](int j) {  // a lane's logits of the step whose first one it has at j
+        if (j - lane + STEP <= j1) {
+            const T* at = from + j;
 #pragma unroll
-    for (int e = 0; e < PER; e++) next[e] = load(j0 + e * NT + tid);
-    __syncthreads();
-    float m = -INFINITY, sum = 0.0f;
-    int have = 0;  // keys of the list
-    for (int j = j0; j < j1; j += PART) {
+            for (int e = 0; e < PER; e++) next[e] = __ldcs(at + e * 32);
+        } else {
+#pragma unroll
+            for (int e = 0; e < PER; e++)
+                next[e] = j + e * 32 < j1 ? (uint32_t)__ldcs(from + j + e * 32)
+                                          : BF16 ? 0xff80u : 0xff800000u;  // -inf
+        }
+    };
+    int j = j0 + warp * STEP + lane;
+    load(j);
+    float m = -INFINITY, sum = 0.0f, bound = -FLT_MAX;
+    int have = 0;  // keys of the list; at least k logits of the run's are not below the bound
+    // k lanes at least, `share` of each warp that has tokens, have a maximum that is not below
+    // the lowest of those warps' share-th largest
+    const int busy = min(WARPS, (j1 - j0 + STEP - 1) / STEP), share = (k + busy - 1) / busy;
+    for (int step = 1; step == 1 || j - lane < j1; j += WARPS * STEP, step++) {
         float x[PER];
 #pragma unroll
         for (int e = 0; e < PER; e++) x[e] = __uint_as_float(BF16 ? next[e] << 16 : next[e]);
-        if (j + PART < j1) {
-#pragma unroll
-            for (int e = 0; e < PER; e++) next[e] = load(j + PART + e * NT + tid);
-        }
+        load(j + WARPS * STEP);
         float top = x[0];
 #pragma unroll
-        for (int e = 1; e < PER; e++) top = fmaxf(top, x[e]);
-        if (top > m) {
-            sum *= tc::ex2((m - top) * LOG2E);
-            m = top;
-        }
+        for (int e = 1; e < PER; e += 2)
+            top = e + 1 < PER ? tc::max3(top, x[e], x[e + 1]) : fmaxf(top, x[e]);
+        const float up = fmaxf(m, top), at = up == -INFINITY ? 0.0f : up;
         // (the difference first: x log2(e) rounded would be off by as much as x is large)
-        const float at = m == -INFINITY ? 0.0f : m;
+        uint64_t s2 = f2(m == up ? sum : sum * tc::ex2((m - at) * LOG2E), 0.0f);
+        m = up;
+        const uint64_t minus = f2(-at, -at), log2e = f2(LOG2E, LOG2E);
 #pragma unroll
-        for (int e = 0; e < PER; e++) sum += tc::ex2((x[e] - at) * LOG2E);
-        // ---- the best ----
-        auto token = [&](int e) { return j + e * NT + tid; };
-        float bound = l.bound;
-        const bool start = bound == -INFINITY;
-        if (start) {  // the k-th largest of the threads' maxima
-            l.most[tid] = top;
-            __syncthreads();
-            int rank = 0;
-            for (int i = 0; i < NT; i++)
-                rank += l.most[i] > top || (l.most[i] == top && i < tid);
-            if (rank == a.k - 1) l.bound = top;  // (a NaN has no rank; its row offers nothing)
-            __syncthreads();
-            bound = l.bound;
+        for (int e = 0; e < PER; e += 2) {
+            float y, z;
+            unf2(mul2(add2(f2(x[e], x[e + 1]), minus), log2e), y, z);
+            s2 = add2(s2, f2(tc::ex2(y), tc::ex2(z)));
         }
-        if (top > bound || (start && top == bound)) {
+        float y, z;
+        unf2(s2, y, z);
+        sum = y + z;
+        // ---- the best: what bounds them rises with the lanes' maxima (looked at after 1, 2,
+        // 4, 8 .. steps) ----
+        if ((step & (step - 1)) == 0) {
+            if (step == 1 && k <= 32) {  // the k-th largest of the warp's own
+                int rank = 0;
 #pragma unroll
-            for (int e = 0; e < PER; e++)
-                if (x[e] > bound || (start && x[e] == bound && x[e] > -INFINITY)) {
-                    const int at_n = atomicAdd(&l.n, 1);
-                    if (at_n < CAP) l.key[at_n] = key_of(x[e], token(e));
+                for (int o = 1; o < 32; o++) {
+                    const float other = __shfl_xor_sync(0xffffffffu, m, o);
+                    rank += other > m || (other == m && (lane ^ o) < lane);
                 }
+                const unsigned kth = __ballot_sync(0xffffffffu, rank == k - 1);
+                if (kth) bound = fmaxf(bound, __shfl_sync(0xffffffffu, m, __ffs(kth) - 1));
+            }
+            if (share <= 16) {
+                uint32_t mine = rank_of(m), top_most = 0;
+                for (int i = 0; i < share; i++) {
+                    top_most = __reduce_max_sync(0xffffffffu, mine);
+                    const unsigned who = __ballot_sync(0xffffffffu, mine == top_most);
+                    if (lane == __ffs(who) - 1) mine = 0;
+                }
+                if (lane == 0) nth[warp] = top_most;
+            }
+            if (step == 1) __syncthreads();  // (every warp has a first step, if one of none)
         }
-        __syncthreads();
-        const int n = l.n;
-        __syncthreads();
-        if (n > CAP) {
-            // more than the list holds (equal logits): the part's best k one by one
-            if (tid == 0) l.n = have;
-            uint64_t below = ~0ull;
-            for (int i = 0; i < a.k; i++) {
-                uint64_t mine = 0;
+        if (share <= 16) {
+            const uint32_t least =
+                __reduce_min_sync(0xffffffffu, lane < busy ? nth[lane % WARPS] : 0xffffffffu);
+            bound = fmaxf(bound, score_of(least));
+        }
+        if (!__any_sync(0xffffffffu, top >= bound)) continue;
+        uint32_t pass = 0;
+#pragma unroll
+        for (int e = 0; e < PER; e++) pass |= (x[e] >= bound ? 1u : 0u) << e;
+        const int mine = __popc(pass);
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        const int added = __shfl_sync(0xffffffffu, before, 31);
+        before += have - mine;
+        if (have + added <= CAP) {
+            for (; pass; pass &= pass - 1) {  // (read once more: no index into registers)
+                const int t = j + (__ffs(pass) - 1) * 32;
+                const uint32_t w = from[t];
+                list[before++] = key_of(__uint_as_float(BF16 ? w << 16 : w), t);
+            }
+            have += added;
+        } else {
+            // more than the list holds: the best k of it and of the step, one by one, into
+            // their places from the front (what is taken from there is kept in registers)
+            uint64_t below = ~0ull, kept[MAX_K / 32] = {};
+            int n = 0;
+            for (; n < k; n++) {
+                uint64_t best = 0;
+                for (int i = lane; i < have; i += 32)
+                    if (list[i] < below && list[i] > best) best = list[i];
 #pragma unroll
                 for (int e = 0; e < PER; e++) {
-                    const uint64_t key = key_of(x[e], token(e));
-                    if (x[e] > -INFINITY && key < below && key > mine) mine = key;
+                    const uint64_t key = key_of(x[e], j + e * 32);
+                    if (x[e] >= -FLT_MAX && key < below && key > best) best = key;
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
-                    const uint64_t y = __shfl_xor_sync(0xffffffffu, mine, o);
-                    if (y > mine) mine = y;
+                    const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
+                    if (v > best) best = v;
                 }
-                if (lane == 0) l.best[warp] = mine;
-                __syncthreads();
+                if (best == 0) break;
+                below = best;
 #pragma unroll
-                for (int w = 0; w < NT / 32; w++)
-                    if (l.best[w] > mine) mine = l.best[w];
-                if (mine == 0) break;
-                below = mine;
-                if (tid == 0) l.key[l.n++] = mine;  // (at most TRIM + k of them)
-                __syncthreads();
+                for (int i = 0; i < MAX_K / 32; i++)
+                    if (n == 32 * i + lane) kept[i] = best;
             }
-            __syncthreads();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < MAX_K / 32; i++)
+                if (32 * i + lane < n) list[32 * i + lane] = kept[i];
+            have = n;
+            if (n == k) bound = fmaxf(bound, x_of(below));
         }
-        if (start || n > TRIM || j + PART >= j1) trim(l, a.k);
-        have = l.n;
-        __syncthreads();
+        __syncwarp();
     }
-    // ---- the run's results ----
-    const int64_t at = row * a.splits + blockIdx.x;
-    for (int i = tid; i < a.k; i += NT) a.keys[at * a.k + i] = i < have ? l.key[i] : 0;
+    // ---- the run's sum ----
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
@@ -199,101 +249,166 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
         sum = sum * tc::ex2((m - ref) * LOG2E) + s2 * tc::ex2((m2 - ref) * LOG2E);
         m = to;
     }
-    if (lane == 0) parts[warp] = make_float2(m, sum);
+    if (lane == 0) {
+        parts[warp] = make_float2(m, sum);
+        n_of[warp] = have;
+        bound_of[warp] = bound;
+    }
+    if (tid == 0) n_all = 0;
     __syncthreads();
+    const int64_t at = row * a.splits + blockIdx.x;
     if (tid == 0) {
-        for (int w = 1; w < NT / 32; w++) m = fmaxf(m, parts[w].x);
+        for (int w = 1; w < WARPS; w++) m = fmaxf(m, parts[w].x);
         const float ref = m == -INFINITY ? 0.0f : m;
         sum = 0.0f;
-        for (int w = 0; w < NT / 32; w++) sum += parts[w].y * tc::ex2((parts[w].x - ref) * LOG2E);
+        for (int w = 0; w < WARPS; w++) sum += parts[w].y * tc::ex2((parts[w].x - ref) * LOG2E);
         a.sums[at] = make_float2(m, sum);
+    }
+    // ---- its best k: what is not below the highest bound, by counting what is better ----
+    for (int w = 0; w < WARPS; w++) bound = fmaxf(bound, bound_of[w]);
+    for (int w = 0; w < WARPS; w++)
+        for (int i = tid; i < n_of[w]; i += NT) {
+            const uint64_t key = lists[w][i];
+            if (x_of(key) < bound) continue;
+            const int to = atomicAdd(&n_all, 1);
+            if (to < WARPS * MAX_K) all[to] = key;
+        }
+    __syncthreads();
+    const int n = n_all;
+    uint64_t* out = a.keys + at * k;
+    if (n <= WARPS * MAX_K) {
+        for (int i = tid; i < n; i += NT) {
+            const uint64_t mine = all[i];
+            int rank = 0;
+            for (int y = 0; y < n; y++) rank += all[y] > mine;
+            if (rank < k) out[rank] = mine;
+        }
+        for (int i = n + tid; i < k; i += NT) out[i] = 0;
+    } else if (warp == 0) {  // (equal logits) one by one
+        uint64_t below = ~0ull;
+        for (int i = 0; i < k; i++) {
+            uint64_t best = 0;
+            for (int w = 0; w < WARPS; w++)
+                for (int y = lane; y < n_of[w]; y += 32)
+                    if (lists[w][y] < below && lists[w][y] > best) best = lists[w][y];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
+                if (v > best) best = v;
+            }
+            below = best;
+            if (lane == 0) out[i] = best;
+        }
     }
 }
 
-// The order of offers: the value, then the lower beam, then within a beam the logit and
-// the lower token.
-struct Offer {
-    double v;
-    int w;
-    uint64_t key;
-};
-__device__ __forceinline__ bool better(const Offer& x, const Offer& y) {
-    if (x.v != y.v) return x.v > y.v;
-    if (x.w != y.w) return x.w < y.w;
-    return x.key > y.key;
-}
-
-// A CTA for a search: the lists of all runs of its beams merged, best first.
+// A CTA for a search: the lists of all runs of its beams merged, best first.  What is not
+// below the last entry of some full list (k offers at least are not) is ranked by counting
+// what is better; more of it than fits is merged from the lists' heads.
 __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ double base[];  // [W]: s_w - L; -inf: the beam offers nothing
+    extern __shared__ double base[];  // [W]: s_w - L; NaN: the beam offers nothing
+    __shared__ Offer all[OFFERS];
+    __shared__ unsigned long long least;
+    __shared__ int n_all, taken[NT / 32];
     __shared__ Offer best[NT / 32];
-    __shared__ int winner[NT / 32];
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
+    const int n_lists = a.W * a.splits;
+    if (tid == 0) {
+        least = 0;
+        n_all = 0;
+    }
     for (int w = tid; w < a.W; w += NT) {
         const int64_t row = (int64_t)b * a.W + w;
-        double to = -INFINITY;
-        if (reads(a, row)) {
-            float m = -INFINITY;
-            double sum = 0.0;
+        double to = NAN;
+        if (a.ended && a.ended[row]) {
+            to = 0.0;
+        } else if (reads(a, row)) {
+            float m = -INFINITY, sum = 0.0f;
             for (int s = 0; s < a.splits; s++) m = fmaxf(m, a.sums[row * a.splits + s].x);
+            const float ref = m == -INFINITY ? 0.0f : m;
             for (int s = 0; s < a.splits; s++) {
                 const float2 p = a.sums[row * a.splits + s];
-                sum += (double)p.y * (p.x == -INFINITY && p.y == 0.0f ? 0.0 : exp((double)p.x - m));
+                sum += p.y * expf(p.x - ref);
             }
             // (a sum that a NaN or an infinity is in is NaN; one of nothing but -inf is 0)
-            if (sum > 0.0 && sum < INFINITY) to = (double)a.scores[row] - ((double)m + log(sum));
+            if (sum > 0.0f && sum < INFINITY)
+                to = (double)a.scores[row] - ((double)m + (double)logf(sum));
         }
         base[w] = to;
     }
     __syncthreads();
-    // the heads of the lists: list h is run h % splits of beam h / splits; an ended beam's
-    // first list is its one offer.  A thread has the lists tid, tid + NT, ... and keeps the
-    // best of their heads.
-    const int lists = a.W * a.splits;
-    auto head = [&](int h, int at) {
-        Offer o{-INFINITY, h / a.splits, 0};
-        const int64_t row = (int64_t)b * a.W + o.w;
+    // List h is run h % splits of beam h / splits; an ended beam's first list is its one offer.
+    auto offer = [&](int h, int i) {
+        const int w = h / a.splits;
+        const int64_t row = (int64_t)b * a.W + w;
+        Offer o{0, 0, w};
         if (a.ended && a.ended[row]) {
             const float s = a.scores[row];
-            if (h % a.splits == 0 && at == 0 && s < INFINITY) {
-                o.v = s;
+            if (h % a.splits == 0 && i == 0 && s < INFINITY) {
+                o.v = order_of(s);
                 o.key = key_of(0.0f, a.end_token);
             }
-        } else if (at < a.k && base[o.w] > -INFINITY) {
-            o.key = a.keys[((int64_t)b * lists + h) * a.k + at];
-            if (o.key) o.v = base[o.w] + (double)x_of(o.key);
+        } else if (i < k && base[w] == base[w]) {
+            o.key = a.keys[((int64_t)b * n_lists + h) * k + i];
+            if (o.key) o.v = order_of(base[w] + (double)x_of(o.key));
         }
-        if (!(o.v > -INFINITY)) o.v = -INFINITY;
         return o;
     };
-    int* at = reinterpret_cast<int*>(base + a.W);  // [lists]: the heads' places
-    for (int h = tid; h < lists; h += NT) at[h] = 0;
+    auto write = [&](int i, const Offer& o) {
+        const int64_t to = (int64_t)b * k + i;
+        a.out[to] = o.v ? (float)number_of(o.v) : -INFINITY;
+        a.parents[to] = o.v ? b * a.W + o.w : -1;
+        a.tokens[to] = o.v ? token_of(o.key) : -1;
+    };
+    for (int h = tid; h < n_lists; h += NT) atomicMax(&least, (unsigned long long)offer(h, k - 1).v);
     __syncthreads();
-    Offer mine{-INFINITY, 0x7fffffff, 0};
-    int from = -1;
-    auto scan = [&] {
-        mine = {-INFINITY, 0x7fffffff, 0};
-        from = -1;
-        for (int h = tid; h < lists; h += NT) {
-            const Offer o = head(h, at[h]);
-            if (o.v > -INFINITY && (from < 0 || better(o, mine))) {
+    const uint64_t from = least;
+    for (int x = tid; x < n_lists * k; x += NT) {
+        const int h = x / k;
+        const Offer o = offer(h, x - h * k);
+        if (o.v == 0 || o.v < from) continue;
+        const int to = atomicAdd(&n_all, 1);
+        if (to < OFFERS) all[to] = o;
+    }
+    __syncthreads();
+    const int n = n_all;
+    if (n <= OFFERS) {
+        for (int i = tid; i < n; i += NT) {
+            const Offer mine = all[i];
+            int rank = 0;
+            for (int y = 0; y < n; y++) rank += better(all[y], mine);
+            if (rank < k) write(rank, mine);
+        }
+        for (int i = n + tid; i < k; i += NT) write(i, Offer{0, 0, 0});
+        return;
+    }
+    int* at = reinterpret_cast<int*>(base + a.W);  // [lists]: the heads' places
+    for (int h = tid; h < n_lists; h += NT) at[h] = 0;
+    Offer mine;
+    int list;
+    auto scan = [&] {  // the best head of this thread's lists
+        mine = Offer{0, 0, 0x7fffffff};
+        list = -1;
+        for (int h = tid; h < n_lists; h += NT) {
+            const Offer o = offer(h, at[h]);
+            if (o.v && (list < 0 || better(o, mine))) {
                 mine = o;
-                from = h;
+                list = h;
             }
         }
     };
     scan();
-    for (int i = 0; i < a.k; i++) {
+    for (int i = 0; i < k; i++) {
         Offer o = mine;
-        int f = from;
+        int f = list;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             Offer y;
             y.v = __shfl_xor_sync(0xffffffffu, o.v, d);
-            y.w = __shfl_xor_sync(0xffffffffu, o.w, d);
             y.key = __shfl_xor_sync(0xffffffffu, o.key, d);
+            y.w = __shfl_xor_sync(0xffffffffu, o.w, d);
             const int g = __shfl_xor_sync(0xffffffffu, f, d);
             if (g >= 0 && (f < 0 || better(y, o))) {
                 o = y;
@@ -302,20 +417,15 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
         }
         if (lane == 0) {
             best[warp] = o;
-            winner[warp] = f;
+            taken[warp] = f;
         }
         __syncthreads();
         for (int w = 0; w < NT / 32; w++)
-            if (winner[w] >= 0 && (f < 0 || better(best[w], o))) {
+            if (taken[w] >= 0 && (f < 0 || better(best[w], o))) {
                 o = best[w];
-                f = winner[w];
+                f = taken[w];
             }
-        if (tid == 0) {
-            const int64_t to = (int64_t)b * a.k + i;
-            a.out[to] = f >= 0 ? (float)o.v : -INFINITY;
-            a.parents[to] = f >= 0 ? b * a.W + o.w : -1;
-            a.tokens[to] = f >= 0 ? token_of(o.key) : -1;
-        }
+        if (tid == 0) write(i, f >= 0 ? o : Offer{0, 0, 0});
         if (f >= 0 && f % NT == tid) {
             at[f]++;
             scan();
@@ -324,17 +434,23 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     }
 }
 
-// Runs of a row: enough for four CTAs an SM over all rows, of a part at least each.
+// Runs of a row: what makes the SM with the most of them end soonest (a run costs its parts and
+// about one more).
 struct Plan {
     int splits, parts;  // runs, and parts of a run
     size_t keys_bytes, sums_bytes;
 };
 Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
     const int64_t parts = (V + PART - 1) / PART, rows = B * W;
-    int64_t splits = (4 * (int64_t)sms + rows - 1) / rows;
-    if (splits > parts) splits = parts;
-    if (splits > 64) splits = 64;
-    if (splits < 1) splits = 1;
+    int64_t splits = 1, best = 0;
+    for (int64_t n = 1; n <= parts && n <= 64; n++) {
+        const int64_t per = (parts + n - 1) / n;
+        const int64_t cost = (rows * n + sms - 1) / sms * (per + 1);
+        if (n == 1 || cost < best) {
+            best = cost;
+            splits = n;
+        }
+    }
     Plan p;
     const int64_t per = (parts + splits - 1) / splits;
     p.splits = (int)((parts + per - 1) / per);

@@ -6,22 +6,24 @@
 // lists, up to its own place.
 //
 // Rows and keys.  A tile of 128 rows is TT tokens times the G heads of a group, an item two
-// such tiles (2 TT neighbouring tokens), as there.  The keys of an item are the union of
-// its tokens' blocks, packed: 128 keys of an MMA block are as many picked blocks (units
-// of at most 128 keys) side by side, each copied by TMA to its own rows.  A row masks the units
-// that its token does not list.  A tile that no token of lists any of a block's units
-// skips it.
+// such tiles (2 TT neighbouring tokens), as there.  A tile's keys are the union of its
+// tokens' blocks, packed: 128 keys of an MMA block (a record) are as many picked blocks
+// (units of at most 128 keys) side by side, each copied by TMA to its own rows.  A row masks
+// the units that its token does not list.  The blocks that both tiles list come first, in
+// records that both read from one copy; then each tile walks the records of its own,
+// the two side by side, so that the tensor core works on one while the softmax of the
+// other runs.
 //
 // Why the union.  A product of 128 rows and 64 keys costs 128 + 128 cycles a unit for the whole
 // tile; token by token (16 rows at most, on mma.sync) the unit's K and V would have to be
 // read from shared memory once for each token that lists it, 256 cycles each time: the
 // union is never twice as slow, and neighbouring tokens mostly list the same blocks.
 //
-// Two kernels.  plan_kernel makes the items' lists: a table of masks in shared memory (a word
+// Two kernels.  plan_kernel makes the items' records: a table of masks in shared memory (a word
 // for 32 tokens and each block), filled from the tokens' lists, is walked in order; what is
-// not empty becomes a slot of a record (128 keys: the units' first rows, and which tokens
-// list them).  block_prompt_kernel is the kernel of ds41_prompt_attn.cu with the records in place of
-// a range of keys.
+// not empty becomes a slot of a record (its first row, and which tokens list it).
+// block_prompt_kernel is the kernel of ds41_prompt_attn.cu with the records in place of a range of
+// keys.
 #include "ds41_prompt.cuh"
 
 namespace ds41 {
@@ -29,19 +31,26 @@ namespace bp {
 
 using namespace pa;
 
-// An item: one head group of one pair of tiles of one sequence.
+// An item: one head group of one pair of tiles of one sequence.  Its records: those of both
+// tiles, of tile 0 alone, of tile 1 alone.  Step i: both tiles on record i, or behind
+// those each on its own next one.
 struct Item {
     int grp;             // head group, -1: nothing
     int q0, n, k0, len;  // its sequence's queries and keys
     int t0;              // first token of tile 0
-    int count;           // records
-    int last[2];         // the last record that tile t takes part in, -1: none
-    int tail, tail_end;  // rows of the last record's V behind the last key
-    int id;
+    int both, own[2];    // records
+    int tail, tail_end;  // rows of V behind the last key, in the record of
+    int tail_step, tail_tile;
+    int id, spare[2];
+    __device__ __forceinline__ int steps(int t) const { return both + (t ? own[1] : own[0]); }
+    __device__ __forceinline__ int steps() const { return both + max(own[0], own[1]); }
+    __device__ __forceinline__ int record(int t, int i) const {
+        return i + (t && i >= both ? own[0] : 0);
+    }
 };
-static_assert(sizeof(Item) == 48, "three 16-byte pieces");
+static_assert(sizeof(Item) == 64, "four 16-byte pieces");
 
-constexpr uint32_t ROW = 0x3fffffffu;  // a unit's word: its first row, and which tiles list it
+constexpr uint32_t ROW = 0x3fffffffu;  // a unit's word: its first row; this: none
 constexpr int PLAN = 256;              // threads of plan_kernel
 constexpr int TABLE = 8192;            // words of its table
 
@@ -90,16 +99,16 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     pdl_wait();
     pdl_trigger();
     __shared__ uint32_t table[TABLE];
-    __shared__ int end[256], sh[PLAN / 32];
-    __shared__ Item it;
+    __shared__ int end[256], sh[PLAN / 32], units_of[3];  // (both tiles', tile 0's, tile 1's)
+    __shared__ __align__(16) Item it;
     const int tid = threadIdx.x, id = blockIdx.x;
     const int w = id / p.n_groups, grp = id - w * p.n_groups, h = grp / p.subs;
     if (tid == 0) {
         it = Item{};
         it.grp = -1;
-        it.last[0] = it.last[1] = -1;
         it.id = id;
     }
+    if (tid < 3) units_of[tid] = 0;
     __syncthreads();
     // the sequence (its pairs of tiles in falling order, as its longest lists are at the end)
     for (int b0 = 0, base = 0; b0 < p.B; b0 += PLAN) {
@@ -151,63 +160,88 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     const int range = TABLE / W;
     const int per = 1 << (p.shift - p.unit_shift), nu = KB >> p.unit_shift;
     uint32_t* recs = p.recs + (int64_t)id * p.max_rec * p.rec_words;
-    int found = 0;
-    for (int r0 = 0; r0 < blocks; r0 += range) {
-        const int size = min(range, blocks - r0);
-        for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
-        __syncthreads();
-        for (int e = tid; e < toks * p.topk; e += PLAN) {
-            const int tok = e / p.topk, i = e - tok * p.topk;
-            if (i > end[tok]) continue;
-            const int x = entry(tok, i);
-            if (i == end[tok]) {
-                if (x != -1 && r0 == 0) raise_status(p.status, DS41_E_INDEX);
-            } else if (x >= r0 && x < r0 + size) {
-                atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
-            }
-        }
-        __syncthreads();
-        for (int x0 = 0; x0 < size; x0 += PLAN) {
-            const int x = x0 + tid;
-            uint32_t tiles = 0;
-            if (x < size)
-                for (int y = 0; y < W; y++) {
-                    const uint32_t m = table[x * W + y], low = low_bits(p.TT - 32 * y);
-                    tiles |= (m & low ? 1u : 0u) | (m & ~low ? 2u : 0u);
+    // once to count the units of each kind, once to put them into their records
+    int base[3] = {0, 0, 0};  // the kinds' first records
+    for (int pass = 0; pass < 2; pass++) {
+        int found[3] = {0, 0, 0};  // blocks so far
+        for (int r0 = 0; r0 < blocks; r0 += range) {
+            const int size = min(range, blocks - r0);
+            if (pass == 0 || blocks > range) {
+                for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
+                __syncthreads();
+                for (int e = tid; e < toks * p.topk; e += PLAN) {
+                    const int tok = e / p.topk, i = e - tok * p.topk;
+                    if (i > end[tok]) continue;
+                    const int x = entry(tok, i);
+                    if (i == end[tok]) {
+                        if (x != -1 && r0 == 0 && pass == 0) raise_status(p.status, DS41_E_INDEX);
+                    } else if (x >= r0 && x < r0 + size) {
+                        atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
+                    }
                 }
-            int sum;
-            const int at = found + prefix(tiles != 0, sh, sum);
-            found += sum;
-            if (!tiles) continue;
-            for (int k = 0; k < per; k++) {
-                const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
-                if (row >= it.len) break;  // (behind the last key: only the last block's)
-                const int u = at * per + k, rec = u / nu, slot = u - rec * nu;
-                uint32_t* to = recs + (int64_t)rec * p.rec_words;
-                to[slot] = (uint32_t)row | tiles << 30;
-                for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
-                if (tiles & 1) atomicMax(&it.last[0], rec);
-                if (tiles & 2) atomicMax(&it.last[1], rec);
-                atomicMax(&it.count, u + 1);
-                if (row + (1 << p.unit_shift) > it.len) {
-                    it.tail = (slot << p.unit_shift) + it.len - row;
-                    it.tail_end = (slot + 1) << p.unit_shift;
+                __syncthreads();
+            }
+            for (int x0 = 0; x0 < size; x0 += PLAN) {
+                const int x = x0 + tid;
+                uint32_t tiles = 0;
+                if (x < size)
+                    for (int y = 0; y < W; y++) {
+                        const uint32_t m = table[x * W + y], low = low_bits(p.TT - 32 * y);
+                        tiles |= (m & low ? 1u : 0u) | (m & ~low ? 2u : 0u);
+                    }
+                // (three counts of at most 256 in one word)
+                const int kind = tiles == 3 ? 0 : (int)tiles;
+                int sums;
+                const int before = prefix(tiles ? 1 << (10 * kind) : 0, sh, sums);
+                const int at = found[0] * (kind == 0) + found[1] * (kind == 1) +
+                               found[2] * (kind == 2) + ((before >> (10 * kind)) & 1023);
+#pragma unroll
+                for (int k = 0; k < 3; k++) found[k] += (sums >> (10 * k)) & 1023;
+                if (!tiles) continue;
+                for (int k = 0; k < per; k++) {
+                    const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
+                    if (row >= it.len) break;  // (behind the last key: only the last block's)
+                    const int u = at * per + k, rec = u / nu, slot = u - rec * nu;
+                    if (pass == 0) {
+                        atomicMax(&units_of[kind], u + 1);
+                        continue;
+                    }
+                    const int first = kind == 0 ? base[0] : kind == 1 ? base[1] : base[2];
+                    uint32_t* to = recs + (int64_t)(first + rec) * p.rec_words;
+                    to[slot] = (uint32_t)row;
+                    for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
+                    if (row + (1 << p.unit_shift) > it.len) {
+                        it.tail = (slot << p.unit_shift) + it.len - row;
+                        it.tail_end = (slot + 1) << p.unit_shift;
+                        it.tail_step = rec + (kind ? base[1] : 0);
+                        it.tail_tile = kind == 2;
+                    }
                 }
             }
+            __syncthreads();
         }
-        __syncthreads();
+        if (pass == 0) {
+            base[1] = (units_of[0] + nu - 1) / nu;
+            base[2] = base[1] + (units_of[1] + nu - 1) / nu;
+        }
     }
-    // slots behind the last unit
-    const int units = it.count, recs_n = (units + nu - 1) / nu;
-    for (int u = units + tid; u < recs_n * nu; u += PLAN) {
-        uint32_t* to = recs + (int64_t)(u / nu) * p.rec_words;
-        to[u % nu] = ROW;
-        for (int y = 0; y < W; y++) to[nu + (u % nu) * W + y] = 0;
+    // slots behind a kind's last unit
+#pragma unroll
+    for (int kind = 0; kind < 3; kind++) {
+        const int n = units_of[kind], slots = (n + nu - 1) / nu * nu;
+        for (int u = n + tid; u < slots; u += PLAN) {
+            uint32_t* to = recs + (int64_t)(base[kind] + u / nu) * p.rec_words;
+            to[u % nu] = ROW;
+            for (int y = 0; y < W; y++) to[nu + (u % nu) * W + y] = 0;
+        }
+    }
+    if (tid == 0) {
+        it.both = base[1];
+        it.own[0] = base[2] - base[1];
+        it.own[1] = (units_of[2] + nu - 1) / nu;
     }
     __syncthreads();
-    if (tid == 0) it.count = recs_n;
-    __syncthreads();
-    if (tid < 3)
+    if (tid < 4)
         reinterpret_cast<int4*>(p.items + id)[tid] = reinterpret_cast<const int4*>(&it)[tid];
 }
 
@@ -240,8 +274,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t* b_end = b_clc + 1;               // every product is complete
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_end + 1);
     volatile int* abort_f = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    Item* items = reinterpret_cast<Item*>(tmem_slot + 2);
-    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 8 + ITEMS * sizeof(Item) <=
+    volatile uint32_t* tail_stage = tmem_slot + 2;  // where the V behind whose rows b_tail asks is
+    Item* items = reinterpret_cast<Item*>(tmem_slot + 4);
+    static_assert((2 * C::QB + 2 * C::STAGES + 12 + 2 * ITEMS) * 8 + 16 + ITEMS * sizeof(Item) <=
                       624,
                   "barrier area");
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -303,11 +338,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         it.k0 = uniform(x.k0);
         it.len = uniform(x.len);
         it.t0 = uniform(x.t0);
-        it.count = uniform(x.count);
-        it.last[0] = uniform(x.last[0]);
-        it.last[1] = uniform(x.last[1]);
+        it.both = uniform(x.both);
+        it.own[0] = uniform(x.own[0]);
+        it.own[1] = uniform(x.own[1]);
         it.tail = uniform(x.tail);
         it.tail_end = uniform(x.tail_end);
+        it.tail_step = uniform(x.tail_step);
+        it.tail_tile = uniform(x.tail_tile);
         it.id = uniform(x.id);
         return it.grp >= 0;
     };
@@ -316,9 +353,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&b_iteme[k % ITEMS]);
     };
     auto records = [&](const Item& it) { return p.recs + (int64_t)it.id * p.max_rec * p.rec_words; };
-    // record j's units, one a lane (none behind the last)
-    auto units = [&](const uint32_t* recs, const Item& it, int j) {
-        return j < it.count && lane < nu ? recs[(int64_t)j * p.rec_words + lane] : ROW;
+    // the units of tile t's step i, one a lane (none behind the last)
+    auto units = [&](const uint32_t* recs, const Item& it, int t, int i) {
+        return i < it.steps(t) && lane < nu ? recs[(int64_t)it.record(t, i) * p.rec_words + lane]
+                                            : ROW;
     };
 
     if (warp < 4) {
@@ -328,21 +366,29 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             Item it;
             for (int k = 0; ok && next_item(k, it); k++) {
-                if (it.count > 0) {
+                const int steps = it.steps();
+                if (steps > 0) {
                     const int head0 = it.grp * p.G, kvh = it.grp / p.subs, qb = nq % C::QB;
                     const uint32_t* recs = records(it);
-                    uint32_t unit = units(recs, it, 0);
+                    // the tiles' units of this step, the next and the one after that
+                    uint32_t now[2], next[2], ahead[2];
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        now[t] = ROW;
+                        next[t] = units(recs, it, t, 0);
+                        ahead[t] = units(recs, it, t, 1);
+                    }
                     if (nq >= C::QB)
                         ok = warp_wait(&b_qe[qb], ((nq / C::QB) - 1) & 1, abort_f, p.status);
                     if (ok) {
                         if (lane == 0) {
                             uint32_t q_tiles = 0;
 #pragma unroll
-                            for (int t = 0; t < 2; t++) q_tiles += it.last[t] >= 0;
+                            for (int t = 0; t < 2; t++) q_tiles += it.steps(t) > 0;
                             mbar_arrive_expect_tx(&b_q[qb], q_tiles * C::NB * (uint32_t)used * 128);
 #pragma unroll
                             for (int t = 0; t < 2; t++)
-                                if (it.last[t] >= 0)
+                                if (it.steps(t) > 0)
                                     for (int x = 0; x < C::NB; x++)
                                         tma_load_3d(sbase + C::Q_OFF + (2 * qb + t) * C::TILE +
                                                         x * C::BLK,
@@ -353,23 +399,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     // lane l copies unit l % nu, columns 64 (l / nu) ..
                     const int slot = lane % nu, x = lane / nu;
-                    for (int j = 0; j < it.count && ok; j++) {
-                        const uint32_t word = __shfl_sync(0xffffffffu, unit, slot) & ROW;
-                        unit = units(recs, it, j + 1);
+                    auto load = [&](uint32_t unit, const CUtensorMap* map) {
+                        const uint32_t word = __shfl_sync(0xffffffffu, unit, slot);
                         // (behind the last unit: rows that do not exist, read as zeros)
                         const int row = word == ROW ? (int)p.Tk : it.k0 + (int)word;
-                        for (int kv = 0; kv < 2 && ok; kv++) {
-                            const uint32_t st = n % C::STAGES, use = n / C::STAGES;
-                            if (use > 0)
-                                ok = warp_wait(&b_empty[st], (use - 1) & 1, abort_f, p.status);
-                            if (!ok) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&b_full[st], C::TILE);
-                            __syncwarp();
-                            if (x < C::NB)
-                                tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
-                                                ((slot << p.unit_shift) * 128),
-                                            kv ? &map_v : &map_k, 64 * x, kvh, row, &b_full[st]);
-                            n++;
+                        const uint32_t st = n % C::STAGES, use = n / C::STAGES;
+                        if (use > 0)
+                            ok = ok && warp_wait(&b_empty[st], (use - 1) & 1, abort_f, p.status);
+                        if (!ok) return;
+                        if (lane == 0) mbar_arrive_expect_tx(&b_full[st], C::TILE);
+                        __syncwarp();
+                        if (x < C::NB)
+                            tma_load_3d(sbase + C::KV_OFF + st * C::TILE + x * C::BLK +
+                                            ((slot << p.unit_shift) * 128),
+                                        map, 64 * x, kvh, row, &b_full[st]);
+                        n++;
+                    };
+                    // in the order in which the products want them (step -1: the first keys)
+                    for (int i = -1; i < steps && ok; i++) {
+#pragma unroll
+                        for (int t = 0; t < 2; t++) {
+                            if (i >= 0 && i < it.steps(t) && (t == 0 || i >= it.both))
+                                load(now[t], &map_v);
+                            if (i + 1 < it.steps(t) && (t == 0 || i + 1 >= it.both))
+                                load(next[t], &map_k);
+                        }
+#pragma unroll
+                        for (int t = 0; t < 2; t++) {
+                            now[t] = next[t];
+                            next[t] = ahead[t];
+                            ahead[t] = units(recs, it, t, i + 3);
                         }
                     }
                 }
@@ -388,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             constexpr uint32_t IDESC_O = idesc_bf16(128, D, 0, 1);
             const uint32_t kd = desc_lo(sbase + C::KV_OFF, 16);
             const uint32_t vd = desc_lo(sbase + C::KV_OFF, C::BLK);
-            uint32_t ring0 = 0, nq = 0, tails = 0, done_p[2] = {0, 0}, outs[2] = {0, 0};
+            uint32_t n = 0, nq = 0, tails = 0, done_p[2] = {0, 0}, outs[2] = {0, 0};
             auto wait_stage = [&](uint32_t n) {
                 const bool r =
                     warp_wait(&b_full[n % C::STAGES], (n / C::STAGES) & 1, abort_f, p.status);
@@ -396,55 +455,45 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return r;
             };
             auto stage_off = [&](uint32_t n) { return ((n % C::STAGES) * C::TILE) >> 4; };
-            // which tiles take part in a record
-            auto tiles_of = [&](uint32_t unit) {
-                return (uint32_t)uniform((int)__reduce_or_sync(0xffffffffu, unit) >> 30) & 3u;
-            };
             bool ok = true;
             Item it;
             for (int k = 0; ok && next_item(k, it); k++) {
-                if (it.count > 0) {
-                    const uint32_t* recs = records(it);
+                const int steps = it.steps();
+                if (steps > 0) {
                     const int qb = nq % C::QB;
                     const uint32_t qd = desc_lo(sbase + C::Q_OFF + 2 * qb * C::TILE, 16);
-                    uint32_t now = tiles_of(units(recs, it, 0)), ahead = units(recs, it, 1);
-                    bool begun[2] = {false, false};
-                    ok = warp_wait(&b_q[qb], (nq / C::QB) & 1, abort_f, p.status) &&
-                         wait_stage(ring0);
+                    ok = warp_wait(&b_q[qb], (nq / C::QB) & 1, abort_f, p.status);
                     nq++;
-                    if (ok && elect_one()) {
-#pragma unroll
-                        for (int t = 0; t < 2; t++)
-                            if ((now >> t) & 1) {
-                                mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
-                                                       qd + ((t * C::TILE) >> 4),
-                                                       kd + stage_off(ring0));
-                                tc_commit(&b_s[t]);
-                            }
-                        tc_commit(&b_empty[ring0 % C::STAGES]);
-                        if (it.count == 1) tc_commit(&b_qe[qb]);
-                    }
-                    __syncwarp();
-                    for (int j = 0; j < it.count && ok; j++) {
-                        const uint32_t next = tiles_of(ahead);
-                        ahead = units(recs, it, j + 2);
-                        const uint32_t nv = ring0 + 2 * (uint32_t)j + 1, nk = nv + 1;
-                        const bool more = j + 1 < it.count;
-                        // (both before the waits for the weights: nothing stands between
-                        // their arrival and the products)
-                        ok = wait_stage(nv) && (!more || wait_stage(nk));
-                        if (ok && !more && it.tail > 0) {
-                            if (lane == 0) mbar_arrive(b_tail);
-                            ok = warp_wait(b_fix, tails & 1, abort_f, p.status);
-                            tails++;
-                            tc_fence_after();
-                        }
+                    uint32_t vs[2] = {0, 0}, ks[2] = {0, 0};  // stages
+                    for (int i = -1; i < steps && ok; i++) {
 #pragma unroll
                         for (int t = 0; t < 2; t++) {
-                            const bool mine = (now >> t) & 1, then = more && ((next >> t) & 1);
+                            const bool mine = i >= 0 && i < it.steps(t);
+                            const bool then = i + 1 < it.steps(t);
+                            const bool same_v = i < it.both, same_k = i + 1 < it.both;
+                            const bool last = i + 1 == it.steps(t);
+                            // (both before the wait for the weights: nothing stands between
+                            // their arrival and the products)
+                            if (mine) {
+                                if (t == 1 && same_v) vs[1] = vs[0];
+                                else ok = ok && wait_stage(vs[t] = n++);
+                            }
+                            if (then) {
+                                if (t == 1 && same_k) ks[1] = ks[0];
+                                else ok = ok && wait_stage(ks[t] = n++);
+                            }
+                            if (mine && it.tail > 0 && i == it.tail_step && t == it.tail_tile) {
+                                if (ok && lane == 0) {
+                                    *tail_stage = vs[t] % C::STAGES;
+                                    mbar_arrive(b_tail);
+                                }
+                                ok = ok && warp_wait(b_fix, tails & 1, abort_f, p.status);
+                                tails++;
+                                tc_fence_after();
+                            }
                             if (ok && mine) {
                                 // the last item's outputs have been read
-                                if (!begun[t] && outs[t] > 0)
+                                if (i == 0 && outs[t] > 0)
                                     ok = warp_wait(&b_oe[t], (outs[t] - 1) & 1, abort_f, p.status);
                                 ok = ok && warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
                                 done_p[t]++;
@@ -454,44 +503,37 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 if (mine) {
                                     mma_output<D, IDESC_O>(tmem + TM_O + 128 * t,
                                                            tmem + TM_S + 128 * t,
-                                                           vd + stage_off(nv), begun[t]);
-                                    if (j == it.last[t]) tc_commit(&b_o[t]);
+                                                           vd + stage_off(vs[t]), i > 0);
+                                    if (last) tc_commit(&b_o[t]);
+                                    if (t == 1 || !same_v) tc_commit(&b_empty[vs[t] % C::STAGES]);
                                 }
-                                if (t == 1) tc_commit(&b_empty[nv % C::STAGES]);
                                 if (then) {
                                     mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
                                                            qd + ((t * C::TILE) >> 4),
-                                                           kd + stage_off(nk));
+                                                           kd + stage_off(ks[t]));
                                     tc_commit(&b_s[t]);
+                                    if (t == 1 || !same_k) tc_commit(&b_empty[ks[t] % C::STAGES]);
                                 }
+                                if (t == 1 && i + 2 == steps) tc_commit(&b_qe[qb]);  // the last scores
                             }
                             __syncwarp();
-                            begun[t] |= mine;
-                            if (mine && j == it.last[t]) outs[t]++;
+                            if (mine && last) outs[t]++;
                         }
-                        if (ok && more && elect_one()) {
-                            tc_commit(&b_empty[nk % C::STAGES]);
-                            if (j + 2 == it.count) tc_commit(&b_qe[qb]);  // the last scores
-                        }
-                        __syncwarp();
-                        now = next;
                     }
-                    ring0 += 2 * (uint32_t)it.count;
                 }
                 done_item(k);
             }
         } else if (warp == 2) {
             // zero the V rows behind the last key
-            uint32_t ring0 = 0, tails = 0;
+            uint32_t tails = 0;
             bool ok = true;
             Item it;
             for (int k = 0; ok && next_item(k, it); k++) {
-                ring0 += 2 * (uint32_t)it.count;
-                if (it.count > 0 && it.tail > 0) {
+                if (it.tail > 0) {
                     ok = warp_wait(b_tail, tails & 1, abort_f, p.status);
                     tails++;
                     if (!ok) break;
-                    uint8_t* v = sm + C::KV_OFF + ((ring0 - 1) % C::STAGES) * C::TILE;
+                    uint8_t* v = sm + C::KV_OFF + (uint32_t)uniform((int)*tail_stage) * C::TILE;
                     for (int x = lane; x < (it.tail_end - it.tail) * C::NB * 8; x += 32) {
                         const int r = it.tail + x / (C::NB * 8), piece = x % (C::NB * 8);
                         *reinterpret_cast<uint4*>(v + (piece / 8) * C::BLK + r * 128 +
@@ -511,12 +553,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = 0, asked = 0; ok && id >= 0;) {
                 if (lane == 0) take_over(response, b_clc);
                 int4 piece = make_int4(-1, 0, 0, 0);
-                if (lane < 3) piece = reinterpret_cast<const int4*>(p.items + id)[lane];
+                if (lane < 4) piece = reinterpret_cast<const int4*>(p.items + id)[lane];
                 if (uniform(piece.x) >= 0) {  // (grp, of lane 0's piece)
                     if (k >= ITEMS)
                         ok = warp_wait(&b_iteme[k % ITEMS], ((k / ITEMS) - 1) & 1, abort_f,
                                        p.status);
-                    if (ok && lane < 3) {
+                    if (ok && lane < 4) {
                         int* to = reinterpret_cast<int*>(&items[k % ITEMS]) + 4 * lane;
                         to[0] = piece.x;
                         to[1] = piece.y;
@@ -560,40 +602,34 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int count = max(0, min(p.TT, it.n - it.t0 - t * p.TT));  // tokens of the tile
             const bool live = tok < count;
             const bool idle = !__any_sync(0xffffffffu, live);
-            const int last = t ? it.last[1] : it.last[0];
+            const int steps = it.steps(t);
             const int pos = it.len - it.n + it.t0 + t * p.TT + tok;  // the last key it sees
             const int bit = live ? t * p.TT + tok : 0;
             const uint32_t* recs = records(it);
-            // The row's view of record j: the keys of the units that its token lists, up to its
-            // place; false if none of the tile's tokens lists any.
-            auto look = [&](int j, uint32_t (&vis)[4]) {
-                const uint32_t* rec = recs + (int64_t)j * p.rec_words;
+            // The row's view of step i: the keys of the units that its token lists, up to its place.
+            auto look = [&](int i, uint32_t (&vis)[4]) {
+                const uint32_t* rec = recs + (int64_t)it.record(t, i) * p.rec_words;
                 const uint32_t* mask = rec + nu + (bit >> 5);
-                uint32_t tiles = 0;
                 auto keys = [&](int unit, int off) {  // of a unit from key off on
-                    const uint32_t word = rec[unit];
-                    tiles |= word >> 30;
                     const bool mine = live && ((mask[unit * p.words] >> (bit & 31)) & 1);
-                    return low_bits(mine ? pos - (int)(word & ROW) - off + 1 : 0);
+                    return low_bits(mine ? pos - (int)rec[unit] - off + 1 : 0);
                 };
                 if (p.unit_shift >= 5) {
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int unit = (32 * i) >> p.unit_shift;
-                        vis[i] = keys(unit, 32 * i - (unit << p.unit_shift));
+                    for (int x = 0; x < 4; x++) {
+                        const int unit = (32 * x) >> p.unit_shift;
+                        vis[x] = keys(unit, 32 * x - (unit << p.unit_shift));
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        vis[i] = (keys(2 * i, 0) & 0xffffu) | keys(2 * i + 1, 0) << 16;
+                    for (int x = 0; x < 4; x++)
+                        vis[x] = (keys(2 * x, 0) & 0xffffu) | keys(2 * x + 1, 0) << 16;
                 }
-                return ((tiles >> t) & 1) != 0;
             };
             RowState st;
-            bool first = true;
-            for (int j = 0; j <= last; j++) {
+            for (int i = 0; i < steps; i++) {
                 uint32_t vis[4];
-                if (!look(j, vis)) continue;
+                look(i, vis);
                 ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
                 if (!ok) break;
                 ph++;
@@ -602,11 +638,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (idle) {
                     // none of the warp's rows exists: whatever its scores hold weighs no one
                 } else if (__all_sync(0xffffffffu, whole)) {
-                    softmax_block<D, false>(tm_s, tm_o, !first, vis, c, live, st);
+                    softmax_block<D, false>(tm_s, tm_o, i > 0, vis, c, live, st);
                 } else {
-                    softmax_block<D, true>(tm_s, tm_o, !first, vis, c, live, st);
+                    softmax_block<D, true>(tm_s, tm_o, i > 0, vis, c, live, st);
                 }
-                first = false;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_p[t]);
@@ -619,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t at = (int64_t)(it.q0 + it.t0 + t * p.TT + tok) * p.nh + head;
             if (live && p.lse) p.lse[at] = end.lse;
             if (count > 0) {
-                const bool any = last >= 0;
+                const bool any = steps > 0;
                 if (any) {
                     ok = warp_wait(&b_o[t], outs & 1, abort_f, p.status);
                     if (!ok) break;
@@ -678,8 +713,8 @@ Plan make_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_k, int64_t topk
     const int64_t toks = 2 * pl.TT < max_q ? 2 * pl.TT : max_q;
     int64_t blocks = (max_k + block - 1) / block;
     if (toks * topk < blocks) blocks = toks * topk;
-    pl.max_rec = (int)((blocks * (block / unit) + nu - 1) / nu);
-    if (pl.max_rec < 1) pl.max_rec = 1;
+    // (three kinds of them, each with a record that is not full)
+    pl.max_rec = (int)((blocks * (block / unit) + nu - 1) / nu) + 2;
     // every sequence has at most one pair of tiles that is not full
     pl.items = (Tq / (2 * pl.TT) + B) * kvh * pl.subs;
     pl.items_bytes = (size_t)pl.items * sizeof(Item);

@@ -33,8 +33,16 @@ __device__ __forceinline__ float int8_row(const float (&x)[4], bool mine, float 
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     bad = __any_sync(0xffffffffu, bad && mine);
     const float s = __fmul_rn(fmaxf(m, FLOOR), STEP);
+    // x / s, correctly rounded, from the correctly rounded reciprocal and the exact remainder of
+    // a fused multiply-add (P. Markstein, 1990).  A scale below 2^-90 and its row are taken
+    // 2^100 times, one above 2^100 and its row 2^-60 times: all of it stays normal.
+    const float f = s < 0x1p-90f ? 0x1p100f : s > 0x1p100f ? 0x1p-60f : 1.0f;
+    const float d = s * f, r = __frcp_rn(d);
 #pragma unroll
-    for (int e = 0; e < 4; e++) code[e] = bad ? 0.0f : rintf(__fdiv_rn(x[e], s));
+    for (int e = 0; e < 4; e++) {
+        const float y = x[e] * f, q = __fmul_rn(y, r);
+        code[e] = bad ? 0.0f : rintf(__fmaf_rn(__fmaf_rn(q, -d, y), r, q));
+    }
     return bad ? __uint_as_float(0x7fc00000u) : s;
 }
 
@@ -51,7 +59,7 @@ struct KeyArgs {
 
 constexpr int KEY_WARPS = 4;
 
-// A warp for a page and head, four elements a lane, sixteen rows in flight.
+// A warp for a page and head, four elements a lane, 16 rows (32 of codes) in flight.
 template <bool E4M3>
 __global__ void __launch_bounds__(KEY_WARPS * 32) keys_kernel(const KeyArgs a) {
     pdl_wait();
@@ -80,34 +88,30 @@ __global__ void __launch_bounds__(KEY_WARPS * 32) keys_kernel(const KeyArgs a) {
         const uint8_t* p = a.kv.k + (row * a.kv.hd + (mine ? lane * 4 : 0)) * (E4M3 ? 1 : 2);
         const int step = a.kv.hd * (E4M3 ? 1 : 2);
         float sum[4] = {0, 0, 0, 0};
-        constexpr int U = 16;
+        constexpr int U = E4M3 ? 32 : 16;
         for (int r0 = 0; r0 < n; r0 += U) {
             uint2 w[U];
-            float s[U];
+            // (rows behind the last are that one once more: no load waits for a branch)
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                w[u] = make_uint2(0, 0);
-                s[u] = 0.0f;
-                if (r0 + u >= n) continue;
-                if (E4M3) {
-                    w[u].x = __ldcs(reinterpret_cast<const uint32_t*>(p + (r0 + u) * step));
-                    s[u] = a.kv.ks[row + r0 + u];
-                } else {
-                    w[u] = __ldcs(reinterpret_cast<const uint2*>(p + (r0 + u) * step));
-                }
+                const uint8_t* at = p + min(r0 + u, n - 1) * step;
+                if (E4M3) w[u].x = __ldcs(reinterpret_cast<const uint32_t*>(at));
+                else w[u] = __ldcs(reinterpret_cast<const uint2*>(at));
             }
+            const float scale = E4M3 ? a.kv.ks[row + min(r0 + lane, n - 1)] : 0.0f;
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 float x[4];
                 if (E4M3) {
+                    const float s = __shfl_sync(0xffffffffu, scale, u);
                     uint32_t lo, hi;
                     e4m3x4_to_f16(w[u].x, lo, hi);
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&lo));
                     const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                    x[0] = __fmul_rn(f.x, s[u]);
-                    x[1] = __fmul_rn(f.y, s[u]);
-                    x[2] = __fmul_rn(g.x, s[u]);
-                    x[3] = __fmul_rn(g.y, s[u]);
+                    x[0] = __fmul_rn(f.x, s);
+                    x[1] = __fmul_rn(f.y, s);
+                    x[2] = __fmul_rn(g.x, s);
+                    x[3] = __fmul_rn(g.y, s);
                 } else {
                     x[0] = __uint_as_float(w[u].x << 16);
                     x[1] = __uint_as_float(w[u].x & 0xffff0000u);
@@ -145,7 +149,7 @@ struct SelectArgs {
     int64_t Tq, n_pages, max_pages;
     int page, page_shift, kvh, hd, G, max_q, max_len, topk, first, local;
     int TT;       // tokens of a CTA
-    int NB;       // room for blocks
+    int NB;       // room for a token's scores: tokens next to each other in different banks
     int heads;    // query heads at a time, even
     unsigned int* status;
 };
@@ -169,13 +173,96 @@ __device__ __forceinline__ uint32_t rank_of(float s) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+// the score of a rank that is neither 0 nor the largest
+__device__ __forceinline__ float score_of(uint32_t rank) {
+    return __uint_as_float((rank >> 31) ? rank ^ 0x80000000u : ~rank);
+}
+
+// A warp: the k of m > k ranks at s, ties to the first, ascending to out as j0 + place.  The
+// k-th largest is found by halving what lies between the smallest rank and the largest:
+// first as scores, which lie evenly enough for about ten counts of all ranks (as integers,
+// bit by bit, it is 30), and as integers if that has not ended it.  R: registers of a lane,
+// 32 R ranks at most; 0: the ranks stay in shared memory.
+template <int R>
+__device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* out, int j0,
+                                     int lane) {
+    constexpr int N = R ? R : 1;
+    uint32_t v[N];
+    uint32_t lo = 0xffffffffu, hi = 0;
+    if (R) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const bool in = 32 * i + lane < m;
+            v[i] = in ? s[32 * i + lane] : 0;
+            lo = min(lo, in ? v[i] : 0xffffffffu);
+            hi = max(hi, v[i]);
+        }
+    } else {
+        for (int j = lane; j < m; j += 32) {
+            lo = min(lo, s[j]);
+            hi = max(hi, s[j]);
+        }
+    }
+    auto count = [&](uint32_t least) {
+        int n = 0;
+        if (R) {
+#pragma unroll
+            for (int i = 0; i < N; i++) n += v[i] >= least;
+        } else {
+#pragma unroll 8
+            for (int j = lane; j < m; j += 32) n += s[j] >= least;
+        }
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    // more than k ranks from lo on, at most k from hi on: `above`
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+    int above = 0;
+    for (int i = 0; above < k && hi - lo > 1; i++) {
+        uint32_t mid = lo + (hi - lo) / 2;
+        if (i < 16) {
+            const uint32_t x = rank_of(0.5f * score_of(lo) + 0.5f * score_of(hi));
+            if (x > lo && x < hi) mid = x;
+        }
+        const int n = count(mid);
+        if (n > k) {
+            lo = mid;
+        } else {
+            hi = mid;
+            above = n;
+        }
+    }
+    // all from hi on, and the first of those equal to lo
+    int ties = k - above, at = 0;
+    const uint32_t below = (1u << lane) - 1u;
+    auto put = [&](uint32_t x, int j) {
+        bool take = x >= hi;
+        if (ties > 0) {
+            const uint32_t eq = __ballot_sync(0xffffffffu, x == lo && j < m);
+            take |= x == lo && j < m && __popc(eq & below) < ties;
+            ties -= min(ties, __popc(eq));
+        }
+        const uint32_t all = __ballot_sync(0xffffffffu, take);
+        if (take) out[at + __popc(all & below)] = j0 + j;
+        at += __popc(all);
+    };
+    if (R) {
+#pragma unroll
+        for (int i = 0; i < N; i++) put(v[i], 32 * i + lane);
+    } else {
+        for (int j = 0; j < m; j += 32) put(j + lane < m ? s[j + lane] : 0, j + lane);
+    }
+}
+
 // Scores of TT tokens of a sequence for one key/value head, then the tokens' picks.
 // Products: 16 blocks (rows, codes straight from global memory into the fragments) by 8
 // columns; column 2 t + e of tile (quad, i) is token 4 quad + t, head 2 i + e, so that a lane
 // has all heads of its token and their maximum takes no exchange.  hd in the order of tree
 // attention's e4m3 fragments: lane c owns the codes 16 c .. and 64 + 16 c .. of a row.
-template <int HD>
-__global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs a) {
+// FEW: a few tokens, one CTA an SM or so: the next blocks' codes are under way while the products
+// of these run.  Else four CTAs an SM hide that.
+template <int HD, bool FEW>
+__global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(const SelectArgs a) {
     pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(16) uint8_t smem[];
@@ -230,27 +317,56 @@ __global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs
             if (lane == 0) qs[t * a.heads + y] = real ? s : __uint_as_float(0x7fc00000u);
         }
         __syncthreads();
-        for (int j0 = warp * 16; j0 < vis; j0 += SEL_WARPS * 16) {
-            uint32_t af[KS][4];
-            float ks[2];
+        // rows g and g + 8 of 16 blocks: pages a round ahead of codes
+        int page[2];
+        uint4 raw[2][KS / 4];
+        float scale[2];
+        auto look = [&](int j0) {
+#pragma unroll
+            for (int r = 0; r < 2; r++) page[r] = j0 + g + 8 * r < vis ? table[j0 + g + 8 * r] : 0;
+        };
+        auto fetch = [&] {
 #pragma unroll
             for (int r = 0; r < 2; r++) {
-                const int j = j0 + g + 8 * r;
-                int64_t pg = j < vis ? table[j] : 0;
-                const bool ok = pg >= 0 && pg < a.n_pages;
+                const bool ok = page[r] >= 0 && page[r] < a.n_pages;
                 if (!ok && c == 0) raise_status(a.status, DS41_E_INDEX);
-                const int64_t at = (ok ? pg : 0) * a.kvh + h;
-                ks[r] = ok ? a.scales[at] : __uint_as_float(0x7fc00000u);
+                const int64_t at = (int64_t)(ok ? page[r] : 0) * a.kvh + h;
+                scale[r] = ok ? a.scales[at] : __uint_as_float(0x7fc00000u);
 #pragma unroll
                 for (int x = 0; x < KS / 4; x++) {
-                    uint4 w = make_uint4(0, 0, 0, 0);
+                    raw[r][x] = make_uint4(0, 0, 0, 0);
                     if ((c + 4 * x) * 16 < a.hd && ok)
-                        w = *reinterpret_cast<const uint4*>(a.codes + at * a.hd + (c + 4 * x) * 16);
+                        raw[r][x] =
+                            *reinterpret_cast<const uint4*>(a.codes + at * a.hd + (c + 4 * x) * 16);
+                }
+            }
+        };
+        constexpr int ROUND = SEL_WARPS * 16;
+        look(warp * 16);
+        if (FEW) {
+            fetch();
+            look(warp * 16 + ROUND);
+        }
+        for (int j0 = warp * 16; j0 < vis; j0 += ROUND) {
+            uint32_t af[KS][4];
+            if (!FEW) {
+                fetch();
+                look(j0 + ROUND);
+            }
+            const float ks[2] = {scale[0], scale[1]};
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int x = 0; x < KS / 4; x++) {
+                    const uint4 w = raw[r][x];
                     int8x4_to_f16(w.x, af[4 * x][r], af[4 * x][r + 2]);
                     int8x4_to_f16(w.y, af[4 * x + 1][r], af[4 * x + 1][r + 2]);
                     int8x4_to_f16(w.z, af[4 * x + 2][r], af[4 * x + 2][r + 2]);
                     int8x4_to_f16(w.w, af[4 * x + 3][r], af[4 * x + 3][r + 2]);
                 }
+            if (FEW) {
+                fetch();
+                look(j0 + 2 * ROUND);
             }
             for (int qd = 0; qd < quads; qd++) {
                 const int t = qd * 4 + c;
@@ -270,7 +386,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs
                 if (t < toks)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
-                        const int j = j0 + g + 8 * r, cur = (p0 + t) >> a.page_shift;
+                        const int j = j0 + g + 8 * r;
                         if (j >= vis) continue;
                         uint32_t* to = sc + t * a.NB + j;
                         float s = best[r];
@@ -279,10 +395,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs
                             *to = __float_as_uint(s);
                             continue;
                         }
-                        // 0: out of sight; the largest: taken in any case
-                        *to = j > cur                                 ? 0u
-                              : j < a.first || j > cur - a.local ? 0xffffffffu
-                                                                 : rank_of(__fmul_rn(s, ks[r]));
+                        *to = rank_of(__fmul_rn(s, ks[r]));
                     }
             }
         }
@@ -291,40 +404,26 @@ __global__ void __launch_bounds__(SEL_WARPS * 32) select_kernel(const SelectArgs
     // ---- the picks: a warp for a token ----
     for (int t = warp; t < toks; t += SEL_WARPS) {
         const uint32_t* s = sc + t * a.NB;
-        const int m = ((p0 + t) >> a.page_shift) + 1;  // blocks that it sees
+        const int cur = (p0 + t) >> a.page_shift;
         int32_t* out = a.idx + ((int64_t)(q0 + t0 + t) * a.kvh + h) * a.topk;
-        uint32_t least = 1;  // what is picked is at least this
-        int ties = m;        // of those equal to it, the first ones
-        if (m > a.topk) {
-            // the topk-th largest, bit by bit
-            least = 0;
-            int count = m;
-            for (int bit = 31; bit >= 0 && count != a.topk; bit--) {
-                const uint32_t to = least | (1u << bit);
-                int k = 0;
-                for (int j = lane; j < m; j += 32) k += s[j] >= to;
-                k = __reduce_add_sync(0xffffffffu, k);
-                if (k >= a.topk) {
-                    least = to;
-                    count = k;
-                }
-            }
-            int above = 0;
-            for (int j = lane; j < m; j += 32) above += s[j] > least;
-            ties = a.topk - __reduce_add_sync(0xffffffffu, above);
+        // all that it sees, or the first and the last ones and what is picked in between
+        if (cur < a.topk) {
+            for (int j = lane; j < a.topk; j += 32) out[j] = j <= cur ? j : -1;
+            continue;
         }
-        int at = 0;
-        const uint32_t below = (1u << lane) - 1u;
-        for (int j0 = 0; j0 < m; j0 += 32) {
-            const uint32_t v = j0 + lane < m ? s[j0 + lane] : 0;
-            const uint32_t eq = __ballot_sync(0xffffffffu, v == least && v != 0);
-            const bool take = v > least || (v == least && v != 0 && __popc(eq & below) < ties);
-            const uint32_t all = __ballot_sync(0xffffffffu, take);
-            if (take) out[at + __popc(all & below)] = j0 + lane;
-            at += __popc(all);
-            ties -= min(ties, __popc(eq));
+        const int k = a.topk - a.first - a.local, m = cur + 1 - a.first - a.local;
+        for (int j = lane; j < a.first; j += 32) out[j] = j;
+        for (int j = lane; j < a.local; j += 32) out[a.first + k + j] = a.first + m + j;
+        s += a.first;
+        out += a.first;
+        if (k == 0) continue;
+        if (m <= 256) {
+            pick<8>(s, m, k, out, a.first, lane);
+        } else if (m <= 512) {
+            pick<16>(s, m, k, out, a.first, lane);
+        } else {
+            pick<0>(s, m, k, out, a.first, lane);
         }
-        for (int j = at + lane; j < a.topk; j += 32) out[j] = -1;
     }
 }
 
@@ -432,10 +531,9 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
     a.first = (int)first;
     a.local = (int)local;
     if (int rc = status_word(&a.status)) return rc;
-    // Tokens of a CTA: 32, or what their scores leave room for (two CTAs an SM), or all;
-    // query heads at a time: a group, or 32 of it.
-    a.NB = (int)((max_len + page - 1) / page);
-    if (a.NB < 1) a.NB = 1;
+    // Tokens of a CTA: 32, or what their scores leave room for (four CTAs an SM, two of few
+    // tokens), or all; query heads at a time: a group, or 32 of it.
+    a.NB = (int)((max_len + page - 1) / page + 31) / 32 * 32 + 8;
     a.heads = a.G >= 32 ? 32 : (a.G + 1) / 2 * 2;
     const int HD = hd <= 64 ? 64 : 128;
     auto bytes = [&](int tt) {
@@ -443,12 +541,19 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
         return (size_t)quads * (a.heads / 2) * (HD / 16) * 256 + (size_t)quads * 16 * a.heads +
                (size_t)tt * a.NB * 4;
     };
+    const bool few = a.max_q <= 4;
     a.TT = a.max_q < 32 ? a.max_q : 32;
-    while (a.TT > 1 && bytes(a.TT) > 100 * 1024) a.TT = a.TT > 4 ? (a.TT - 1) / 4 * 4 : a.TT - 1;
+    while (a.TT > 1 && bytes(a.TT) > (few ? 110 : 55) * 1024)
+        a.TT = a.TT > 4 ? (a.TT - 1) / 4 * 4 : a.TT - 1;
     const size_t smem = bytes(a.TT);
-    auto kern = HD == 64 ? blocks::select_kernel<64> : blocks::select_kernel<128>;
-    if (int rc = HD == 64 ? allow_smem<blocks::select_kernel<64>>(224 * 1024, name)
-                          : allow_smem<blocks::select_kernel<128>>(224 * 1024, name))
+    constexpr int MOST = 224 * 1024;
+    auto kern = HD == 64 ? (few ? blocks::select_kernel<64, true> : blocks::select_kernel<64, false>)
+                         : (few ? blocks::select_kernel<128, true>
+                                : blocks::select_kernel<128, false>);
+    if (int rc = HD == 64 ? (few ? allow_smem<blocks::select_kernel<64, true>>(MOST, name)
+                                 : allow_smem<blocks::select_kernel<64, false>>(MOST, name))
+                          : (few ? allow_smem<blocks::select_kernel<128, true>>(MOST, name)
+                                 : allow_smem<blocks::select_kernel<128, false>>(MOST, name)))
         return rc;
     return launch_pdl(kern,
                       dim3((unsigned)((a.max_q + a.TT - 1) / a.TT), (unsigned)B, (unsigned)kvh),
