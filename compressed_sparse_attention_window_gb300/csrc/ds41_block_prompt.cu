@@ -52,7 +52,7 @@ static_assert(sizeof(Item) == 64, "four 16-byte pieces");
 
 constexpr uint32_t ROW = 0x3fffffffu;  // a unit's word: its first row; this: none
 constexpr int PLAN = 256;              // threads of plan_kernel
-constexpr int TABLE = 8192;            // words of its table
+constexpr int TABLE = 8192;            // words of its table, at most
 
 struct Params {
     const int32_t* cu_q;
@@ -63,10 +63,12 @@ struct Params {
     float* lse;
     int64_t Tq, Tk;
     int B, max_q, max_k, nh, kvh, hd, topk;
-    int G, TT, n_groups, subs;
+    int G, TT, subs;
+    int pairs;              // of tiles, at most
     int shift, unit_shift;  // log2 of a block's keys, of a unit's
     int words;              // of a unit's mask: 2 TT tokens
     int rec_words, max_rec;
+    int table;              // words of plan_kernel's
     float c;
     Item* items;
     uint32_t* recs;         // [item][max_rec][rec_words]: the units' words, their masks
@@ -98,11 +100,13 @@ __device__ __forceinline__ int prefix(int v, int* sh, int& sum) {
 __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     pdl_wait();
     pdl_trigger();
-    __shared__ uint32_t table[TABLE];
+    extern __shared__ uint32_t table[];
     __shared__ int end[256], sh[PLAN / 32], units_of[3];  // (both tiles', tile 0's, tile 1's)
     __shared__ __align__(16) Item it;
     const int tid = threadIdx.x, id = blockIdx.x;
-    const int w = id / p.n_groups, grp = id - w * p.n_groups, h = grp / p.subs;
+    // (head group by head group: what is under way at a time reads the keys of one or two, which
+    // the L2 holds)
+    const int grp = id / p.pairs, w = id - grp * p.pairs, h = grp / p.subs;
     if (tid == 0) {
         it = Item{};
         it.grp = -1;
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     }
     __syncthreads();
     const int blocks = ((p0 + toks - 1) >> p.shift) + 1, W = p.words;
-    const int range = TABLE / W;
+    const int range = p.table / W;
     const int per = 1 << (p.shift - p.unit_shift), nu = KB >> p.unit_shift;
     uint32_t* recs = p.recs + (int64_t)id * p.max_rec * p.rec_words;
     // once to count the units of each kind, once to put them into their records
@@ -243,6 +247,55 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     __syncthreads();
     if (tid < 4)
         reinterpret_cast<int4*>(p.items + id)[tid] = reinterpret_cast<const int4*>(&it)[tid];
+}
+
+// One thread's row of 128 scores, as softmax_block, where each word of 32 keys is seen whole or
+// not at all (all but a row's own block and blocks of 16): the word's maximum and sum count
+// or not, and its weights are kept or cleared, whatever its scores hold.  (Key by key, as
+// softmax_block masks, a block takes twice the instructions; with a branch around each word that
+// no row of the warp sees it was slower than that.)
+template <int D>
+__device__ __forceinline__ void softmax_words(uint32_t tm_s, uint32_t tm_o, bool have_o,
+                                              const uint32_t (&vis)[4], float c, bool live,
+                                              RowState& st) {
+    uint32_t s[4][32];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 4; i++) top = fmaxf(top, vis[i] ? max32(s[i]) : -INFINITY);
+    // (-inf - -inf is NaN: no move)
+    const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
+    if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? ex2((st.m - top) * c) : 1.0f;
+        if (move) st.m = top;
+        st.l *= f;
+        if (have_o) rescale<D>(tm_o, f);
+    }
+    float base = st.m == -INFINITY ? 0.0f : st.m * c;
+    if (fabsf(base) > 0x1p22f) {
+        // c m itself is rounded by more than a fraction of one power of two: take
+        // the differences first
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        base = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t pk[16];
+        uint64_t part[2] = {0, 0};
+        weights32<false, false>(s[i], pk, c, base, nullptr, 0, part);
+        float x, y;
+        unf2(add2(part[0], part[1]), x, y);
+        st.l += vis[i] ? x + y : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; e++) pk[e] &= vis[i];
+        tc_st16(tm_s + 16 * i, pk);
+    }
+    tc_wait_st();
 }
 
 template <int D>
@@ -458,67 +511,99 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool ok = true;
             Item it;
             for (int k = 0; ok && next_item(k, it); k++) {
-                const int steps = it.steps();
-                if (steps > 0) {
+                const int both = it.both, own0 = it.own[0], own1 = it.own[1];
+                if (both + own0 + own1 > 0) {
                     const int qb = nq % C::QB;
                     const uint32_t qd = desc_lo(sbase + C::Q_OFF + 2 * qb * C::TILE, 16);
                     ok = warp_wait(&b_q[qb], (nq / C::QB) & 1, abort_f, p.status);
                     nq++;
-                    uint32_t vs[2] = {0, 0}, ks[2] = {0, 0};  // stages
-                    for (int i = -1; i < steps && ok; i++) {
-#pragma unroll
-                        for (int t = 0; t < 2; t++) {
-                            const bool mine = i >= 0 && i < it.steps(t);
-                            const bool then = i + 1 < it.steps(t);
-                            const bool same_v = i < it.both, same_k = i + 1 < it.both;
-                            const bool last = i + 1 == it.steps(t);
-                            // (both before the wait for the weights: nothing stands between
-                            // their arrival and the products)
-                            if (mine) {
-                                if (t == 1 && same_v) vs[1] = vs[0];
-                                else ok = ok && wait_stage(vs[t] = n++);
+                    // Tile t's scores on stage k.  (free: nobody else reads the stage)
+                    auto scores = [&](int t, uint32_t k, bool free) {
+                        mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t, qd + ((t * C::TILE) >> 4),
+                                               kd + stage_off(k));
+                        tc_commit(&b_s[t]);
+                        if (free) tc_commit(&b_empty[k % C::STAGES]);
+                    };
+                    // Tile t's step i: the output on stage v (if mine), then the next scores on
+                    // stage k (if then).
+                    // (late: nobody has waited for that stage yet)
+                    auto step = [&](int t, int i, bool mine, uint32_t v, bool free_v, bool last,
+                                    bool then, uint32_t k, bool free_k, bool end, bool late) {
+                        if (ok && mine && it.tail > 0 && i == it.tail_step && t == it.tail_tile) {
+                            if (lane == 0) {
+                                *tail_stage = v % C::STAGES;
+                                mbar_arrive(b_tail);
                             }
-                            if (then) {
-                                if (t == 1 && same_k) ks[1] = ks[0];
-                                else ok = ok && wait_stage(ks[t] = n++);
-                            }
-                            if (mine && it.tail > 0 && i == it.tail_step && t == it.tail_tile) {
-                                if (ok && lane == 0) {
-                                    *tail_stage = vs[t] % C::STAGES;
-                                    mbar_arrive(b_tail);
-                                }
-                                ok = ok && warp_wait(b_fix, tails & 1, abort_f, p.status);
-                                tails++;
-                                tc_fence_after();
-                            }
-                            if (ok && mine) {
-                                // the last item's outputs have been read
-                                if (i == 0 && outs[t] > 0)
-                                    ok = warp_wait(&b_oe[t], (outs[t] - 1) & 1, abort_f, p.status);
-                                ok = ok && warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
-                                done_p[t]++;
-                                tc_fence_after();
-                            }
-                            if (ok && elect_one()) {
-                                if (mine) {
-                                    mma_output<D, IDESC_O>(tmem + TM_O + 128 * t,
-                                                           tmem + TM_S + 128 * t,
-                                                           vd + stage_off(vs[t]), i > 0);
-                                    if (last) tc_commit(&b_o[t]);
-                                    if (t == 1 || !same_v) tc_commit(&b_empty[vs[t] % C::STAGES]);
-                                }
-                                if (then) {
-                                    mma_scores<D, IDESC_S>(tmem + TM_S + 128 * t,
-                                                           qd + ((t * C::TILE) >> 4),
-                                                           kd + stage_off(ks[t]));
-                                    tc_commit(&b_s[t]);
-                                    if (t == 1 || !same_k) tc_commit(&b_empty[ks[t] % C::STAGES]);
-                                }
-                                if (t == 1 && i + 2 == steps) tc_commit(&b_qe[qb]);  // the last scores
-                            }
-                            __syncwarp();
-                            if (mine && last) outs[t]++;
+                            ok = warp_wait(b_fix, tails & 1, abort_f, p.status);
+                            tails++;
+                            tc_fence_after();
                         }
+                        if (ok && mine) {
+                            // the last item's outputs have been read
+                            if (i == 0 && outs[t] > 0)
+                                ok = warp_wait(&b_oe[t], (outs[t] - 1) & 1, abort_f, p.status);
+                            ok = ok && warp_wait(&b_p[t], done_p[t] & 1, abort_f, p.status);
+                            done_p[t]++;
+                            tc_fence_after();
+                        }
+                        if (ok && elect_one()) {
+                            if (mine) {
+                                mma_output<D, IDESC_O>(tmem + TM_O + 128 * t, tmem + TM_S + 128 * t,
+                                                       vd + stage_off(v), i > 0);
+                                if (last) tc_commit(&b_o[t]);
+                                if (free_v) tc_commit(&b_empty[v % C::STAGES]);
+                            }
+                        }
+                        __syncwarp();
+                        if (ok && late && then) ok = wait_stage(k);
+                        if (ok && elect_one()) {
+                            if (then) scores(t, k, free_k);
+                            if (end) tc_commit(&b_qe[qb]);  // the last scores
+                        }
+                        __syncwarp();
+                        if (mine && last) outs[t]++;
+                    };
+                    // the first scores
+                    const bool any0 = own0 > 0, any1 = own1 > 0;
+                    if (both > 0) {
+                        ok = ok && wait_stage(n);
+                        if (ok && elect_one()) {
+                            scores(0, n, false);
+                            scores(1, n, true);
+                        }
+                    } else {
+                        ok = ok && (!any0 || wait_stage(n)) && (!any1 || wait_stage(n + any0));
+                        if (ok && elect_one()) {
+                            if (any0) scores(0, n, true);
+                            if (any1) scores(1, n + any0, true);
+                        }
+                    }
+                    const int steps = it.steps();
+                    if (ok && steps == 1 && elect_one()) tc_commit(&b_qe[qb]);
+                    __syncwarp();
+                    // (stages are waited for before the weights: nothing stands between their
+                    // arrival and the products.  Their numbers follow from the step's.)
+                    for (int i = 0; i < both && ok; i++) {
+                        const bool more = i + 1 < both;
+                        const uint32_t v = n + 2 * i + 1, k0 = v + 1, k1 = more ? k0 : k0 + any0;
+                        ok = wait_stage(v) && (!(more || any0) || wait_stage(k0)) &&
+                             (more || !any1 || wait_stage(k1));
+                        step(0, i, true, v, false, !more && !any0, more || any0, k0, !more, false,
+                             false);
+                        step(1, i, true, v, true, !more && !any1, more || any1, k1, true,
+                             i + 2 == steps, false);
+                    }
+                    n += 2 * both + any0 + any1;
+                    for (int m = 0; m + both < steps && ok; m++) {
+                        const bool a0 = m < own0, c0 = m + 1 < own0;
+                        const bool a1 = m < own1, c1 = m + 1 < own1;
+                        const uint32_t k0 = n + a0, v1 = k0 + c0, k1 = v1 + a1;
+                        const int i = both + m;
+                        ok = !a0 || wait_stage(n);
+                        step(0, i, a0, n, true, !c0, c0, k0, true, false, true);
+                        ok = ok && (!a1 || wait_stage(v1));
+                        step(1, i, a1, v1, true, !c1, c1, k1, true, i + 2 == steps, true);
+                        n = k1 + c1;
                     }
                 }
                 done_item(k);
@@ -605,14 +690,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int steps = it.steps(t);
             const int pos = it.len - it.n + it.t0 + t * p.TT + tok;  // the last key it sees
             const int bit = live ? t * p.TT + tok : 0;
-            const uint32_t* recs = records(it);
-            // The row's view of step i: the keys of the units that its token lists, up to its place.
-            auto look = [&](int i, uint32_t (&vis)[4]) {
-                const uint32_t* rec = recs + (int64_t)it.record(t, i) * p.rec_words;
-                const uint32_t* mask = rec + nu + (bit >> 5);
+            // Step i's record, a word a lane (a step ahead; longer ones are read when wanted).
+            const bool held = p.rec_words <= 32;
+            auto fetch = [&](int i) {
+                return held && i < steps && lane < p.rec_words
+                           ? records(it)[(int64_t)it.record(t, i) * p.rec_words + lane]
+                           : 0u;
+            };
+            // The row's view of it: the keys of the units that its token lists, up to its place.
+            auto look = [&](int i, uint32_t word, uint32_t (&vis)[4]) {
+                const uint32_t* rec = records(it) + (int64_t)it.record(t, i) * p.rec_words;
+                auto at = [&](int x) { return held ? __shfl_sync(0xffffffffu, word, x) : rec[x]; };
                 auto keys = [&](int unit, int off) {  // of a unit from key off on
-                    const bool mine = live && ((mask[unit * p.words] >> (bit & 31)) & 1);
-                    return low_bits(mine ? pos - (int)rec[unit] - off + 1 : 0);
+                    const uint32_t mask = at(nu + unit * p.words + (bit >> 5));
+                    const int n = pos - (int)at(unit) - off + 1;
+                    return low_bits(live && ((mask >> (bit & 31)) & 1) ? n : 0);
                 };
                 if (p.unit_shift >= 5) {
 #pragma unroll
@@ -626,19 +718,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                         vis[x] = (keys(2 * x, 0) & 0xffffu) | keys(2 * x + 1, 0) << 16;
                 }
             };
+            uint32_t word = fetch(0);
             RowState st;
             for (int i = 0; i < steps; i++) {
                 uint32_t vis[4];
-                look(i, vis);
+                look(i, word, vis);
+                word = fetch(i + 1);
+                const bool words = !__any_sync(  // (a word is 0 or all ones)
+                    0xffffffffu, vis[0] + 1 > 1 || vis[1] + 1 > 1 || vis[2] + 1 > 1 ||
+                                     vis[3] + 1 > 1);
                 ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
                 if (!ok) break;
                 ph++;
                 tc_fence_after();
-                const bool whole = (vis[0] & vis[1] & vis[2] & vis[3]) == 0xffffffffu;
                 if (idle) {
                     // none of the warp's rows exists: whatever its scores hold weighs no one
-                } else if (__all_sync(0xffffffffu, whole)) {
-                    softmax_block<D, false>(tm_s, tm_o, i > 0, vis, c, live, st);
+                } else if (words) {
+                    softmax_words<D>(tm_s, tm_o, i > 0, vis, c, live, st);
                 } else {
                     softmax_block<D, true>(tm_s, tm_o, i > 0, vis, c, live, st);
                 }
@@ -800,7 +896,7 @@ extern "C" int ds41_block_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int
     p.G = pl.G;
     p.TT = pl.TT;
     p.subs = pl.subs;
-    p.n_groups = (int)kvh * pl.subs;
+    p.pairs = (int)(pl.items / (kvh * pl.subs));
     while ((1 << p.shift) < block) p.shift++;
     p.unit_shift = pl.unit_shift;
     p.words = pl.words;
@@ -823,7 +919,11 @@ extern "C" int ds41_block_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int
     }
     cudaStream_t st = (cudaStream_t)stream;
     const dim3 grid((unsigned)pl.items);
-    if (int rc = launch_pdl(bp::plan_kernel, grid, dim3(bp::PLAN), 0, st, name, p)) return rc;
+    // (no larger than the blocks need: more CTAs fit an SM)
+    const int64_t words = ((max_k + block - 1) / block) * pl.words;
+    p.table = (int)(words < bp::TABLE ? (words > 0 ? words : pl.words) : bp::TABLE);
+    if (int rc = launch_pdl(bp::plan_kernel, grid, dim3(bp::PLAN), (size_t)p.table * 4, st, name, p))
+        return rc;
     auto kern = hd <= 64 ? bp::block_prompt_kernel<64> : bp::block_prompt_kernel<128>;
     const size_t smem = hd <= 64 ? pa::Cfg<64>::SMEM : pa::Cfg<128>::SMEM;
     if (int rc = hd <= 64 ? allow_smem<bp::block_prompt_kernel<64>>((int)smem, name)
