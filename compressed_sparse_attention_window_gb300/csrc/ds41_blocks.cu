@@ -20,18 +20,15 @@ namespace blocks {
 constexpr float STEP = 1.0f / 127.0f;
 constexpr float FLOOR = 127.0f * 0x1p-126f;
 
-// Four elements of a row a lane (of hd of them, 0 behind): codes in a word, the row's scale.
-__device__ __forceinline__ float int8_row(const float (&x)[4], bool mine, float (&code)[4]) {
-    float m = 0.0f;
-    bool bad = false;
+// Four elements of a row a lane (0 behind its end): their codes, and the row's scale.
+__device__ __forceinline__ float int8_row(const float (&x)[4], float (&code)[4]) {
+    // (the bits of magnitudes are ordered as they are, infinities and NaN above all)
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        m = fmaxf(m, fabsf(x[e]));
-        bad |= !(fabsf(x[e]) < INFINITY);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    bad = __any_sync(0xffffffffu, bad && mine);
+    for (int e = 0; e < 4; e++) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool bad = top >= 0x7f800000u;
+    const float m = __uint_as_float(top);
     const float s = __fmul_rn(fmaxf(m, FLOOR), STEP);
     // x / s, correctly rounded, from the correctly rounded reciprocal and the exact remainder of
     // a fused multiply-add (P. Markstein, 1990).  A scale below 2^-90 and its row are taken
@@ -126,7 +123,7 @@ __global__ void __launch_bounds__(KEY_WARPS * 32) keys_kernel(const KeyArgs a) {
         float code[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) sum[e] = mine ? __fdiv_rn(sum[e], (float)n) : 0.0f;
-        const float s = int8_row(sum, mine, code);
+        const float s = int8_row(sum, code);
         if (mine) {
             uint32_t c = 0;
 #pragma unroll
@@ -284,39 +281,13 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
     const int vis = ((p0 + toks - 1) >> a.page_shift) + 1;  // blocks that some token sees
     // shared memory: the queries' fragments, their scales, the scores
     const int pairs = a.heads / 2;
-    uint2* frag = reinterpret_cast<uint2*>(smem);  // [quad][pair][k step][32]
+    uint2* frag = reinterpret_cast<uint2*>(smem);  // [quad][pair][two k steps][32][2]
     float* qs = reinterpret_cast<float*>(frag + (a.TT + 3) / 4 * pairs * KS * 32);  // [token][heads]
     uint32_t* sc = reinterpret_cast<uint32_t*>(qs + (a.TT + 3) / 4 * 4 * a.heads);  // [token][NB]
     const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
     for (int h0 = 0; h0 < a.G; h0 += a.heads) {
         const int hs = min(a.heads, a.G - h0), hp = (hs + 1) / 2;
-        for (int x = warp; x < quads * 4 * hp * 2; x += SEL_WARPS) {
-            const int t = x / (2 * hp), y = x % (2 * hp);
-            const bool real = t < toks && y < hs;
-            float v[4] = {0, 0, 0, 0}, code[4];
-            const bool mine = lane * 4 < a.hd;
-            if (real && mine) {
-                const uint2 w = *reinterpret_cast<const uint2*>(
-                    a.q + (q0 + t0 + t) * a.q_tok + ((int64_t)h * a.G + h0 + y) * a.q_head + lane * 4);
-                v[0] = __uint_as_float(w.x << 16);
-                v[1] = __uint_as_float(w.x & 0xffff0000u);
-                v[2] = __uint_as_float(w.y << 16);
-                v[3] = __uint_as_float(w.y & 0xffff0000u);
-            }
-            const float s = int8_row(v, mine, code);
-            if (lane * 4 < HD) {
-                const __half2 lo = __floats2half2_rn(code[0], code[1]);
-                const __half2 hi = __floats2half2_rn(code[2], code[3]);
-                const int piece = lane >> 2;
-                const int st = (piece >> 2) * 4 + (lane & 3), col = 2 * (t & 3) + (y & 1);
-                frag[(((t >> 2) * pairs + (y >> 1)) * KS + st) * 32 + col * 4 + (piece & 3)] =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                               *reinterpret_cast<const uint32_t*>(&hi));
-            }
-            if (lane == 0) qs[t * a.heads + y] = real ? s : __uint_as_float(0x7fc00000u);
-        }
-        __syncthreads();
         // rows g and g + 8 of 16 blocks: pages a round ahead of codes
         int page[2];
         uint4 raw[2][KS / 4];
@@ -347,6 +318,45 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
             fetch();
             look(warp * 16 + ROUND);
         }
+        // the queries, four rows at a time
+        const int rows = quads * 4 * hp * 2;
+        for (int x0 = warp; x0 < rows; x0 += 4 * SEL_WARPS) {
+            uint2 w[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int x = x0 + u * SEL_WARPS, t = x / (2 * hp), y = x - t * 2 * hp;
+                w[u] = make_uint2(0, 0);
+                if (t < toks && y < hs && lane * 4 < a.hd)
+                    w[u] = *reinterpret_cast<const uint2*>(a.q + (q0 + t0 + t) * a.q_tok +
+                                                           ((int64_t)h * a.G + h0 + y) * a.q_head +
+                                                           lane * 4);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const int x = x0 + u * SEL_WARPS, t = x / (2 * hp), y = x - t * 2 * hp;
+                if (x >= rows) break;
+                const float v[4] = {
+                    __uint_as_float(w[u].x << 16), __uint_as_float(w[u].x & 0xffff0000u),
+                    __uint_as_float(w[u].y << 16), __uint_as_float(w[u].y & 0xffff0000u)};
+                float code[4];
+                const float s = int8_row(v, code);
+                if (lane * 4 < HD) {
+                    const __half2 lo = __floats2half2_rn(code[0], code[1]);
+                    const __half2 hi = __floats2half2_rn(code[2], code[3]);
+                    const int piece = lane >> 2;
+                    const int st = (piece >> 2) * 4 + (lane & 3), col = 2 * (t & 3) + (y & 1);
+                    // (two steps' words side by side)
+                    frag[((((t >> 2) * pairs + (y >> 1)) * KS + (st & ~1)) * 32 +
+                          (col * 4 + (piece & 3)) * 2) + (st & 1)] =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                   *reinterpret_cast<const uint32_t*>(&hi));
+                }
+                // (a head that is not there does not count)
+                if (lane == 0)
+                    qs[t * a.heads + y] = t < toks && y < hs ? s : __uint_as_float(0x7fc00000u);
+            }
+        }
+        __syncthreads();
         for (int j0 = warp * 16; j0 < vis; j0 += ROUND) {
             uint32_t af[KS][4];
             if (!FEW) {
@@ -372,12 +382,15 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
                 const int t = qd * 4 + c;
                 float best[2] = {__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u)};
                 for (int i = 0; i < hp; i++) {
-                    const uint2* f = frag + (qd * pairs + i) * KS * 32 + lane;
+                    const uint4* f =
+                        reinterpret_cast<const uint4*>(frag + (qd * pairs + i) * KS * 32) + lane;
                     float d[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int st = 0; st < KS; st++) {
-                        const uint2 w = f[st * 32];
+                    for (int st = 0; st < KS; st += 2) {
+                        const uint4 w = f[st * 16];
                         mma_f16(d, af[st][0], af[st][1], af[st][2], af[st][3], w.x, w.y);
+                        mma_f16(d, af[st + 1][0], af[st + 1][1], af[st + 1][2], af[st + 1][3], w.z,
+                                w.w);
                     }
                     const float2 s = *reinterpret_cast<const float2*>(qs + t * a.heads + 2 * i);
                     best[0] = fmaxf(best[0], fmaxf(__fmul_rn(d[0], s.x), __fmul_rn(d[1], s.y)));
