@@ -6,11 +6,11 @@
 // the end) and the row's best k logits; the beams' lists are then merged by offers
 // worked out in 64 bits.
 //
-// The best k.  A bound that k logits of a run reach follows from the lanes' maxima: k lanes
-// at least have one that is not below the lowest, over the 8 warps, of a warp's (k / 8)-th
-// largest.  What is not below the bound (fewer and fewer) goes to the warp's list as a
-// key, x as an ordered integer and then the lower token.  The lists are joined without
-// sorting: what is among the best k has fewer than k above it.
+// The best k.  The pass keeps the largest of each 16 logits (a cell); a bound that k logits of
+// the run reach follows from the lanes' largest: k lanes at least have one that is not below
+// the lowest, over the 8 warps, of a warp's (k / 8)-th largest.  Few cells reach it; their
+// logits are read once more and become keys, x as an ordered integer and then the lower
+// token, ranked by counting what is better.
 //
 // What bounds it.  The logits are read once: HBM, if the exponentials (16 a cycle and SM)
 // and the instructions around them keep up.  A row is cut into runs so that every SM has
@@ -28,7 +28,8 @@ constexpr int NT = WARPS * 32;
 constexpr int PER = 16;          // logits of a lane in a step
 constexpr int STEP = 32 * PER;   // tokens of a warp's step
 constexpr int PART = WARPS * STEP;
-constexpr int CAP = STEP;        // keys of a warp's list
+constexpr int CELLS = 512;       // cells that are looked into at once
+constexpr int MAX_PARTS = 32;    // of a run: 32 KiB of cells
 constexpr int MAX_K = 128;
 constexpr int OFFERS = 1024;     // that are ranked at once
 constexpr float LOG2E = 1.4426950408889634f;
@@ -93,27 +94,29 @@ __device__ __forceinline__ double number_of(uint64_t o) {
     return __longlong_as_double((long long)((o >> 63) ? o ^ 0x8000000000000000ull : ~o));
 }
 
-// A warp has the tokens of every eighth step of 512 of a run, token `lane` of each 32 of them,
-// whatever the row's alignment: equal rows have equal sums to the last bit, and their
-// offers tie.
+// A warp has the tokens of every eighth step of 512 of a run, a lane those at `lane` of each 32
+// of them (a cell), whatever the row's alignment: equal rows have equal sums to the last
+// bit, and their offers tie.
 template <bool BF16>
 __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    __shared__ uint64_t lists[WARPS][CAP];
-    __shared__ uint64_t all[WARPS * MAX_K];
-    __shared__ int n_of[WARPS], n_all;
-    __shared__ float bound_of[WARPS];
-    __shared__ volatile uint32_t nth[WARPS];  // the warps' r-th largest lane maxima, as ranks
+    using T = typename std::conditional<BF16, uint16_t, uint32_t>::type;
+    extern __shared__ float most[];  // [cells] a cell's largest logit
+    __shared__ uint64_t keys[OFFERS], best[WARPS];
+    __shared__ int open[CELLS], n_open, n_keys;
+    __shared__ uint32_t nth[WARPS];
     __shared__ float2 parts[WARPS];
     const int64_t row = blockIdx.y;
     if (!reads(a, row)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
-    const int64_t b = row / a.W, first = b * a.b_stride + (row - b * a.W) * a.w_stride;
+    const int64_t b = row / a.W;
+    const T* from = static_cast<const T*>(a.x) + b * a.b_stride + (row - b * a.W) * a.w_stride;
     const int j0 = blockIdx.x * a.run, j1 = min(a.V, j0 + a.run);
-    using T = typename std::conditional<BF16, uint16_t, uint32_t>::type;
-    const T* from = static_cast<const T*>(a.x) + first;
-    uint64_t* list = lists[warp];
+    auto logit = [&](int t) {
+        const uint32_t w = __ldcs(from + t);
+        return __uint_as_float(BF16 ? w << 16 : w);
+    };
     uint32_t next[PER];
     auto load = [&](int j) {  // a lane's logits of the step whose first one it has at j
         if (j - lane + STEP <= j1) {
@@ -127,22 +130,20 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
                                           : BF16 ? 0xff80u : 0xff800000u;  // -inf
         }
     };
+    // ---- one pass: the sum, and the largest of each cell ----
     int j = j0 + warp * STEP + lane;
     load(j);
-    float m = -INFINITY, sum = 0.0f, bound = -FLT_MAX;
-    int have = 0;  // keys of the list; at least k logits of the run's are not below the bound
-    // k lanes at least, `share` of each warp that has tokens, have a maximum that is not below
-    // the lowest of those warps' share-th largest
-    const int busy = min(WARPS, (j1 - j0 + STEP - 1) / STEP), share = (k + busy - 1) / busy;
-    for (int step = 1; step == 1 || j - lane < j1; j += WARPS * STEP, step++) {
+    float m = -INFINITY, sum = 0.0f;
+    for (int cell = tid; j - lane < j1; j += PART, cell += NT) {
         float x[PER];
 #pragma unroll
         for (int e = 0; e < PER; e++) x[e] = __uint_as_float(BF16 ? next[e] << 16 : next[e]);
-        load(j + WARPS * STEP);
+        load(j + PART);
         float top = x[0];
 #pragma unroll
         for (int e = 1; e < PER; e += 2)
             top = e + 1 < PER ? tc::max3(top, x[e], x[e + 1]) : fmaxf(top, x[e]);
+        most[cell] = top;
         const float up = fmaxf(m, top), at = up == -INFINITY ? 0.0f : up;
         // (the difference first: x log2(e) rounded would be off by as much as x is large)
         uint64_t s2 = f2(m == up ? sum : sum * tc::ex2((m - at) * LOG2E), 0.0f);
@@ -157,90 +158,19 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
         float y, z;
         unf2(s2, y, z);
         sum = y + z;
-        // ---- the best: what bounds them rises with the lanes' maxima (looked at after 1, 2,
-        // 4, 8 .. steps) ----
-        if ((step & (step - 1)) == 0) {
-            if (step == 1 && k <= 32) {  // the k-th largest of the warp's own
-                int rank = 0;
-#pragma unroll
-                for (int o = 1; o < 32; o++) {
-                    const float other = __shfl_xor_sync(0xffffffffu, m, o);
-                    rank += other > m || (other == m && (lane ^ o) < lane);
-                }
-                const unsigned kth = __ballot_sync(0xffffffffu, rank == k - 1);
-                if (kth) bound = fmaxf(bound, __shfl_sync(0xffffffffu, m, __ffs(kth) - 1));
-            }
-            if (share <= 16) {
-                uint32_t mine = rank_of(m), top_most = 0;
-                for (int i = 0; i < share; i++) {
-                    top_most = __reduce_max_sync(0xffffffffu, mine);
-                    const unsigned who = __ballot_sync(0xffffffffu, mine == top_most);
-                    if (lane == __ffs(who) - 1) mine = 0;
-                }
-                if (lane == 0) nth[warp] = top_most;
-            }
-            if (step == 1) __syncthreads();  // (every warp has a first step, if one of none)
-        }
-        if (share <= 16) {
-            const uint32_t least =
-                __reduce_min_sync(0xffffffffu, lane < busy ? nth[lane % WARPS] : 0xffffffffu);
-            bound = fmaxf(bound, score_of(least));
-        }
-        if (!__any_sync(0xffffffffu, top >= bound)) continue;
-        uint32_t pass = 0;
-#pragma unroll
-        for (int e = 0; e < PER; e++) pass |= (x[e] >= bound ? 1u : 0u) << e;
-        const int mine = __popc(pass);
-        int before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += v;
-        }
-        const int added = __shfl_sync(0xffffffffu, before, 31);
-        before += have - mine;
-        if (have + added <= CAP) {
-            for (; pass; pass &= pass - 1) {  // (read once more: no index into registers)
-                const int t = j + (__ffs(pass) - 1) * 32;
-                const uint32_t w = from[t];
-                list[before++] = key_of(__uint_as_float(BF16 ? w << 16 : w), t);
-            }
-            have += added;
-        } else {
-            // more than the list holds: the best k of it and of the step, one by one, into
-            // their places from the front (what is taken from there is kept in registers)
-            uint64_t below = ~0ull, kept[MAX_K / 32] = {};
-            int n = 0;
-            for (; n < k; n++) {
-                uint64_t best = 0;
-                for (int i = lane; i < have; i += 32)
-                    if (list[i] < below && list[i] > best) best = list[i];
-#pragma unroll
-                for (int e = 0; e < PER; e++) {
-                    const uint64_t key = key_of(x[e], j + e * 32);
-                    if (x[e] >= -FLT_MAX && key < below && key > best) best = key;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-                    if (v > best) best = v;
-                }
-                if (best == 0) break;
-                below = best;
-#pragma unroll
-                for (int i = 0; i < MAX_K / 32; i++)
-                    if (n == 32 * i + lane) kept[i] = best;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < MAX_K / 32; i++)
-                if (32 * i + lane < n) list[32 * i + lane] = kept[i];
-            have = n;
-            if (n == k) bound = fmaxf(bound, x_of(below));
-        }
-        __syncwarp();
     }
-    // ---- the run's sum ----
+    // ---- a bound that k logits reach: k lanes at least, `share` of each warp that has tokens,
+    // have a largest one that is not below the lowest of those warps' share-th largest ----
+    const int busy = min(WARPS, (j1 - j0 + STEP - 1) / STEP), share = (k + busy - 1) / busy;
+    if (share <= 32) {
+        uint32_t mine = rank_of(m), lowest = 0;
+        for (int i = 0; i < share; i++) {
+            lowest = __reduce_max_sync(0xffffffffu, mine);
+            const unsigned who = __ballot_sync(0xffffffffu, mine == lowest);
+            if (lane == __ffs(who) - 1) mine = 0;
+        }
+        if (lane == 0) nth[warp] = lowest;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
@@ -249,55 +179,87 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
         sum = sum * tc::ex2((m - ref) * LOG2E) + s2 * tc::ex2((m2 - ref) * LOG2E);
         m = to;
     }
-    if (lane == 0) {
-        parts[warp] = make_float2(m, sum);
-        n_of[warp] = have;
-        bound_of[warp] = bound;
-    }
-    if (tid == 0) n_all = 0;
+    if (lane == 0) parts[warp] = make_float2(m, sum);
+    if (tid == 0) n_open = n_keys = 0;
     __syncthreads();
     const int64_t at = row * a.splits + blockIdx.x;
-    if (tid == 0) {
-        for (int w = 1; w < WARPS; w++) m = fmaxf(m, parts[w].x);
-        const float ref = m == -INFINITY ? 0.0f : m;
-        sum = 0.0f;
-        for (int w = 0; w < WARPS; w++) sum += parts[w].y * tc::ex2((parts[w].x - ref) * LOG2E);
-        a.sums[at] = make_float2(m, sum);
+    if (warp == WARPS - 1) {  // the run's sum
+        const float2 p = lane < WARPS ? parts[lane] : make_float2(-INFINITY, 0.0f);
+        m = p.x;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = __shfl_sync(0xffffffffu, m, 0);
+        sum = lane < WARPS ? p.y * tc::ex2((p.x - (m == -INFINITY ? 0.0f : m)) * LOG2E) : 0.0f;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) a.sums[at] = make_float2(m, sum);
     }
-    // ---- its best k: what is not below the highest bound, by counting what is better ----
-    for (int w = 0; w < WARPS; w++) bound = fmaxf(bound, bound_of[w]);
-    for (int w = 0; w < WARPS; w++)
-        for (int i = tid; i < n_of[w]; i += NT) {
-            const uint64_t key = lists[w][i];
-            if (x_of(key) < bound) continue;
-            const int to = atomicAdd(&n_all, 1);
-            if (to < WARPS * MAX_K) all[to] = key;
+    float bound = -FLT_MAX;
+    if (share <= 32)
+        bound = fmaxf(bound, score_of(__reduce_min_sync(
+                                 0xffffffffu, lane < busy ? nth[lane % WARPS] : 0xffffffffu)));
+    // ---- the cells that reach it, and their logits that do ----
+    const int cells = (j1 - j0 + STEP - 1) / STEP * 32;
+    for (int c = tid; c < cells; c += NT)
+        if (most[c] >= bound) {
+            const int to = atomicAdd(&n_open, 1);
+            if (to < CELLS) open[to] = c;
         }
     __syncthreads();
-    const int n = n_all;
+    auto token = [&](int c, int e) { return j0 + (c >> 5) * STEP + e * 32 + (c & 31); };
+    if (n_open <= CELLS)
+        for (int i = tid; i < n_open * PER; i += NT) {
+            const int t = token(open[i / PER], i % PER);
+            const float x = t < j1 ? logit(t) : -INFINITY;
+            if (x >= bound) {
+                const int to = atomicAdd(&n_keys, 1);
+                if (to < OFFERS) keys[to] = key_of(x, t);
+            }
+        }
+    __syncthreads();
+    // ---- the best k: by counting what is better ----
+    const int n = n_keys;
     uint64_t* out = a.keys + at * k;
-    if (n <= WARPS * MAX_K) {
+    if (n_open <= CELLS && n <= OFFERS) {
         for (int i = tid; i < n; i += NT) {
-            const uint64_t mine = all[i];
+            const uint64_t mine = keys[i];
             int rank = 0;
-            for (int y = 0; y < n; y++) rank += all[y] > mine;
+            for (int y = 0; y < n; y++) rank += keys[y] > mine;
             if (rank < k) out[rank] = mine;
         }
         for (int i = n + tid; i < k; i += NT) out[i] = 0;
-    } else if (warp == 0) {  // (equal logits) one by one
-        uint64_t below = ~0ull;
-        for (int i = 0; i < k; i++) {
-            uint64_t best = 0;
-            for (int w = 0; w < WARPS; w++)
-                for (int y = lane; y < n_of[w]; y += 32)
-                    if (lists[w][y] < below && lists[w][y] > best) best = lists[w][y];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-                if (v > best) best = v;
+        return;
+    }
+    // (equal logits) one by one: a cell is read again if it may hold a better one than the
+    // thread's best so far
+    uint64_t below = ~0ull;
+    for (int i = 0; i < k; i++) {
+        uint64_t mine = 0;
+        for (int c = tid; c < cells; c += NT) {
+            if (!(most[c] >= -FLT_MAX) || key_of(most[c], token(c, 0)) < mine) continue;
+            for (int e = 0; e < PER; e++) {
+                const int t = token(c, e);
+                const float x = t < j1 ? logit(t) : -INFINITY;
+                const uint64_t key = key_of(x, t);
+                if (x >= -FLT_MAX && key < below && key > mine) mine = key;
             }
-            below = best;
-            if (lane == 0) out[i] = best;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t v = __shfl_xor_sync(0xffffffffu, mine, o);
+            if (v > mine) mine = v;
+        }
+        if (lane == 0) best[warp] = mine;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; w++)
+            if (best[w] > mine) mine = best[w];
+        below = mine;
+        if (tid == 0) out[i] = mine;
+        __syncthreads();
+        if (mine == 0) {
+            for (int y = i + 1 + tid; y < k; y += NT) out[y] = 0;
+            break;
         }
     }
 }
@@ -443,10 +405,10 @@ struct Plan {
 Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
     const int64_t parts = (V + PART - 1) / PART, rows = B * W;
     int64_t splits = 1, best = 0;
-    for (int64_t n = 1; n <= parts && n <= 64; n++) {
+    for (int64_t n = (parts + MAX_PARTS - 1) / MAX_PARTS, end = n + 64; n <= parts && n < end; n++) {
         const int64_t per = (parts + n - 1) / n;
         const int64_t cost = (rows * n + sms - 1) / sms * (per + 1);
-        if (n == 1 || cost < best) {
+        if (best == 0 || cost < best) {
             best = cost;
             splits = n;
         }
@@ -524,8 +486,8 @@ extern "C" int ds41_beam_select(const void* logits, int fmt, int64_t b_stride, i
     a.sums = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.keys_bytes);
     cudaStream_t st = (cudaStream_t)stream;
     if (int rc = launch_pdl(bf16 ? beam::runs_kernel<true> : beam::runs_kernel<false>,
-                            dim3((unsigned)p.splits, (unsigned)(B * W)), dim3(beam::NT), 0, st,
-                            name, a))
+                            dim3((unsigned)p.splits, (unsigned)(B * W)), dim3(beam::NT),
+                            (size_t)p.parts * beam::NT * 4, st, name, a))
         return rc;
     const size_t smem = (size_t)W * 8 + (size_t)W * p.splits * 4;
     if (smem > 40 * 1024)
