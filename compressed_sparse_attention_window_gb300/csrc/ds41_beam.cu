@@ -30,8 +30,12 @@ constexpr int STEP = 32 * PER;   // tokens of a warp's step
 constexpr int PART = WARPS * STEP;
 constexpr int CELLS = 512;       // cells that are looked into at once
 constexpr int MAX_PARTS = 32;    // of a run: 32 KiB of cells
+constexpr int STAGES = 3;        // of a warp's ring: a step each, and the piece that may begin
+template <typename T>            // before it
+constexpr int STAGE = STEP * (int)sizeof(T) + 16;
 constexpr int MAX_K = 128;
 constexpr int OFFERS = 1024;     // that are ranked at once
+constexpr int HOLD = 4;          // of them that a merging thread has in registers
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct Args {
@@ -84,10 +88,10 @@ __device__ __forceinline__ bool better(const Offer& x, const Offer& y) {
     if (x.w != y.w) return x.w < y.w;
     return x.key > y.key;
 }
-// larger for larger numbers, 0 for -inf and what is none; -0 is 0
+// larger for larger numbers (finite ones), -0 as 0; 0 is none
 __device__ __forceinline__ uint64_t order_of(double v) {
-    if (!(v > -INFINITY)) return 0;
-    const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+    uint64_t u = (uint64_t)__double_as_longlong(v);
+    if (u == 0x8000000000000000ull) u = 0;
     return u ^ ((u >> 63) ? ~0ull : 0x8000000000000000ull);
 }
 __device__ __forceinline__ double number_of(uint64_t o) {
@@ -117,28 +121,55 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
         const uint32_t w = __ldcs(from + t);
         return __uint_as_float(BF16 ? w << 16 : w);
     };
-    uint32_t next[PER];
-    auto load = [&](int j) {  // a lane's logits of the step whose first one it has at j
-        if (j - lane + STEP <= j1) {
-            const T* at = from + j;
+    // The run comes through a ring of stages of each warp, in pieces of 16 bytes on 16-byte
+    // boundaries, whatever the row's (off: the row's first logit in its first piece; that
+    // piece, which begins before the row, is read logit by logit).
+    constexpr int SIZE = sizeof(T), VE = 16 / SIZE, PIECES = STEP / VE;
+    uint8_t* ring = reinterpret_cast<uint8_t*>(most + a.run / PER) + warp * (STAGES * STAGE<T>);
+    const uint32_t ring_u = smem_u32(ring);
+    const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15) / SIZE;
+    const T* base = from - off;
+    auto fetch = [&](int step) {
+        const int s0 = j0 + (step * WARPS + warp) * STEP;  // (a multiple of VE)
+        const uint32_t to = ring_u + step % STAGES * STAGE<T>;
 #pragma unroll
-            for (int e = 0; e < PER; e++) next[e] = __ldcs(at + e * 32);
-        } else {
-#pragma unroll
-            for (int e = 0; e < PER; e++)
-                next[e] = j + e * 32 < j1 ? (uint32_t)__ldcs(from + j + e * 32)
-                                          : BF16 ? 0xff80u : 0xff800000u;  // -inf
+        for (int u = 0; u < PIECES / 32 + 1; u++) {
+            const int i = u * 32 + lane;
+            const int t = s0 + i * VE - off;  // the piece's first logit
+            if (i > PIECES || t >= j1) continue;
+            if (t >= 0) {
+                const int bytes = min(16, (a.V - t) * SIZE);  // (none behind the row's last)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to + i * 16),
+                             "l"(base + s0 + i * VE), "r"(bytes));
+            } else {
+                T* at = reinterpret_cast<T*>(ring + step % STAGES * STAGE<T>);
+                for (int e = off; e < VE && e - off < a.V; e++) at[e] = from[e - off];
+            }
         }
+        cp_async_commit();
     };
     // ---- one pass: the sum, and the largest of each cell ----
-    int j = j0 + warp * STEP + lane;
-    load(j);
+#pragma unroll
+    for (int x = 0; x < STAGES - 1; x++) fetch(x);
     float m = -INFINITY, sum = 0.0f;
-    for (int cell = tid; j - lane < j1; j += PART, cell += NT) {
+    int j = j0 + warp * STEP + lane;
+    for (int cell = tid, step = 0; j - lane < j1; j += PART, cell += NT, step++) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();  // the stage is there for all lanes, and the one before it has been read
+        fetch(step + STAGES - 1);
+        const T* in = reinterpret_cast<const T*>(ring + step % STAGES * STAGE<T>) + off + lane;
         float x[PER];
 #pragma unroll
-        for (int e = 0; e < PER; e++) x[e] = __uint_as_float(BF16 ? next[e] << 16 : next[e]);
-        load(j + PART);
+        for (int e = 0; e < PER; e++) {
+            uint32_t w = in[e * 32];
+            if (BF16) w <<= 16;
+            x[e] = __uint_as_float(w);
+        }
+        if (j - lane + STEP > j1) {
+#pragma unroll
+            for (int e = 0; e < PER; e++)
+                if (j + e * 32 >= j1) x[e] = -INFINITY;
+        }
         float top = x[0];
 #pragma unroll
         for (int e = 1; e < PER; e += 2)
@@ -159,6 +190,7 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
         unf2(s2, y, z);
         sum = y + z;
     }
+    cp_async_wait<0>();
     // ---- a bound that k logits reach: k lanes at least, `share` of each warp that has tokens,
     // have a largest one that is not below the lowest of those warps' share-th largest ----
     const int busy = min(WARPS, (j1 - j0 + STEP - 1) / STEP), share = (k + busy - 1) / busy;
@@ -270,69 +302,87 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
 __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ double base[];  // [W]: s_w - L; NaN: the beam offers nothing
+    extern __shared__ double base[];  // [W]: s_w - L; NaN: the beam offers nothing, or has ended
+    uint64_t* ends = reinterpret_cast<uint64_t*>(base + a.W);  // [W]: an ended beam's offer
     __shared__ Offer all[OFFERS];
     __shared__ unsigned long long least;
     __shared__ int n_all, taken[NT / 32];
     __shared__ Offer best[NT / 32];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
-    const int n_lists = a.W * a.splits;
+    const int n_lists = a.W * a.splits, n_keys = n_lists * k;
+    const uint64_t* keys = a.keys + (int64_t)b * n_keys;
+    // (on their way while the sums are joined; keys of beams that have none may be anything)
+    uint64_t held[HOLD];
+#pragma unroll
+    for (int u = 0; u < HOLD; u++) held[u] = u * NT + tid < n_keys ? keys[u * NT + tid] : 0;
     if (tid == 0) {
         least = 0;
         n_all = 0;
     }
     for (int w = tid; w < a.W; w += NT) {
         const int64_t row = (int64_t)b * a.W + w;
-        double to = NAN;
-        if (a.ended && a.ended[row]) {
-            to = 0.0;
-        } else if (reads(a, row)) {
-            float m = -INFINITY, sum = 0.0f;
-            for (int s = 0; s < a.splits; s++) m = fmaxf(m, a.sums[row * a.splits + s].x);
-            const float ref = m == -INFINITY ? 0.0f : m;
-            for (int s = 0; s < a.splits; s++) {
-                const float2 p = a.sums[row * a.splits + s];
-                sum += p.y * expf(p.x - ref);
-            }
-            // (a sum that a NaN or an infinity is in is NaN; one of nothing but -inf is 0)
-            if (sum > 0.0f && sum < INFINITY)
-                to = (double)a.scores[row] - ((double)m + (double)logf(sum));
+        const float score = a.scores[row];
+        const bool over = a.ended && a.ended[row];
+        float m = -INFINITY, sum = 0.0f;
+        for (int s = 0; s < a.splits; s++) m = fmaxf(m, a.sums[row * a.splits + s].x);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        for (int s = 0; s < a.splits; s++) {
+            const float2 p = a.sums[row * a.splits + s];
+            sum += p.y * expf(p.x - ref);
         }
+        // (a sum that a NaN or an infinity is in is NaN; one of nothing but -inf is 0)
+        double to = NAN;
+        if (!over && score > -INFINITY && score < INFINITY && sum > 0.0f && sum < INFINITY)
+            to = (double)score - ((double)m + (double)logf(sum));
         base[w] = to;
+        // an ended beam's one offer is in the place of its first list's first
+        ends[w] = over && score > -INFINITY && score < INFINITY ? order_of(score) : 0;
     }
     __syncthreads();
-    // List h is run h % splits of beam h / splits; an ended beam's first list is its one offer.
-    auto offer = [&](int h, int i) {
+    // offer i of list h, which is run h % splits of beam h / splits
+    auto offer_of = [&](int h, int i, uint64_t key) {
         const int w = h / a.splits;
-        const int64_t row = (int64_t)b * a.W + w;
         Offer o{0, 0, w};
-        if (a.ended && a.ended[row]) {
-            const float s = a.scores[row];
-            if (h % a.splits == 0 && i == 0 && s < INFINITY) {
-                o.v = order_of(s);
-                o.key = key_of(0.0f, a.end_token);
-            }
-        } else if (i < k && base[w] == base[w]) {
-            o.key = a.keys[((int64_t)b * n_lists + h) * k + i];
-            if (o.key) o.v = order_of(base[w] + (double)x_of(o.key));
+        if (i >= k) return o;
+        if (base[w] == base[w]) {
+            o.key = key;
+            if (key) o.v = order_of(base[w] + (double)x_of(key));
+        } else if (i == 0 && h == w * a.splits) {
+            o.key = key_of(0.0f, a.end_token);
+            o.v = ends[w];
         }
         return o;
     };
+    auto offer = [&](int h, int i) { return offer_of(h, i, i < k ? keys[h * k + i] : 0); };
     auto write = [&](int i, const Offer& o) {
         const int64_t to = (int64_t)b * k + i;
         a.out[to] = o.v ? (float)number_of(o.v) : -INFINITY;
         a.parents[to] = o.v ? b * a.W + o.w : -1;
         a.tokens[to] = o.v ? token_of(o.key) : -1;
     };
-    for (int h = tid; h < n_lists; h += NT) atomicMax(&least, (unsigned long long)offer(h, k - 1).v);
+    // (arithmetic in 64 bits is slow here, two operations a cycle and SM: once an offer)
+    Offer mine_of[HOLD];
+#pragma unroll
+    for (int u = 0; u < HOLD; u++) {
+        const int x = u * NT + tid, h = x / k;
+        mine_of[u] = x < n_keys ? offer_of(h, x - h * k, held[u]) : Offer{0, 0, 0};
+        if (x < n_keys && x - h * k == k - 1 && mine_of[u].v)
+            atomicMax(&least, (unsigned long long)mine_of[u].v);
+    }
+    for (int h = HOLD * NT / k + tid; h < n_lists; h += NT)  // (lists that end behind those)
+        atomicMax(&least, (unsigned long long)offer(h, k - 1).v);
     __syncthreads();
     const uint64_t from = least;
-    for (int x = tid; x < n_lists * k; x += NT) {
-        const int h = x / k;
-        const Offer o = offer(h, x - h * k);
-        if (o.v == 0 || o.v < from) continue;
+    auto keep = [&](const Offer& o) {
+        if (o.v == 0 || o.v < from) return;
         const int to = atomicAdd(&n_all, 1);
         if (to < OFFERS) all[to] = o;
+    };
+#pragma unroll
+    for (int u = 0; u < HOLD; u++) keep(mine_of[u]);
+    for (int x = HOLD * NT + tid; x < n_keys; x += NT) {
+        const int h = x / k;
+        keep(offer(h, x - h * k));
     }
     __syncthreads();
     const int n = n_all;
@@ -346,7 +396,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
         for (int i = n + tid; i < k; i += NT) write(i, Offer{0, 0, 0});
         return;
     }
-    int* at = reinterpret_cast<int*>(base + a.W);  // [lists]: the heads' places
+    int* at = reinterpret_cast<int*>(ends + a.W);  // [lists]: the heads' places
     for (int h = tid; h < n_lists; h += NT) at[h] = 0;
     Offer mine;
     int list;
@@ -404,8 +454,9 @@ struct Plan {
 };
 Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
     const int64_t parts = (V + PART - 1) / PART, rows = B * W;
-    int64_t splits = 1, best = 0;
+    int64_t splits = 0, best = 0;
     for (int64_t n = (parts + MAX_PARTS - 1) / MAX_PARTS, end = n + 64; n <= parts && n < end; n++) {
+        if (splits > 0 && W * n > 32768) break;  // (the merge keeps a place for each list)
         const int64_t per = (parts + n - 1) / n;
         const int64_t cost = (rows * n + sms - 1) / sms * (per + 1);
         if (best == 0 || cost < best) {
@@ -423,7 +474,7 @@ Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
 }
 int check_sizes(const char* name, int64_t B, int64_t W, int64_t V, int64_t k) {
     DS41_REQUIRE(B >= 0 && B < 65536 && W >= 1 && W <= 1024 && B * W < 65536 && V >= 1 &&
-                     V < int64_t(1) << 30,
+                     V <= int64_t(1) << 22,
                  DS41_E_RANGE, "%s: B=%lld W=%lld V=%lld", name, (long long)B, (long long)W,
                  (long long)V);
     DS41_REQUIRE(k >= 1 && k <= MAX_K, DS41_E_ARG, "%s: k=%lld (1 .. %d)", name, (long long)k,
@@ -485,12 +536,20 @@ extern "C" int ds41_beam_select(const void* logits, int fmt, int64_t b_stride, i
     a.keys = static_cast<uint64_t*>(ws);
     a.sums = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.keys_bytes);
     cudaStream_t st = (cudaStream_t)stream;
+    const int ring = beam::WARPS * beam::STAGES *
+                     (bf16 ? beam::STAGE<uint16_t> : beam::STAGE<uint32_t>);
+    const int smem = p.parts * beam::NT * 4 + ring;
+    constexpr int MOST = beam::MAX_PARTS * beam::NT * 4 +
+                         beam::WARPS * beam::STAGES * beam::STAGE<uint32_t>;
+    if (int rc = bf16 ? allow_smem<beam::runs_kernel<true>>(MOST, name)
+                      : allow_smem<beam::runs_kernel<false>>(MOST, name))
+        return rc;
     if (int rc = launch_pdl(bf16 ? beam::runs_kernel<true> : beam::runs_kernel<false>,
                             dim3((unsigned)p.splits, (unsigned)(B * W)), dim3(beam::NT),
-                            (size_t)p.parts * beam::NT * 4, st, name, a))
+                            smem, st, name, a))
         return rc;
-    const size_t smem = (size_t)W * 8 + (size_t)W * p.splits * 4;
-    if (smem > 40 * 1024)
+    const size_t places = (size_t)W * 16 + (size_t)W * p.splits * 4;
+    if (places > 16 * 1024)
         if (int rc = allow_smem<beam::merge_kernel>(200 * 1024, name)) return rc;
-    return launch_pdl(beam::merge_kernel, dim3((unsigned)B), dim3(beam::NT), smem, st, name, a);
+    return launch_pdl(beam::merge_kernel, dim3((unsigned)B), dim3(beam::NT), places, st, name, a);
 }

@@ -743,8 +743,8 @@ size_t ds41_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t
  *     takes), tokens [B, k] int32 outputs; where fewer than k offers are above
  *     -inf the rest is -inf, -1, -1
  * A beam whose logits hold a NaN or +inf, or nothing but -inf, or whose score is NaN
- * or +inf, offers nothing.  1 <= k <= 128, W <= 1024, 0 <= end_token < V with
- * ended. */
+ * or +inf, offers nothing.  1 <= k <= 128, W <= 1024, V <= 2^22, B * W < 65536, 0 <= end_token
+ * < V with ended. */
 int ds41_beam_select(const void* logits, int fmt, int64_t b_stride, int64_t w_stride,
                      const float* scores, const uint8_t* ended, int64_t end_token, int64_t B,
                      int64_t W, int64_t V, int64_t k, float* out_scores, int32_t* parents,
