@@ -573,9 +573,10 @@ extern "C" int ds41_kv_pages_fork(void* k_cache, void* v_cache, float* k_scales,
                  "%s: refs, page_table, lens, parents, table_out and lens_out must be non-null and "
                  "aligned", name);
     DS41_REQUIRE(n == 0 || B == 0 ||
-                     (page_table + B * max_pages <= table_out ||
-                      table_out + n * max_pages <= page_table),
-                 DS41_E_ARG, "%s: table_out lies in page_table", name);
+                     ((page_table + B * max_pages <= table_out ||
+                       table_out + n * max_pages <= page_table) &&
+                      (lens + B <= lens_out || lens_out + n <= lens)),
+                 DS41_E_ARG, "%s: table_out lies in page_table, or lens_out in lens", name);
     const size_t one = up16((size_t)n * 4);
     DS41_REQUIRE(n == 0 || (ws && aligned16(ws) && ws_bytes >= 4 * one), DS41_E_WORKSPACE,
                  "%s: needs %zu bytes of workspace, got %zu", name, 4 * one, ws ? ws_bytes : 0);

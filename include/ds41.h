@@ -682,8 +682,8 @@ size_t ds41_kv_pages_fork_workspace_bytes(int64_t n_pages, int64_t B, int64_t n)
 /* n children go on from where their parents are: child i has the rows of sequence
  * parents[i] (-1: none).  It shares the full pages, whose refs rise; the rows of a last
  * page that is not full are copied to a free page.
- *   parents [n] int32;  table_out [n, max_pages] int32 (not page_table) and lens_out [n]
- *   int32 outputs, entries behind a child's pages -1
+ *   parents [n] int32;  table_out [n, max_pages] int32 and lens_out [n] int32 outputs
+ *   (apart from page_table and lens), entries behind a child's pages -1
  *   replace != 0: the children are instead of the parents (a beam search's step, with
  *   the parents ds41_beam_select gives): the parents' references are dropped, the first child of a
  *   parent takes its last page over, and pages that nobody has any more are free for
