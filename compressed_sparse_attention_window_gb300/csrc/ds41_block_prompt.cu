@@ -101,9 +101,9 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     pdl_wait();
     pdl_trigger();
     extern __shared__ uint32_t table[];
-    __shared__ int end[256], sh[PLAN / 32], units_of[3];  // (both tiles', tile 0's, tile 1's)
+    __shared__ int sh[PLAN / 32], units_of[3];  // (both tiles', tile 0's, tile 1's)
     __shared__ __align__(16) Item it;
-    const int tid = threadIdx.x, id = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = blockIdx.x;
     // (head group by head group: what is under way at a time reads the keys of one or two, which
     // the L2 holds)
     const int grp = id / p.pairs, w = id - grp * p.pairs, h = grp / p.subs;
@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
         base += sum;
         if (w < base && id != 0) break;
     }
-    if (tid < 256) end[tid] = p.topk;
     __syncthreads();
     if (it.grp < 0) {
         if (tid == 0) p.items[id].grp = -1;
@@ -152,117 +151,139 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     }
     const int toks = min(2 * p.TT, it.n - it.t0), p0 = it.len - it.n + it.t0;
     const int32_t* lists = p.idx + ((int64_t)(it.q0 + it.t0) * p.kvh + h) * p.topk;
-    auto entry = [&](int tok, int i) { return lists[(int64_t)tok * p.kvh * p.topk + i]; };
-    // a list ends at the first entry that does not rise or lies past its token
-    for (int e = tid; e < toks * p.topk; e += PLAN) {
-        const int tok = e / p.topk, i = e - tok * p.topk;
-        const int x = entry(tok, i), before = i > 0 ? entry(tok, i - 1) : -1;
-        if (x <= before || x > (p0 + tok) >> p.shift) atomicMin(&end[tok], i);
-    }
-    __syncthreads();
     const int blocks = ((p0 + toks - 1) >> p.shift) + 1, W = p.words;
     const int range = p.table / W;
-    const int per = 1 << (p.shift - p.unit_shift), nu = KB >> p.unit_shift;
+    const int per = 1 << (p.shift - p.unit_shift);
+    const int nu_shift = 7 - p.unit_shift, nu = 1 << nu_shift;
     uint32_t* recs = p.recs + (int64_t)id * p.max_rec * p.rec_words;
-    // once to count the units of each kind, once to put them into their records
-    int base[3] = {0, 0, 0};  // the kinds' first records
-    for (int pass = 0; pass < 2; pass++) {
-        int found[3] = {0, 0, 0};  // blocks so far
-        for (int r0 = 0; r0 < blocks; r0 += range) {
-            const int size = min(range, blocks - r0);
-            if (pass == 0 || blocks > range) {
-                for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
-                __syncthreads();
-                for (int e = tid; e < toks * p.topk; e += PLAN) {
-                    const int tok = e / p.topk, i = e - tok * p.topk;
-                    if (i > end[tok]) continue;
-                    const int x = entry(tok, i);
-                    if (i == end[tok]) {
-                        if (x != -1 && r0 == 0 && pass == 0) raise_status(p.status, DS41_E_INDEX);
-                    } else if (x >= r0 && x < r0 + size) {
-                        atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
-                    }
-                }
-                __syncthreads();
+    // the masks of the blocks from r0 on: a warp for a token, its list 32 entries at a time
+    auto fill = [&](int r0, int size, bool report) {
+        for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
+        __syncthreads();
+        for (int tok = warp; tok < toks; tok += PLAN / 32) {
+            const int32_t* list = lists + (int64_t)tok * p.kvh * p.topk;
+            const int cur = (p0 + tok) >> p.shift;
+            for (int i0 = 0, last = -1; i0 < p.topk; i0 += 32) {
+                const int x = i0 + lane < p.topk ? list[i0 + lane] : -1;
+                int before = __shfl_up_sync(0xffffffffu, x, 1);
+                if (lane == 0) before = last;
+                last = __shfl_sync(0xffffffffu, x, 31);
+                // it ends at the first entry that does not rise or lies past its token
+                const unsigned bad = __ballot_sync(0xffffffffu, x <= before || x > cur);
+                const int end = bad ? __ffs(bad) - 1 : 32;
+                if (lane < end && x >= r0 && x < r0 + size)
+                    atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
+                if (report && lane == end && x != -1) raise_status(p.status, DS41_E_INDEX);
+                if (bad) break;
             }
-            for (int x0 = 0; x0 < size; x0 += PLAN) {
-                const int x = x0 + tid;
-                uint32_t tiles = 0;
-                if (x < size)
-                    for (int y = 0; y < W; y++) {
-                        const uint32_t m = table[x * W + y], low = low_bits(p.TT - 32 * y);
-                        tiles |= (m & low ? 1u : 0u) | (m & ~low ? 2u : 0u);
-                    }
-                // (three counts of at most 256 in one word)
-                const int kind = tiles == 3 ? 0 : (int)tiles;
-                int sums;
-                const int before = prefix(tiles ? 1 << (10 * kind) : 0, sh, sums);
-                const int at = found[0] * (kind == 0) + found[1] * (kind == 1) +
-                               found[2] * (kind == 2) + ((before >> (10 * kind)) & 1023);
+        }
+        __syncthreads();
+    };
+    // which tiles list block r0 + x: 0 neither, 1 tile 0, 2 tile 1, 3 both
+    auto tiles_of = [&](int x, int size) {
+        uint32_t tiles = 0;
+        if (x < size)
+            for (int y = 0; y < W; y++) {
+                const uint32_t m = table[x * W + y], low = low_bits(p.TT - 32 * y);
+                tiles |= (m & low ? 1u : 0u) | (m & ~low ? 2u : 0u);
+            }
+        return tiles;
+    };
+    // the units of each kind
+    for (int r0 = 0; r0 < blocks; r0 += range) {
+        const int size = min(range, blocks - r0);
+        fill(r0, size, r0 == 0);
+        uint32_t mine = 0;  // (three counts in one word: at most 32 blocks a thread, two units each)
+        for (int x = tid; x < size; x += PLAN) {
+            const uint32_t tiles = tiles_of(x, size);
+            // (a block's second unit may lie behind the last key)
+            const int n = per == 1 || ((r0 + x) << p.shift) + KB < it.len ? per : 1;
+            if (tiles) mine += (uint32_t)n << (10 * (tiles == 3 ? 0 : tiles));
+        }
 #pragma unroll
-                for (int k = 0; k < 3; k++) found[k] += (sums >> (10 * k)) & 1023;
-                if (!tiles) continue;
-                for (int k = 0; k < per; k++) {
-                    const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
-                    if (row >= it.len) break;  // (behind the last key: only the last block's)
-                    const int u = at * per + k, rec = u / nu, slot = u - rec * nu;
-                    if (pass == 0) {
-                        atomicMax(&units_of[kind], u + 1);
-                        continue;
-                    }
-                    const int first = kind == 0 ? base[0] : kind == 1 ? base[1] : base[2];
-                    uint32_t* to = recs + (int64_t)(first + rec) * p.rec_words;
-                    to[slot] = (uint32_t)row;
-                    for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
-                    if (row + (1 << p.unit_shift) > it.len) {
-                        it.tail = (slot << p.unit_shift) + it.len - row;
-                        it.tail_end = (slot + 1) << p.unit_shift;
-                        it.tail_step = rec + (kind ? base[1] : 0);
-                        it.tail_tile = kind == 2;
-                    }
+        for (int k = 0; k < 3; k++) {
+            const int n = __reduce_add_sync(0xffffffffu, (mine >> (10 * k)) & 1023);
+            if (lane == 0 && n) atomicAdd(&units_of[k], n);
+        }
+        __syncthreads();
+    }
+    const int base[3] = {0, (units_of[0] + nu - 1) >> nu_shift,
+                         ((units_of[0] + nu - 1) >> nu_shift) + ((units_of[1] + nu - 1) >> nu_shift)};
+    // into their records
+    int found[3] = {0, 0, 0};  // blocks so far
+    for (int r0 = 0; r0 < blocks; r0 += range) {
+        const int size = min(range, blocks - r0);
+        if (blocks > range) fill(r0, size, false);
+        for (int x0 = 0; x0 < size; x0 += PLAN) {
+            const int x = x0 + tid;
+            const uint32_t tiles = tiles_of(x, size);
+            // (three counts of at most 256 in one word)
+            const int kind = tiles == 3 ? 0 : (int)tiles;
+            int sums;
+            const int before = prefix(tiles ? 1 << (10 * kind) : 0, sh, sums);
+            const int at = (kind == 0 ? found[0] : kind == 1 ? found[1] : found[2]) +
+                           ((before >> (10 * kind)) & 1023);
+#pragma unroll
+            for (int k = 0; k < 3; k++) found[k] += (sums >> (10 * k)) & 1023;
+            if (!tiles) continue;
+            for (int k = 0; k < per; k++) {
+                const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
+                if (row >= it.len) break;  // (behind the last key: only the last block's)
+                const int u = at * per + k, rec = u >> nu_shift, slot = u & (nu - 1);
+                const int first = kind == 0 ? base[0] : kind == 1 ? base[1] : base[2];
+                uint32_t* to = recs + (int64_t)(first + rec) * p.rec_words;
+                to[slot] = (uint32_t)row;
+                for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
+                if (row + (1 << p.unit_shift) > it.len) {
+                    it.tail = (slot << p.unit_shift) + it.len - row;
+                    it.tail_end = (slot + 1) << p.unit_shift;
+                    it.tail_step = rec + (kind ? base[1] : 0);
+                    it.tail_tile = kind == 2;
                 }
             }
-            __syncthreads();
         }
-        if (pass == 0) {
-            base[1] = (units_of[0] + nu - 1) / nu;
-            base[2] = base[1] + (units_of[1] + nu - 1) / nu;
-        }
+        __syncthreads();
     }
     // slots behind a kind's last unit
 #pragma unroll
     for (int kind = 0; kind < 3; kind++) {
-        const int n = units_of[kind], slots = (n + nu - 1) / nu * nu;
+        const int n = units_of[kind], slots = (n + nu - 1) >> nu_shift << nu_shift;
         for (int u = n + tid; u < slots; u += PLAN) {
-            uint32_t* to = recs + (int64_t)(base[kind] + u / nu) * p.rec_words;
-            to[u % nu] = ROW;
-            for (int y = 0; y < W; y++) to[nu + (u % nu) * W + y] = 0;
+            uint32_t* to = recs + (int64_t)(base[kind] + (u >> nu_shift)) * p.rec_words;
+            const int slot = u & (nu - 1);
+            to[slot] = ROW;
+            for (int y = 0; y < W; y++) to[nu + slot * W + y] = 0;
         }
     }
     if (tid == 0) {
         it.both = base[1];
         it.own[0] = base[2] - base[1];
-        it.own[1] = (units_of[2] + nu - 1) / nu;
+        it.own[1] = (units_of[2] + nu - 1) >> nu_shift;
     }
     __syncthreads();
     if (tid < 4)
         reinterpret_cast<int4*>(p.items + id)[tid] = reinterpret_cast<const int4*>(&it)[tid];
 }
 
-// One thread's row of 128 scores, as softmax_block, where each word of 32 keys is seen whole or
-// not at all (all but a row's own block and blocks of 16): the word's maximum and sum count
-// or not, and its weights are kept or cleared, whatever its scores hold.  (Key by key, as
-// softmax_block masks, a block takes twice the instructions; with a branch around each word that
-// no row of the warp sees it was slower than that.)
+// One thread's row of 128 scores, as softmax_block, with masks that are mostly whole words of
+// 32 keys: a word's maximum and sum count or not, and its weights are kept or cleared,
+// whatever its scores hold.  Only where some row of the warp sees a part of a word (its own
+// block, or half a word of a block of 16) are scores masked key by key first.  (Two
+// instances, one masked throughout, cost 36 us of 416 for the few blocks that need it: 8192 tokens
+// over 32768 keys.)
 template <int D>
 __device__ __forceinline__ void softmax_words(uint32_t tm_s, uint32_t tm_o, bool have_o,
-                                              const uint32_t (&vis)[4], float c, bool live,
-                                              RowState& st) {
+                                              const uint32_t (&vis)[4], bool parts, float c,
+                                              bool live, RowState& st) {
     uint32_t s[4][32];
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
     tc_wait_ld();
+    if (parts) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) prepare32<false, true>(s[i], nullptr, vis[i]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) top = fmaxf(top, vis[i] ? max32(s[i]) : -INFINITY);
     // (-inf - -inf is NaN: no move)
@@ -292,7 +313,7 @@ __device__ __forceinline__ void softmax_words(uint32_t tm_s, uint32_t tm_o, bool
         unf2(add2(part[0], part[1]), x, y);
         st.l += vis[i] ? x + y : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; e++) pk[e] &= vis[i];
+        for (int e = 0; e < 16; e++) pk[e] &= vis[i] ? 0xffffffffu : 0u;
         tc_st16(tm_s + 16 * i, pk);
     }
     tc_wait_st();
@@ -724,20 +745,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint32_t vis[4];
                 look(i, word, vis);
                 word = fetch(i + 1);
-                const bool words = !__any_sync(  // (a word is 0 or all ones)
+                const bool parts = __any_sync(  // (a word that is neither 0 nor all ones)
                     0xffffffffu, vis[0] + 1 > 1 || vis[1] + 1 > 1 || vis[2] + 1 > 1 ||
                                      vis[3] + 1 > 1);
                 ok = warp_wait(&b_s[t], ph & 1, abort_f, p.status);
                 if (!ok) break;
                 ph++;
                 tc_fence_after();
-                if (idle) {
-                    // none of the warp's rows exists: whatever its scores hold weighs no one
-                } else if (words) {
-                    softmax_words<D>(tm_s, tm_o, i > 0, vis, c, live, st);
-                } else {
-                    softmax_block<D, true>(tm_s, tm_o, i > 0, vis, c, live, st);
-                }
+                // (where none of the warp's rows exists, whatever its scores hold weighs no one)
+                if (!idle) softmax_words<D>(tm_s, tm_o, i > 0, vis, parts, c, live, st);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b_p[t]);
