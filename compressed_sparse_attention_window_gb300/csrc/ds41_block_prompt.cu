@@ -160,21 +160,34 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     auto fill = [&](int r0, int size, bool report) {
         for (int x = tid; x < size * W; x += PLAN) table[x] = 0;
         __syncthreads();
-        for (int tok = warp; tok < toks; tok += PLAN / 32) {
-            const int32_t* list = lists + (int64_t)tok * p.kvh * p.topk;
-            const int cur = (p0 + tok) >> p.shift;
-            for (int i0 = 0, last = -1; i0 < p.topk; i0 += 32) {
-                const int x = i0 + lane < p.topk ? list[i0 + lane] : -1;
-                int before = __shfl_up_sync(0xffffffffu, x, 1);
-                if (lane == 0) before = last;
-                last = __shfl_sync(0xffffffffu, x, 31);
-                // it ends at the first entry that does not rise or lies past its token
-                const unsigned bad = __ballot_sync(0xffffffffu, x <= before || x > cur);
-                const int end = bad ? __ffs(bad) - 1 : 32;
-                if (lane < end && x >= r0 && x < r0 + size)
-                    atomicOr(&table[(x - r0) * W + (tok >> 5)], 1u << (tok & 31));
-                if (report && lane == end && x != -1) raise_status(p.status, DS41_E_INDEX);
-                if (bad) break;
+        constexpr int U = 4, NW = PLAN / 32;  // tokens of a warp at a time
+        for (int tok0 = warp; tok0 < toks; tok0 += U * NW) {
+            int x[U];
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                x[u] = tok0 + u * NW < toks && lane < p.topk
+                           ? lists[(int64_t)(tok0 + u * NW) * p.kvh * p.topk + lane]
+                           : -1;
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int tok = tok0 + u * NW;
+                if (tok >= toks) break;
+                const int32_t* list = lists + (int64_t)tok * p.kvh * p.topk;
+                const int cur = (p0 + tok) >> p.shift;
+                for (int i0 = 0, last = -1;; ) {
+                    int before = __shfl_up_sync(0xffffffffu, x[u], 1);
+                    if (lane == 0) before = last;
+                    last = __shfl_sync(0xffffffffu, x[u], 31);
+                    // it ends at the first entry that does not rise or lies past its token
+                    const unsigned bad = __ballot_sync(0xffffffffu, x[u] <= before || x[u] > cur);
+                    const int end = bad ? __ffs(bad) - 1 : 32;
+                    if (lane < end && x[u] >= r0 && x[u] < r0 + size)
+                        atomicOr(&table[(x[u] - r0) * W + (tok >> 5)], 1u << (tok & 31));
+                    if (report && lane == end && x[u] != -1) raise_status(p.status, DS41_E_INDEX);
+                    i0 += 32;
+                    if (bad || i0 >= p.topk) break;
+                    x[u] = i0 + lane < p.topk ? list[i0 + lane] : -1;
+                }
             }
         }
         __syncthreads();
