@@ -12,7 +12,7 @@
 // step of few tokens: a chain of latencies (the page table, the keys, the scores'
 // exchange, the ranking).  For prompts: the products (m16n8k16, blocks by columns of query
 // heads) and the ranking about alike.
-#include "ds41_dense.cuh"
+#include "ds41_softmax_tc.cuh"
 
 namespace ds41 {
 namespace blocks {
@@ -20,28 +20,28 @@ namespace blocks {
 constexpr float STEP = 1.0f / 127.0f;
 constexpr float FLOOR = 127.0f * 0x1p-126f;
 
-// Four elements of a row a lane (0 behind its end): their codes, and the row's scale.
-__device__ __forceinline__ float int8_row(const float (&x)[4], float (&code)[4]) {
-    // (the bits of magnitudes are ordered as they are, infinities and NaN above all)
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 4; e++) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    const bool bad = top >= 0x7f800000u;
-    const float m = __uint_as_float(top);
-    const float s = __fmul_rn(fmaxf(m, FLOOR), STEP);
-    // x / s, correctly rounded, from the correctly rounded reciprocal and the exact remainder of
-    // a fused multiply-add (P. Markstein, 1990).  A scale below 2^-90 and its row are taken
-    // 2^100 times, one above 2^100 and its row 2^-60 times: all of it stays normal.
-    const float f = s < 0x1p-90f ? 0x1p100f : s > 0x1p100f ? 0x1p-60f : 1.0f;
-    const float d = s * f, r = __frcp_rn(d);
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const float y = x[e] * f, q = __fmul_rn(y, r);
-        code[e] = bad ? 0.0f : rintf(__fmaf_rn(__fmaf_rn(q, -d, y), r, q));
+// The int8 form of a row, from the bits of its largest magnitude (they are ordered as the
+// magnitudes are, infinities and NaN above all: the scale is NaN then, the codes 0).
+struct Int8 {
+    float scale;
+    float f, d, r;  // quotients by the scale: see code()
+    __device__ __forceinline__ explicit Int8(uint32_t top) {
+        const bool bad = top >= 0x7f800000u;
+        const float s = __fmul_rn(fmaxf(__uint_as_float(top), FLOOR), STEP);
+        // A scale below 2^-90 and its row are taken 2^100 times, one above 2^100 and its row
+        // 2^-60 times: the remainders stay normal numbers.
+        f = bad ? 0.0f : s < 0x1p-90f ? 0x1p100f : s > 0x1p100f ? 0x1p-60f : 1.0f;
+        d = bad ? 1.0f : s * f;
+        r = __frcp_rn(d);
+        scale = bad ? __uint_as_float(0x7fc00000u) : s;
     }
-    return bad ? __uint_as_float(0x7fc00000u) : s;
-}
+    // rint(x / scale): the quotient correctly rounded, from the correctly rounded reciprocal
+    // and the exact remainder of a fused multiply-add (P. Markstein, 1990).
+    __device__ __forceinline__ float code(float x) const {
+        const float y = f == 0.0f ? 0.0f : x * f, q = __fmul_rn(y, r);
+        return rintf(__fmaf_rn(__fmaf_rn(q, -d, y), r, q));
+    }
+};
 
 struct KeyArgs {
     PagedKv kv;
@@ -120,17 +120,20 @@ __global__ void __launch_bounds__(KEY_WARPS * 32) keys_kernel(const KeyArgs a) {
                     for (int e = 0; e < 4; e++) sum[e] = __fadd_rn(sum[e], x[e]);
             }
         }
-        float code[4];
+        uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; e++) sum[e] = mine ? __fdiv_rn(sum[e], (float)n) : 0.0f;
-        const float s = int8_row(sum, code);
+        for (int e = 0; e < 4; e++) {
+            sum[e] = mine ? __fdiv_rn(sum[e], (float)n) : 0.0f;
+            top = max(top, __float_as_uint(sum[e]) & 0x7fffffffu);
+        }
+        const Int8 key(__reduce_max_sync(0xffffffffu, top));
         if (mine) {
             uint32_t c = 0;
 #pragma unroll
-            for (int e = 0; e < 4; e++) c |= ((uint32_t)(int)code[e] & 0xffu) << (8 * e);
+            for (int e = 0; e < 4; e++) c |= ((uint32_t)(int)key.code(sum[e]) & 0xffu) << (8 * e);
             *reinterpret_cast<uint32_t*>(a.codes + (pg * a.kv.kvh + h) * a.kv.hd + lane * 4) = c;
         }
-        if (lane == 0) a.scales[pg * a.kv.kvh + h] = s;
+        if (lane == 0) a.scales[pg * a.kv.kvh + h] = key.scale;
     }
 }
 
@@ -151,7 +154,8 @@ struct SelectArgs {
     unsigned int* status;
 };
 
-constexpr int SEL_WARPS = 8;
+template <bool FEW>
+constexpr int SELECT_WARPS = FEW ? 8 : 16;  // of a CTA
 
 // four int8 codes -> their values as f16, exactly: a code plus 128 in the low bits of 1024
 __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
@@ -175,11 +179,39 @@ __device__ __forceinline__ float score_of(uint32_t rank) {
     return __uint_as_float((rank >> 31) ? rank ^ 0x80000000u : ~rank);
 }
 
+// Where the k-th largest of m ranks would be if their scores were normally distributed
+// (mean and spread from every second register; the quantile by Hastings' approximation,
+// Abramowitz and Stegun 26.2.22), and what a doubling of the count moves it by there.
+template <int R>
+__device__ __forceinline__ float normal(const uint32_t (&v)[R], int m, int k, int lane,
+                                        float& slope) {
+    float sum = 0.0f, squares = 0.0f;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R; i += 2) {
+        const float x = 32 * i + lane < m ? score_of(v[i]) : 0.0f;
+        sum += x;
+        squares += x * x;
+        n += max(0, min(32, m - 32 * i));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        squares += __shfl_xor_sync(0xffffffffu, squares, o);
+    }
+    const float mean = sum / n, spread = sqrtf(fmaxf(squares / n - mean * mean, 0.0f));
+    const float t = sqrtf(-2.0f * tc::SM_LN2 * tc::lg2(fminf((float)k / (float)m, 0.5f)));
+    const float z = t - (2.30753f + 0.27061f * t) / (1.0f + t * (0.99229f + 0.04481f * t));
+    slope = spread / z * tc::SM_LN2 * 1.3f;
+    return mean + spread * z;
+}
+
 // A warp: the k of m > k ranks at s, ties to the first, ascending to out as j0 + place.  The
-// k-th largest is found by halving what lies between the smallest rank and the largest:
-// first as scores, which lie evenly enough for about ten counts of all ranks (as integers,
-// bit by bit, it is 30), and as integers if that has not ended it.  R: registers of a lane,
-// 32 R ranks at most; 0: the ranks stay in shared memory.
+// k-th largest is looked for between the smallest rank and the largest: where it would be
+// among normally distributed scores, then by halving what is left, as scores (about five
+// counts of all ranks in all, where bit by bit it is 30; a guess that is wrong, or no number,
+// costs a count), and as integers if that has not ended it.  R: registers of a lane, 32 R
+// ranks at most; 0: the ranks stay in shared memory.
 template <int R>
 __device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* out, int j0,
                                      int lane) {
@@ -214,14 +246,18 @@ __device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* o
     // more than k ranks from lo on, at most k from hi on: `above`
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi) + 1;
-    int above = 0;
+    int above = 0, n = m;
+    float slope = 0.0f, at = 0.0f;
     for (int i = 0; above < k && hi - lo > 1; i++) {
         uint32_t mid = lo + (hi - lo) / 2;
         if (i < 16) {
-            const uint32_t x = rank_of(0.5f * score_of(lo) + 0.5f * score_of(hi));
+            if (R && i == 0) at = normal<N>(v, m, k, lane, slope);
+            else if (R && i == 1) at += slope * tc::lg2((float)n / (float)k);
+            else at = 0.5f * score_of(lo) + 0.5f * score_of(hi);
+            const uint32_t x = rank_of(at);
             if (x > lo && x < hi) mid = x;
         }
-        const int n = count(mid);
+        n = count(mid);
         if (n > k) {
             lo = mid;
         } else {
@@ -230,7 +266,7 @@ __device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* o
         }
     }
     // all from hi on, and the first of those equal to lo
-    int ties = k - above, at = 0;
+    int ties = k - above, to = 0;
     const uint32_t below = (1u << lane) - 1u;
     auto put = [&](uint32_t x, int j) {
         bool take = x >= hi;
@@ -240,8 +276,8 @@ __device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* o
             ties -= min(ties, __popc(eq));
         }
         const uint32_t all = __ballot_sync(0xffffffffu, take);
-        if (take) out[at + __popc(all & below)] = j0 + j;
-        at += __popc(all);
+        if (take) out[to + __popc(all & below)] = j0 + j;
+        to += __popc(all);
     };
     if (R) {
 #pragma unroll
@@ -257,9 +293,10 @@ __device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* o
 // has all heads of its token and their maximum takes no exchange.  hd in the order of tree
 // attention's e4m3 fragments: lane c owns the codes 16 c .. and 64 + 16 c .. of a row.
 // FEW: a few tokens, one CTA an SM or so: the next blocks' codes are under way while the products
-// of these run.  Else four CTAs an SM hide that.
+// of these run.  Else 32 warps an SM hide that.
 template <int HD, bool FEW>
-__global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const SelectArgs a) {
+    constexpr int SEL_WARPS = SELECT_WARPS<FEW>;
     pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(16) uint8_t smem[];
@@ -281,8 +318,8 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
     const int vis = ((p0 + toks - 1) >> a.page_shift) + 1;  // blocks that some token sees
     // shared memory: the queries' fragments, their scales, the scores
     const int pairs = a.heads / 2;
-    uint2* frag = reinterpret_cast<uint2*>(smem);  // [quad][pair][two k steps][32][2]
-    float* qs = reinterpret_cast<float*>(frag + (a.TT + 3) / 4 * pairs * KS * 32);  // [token][heads]
+    uint4* frag = reinterpret_cast<uint4*>(smem);  // [quad][pair][two k steps][32]
+    float* qs = reinterpret_cast<float*>(frag + (a.TT + 3) / 4 * pairs * KS * 16);  // [token][heads]
     uint32_t* sc = reinterpret_cast<uint32_t*>(qs + (a.TT + 3) / 4 * 4 * a.heads);  // [token][NB]
     const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
@@ -318,42 +355,49 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
             fetch();
             look(warp * 16 + ROUND);
         }
-        // the queries, four rows at a time
-        const int rows = quads * 4 * hp * 2;
-        for (int x0 = warp; x0 < rows; x0 += 4 * SEL_WARPS) {
-            uint2 w[4];
+        // the queries: half a warp a row, eight elements a lane, two rows of each half at a time
+        const int rows = quads * 4 * hp * 2, half = lane >> 4, l = lane & 15;
+        const int by = (65536 + 2 * hp - 1) / (2 * hp);  // x / (2 hp), x at most 32 * 32
+        for (int x0 = 2 * warp + half; x0 < rows; x0 += 4 * SEL_WARPS) {
+            uint4 w[2];
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const int x = x0 + u * SEL_WARPS, t = x / (2 * hp), y = x - t * 2 * hp;
-                w[u] = make_uint2(0, 0);
-                if (t < toks && y < hs && lane * 4 < a.hd)
-                    w[u] = *reinterpret_cast<const uint2*>(a.q + (q0 + t0 + t) * a.q_tok +
+            for (int u = 0; u < 2; u++) {
+                const int x = x0 + u * 2 * SEL_WARPS, t = (x * by) >> 16, y = x - t * 2 * hp;
+                w[u] = make_uint4(0, 0, 0, 0);
+                if (t < toks && y < hs && l * 8 < a.hd)
+                    w[u] = *reinterpret_cast<const uint4*>(a.q + (q0 + t0 + t) * a.q_tok +
                                                            ((int64_t)h * a.G + h0 + y) * a.q_head +
-                                                           lane * 4);
+                                                           l * 8);
             }
 #pragma unroll
-            for (int u = 0; u < 4; u++) {
-                const int x = x0 + u * SEL_WARPS, t = x / (2 * hp), y = x - t * 2 * hp;
-                if (x >= rows) break;
-                const float v[4] = {
-                    __uint_as_float(w[u].x << 16), __uint_as_float(w[u].x & 0xffff0000u),
-                    __uint_as_float(w[u].y << 16), __uint_as_float(w[u].y & 0xffff0000u)};
-                float code[4];
-                const float s = int8_row(v, code);
-                if (lane * 4 < HD) {
-                    const __half2 lo = __floats2half2_rn(code[0], code[1]);
-                    const __half2 hi = __floats2half2_rn(code[2], code[3]);
-                    const int piece = lane >> 2;
-                    const int st = (piece >> 2) * 4 + (lane & 3), col = 2 * (t & 3) + (y & 1);
-                    // (two steps' words side by side)
-                    frag[((((t >> 2) * pairs + (y >> 1)) * KS + (st & ~1)) * 32 +
-                          (col * 4 + (piece & 3)) * 2) + (st & 1)] =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                   *reinterpret_cast<const uint32_t*>(&hi));
+            for (int u = 0; u < 2; u++) {
+                const int x = x0 + u * 2 * SEL_WARPS, t = (x * by) >> 16, y = x - t * 2 * hp;
+                uint32_t top = __vmaxu2(__vmaxu2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu),
+                                        __vmaxu2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+                    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const Int8 r(max(top & 0xffffu, top >> 16) << 16);
+                const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                uint32_t out[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const __half2 c2 =
+                        __floats2half2_rn(r.code(__uint_as_float(in[e] << 16)),
+                                          r.code(__uint_as_float(in[e] & 0xffff0000u)));
+                    out[e] = *reinterpret_cast<const uint32_t*>(&c2);
+                }
+                if (x >= rows) continue;
+                // elements 8 l ..: two steps' words of lane (column, l / 2 % 4), side by side
+                if (l * 8 < HD) {
+                    const int st = (l >> 3) * 4 + 2 * (l & 1), col = 2 * (t & 3) + (y & 1);
+                    frag[(((t >> 2) * pairs + (y >> 1)) * KS + st) * 16 + col * 4 +
+                         ((l >> 1) & 3)] = make_uint4(out[0], out[1], out[2], out[3]);
                 }
                 // (a head that is not there does not count)
-                if (lane == 0)
-                    qs[t * a.heads + y] = t < toks && y < hs ? s : __uint_as_float(0x7fc00000u);
+                if (l == 0)
+                    qs[t * a.heads + y] =
+                        t < toks && y < hs ? r.scale : __uint_as_float(0x7fc00000u);
             }
         }
         __syncthreads();
@@ -382,8 +426,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
                 const int t = qd * 4 + c;
                 float best[2] = {__uint_as_float(0x7fc00000u), __uint_as_float(0x7fc00000u)};
                 for (int i = 0; i < hp; i++) {
-                    const uint4* f =
-                        reinterpret_cast<const uint4*>(frag + (qd * pairs + i) * KS * 32) + lane;
+                    const uint4* f = frag + (qd * pairs + i) * KS * 16 + lane;
                     float d[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int st = 0; st < KS; st += 2) {
@@ -396,20 +439,21 @@ __global__ void __launch_bounds__(SEL_WARPS * 32, FEW ? 2 : 4) select_kernel(con
                     best[0] = fmaxf(best[0], fmaxf(__fmul_rn(d[0], s.x), __fmul_rn(d[1], s.y)));
                     best[1] = fmaxf(best[1], fmaxf(__fmul_rn(d[2], s.x), __fmul_rn(d[3], s.y)));
                 }
-                if (t < toks)
+                if (t >= toks) continue;
+                uint32_t* to = sc + t * a.NB + j0 + g;
 #pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const int j = j0 + g + 8 * r;
-                        if (j >= vis) continue;
-                        uint32_t* to = sc + t * a.NB + j;
-                        float s = best[r];
+                for (int r = 0; r < 2; r++, to += 8) {
+                    if (j0 + g + 8 * r >= vis) break;
+                    float s = best[r];
+                    if (a.heads < a.G) {  // the group's heads come in turns
                         if (h0 > 0) s = fmaxf(s, __uint_as_float(*to));
                         if (h0 + a.heads < a.G) {
                             *to = __float_as_uint(s);
                             continue;
                         }
-                        *to = rank_of(__fmul_rn(s, ks[r]));
                     }
+                    *to = rank_of(__fmul_rn(s, ks[r]));
+                }
             }
         }
         __syncthreads();
@@ -544,8 +588,8 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
     a.first = (int)first;
     a.local = (int)local;
     if (int rc = status_word(&a.status)) return rc;
-    // Tokens of a CTA: 32, or what their scores leave room for (four CTAs an SM, two of few
-    // tokens), or all; query heads at a time: a group, or 32 of it.
+    // Tokens of a CTA: 32, or what their scores leave room for (two CTAs an SM), or all; query
+    // heads at a time: a group, or 32 of it.
     a.NB = (int)((max_len + page - 1) / page + 31) / 32 * 32 + 8;
     a.heads = a.G >= 32 ? 32 : (a.G + 1) / 2 * 2;
     const int HD = hd <= 64 ? 64 : 128;
@@ -556,7 +600,7 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
     };
     const bool few = a.max_q <= 4;
     a.TT = a.max_q < 32 ? a.max_q : 32;
-    while (a.TT > 1 && bytes(a.TT) > (few ? 110 : 55) * 1024)
+    while (a.TT > 1 && bytes(a.TT) > 110 * 1024)
         a.TT = a.TT > 4 ? (a.TT - 1) / 4 * 4 : a.TT - 1;
     const size_t smem = bytes(a.TT);
     constexpr int MOST = 224 * 1024;
@@ -570,5 +614,5 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
         return rc;
     return launch_pdl(kern,
                       dim3((unsigned)((a.max_q + a.TT - 1) / a.TT), (unsigned)B, (unsigned)kvh),
-                      dim3(blocks::SEL_WARPS * 32), smem, (cudaStream_t)stream, name, a);
+                      dim3((few ? blocks::SELECT_WARPS<true> : blocks::SELECT_WARPS<false>) * 32), smem, (cudaStream_t)stream, name, a);
 }
