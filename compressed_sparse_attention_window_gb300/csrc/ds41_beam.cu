@@ -132,6 +132,15 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
     auto fetch = [&](int step) {
         const int s0 = j0 + (step * WARPS + warp) * STEP;  // (a multiple of VE)
         const uint32_t to = ring_u + step % STAGES * STAGE<T>;
+        if (s0 > 0 && s0 + STEP + VE <= j1) {  // whole pieces
+            const T* at = base + s0 + lane * VE;
+#pragma unroll
+            for (int u = 0; u < PIECES / 32; u++)
+                cp_async16(to + (u * 32 + lane) * 16, at + u * 32 * VE, true);
+            if (lane == 0) cp_async16(to + PIECES * 16, at + PIECES * VE, true);
+            cp_async_commit();
+            return;
+        }
 #pragma unroll
         for (int u = 0; u < PIECES / 32 + 1; u++) {
             const int i = u * 32 + lane;
