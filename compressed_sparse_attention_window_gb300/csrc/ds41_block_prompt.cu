@@ -281,24 +281,32 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
 // One thread's row of 128 scores, as softmax_block, with masks that are mostly whole words of
 // 32 keys: a word's maximum and sum count or not, and its weights are kept or cleared,
 // whatever its scores hold.  Only where some row of the warp sees a part of a word (its own
-// block, or half a word of a block of 16) are scores masked key by key first.  (Two
-// instances, one masked throughout, cost 36 us of 416 for the few blocks that need it: 8192 tokens
-// over 32768 keys.)
+// block, or half a word of a block of 16) are scores masked key by key first.  The
+// weights are worked out a word at a time in a loop, the scores read once more from tensor
+// memory: unrolled, with all scores in registers, the code streams through the instruction
+// caches at every step.  (8192 tokens over 32768 keys: 354 us; unrolled 389; with a second
+// instance that masks throughout, for the few steps that need it, 416.)
 template <int D>
 __device__ __forceinline__ void softmax_words(uint32_t tm_s, uint32_t tm_o, bool have_o,
                                               const uint32_t (&vis)[4], bool parts, float c,
                                               bool live, RowState& st) {
-    uint32_t s[4][32];
     float top = -INFINITY;
+    {
+        uint32_t s[4][32];
 #pragma unroll
-    for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
-    tc_wait_ld();
-    if (parts) {
+        for (int i = 0; i < 4; i++) tc_ld32(tm_s + 32 * i, s[i]);
+        tc_wait_ld();
+        if (parts) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) prepare32<false, true>(s[i], nullptr, vis[i]);
+            for (int i = 0; i < 4; i++) {
+                prepare32<false, true>(s[i], nullptr, vis[i]);
+                tc_st32(tm_s + 32 * i, s[i]);
+            }
+            tc_wait_st();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) top = fmaxf(top, vis[i] ? max32(s[i]) : -INFINITY);
     }
-#pragma unroll
-    for (int i = 0; i < 4; i++) top = fmaxf(top, vis[i] ? max32(s[i]) : -INFINITY);
     // (-inf - -inf is NaN: no move)
     const bool move = (top - st.m) * c > SM_RESCALE_LOG2 && live;
     if (__any_sync(0xffffffffu, move)) {
@@ -307,26 +315,33 @@ __device__ __forceinline__ void softmax_words(uint32_t tm_s, uint32_t tm_o, bool
         st.l *= f;
         if (have_o) rescale<D>(tm_o, f);
     }
-    float base = st.m == -INFINITY ? 0.0f : st.m * c;
+    float base = st.m == -INFINITY ? 0.0f : st.m * c, less = 0.0f;
     if (fabsf(base) > 0x1p22f) {
         // c m itself is rounded by more than a fraction of one power of two: take
         // the differences first
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int e = 0; e < 32; e++) s[i][e] = __float_as_uint(u2f(s[i][e]) - st.m);
+        less = st.m;
         base = 0.0f;
     }
-#pragma unroll
+    const bool far = __any_sync(0xffffffffu, less != 0.0f);
+    const uint32_t seen =
+        (vis[0] ? 1u : 0u) | (vis[1] ? 2u : 0u) | (vis[2] ? 4u : 0u) | (vis[3] ? 8u : 0u);
+#pragma unroll 1
     for (int i = 0; i < 4; i++) {
-        uint32_t pk[16];
+        uint32_t s[32], pk[16];
+        tc_ld32(tm_s + 32 * i, s);
+        tc_wait_ld();
+        if (far) {
+#pragma unroll
+            for (int e = 0; e < 32; e++) s[e] = __float_as_uint(u2f(s[e]) - less);
+        }
         uint64_t part[2] = {0, 0};
-        weights32<false, false>(s[i], pk, c, base, nullptr, 0, part);
+        weights32<false, false>(s, pk, c, base, nullptr, 0, part);
         float x, y;
         unf2(add2(part[0], part[1]), x, y);
-        st.l += vis[i] ? x + y : 0.0f;
+        const bool on = (seen >> i) & 1;
+        st.l += on ? x + y : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; e++) pk[e] &= vis[i] ? 0xffffffffu : 0u;
+        for (int e = 0; e < 16; e++) pk[e] &= on ? 0xffffffffu : 0u;
         tc_st16(tm_s + 16 * i, pk);
     }
     tc_wait_st();
