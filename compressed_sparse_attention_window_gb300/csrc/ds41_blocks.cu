@@ -206,85 +206,155 @@ __device__ __forceinline__ float normal(const uint32_t (&v)[R], int m, int k, in
     return mean + spread * z;
 }
 
-// A warp: the k of m > k ranks at s, ties to the first, ascending to out as j0 + place.  The
-// k-th largest is looked for between the smallest rank and the largest: where it would be
-// among normally distributed scores, then by halving what is left, as scores (about five
-// counts of all ranks in all, where bit by bit it is 30; a guess that is wrong, or no number,
-// costs a count), and as integers if that has not ended it.  R: registers of a lane, 32 R
-// ranks at most; 0: the ranks stay in shared memory.
+// Where the k-th largest of m > k ranks lies (a warp, 32 R of them in registers, 0 behind the
+// last): more than k ranks are lo or above, `above` <= k are hi or above.  Looked for between
+// the smallest and the largest: where it would be among normally distributed scores, then by
+// halving what is left, as scores (about five counts of all ranks in all, where bit by bit
+// it is 30; a guess that is wrong, or no number, costs a count), and as integers if that
+// has not ended it.  It ends with above == k, with nothing between lo and hi, or, with
+// slack, once at most k + slack are lo or above.
+struct Cut {
+    uint32_t lo, hi;
+    int above;
+};
 template <int R>
-__device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* out, int j0,
-                                     int lane) {
-    constexpr int N = R ? R : 1;
-    uint32_t v[N];
-    uint32_t lo = 0xffffffffu, hi = 0;
-    if (R) {
+__device__ __forceinline__ Cut cut(const uint32_t (&v)[R], int m, int k, int slack, int lane) {
+    Cut c{0xffffffffu, 0, 0};
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            const bool in = 32 * i + lane < m;
-            v[i] = in ? s[32 * i + lane] : 0;
-            lo = min(lo, in ? v[i] : 0xffffffffu);
-            hi = max(hi, v[i]);
-        }
-    } else {
-        for (int j = lane; j < m; j += 32) {
-            lo = min(lo, s[j]);
-            hi = max(hi, s[j]);
-        }
+    for (int i = 0; i < R; i++) {
+        c.lo = min(c.lo, 32 * i + lane < m ? v[i] : 0xffffffffu);
+        c.hi = max(c.hi, v[i]);
     }
-    auto count = [&](uint32_t least) {
-        int n = 0;
-        if (R) {
-#pragma unroll
-            for (int i = 0; i < N; i++) n += v[i] >= least;
-        } else {
-#pragma unroll 8
-            for (int j = lane; j < m; j += 32) n += s[j] >= least;
-        }
-        return __reduce_add_sync(0xffffffffu, n);
-    };
-    // more than k ranks from lo on, at most k from hi on: `above`
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi) + 1;
-    int above = 0, n = m;
+    c.lo = __reduce_min_sync(0xffffffffu, c.lo);
+    c.hi = __reduce_max_sync(0xffffffffu, c.hi) + 1;
+    int n = m, n_lo = m;
     float slope = 0.0f, at = 0.0f;
-    for (int i = 0; above < k && hi - lo > 1; i++) {
-        uint32_t mid = lo + (hi - lo) / 2;
+    for (int i = 0; c.above < k && (slack == 0 || n_lo > k + slack) && c.hi - c.lo > 1; i++) {
+        uint32_t mid = c.lo + (c.hi - c.lo) / 2;
         if (i < 16) {
-            if (R && i == 0) at = normal<N>(v, m, k, lane, slope);
-            else if (R && i == 1) at += slope * tc::lg2((float)n / (float)k);
-            else at = 0.5f * score_of(lo) + 0.5f * score_of(hi);
+            if (i == 0) at = normal<R>(v, m, k, lane, slope);
+            else if (i == 1) at += slope * tc::lg2((float)n / (float)k);
+            else at = 0.5f * score_of(c.lo) + 0.5f * score_of(c.hi);
             const uint32_t x = rank_of(at);
-            if (x > lo && x < hi) mid = x;
+            if (x > c.lo && x < c.hi) mid = x;
         }
-        n = count(mid);
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < R; i++) n += v[i] >= mid;
+        n = __reduce_add_sync(0xffffffffu, n);
         if (n > k) {
-            lo = mid;
+            c.lo = mid;
+            n_lo = n;
         } else {
-            hi = mid;
-            above = n;
+            c.hi = mid;
+            c.above = n;
         }
     }
-    // all from hi on, and the first of those equal to lo
-    int ties = k - above, to = 0;
-    const uint32_t below = (1u << lane) - 1u;
-    auto put = [&](uint32_t x, int j) {
+    return c;
+}
+// What a cut leaves, written in order: all from hi on, and the first of those equal to lo.
+struct Writer {
+    int32_t* out;
+    int ties, to, lane;
+    uint32_t lo, hi;
+    __device__ __forceinline__ Writer(int32_t* out, const Cut& c, int k, int lane)
+        : out(out), ties(k - c.above), to(0), lane(lane), lo(c.lo), hi(c.hi) {}
+    // (a lane's rank x of block j; real: there is one)
+    __device__ __forceinline__ void put(uint32_t x, int j, bool real) {
+        const uint32_t below = (1u << lane) - 1u;
         bool take = x >= hi;
         if (ties > 0) {
-            const uint32_t eq = __ballot_sync(0xffffffffu, x == lo && j < m);
-            take |= x == lo && j < m && __popc(eq & below) < ties;
+            const uint32_t eq = __ballot_sync(0xffffffffu, x == lo && real);
+            take |= x == lo && real && __popc(eq & below) < ties;
             ties -= min(ties, __popc(eq));
         }
         const uint32_t all = __ballot_sync(0xffffffffu, take);
-        if (take) out[to + __popc(all & below)] = j0 + j;
+        if (take) out[to + __popc(all & below)] = j;
         to += __popc(all);
-    };
-    if (R) {
-#pragma unroll
-        for (int i = 0; i < N; i++) put(v[i], 32 * i + lane);
-    } else {
-        for (int j = 0; j < m; j += 32) put(j + lane < m ? s[j + lane] : 0, j + lane);
     }
+};
+
+// The k of m > k ranks at s, at most 32 R of them, by a warp: ties to the first, ascending to
+// out as j0 + place.
+template <int R>
+__device__ __forceinline__ void pick(const uint32_t* s, int m, int k, int32_t* out, int j0,
+                                     int lane) {
+    uint32_t v[R];
+#pragma unroll
+    for (int i = 0; i < R; i++) v[i] = 32 * i + lane < m ? s[32 * i + lane] : 0;
+    Writer w(out, cut(v, m, k, 0, lane), k, lane);
+#pragma unroll
+    for (int i = 0; i < R; i++) w.put(v[i], j0 + 32 * i + lane, 32 * i + lane < m);
+}
+
+// The same of any number.  First those that may be among the k: from a sample of 128,
+// evenly spread, follows a bound that at least k reach (the k-th largest of some is never
+// above that of all) and about m / 100 k others; their places go to `list`, 16 bits each,
+// and they alone are cut.  (Up to 512 ranks the registers of pick hold, and two cuts cost
+// more than one: 448 ranks, 29 of them, 219 us for a chunk's selection, this way 240.)
+constexpr int LIST = 256;
+__device__ __forceinline__ void pick_of_many(const uint32_t* s, int m, int k, int32_t* out,
+                                             int j0, uint16_t* list, int lane) {
+    uint32_t v[LIST / 32];
+    auto count = [&](uint32_t least) {
+        int n = 0;
+#pragma unroll 8
+        for (int j = lane; j < m; j += 32) n += s[j] >= least;
+        return __reduce_add_sync(0xffffffffu, n);
+    };
+    // a bound that at least k ranks reach
+    uint32_t lo = 1, hi = 0;
+    if (3 * k <= 128) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[i] = s[((32 * i + lane) * m) >> 7];
+        const Cut c = cut(x, 128, k, k / 4 + 2, lane);
+        lo = c.above == k ? c.hi : c.lo;
+    }
+    for (int j = lane; j < m; j += 32) hi = max(hi, s[j]);
+    hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+    // raised until the list holds those that do; `above` < k are hi or above
+    int n = count(lo), above = 0;
+    for (int i = 0; n > LIST && hi - lo > 1; i++) {
+        uint32_t mid = lo + (hi - lo) / 2;
+        const uint32_t x = rank_of(0.5f * score_of(lo) + 0.5f * score_of(hi));
+        if (i < 16 && x > lo && x < hi) mid = x;
+        const int at_mid = count(mid);
+        if (at_mid >= k) {
+            lo = mid;
+            n = at_mid;
+        } else {
+            hi = mid;
+            above = at_mid;
+        }
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    if (n > LIST) {  // (equal scores in masses)
+        Writer w(out, Cut{lo, hi, above}, k, lane);
+        for (int j = 0; j < m; j += 32)
+            w.put(j + lane < m ? s[j + lane] : 0, j0 + j + lane, j + lane < m);
+        return;
+    }
+    int to = 0;
+#pragma unroll 4
+    for (int j = 0; j < m; j += 32) {
+        const bool keep = j + lane < m && s[j + lane] >= lo;
+        const uint32_t all = __ballot_sync(0xffffffffu, keep);
+        if (keep) list[to + __popc(all & below)] = (uint16_t)(j + lane);
+        to += __popc(all);
+    }
+    __syncwarp();
+    int place[LIST / 32];
+#pragma unroll
+    for (int i = 0; i < LIST / 32; i++) {
+        place[i] = 32 * i + lane < n ? list[32 * i + lane] : 0;
+        v[i] = 32 * i + lane < n ? s[place[i]] : 0;
+    }
+    const Cut c = n == k ? Cut{0, 1, k} : cut(v, n, k, 0, lane);
+    Writer w(out, c, k, lane);
+#pragma unroll
+    for (int i = 0; i < LIST / 32; i++) w.put(v[i], j0 + place[i], 32 * i + lane < n);
+    __syncwarp();  // (the list is the warp's next token's, too)
 }
 
 // Scores of TT tokens of a sequence for one key/value head, then the tokens' picks.
@@ -321,6 +391,7 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
     uint4* frag = reinterpret_cast<uint4*>(smem);  // [quad][pair][two k steps][32]
     float* qs = reinterpret_cast<float*>(frag + (a.TT + 3) / 4 * pairs * KS * 16);  // [token][heads]
     uint32_t* sc = reinterpret_cast<uint32_t*>(qs + (a.TT + 3) / 4 * 4 * a.heads);  // [token][NB]
+    uint16_t* lists = reinterpret_cast<uint16_t*>(sc + a.TT * a.NB);               // [warp][LIST]
     const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
     for (int h0 = 0; h0 < a.G; h0 += a.heads) {
@@ -474,13 +545,9 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
         s += a.first;
         out += a.first;
         if (k == 0) continue;
-        if (m <= 256) {
-            pick<8>(s, m, k, out, a.first, lane);
-        } else if (m <= 512) {
-            pick<16>(s, m, k, out, a.first, lane);
-        } else {
-            pick<0>(s, m, k, out, a.first, lane);
-        }
+        if (m <= 256) pick<8>(s, m, k, out, a.first, lane);
+        else if (m <= 512) pick<16>(s, m, k, out, a.first, lane);
+        else pick_of_many(s, m, k, out, a.first, lists + warp * LIST, lane);
     }
 }
 
@@ -593,12 +660,12 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
     a.NB = (int)((max_len + page - 1) / page + 31) / 32 * 32 + 8;
     a.heads = a.G >= 32 ? 32 : (a.G + 1) / 2 * 2;
     const int HD = hd <= 64 ? 64 : 128;
+    const bool few = a.max_q <= 4;
     auto bytes = [&](int tt) {
         const int quads = (tt + 3) / 4;
         return (size_t)quads * (a.heads / 2) * (HD / 16) * 256 + (size_t)quads * 16 * a.heads +
-               (size_t)tt * a.NB * 4;
+               (size_t)tt * a.NB * 4 + (few ? 8 : 16) * blocks::LIST * 2;
     };
-    const bool few = a.max_q <= 4;
     a.TT = a.max_q < 32 ? a.max_q : 32;
     while (a.TT > 1 && bytes(a.TT) > 110 * 1024)
         a.TT = a.TT > 4 ? (a.TT - 1) / 4 * 4 : a.TT - 1;
