@@ -151,6 +151,7 @@ struct SelectArgs {
     int TT;       // tokens of a CTA
     int NB;       // room for a token's scores: tokens next to each other in different banks
     int heads;    // query heads at a time, even
+    int runs;     // CTAs that share the blocks of a few tokens: a cluster
     unsigned int* status;
 };
 
@@ -363,7 +364,8 @@ __device__ __forceinline__ void pick_of_many(const uint32_t* s, int m, int k, in
 // has all heads of its token and their maximum takes no exchange.  hd in the order of tree
 // attention's e4m3 fragments: lane c owns the codes 16 c .. and 64 + 16 c .. of a row.
 // FEW: a few tokens, one CTA an SM or so: the next blocks' codes are under way while the products
-// of these run.  Else 32 warps an SM hide that.
+// of these run (else 32 warps an SM hide that); where there are fewer CTAs than that, a
+// cluster shares the blocks, and each token's scores go to the CTA that picks for it.
 template <int HD, bool FEW>
 __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const SelectArgs a) {
     constexpr int SEL_WARPS = SELECT_WARPS<FEW>;
@@ -381,11 +383,14 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
         if (blockIdx.x == 0 && h == 0 && tid == 0) raise_status(a.status, DS41_E_INDEX);
         return;
     }
-    const int n = (int)n64, t0 = blockIdx.x * a.TT;
+    const int runs = FEW ? a.runs : 1, run = FEW ? (int)blockIdx.x % runs : 0;
+    const int n = (int)n64, t0 = (FEW ? (int)blockIdx.x / runs : (int)blockIdx.x) * a.TT;
     if (t0 >= n) return;
     const int toks = min(a.TT, n - t0), quads = (toks + 3) / 4;
     const int p0 = len - n + t0;                           // the first token's place
     const int vis = ((p0 + toks - 1) >> a.page_shift) + 1;  // blocks that some token sees
+    // (nobody writes into a CTA that has not started)
+    if (FEW && runs > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
     // shared memory: the queries' fragments, their scales, the scores
     const int pairs = a.heads / 2;
     uint4* frag = reinterpret_cast<uint4*>(smem);  // [quad][pair][two k steps][32]
@@ -420,11 +425,11 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
                 }
             }
         };
-        constexpr int ROUND = SEL_WARPS * 16;
-        look(warp * 16);
+        const int round = runs * SEL_WARPS * 16, start = (run * SEL_WARPS + warp) * 16;
+        look(start);
         if (FEW) {
             fetch();
-            look(warp * 16 + ROUND);
+            look(start + round);
         }
         // the queries: half a warp a row, eight elements a lane, two rows of each half at a time
         const int rows = quads * 4 * hp * 2, half = lane >> 4, l = lane & 15;
@@ -472,11 +477,12 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
             }
         }
         __syncthreads();
-        for (int j0 = warp * 16; j0 < vis; j0 += ROUND) {
+        if (FEW && runs > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+        for (int j0 = start; j0 < vis; j0 += round) {
             uint32_t af[KS][4];
             if (!FEW) {
                 fetch();
-                look(j0 + ROUND);
+                look(j0 + round);
             }
             const float ks[2] = {scale[0], scale[1]};
 #pragma unroll
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
                 }
             if (FEW) {
                 fetch();
-                look(j0 + 2 * ROUND);
+                look(j0 + 2 * round);
             }
             for (int qd = 0; qd < quads; qd++) {
                 const int t = qd * 4 + c;
@@ -523,14 +529,25 @@ __global__ void __launch_bounds__(SELECT_WARPS<FEW> * 32, 2) select_kernel(const
                             continue;
                         }
                     }
-                    *to = rank_of(__fmul_rn(s, ks[r]));
+                    const uint32_t rank = rank_of(__fmul_rn(s, ks[r]));
+                    if (FEW && runs > 1)
+                        asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(
+                                         cluster_addr(to, t % runs)),
+                                     "r"(rank)
+                                     : "memory");
+                    else
+                        *to = rank;
                 }
             }
         }
         __syncthreads();
     }
+    if (FEW && runs > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                     "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     // ---- the picks: a warp for a token ----
     for (int t = warp; t < toks; t += SEL_WARPS) {
+        if (FEW && t % runs != run) continue;
         const uint32_t* s = sc + t * a.NB;
         const int cur = (p0 + t) >> a.page_shift;
         int32_t* out = a.idx + ((int64_t)(q0 + t0 + t) * a.kvh + h) * a.topk;
@@ -679,7 +696,26 @@ extern "C" int ds41_block_select(const ds41_bf16* q, int64_t q_tok, int64_t q_he
                           : (few ? allow_smem<blocks::select_kernel<128, true>>(MOST, name)
                                  : allow_smem<blocks::select_kernel<128, false>>(MOST, name)))
         return rc;
-    return launch_pdl(kern,
-                      dim3((unsigned)((a.max_q + a.TT - 1) / a.TT), (unsigned)B, (unsigned)kvh),
-                      dim3((few ? blocks::SELECT_WARPS<true> : blocks::SELECT_WARPS<false>) * 32), smem, (cudaStream_t)stream, name, a);
+    const unsigned tiles = (unsigned)((a.max_q + a.TT - 1) / a.TT);
+    // CTAs of a cluster: what two an SM leave room for, of a round of blocks each; heads that
+    // come in turns read their scores back, which only a CTA's own are for
+    const int64_t fit = 2 * (int64_t)sm_count_once() / ((int64_t)tiles * B * kvh);
+    const int64_t rounds = (max_len / page + 127) / 128;
+    int64_t runs = !few || a.heads < a.G ? 1 : fit < rounds ? fit : rounds;
+    a.runs = (int)(runs < 1 ? 1 : runs < 8 ? runs : 8);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * (unsigned)a.runs, (unsigned)B, (unsigned)kvh);
+    cfg.blockDim = dim3((few ? blocks::SELECT_WARPS<true> : blocks::SELECT_WARPS<false>) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.runs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.runs > 1 ? 2 : 1;
+    if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, kern, a), name)) return rc;
+    return launch_check(name);
 }

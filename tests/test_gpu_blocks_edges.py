@@ -254,3 +254,46 @@ def test_captured_reordering():
         assert torch.equal(a, b)
     held = [p for row, n in zip(tables_[0].tolist(), lens_[0].tolist()) for p in row[:-(-n // page)]]
     assert refs.tolist() == [held.count(p) for p in range(P)]
+
+
+@pytest.mark.parametrize("lens,news,nh,kvh,hd,page,topk,first,local", [
+    ([9000, 40], [3, 1], 5, 1, 80, 16, 20, 1, 2), ([33000], [1], 8, 1, 128, 16, 50, 0, 1),
+    ([20011, 0, 17000], [4, 0, 2], 6, 2, 64, 16, 9, 1, 1), ([16384], [2], 80, 1, 64, 16, 200, 2, 2),
+    ([9000], [6], 4, 1, 128, 16, 90, 1, 2)])
+def test_select_over_many_blocks(lens, news, nh, kvh, hd, page, topk, first, local):
+    """More than 512 blocks, by clusters where the tokens are few; scores that repeat."""
+    g = gen(sum(lens))
+    n_pages, rows = tables(g, lens, page)
+    keys = filled_keys(g, n_pages, kvh, hd)
+    keys.scales.add_(0.01)
+    keys.codes[n_pages // 2:] = keys.codes[:n_pages - n_pages // 2].clone()
+    keys.scales[n_pages // 2:] = keys.scales[:n_pages - n_pages // 2].clone()
+    q = randn(g, sum(news), nh, hd)
+    got = ds41.block_select(q, keys, page, ints(rows), ints(lens), cu(news), max(news), max(lens), topk, first, local).tolist()
+    codes, scales = keys.codes.double(), keys.scales.double()
+    at = 0
+    for b, (n, m) in enumerate(zip(lens, news)):
+        mine = torch.tensor(rows[b][:-(-n // page)], device=DEV, dtype=torch.long)
+        for i in range(m):
+            for h in range(kvh):
+                w = br.picks(q[at + i, h * nh // kvh:(h + 1) * nh // kvh], codes[mine, h], scales[mine, h], n - m + i,
+                             page, topk, first, local)
+                assert got[at + i][h] == w + [-1] * (topk - len(w)), (b, i, h)
+        at += m
+
+
+def test_select_equal_scores_of_many_blocks():
+    """Thousands of blocks alike, or in two kinds: the lowest are taken."""
+    page, kvh, hd, topk, n = 16, 1, 64, 70, 60000
+    NB = n // page
+    table = torch.arange(NB, dtype=torch.int32, device=DEV)[None]
+    keys = ds41.make_block_keys(NB, kvh, hd)
+    keys.codes.fill_(3)
+    keys.scales.fill_(0.5)
+    q = torch.ones(1, 2, hd, dtype=torch.bfloat16, device=DEV)
+    for k in (topk, 20):
+        got = ds41.block_select(q, keys, page, table, ints([n]), cu([1]), 1, n, k, 1, 2)
+        assert got[0, 0].tolist() == list(range(k - 2)) + [NB - 2, NB - 1]
+    keys.scales[1000:1005] = 1.0
+    got = ds41.block_select(q, keys, page, table, ints([n]), cu([1]), 1, n, 20, 1, 2)
+    assert got[0, 0].tolist() == list(range(13)) + list(range(1000, 1005)) + [NB - 2, NB - 1]
