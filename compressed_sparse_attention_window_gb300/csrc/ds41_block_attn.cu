@@ -122,14 +122,15 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) 
     const Seq s = load_seq(a, b);
     if (!s.ok || t < s.q0 || t >= s.q0 + s.n) return;
     const int p = s.len - s.n + (t - s.q0), cur = p >> a.block_shift;
-    // the list ends at the first entry that does not rise or lies past the token
+    // the list ends at the first entry that does not rise or lies past the token (an entry
+    // behind the end may be anything: one below 0 can rise above another)
     const int32_t* table = a.table + (int64_t)b * a.max_pages;
     int end = a.topk;
 #pragma unroll
     for (int k = 0; k < MAX_LIST / NT; k++) {
         const int i = k * NT + tid;
         if (i < a.topk) {
-            if (mine[k] <= before[k] || mine[k] > cur) {
+            if (mine[k] < 0 || mine[k] <= before[k] || mine[k] > cur) {
                 end = min(end, i);
             } else {
                 const int pg = table[mine[k]];

@@ -297,3 +297,23 @@ def test_select_equal_scores_of_many_blocks():
     keys.scales[1000:1005] = 1.0
     got = ds41.block_select(q, keys, page, table, ints([n]), cu([1]), 1, n, 20, 1, 2)
     assert got[0, 0].tolist() == list(range(13)) + list(range(1000, 1005)) + [NB - 2, NB - 1]
+
+
+@pytest.mark.parametrize("behind", [[-7, -5, -3], [-(1 << 31), -(1 << 30), -(1 << 29)], [1 << 30, -(1 << 30), 0], [-2, -1, 0]])
+def test_entries_behind_a_lists_end_may_be_anything(behind):
+    """Entries below 0 that rise, or far outside the table, behind the one that ends the list."""
+    g = gen(21)
+    n, page = 100, 16
+    n_pages, rows = tables(g, [n], page)
+    cache = filled_cache(g, n_pages, 1, page, 64, False)
+    q = randn(g, 1, 4, 64)
+    k, v, _ = sequence(cache, rows[0], n, page)
+    w = br.attend(q, k, v, [[[2]]], n - 1, page, 0.1, None)
+    i = ints([[[2] + behind]])
+    o, lse = torch.empty_like(q), torch.empty(1, 4, device=DEV)
+    ds41.block_attn_fwd(q, cache, ints(rows), ints([n]), cu([1]), 1, i, 0.1, o=o, lse=lse)
+    assert ds41.device_status() == 4
+    ref.close(o, lse, *w)
+    ds41.block_prompt_attn_fwd(q, k.bfloat16(), v.bfloat16(), cu([1]), cu([n]), 1, n, i, page, 0.1, o=o, lse=lse)
+    assert ds41.device_status() == 4
+    ref.close(o, lse, *w)
