@@ -367,9 +367,11 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     auto offer = [&](int h, int i) { return offer_of(h, i, i < k ? keys[h * k + i] : 0); };
     auto write = [&](int i, const Offer& o) {
         const int64_t to = (int64_t)b * k + i;
-        a.out[to] = o.v ? (float)number_of(o.v) : -INFINITY;
-        a.parents[to] = o.v ? b * a.W + o.w : -1;
-        a.tokens[to] = o.v ? token_of(o.key) : -1;
+        // (one that f32 does not hold any more is none: those are the last)
+        const float v = o.v ? (float)number_of(o.v) : -INFINITY;
+        a.out[to] = v;
+        a.parents[to] = v > -INFINITY ? b * a.W + o.w : -1;
+        a.tokens[to] = v > -INFINITY ? token_of(o.key) : -1;
     };
     // (arithmetic in 64 bits is slow here, two operations a cycle and SM: once an offer)
     Offer mine_of[HOLD];

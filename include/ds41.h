@@ -654,7 +654,8 @@ int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const 
  * device, so that a captured step can hand pages out:
  *   refs [n_pages] int32: how many sequences have the page; 0: it is free
  *   page_table [B, max_pages] int32, lens [B] int32: sequence b has len rows in the
- *   pages of its first ceil(len / page) entries
+ *   pages of its first ceil(len / page) entries.  Those behind are not looked at: a page
+ *   taken for rows that len does not count yet is not freed, shared or moved with it
  * Full pages may be shared; a page that is not full belongs to one sequence, which
  * writes on in it.  Free pages are handed out lowest first, to the sequences in their
  * order, so equal calls give equal tables.  A length below 0 or past max_pages * page
@@ -741,7 +742,7 @@ size_t ds41_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t
  *     at s_w
  *   out_scores [B, k] f32, parents [B, k] int32 (b * W + w, what ds41_kv_pages_fork
  *     takes), tokens [B, k] int32 outputs; where fewer than k offers are above
- *     -inf the rest is -inf, -1, -1
+ *     -inf (as f32) the rest is -inf, -1, -1.  out_scores may be scores where k == W
  * A beam whose logits hold a NaN or +inf, or nothing but -inf, or whose score is NaN
  * or +inf, offers nothing.  1 <= k <= 128, W <= 1024, V <= 2^22, B * W < 65536, 0 <= end_token
  * < V with ended. */

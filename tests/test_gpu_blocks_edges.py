@@ -317,3 +317,67 @@ def test_entries_behind_a_lists_end_may_be_anything(behind):
     ds41.block_prompt_attn_fwd(q, k.bfloat16(), v.bfloat16(), cu([1]), cu([n]), 1, n, i, page, 0.1, o=o, lse=lse)
     assert ds41.device_status() == 4
     ref.close(o, lse, *w)
+
+
+def test_beam_scores_in_place():
+    """out_scores may be scores: a search's are read before they are written."""
+    g = gen(22)
+    x, scores = randn(g, 30, 6, 9000).float(), -torch.rand(30, 6, generator=g, device=DEV)
+    want = [t.clone() for t in ds41.beam_select(x, scores, 6)]
+    for _ in range(3):
+        s = scores.clone()
+        got = ds41.beam_select(x, s, 6, out_scores=s)
+        assert got[0] is s and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_beam_offers_that_f32_does_not_hold():
+    """-3e38 - 3e38 is no f32: such offers are none, whichever beam they are of."""
+    x = torch.zeros(1, 3, 10, device=DEV)
+    x[0, 0, 4:] = -3e38
+    s = torch.tensor([[-3e38, -math.inf, -1.0]], device=DEV)
+    ended = torch.tensor([[False, False, True]], device=DEV)
+    out, parents, tokens = ds41.beam_select(x, s, 8, ended=ended, end_token=7)
+    assert parents.tolist() == [[2, 0, 0, 0, 0, -1, -1, -1]] and tokens.tolist() == [[7, 0, 1, 2, 3, -1, -1, -1]]
+    assert out[0, 0] == -1 and (out[0, 5:] == -math.inf).all()
+    assert torch.allclose(out[0, 1:5], torch.tensor(-3e38, device=DEV), rtol=2.0 ** -23)
+
+
+def test_nothing_to_do():
+    """No sequences, no tokens, no children: nothing happens, and parents without children
+    give their pages back."""
+    g = gen(23)
+    cache, keys = filled_cache(g, 6, 2, 16, 64, True), filled_keys(g, 6, 2, 64)
+    before = [t.clone().view(torch.uint8) for t in list(cache) + list(keys)]
+    refs, none, table = ints([1, 1, 0, 2, 0, 0]), ints([]), ints([[0, 1, 3]])
+    ds41.kv_pages_take(refs, table[:0], none, none, 16)
+    ds41.kv_pages_free(refs, table[:0], none, 16)
+    out, lens = ds41.kv_pages_fork(cache, refs, table, ints([40]), none, keys=keys)
+    assert out.shape == (0, 3) and lens.shape == (0,)
+    ds41.kv_pages_copy(cache, none, none, keys=keys)
+    out, lens = ds41.kv_pages_fork(cache, refs, table[:0], none, ints([-1, -1]), keys=keys)
+    assert out.tolist() == [[-1] * 3] * 2 and lens.tolist() == [0, 0]
+    assert refs.tolist() == [1, 1, 0, 2, 0, 0]
+    ds41.kv_pages_fork(cache, refs, table, ints([40]), none, replace=True, keys=keys)
+    assert refs.tolist() == [0, 0, 0, 1, 0, 0]
+    ds41.kv_block_keys(cache, keys, table, ints([40]), 0, starts=ints([40]))
+    q = randn(g, 0, 4, 64)
+    idx = ds41.block_select(q, keys, 16, table, ints([40]), cu([0]), 1, 48, 3, first=1, local=1)
+    assert idx.shape == (0, 2, 3)
+    assert ds41.block_attn_fwd(q, cache, table, ints([40]), cu([0]), 1, idx, 0.1).shape == q.shape
+    k = randn(g, 0, 2, 64)
+    assert ds41.block_prompt_attn_fwd(q, k, k, cu([0]), cu([0]), 0, 0, idx, 16, 0.1).shape == q.shape
+    s, p, t = ds41.beam_select(randn(g, 0, 2, 9), torch.zeros(0, 2, device=DEV), 4)
+    assert s.shape == p.shape == t.shape == (0, 4)
+    for a, b in zip(list(cache) + list(keys), before):
+        assert torch.equal(a.view(torch.uint8), b)
+
+
+def test_keys_without_values():
+    """Prompts whose keys are none but whose queries are: refused sequence by sequence, outputs
+    as they were."""
+    g = gen(24)
+    q, k = randn(g, 3, 4, 64), randn(g, 0, 2, 64)
+    o, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device=DEV)
+    ds41.block_prompt_attn_fwd(q, k, k, cu([3]), cu([0]), 3, 16, ints([[[0]] * 2] * 3), 16, 0.1, o=o, lse=lse)
+    assert ds41.device_status() == 4
+    assert (o == 7).all() and (lse == 7).all()
