@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     extern __shared__ double base[];  // [W]: s_w - L; NaN: the beam offers nothing, or has ended
     uint64_t* ends = reinterpret_cast<uint64_t*>(base + a.W);  // [W]: an ended beam's offer
     __shared__ Offer all[OFFERS];
-    __shared__ unsigned long long least;
+    __shared__ uint64_t least[NT / 32];
     __shared__ int n_all, taken[NT / 32];
     __shared__ Offer best[NT / 32];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
@@ -326,10 +326,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     uint64_t held[HOLD];
 #pragma unroll
     for (int u = 0; u < HOLD; u++) held[u] = u * NT + tid < n_keys ? keys[u * NT + tid] : 0;
-    if (tid == 0) {
-        least = 0;
-        n_all = 0;
-    }
+    if (tid == 0) n_all = 0;
     for (int w = tid; w < a.W; w += NT) {
         const int64_t row = (int64_t)b * a.W + w;
         const float score = a.scores[row];
@@ -375,17 +372,23 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     };
     // (arithmetic in 64 bits is slow here, two operations a cycle and SM: once an offer)
     Offer mine_of[HOLD];
+    uint64_t from = 0;
 #pragma unroll
     for (int u = 0; u < HOLD; u++) {
         const int x = u * NT + tid, h = x / k;
         mine_of[u] = x < n_keys ? offer_of(h, x - h * k, held[u]) : Offer{0, 0, 0};
-        if (x < n_keys && x - h * k == k - 1 && mine_of[u].v)
-            atomicMax(&least, (unsigned long long)mine_of[u].v);
+        if (x < n_keys && x - h * k == k - 1) from = max(from, mine_of[u].v);
     }
     for (int h = HOLD * NT / k + tid; h < n_lists; h += NT)  // (lists that end behind those)
-        atomicMax(&least, (unsigned long long)offer(h, k - 1).v);
+        from = max(from, offer(h, k - 1).v);
+    // (an atomic of 64 bits on shared memory is a loop that 32 lists take one after another)
+    const uint32_t high = __reduce_max_sync(0xffffffffu, (uint32_t)(from >> 32));
+    const uint32_t low =
+        __reduce_max_sync(0xffffffffu, (uint32_t)(from >> 32) == high ? (uint32_t)from : 0u);
+    if (lane == 0) least[warp] = (uint64_t)high << 32 | low;
     __syncthreads();
-    const uint64_t from = least;
+#pragma unroll
+    for (int w = 0; w < NT / 32; w++) from = max(from, least[w]);
     auto keep = [&](const Offer& o) {
         if (o.v == 0 || o.v < from) return;
         const int to = atomicAdd(&n_all, 1);
