@@ -4,7 +4,8 @@
 // Mathematics.  As tree attention of few rows (ds41_tree_attn.cu, ds41_few.cuh): one pass
 // over the rows j <= p of the listed pages, with a lazily moved reference per row.  The
 // rows of a tile are the query heads of one token that share a key/value head (lists
-// differ from token to token), at most 16.
+// differ from token to token), at most 16; groups of at most 8 heads take the transposed
+// products, whose tiles have 8.
 //
 // What bounds it.  Each listed row is read once a token: HBM when there are tokens
 // enough.  A token's list is cut into as many runs as fill the GPU, at most eight, the
@@ -13,6 +14,8 @@
 // length, the list, the table) is walked by all threads at once.  (16 tokens of 64 heads of
 // 128 over 8, 64 blocks of 64 e4m3 rows each: 31.8 us, 4.4 TB/s; 12 warps an SM do not hide the
 // chain of a group of keys.)
+#include <type_traits>
+
 #include "ds41_few.cuh"
 
 namespace ds41 {
@@ -34,7 +37,7 @@ struct Args {
     int64_t Tq, max_pages;
     int B, max_q, nh, kvh, hd, G, topk, block, block_shift;
     float scale;
-    int tiles;  // of 16 query heads of a group
+    int tiles;  // of a group's query heads
     int runs;   // of a list
     unsigned int* status;
 };
@@ -59,11 +62,18 @@ constexpr int NT = WARPS * 32;
 constexpr int MAX_LIST = 1024;
 constexpr int MAX_RUNS = 8;  // CTAs of a cluster
 
-template <int HD, bool E4M3>
-constexpr int tokens_bytes() {
+// RT: rows of a tile, 8 or 16
+template <int HD, bool E4M3, int RT>
+struct Shape {
     using C = few::Cfg<HD, E4M3>;
-    return WARPS * (C::RING > 16 * C::P * 4 ? C::RING : 16 * C::P * 4);
-}
+    // CTAs of an SM: what the registers and the rings leave room for
+    static constexpr int CTAS = C::RB == 256 ? 2 : RT == 8 ? 4 : E4M3 ? 3 : 2;
+    static constexpr int STAGES = CTAS == 4 && C::RB == 128 ? 3 : C::STAGES;
+    static constexpr int RING = STAGES * C::STAGE;  // of a warp
+    static constexpr int OUT = RT * C::P * 4;
+    static constexpr int BYTES = WARPS * (RING > OUT ? RING : OUT);
+    static_assert(CTAS * (BYTES + 6144) <= 232448, "shared memory of an SM");
+};
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
@@ -86,10 +96,11 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
     return v;
 }
 
-template <int HD, bool E4M3>
-__global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) {
+template <int HD, bool E4M3, int RT>
+__global__ void __launch_bounds__(NT, Shape<HD, E4M3, RT>::CTAS) tokens_kernel(const Args a) {
     pdl_wait();
     using C = few::Cfg<HD, E4M3>;
+    using S = Shape<HD, E4M3, RT>;
     constexpr int P = C::P;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int list[MAX_LIST];  // pages, -1: outside the cache
@@ -97,7 +108,7 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int run = blockIdx.x % a.runs, item = blockIdx.x / a.runs;
     const int unit = item / a.tiles, h = unit % a.kvh, t = unit / a.kvh;
-    const int y0 = (item - unit * a.tiles) * 16, rows = min(16, a.G - y0);
+    const int y0 = (item - unit * a.tiles) * RT, rows = min(RT, a.G - y0);
     if (blockIdx.x == 0)
         for (int b = tid; b < a.B; b += NT)
             if (!load_seq(a, b).ok) raise_status(a.status, DS41_E_INDEX);
@@ -159,14 +170,14 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) 
     const int own = (int)((int64_t)groups * (run + 1) / a.runs) - first;
     const int n_mine = (own - warp + WARPS - 1) / WARPS;  // groups first + warp, + 4, ...
 
-    uint8_t* ring = smem + warp * C::RING;
+    uint8_t* ring = smem + warp * S::RING;
     const uint32_t ring_u = smem_u32(ring);
     const few::Copier<HD, E4M3> copier(a.hd, lane);
     const int per = a.block_shift - 4;  // log2 of a page's groups
     unsigned bad = 0;                   // stages whose page does not exist
     auto fetch = [&](int i) {
         if (i < n_mine) {
-            const int st = i % C::STAGES, x = first + i * WARPS + warp;
+            const int st = i % S::STAGES, x = first + i * WARPS + warp;
             const int pg = list[x >> per];
             const bool ok = pg >= 0;
             bad = ok ? bad & ~(1u << st) : bad | (1u << st);
@@ -179,47 +190,54 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) 
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; i++) fetch(i);
+    for (int i = 0; i < S::STAGES - 1; i++) fetch(i);
 
-    few::Rows<HD, E4M3> mem;
+    typename std::conditional<RT == 8, few::Rows8<HD, E4M3>, few::Rows<HD, E4M3>>::type mem;
     const uint16_t* q = a.q + t * a.q_tok + ((int64_t)h * a.G + y0) * a.q_head;
+    if constexpr (RT == 8) {
+        mem.query(q + min(g, rows - 1) * a.q_head, a.hd, a.scale * tc::SM_LOG2E, c);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; i++) mem.query(i, q + min(g + 8 * i, rows - 1) * a.q_head, a.hd, c);
-    mem.start(a.scale * tc::SM_LOG2E);
+        for (int i = 0; i < 2; i++) mem.query(i, q + min(g + 8 * i, rows - 1) * a.q_head, a.hd, c);
+        mem.start(a.scale * tc::SM_LOG2E);
+    }
     for (int i = 0; i < n_mine; i++) {
-        fetch(i + C::STAGES - 1);
-        cp_async_wait<C::STAGES - 1>();
+        fetch(i + S::STAGES - 1);
+        cp_async_wait<S::STAGES - 1>();
         __syncwarp();
-        const int st = i % C::STAGES, live = keys - (first + i * WARPS + warp) * GROUP;
+        const int st = i % S::STAGES, live = keys - (first + i * WARPS + warp) * GROUP;
         const bool none = (bad >> st) & 1;
-        mem.group(
-            ring + st * C::STAGE, none || live < GROUP,
-            [&](int, int x) { return !none && x < live; }, g, c);
+        if constexpr (RT == 8)
+            mem.group(ring + st * C::STAGE, none ? 0 : live, g, c);
+        else
+            mem.group(
+                ring + st * C::STAGE, none || live < GROUP,
+                [&](int, int x) { return !none && x < live; }, g, c);
         __syncwarp();  // the stage is read before it is filled again
     }
     cp_async_wait<0>();
     __syncthreads();
     // ---- the warps' results joined into warp 0's place ----
     float* out = reinterpret_cast<float*>(smem);
-    mem.put(out + warp * 16 * P, g, c);
+    mem.put(out + warp * RT * P, g, c);
     __syncthreads();
-    constexpr int PER = NT / 16;  // threads of a row
+    constexpr int PER = NT / RT;  // threads of a row
     const int r = tid / PER, part = tid % PER;
     float mm = -INFINITY, f[WARPS], ll = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * 16 + r) * P + HD]);
+    for (int w = 0; w < WARPS; w++) mm = fmaxf(mm, out[(w * RT + r) * P + HD]);
     const float ref = mm == -INFINITY ? 0.0f : mm;
 #pragma unroll
     for (int w = 0; w < WARPS; w++) {
-        f[w] = exp2f(out[(w * 16 + r) * P + HD] - ref);
-        ll += f[w] * out[(w * 16 + r) * P + HD + 1];
+        f[w] = exp2f(out[(w * RT + r) * P + HD] - ref);
+        ll += f[w] * out[(w * RT + r) * P + HD + 1];
     }
     __syncwarp();  // (a row's threads are in one warp)
     for (int x = part * 4; x < a.hd; x += PER * 4) {
         float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
         for (int w = 0; w < WARPS; w++) {
-            const float4 ow = *reinterpret_cast<const float4*>(&out[(w * 16 + r) * P + x]);
+            const float4 ow = *reinterpret_cast<const float4*>(&out[(w * RT + r) * P + x]);
             v.x += f[w] * ow.x;
             v.y += f[w] * ow.y;
             v.z += f[w] * ow.z;
@@ -279,10 +297,22 @@ __global__ void __launch_bounds__(NT, E4M3 ? 3 : 2) tokens_kernel(const Args a) 
     if (a.runs > 1) cluster_sync();  // nobody leaves while its results are read
 }
 
-template <int HD, bool E4M3>
-int launch_tokens(const Args& a, unsigned ctas, const char* name, cudaStream_t st) {
-    constexpr int smem = tokens_bytes<HD, E4M3>();
-    if (int rc = allow_smem<tokens_kernel<HD, E4M3>>(smem, name)) return rc;
+template <int HD, bool E4M3, int RT>
+int launch_tokens(Args& a, int64_t page, const char* name, cudaStream_t st) {
+    using S = Shape<HD, E4M3, RT>;
+    constexpr int smem = S::BYTES;
+    a.tiles = (a.G + RT - 1) / RT;
+    // runs of a list: as many as the GPU holds CTAs for, of two groups a warp at least
+    const int64_t items = a.Tq * a.kvh * a.tiles;
+    const int64_t fit = (int64_t)sm_count_once() * S::CTAS / items;
+    const int64_t most = a.topk * page / (2 * WARPS * GROUP);
+    const int64_t runs = fit < most ? fit : most;
+    a.runs = (int)(runs < 1 ? 1 : runs < MAX_RUNS ? runs : MAX_RUNS);
+    DS41_REQUIRE(items * a.runs < int64_t(1) << 31, DS41_E_RANGE, "%s: Tq=%lld kvh=%d", name,
+                 (long long)a.Tq, a.kvh);
+    const unsigned ctas = (unsigned)(items * a.runs);
+    if (int rc = status_word(&a.status)) return rc;
+    if (int rc = allow_smem<tokens_kernel<HD, E4M3, RT>>(smem, name)) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(NT);
@@ -296,7 +326,7 @@ int launch_tokens(const Args& a, unsigned ctas, const char* name, cudaStream_t s
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.runs > 1 ? 2 : 1;
-    if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, tokens_kernel<HD, E4M3>, a), name)) return rc;
+    if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, tokens_kernel<HD, E4M3, RT>, a), name)) return rc;
     return launch_check(name);
 }
 
@@ -359,22 +389,16 @@ extern "C" int ds41_block_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_
     a.block = (int)page;
     a.block_shift = a.kv.page_shift;
     a.scale = scale;
-    a.tiles = (a.G + 15) / 16;
-    // runs of a list: as many as the GPU holds CTAs for (three an SM on an e4m3 cache, two on
-    // bf16), of two groups a warp at least
-    const int64_t items = Tq * kvh * a.tiles;
-    const int64_t fit = (int64_t)sm_count_once() * (fmt == DS41_KV_E4M3 ? 3 : 2) / items;
-    const int64_t most = topk * page / (2 * ba::WARPS * GROUP);
-    int64_t runs = fit < most ? fit : most;
-    a.runs = (int)(runs < 1 ? 1 : runs < ba::MAX_RUNS ? runs : ba::MAX_RUNS);
-    DS41_REQUIRE(items * a.runs < lim, DS41_E_RANGE, "%s: Tq=%lld kvh=%lld", name, (long long)Tq,
-                 (long long)kvh);
-    if (int rc = status_word(&a.status)) return rc;
-    const unsigned ctas = (unsigned)(items * a.runs);
     cudaStream_t st = (cudaStream_t)stream;
+    const auto launch = [&](auto hd_, auto e4m3) {
+        constexpr int HD = decltype(hd_)::value;
+        constexpr bool E4M3 = decltype(e4m3)::value;
+        return a.G <= 8 ? ba::launch_tokens<HD, E4M3, 8>(a, page, name, st)
+                        : ba::launch_tokens<HD, E4M3, 16>(a, page, name, st);
+    };
+    using W64 = std::integral_constant<int, 64>;
+    using W128 = std::integral_constant<int, 128>;
     if (fmt == DS41_KV_E4M3)
-        return hd <= 64 ? ba::launch_tokens<64, true>(a, ctas, name, st)
-                        : ba::launch_tokens<128, true>(a, ctas, name, st);
-    return hd <= 64 ? ba::launch_tokens<64, false>(a, ctas, name, st)
-                    : ba::launch_tokens<128, false>(a, ctas, name, st);
+        return hd <= 64 ? launch(W64{}, std::true_type{}) : launch(W128{}, std::true_type{});
+    return hd <= 64 ? launch(W64{}, std::false_type{}) : launch(W128{}, std::false_type{});
 }
