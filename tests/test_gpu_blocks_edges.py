@@ -10,6 +10,7 @@ import blocks_ref as br
 import dense_ref as ref
 from compressed_sparse_attention_window_gb300 import ds41
 from test_gpu_blocks import DEV, cu, filled_cache, gen, ints, randn, random_lists, sequence, tables
+from test_gpu_dense_attention_edges import aligned, close_by_weight, packed_cache
 from test_gpu_pages import check_beam, filled_keys
 
 pytestmark = pytest.mark.gpu
@@ -381,3 +382,75 @@ def test_keys_without_values():
     ds41.block_prompt_attn_fwd(q, k, k, cu([3]), cu([0]), 3, 16, ints([[[0]] * 2] * 3), 16, 0.1, o=o, lse=lse)
     assert ds41.device_status() == 4
     assert (o == 7).all() and (lse == 7).all()
+
+
+def some_blocks(g, d, n, page, share):
+    """Lists for d tokens at n - d .. n - 1, alike for all heads: a token's own block and `share`
+    of the others; what each sees of the n rows."""
+    lists, seen = [], torch.zeros(d, n, dtype=torch.bool)
+    for t in range(d):
+        cur = (n - d + t) // page
+        keep = torch.rand(cur, generator=g, device=DEV).tolist()
+        lists.append([x for x in range(cur) if keep[x] < share] + [cur])
+        for x in lists[-1]:
+            seen[t, x * page:min((x + 1) * page, n - d + t + 1)] = True
+    width = max(map(len, lists))
+    return [x + [-1] * (width - len(x)) for x in lists], seen.to(DEV)
+
+
+def run_tokens(g, q, cache, table, n, kvh, page, share, sink=None):
+    d, nh, hd = q.shape
+    lists, seen = some_blocks(g, d, n, page, share)
+    idx = ints([[x] * kvh for x in lists])
+    o, lse = torch.empty_like(q), torch.empty(d, nh, device=DEV)
+    ds41.block_attn_fwd(q, cache, table, ints([n]), cu([d]), d, idx, hd ** -0.5, sink=sink, o=o, lse=lse)
+    close_by_weight(q, cache, table, n, seen, (o, lse), sink)
+
+
+TILES = [(2, 8, 2), (3, 8, 1), (2, 18, 2), (1, 20, 1)]  # tokens, heads: 4, 8, 9 and 20 of a group
+
+
+@pytest.mark.parametrize("spread", [6, 20, 50])
+@pytest.mark.parametrize("d,nh,kvh", TILES)
+@pytest.mark.parametrize("n,share", [(64, 1.0), (3000, 0.5)])
+def test_tokens_value_scales_far_apart(n, share, d, nh, kvh, spread):
+    g = gen(n + spread + nh)
+    q, k, v = randn(g, d, nh, 128), randn(g, n, kvh, 128) * 3.0, randn(g, n, kvh, 128)
+    cache, table = packed_cache(k, v, 64, True)
+    e = torch.randint(-spread, spread + 1, cache.v_scales.shape, generator=g, device=DEV)
+    cache.v_scales.mul_(torch.exp2(e.float()))
+    for sink in (None, torch.randn(nh, generator=g, device=DEV)):
+        run_tokens(g, q, cache, table, n, kvh, 64, share, sink)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** 8, 2.0 ** 20, 2.0 ** 40])
+@pytest.mark.parametrize("d,nh,kvh", TILES)
+@pytest.mark.parametrize("hd", [64, 128])
+def test_tokens_large_value_row_of_little_weight(hd, d, nh, kvh, gain):
+    q, k, v = aligned(gen(hd + nh), d, nh, 800, kvh, hd)
+    k[300, :, 0] = -300.0
+    v[300] *= gain
+    cache, table = packed_cache(k, v, 32, True)
+    run_tokens(gen(1), q, cache, table, 800, kvh, 32, 1.0)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -60, 2.0 ** 60, 2.0 ** 96])
+@pytest.mark.parametrize("d,nh,kvh", TILES)
+def test_tokens_values_all_small_or_all_large(d, nh, kvh, size):
+    g = gen(nh)
+    q, k, v = randn(g, d, nh, 64), randn(g, 900, kvh, 64), randn(g, 900, kvh, 64) * size
+    v[5] = 0.0
+    cache, table = packed_cache(k, v, 128, True)
+    run_tokens(g, q, cache, table, 900, kvh, 128, 0.8)
+
+
+@pytest.mark.parametrize("d,nh,kvh", TILES)
+def test_tokens_queries_with_outliers(d, nh, kvh):
+    """A channel 1000 times the rest, a zero query, one next to nothing."""
+    g = gen(nh + 1)
+    q, k, v = randn(g, d, nh, 128), randn(g, 700, kvh, 128), randn(g, 700, kvh, 128)
+    q[:, :, 5] *= 1000.0
+    q[0, 1] = 0.0
+    q[0, 2] *= 2.0 ** -90
+    cache, table = packed_cache(k, v, 16, True)
+    run_tokens(g, q, cache, table, 700, kvh, 16, 0.7)
