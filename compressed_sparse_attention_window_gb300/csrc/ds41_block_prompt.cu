@@ -227,8 +227,14 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
         }
         __syncthreads();
     }
-    const int base[3] = {0, (units_of[0] + nu - 1) >> nu_shift,
-                         ((units_of[0] + nu - 1) >> nu_shift) + ((units_of[1] + nu - 1) >> nu_shift)};
+    // The units of both tiles that do not fill a record (their first ones: the last may end behind
+    // the last key) go to the tiles' own records where that saves a step.
+    auto recs_of = [&](int units) { return (units + nu - 1) >> nu_shift; };
+    const int most = max(units_of[1], units_of[2]), over = units_of[0] & (nu - 1);
+    const int moved = units_of[0] > over && recs_of(most + over) == recs_of(most) ? over : 0;
+    const int n_both = recs_of(units_of[0] - moved), n_own[2] = {recs_of(units_of[1] + moved),
+                                                                 recs_of(units_of[2] + moved)};
+    const int base[3] = {0, n_both, n_both + n_own[0]};
     // into their records
     int found[3] = {0, 0, 0};  // blocks so far
     for (int r0 = 0; r0 < blocks; r0 += range) {
@@ -249,11 +255,21 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
             for (int k = 0; k < per; k++) {
                 const int row = ((r0 + x) << p.shift) + (k << p.unit_shift);
                 if (row >= it.len) break;  // (behind the last key: only the last block's)
-                const int u = at * per + k, rec = u >> nu_shift, slot = u & (nu - 1);
-                const int first = kind == 0 ? base[0] : kind == 1 ? base[1] : base[2];
-                uint32_t* to = recs + (int64_t)(first + rec) * p.rec_words;
-                to[slot] = (uint32_t)row;
-                for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
+                int u = at * per + k;
+                auto put = [&](int first, int u) {
+                    const int slot = u & (nu - 1);
+                    uint32_t* to = recs + (int64_t)(first + (u >> nu_shift)) * p.rec_words;
+                    to[slot] = (uint32_t)row;
+                    for (int y = 0; y < W; y++) to[nu + slot * W + y] = table[x * W + y];
+                };
+                if (kind == 0 && u < moved) {
+                    put(base[1], units_of[1] + u);
+                    put(base[2], units_of[2] + u);
+                    continue;
+                }
+                u -= kind == 0 ? moved : 0;
+                const int rec = u >> nu_shift, slot = u & (nu - 1);
+                put(kind == 0 ? base[0] : kind == 1 ? base[1] : base[2], u);
                 if (row + (1 << p.unit_shift) > it.len) {
                     it.tail = (slot << p.unit_shift) + it.len - row;
                     it.tail_end = (slot + 1) << p.unit_shift;
@@ -267,7 +283,7 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     // slots behind a kind's last unit
 #pragma unroll
     for (int kind = 0; kind < 3; kind++) {
-        const int n = units_of[kind], slots = (n + nu - 1) >> nu_shift << nu_shift;
+        const int n = units_of[kind] + (kind ? moved : -moved), slots = recs_of(n) << nu_shift;
         for (int u = n + tid; u < slots; u += PLAN) {
             uint32_t* to = recs + (int64_t)(base[kind] + (u >> nu_shift)) * p.rec_words;
             const int slot = u & (nu - 1);
@@ -276,9 +292,9 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
         }
     }
     if (tid == 0) {
-        it.both = base[1];
-        it.own[0] = base[2] - base[1];
-        it.own[1] = (units_of[2] + nu - 1) >> nu_shift;
+        it.both = n_both;
+        it.own[0] = n_own[0];
+        it.own[1] = n_own[1];
     }
     __syncthreads();
     if (tid < 4)
@@ -860,7 +876,8 @@ Plan make_plan(int64_t B, int64_t Tq, int64_t max_q, int64_t max_k, int64_t topk
     const int64_t toks = 2 * pl.TT < max_q ? 2 * pl.TT : max_q;
     int64_t blocks = (max_k + block - 1) / block;
     if (toks * topk < blocks) blocks = toks * topk;
-    // (three kinds of them, each with a record that is not full)
+    // (three kinds of them, each with a record that is not full; units of both tiles that move to
+    // the tiles' own records free one, and the shorter of those may need one more)
     pl.max_rec = (int)((blocks * (block / unit) + nu - 1) / nu) + 2;
     // every sequence has at most one pair of tiles that is not full
     pl.items = (Tq / (2 * pl.TT) + B) * kvh * pl.subs;
