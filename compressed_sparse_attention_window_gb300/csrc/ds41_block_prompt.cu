@@ -29,7 +29,7 @@
 // (tensor pipe half busy), and the union's surplus over a token's own blocks.  (Chunk of 8192
 // tokens behind 24576, 32 blocks of 64 rows each, alike for 32 tokens one after another, 32
 // heads of 128 over 8: 354 us, the plan 19 of them; over all rows 2310.  Six prompts of up to
-// 2001 tokens whose lists have nothing in common, 16 heads of 64 over 2: 86 us, over all rows
+// 2001 tokens whose lists have nothing in common, 16 heads of 64 over 2: 75 us, over all rows
 // 61.)
 #include "ds41_prompt.cuh"
 
@@ -59,6 +59,7 @@ static_assert(sizeof(Item) == 64, "four 16-byte pieces");
 
 constexpr uint32_t ROW = 0x3fffffffu;  // a unit's word: its first row; this: none
 constexpr int PLAN = 256;              // threads of plan_kernel
+constexpr int SORTED = 64;             // sequences whose pairs it puts in order, at most
 constexpr int TABLE = 8192;            // words of its table, at most
 
 struct Params {
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     pdl_wait();
     pdl_trigger();
     extern __shared__ uint32_t table[];
-    __shared__ int sh[PLAN / 32], units_of[3];  // (both tiles', tile 0's, tile 1's)
+    __shared__ int sh[PLAN / 32], pairs_of[SORTED], units_of[3];  // (both tiles', tile 0's, tile 1's)
     __shared__ __align__(16) Item it;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, id = blockIdx.x;
     // (head group by head group: what is under way at a time reads the keys of one or two, which
@@ -121,10 +122,9 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
     }
     if (tid < 3) units_of[tid] = 0;
     __syncthreads();
-    // the sequence (its pairs of tiles in falling order, as its longest lists are at the end)
-    for (int b0 = 0, base = 0; b0 < p.B; b0 += PLAN) {
-        const int b = b0 + tid;
-        int q0 = 0, n = 0, k0 = 0, len = 0;
+    // sequence b's pairs of tiles
+    auto load = [&](int b, int& q0, int& n, int& k0, int& len) {
+        q0 = n = k0 = len = 0;
         if (b < p.B) {
             q0 = p.cu_q[b];
             k0 = p.cu_k[b];
@@ -137,19 +137,53 @@ __global__ void __launch_bounds__(PLAN) plan_kernel(const Params p) {
                 raise_status(p.status, DS41_E_INDEX);
             }
         }
-        const int tiles = (n + 2 * p.TT - 1) / (2 * p.TT);
-        int sum;
-        const int at = base + prefix(tiles, sh, sum);
-        if (w >= at && w < at + tiles) {
-            it.grp = grp;
-            it.q0 = q0;
-            it.n = n;
-            it.k0 = k0;
-            it.len = len;
-            it.t0 = (at + tiles - 1 - w) * 2 * p.TT;
+        return (n + 2 * p.TT - 1) / (2 * p.TT);
+    };
+    auto take = [&](int q0, int n, int k0, int len, int pair) {
+        it.grp = grp;
+        it.q0 = q0;
+        it.n = n;
+        it.k0 = k0;
+        it.len = len;
+        it.t0 = pair * 2 * p.TT;
+    };
+    // the sequence and the pair: all sequences' latest first, as their lists are the longest (six
+    // prompts of 1175 .. 2001 tokens: 75 us, sequence by sequence 84; more than 64 sequences
+    // are taken one after the other)
+    if (p.B > 1 && p.B <= SORTED) {
+        int q0, n, k0, len;
+        const int mine = load(tid, q0, n, k0, len);
+        if (tid < SORTED) pairs_of[tid] = mine;
+        __syncthreads();
+        // how many pairs are at place x of their sequence or behind it
+        auto behind = [&](int x) {
+            int sum = 0;
+            for (int b = 0; b < p.B; b++) sum += max(0, pairs_of[b] - x);
+            return sum;
+        };
+        // the last place at which there are more than w
+        int at = 0;
+        int span = (int)((min((int64_t)p.max_q, p.Tq) + 2 * p.TT - 1) / (2 * p.TT));
+        for (int step; span > 0; span = step) {
+            step = (span + PLAN - 1) / PLAN;
+            const int yes = __syncthreads_count(tid * step < span && behind(at + tid * step) > w);
+            at = yes ? at + (yes - 1) * step : -1;
+            if (at < 0 || step == 1) break;
         }
-        base += sum;
-        if (w < base && id != 0) break;
+        if (at >= 0) {
+            int sum;
+            const int rank = prefix(mine > at, sh, sum);
+            if (mine > at && rank == w - behind(at + 1)) take(q0, n, k0, len, at);
+        }
+    } else {
+        for (int b0 = 0, base = 0; b0 < p.B; b0 += PLAN) {
+            int q0, n, k0, len, sum;
+            const int mine = load(b0 + tid, q0, n, k0, len);
+            const int at = base + prefix(mine, sh, sum);
+            if (w >= at && w < at + mine) take(q0, n, k0, len, at + mine - 1 - w);
+            base += sum;
+            if (w < base && id != 0) break;
+        }
     }
     __syncthreads();
     if (it.grp < 0) {

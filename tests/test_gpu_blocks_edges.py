@@ -8,6 +8,7 @@ import torch
 
 import blocks_ref as br
 import dense_ref as ref
+import test_gpu_blocks as blocks
 from compressed_sparse_attention_window_gb300 import ds41
 from test_gpu_blocks import DEV, cu, filled_cache, gen, ints, randn, random_lists, sequence, tables
 from test_gpu_dense_attention_edges import aligned, close_by_weight, packed_cache
@@ -454,3 +455,25 @@ def test_tokens_queries_with_outliers(d, nh, kvh):
     q[0, 2] *= 2.0 ** -90
     cache, table = packed_cache(k, v, 16, True)
     run_tokens(g, q, cache, table, 700, kvh, 16, 0.7)
+
+
+@pytest.mark.parametrize("lens,nh,block", [
+    ([70, 3, 0, 41], 16, 16), ([600, 3, 700], 128, 32), ([0, 0, 530], 128, 64), ([17] * 64, 32, 16),
+    ([x * 7 % 31 for x in range(64)], 16, 32), ([x * 5 % 23 for x in range(65)], 16, 16),
+    ([x % 4 for x in range(300)], 64, 16)])
+def test_prompt_of_many_sequences(lens, nh, block):
+    """Pairs of tiles of all sequences, the latest first, or sequence by sequence; some empty."""
+    blocks.test_prompt(lens, 20, nh, 1, 32, block, 3, True)
+
+
+def test_prompt_with_sequences_that_are_skipped():
+    """Sequences that break their limits between others, whose results are as without them."""
+    g = gen(25)
+    lens, nh, kvh, hd, block = [40, 90, 33, 7], 16, 2, 64, 16
+    q, k = randn(g, sum(lens), nh, hd), randn(g, sum(lens), kvh, hd)
+    idx = ints([[[0, min(3, t // block)][:1 + (t >= block)] + [-1] * (t < block)] * kvh for n in lens for t in range(n)])
+    o, want = torch.full_like(q, 7.0), torch.empty_like(q)
+    ds41.block_prompt_attn_fwd(q, k, k, cu(lens), cu(lens), 90, 90, idx, block, 0.1, o=want)
+    ds41.block_prompt_attn_fwd(q, k, k, cu(lens), cu(lens), 89, 90, idx, block, 0.1, o=o)
+    assert ds41.device_status() == 4
+    assert (o[40:130] == 7).all() and torch.equal(o[:40], want[:40]) and torch.equal(o[130:], want[130:])
