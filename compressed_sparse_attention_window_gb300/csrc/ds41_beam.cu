@@ -15,8 +15,8 @@
 // What bounds it.  The logits are read once: HBM, if the exponentials (16 a cycle and SM)
 // and the instructions around them keep up.  A row is cut into runs so that every SM has
 // some; a warp goes through its part of a run alone, with the next steps' logits in flight.
-// (64 searches of 8 beams over 129281 bf16 logits, a fifth of them ended: 39.5 us with the
-// merge, 34 in runs_kernel, 3.1 TB/s.)
+// (64 searches of 8 beams over 129281 bf16 logits, a fifth of them ended: 39 us with the
+// merge, 33 in runs_kernel, 3.2 TB/s.)
 #include <cfloat>
 #include <type_traits>
 
@@ -104,21 +104,18 @@ __device__ __forceinline__ double number_of(uint64_t o) {
 // of them (a cell), whatever the row's alignment: equal rows have equal sums to the last
 // bit, and their offers tie.
 template <bool BF16>
-__global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
-    pdl_wait();
-    pdl_trigger();
+__device__ __forceinline__ void one_run(const Args& a, int64_t row, int split, float* most) {
     using T = typename std::conditional<BF16, uint16_t, uint32_t>::type;
-    extern __shared__ float most[];  // [cells] a cell's largest logit
+    // most: [cells] a cell's largest logit, and the ring behind them
     __shared__ uint64_t keys[OFFERS], best[WARPS];
     __shared__ int open[CELLS], n_open, n_keys;
     __shared__ uint32_t nth[WARPS];
     __shared__ float2 parts[WARPS];
-    const int64_t row = blockIdx.y;
     if (!reads(a, row)) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
     const int64_t b = row / a.W;
     const T* from = static_cast<const T*>(a.x) + b * a.b_stride + (row - b * a.W) * a.w_stride;
-    const int j0 = blockIdx.x * a.run, j1 = min(a.V, j0 + a.run);
+    const int j0 = split * a.run, j1 = min(a.V, j0 + a.run);
     auto logit = [&](int t) {
         const uint32_t w = __ldcs(from + t);
         return __uint_as_float(BF16 ? w << 16 : w);
@@ -225,7 +222,7 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
     if (lane == 0) parts[warp] = make_float2(m, sum);
     if (tid == 0) n_open = n_keys = 0;
     __syncthreads();
-    const int64_t at = row * a.splits + blockIdx.x;
+    const int64_t at = row * a.splits + split;
     if (warp == WARPS - 1) {  // the run's sum
         const float2 p = lane < WARPS ? parts[lane] : make_float2(-INFINITY, 0.0f);
         m = p.x;
@@ -307,35 +304,33 @@ __global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
     }
 }
 
-// A CTA for a search: the lists of all runs of its beams merged, best first.  What is not
+// The lists of all runs of a search's beams merged, best first, by a CTA.  What is not
 // below the last entry of some full list (k offers at least are not) is ranked by counting
 // what is better; more of it than fits is merged from the lists' heads.
-__global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
-    pdl_wait();
-    pdl_trigger();
-    extern __shared__ double base[];  // [W]: s_w - L; NaN: the beam offers nothing, or has ended
+__device__ __forceinline__ void merge(const Args& a, int b, double* base) {
+    // base [W]: s_w - L; NaN: the beam offers nothing, or has ended
     uint64_t* ends = reinterpret_cast<uint64_t*>(base + a.W);  // [W]: an ended beam's offer
     __shared__ Offer all[OFFERS];
     __shared__ uint64_t least[NT / 32];
     __shared__ int n_all, taken[NT / 32];
     __shared__ Offer best[NT / 32];
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.k;
     const int n_lists = a.W * a.splits, n_keys = n_lists * k;
     const uint64_t* keys = a.keys + (int64_t)b * n_keys;
     // (on their way while the sums are joined; keys of beams that have none may be anything)
     uint64_t held[HOLD];
 #pragma unroll
-    for (int u = 0; u < HOLD; u++) held[u] = u * NT + tid < n_keys ? keys[u * NT + tid] : 0;
+    for (int u = 0; u < HOLD; u++) held[u] = u * NT + tid < n_keys ? __ldcg(keys + u * NT + tid) : 0;
     if (tid == 0) n_all = 0;
     for (int w = tid; w < a.W; w += NT) {
         const int64_t row = (int64_t)b * a.W + w;
         const float score = a.scores[row];
         const bool over = a.ended && a.ended[row];
         float m = -INFINITY, sum = 0.0f;
-        for (int s = 0; s < a.splits; s++) m = fmaxf(m, a.sums[row * a.splits + s].x);
+        for (int s = 0; s < a.splits; s++) m = fmaxf(m, __ldcg(a.sums + row * a.splits + s).x);
         const float ref = m == -INFINITY ? 0.0f : m;
         for (int s = 0; s < a.splits; s++) {
-            const float2 p = a.sums[row * a.splits + s];
+            const float2 p = __ldcg(a.sums + row * a.splits + s);
             sum += p.y * expf(p.x - ref);
         }
         // (a sum that a NaN or an infinity is in is NaN; one of nothing but -inf is 0)
@@ -361,7 +356,7 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
         }
         return o;
     };
-    auto offer = [&](int h, int i) { return offer_of(h, i, i < k ? keys[h * k + i] : 0); };
+    auto offer = [&](int h, int i) { return offer_of(h, i, i < k ? __ldcg(keys + h * k + i) : 0); };
     auto write = [&](int i, const Offer& o) {
         const int64_t to = (int64_t)b * k + i;
         // (one that f32 does not hold any more is none: those are the last)
@@ -462,10 +457,40 @@ __global__ void __launch_bounds__(NT) merge_kernel(const Args a) {
     }
 }
 
+template <bool BF16>
+__global__ void __launch_bounds__(NT, 4) runs_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) float smem[];
+    one_run<BF16>(a, blockIdx.y, blockIdx.x, smem);
+}
+__global__ void __launch_bounds__(NT, 2) merge_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) float smem[];
+    merge(a, blockIdx.x, reinterpret_cast<double*>(smem));
+}
+// Few short rows: a search's runs are a cluster, whose first CTA merges them.
+template <bool BF16>
+__global__ void __launch_bounds__(NT, 2) search_kernel(const Args a) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) float smem[];
+    const int b = blockIdx.y, run = blockIdx.x;
+    one_run<BF16>(a, (int64_t)b * a.W + run / a.splits, run % a.splits, smem);
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
+                     : "memory");
+    if (run == 0) merge(a, b, reinterpret_cast<double*>(smem));
+}
+
 // Runs of a row: what makes the SM with the most of them end soonest (a run costs its parts and
 // about one more).
+constexpr int CLUSTER = 8;  // CTAs of a search that is merged in its own launch
+constexpr int SHORT = 4;    // parts of a run there, at most
 struct Plan {
     int splits, parts;  // runs, and parts of a run
+    bool whole;         // one launch (one search of 4 beams over 32000 tokens 9.3 us, two launches 10.2)
     size_t keys_bytes, sums_bytes;
 };
 Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
@@ -481,6 +506,12 @@ Plan make_plan(int64_t B, int64_t W, int64_t V, int64_t k, int sms) {
         }
     }
     Plan p;
+    p.whole = false;
+    const int64_t runs = W <= CLUSTER ? CLUSTER / W : 0;  // of a row, in a cluster
+    if (runs > 0 && rows * runs <= 2 * sms && (parts + runs - 1) / runs <= SHORT) {
+        p.whole = true;
+        splits = runs < parts ? runs : parts;
+    }
     const int64_t per = (parts + splits - 1) / splits;
     p.splits = (int)((parts + per - 1) / per);
     p.parts = (int)per;
@@ -557,6 +588,29 @@ extern "C" int ds41_beam_select(const void* logits, int fmt, int64_t b_stride, i
     const int smem = p.parts * beam::NT * 4 + ring;
     constexpr int MOST = beam::MAX_PARTS * beam::NT * 4 +
                          beam::WARPS * beam::STAGES * beam::STAGE<uint32_t>;
+    if (p.whole) {
+        if (int rc = bf16 ? allow_smem<beam::search_kernel<true>>(MOST, name)
+                          : allow_smem<beam::search_kernel<false>>(MOST, name))
+            return rc;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(W * p.splits), (unsigned)B);
+        cfg.blockDim = dim3(beam::NT);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)(W * p.splits);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, bf16 ? beam::search_kernel<true>
+                                                              : beam::search_kernel<false>, a),
+                                name))
+            return rc;
+        return launch_check(name);
+    }
     if (int rc = bf16 ? allow_smem<beam::runs_kernel<true>>(MOST, name)
                       : allow_smem<beam::runs_kernel<false>>(MOST, name))
         return rc;
