@@ -217,24 +217,24 @@ struct ForkArgs {
     unsigned int* status;
 };
 
-// CTAs 0 .. n - 1: the children's rows of the table.  CTAs n .. n + B - 1: the parents'
-// references.
-__global__ void __launch_bounds__(128) fork_kernel(const ForkArgs a) {
-    pdl_wait();
-    pdl_trigger();
+// Row r of the work: r < n: a child's row of the table; n .. n + B - 1: a parent's references.  By
+// WIDTH threads, a warp or a CTA, of which this is number tid.
+template <int WIDTH>
+__device__ __forceinline__ void fork_row(const ForkArgs& a, int r, int tid) {
     const int64_t cap = a.max_pages << a.page_shift;
-    const int mask = (1 << a.page_shift) - 1, tid = threadIdx.x;
-    if ((int)blockIdx.x < a.n) {
-        const int i = blockIdx.x, p = a.parents[i];
+    const int mask = (1 << a.page_shift) - 1;
+    if (r < a.n) {
+        const int i = r, p = a.parents[i];
         int len = 0;
         if (p >= 0 && p < a.B) len = sequence_len(a.lens, p, cap, a.status, false);
         else if (p != -1 && tid == 0) raise_status(a.status, DS41_E_INDEX);
         const int whole = len >> a.page_shift, part = len & mask;
         bool elder = false;  // an earlier child takes the last page over
         if (a.replace && part)
-            for (int j = tid; j < i && !elder; j += 128) elder = a.parents[j] == p;
-        const bool heir = __syncthreads_or(elder) == 0 && a.replace;
-        for (int64_t x = tid; x < a.max_pages; x += 128) {
+            for (int j = tid; j < i && !elder; j += WIDTH) elder = a.parents[j] == p;
+        const bool some = WIDTH == 32 ? __any_sync(0xffffffffu, elder) : __syncthreads_or(elder);
+        const bool heir = !some && a.replace;
+        for (int64_t x = tid; x < a.max_pages; x += WIDTH) {
             int pg = -1;
             if (x < whole || (x == whole && part)) {
                 pg = a.table[(int64_t)p * a.max_pages + x];
@@ -256,17 +256,21 @@ __global__ void __launch_bounds__(128) fork_kernel(const ForkArgs a) {
         }
         return;
     }
-    const int b = blockIdx.x - a.n;
+    const int b = r - a.n;
     const int len = sequence_len(a.lens, b, cap, a.status, tid == 0);
     int born = 0;
-    for (int j = tid; j < a.n; j += 128) born += a.parents[j] == b;
-    __shared__ int sums[4];
+    for (int j = tid; j < a.n; j += WIDTH) born += a.parents[j] == b;
     born = __reduce_add_sync(0xffffffffu, born);
-    if ((tid & 31) == 0) sums[tid >> 5] = born;
-    __syncthreads();
-    born = sums[0] + sums[1] + sums[2] + sums[3];
+    if (WIDTH > 32) {
+        __shared__ int sums[WIDTH / 32];
+        if ((tid & 31) == 0) sums[tid >> 5] = born;
+        __syncthreads();
+        born = 0;
+#pragma unroll
+        for (int w = 0; w < WIDTH / 32; w++) born += sums[w];
+    }
     const int whole = len >> a.page_shift, part = len & mask;
-    for (int x = tid; x < whole + (part ? 1 : 0); x += 128) {
+    for (int x = tid; x < whole + (part ? 1 : 0); x += WIDTH) {
         const int change = x < whole ? born - a.replace : (a.replace && !born ? -1 : 0);
         const int pg = a.table[(int64_t)b * a.max_pages + x];
         if (pg < 0 || pg >= a.n_pages) {
@@ -278,10 +282,8 @@ __global__ void __launch_bounds__(128) fork_kernel(const ForkArgs a) {
     }
 }
 
-// The pages for the copies, in the children's order.
-__global__ void __launch_bounds__(SCAN) fork_pages_kernel(const ForkArgs a) {
-    pdl_wait();
-    pdl_trigger();
+// The pages for the copies, in the children's order, by a CTA of SCAN threads.
+__device__ __forceinline__ void fork_pages(const ForkArgs& a) {
     __shared__ int64_t sh64[33];
     __shared__ int sh[STEP * 32 + 1];
     int64_t want = 0;
@@ -306,6 +308,32 @@ __global__ void __launch_bounds__(SCAN) fork_pages_kernel(const ForkArgs a) {
         }
         at += sum;
     }
+}
+
+// a CTA for a row
+__global__ void __launch_bounds__(128) fork_kernel(const ForkArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    fork_row<128>(a, blockIdx.x, threadIdx.x);
+}
+__global__ void __launch_bounds__(SCAN) fork_pages_kernel(const ForkArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    fork_pages(a);
+}
+// Both in one launch, a cluster with a warp for a row, where the tables are small: 64 beams of 33
+// entries 17.1 -> 15.4 us, 64 of 128 14.9 -> 14.4; 256 samples of 257 entries 20.7, this way 25.6.
+constexpr int FORK_CTAS = 8, FORK_ROWS = 256, FORK_ENTRIES = 8192;
+__global__ void __launch_bounds__(SCAN) fork_few_kernel(const ForkArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    for (int r = blockIdx.x * (SCAN / 32) + (threadIdx.x >> 5); r < a.n + a.B;
+         r += FORK_CTAS * (SCAN / 32))
+        fork_row<32>(a, r, threadIdx.x & 31);
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::
+                     : "memory");
+    if (blockIdx.x == 0) fork_pages(a);
 }
 
 struct CompactArgs {
@@ -589,10 +617,27 @@ extern "C" int ds41_kv_pages_fork(void* k_cache, void* v_cache, float* k_scales,
         *parts[i] = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + i * one);
     if (int rc = status_word(&a.status)) return rc;
     cudaStream_t st = (cudaStream_t)stream;
-    if (int rc = launch_pdl(fork_kernel, dim3((unsigned)(n + B)), dim3(128), 0, st, name, a))
-        return rc;
-    if (n == 0) return DS41_OK;
-    if (int rc = launch_pdl(fork_pages_kernel, dim3(1), dim3(SCAN), 0, st, name, a)) return rc;
+    if (n > 0 && n + B <= FORK_ROWS && (n + B) * max_pages <= FORK_ENTRIES) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(FORK_CTAS);
+        cfg.blockDim = dim3(SCAN);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = FORK_CTAS;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (int rc = cuda_check(cudaLaunchKernelEx(&cfg, fork_few_kernel, a), name)) return rc;
+        if (int rc = launch_check(name)) return rc;
+    } else {
+        if (int rc = launch_pdl(fork_kernel, dim3((unsigned)(n + B)), dim3(128), 0, st, name, a))
+            return rc;
+        if (n == 0) return DS41_OK;
+        if (int rc = launch_pdl(fork_pages_kernel, dim3(1), dim3(SCAN), 0, st, name, a)) return rc;
+    }
     c.src = a.src;
     c.dst = a.dst;
     c.rows = a.rows;
