@@ -4,8 +4,7 @@
 // Mathematics.  As tree attention of few rows (ds41_tree_attn.cu, ds41_few.cuh): one pass
 // over the rows j <= p of the listed pages, with a lazily moved reference per row.  The
 // rows of a tile are the query heads of one token that share a key/value head (lists
-// differ from token to token), at most 16; groups of at most 8 heads take the transposed
-// products, whose tiles have 8.
+// differ from token to token), 8 for groups of at most 8 heads, else 16.
 //
 // What bounds it.  Each listed row is read once a token: HBM when there are tokens
 // enough.  A token's list is cut into as many runs as fill the GPU, at most eight, the
@@ -192,27 +191,18 @@ __global__ void __launch_bounds__(NT, Shape<HD, E4M3, RT>::CTAS) tokens_kernel(c
 #pragma unroll
     for (int i = 0; i < S::STAGES - 1; i++) fetch(i);
 
-    typename std::conditional<RT == 8, few::Rows8<HD, E4M3>, few::Rows<HD, E4M3>>::type mem;
+    few::Rows<HD, E4M3, RT / 8> mem;
     const uint16_t* q = a.q + t * a.q_tok + ((int64_t)h * a.G + y0) * a.q_head;
-    if constexpr (RT == 8) {
-        mem.query(q + min(g, rows - 1) * a.q_head, a.hd, a.scale * tc::SM_LOG2E, c);
-    } else {
 #pragma unroll
-        for (int i = 0; i < 2; i++) mem.query(i, q + min(g + 8 * i, rows - 1) * a.q_head, a.hd, c);
-        mem.start(a.scale * tc::SM_LOG2E);
-    }
+    for (int n = 0; n < RT / 8; n++)
+        mem.query(n, q + min(8 * n + g, rows - 1) * a.q_head, a.hd, a.scale * tc::SM_LOG2E, c);
     for (int i = 0; i < n_mine; i++) {
         fetch(i + S::STAGES - 1);
         cp_async_wait<S::STAGES - 1>();
         __syncwarp();
         const int st = i % S::STAGES, live = keys - (first + i * WARPS + warp) * GROUP;
         const bool none = (bad >> st) & 1;
-        if constexpr (RT == 8)
-            mem.group(ring + st * C::STAGE, none ? 0 : live, g, c);
-        else
-            mem.group(
-                ring + st * C::STAGE, none || live < GROUP,
-                [&](int, int x) { return !none && x < live; }, g, c);
+        mem.group(ring + st * C::STAGE, none ? 0 : live, g, c);
         __syncwarp();  // the stage is read before it is filled again
     }
     cp_async_wait<0>();
