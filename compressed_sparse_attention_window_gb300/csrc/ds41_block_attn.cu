@@ -65,8 +65,9 @@ constexpr int MAX_RUNS = 8;  // CTAs of a cluster
 template <int HD, bool E4M3, int RT>
 struct Shape {
     using C = few::Cfg<HD, E4M3>;
-    // CTAs of an SM: what the registers and the rings leave room for
-    static constexpr int CTAS = C::RB == 256 ? 2 : RT == 8 ? 4 : E4M3 ? 3 : 2;
+    // CTAs of an SM: what the registers and the rings leave room for (three of 16 rows, which
+    // spill some registers: 16 tokens of 128 heads over 8, e4m3, 35.1 us, two 32.7)
+    static constexpr int CTAS = C::RB < 256 && RT == 8 ? 4 : 2;
     static constexpr int STAGES = CTAS == 4 && C::RB == 128 ? 3 : C::STAGES;
     static constexpr int RING = STAGES * C::STAGE;  // of a warp
     static constexpr int OUT = RT * C::P * 4;
