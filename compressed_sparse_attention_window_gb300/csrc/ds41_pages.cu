@@ -425,10 +425,13 @@ __global__ void __launch_bounds__(COPY) copy_kernel(const CopyArgs a) {
         for (int64_t b = blockIdx.x; b < a.B; b += gridDim.x) {
             const int len = sequence_len(a.lens, b, a.max_pages << a.page_shift, a.status, tid == 0);
             const int used = (int)(((int64_t)len + a.page - 1) >> a.page_shift);
-            for (int i = tid; i < used; i += COPY) {
+            // (all entries, not the counted ones alone: behind those may be pages that were taken
+            // for rows to come, which have moved like the rest)
+            for (int64_t i = tid; i < a.max_pages; i += COPY) {
                 int32_t* e = a.table + b * a.max_pages + i;
-                if (*e < 0 || *e >= a.n_pages) raise_status(a.status, DS41_E_INDEX);
-                else *e = a.to[*e];
+                const int pg = *e;
+                if (pg >= 0 && pg < a.n_pages) *e = a.to[pg];
+                else if (i < used) raise_status(a.status, DS41_E_INDEX);
             }
         }
     const int64_t units = (a.count ? (int64_t)*a.count : a.n) * a.kvh;

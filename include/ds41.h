@@ -654,8 +654,10 @@ int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const 
  * device, so that a captured step can hand pages out:
  *   refs [n_pages] int32: how many sequences have the page; 0: it is free
  *   page_table [B, max_pages] int32, lens [B] int32: sequence b has len rows in the
- *   pages of its first ceil(len / page) entries.  Those behind are not looked at: a page
- *   taken for rows that len does not count yet is not freed, shared or moved with it
+ *   pages of its first ceil(len / page) entries.  A page taken for rows that len does
+ *   not count yet is behind those: it is neither freed nor shared with its sequence, unless the
+ *   call is given the lengths that count it (new_lens).  A fork with replace leaves it
+ *   out of the children's rows, counted as before; compacting moves it and its entry
  * Full pages may be shared; a page that is not full belongs to one sequence, which
  * writes on in it.  Free pages are handed out lowest first, to the sequences in their
  * order, so equal calls give equal tables.  A length below 0 or past max_pages * page
@@ -712,8 +714,9 @@ size_t ds41_kv_pages_compact_workspace_bytes(int64_t n_pages);
 
 /* The pages that somebody has move to the front: live of them in all, the i-th free
  * page below that number gets the i-th one in use from there on, with its refs; the
- * table's entries follow (every sequence with pages has to be in it: one call, one
- * pool).  Pages live .. n_pages - 1 are free then.
+ * table's entries follow, those behind a sequence's len rows too where they name a page
+ * (every sequence with pages has to be in it: one call, one pool).  Pages live ..
+ * n_pages - 1 are free then.
  *   live [1] int32 output */
 int ds41_kv_pages_compact(void* k_cache, void* v_cache, float* k_scales, float* v_scales, int fmt,
                           int64_t n_pages, int64_t page, int64_t kvh, int64_t hd, int8_t* codes,
