@@ -597,8 +597,9 @@ extern "C" int ds41_kv_pages_fork(void* k_cache, void* v_cache, float* k_scales,
         return rc;
     Pool p;
     if (int rc = check_pool(name, n_pages, page, max_pages, B, &p)) return rc;
-    DS41_REQUIRE(n >= 0 && n + B < int64_t(1) << 30, DS41_E_RANGE, "%s: n=%lld B=%lld", name,
-                 (long long)n, (long long)B);
+    // (each child and each parent counts among all children: (n + B) n reads)
+    DS41_REQUIRE(n >= 0 && n < 65536 && B < 65536, DS41_E_RANGE, "%s: n=%lld B=%lld (below 65536)",
+                 name, (long long)n, (long long)B);
     if (n + (replace ? B : 0) == 0) return DS41_OK;
     DS41_REQUIRE(words(refs) && (B == 0 || (words(page_table) && words(lens))) &&
                      (n == 0 || (words(parents) && words(table_out) && words(lens_out))),

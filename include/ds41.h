@@ -691,6 +691,7 @@ size_t ds41_kv_pages_fork_workspace_bytes(int64_t n_pages, int64_t B, int64_t n)
  *   the parents ds41_beam_select gives): the parents' references are dropped, the first child of a
  *   parent takes its last page over, and pages that nobody has any more are free for
  *   the copies of this call already; what they hold is then overwritten.
+ * B and n are below 65536 (DS41_E_RANGE).
  * A parent outside -1 .. B - 1 raises DS41_E_INDEX; its child has no rows.  Where no
  * page is left the entry becomes -1 and DS41_E_PAGES is raised. */
 int ds41_kv_pages_fork(void* k_cache, void* v_cache, float* k_scales, float* v_scales, int fmt,

@@ -117,6 +117,14 @@ def test_pages_refuse(lib):
     assert lib.ds41_kv_pages_compact_workspace_bytes(5) == 3 * 32 + 16
 
 
+@pytest.mark.parametrize("kw", [dict(n=65536), dict(B=65536), dict(n=1 << 29), dict(B=1 << 29), dict(n=0, B=65536, replace=1)])
+def test_forks_of_masses_are_refused(lib, kw):
+    """Every child and parent looks through all children: 2^20 of them would be 2^41 reads, minutes in one launch."""
+    far = dict(out=ctypes.c_void_p(1 << 50), out_lens=ctypes.c_void_p(1 << 51))
+    assert fork(lib, **far, **kw) == RANGE
+    assert b"65536" in lib.ds41_last_error()
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(fmt=3), ARG), (dict(page=20), ARG), (dict(k=ODD), ARG), (dict(codes=None), ARG), (dict(codes=ODD), ARG),
     (dict(kscales=None), ARG), (dict(table=None), ARG), (dict(lens=OFF), ARG), (dict(starts=OFF), ARG),
