@@ -738,7 +738,11 @@ size_t ds41_beam_select_workspace_bytes(int64_t B, int64_t W, int64_t V, int64_t
  * offers token t at
  *   s_w + x_wt - log sum_u e^{x_wu}
  * and a search keeps the k best offers of its W * V, best first, ties to the lower w * V + t.
- * The offers are compared in 64 bits, within a beam by x_wt alone.
+ * The offers are compared in 64 bits, within a beam by x_wt alone.  The sum over u is one
+ * of f32 numbers: its logarithm moves all offers of a beam by less than 2 10^-5 (measured:
+ * by 3.4 10^-7 at most), so offers of different beams that are nearer than that can be
+ * in either order, those of beams with the same logits in another order among them.
+ * Beams with the same logits in the same order tie.
  *   logits [B, W, V] f32 or bf16 (fmt), elements between searches and between beams
  *     b_stride, w_stride (>= V), the vocabulary dense; any alignment of its type
  *   scores [B, W] f32: -inf = no beam

@@ -1,5 +1,7 @@
-"""Pages where they could go wrong beside the plain cases: pages taken ahead of the lengths
-when a pool is compacted."""
+"""Pages and beams where they could go wrong beside the plain cases: pages taken ahead of
+the lengths when a pool is compacted, offers of different beams next to each other."""
+import math
+
 import pytest
 import torch
 
@@ -60,3 +62,59 @@ def test_compact_between_taking_pages_and_counting_them(e4m3):
     ds41.kv_pages_compact(cache, refs, table, lens, keys=keys)
     assert ds41.device_status() == 4
     assert table[0, 1] == P + 3
+
+
+# ---------------------------------------------------------------------------
+# Beams
+# ---------------------------------------------------------------------------
+def test_beam_order_of_offers_next_to_each_other():
+    """Rows of n zeros, -inf besides: the sum n is exact in f32, so that a beam's offers are at s - log n but for
+    the logarithm.  Scores that are log n rounded to f32 set two beams' offers 2.4e-7 .. 1e-6 apart
+    (the rounding of a logarithm of 8 .. 10 in f32 alone is 4.8e-7); the logarithm is worked out
+    as e ln 2 in 64 bits and that of a factor of 3/4 .. 3/2 in f32, off by 2^-25 for each of the two."""
+    r = torch.Generator().manual_seed(34)
+    V = 20000
+    pairs = []
+    while len(pairs) < 300:
+        n = torch.randint(3000, V, (2,), generator=r)
+        exact = n.double().log()
+        s = exact.float()
+        gap = (s[0].double() - exact[0]) - (s[1].double() - exact[1])
+        if abs(gap) >= 2.0 ** -22:
+            pairs.append((n.tolist(), s, 0 if gap > 0 else 1))
+    x = torch.full((len(pairs), 2, V), -math.inf)
+    want, first = [], []
+    for b, (n, s, best) in enumerate(pairs):
+        for w in range(2):
+            at = torch.randperm(V, generator=r)[:n[w]]
+            x[b, w, at] = 0.0
+            if w == best:
+                want.append([2 * b + w])
+                first.append([int(at.min())])
+    scores = torch.stack([s for _, s, _ in pairs]).to(DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        _, parents, tokens = ds41.beam_select(x.to(DEV, dtype), scores, 1)
+        wrong = [b for b, (p, w) in enumerate(zip(parents.tolist(), want)) if p != w]
+        assert not wrong, f"{len(wrong)} of {len(pairs)} searches keep the lower offer"
+        assert tokens.tolist() == first
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_beam_order_of_rows_in_other_orders(dtype):
+    """Beams with the same logits in other orders: their sums differ by their roundings, which check_beam bounds by
+    tol for each.  Scores 2 tol apart decide; equal scores leave the order of equal logits to the sums."""
+    g = gen(35)
+    V, W, k = 3001, 6, 24
+    tol = (V / 256 + 16) * 2.0 ** -24 + 2.0 ** -20
+    row = torch.randn(V, generator=g, device=DEV).to(dtype)
+    row[:8] = torch.arange(8, device=DEV).to(dtype) * 0.5 + 5  # (the best ones far apart)
+    order = [torch.randperm(V, generator=g, device=DEV) for _ in range(W)]
+    x = torch.stack([row[o] for o in order])[None]
+    scores = (torch.arange(W, device=DEV) * 2.5 * tol)[None].float()
+    _, parents, tokens = ds41.beam_select(x, scores, k)
+    assert parents[0].tolist() == [W - 1 - i % W for i in range(k)]
+    assert x[0, parents[0].long(), tokens[0].long()].tolist() == [row[7 - i // W].item() for i in range(k)]
+    _, parents, tokens = ds41.beam_select(x, torch.zeros(1, W, device=DEV), k)
+    for i in range(0, k, W):
+        assert sorted(parents[0, i:i + W].tolist()) == list(range(W))
+    assert x[0, parents[0].long(), tokens[0].long()].tolist() == [row[7 - i // W].item() for i in range(k)]
