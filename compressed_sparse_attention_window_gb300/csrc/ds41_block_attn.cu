@@ -112,10 +112,13 @@ __global__ void __launch_bounds__(NT, Shape<HD, E4M3, RT>::CTAS) tokens_kernel(c
     if (blockIdx.x == 0)
         for (int b = tid; b < a.B; b += NT)
             if (!load_seq(a, b).ok) raise_status(a.status, DS41_E_INDEX);
-    // the last sequence that begins at or before the token
+    // the sequence that has the token (among prefix sums that fall, too: those of a sequence
+    // that is skipped do not hide another's)
     int b = -1;
-    for (int x = tid; x < a.B; x += NT)
-        if (a.cu_q[x] <= t) b = x;
+    for (int x = tid; x < a.B; x += NT) {
+        const int from = a.cu_q[x], to = a.cu_q[x + 1];
+        if (from >= 0 && from <= t && t < to && to <= a.Tq && to - from <= a.max_q) b = x;
+    }
     const int32_t* src = a.idx + ((int64_t)t * a.kvh + h) * a.topk;
     int mine[MAX_LIST / NT], before[MAX_LIST / NT];
 #pragma unroll
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(NT, Shape<HD, E4M3, RT>::CTAS) tokens_kernel(c
     b = max(max(found[0][0], found[0][1]), max(found[0][2], found[0][3]));
     if (b < 0) return;  // (the same for the whole cluster)
     const Seq s = load_seq(a, b);
-    if (!s.ok || t < s.q0 || t >= s.q0 + s.n) return;
+    if (!s.ok) return;
     const int p = s.len - s.n + (t - s.q0), cur = p >> a.block_shift;
     // the list ends at the first entry that does not rise or lies past the token (an entry
     // behind the end may be anything: one below 0 can rise above another)
