@@ -1,7 +1,9 @@
-"""Block attention at the ends of what it takes: prefix sums that fall between good sequences."""
+"""Block selection and attention at the ends of what they take: hundreds of picks among
+thousands of blocks, prefix sums that fall between good sequences."""
 import pytest
 import torch
 
+import test_gpu_blocks_edges as edges
 from compressed_sparse_attention_window_gb300 import ds41
 from test_gpu_blocks import DEV, filled_cache, gen, ints, randn, tables
 
@@ -20,6 +22,15 @@ def _cuda():
 def _clean_status():
     yield
     assert ds41.device_status() == 0
+
+
+@pytest.mark.parametrize("lens,news,nh,kvh,hd,page,topk,first,local", [
+    ([16000], [2], 4, 1, 64, 16, 300, 1, 2), ([30000, 9000], [5, 1], 2, 1, 64, 16, 1024, 0, 1),
+    ([17000], [1], 8, 2, 128, 16, 1024, 500, 20), ([9000], [9], 3, 1, 80, 16, 257, 1, 1),
+    ([16400], [1], 4, 1, 64, 16, 1024, 1, 2), ([200000], [1], 2, 1, 16, 16, 300, 1, 2)])
+def test_select_hundreds_of_many_blocks(lens, news, nh, kvh, hd, page, topk, first, local):
+    """More picks than the list of candidates holds, more than 512 blocks."""
+    edges.test_select_over_many_blocks(lens, news, nh, kvh, hd, page, topk, first, local)
 
 
 @pytest.mark.parametrize("c", [[0, 4, -3, 8], [0, 3, 100, 4, 8], [4, 6, 1, 3], [5, 9, 12, 2, 5]])

@@ -1,13 +1,15 @@
 """Pages and beams where they could go wrong beside the plain cases: pages taken ahead of
-the lengths when a pool is compacted, offers of different beams next to each other."""
+the lengths when a pool is compacted, tables of more than 128 pages, whole prompts under a
+beam search, many beams and the longest rows, offers of different beams next to each other."""
 import math
 
 import pytest
 import torch
 
+import test_gpu_pages as pages
 from compressed_sparse_attention_window_gb300 import ds41
 from test_gpu_blocks import DEV, filled_cache, gen, ints
-from test_gpu_pages import everything, filled_keys
+from test_gpu_pages import check_beam, everything, filled_keys, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -64,9 +66,61 @@ def test_compact_between_taking_pages_and_counting_them(e4m3):
     assert table[0, 1] == P + 3
 
 
+@pytest.mark.parametrize("replace", [False, True])
+@pytest.mark.parametrize("lens,n", [([128 * 16 + 5, 127 * 16 + 3, 129 * 16, 257 * 16 + 9], 200), ([2049] * 8, 256),
+                                    ([300 * 16 + 1, 0, 5], 40)])
+def test_fork_of_long_tables(lens, n, replace):
+    """More pages a row than the threads of a CTA, in two launches."""
+    pages.test_fork(lens, n, 1, 16, 16, n + 3, replace, True)
+
+
+def test_beams_keep_their_prompts():
+    """Every beam has its prompt's rows, K, V and the scales, through forks that share whole pages and copy
+    the last one, and through steps that replace the beams by their children."""
+    g = gen(32)
+    B, W, V, page, kvh, hd = 3, 4, 300, 16, 2, 32
+    n0 = [20, 33, 16]
+    P = 3 * W * 6 + 4
+    cache, refs = filled_cache(g, P, kvh, page, hd, True), torch.zeros(P, dtype=torch.int32, device=DEV)
+    table = torch.full((B, 8), -1, dtype=torch.int32, device=DEV)
+    lens = ints(n0)
+
+    def rows(row, n):  # [tensor][n, kvh, ..]
+        at = row[:-(-n // page)].long()
+        return [u8(t)[at].transpose(1, 2).flatten(0, 1)[:n].clone() for t in cache]
+    ds41.kv_pages_take(refs, table, torch.zeros_like(lens), lens, page)
+    prompts = [rows(table[b], n) for b, n in enumerate(n0)]
+    start = table.clone()
+    table, lens = ds41.kv_pages_fork(cache, refs, table, lens, ints([b for b in range(B) for _ in range(W)]))
+    ds41.kv_pages_free(refs, start, ints(n0), page)
+    scores = torch.full((B, W), -math.inf, device=DEV)
+    scores[:, 0] = 0.0
+    for step in range(20):
+        scores, parents, _ = ds41.beam_select(torch.randn(B, W, V, generator=g, device=DEV) * 2, scores, W)
+        table, lens = ds41.kv_pages_fork(cache, refs, table, lens, parents.view(-1), replace=True)
+        new = lens + 1
+        ds41.kv_pages_take(refs, table, lens, new, page)
+        pos = lens.long()
+        slots = torch.gather(table.long(), 1, (pos // page)[:, None])[:, 0] * page + pos % page
+        k = torch.randn(B * W, kvh, hd, generator=g, device=DEV).bfloat16()
+        ds41.kv_cache_write(cache, k, k, slots)
+        lens = new
+        for i in range(B * W):
+            assert int(lens[i]) == n0[i // W] + step + 1
+            for got, want in zip(rows(table[i], n0[i // W]), prompts[i // W]):
+                assert torch.equal(got, want), (step, i)
+
+
 # ---------------------------------------------------------------------------
 # Beams
 # ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,W,V,k", [(1, 1024, 5000, 64), (2, 700, 9000, 128), (1, 4, 1 << 22, 16)])
+def test_beam_of_many_beams_and_of_long_rows(B, W, V, k):
+    g = gen(33)
+    x = torch.randn(B, W, V, generator=g, device=DEV).bfloat16()
+    check_beam(x, torch.zeros(B, W, device=DEV), k)
+
+
 def test_beam_order_of_offers_next_to_each_other():
     """Rows of n zeros, -inf besides: the sum n is exact in f32, so that a beam's offers are at s - log n but for
     the logarithm.  Scores that are log n rounded to f32 set two beams' offers 2.4e-7 .. 1e-6 apart
