@@ -8,11 +8,15 @@
 // score is two f32 products away, so the picks are the same wherever they are worked out.
 // The scale of a block is not negative, so it may follow the maximum over the heads.
 //
-// What bounds it.  The keys' sums: HBM, one read of the new rows' pages.  Selection for a
-// step of few tokens: a chain of latencies (the page table, the keys, the scores'
-// exchange, the ranking).  For prompts: instructions, a third of them around the products
-// (m16n8k16, blocks by columns of query heads), 40% in the ranking.  (One token of 24 sequences,
-// up to 512 blocks, 32 heads of 128 over 8: 12 us; 8192 tokens, up to 512 blocks: 221 us.)
+// What bounds it.  The keys' sums read the new rows' pages once, by latencies: a warp has one
+// page and head, 16 rows of it in flight behind the table's entry (8 heads of 128, bf16, pages
+// of 64: 8192 rows 8.6 us, 2.0 TB/s; 32768 rows 16.8 us, 4.0 TB/s).  Selection for a step of few
+// tokens: a chain of latencies (the page table, the keys, the scores' exchange, the ranking).  For
+// prompts: instructions, a third of them around the products (m16n8k16, blocks by columns of
+// query heads), 40% in the ranking.  (One token of 24 sequences, up to 512 blocks, 32 heads of 128
+// over 8: 12 us; 8192 tokens, up to 512 blocks: 221 us.  64 picks of 2048 blocks against 512: 24
+// tokens 35 us against 16, 2048 tokens 258 against 74: from 43 picks on no sample gives a bound,
+// and all ranks are counted several times.)
 #include "ds41_softmax_tc.cuh"
 
 namespace ds41 {

@@ -12,6 +12,11 @@
 // the queries its 8 columns, so that 8 rows leave no half of a tile to padding.  A lane has
 // the keys g and g + 8 of a group and the queries 2 c and 2 c + 1 of each 8; the weights
 // change places (movmatrix) on their way to being the other product's columns.
+//
+// Roundings.  The second product takes 16-bit operands: weights are rounded to bf16 beside bf16
+// values (off by 2^-8 of themselves; the sum of the weights is taken before), to f16 in a row's
+// own unit beside e4m3 ones.  (Outputs to 64 bits: bf16 2.3e-3 at most, with weights in 32 bits
+// 1.7e-3, which is the outputs' own rounding; e4m3 1.7e-3, as with weights in 32 bits.)
 #pragma once
 
 #include "ds41_softmax_tc.cuh"

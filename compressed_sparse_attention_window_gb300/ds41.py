@@ -974,7 +974,8 @@ def block_prompt_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
                           o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                           ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ds41_block_prompt_attn_fwd: packed prompts (q, k, v as prompt_attn_fwd) over the
-    blocks idx [Tq, kvh, topk] of ``block`` rows of their sequences.  Returns o [Tq, nh, hd]
-    (and fills lse [Tq, nh] f32 if given)."""
+    blocks idx [Tq, kvh, topk] of ``block`` rows of their sequences.  Neighbouring tokens'
+    lists are read as their union: where it is most of the keys, prompt_attn_fwd over all keys is
+    the faster call.  Returns o [Tq, nh, hd] (and fills lse [Tq, nh] f32 if given)."""
     return (_binding or _dense()).block_prompt_attn_fwd(q, k, v, cu_q, cu_k, max_q, max_k, idx,
                                                         block, scale, sink, o, lse, ws)

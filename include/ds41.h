@@ -655,16 +655,20 @@ int ds41_tree_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head, const 
  *   refs [n_pages] int32: how many sequences have the page; 0: it is free
  *   page_table [B, max_pages] int32, lens [B] int32: sequence b has len rows in the
  *   pages of its first ceil(len / page) entries.  A page taken for rows that len does
- *   not count yet is behind those: it is neither freed nor shared with its sequence, unless the
- *   call is given the lengths that count it (new_lens).  A fork with replace leaves it
- *   out of the children's rows, counted as before; compacting moves it and its entry
+ *   not count yet is behind those: it is neither freed nor shared with its sequence,
+ *   unless the call is given the lengths that count it (new_lens).  A fork with replace
+ *   leaves it out of the children's rows, counted as before; compacting moves it and
+ *   its entry
  * Full pages may be shared; a page that is not full belongs to one sequence, which
- * writes on in it.  Free pages are handed out lowest first, to the sequences in their
- * order, so equal calls give equal tables.  A length below 0 or past max_pages * page
+ * writes on in it (so a length is not cut back into a shared page).  Free pages are
+ * handed out lowest first, to the sequences in their order, so equal calls give equal
+ * tables.  A length below 0 or past max_pages * page
  * makes its sequence one without pages and raises DS41_E_INDEX, as an entry
  * outside 0 .. n_pages - 1 does, which is skipped.  Block keys (ds41_kv_block_keys)
  * go where their pages go: codes and key_scales, both NULL where there are none.
- * Calls on one pool are ordered on one stream. */
+ * Calls on one pool are ordered on one stream.  Scratch, here and below, holds nothing
+ * between calls; calls that may run at the same time, captured graphs among them, need
+ * one each. */
 
 /* Pages for rows lens .. new_lens - 1 (new_lens <= lens: none): entries
  * ceil(len / page) .. ceil(new_len / page) - 1 of the sequence's table row become free
@@ -831,10 +835,15 @@ size_t ds41_block_prompt_attn_workspace_bytes(int64_t B, int64_t Tq, int64_t max
 /* The same over packed prompts, keys and values as ds41_prompt_attn_fwd takes them: query
  * i of sequence b stands at p = i + lk - lq and sees the keys j <= p of the blocks in
  * idx (block x: keys x * block .. of the sequence, block a power of two of 16 .. 256).
- * Lists as ds41_block_attn_fwd's.  max_q, max_k: no sequence has more queries, keys (one
- * that has, or lk < lq, is skipped and raises DS41_E_INDEX); max_k / block at most
- * 32768.  A NaN or an infinity in a v row of a listed block can reach the queries that
- * stand within 2 * 128 / (nh / kvh) tokens of one that lists it. */
+ * Lists as ds41_block_attn_fwd's, softmax, sink, o, lse and roundings as
+ * ds41_prompt_attn_fwd's.  What is read and multiplied is the union of the lists of up to
+ * 2 * 128 / (nh / kvh) neighbouring tokens: where those have little in common and the
+ * union is most of the keys, ds41_prompt_attn_fwd over all keys takes less time (six
+ * prompts of up to 2001 tokens, 12 blocks of 32 keys each at random: 75 us against 61).
+ * max_q, max_k: no sequence has more queries, keys (one that has, or lk < lq, is
+ * skipped and raises DS41_E_INDEX); max_k / block at most 32768.  A NaN or an infinity
+ * in a v row of a listed block can reach the queries that stand within
+ * 2 * 128 / (nh / kvh) tokens of one that lists it. */
 int ds41_block_prompt_attn_fwd(const ds41_bf16* q, int64_t q_tok, int64_t q_head,
                                const ds41_bf16* k, int64_t k_tok, int64_t k_head,
                                const ds41_bf16* v, int64_t v_tok, int64_t v_head,
